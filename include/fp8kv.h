@@ -60,8 +60,26 @@ typedef enum {
 
 typedef enum {
     FP8KV_CACHE_E4M3 = 0,       /* 1 byte per element, E4M3FN codes, scaled          */
-    FP8KV_CACHE_BF16 = 1        /* 2 bytes per element, stored as is, scales unused  */
+    FP8KV_CACHE_BF16 = 1,       /* 2 bytes per element, stored as is, scales unused  */
+    FP8KV_CACHE_INT4 = 2        /* 4.5 bits per element: 4-bit codes in blocks of 16, one E4M3 scale a block */
 } fp8kv_cache_dtype;
+
+/*
+ * The INT4 cache.  A row (one token of one KV head, 128 elements) is 8 blocks
+ * of 16 elements.  With the calibrated tensor scale c (k_scale or v_scale, as
+ * for E4M3; 2^-100 <= c <= 2^100) a block x is stored as the E4M3 scale s and
+ * 16 integers n, every step rounded to fp32:
+ *     r = amax|x| / (7 c)         s = max(e4m3_rne_satfinite(r), 2^-9)
+ *     inv = 1 / (s c)             n = clamp(rint(x inv), -7, 7)   (ties to even)
+ * and stands for n s c: off by at most half a step s c / 2 (and 2^-20 of it),
+ * unless it saturates at 7 * 448 c.  A NaN in the block makes s NaN (0x7F) and
+ * n = 0: the whole block reads as NaN.  Infinities saturate.
+ * k_cache, v_cache: [num_pages][Hkv][page_size * 72] bytes; the bytes of one
+ * (page, head) are page_size rows of 64 code bytes (byte i: element 2i in the
+ * low nibble, element 2i + 1 in the high one, each as n + 8), then page_size
+ * rows of 8 scale bytes.
+ */
+#define FP8KV_INT4_ROW_BYTES 72
 
 /* Device status bits (fp8kv_device_status). */
 #define FP8KV_DEV_BAD_SLOT      0x1u  /* slot_mapping entry >= num_pages*page_size   */
@@ -80,13 +98,15 @@ typedef enum {
  *     BF16:  cache[...] = x[t][h][d]  (bits copied, scales ignored, may be NULL)
  * with fp32 IEEE division, round to nearest even, saturation to +-448
  * (infinities included), NaN -> 0x7F with the input's sign, -0 -> 0x80.
+ *     INT4:  the row's codes and block scales as described above.
  * Slots < 0 are skipped; slots not named are left untouched.  Duplicate
  * non-negative slots race (unspecified which token wins).
  *
  *   k, v          (device) bf16 [T][Hkv][D]
  *   slot_mapping  (device) int64 [T]
- *   k_scale, v_scale (device) one fp32 each, > 0 (E4M3 only)
+ *   k_scale, v_scale (device) one fp32 each, > 0 (E4M3 and INT4 only)
  *   k_cache, v_cache (device) [num_pages][Hkv][page_size][D] of the cache dtype
+ *                ([num_pages][Hkv][page_size * 72] bytes for INT4)
  *   D must be 128; page_size 32 or 64; T may be 0 (no launch, FP8KV_OK, no
  *   pointer is read).
  * Device check: slot >= num_pages*page_size -> row skipped, FP8KV_DEV_BAD_SLOT.
@@ -112,6 +132,26 @@ int fp8kv_cache_insert_per_head(const void* k, const void* v, const int64_t* slo
                                 int Hkv, int D, const float* k_scale, const float* v_scale,
                                 void* k_cache, void* v_cache, int num_pages, int page_size,
                                 void* stream);
+
+/*
+ * fp8kv_cache_gather -- read T stored tokens back as bf16: for every token t
+ * with slot s = slot_mapping[t] >= 0, head h, element d:
+ *     k_out[t][h][d] = bf16( fp32( value of the stored k ) )
+ * where the stored value is decode(code) * k_scale (E4M3), the stored bf16
+ * bits (BF16), or n s k_scale (INT4), the product rounded to fp32 and then to
+ * bf16; V likewise.  Rows of tokens with a negative slot are left as they are.
+ * For reusing or inspecting cached tokens outside the attention kernels (the
+ * pages have no counterpart).  Caches with per-tensor scales only.
+ *
+ *   slot_mapping  (device) int64 [T]; slots may repeat
+ *   k_scale, v_scale, k_cache, v_cache, page sizes, D: as fp8kv_cache_insert
+ *   k_out, v_out  (device) bf16 [T][Hkv][D]
+ *   T may be 0 (no launch, FP8KV_OK, no pointer is read).
+ * Device check: slot >= num_pages*page_size -> row skipped, FP8KV_DEV_BAD_SLOT.
+ */
+int fp8kv_cache_gather(const int64_t* slot_mapping, int T, int Hkv, int D, const float* k_scale,
+                       const float* v_scale, const void* k_cache, const void* v_cache, int num_pages,
+                       int page_size, int cache_dtype, void* k_out, void* v_out, void* stream);
 
 /*
  * fp8kv_qk_norm_rope_insert -- the Q/K RMSNorm + RoPE boundary fused with the
@@ -181,7 +221,7 @@ size_t fp8kv_paged_attention_workspace_size(int B, int M, int Hq, int Hkv, int D
  * row itself is window_left = W - 1).  Logical key j lives in physical page
  * block_table[b][j / page_size] at offset j % page_size.  With
  * Kd = decode(k_code) * k_scale, Vd = decode(v_code) * v_scale (BF16 cache:
- * the stored values, scales unused):
+ * the stored values, scales unused; INT4 cache: n s k_scale, n s v_scale):
  *     out[b][m][h] = softmax_j( (q . Kd_j) * sm_scale ) . Vd      (rounded to bf16)
  * computed with fp32 accumulation.  Long contexts are cut into partitions of
  * split_tokens keys whose partial (max, sum, unnormalised output) are combined
@@ -195,7 +235,7 @@ size_t fp8kv_paged_attention_workspace_size(int B, int M, int Hq, int Hkv, int D
  *   block_table  (device) int32 [B][max_pages_per_seq]; entries of pages with
  *                no visible key are never read
  *   seq_lens     (device) int32 [B]; max_seq_len (host) >= every seq_lens[b]
- *   k_scale, v_scale (device) fp32 scalars (E4M3 only)
+ *   k_scale, v_scale (device) fp32 scalars (E4M3 and INT4 only)
  *   sm_scale     (host) fp32 logit multiplier, e.g. 1/sqrt(D)
  *   window_left  (host) -1 for a global layer, else >= 0
  *   split_tokens (host) 0 = automatic, else a multiple of page_size

@@ -1,0 +1,373 @@
+"""The INT4 cache: its definition (CPU), argument checks (CPU), and insert,
+append, gather and paged attention on the GPU against the numpy oracle."""
+import ctypes
+
+import numpy as np
+import pytest
+import torch
+
+from oracle import int4_np
+from verify_attention_gb300 import build, fp8kv, inputs as gen
+
+NULL = ctypes.c_void_p(0)
+P16 = ctypes.c_void_p(1 << 20)          # fake, 16-byte aligned: never dereferenced
+SM = 128 ** -0.5
+
+
+@pytest.fixture(scope="module")
+def L():
+    build.build()
+    return fp8kv.lib()
+
+
+# ------------------------------------------------------------ definition
+
+def _bf16(x):
+    return torch.tensor(np.asarray(x, np.float32)).to(torch.bfloat16)
+
+
+def test_e4m3_codec_against_the_format():
+    v = int4_np.e4m3_value(np.arange(256))
+    assert v[0x7e] == 448 and v[1] == 2.0 ** -9 and np.isnan(v[0x7f]) and v[0x38] == 1.0
+    assert np.array_equal(int4_np.e4m3_code(v[:127]), np.arange(127))
+    mid = (v[:126] + v[1:127]) / 2                       # ties go to the even code
+    assert np.array_equal(int4_np.e4m3_code(mid), np.arange(126) + np.arange(126) % 2)
+    assert int4_np.e4m3_code(np.array([1e9, np.inf]))[0] == 0x7e
+
+
+@pytest.mark.parametrize("c", [1.0, 0.0123, 37.0])
+def test_encode_is_within_half_a_step(c):
+    x = _bf16(np.random.default_rng(3).normal(size=(50, 2, 128)) * c * 20).float().numpy()
+    n, sc = int4_np.encode_rows(x, c)
+    step = np.repeat(int4_np.e4m3_value(sc), 16, -1) * float(np.float32(c))
+    # amax / step <= 7 (1 + 2^-4) < 7.5: clamping never costs more than rounding;
+    # the fp32 roundings of s c, its reciprocal and the product: 3 * 2^-24 of n
+    assert np.all(np.abs(x - n * step) <= step * (0.5 + 8 * 2.0 ** -22))
+
+
+def test_page_bytes_round_trip():
+    rng = np.random.default_rng(5)
+    n = rng.integers(-7, 8, (40, 3, 128)).astype(np.int8)
+    sc = rng.integers(1, 127, (40, 3, 8)).astype(np.uint8)
+    cache = np.zeros((2, 3, 32 * 72), np.uint8)
+    slots = rng.permutation(64)[:40]
+    int4_np.write_rows(cache, 32, slots, n, sc)
+    got = int4_np.read_pages(cache, 32)[slots // 32, :, slots % 32]
+    assert np.array_equal(got, n * np.repeat(int4_np.e4m3_value(sc), 16, -1))
+
+
+# ------------------------------------------------------- argument checks
+
+def test_int4_entry_points_check_their_arguments(L):
+    ins = [P16, P16, P16, 4, 8, 128, P16, P16, P16, P16, 16, 32, 2, NULL]
+    for at, bad, want in ((0, NULL, 1), (6, NULL, 1), (7, NULL, 1), (5, 96, 2), (11, 48, 2), (3, -1, 1), (3, 0, 0),
+                          (8, ctypes.c_void_p((1 << 20) + 8), 1), (12, 3, 1)):
+        assert L.fp8kv_cache_insert(*[bad if i == at else a for i, a in enumerate(ins)]) == want, at
+    gat = [P16, 4, 8, 128, P16, P16, P16, P16, 16, 32, 2, P16, P16, NULL]
+    for at, bad, want in ((0, NULL, 1), (4, NULL, 1), (6, NULL, 1), (11, NULL, 1), (3, 64, 2), (9, 16, 2), (10, 5, 1),
+                          (1, 0, 0), (1, -1, 1), (12, ctypes.c_void_p((1 << 20) + 4), 1)):
+        for dt in (0, 2):
+            a = [bad if i == at else (dt if i == 10 else x) for i, x in enumerate(gat)]
+            assert L.fp8kv_cache_gather(*a) == want, (at, dt)
+    att = dict(q=P16, k=P16, v=P16, dt=2, bt=P16, mpps=4, sl=P16, maxL=100, B=1, M=1, Hq=72, Hkv=8, D=128, ps=32, P=16,
+               ks=P16, vs=P16, sm=0.088, wl=-1, split=32, ws=P16, wsb=1 << 30, out=P16, stream=NULL)
+    for over, want in (({"ks": NULL}, 1), ({"vs": NULL}, 1), ({"M": 17, "split": 0}, 2), ({"D": 64}, 2),
+                       ({"M": 16, "Hq": 80, "split": 0}, 2), ({"ws": NULL}, 3), ({"wsb": 16}, 3), ({"maxL": 200}, 1),
+                       ({"ps": 16, "split": 0}, 2), ({"wl": -2}, 1), ({"B": 0}, 0),
+                       ({"k": ctypes.c_void_p((1 << 20) + 8)}, 1)):
+        assert L.fp8kv_paged_attention(*{**att, **over}.values()) == want, over
+    layers = (fp8kv.fp8kv_layer * 1)()
+    assert L.fp8kv_paged_attention_layers(ctypes.byref(layers), 1, 1, 12, 72, 8, 128, 32, 2, P16, 1 << 30, NULL) in (1, 2)
+
+
+def test_binding_refuses_other_shapes():
+    assert fp8kv._cache_dtype(torch.zeros((2, 8, 32 * 72), dtype=torch.uint8)) == fp8kv.FP8KV_CACHE_INT4
+    assert fp8kv._cache_dtype(torch.zeros((2, 8, 32, 128), dtype=torch.uint8)) == fp8kv.FP8KV_CACHE_E4M3
+    c = torch.zeros((2, 8, 32 * 72), dtype=torch.uint8)
+    assert fp8kv._cache_shape(c, c, 2) == (2, 8, 32)
+    with pytest.raises(ValueError):
+        fp8kv._cache_shape(torch.zeros((2, 8, 100), dtype=torch.uint8), c, 2)
+    with pytest.raises(ValueError):
+        fp8kv._cache_shape(c, torch.zeros((3, 8, 32 * 72), dtype=torch.uint8), 2)
+
+
+# --------------------------------------------------------------- GPU: rows
+
+def _scale(c):
+    return torch.tensor([c], dtype=torch.float32, device="cuda")
+
+
+def _insert(k, v, slots, pages, ps, ck, cv, poison=0xA5):
+    kc = torch.full((pages, k.shape[1], ps * 72), poison, dtype=torch.uint8, device="cuda")
+    vc = kc.clone()
+    fp8kv.fp8kv_cache_insert(k.cuda(), v.cuda(), slots.cuda(), _scale(ck), _scale(cv), kc, vc)
+    return kc, vc
+
+
+def _special(rng, T, H):
+    """Rows with zeros, signed zeros, tiny and huge values, infinities and NaN."""
+    x = rng.normal(size=(T, H, 128)).astype(np.float32)
+    for i, val in enumerate((0.0, -0.0, 1e-38, -3e38, np.inf, -np.inf, np.nan, 1e-5, 7.5, 2.0 ** -20)):
+        x[i % T, i % H, (13 * i) % 128] = val
+        x[(i + 3) % T, (i + 1) % H, 16 * (i % 8):16 * (i % 8) + 16] = val
+    return _bf16(x)
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("T,H,ps,ck,cv", [(1, 1, 32, 1.0, 1.0), (7, 2, 64, 0.01, 2.0), (97, 8, 32, 12 / 448, 6 / 448),
+                                          (300, 3, 64, 1e-3, 1e4), (33, 5, 32, 2.0 ** -100, 2.0 ** 100)])
+def test_insert_is_bit_exact(T, H, ps, ck, cv):
+    rng = np.random.default_rng(T)
+    k, v = _special(rng, T, H), _special(rng, T, H)
+    pages = T // ps + 2
+    slots = torch.from_numpy(rng.permutation(pages * ps)[:T].copy())
+    if T > 2:
+        slots[T // 2] = -1
+        slots[1] = -7
+    kc, vc = _insert(k, v, slots, pages, ps, ck, cv)
+    for x, c, got in ((k, ck, kc), (v, cv, vc)):
+        want = np.full((pages, H, ps * 72), 0xA5, np.uint8)
+        int4_np.write_rows(want, ps, slots.numpy(), *int4_np.encode_rows(x.float().numpy(), c))
+        assert np.array_equal(got.cpu().numpy(), want)
+
+
+@pytest.mark.gpu
+def test_every_bf16_value_in_one_block():
+    """Each of the 65536 bf16 patterns as a block of its own beside a 1.0."""
+    bits = np.arange(65536, dtype=np.uint32)
+    x = np.full((512, 1, 128), 1.0, np.float32).reshape(-1, 16)
+    x = np.concatenate([x] * 16)                          # 65536 blocks
+    x[:, 5] = (bits << 16).view(np.float32)
+    x = torch.from_numpy(x.reshape(8192, 1, 128)).to(torch.bfloat16)
+    slots = torch.arange(8192)
+    kc, _ = _insert(x, x, slots, 256, 32, 0.037, 0.037)
+    want = np.zeros((256, 1, 32 * 72), np.uint8)
+    int4_np.write_rows(want, 32, slots.numpy(), *int4_np.encode_rows(x.float().numpy(), 0.037))
+    assert np.array_equal(kc.cpu().numpy(), want)
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("dt", ["int4", "e4m3", "bf16"])
+@pytest.mark.parametrize("T,H,ps", [(1, 1, 64), (45, 8, 32), (130, 3, 64)])
+def test_gather_reads_back_what_is_stored(dt, T, H, ps):
+    rng = np.random.default_rng(T + H)
+    k, v = _special(rng, T, H).cuda(), _bf16(rng.normal(size=(T, H, 128))).cuda()
+    pages = T // ps + 2
+    if dt == "int4":
+        kc = fp8kv.fp8kv_int4_cache(pages, H, ps)
+    else:
+        kc = torch.zeros((pages, H, ps, 128), dtype=torch.uint8 if dt == "e4m3" else torch.bfloat16, device="cuda")
+    vc = kc.clone()
+    slots = torch.from_numpy(rng.permutation(pages * ps)[:T].copy()).cuda()
+    ks, vs = _scale(0.02), _scale(0.013)
+    fp8kv.fp8kv_cache_insert(k, v, slots, ks, vs, kc, vc)
+    read = torch.cat([slots, slots[:1], torch.tensor([-1], device="cuda")])          # a slot twice, one skipped
+    ko = torch.full((T + 2, H, 128), 3.0, dtype=torch.bfloat16, device="cuda")
+    vo = ko.clone()
+    fp8kv.fp8kv_cache_gather(read, ks, vs, kc, vc, ko, vo)
+    for c, s, o in ((kc, ks, ko), (vc, vs, vo)):
+        if dt == "int4":
+            x = torch.from_numpy(int4_np.read_pages(c.cpu().numpy(), ps)).float()
+        elif dt == "e4m3":
+            x = torch.from_numpy(int4_np.e4m3_value(c.cpu().numpy())).float()
+        else:
+            x = c.float().cpu()
+        x = x if dt == "bf16" else x * s.cpu()
+        at = read.cpu()[:-1]
+        want = x[at // ps, :, at % ps].to(torch.bfloat16)
+        assert torch.equal(torch.nan_to_num(o[:-1].cpu(), nan=99.0), torch.nan_to_num(want, nan=99.0))
+        assert bool((o[-1] == 3.0).all())
+
+
+@pytest.mark.gpu
+def test_bad_slots_are_flagged_and_skipped():
+    fp8kv.fp8kv_device_status(clear=True)
+    k = _bf16(np.ones((3, 2, 128)))
+    slots = torch.tensor([5, 64, 1 << 40])
+    kc, vc = _insert(k, k, slots, 2, 32, 1.0, 1.0)
+    assert fp8kv.fp8kv_device_status(clear=True) == fp8kv.DEV_BAD_SLOT
+    rest = torch.cat([kc[0, :, :5 * 64].flatten(), kc[0, :, 6 * 64:32 * 64].flatten(), kc[1].flatten()])
+    assert bool((rest == 0xA5).all())
+    o = torch.full((3, 2, 128), 7.0, dtype=torch.bfloat16, device="cuda")
+    fp8kv.fp8kv_cache_gather(slots.cuda(), _scale(1.0), _scale(1.0), kc, vc, o, o.clone())
+    assert fp8kv.fp8kv_device_status(clear=True) == fp8kv.DEV_BAD_SLOT
+    # a block of ones with tensor scale 1: s is the E4M3 value nearest to 1/7 =
+    # 0.142857..., between 9/64 = 0.140625 and 10/64 the former, n = rint(64/9) = 7,
+    # and the row reads as 7 * 9/64 = 0.984375 (exact in bf16)
+    assert bool((o[0] == 0.984375).all()) and bool((o[1:] == 7.0).all())
+
+
+# ---------------------------------------------------------- GPU: attention
+
+def _case(seed, lens, M, G, H, ps, extra=1):
+    g = gen.generator(seed)
+    lay = gen.paged_layout(lens, ps, g, extra_pages=extra)
+    B = len(lens)
+    q = torch.randn((B, M, G * H, 128), generator=g).to(torch.bfloat16).cuda()
+    # stale bytes everywhere (NaN scales, arbitrary codes) behind what is written
+    kc = torch.full((lay.num_pages, H, ps * 72), 0x7F, dtype=torch.uint8, device="cuda")
+    vc = kc.clone()
+    ks, vs = _scale(6 / 448), _scale(5 / 448)
+    x = [torch.randn((sum(lens), H, 128), generator=g).to(torch.bfloat16).cuda() for _ in range(2)]
+    slots = torch.cat([lay.slots(b, range(n)) for b, n in enumerate(lens)]).cuda()
+    return lay, q, kc, vc, ks, vs, x[0], x[1], slots
+
+
+def _attend(lay, q, kc, vc, ks, vs, window=-1, **kw):
+    return fp8kv.fp8kv_paged_attention(q, kc, vc, lay.block_table.cuda(), lay.seq_lens.cuda(), int(lay.seq_lens.max()),
+                                       ks, vs, SM, window_left=window, **kw)
+
+
+def _check(out, lay, q, kc, vc, ks, vs, ps, window=-1, rows=None):
+    ref, mag, lmag, vsum = int4_np.paged_attention(q.double().cpu().numpy(), kc.cpu().numpy(), vc.cpu().numpy(), ps,
+                                                   lay.block_table.numpy(), lay.seq_lens.numpy(), ks.item(), vs.item(),
+                                                   SM, window)
+    # bf16 output: half a step, 2^-8 of the value.  Softmax weights: f16 of 2^15
+    # times the weight against the running maximum, off by 2^-11 of itself (with
+    # exponentials, sums and the f32 product with the scale below 2^-14 more:
+    # under 2^-10 of mag) or, below f16's normal range, by 2^-25, that is 2^-40
+    # of the row's sum (at least 2^15): 2^-40 vsum.  Logits: a sum of 128
+    # products is eight accumulating steps of 16, each off by at most an ulp
+    # (2^-23) of the partial sum, whose size is at most a: 8 * 2^-23 a, which
+    # moves the output by at most 2^-20 lmag.  (That term matters only where
+    # |q| |k| is in the hundreds: with a = 560, 2 * 560 * 2^-20 is already 2^-10.)
+    err = np.abs(out.double().cpu().numpy() - ref)
+    tol = 2.0 ** -8 * np.abs(ref) + 2.0 ** -10 * mag + 2.0 ** -20 * lmag + 2.0 ** -40 * vsum
+    assert np.all(err <= tol), (float((err / tol).max()), float(err.max()))
+
+
+ATTENTION = [
+    # lens, M, G, H, ps, window, split_tokens
+    ([1], 1, 1, 1, 32, -1, 0),
+    ([256], 1, 9, 8, 32, -1, 0),
+    ([33, 1, 64, 500], 1, 4, 2, 64, -1, 64),
+    ([31, 32, 33, 63, 65], 1, 12, 1, 32, -1, 32),
+    ([5000], 1, 9, 2, 64, -1, 0),
+    ([3001, 2, 1024], 2, 8, 2, 32, -1, 256),
+    ([1500, 700], 1, 16, 2, 32, 99, 0),
+    ([400, 90], 1, 9, 2, 64, 0, 0),
+    ([12, 300], 12, 9, 2, 32, -1, 0),
+    ([1000], 12, 9, 2, 64, -1, 0),
+    ([1000], 12, 9, 2, 32, -1, 96),
+    ([2100, 13, 640], 12, 9, 1, 32, 511, 0),
+    ([777, 40], 7, 5, 3, 64, 20, 0),
+    ([2500, 130], 16, 9, 1, 64, -1, 0),
+    ([600], 16, 1, 2, 32, 100, 64),
+    ([300, 17], 3, 6, 2, 32, -1, 0),
+]
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("lens,M,G,H,ps,window,split", ATTENTION)
+def test_attention_matches_the_oracle(lens, M, G, H, ps, window, split):
+    fp8kv.fp8kv_device_status(clear=True)
+    lay, q, kc, vc, ks, vs, k, v, slots = _case(sum(lens) + M, lens, M, G, H, ps)
+    fp8kv.fp8kv_cache_insert(k, v, slots, ks, vs, kc, vc)
+    out = _attend(lay, q, kc, vc, ks, vs, window, split_tokens=split)
+    assert "int4" in fp8kv.fp8kv_last_dispatch()
+    _check(out, lay, q, kc, vc, ks, vs, ps, window)
+    assert fp8kv.fp8kv_device_status(clear=True) == 0
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("lens,M,G,H,ps,window", [([1, 70], 1, 9, 2, 32, -1), ([12, 95, 1000], 12, 9, 2, 32, -1),
+                                                  ([2000], 12, 9, 2, 64, 127), ([64, 65], 4, 4, 3, 64, -1)])
+def test_append_equals_insert_then_attention(lens, M, G, H, ps, window):
+    lay, q, kc, vc, ks, vs, k, v, slots = _case(7 * sum(lens), lens, M, G, H, ps)
+    fp8kv.fp8kv_cache_insert(k, v, slots, ks, vs, kc, vc)
+    want = _attend(lay, q, kc, vc, ks, vs, window)
+    _check(want, lay, q, kc, vc, ks, vs, ps, window)
+    new = torch.cat([torch.arange(sum(lens[:b + 1]) - M, sum(lens[:b + 1])) for b in range(len(lens))]).cuda()
+    kc2, vc2 = kc.clone(), vc.clone()
+    old = torch.ones(len(slots), dtype=torch.bool, device="cuda")
+    old[new] = False
+    zero = torch.zeros_like(k)
+    fp8kv.fp8kv_cache_insert(zero, zero, torch.where(old, -1, slots), ks, vs, kc2, vc2)     # new rows wiped
+    shape = (len(lens), M, H, 128)
+    out = fp8kv.fp8kv_append_paged_attention(k[new].view(shape), v[new].view(shape), q, kc2, vc2,
+                                             lay.block_table.cuda(), lay.seq_lens.cuda(), max(lens), ks, vs, SM,
+                                             window_left=window)
+    assert torch.equal(kc2, kc) and torch.equal(vc2, vc)
+    assert torch.equal(out, want)
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("M", [1, 12])
+def test_extreme_scales_logits_and_values(M):
+    """Block scales up to 448 (a tensor scale far below the calibrated one) and
+    at the smallest step, queries of very different sizes, one dominant key."""
+    lay, q, kc, vc, ks, vs, k, v, slots = _case(91 + M, [700], M, 9, 2, 32)
+    k[::7] *= 100
+    k[3::7] *= 1e-4
+    k[123] *= 5
+    v[::5] *= 300
+    q[:, :, ::2] *= 2.0 ** -30
+    q[:, :, 5] = 0
+    ks, vs = _scale(2e-2), _scale(1e-2)
+    fp8kv.fp8kv_cache_insert(k, v, slots, ks, vs, kc, vc)
+    assert int(kc[:, :, 32 * 64:].max()) >= 0x70
+    out = _attend(lay, q, kc, vc, ks, vs)
+    _check(out, lay, q, kc, vc, ks, vs, 32)
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("M,split", [(1, 0), (1, 128), (12, 0), (12, 128)])
+def test_bad_pages_read_zeros_and_bad_lengths_leave_the_output(M, split):
+    fp8kv.fp8kv_device_status(clear=True)
+    lens = [200, 90, 150]
+    lay, q, kc, vc, ks, vs, k, v, slots = _case(17, lens, M, 9, 2, 32)
+    fp8kv.fp8kv_cache_insert(k, v, slots, ks, vs, kc, vc)
+    lay.block_table[0, 2] = lay.num_pages + 5
+    lay.block_table[0, 3] = -3
+    out = _attend(lay, q, kc, vc, ks, vs, split_tokens=split)
+    _check(out, lay, q, kc, vc, ks, vs, 32)
+    assert fp8kv.fp8kv_device_status(clear=True) == 0
+    sl = lay.seq_lens.cuda()
+    sl[1] = M - 1                                       # fewer keys than rows
+    sl[2] = 201                                         # above max_seq_len
+    out2 = torch.full_like(q, 3.0)
+    fp8kv.fp8kv_paged_attention(q, kc, vc, lay.block_table.cuda(), sl, 200, ks, vs, SM, split_tokens=split, out=out2)
+    assert fp8kv.fp8kv_device_status(clear=True) == fp8kv.DEV_BAD_SEQ_LEN
+    assert torch.equal(out2[0], out[0]) and bool((out2[1:] == 3.0).all())
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("M", [1, 12])
+def test_noalloc_prepared_and_captured_calls(M):
+    lay, q, kc, vc, ks, vs, k, v, slots = _case(29, [1500, 800], M, 9, 2, 32)
+    fp8kv.fp8kv_cache_insert(k, v, slots, ks, vs, kc, vc)
+    bt, sl = lay.block_table.cuda(), lay.seq_lens.cuda()
+    want = _attend(lay, q, kc, vc, ks, vs)
+    out = torch.empty_like(q)
+    fp8kv.fp8kv_paged_attention_noalloc(q, kc, vc, bt, sl, 1500, ks, vs, SM, out)
+    assert torch.equal(out, want)
+    # two prepared calls captured into one graph, on two side streams, each
+    # with its own workspace; replayed with other queries in place
+    calls = [fp8kv.PreparedAttention(q, kc, vc, bt, sl, 1500, ks, vs, SM) for _ in range(2)]
+    side = [torch.cuda.Stream() for _ in range(2)]
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        main = torch.cuda.current_stream()
+        for c, s in zip(calls, side):
+            s.wait_stream(main)
+            with torch.cuda.stream(s):
+                c()
+            main.wait_stream(s)
+    q.copy_(q.flip(0))
+    want = _attend(lay, q, kc, vc, ks, vs)
+    for _ in range(3):
+        graph.replay()
+    torch.cuda.synchronize()
+    assert all(torch.equal(c.out, want) for c in calls)
+
+
+@pytest.mark.gpu
+def test_page_order_does_not_matter():
+    lay, q, kc, vc, ks, vs, k, v, slots = _case(31, [900], 12, 9, 2, 32)
+    fp8kv.fp8kv_cache_insert(k, v, slots, ks, vs, kc, vc)
+    want = _attend(lay, q, kc, vc, ks, vs)
+    perm = torch.randperm(lay.num_pages)
+    inv = torch.empty_like(perm)
+    inv[perm] = torch.arange(lay.num_pages)
+    lay.block_table = inv[lay.block_table.long()].to(torch.int32)
+    assert torch.equal(_attend(lay, q, kc[perm.cuda()], vc[perm.cuda()], ks, vs), want)

@@ -1048,8 +1048,9 @@ static int attention_call(const void* k_new, const void* v_new, const void* q, c
                           int page_size, int num_pages, const float* k_scale, const float* v_scale, int scale_stride,
                           float sm_scale, int window_left, int split_tokens, void* workspace, size_t workspace_bytes,
                           void* out, void* stream) {
-    if (cache_dtype != FP8KV_CACHE_E4M3 && cache_dtype != FP8KV_CACHE_BF16) return FP8KV_ERR_INVALID_ARG;
-    const bool fp8 = cache_dtype == FP8KV_CACHE_E4M3;
+    if (cache_dtype != FP8KV_CACHE_E4M3 && cache_dtype != FP8KV_CACHE_BF16 && cache_dtype != FP8KV_CACHE_INT4)
+        return FP8KV_ERR_INVALID_ARG;
+    const bool fp8 = cache_dtype == FP8KV_CACHE_E4M3, int4 = cache_dtype == FP8KV_CACHE_INT4;
     Plan plan;
     int rc = make_plan(B, M, Hq, Hkv, D, page_size, max_seq_len, window_left, split_tokens, &plan);
     if (rc) return rc;
@@ -1062,7 +1063,7 @@ static int attention_call(const void* k_new, const void* v_new, const void* q, c
     if (!q || !k_cache || !v_cache || !block_table || !seq_lens || !out) return FP8KV_ERR_INVALID_ARG;
     if ((k_new != nullptr) != (v_new != nullptr) || (k_new && (!al16(k_new) || !al16(v_new))))
         return FP8KV_ERR_INVALID_ARG;
-    if (fp8 && (!k_scale || !v_scale)) return FP8KV_ERR_INVALID_ARG;
+    if ((fp8 || int4) && (!k_scale || !v_scale)) return FP8KV_ERR_INVALID_ARG;
     if (!al16(q) || !al16(k_cache) || !al16(v_cache) || !al16(out)) return FP8KV_ERR_INVALID_ARG;
     if (num_pages <= 0 || max_pages_per_seq <= 0) return FP8KV_ERR_INVALID_ARG;
     if (max_seq_len < M || (int64_t)max_seq_len > (int64_t)max_pages_per_seq * page_size)
@@ -1072,8 +1073,8 @@ static int attention_call(const void* k_new, const void* v_new, const void* q, c
     if (need && (!workspace || workspace_bytes < need || !al16(workspace))) return FP8KV_ERR_WORKSPACE;
 
     CUtensorMap tk, tv;
-    if (!cache_map(&tk, k_cache, fp8, Hkv, page_size, num_pages) ||
-        !cache_map(&tv, v_cache, fp8, Hkv, page_size, num_pages))
+    if (!int4 && (!cache_map(&tk, k_cache, fp8, Hkv, page_size, num_pages) ||
+                  !cache_map(&tv, v_cache, fp8, Hkv, page_size, num_pages)))
         return FP8KV_ERR_CUDA;
 
     AttnParams P = {};
@@ -1122,6 +1123,32 @@ static int attention_call(const void* k_new, const void* v_new, const void* q, c
     P.max_seq_len = max_seq_len;
 
     cudaStream_t s = (cudaStream_t)stream;
+    if (int4) {
+        P.k_cache = (uint8_t*)k_cache;
+        P.v_cache = (uint8_t*)v_cache;
+        P.num_pages = num_pages;
+        if (k_new) {
+            rc = launch_append_int4(k_new, v_new, seq_lens, block_table, max_pages_per_seq, B, M, Hkv, k_scale,
+                                    v_scale, (void*)k_cache, (void*)v_cache, num_pages, page_size, max_seq_len, s);
+            if (rc) return rc;
+        }
+        char text[256];
+        rc = launch_attention_int4(P, s, text, sizeof text);
+        if (rc) return rc;
+        if (plan.num_splits > 1) {
+            const int64_t warps = (int64_t)B * M * Hq;
+            cudaError_t e = launch_pdl(attn_reduce_kernel<false>, dim3((unsigned)((warps + 7) / 8)), dim3(256), 0, s,
+                                       (const float*)P.ws_o, (const float*)P.ws_ml, seq_lens, B, M, Hq, P.G, P.R,
+                                       max_pages_per_seq, page_size, window_left, plan.split_pages, plan.num_splits,
+                                       max_seq_len, v_scale, scale_stride, (uint16_t*)out);
+            if (e != cudaSuccess) {
+                cudaGetLastError();
+                return FP8KV_ERR_CUDA;
+            }
+        }
+        set_dispatch(text);
+        return FP8KV_OK;
+    }
     const int RT = use_tc ? row_tiles(M, Hq, Hkv) : 1;
     // one sequence in at most 8 partitions and one row tile: the partitions
     // of a KV head run as one thread-block cluster and combine in distributed

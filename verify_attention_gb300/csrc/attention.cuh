@@ -84,6 +84,16 @@ int launch_append(const void* k, const void* v, const int32_t* seq_lens, const i
                   void* v_cache,
                   int num_pages, int page_size, bool fp8, cudaStream_t s);
 
+// The same for an INT4 cache (insert.cu).
+int launch_append_int4(const void* k, const void* v, const int32_t* seq_lens, const int32_t* block_table, int mpps,
+                       int B, int M, int Hkv, const float* k_scale, const float* v_scale, void* k_cache,
+                       void* v_cache, int num_pages, int page_size, int max_seq_len, cudaStream_t s);
+
+// Host launcher of the INT4 cache kernel (attention_int4.cu): partials as the
+// mma.sync kernels write them (fp32 O * v_scale, (max, sum)), partitions cut
+// from the key range of all R rows.  `text` describes the launch.
+int launch_attention_int4(const AttnParams& P, cudaStream_t s, char* text, size_t text_bytes);
+
 // Host launcher of the tcgen05 kernel (attention_tc.cu).  Returns
 // FP8KV_ERR_UNSUPPORTED when the shape is not one it implements.
 int launch_attention_tc(const CUtensorMap& tk, const CUtensorMap& tv, const AttnParams& P, cudaStream_t s);

@@ -1,0 +1,433 @@
+// attention_int4.cu -- paged decode / verifier attention over a cache held in
+// 4 bits (FP8KV_CACHE_INT4, include/fp8kv.h): per 16 elements an E4M3 scale s
+// and integers n in [-7, 7], value n s c with the tensor scale c.
+//
+// What bounds it: a row is 72 bytes, K and V of one token and head 144 for 256
+// elements, so one SM's share of the HBM rate brings about 42 elements a cycle
+// and the instructions that widen them count.  Widening is exact and costs one
+// logic operation and one fma for two elements: the code n + 8 becomes the low
+// mantissa bits of the f16 values 256 + code or 16 + code (bits 2..5 or 6..9
+// of the half word), and fma(v, s, -264 s) or fma(v, s, -24 s) is n s exactly
+// (264 s and 24 s have at most 10 significant bits, n s at most 7).  Two
+// shifts serve the eight codes of a word.  The tensor scales are applied to
+// the logits and to the output.
+//
+// One CTA per (partition, KV head x tile of 16 query rows, sequence).  Its
+// warps take chunks of 32 keys in turn, each with its own ring of chunks
+// filled by cp.async (no producer, no barriers), and run both products on
+// mma.sync m16n8k16 (rows x keys, f16 in, fp32 out), online softmax in the
+// log2 domain; they merge through shared memory at the end.  Order of the
+// fragments: in Q.K^T a thread's B elements are 32 dimensions of one key (16
+// code bytes); in P.V they are the 16 dimensions of one scale block of four
+// keys.  Both are contiguous in a row, and the key order inside a group of
+// eight, key = 4 (n & 1) + (n >> 1) for column n, makes the eight-byte V reads
+// free of bank conflicts.
+#include <stdio.h>
+
+#include <mutex>
+#include <set>
+#include <utility>
+
+#include "attention.cuh"
+#include "common.cuh"
+
+namespace fp8kv {
+
+int status_attention_int4(unsigned int* s, int clear) { return read_status(s, clear); }
+
+namespace i4 {
+
+constexpr int WARPS = 12, THREADS = WARPS * 32;         // 168 registers a thread at one CTA per SM
+constexpr int STAGES = 4;                               // chunks of a warp's ring
+constexpr int CK = 32;                                  // keys per chunk
+constexpr int OFF_V = CK * kInt4CodeBytes;              // K codes, V codes, K scales, V scales
+constexpr int OFF_KS = 2 * CK * kInt4CodeBytes;
+constexpr int OFF_VS = OFF_KS + CK * kInt4ScaleBytes;
+constexpr int STAGE_BYTES = OFF_VS + CK * kInt4ScaleBytes;   // 4608
+constexpr int MERGE_STRIDE = 132;                       // floats per merged row: 128 of O, max, sum
+constexpr int SMEM = WARPS * STAGES * STAGE_BYTES;
+static_assert(WARPS * 16 * MERGE_STRIDE * 4 <= SMEM, "merge area exceeds the rings");
+
+__device__ __forceinline__ void cp16(uint32_t dst, const void* src, bool valid) {
+    asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst), "l"(src), "r"(valid ? 16 : 0) : "memory");
+}
+__device__ __forceinline__ void cp_commit() { asm volatile("cp.async.commit_group;" ::: "memory"); }
+template <int N>
+__device__ __forceinline__ void cp_wait() { asm volatile("cp.async.wait_group %0;" ::"n"(N) : "memory"); }
+
+__device__ __forceinline__ uint32_t hfma2(uint32_t a, uint32_t b, uint32_t c) {
+    uint32_t r;
+    asm("fma.rn.f16x2 %0, %1, %2, %3;" : "=r"(r) : "r"(a), "r"(b), "r"(c));
+    return r;
+}
+__device__ __forceinline__ uint32_t hmul2(uint32_t a, uint32_t b) {
+    uint32_t r;
+    asm("mul.rn.f16x2 %0, %1, %2;" : "=r"(r) : "r"(a), "r"(b));
+    return r;
+}
+
+// The four codes of each half word of z times the scales of s (f16x2, one per
+// half word) over 4: v[i] = the i-th codes' values n s / 4.
+struct Scale2 {
+    uint32_t s, c256, c16;      // s / 4, -264 s / 4, -24 s / 4
+};
+__device__ __forceinline__ Scale2 scale2(uint32_t s) {
+    return {hmul2(s, 0x34003400u), hmul2(s, 0xd420d420u), hmul2(s, 0xc600c600u)};
+}
+__device__ __forceinline__ void widen4(uint32_t z, const Scale2& k, uint32_t (&v)[4]) {
+    const uint32_t x = z << 2, y = z >> 6;
+    v[0] = hfma2((x & 0x003c003cu) | 0x5c005c00u, k.s, k.c256);
+    v[1] = hfma2((x & 0x03c003c0u) | 0x4c004c00u, k.s, k.c16);
+    v[2] = hfma2((y & 0x003c003cu) | 0x5c005c00u, k.s, k.c256);
+    v[3] = hfma2((y & 0x03c003c0u) | 0x4c004c00u, k.s, k.c16);
+}
+
+// Issue the copies of chunk `key0 / 32` of page `page` into a stage: K rows at
+// their column position (see the key order above), V rows with the 16-byte
+// units exchanged on keys 2 and 3 of 4.  Pages outside the pool read as zeros.
+template <int PS>
+__device__ __forceinline__ void issue_chunk(uint32_t stage, const AttnParams& P, int page, int hk, int key_in_page,
+                                            int lane) {
+    const bool valid = page >= 0 && page < P.num_pages;
+    const int64_t base = valid ? ((int64_t)page * P.Hkv + hk) * (PS * kInt4RowBytes) : 0;
+    const uint8_t* kp = P.k_cache + base;
+    const uint8_t* vp = P.v_cache + base;
+    const int code0 = key_in_page * kInt4CodeBytes, scale0 = PS * kInt4CodeBytes + key_in_page * kInt4ScaleBytes;
+#pragma unroll
+    for (int u = 0; u < 4; ++u) {
+        const int i = lane + 32 * u, row = i >> 2, ch = i & 3;
+        const int kpos = (row & ~7) | ((row & 3) << 1) | ((row >> 2) & 1);
+        cp16(stage + kpos * 64 + ch * 16, kp + code0 + i * 16, valid);
+        cp16(stage + OFF_V + row * 64 + ((ch ^ (row & 2)) << 4), vp + code0 + i * 16, valid);
+    }
+    const uint8_t* sp = lane < 16 ? kp : vp;
+    cp16(stage + OFF_KS + lane * 16, sp + scale0 + (lane & 15) * 16, valid);
+}
+
+template <int PS>
+__global__ void __launch_bounds__(THREADS, 1) paged_attention_int4_kernel(AttnParams P) {
+    extern __shared__ __align__(128) uint8_t smem[];
+    const int split = blockIdx.x, rt = blockIdx.y % P.NT, hk = blockIdx.y / P.NT, b = blockIdx.z;
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    const int g = lane >> 2, t = lane & 3;
+    pdl_launch_dependents();
+    pdl_wait();
+    const int L = P.seq_lens[b];
+    if (L < P.M || L > P.max_seq_len || (L + PS - 1) / PS > P.mpps) {
+        if (threadIdx.x == 0 && split == 0 && blockIdx.y == 0) flag(FP8KV_DEV_BAD_SEQ_LEN);
+        return;
+    }
+    // partitions are cut from the keys that any of the R rows sees
+    const int lo0 = (P.window_left >= 0) ? max(0, L - P.M - P.window_left) : 0;
+    const int first_page = lo0 / PS, last_page = (L - 1) / PS;
+    const int nsplit_b = (last_page - first_page + P.split_pages) / P.split_pages;
+    if (nsplit_b > P.num_splits) {   // cannot happen when L <= max_seq_len; never index past the plan
+        if (threadIdx.x == 0 && split == 0 && blockIdx.y == 0) flag(FP8KV_DEV_BAD_SEQ_LEN);
+        return;
+    }
+    if (split >= nsplit_b) return;
+    const int page_begin = first_page + split * P.split_pages;
+    const int n_pages = min(P.split_pages, last_page + 1 - page_begin);
+    const int key_begin = page_begin * PS;
+    const int n_chunks = (min(n_pages * PS, L - key_begin) + CK - 1) / CK;
+    const int32_t* bt = P.block_table + (int64_t)b * P.mpps + page_begin;
+    const uint32_t ring = smem_u32(smem) + warp * STAGES * STAGE_BYTES;
+    constexpr int CPP = PS / CK;                        // chunks per page
+
+    // this warp's chunks: warp, warp + WARPS, ...; their page ids are read one
+    // round ahead of the copies
+    int next = warp;
+    int page = next < n_chunks ? bt[next / CPP] : -1;
+    auto issue = [&](int slot) {
+        if (next < n_chunks) {
+            const int cur = page, at = next;
+            next += WARPS;
+            page = next < n_chunks ? bt[next / CPP] : -1;
+            issue_chunk<PS>(ring + slot * STAGE_BYTES, P, cur, hk, (at % CPP) * CK, lane);
+        }
+        cp_commit();
+    };
+#pragma unroll
+    for (int s = 0; s < STAGES - 1; ++s) issue(s);
+
+    // ---- rows g and g + 8 of the tile: positions, Q fragments
+    const int R0 = rt * 16;
+    int pr[2], lor[2];
+    float mult[2];
+    uint32_t qa[8][4];
+    {
+        float qf[2][32];
+        const float ks = *P.k_scale;
+#pragma unroll
+        for (int hr = 0; hr < 2; ++hr) {
+            const int r = R0 + g + 8 * hr;
+            const int m = min(r, P.R - 1) / P.G;
+            pr[hr] = L - P.M + m;
+            lor[hr] = (P.window_left >= 0) ? max(0, pr[hr] - P.window_left) : 0;
+#pragma unroll
+            for (int j = 0; j < 32; ++j) qf[hr][j] = 0.f;
+            if (r < P.R) {
+                const uint4* src =
+                    (const uint4*)(P.q + (((int64_t)b * P.M + m) * P.Hq + hk * P.G + r % P.G) * 128) + 4 * t;
+#pragma unroll
+                for (int u = 0; u < 4; ++u) {
+                    const uint4 w = src[u];
+                    const uint32_t ww[4] = {w.x, w.y, w.z, w.w};
+#pragma unroll
+                    for (int e = 0; e < 4; ++e) {
+                        qf[hr][8 * u + 2 * e] = bf16_lo(ww[e]);
+                        qf[hr][8 * u + 2 * e + 1] = bf16_hi(ww[e]);
+                    }
+                }
+            }
+            // a power of two that puts the row maximum in [2^4, 2^5): the f16
+            // copy of q is then exact down to 2^-18 of the row maximum, and
+            // q . (n s) stays below 128 * 2^5 * 7 * 448 < 2^24
+            float amax = 0.f;
+#pragma unroll
+            for (int j = 0; j < 32; ++j) amax = fmaxf(amax, fabsf(qf[hr][j]));
+            amax = fmaxf(amax, __shfl_xor_sync(0xffffffffu, amax, 1));
+            amax = fmaxf(amax, __shfl_xor_sync(0xffffffffu, amax, 2));
+            int e = 4;
+            const uint32_t ab = __float_as_uint(amax);
+            if (amax > 0.f && ((ab >> 23) & 0xff) != 0xff) {
+                const int be = (int)((ab >> 23) & 0xff);
+                e = be ? be - 127 : -127;
+            }
+            const int sh = max(-120, min(120, 4 - e));
+            const float scale = ldexpf(1.0f, sh);
+#pragma unroll
+            for (int j = 0; j < 32; ++j) qf[hr][j] *= scale;
+            mult[hr] = 4.0f * ks * P.sm_scale * 1.4426950408889634f * ldexpf(1.0f, -sh);
+        }
+        // word w of a key's 16 code bytes holds dims 8w .. 8w + 7 of the 32;
+        // widen4 pairs dim f with f + 4, f = 0..3, and fills two k-steps
+#pragma unroll
+        for (int w = 0; w < 4; ++w) {
+#pragma unroll
+            for (int f = 0; f < 4; ++f) {
+                qa[2 * w + (f >> 1)][2 * (f & 1)] = pack_f16x2(qf[0][8 * w + f], qf[0][8 * w + f + 4]);
+                qa[2 * w + (f >> 1)][2 * (f & 1) + 1] = pack_f16x2(qf[1][8 * w + f], qf[1][8 * w + f + 4]);
+            }
+        }
+    }
+    // bounds of the warp's rows, to skip the masks on interior chunks
+    int pmin = min(pr[0], pr[1]), lomax = max(lor[0], lor[1]);
+#pragma unroll
+    for (int off = 4; off <= 16; off <<= 1) {
+        pmin = min(pmin, __shfl_xor_sync(0xffffffffu, pmin, off));
+        lomax = max(lomax, __shfl_xor_sync(0xffffffffu, lomax, off));
+    }
+
+    float o[16][4];
+#pragma unroll
+    for (int i = 0; i < 16; ++i) o[i][0] = o[i][1] = o[i][2] = o[i][3] = 0.f;
+    float mrow[2] = {-INFINITY, -INFINITY}, lrow[2] = {0.f, 0.f};
+
+    int slot = 0, fill = STAGES - 1;
+#pragma unroll 1
+    for (int c = warp; c < n_chunks; c += WARPS) {
+        cp_wait<STAGES - 2>();
+        __syncwarp();                                   // every lane's copies of this chunk; reads of the last one done
+        issue(fill);
+        fill = fill + 1 == STAGES ? 0 : fill + 1;
+        const uint8_t* st = smem + (warp * STAGES + slot) * STAGE_BYTES;
+        slot = slot + 1 == STAGES ? 0 : slot + 1;
+        const int k0 = key_begin + c * CK;
+
+        // ---- S = Q K^T
+        float sacc[4][4];
+#pragma unroll
+        for (int j = 0; j < 4; ++j) {
+            sacc[j][0] = sacc[j][1] = sacc[j][2] = sacc[j][3] = 0.f;
+            const uint4 kw4 = *(const uint4*)(st + (8 * j + g) * 64 + 16 * t);
+            const int key = 8 * j + 4 * (g & 1) + (g >> 1);
+            const uint32_t s2 = e4m3x2_to_f16x2(*(const uint16_t*)(st + OFF_KS + key * 8 + 2 * t));
+            const Scale2 sa = scale2(prmt(s2, s2, 0x1010)), sb = scale2(prmt(s2, s2, 0x3232));
+            const uint32_t kw[4] = {kw4.x, kw4.y, kw4.z, kw4.w};
+#pragma unroll
+            for (int w = 0; w < 4; ++w) {
+                uint32_t v[4];
+                widen4(kw[w], w < 2 ? sa : sb, v);
+                mma_f16(sacc[j], qa[2 * w], v[0], v[1]);
+                mma_f16(sacc[j], qa[2 * w + 1], v[2], v[3]);
+            }
+        }
+        // ---- log2 units, masks, online softmax
+        const bool need_mask = (k0 + CK - 1 > pmin) || (k0 < lomax);
+#pragma unroll
+        for (int j = 0; j < 4; ++j) {
+#pragma unroll
+            for (int e = 0; e < 4; ++e) {
+                float x = sacc[j][e] * mult[e >> 1];
+                if (need_mask) {
+                    const int key = k0 + 8 * j + 4 * (e & 1) + t;
+                    if (key > pr[e >> 1] || key < lor[e >> 1]) x = -INFINITY;
+                }
+                sacc[j][e] = x;
+            }
+        }
+        float alpha[2];
+#pragma unroll
+        for (int hr = 0; hr < 2; ++hr) {
+            float tmax = -INFINITY;
+#pragma unroll
+            for (int j = 0; j < 4; ++j) tmax = fmaxf(tmax, fmaxf(sacc[j][2 * hr], sacc[j][2 * hr + 1]));
+            tmax = fmaxf(tmax, __shfl_xor_sync(0xffffffffu, tmax, 1));
+            tmax = fmaxf(tmax, __shfl_xor_sync(0xffffffffu, tmax, 2));
+            const float mnew = fmaxf(mrow[hr], tmax);
+            alpha[hr] = (mnew == -INFINITY) ? 1.f : ex2(mrow[hr] - mnew);
+            // weights as 2^15 times 2^(x - max): f16 then keeps 11 bits of
+            // every weight down to 2^-29 of the largest
+            const float mref = (mnew == -INFINITY) ? 0.f : mnew - 15.0f;
+            mrow[hr] = mnew;
+            float sum = 0.f;
+#pragma unroll
+            for (int j = 0; j < 4; ++j) {
+                sacc[j][2 * hr] = ex2(sacc[j][2 * hr] - mref);
+                sacc[j][2 * hr + 1] = ex2(sacc[j][2 * hr + 1] - mref);
+                sum += sacc[j][2 * hr] + sacc[j][2 * hr + 1];
+            }
+            lrow[hr] = lrow[hr] * alpha[hr] + sum;
+        }
+        if (__any_sync(0xffffffffu, alpha[0] != 1.f || alpha[1] != 1.f)) {
+#pragma unroll
+            for (int i = 0; i < 16; ++i) {
+                o[i][0] *= alpha[0];
+                o[i][1] *= alpha[0];
+                o[i][2] *= alpha[1];
+                o[i][3] *= alpha[1];
+            }
+        }
+        // ---- O += P V.  Keys that no row sees (behind the end, before the
+        // first window) get scale 0: whatever their bytes are, 0 reaches O
+        const bool zero_v = (k0 + CK > L) || (k0 < lo0);
+#pragma unroll
+        for (int kk = 0; kk < 2; ++kk) {
+            uint32_t pa[4];
+            pa[0] = pack_f16x2(sacc[2 * kk][0], sacc[2 * kk][1]);
+            pa[1] = pack_f16x2(sacc[2 * kk][2], sacc[2 * kk][3]);
+            pa[2] = pack_f16x2(sacc[2 * kk + 1][0], sacc[2 * kk + 1][1]);
+            pa[3] = pack_f16x2(sacc[2 * kk + 1][2], sacc[2 * kk + 1][3]);
+            uint32_t w[4][2];                           // keys 16 kk + {0, 4, 8, 12} + t, block g
+            Scale2 sc[2];
+#pragma unroll
+            for (int pr2 = 0; pr2 < 2; ++pr2) {
+                uint32_t by[2];
+#pragma unroll
+                for (int e = 0; e < 2; ++e) {
+                    const int key = 16 * kk + 8 * pr2 + 4 * e + t;
+                    const uint2 x = *(const uint2*)(st + OFF_V + key * 64 + ((((g >> 1) ^ (key & 2))) << 4) + (g & 1) * 8);
+                    w[2 * pr2 + e][0] = x.x;
+                    w[2 * pr2 + e][1] = x.y;
+                    by[e] = st[OFF_VS + key * 8 + g];
+                    if (zero_v && (k0 + key >= L || k0 + key < lo0)) by[e] = 0;
+                }
+                sc[pr2] = scale2(e4m3x2_to_f16x2(by[0] | (by[1] << 8)));
+            }
+#pragma unroll
+            for (int i = 0; i < 2; ++i) {
+#pragma unroll
+                for (int h = 0; h < 2; ++h) {
+                    uint32_t va[4], vb[4];
+                    widen4(prmt(w[0][i], w[1][i], h ? 0x7632 : 0x5410), sc[0], va);
+                    widen4(prmt(w[2][i], w[3][i], h ? 0x7632 : 0x5410), sc[1], vb);
+#pragma unroll
+                    for (int f = 0; f < 4; ++f) mma_f16(o[8 * i + 4 * h + f], pa, va[f], vb[f]);
+                }
+            }
+        }
+    }
+    cp_wait<0>();
+
+    // ---- merge the warps' (max, sum, O): n-tile i, column n -> dim 16 n + i
+#pragma unroll
+    for (int hr = 0; hr < 2; ++hr) {
+        lrow[hr] += __shfl_xor_sync(0xffffffffu, lrow[hr], 1);
+        lrow[hr] += __shfl_xor_sync(0xffffffffu, lrow[hr], 2);
+    }
+    __syncthreads();                                    // every ring is consumed
+    float* merge = (float*)smem;
+#pragma unroll
+    for (int hr = 0; hr < 2; ++hr) {
+        float* dst = merge + (warp * 16 + g + 8 * hr) * MERGE_STRIDE;
+#pragma unroll
+        for (int i = 0; i < 16; i += 4) {
+            *(float4*)(dst + 32 * t + i) =
+                make_float4(o[i][2 * hr], o[i + 1][2 * hr], o[i + 2][2 * hr], o[i + 3][2 * hr]);
+            *(float4*)(dst + 32 * t + 16 + i) =
+                make_float4(o[i][2 * hr + 1], o[i + 1][2 * hr + 1], o[i + 2][2 * hr + 1], o[i + 3][2 * hr + 1]);
+        }
+        if (t == 0) {
+            dst[128] = mrow[hr];
+            dst[129] = lrow[hr];
+        }
+    }
+    __syncthreads();
+    const float vs = 4.0f * *P.v_scale;
+    const int rows = min(16, P.R - R0), nw = min(WARPS, n_chunks);
+    for (int item = threadIdx.x; item < rows * 32; item += THREADS) {
+        const int r = item >> 5, d4 = (item & 31) * 4;
+        float mstar = -INFINITY;
+        for (int w = 0; w < nw; ++w) mstar = fmaxf(mstar, merge[(w * 16 + r) * MERGE_STRIDE + 128]);
+        float l = 0.f;
+        float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
+        if (mstar != -INFINITY) {
+            for (int w = 0; w < nw; ++w) {
+                const float* src = merge + (w * 16 + r) * MERGE_STRIDE;
+                const float wt = ex2(src[128] - mstar);
+                l += wt * src[129];
+                const float4 v4 = *(const float4*)(src + d4);
+                acc.x += wt * v4.x;
+                acc.y += wt * v4.y;
+                acc.z += wt * v4.z;
+                acc.w += wt * v4.w;
+            }
+        }
+        const int m = (R0 + r) / P.G, hq = hk * P.G + (R0 + r) % P.G;
+        const int64_t row_idx = ((int64_t)b * P.M + m) * P.Hq + hq;
+        if (nsplit_b == 1) {
+            const float f = vs / l;
+            *(uint2*)(P.out + row_idx * 128 + d4) =
+                make_uint2(pack_bf16x2(acc.x * f, acc.y * f), pack_bf16x2(acc.z * f, acc.w * f));
+        } else {
+            *(float4*)(P.ws_o + (row_idx * P.num_splits + split) * 128 + d4) =
+                make_float4(acc.x * vs, acc.y * vs, acc.z * vs, acc.w * vs);
+            if (d4 == 0) {
+                P.ws_ml[(row_idx * P.num_splits + split) * 2] = mstar;
+                P.ws_ml[(row_idx * P.num_splits + split) * 2 + 1] = l;
+            }
+        }
+    }
+}
+
+}  // namespace i4
+
+int launch_attention_int4(const AttnParams& P, cudaStream_t s, char* text, size_t text_bytes) {
+    if ((int64_t)P.Hkv * P.NT > 65535) return FP8KV_ERR_UNSUPPORTED;
+    static std::mutex mu;
+    static std::set<std::pair<int, const void*>> done;
+    auto kern = P.page_size == 32 ? i4::paged_attention_int4_kernel<32> : i4::paged_attention_int4_kernel<64>;
+    {
+        int dev = 0;
+        if (cudaGetDevice(&dev) != cudaSuccess) return FP8KV_ERR_CUDA;
+        std::lock_guard<std::mutex> lock(mu);
+        if (!done.count({dev, (const void*)kern})) {
+            if (cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, i4::SMEM) != cudaSuccess)
+                return FP8KV_ERR_CUDA;
+            done.insert({dev, (const void*)kern});
+        }
+    }
+    const dim3 grid(P.num_splits, P.Hkv * P.NT, P.B);
+    const cudaError_t e = launch_pdl(kern, grid, dim3(i4::THREADS), i4::SMEM, s, P);
+    if (e != cudaSuccess) {
+        cudaGetLastError();
+        return FP8KV_ERR_CUDA;
+    }
+    snprintf(text, text_bytes, "paged_attention_int4_mma<ps=%d> rows=%d row_tiles=%d splits=%d grid=%dx%dx%d threads=%d reduce=%d",
+             P.page_size, P.R, P.NT, P.num_splits, P.num_splits, P.Hkv * P.NT, P.B, i4::THREADS,
+             P.num_splits > 1 ? 1 : 0);
+    return FP8KV_OK;
+}
+
+}  // namespace fp8kv

@@ -100,6 +100,44 @@ __device__ __forceinline__ uint2 e4m3_encode8(uint4 x, float scale) {
     return o;
 }
 
+// ------------------------------------------------------------------ INT4
+//
+// A page of one head of an INT4 cache: page_size rows of 64 code bytes, then
+// page_size rows of 8 scale bytes (include/fp8kv.h).
+constexpr int kInt4CodeBytes = 64, kInt4ScaleBytes = 8, kInt4RowBytes = kInt4CodeBytes + kInt4ScaleBytes;
+
+// 16 bf16 values (one block) -> 8 bytes of 4-bit codes and the E4M3 scale
+// code, with the tensor scale c and fp32 roundings throughout:
+//     s = max(e4m3(amax / (7 c)), 2^-9),  n = clamp(rint(x * (1 / (s c))), -7, 7)
+// The maximum is taken over the bit patterns, where NaN is above infinity: a
+// NaN anywhere makes the block's scale NaN (and its codes n = 0).
+__device__ __forceinline__ uint2 int4_encode16(uint4 a, uint4 b, float c, uint8_t& scale_code) {
+    const uint32_t w[8] = {a.x, a.y, a.z, a.w, b.x, b.y, b.z, b.w};
+    uint32_t m2 = 0;
+#pragma unroll
+    for (int i = 0; i < 8; ++i) m2 = __vmaxu2(m2, w[i] & 0x7fff7fffu);
+    const float amax = __uint_as_float(max(m2 & 0xffffu, m2 >> 16) << 16);
+    const float r = __fdiv_rn(amax, __fmul_rn(7.0f, c));
+    const uint32_t sc = max(e4m3x2(r, 0.0f) & 0xffu, 1u);       // >= 2^-9; NaN is 0x7f
+    scale_code = (uint8_t)sc;
+    if (sc == 0x7fu) return make_uint2(0x88888888u, 0x88888888u);
+    float s, unused;
+    e4m3x2_to_f32x2(sc, s, unused);
+    const float inv = __fdiv_rn(1.0f, __fmul_rn(s, c));
+    uint32_t o[2] = {0u, 0u};
+#pragma unroll
+    for (int i = 0; i < 8; ++i) {
+        // n + 8 in the low mantissa bits of 2^23 + 8 + n: the addition rounds
+        // to the nearest integer, ties to even
+        const float lo = fminf(fmaxf(__fmul_rn(bf16_lo(w[i]), inv), -7.0f), 7.0f);
+        const float hi = fminf(fmaxf(__fmul_rn(bf16_hi(w[i]), inv), -7.0f), 7.0f);
+        const uint32_t cl = __float_as_uint(__fadd_rn(lo, 8388616.0f)) & 15u;
+        const uint32_t ch = __float_as_uint(__fadd_rn(hi, 8388616.0f)) & 15u;
+        o[i >> 2] |= (cl | (ch << 4)) << (8 * (i & 3));
+    }
+    return make_uint2(o[0], o[1]);
+}
+
 __device__ __forceinline__ uint32_t prmt(uint32_t a, uint32_t b, uint32_t sel) {
     uint32_t r;
     asm("prmt.b32 %0, %1, %2, %3;" : "=r"(r) : "r"(a), "r"(b), "r"(sel));
@@ -322,6 +360,7 @@ int num_sms();                          // SM count of the current device
 void set_dispatch(const char* text);    // per-thread record of the last dispatch
 int status_insert(unsigned int* s, int clear);     // insert.cu
 int status_attention(unsigned int* s, int clear);  // attention.cu
+int status_attention_int4(unsigned int* s, int clear);  // attention_int4.cu
 
 // OR this translation unit's status word into *s, optionally clearing it.
 static inline int read_status(unsigned int* s, int clear) {

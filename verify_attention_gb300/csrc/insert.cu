@@ -111,6 +111,159 @@ int launch_append(const void* k, const void* v, const int32_t* seq_lens, const i
     return e == cudaSuccess ? FP8KV_OK : (cudaGetLastError(), FP8KV_ERR_CUDA);
 }
 
+// ------------------------------------------------------- 4-bit insert/append
+
+// One block of 16 elements of K and of V into an INT4 cache row (page, head,
+// offset): 8 code bytes and one scale byte each.
+__device__ __forceinline__ void int4_store(const uint4* __restrict__ k, const uint4* __restrict__ v, int64_t src,
+                                           float ks, float vs, uint8_t* __restrict__ k_cache,
+                                           uint8_t* __restrict__ v_cache, int64_t page, int off, int h, int Hkv,
+                                           int page_size, int block) {
+    const int64_t base = (page * Hkv + h) * page_size * kInt4RowBytes;
+    const int64_t code = base + off * kInt4CodeBytes + block * 8;
+    const int64_t scale = base + page_size * kInt4CodeBytes + off * kInt4ScaleBytes + block;
+    uint8_t sk, sv;
+    const uint2 ck = int4_encode16(k[src], k[src + 1], ks, sk), cv = int4_encode16(v[src], v[src + 1], vs, sv);
+    *reinterpret_cast<uint2*>(k_cache + code) = ck;
+    *reinterpret_cast<uint2*>(v_cache + code) = cv;
+    k_cache[scale] = sk;
+    v_cache[scale] = sv;
+}
+
+// One thread per (token, head, 16-element block) of K and V: 64 bytes in, 18
+// bytes out; the eight threads of a row write its 64 code bytes and its 8
+// scale bytes side by side.
+__global__ void __launch_bounds__(256) insert_int4_kernel(
+    const uint4* __restrict__ k, const uint4* __restrict__ v, const int64_t* __restrict__ slots, int T, int Hkv,
+    const float* __restrict__ k_scale, const float* __restrict__ v_scale, uint8_t* __restrict__ k_cache,
+    uint8_t* __restrict__ v_cache, int64_t num_slots, int page_size) {
+    pdl_launch_dependents();
+    pdl_wait();
+    const int64_t i = (int64_t)blockIdx.x * blockDim.x + threadIdx.x;
+    if (i >= (int64_t)T * Hkv * 8) return;
+    const int block = (int)(i & 7);
+    const int64_t row = i >> 3, t = row / Hkv;
+    const int h = (int)(row - t * Hkv);
+    const int64_t slot = slots[t];
+    if (slot < 0) return;
+    if (slot >= num_slots) {
+        if (block == 0) flag(FP8KV_DEV_BAD_SLOT);
+        return;
+    }
+    const int64_t page = slot / page_size;
+    int4_store(k, v, 2 * i, *k_scale, *v_scale, k_cache, v_cache, page, (int)(slot - page * page_size), h, Hkv,
+               page_size, block);
+}
+
+// The M new tokens of every sequence to positions L_b - M + m.
+__global__ void __launch_bounds__(256) append_int4_kernel(
+    const uint4* __restrict__ k, const uint4* __restrict__ v, const int32_t* __restrict__ seq_lens,
+    const int32_t* __restrict__ block_table, int mpps, int B, int M, int Hkv, const float* __restrict__ k_scale,
+    const float* __restrict__ v_scale, uint8_t* __restrict__ k_cache, uint8_t* __restrict__ v_cache, int num_pages,
+    int page_size, int max_seq_len) {
+    pdl_launch_dependents();
+    pdl_wait();
+    const int64_t i = (int64_t)blockIdx.x * blockDim.x + threadIdx.x;
+    if (i >= (int64_t)B * M * Hkv * 8) return;
+    const int block = (int)(i & 7);
+    const int64_t row = i >> 3, bm = row / Hkv;
+    const int h = (int)(row - bm * Hkv), b = (int)(bm / M), m = (int)(bm % M);
+    const int L = seq_lens[b];
+    if (L < M || L > max_seq_len || (L + page_size - 1) / page_size > mpps) {
+        if (block == 0) flag(FP8KV_DEV_BAD_SEQ_LEN);
+        return;
+    }
+    const int pos = L - M + m;
+    const int page = block_table[(int64_t)b * mpps + pos / page_size];
+    if (page < 0 || page >= num_pages) {
+        if (block == 0) flag(FP8KV_DEV_BAD_SLOT);
+        return;
+    }
+    int4_store(k, v, 2 * i, *k_scale, *v_scale, k_cache, v_cache, page, pos % page_size, h, Hkv, page_size, block);
+}
+
+int launch_append_int4(const void* k, const void* v, const int32_t* seq_lens, const int32_t* block_table, int mpps,
+                       int B, int M, int Hkv, const float* k_scale, const float* v_scale, void* k_cache,
+                       void* v_cache, int num_pages, int page_size, int max_seq_len, cudaStream_t s) {
+    const int64_t blocks = ((int64_t)B * M * Hkv * 8 + 255) / 256;
+    if (blocks > 0x7fffffff) return FP8KV_ERR_UNSUPPORTED;
+    cudaError_t e = launch_pdl(append_int4_kernel, dim3((unsigned)blocks), dim3(256), 0, s, (const uint4*)k,
+                               (const uint4*)v, seq_lens, block_table, mpps, B, M, Hkv, k_scale, v_scale,
+                               (uint8_t*)k_cache, (uint8_t*)v_cache, num_pages, page_size, max_seq_len);
+    return e == cudaSuccess ? FP8KV_OK : (cudaGetLastError(), FP8KV_ERR_CUDA);
+}
+
+// ------------------------------------------------------------------- gather
+
+// 16 stored values of one cache as bf16 (two 16-byte stores): the row's
+// elements 16 * block ... + 15 of (page, head, offset).
+template <int DT>
+__device__ __forceinline__ void gather16(const uint8_t* __restrict__ cache, float c, int64_t page, int off, int h,
+                                         int Hkv, int page_size, int block, uint4* __restrict__ out) {
+    const int64_t ph = page * Hkv + h;
+    uint32_t w[8];
+    if (DT == FP8KV_CACHE_BF16) {
+        const uint4* src = reinterpret_cast<const uint4*>(cache) + ((ph * page_size + off) * 16 + 2 * block);
+        out[0] = src[0];
+        out[1] = src[1];
+        return;
+    }
+    if (DT == FP8KV_CACHE_E4M3) {
+        const uint4 x = *reinterpret_cast<const uint4*>(cache + (ph * page_size + off) * 128 + 16 * block);
+        const uint32_t cw[4] = {x.x, x.y, x.z, x.w};
+#pragma unroll
+        for (int j = 0; j < 8; ++j) {
+            float lo, hi;
+            e4m3x2_to_f32x2(cw[j >> 1] >> (16 * (j & 1)), lo, hi);
+            w[j] = pack_bf16x2(__fmul_rn(lo, c), __fmul_rn(hi, c));
+        }
+    } else {
+        const int64_t base = ph * page_size * kInt4RowBytes;
+        const uint2 x = *reinterpret_cast<const uint2*>(cache + base + off * kInt4CodeBytes + block * 8);
+        const uint32_t cw[2] = {x.x, x.y};
+        float s, unused;
+        e4m3x2_to_f32x2(cache[base + page_size * kInt4CodeBytes + off * kInt4ScaleBytes + block], s, unused);
+#pragma unroll
+        for (int j = 0; j < 8; ++j) {
+            const uint32_t b = cw[j >> 2] >> (8 * (j & 3));
+            // n s is exact in fp32 (3 + 4 significant bits)
+            const float lo = (float)((int)(b & 15u) - 8) * s, hi = (float)((int)((b >> 4) & 15u) - 8) * s;
+            w[j] = pack_bf16x2(__fmul_rn(lo, c), __fmul_rn(hi, c));
+        }
+    }
+    out[0] = make_uint4(w[0], w[1], w[2], w[3]);
+    out[1] = make_uint4(w[4], w[5], w[6], w[7]);
+}
+
+// One thread per (token, head, 16-element block) of K and V.
+template <int DT>
+__global__ void __launch_bounds__(256) gather_kernel(const int64_t* __restrict__ slots, int T, int Hkv,
+                                                     const float* __restrict__ k_scale,
+                                                     const float* __restrict__ v_scale,
+                                                     const uint8_t* __restrict__ k_cache,
+                                                     const uint8_t* __restrict__ v_cache, int64_t num_slots,
+                                                     int page_size, uint4* __restrict__ k_out,
+                                                     uint4* __restrict__ v_out) {
+    pdl_launch_dependents();
+    pdl_wait();
+    const int64_t i = (int64_t)blockIdx.x * blockDim.x + threadIdx.x;
+    if (i >= (int64_t)T * Hkv * 8) return;
+    const int block = (int)(i & 7);
+    const int64_t row = i >> 3, t = row / Hkv;
+    const int h = (int)(row - t * Hkv);
+    const int64_t slot = slots[t];
+    if (slot < 0) return;
+    if (slot >= num_slots) {
+        if (block == 0) flag(FP8KV_DEV_BAD_SLOT);
+        return;
+    }
+    const float ks = DT == FP8KV_CACHE_BF16 ? 1.f : *k_scale, vs = DT == FP8KV_CACHE_BF16 ? 1.f : *v_scale;
+    const int64_t page = slot / page_size;
+    const int off = (int)(slot - page * page_size);
+    gather16<DT>(k_cache, ks, page, off, h, Hkv, page_size, block, k_out + 2 * i);
+    gather16<DT>(v_cache, vs, page, off, h, Hkv, page_size, block, v_out + 2 * i);
+}
+
 // ------------------------------------------------ fused RMSNorm+RoPE+insert
 
 // One warp per (token, head) row; heads 0..Hq-1 are Q rows, Hq..Hq+Hkv-1 are
@@ -256,20 +409,29 @@ static int cache_insert(const void* k, const void* v, const int64_t* slot_mappin
                         const float* k_scale, const float* v_scale, int scale_stride, void* k_cache, void* v_cache,
                         int num_pages, int page_size, int cache_dtype, void* stream) {
     if (T < 0 || Hkv <= 0 || num_pages <= 0) return FP8KV_ERR_INVALID_ARG;
-    if (cache_dtype != FP8KV_CACHE_E4M3 && cache_dtype != FP8KV_CACHE_BF16) return FP8KV_ERR_INVALID_ARG;
+    if (cache_dtype != FP8KV_CACHE_E4M3 && cache_dtype != FP8KV_CACHE_BF16 && cache_dtype != FP8KV_CACHE_INT4)
+        return FP8KV_ERR_INVALID_ARG;
     if (D != 128) return FP8KV_ERR_UNSUPPORTED;
     if (page_size != 32 && page_size != 64) return FP8KV_ERR_UNSUPPORTED;
     if (T == 0) return FP8KV_OK;                                // nothing to do; no pointer is read
     if (!k || !v || !slot_mapping || !k_cache || !v_cache) return FP8KV_ERR_INVALID_ARG;
-    if (cache_dtype == FP8KV_CACHE_E4M3 && (!k_scale || !v_scale)) return FP8KV_ERR_INVALID_ARG;
+    if (cache_dtype != FP8KV_CACHE_BF16 && (!k_scale || !v_scale)) return FP8KV_ERR_INVALID_ARG;
     if (!aligned16(k) || !aligned16(v) || !aligned16(k_cache) || !aligned16(v_cache))
         return FP8KV_ERR_INVALID_ARG;
-    const int64_t items = (int64_t)T * Hkv * 16;
     const int threads = 256;
-    const int64_t blocks = (items + threads - 1) / threads;
-    if (blocks > 0x7fffffff) return FP8KV_ERR_UNSUPPORTED;
     cudaStream_t s = (cudaStream_t)stream;
     const int64_t num_slots = (int64_t)num_pages * page_size;
+    if (cache_dtype == FP8KV_CACHE_INT4) {
+        const int64_t blocks4 = ((int64_t)T * Hkv * 8 + threads - 1) / threads;
+        if (blocks4 > 0x7fffffff) return FP8KV_ERR_UNSUPPORTED;
+        cudaError_t e = launch_pdl(insert_int4_kernel, dim3((unsigned)blocks4), dim3(threads), 0, s, (const uint4*)k,
+                                   (const uint4*)v, slot_mapping, T, Hkv, k_scale, v_scale, (uint8_t*)k_cache,
+                                   (uint8_t*)v_cache, num_slots, page_size);
+        return e == cudaSuccess ? FP8KV_OK : (cudaGetLastError(), FP8KV_ERR_CUDA);
+    }
+    const int64_t items = (int64_t)T * Hkv * 16;
+    const int64_t blocks = (items + threads - 1) / threads;
+    if (blocks > 0x7fffffff) return FP8KV_ERR_UNSUPPORTED;
     cudaError_t e = launch_pdl(cache_dtype == FP8KV_CACHE_E4M3 ? insert_kernel<true> : insert_kernel<false>,
                                dim3((unsigned)blocks), dim3(threads), 0, s, (const uint4*)k, (const uint4*)v,
                                slot_mapping, T, Hkv, k_scale, v_scale, scale_stride, (uint8_t*)k_cache,
@@ -291,6 +453,30 @@ extern "C" int fp8kv_cache_insert_per_head(const void* k, const void* v, const i
                                            void* stream) {
     return cache_insert(k, v, slot_mapping, T, Hkv, D, k_scale, v_scale, 1, k_cache, v_cache, num_pages, page_size,
                         FP8KV_CACHE_E4M3, stream);
+}
+
+extern "C" int fp8kv_cache_gather(const int64_t* slot_mapping, int T, int Hkv, int D, const float* k_scale,
+                                  const float* v_scale, const void* k_cache, const void* v_cache, int num_pages,
+                                  int page_size, int cache_dtype, void* k_out, void* v_out, void* stream) {
+    if (T < 0 || Hkv <= 0 || num_pages <= 0) return FP8KV_ERR_INVALID_ARG;
+    if (cache_dtype != FP8KV_CACHE_E4M3 && cache_dtype != FP8KV_CACHE_BF16 && cache_dtype != FP8KV_CACHE_INT4)
+        return FP8KV_ERR_INVALID_ARG;
+    if (D != 128) return FP8KV_ERR_UNSUPPORTED;
+    if (page_size != 32 && page_size != 64) return FP8KV_ERR_UNSUPPORTED;
+    if (T == 0) return FP8KV_OK;                                // nothing to do; no pointer is read
+    if (!slot_mapping || !k_cache || !v_cache || !k_out || !v_out) return FP8KV_ERR_INVALID_ARG;
+    if (cache_dtype != FP8KV_CACHE_BF16 && (!k_scale || !v_scale)) return FP8KV_ERR_INVALID_ARG;
+    if (!aligned16(k_cache) || !aligned16(v_cache) || !aligned16(k_out) || !aligned16(v_out))
+        return FP8KV_ERR_INVALID_ARG;
+    const int64_t blocks = ((int64_t)T * Hkv * 8 + 255) / 256;
+    if (blocks > 0x7fffffff) return FP8KV_ERR_UNSUPPORTED;
+    auto kern = cache_dtype == FP8KV_CACHE_INT4   ? gather_kernel<FP8KV_CACHE_INT4>
+                : cache_dtype == FP8KV_CACHE_E4M3 ? gather_kernel<FP8KV_CACHE_E4M3>
+                                                  : gather_kernel<FP8KV_CACHE_BF16>;
+    cudaError_t e = launch_pdl(kern, dim3((unsigned)blocks), dim3(256), 0, (cudaStream_t)stream, slot_mapping, T, Hkv,
+                               k_scale, v_scale, (const uint8_t*)k_cache, (const uint8_t*)v_cache,
+                               (int64_t)num_pages * page_size, page_size, (uint4*)k_out, (uint4*)v_out);
+    return e == cudaSuccess ? FP8KV_OK : (cudaGetLastError(), FP8KV_ERR_CUDA);
 }
 
 extern "C" int fp8kv_qk_norm_rope_insert(const void* q, const void* k, const void* v,

@@ -19,6 +19,8 @@ LIB_PATH = os.path.join(_HERE, "_build", "libfp8kv.so")
 
 FP8KV_CACHE_E4M3 = 0
 FP8KV_CACHE_BF16 = 1
+FP8KV_CACHE_INT4 = 2
+INT4_ROW_BYTES = 72         # a row of an INT4 cache: 64 bytes of codes, 8 of block scales
 DEV_BAD_SLOT, DEV_BAD_POSITION, DEV_BAD_SEQ_LEN, DEV_WAIT_TIMEOUT = 0x1, 0x2, 0x4, 0x8
 
 _lib = None
@@ -41,6 +43,8 @@ def lib() -> ctypes.CDLL:
                                  ctypes.c_size_t)
         L.fp8kv_cache_insert.restype = i32
         L.fp8kv_cache_insert.argtypes = [vp, vp, vp, i32, i32, i32, vp, vp, vp, vp, i32, i32, i32, vp]
+        L.fp8kv_cache_gather.restype = i32
+        L.fp8kv_cache_gather.argtypes = [vp, i32, i32, i32, vp, vp, vp, vp, i32, i32, i32, vp, vp, vp]
         L.fp8kv_qk_norm_rope_insert.restype = i32
         L.fp8kv_qk_norm_rope_insert.argtypes = [vp, vp, vp, vp, vp, vp, f32, vp, i32, vp, vp, i32, i32,
                                                 i32, i32, vp, vp, vp, vp, i32, i32, vp]
@@ -111,10 +115,30 @@ def _dev(t: torch.Tensor, name: str, dtype=None):
 
 def _cache_dtype(cache: torch.Tensor) -> int:
     if cache.dtype == torch.uint8:
-        return FP8KV_CACHE_E4M3
+        return FP8KV_CACHE_INT4 if cache.dim() == 3 else FP8KV_CACHE_E4M3
     if cache.dtype == torch.bfloat16:
         return FP8KV_CACHE_BF16
-    raise ValueError("cache must be uint8 (E4M3 codes) or bfloat16")
+    raise ValueError("cache must be uint8 (E4M3 codes, or INT4 pages) or bfloat16")
+
+
+def _cache_shape(k_cache: torch.Tensor, v_cache: torch.Tensor, dt: int):
+    """(num_pages, Hkv, page_size) of a pair of caches."""
+    if dt != FP8KV_CACHE_INT4:
+        num_pages, Hkv, page_size, _ = k_cache.shape
+        return num_pages, Hkv, page_size
+    num_pages, Hkv, nbytes = k_cache.shape
+    if nbytes % INT4_ROW_BYTES:
+        raise ValueError(f"an INT4 cache is [num_pages][Hkv][page_size * {INT4_ROW_BYTES}] bytes")
+    if v_cache.dtype != torch.uint8 or v_cache.shape != k_cache.shape:
+        raise ValueError("k_cache and v_cache must have the same type and shape")
+    return num_pages, Hkv, nbytes // INT4_ROW_BYTES
+
+
+def fp8kv_int4_cache(num_pages, Hkv, page_size, device=None):
+    """One INT4 cache (K or V): uint8 [num_pages][Hkv][page_size * 72], zeroed
+    (every row reads as zeros)."""
+    return torch.zeros((num_pages, Hkv, page_size * INT4_ROW_BYTES), dtype=torch.uint8,
+                       device="cuda" if device is None else device)
 
 
 def fp8kv_status_string(status: int) -> str:
@@ -122,17 +146,52 @@ def fp8kv_status_string(status: int) -> str:
 
 
 def fp8kv_cache_insert(k, v, slot_mapping, k_scale, v_scale, k_cache, v_cache, stream=None):
-    """k, v bf16 [T][Hkv][D]; slot_mapping int64 [T]; scales fp32 [1] (E4M3 only);
-    caches [num_pages][Hkv][page_size][D] uint8 (E4M3) or bf16."""
+    """k, v bf16 [T][Hkv][D]; slot_mapping int64 [T]; scales fp32 [1] (E4M3, INT4);
+    caches [num_pages][Hkv][page_size][D] uint8 (E4M3) or bf16, or the INT4 pages
+    of fp8kv_int4_cache."""
     dt = _cache_dtype(k_cache)
     _dev(k, "k", torch.bfloat16), _dev(v, "v", torch.bfloat16)
     _dev(slot_mapping, "slot_mapping", torch.int64), _dev(k_cache, "k_cache"), _dev(v_cache, "v_cache")
     T, Hkv, D = k.shape
-    num_pages, _, page_size, _ = k_cache.shape
+    num_pages, heads, page_size = _cache_shape(k_cache, v_cache, dt)
+    if dt == FP8KV_CACHE_INT4:
+        _int4_rows(k, v, slot_mapping, heads, k_scale, v_scale)
     rc = lib().fp8kv_cache_insert(_ptr(k), _ptr(v), _ptr(slot_mapping), T, Hkv, D, _ptr(k_scale),
                                   _ptr(v_scale), _ptr(k_cache), _ptr(v_cache), num_pages, page_size,
                                   dt, _stream(stream))
     _check("fp8kv_cache_insert", rc)
+
+
+def _int4_rows(k, v, slot_mapping, heads, k_scale, v_scale):
+    if v.shape != k.shape or k.shape[1] != heads or slot_mapping.numel() != k.shape[0]:
+        raise ValueError(f"k, v must be [T][{heads}][D] and slot_mapping [T]")
+    _dev(k_scale, "k_scale", torch.float32), _dev(v_scale, "v_scale", torch.float32)
+
+
+def fp8kv_cache_gather(slot_mapping, k_scale, v_scale, k_cache, v_cache, k_out=None, v_out=None, stream=None):
+    """The stored K and V of the tokens in slot_mapping (int64 [T]) as bf16
+    [T][Hkv][D]; rows with a negative slot are left as they are (zeros when the
+    outputs are allocated here).  Any cache type, per-tensor scales."""
+    dt = _cache_dtype(k_cache)
+    _dev(slot_mapping, "slot_mapping", torch.int64), _dev(k_cache, "k_cache"), _dev(v_cache, "v_cache")
+    if v_cache.dtype != k_cache.dtype or v_cache.shape != k_cache.shape:
+        raise ValueError("k_cache and v_cache must have the same type and shape")
+    num_pages, Hkv, page_size = _cache_shape(k_cache, v_cache, dt)
+    T, D = slot_mapping.numel(), 128 if dt == FP8KV_CACHE_INT4 else k_cache.shape[3]
+    if dt != FP8KV_CACHE_BF16:
+        _dev(k_scale, "k_scale", torch.float32), _dev(v_scale, "v_scale", torch.float32)
+    outs = []
+    for t, n in ((k_out, "k_out"), (v_out, "v_out")):
+        if t is None:
+            t = torch.zeros((T, Hkv, D), dtype=torch.bfloat16, device=k_cache.device)
+        if tuple(_dev(t, n, torch.bfloat16).shape) != (T, Hkv, D):
+            raise ValueError(f"{n} must be {(T, Hkv, D)}, got {tuple(t.shape)}")
+        outs.append(t)
+    rc = lib().fp8kv_cache_gather(_ptr(slot_mapping), T, Hkv, D, _ptr(k_scale), _ptr(v_scale), _ptr(k_cache),
+                                  _ptr(v_cache), num_pages, page_size, dt, _ptr(outs[0]), _ptr(outs[1]),
+                                  _stream(stream))
+    _check("fp8kv_cache_gather", rc)
+    return tuple(outs)
 
 
 def _head_scales(k_scale, v_scale, Hkv):
@@ -195,15 +254,15 @@ def fp8kv_paged_attention_workspace_size(B, M, Hq, Hkv, D, page_size, max_seq_le
 def fp8kv_paged_attention(q, k_cache, v_cache, block_table, seq_lens, max_seq_len, k_scale, v_scale,
                           sm_scale, window_left=-1, split_tokens=0, workspace=None, out=None,
                           num_pages=None, stream=None):
-    """q bf16 [B][M][Hq][D]; caches [num_pages][Hkv][page_size][D]; block_table int32
-    [B][max_pages_per_seq]; seq_lens int32 [B] (context incl. the M new rows).
+    """q bf16 [B][M][Hq][D]; caches [num_pages][Hkv][page_size][D] (or INT4 pages,
+    fp8kv_int4_cache); block_table int32 [B][max_pages_per_seq]; seq_lens int32 [B] (context incl. the M new rows).
     Returns out bf16 [B][M][Hq][D].  ``workspace`` (uint8 CUDA tensor) is
     allocated by torch here when not given and needed."""
     dt = _cache_dtype(k_cache)
     _dev(q, "q", torch.bfloat16), _dev(k_cache, "k_cache"), _dev(v_cache, "v_cache")
     _dev(block_table, "block_table", torch.int32), _dev(seq_lens, "seq_lens", torch.int32)
     B, M, Hq, D = q.shape
-    P, Hkv, page_size, _ = k_cache.shape
+    P, Hkv, page_size = _cache_shape(k_cache, v_cache, dt)
     if num_pages is None:
         num_pages = P
     need = fp8kv_paged_attention_workspace_size(B, M, Hq, Hkv, D, page_size, max_seq_len, window_left,
@@ -231,7 +290,7 @@ def fp8kv_append_paged_attention(k_new, v_new, q, k_cache, v_cache, block_table,
     _dev(q, "q", torch.bfloat16), _dev(k_cache, "k_cache"), _dev(v_cache, "v_cache")
     _dev(block_table, "block_table", torch.int32), _dev(seq_lens, "seq_lens", torch.int32)
     B, M, Hq, D = q.shape
-    P, Hkv, page_size, _ = k_cache.shape
+    P, Hkv, page_size = _cache_shape(k_cache, v_cache, dt)
     if tuple(k_new.shape) != (B, M, Hkv, D) or tuple(v_new.shape) != (B, M, Hkv, D):
         raise ValueError("k_new, v_new must be [B][M][Hkv][D]")
     if num_pages is None:
@@ -312,7 +371,7 @@ class PreparedAttention:
         _dev(q, "q", torch.bfloat16), _dev(k_cache, "k_cache"), _dev(v_cache, "v_cache")
         _dev(block_table, "block_table", torch.int32), _dev(seq_lens, "seq_lens", torch.int32)
         B, M, Hq, D = q.shape
-        P, Hkv, page_size, _ = k_cache.shape
+        P, Hkv, page_size = _cache_shape(k_cache, v_cache, dt)
         if (k_new is None) != (v_new is None):
             raise ValueError("k_new and v_new go together")
         if k_new is not None:
@@ -360,7 +419,7 @@ def fp8kv_paged_attention_noalloc(q, k_cache, v_cache, block_table, seq_lens, ma
     if out.shape != q.shape or out.device != q.device:
         raise ValueError(f"out must have the shape and device of q {tuple(q.shape)}, got {tuple(out.shape)}")
     B, M, Hq, D = q.shape
-    P, Hkv, page_size, _ = k_cache.shape
+    P, Hkv, page_size = _cache_shape(k_cache, v_cache, dt)
     rc = lib().fp8kv_paged_attention_noalloc(
         _ptr(q), _ptr(k_cache), _ptr(v_cache), dt, _ptr(block_table), block_table.shape[1], _ptr(seq_lens),
         int(max_seq_len), B, M, Hq, Hkv, D, page_size, int(P if num_pages is None else num_pages),
