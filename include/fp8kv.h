@@ -189,6 +189,44 @@ int fp8kv_qk_norm_rope_insert(const void* q, const void* k, const void* v,
                               int num_pages, int page_size, void* stream);
 
 /*
+ * fp8kv_prompt_attention -- causal attention of whole prompts over the rows the
+ * projection produced (before, or beside, their cache insert): B sequences
+ * packed one after another, with the masks and head grouping of
+ * fp8kv_paged_attention.  (The pages have no counterpart: their prefill is the
+ * serving engine's own.)
+ *
+ * Sequence b is the tokens cu_seqlens[b] .. cu_seqlens[b + 1] - 1; its token
+ * at position p sees the keys j of the same sequence with j <= p and, when
+ * window_left >= 0, j >= p - window_left; query head h reads KV head
+ * h / (Hq/Hkv):
+ *     out[t][h] = softmax_j( (q[t][h] . k[j][h']) * sm_scale ) . v[j][h']
+ * computed on the tensor cores with fp32 accumulation, the softmax weights
+ * rounded to bf16 for the second product, the result rounded to bf16.
+ *
+ *   q (device) bf16 [T][Hq][D], tokens q_stride elements apart; k, v bf16
+ *     [T][Hkv][D], k_stride and v_stride apart (views of one projection's
+ *     output are fine); strides >= heads * D and multiples of 8
+ *   cu_seqlens (device) int32 [B + 1], non-decreasing, 0 <= ... <= T; equal
+ *     neighbours are an empty sequence
+ *   max_seq_len (host) >= every length
+ *   sm_scale (host) > 0;  window_left (host) -1, or >= 0
+ *   out (device) bf16 [T][Hq][D], dense; must not overlap the inputs.  Rows of
+ *     no sequence (before the first, behind the last) are left as they are, and
+ *     q, k, v there may hold anything.
+ * Supported: D = 128, Hq/Hkv <= 128, T / (2 * floor(128 / (Hq/Hkv))) + B <= 65535;
+ * no workspace.  B = 0 or T = 0 launches nothing and reads no pointer.
+ * An infinity or NaN in a v row may reach, beyond the rows that see it, the
+ * rows up to 2 * floor(128 / (Hq/Hkv)) positions around it (0 * infinity).
+ * Device check: a sequence with bounds outside [0, T], out of order, or longer
+ * than max_seq_len is skipped, its output rows left as they are
+ * (FP8KV_DEV_BAD_SEQ_LEN); with bounds out of order other sequences may be
+ * skipped too.
+ */
+int fp8kv_prompt_attention(const void* q, int64_t q_stride, const void* k, int64_t k_stride, const void* v,
+                           int64_t v_stride, const int32_t* cu_seqlens, int B, int T, int max_seq_len,
+                           int Hq, int Hkv, int D, float sm_scale, int window_left, void* out, void* stream);
+
+/*
  * fp8kv_paged_attention_plan -- the split-KV partition fp8kv_paged_attention
  * will use for these host-visible sizes on the current device.
  *   split_tokens: 0 = choose automatically; otherwise a positive multiple of

@@ -854,6 +854,22 @@ static bool make_cache_map(CUtensorMap* m, const void* base, bool fp8, int Hkv, 
     return r == CUDA_SUCCESS;
 }
 
+// 3-D view of bf16 rows [tokens][heads][128] whose tokens are `stride` elements
+// apart: x = element, y = head, z = token; boxes of 64 elements (128 bytes,
+// swizzled) x box_heads x box_tokens.
+bool rows_map(CUtensorMap* m, const void* base, int heads, int64_t stride, int tokens, int box_heads,
+              int box_tokens) {
+    auto fn = encode_fn();
+    if (!fn) return false;
+    cuuint64_t dims[3] = {128, (cuuint64_t)heads, (cuuint64_t)tokens};
+    cuuint64_t strides[2] = {256, (cuuint64_t)stride * 2};
+    cuuint32_t box[3] = {64u, (cuuint32_t)box_heads, (cuuint32_t)box_tokens};
+    cuuint32_t es[3] = {1, 1, 1};
+    return fn(m, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 3, const_cast<void*>(base), dims, strides, box, es,
+              CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+              CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
+
 // Tensor maps by (cache base, dtype, heads, page size, pages): a map is a pure
 // function of these, so repeated calls over the same persistent cache reuse
 // it instead of encoding it again.  A small direct-mapped table per process.

@@ -78,6 +78,9 @@ int status_attention_layers(unsigned int* s, int clear);
 // The cached 3-D tensor map of a [num_pages][Hkv][PS][128] cache (attention.cu).
 bool cache_map(CUtensorMap* m, const void* base, bool fp8, int Hkv, int PS, int num_pages);
 
+// Tensor map of bf16 rows [tokens][heads][128], `stride` elements a token (attention.cu).
+bool rows_map(CUtensorMap* m, const void* base, int heads, int64_t stride, int tokens, int box_heads, int box_tokens);
+
 // Append kernel (insert.cu): the same encoding for the other attention paths.
 int launch_append(const void* k, const void* v, const int32_t* seq_lens, const int32_t* block_table, int mpps, int B,
                   int M, int Hkv, const float* k_scale, const float* v_scale, int scale_stride, void* k_cache,

@@ -39,8 +39,8 @@ def lib() -> ctypes.CDLL:
             raise RuntimeError(f"{LIB_PATH} is missing: build it with "
                                "`python -m verify_attention_gb300.build` (nvcc, sm_103a)")
         L = ctypes.CDLL(LIB_PATH)
-        vp, i32, u32, f32, sz = (ctypes.c_void_p, ctypes.c_int, ctypes.c_uint32, ctypes.c_float,
-                                 ctypes.c_size_t)
+        vp, i32, u32, f32, sz, i64 = (ctypes.c_void_p, ctypes.c_int, ctypes.c_uint32, ctypes.c_float,
+                                      ctypes.c_size_t, ctypes.c_int64)
         L.fp8kv_cache_insert.restype = i32
         L.fp8kv_cache_insert.argtypes = [vp, vp, vp, i32, i32, i32, vp, vp, vp, vp, i32, i32, i32, vp]
         L.fp8kv_cache_gather.restype = i32
@@ -48,6 +48,9 @@ def lib() -> ctypes.CDLL:
         L.fp8kv_qk_norm_rope_insert.restype = i32
         L.fp8kv_qk_norm_rope_insert.argtypes = [vp, vp, vp, vp, vp, vp, f32, vp, i32, vp, vp, i32, i32,
                                                 i32, i32, vp, vp, vp, vp, i32, i32, vp]
+        L.fp8kv_prompt_attention.restype = i32
+        L.fp8kv_prompt_attention.argtypes = [vp, i64, vp, i64, vp, i64, vp, i32, i32, i32, i32, i32, i32, f32, i32,
+                                             vp, vp]
         L.fp8kv_paged_attention_plan.restype = i32
         L.fp8kv_paged_attention_plan.argtypes = [i32] * 9 + [ctypes.POINTER(i32), ctypes.POINTER(i32)]
         L.fp8kv_paged_attention_workspace_size.restype = sz
@@ -232,6 +235,41 @@ def fp8kv_qk_norm_rope_insert(q, k, v, positions, q_norm_w, k_norm_w, eps, cos_s
         _ptr(cos_sin), cos_sin.shape[0], _ptr(q_out), _ptr(slot_mapping), T, Hq, Hkv, D, _ptr(k_scale),
         _ptr(v_scale), _ptr(k_cache), _ptr(v_cache), num_pages, page_size, _stream(stream))
     _check("fp8kv_qk_norm_rope_insert", rc)
+
+
+def _token_rows(t: torch.Tensor, name: str, T: int):
+    """bf16 [T][heads][D] with dense tokens; returns the elements between tokens."""
+    if not t.is_cuda:
+        raise ValueError(f"{name} must be a CUDA tensor")
+    if t.dtype != torch.bfloat16:
+        raise ValueError(f"{name} must be {torch.bfloat16}, got {t.dtype}")
+    n, heads, D = t.shape
+    st = t.stride()
+    if n != T or st[2] != 1 or (heads > 1 and st[1] != D):
+        raise ValueError(f"{name} must be [{T}][heads][D] with dense tokens")
+    return st[0] if n > 1 else heads * D
+
+
+def fp8kv_prompt_attention(q, k, v, cu_seqlens, max_seq_len, sm_scale, window_left=-1, out=None, stream=None):
+    """Causal attention of packed prompts: q bf16 [T][Hq][D], k, v bf16
+    [T][Hkv][D] (tokens dense, any distance apart: views of a fused projection
+    are fine), cu_seqlens int32 [B + 1].  Returns out bf16 [T][Hq][D]; rows of no
+    sequence are left as they are (zeros when allocated here)."""
+    T, Hq, D = q.shape
+    Hkv = k.shape[1]
+    if k.shape[2] != D or v.shape != k.shape:
+        raise ValueError("k and v must be [T][Hkv][D] with the D of q")
+    strides = [_token_rows(t, n, T) for t, n in ((q, "q"), (k, "k"), (v, "v"))]
+    _dev(cu_seqlens, "cu_seqlens", torch.int32)
+    if out is None:
+        out = torch.zeros((T, Hq, D), dtype=torch.bfloat16, device=q.device)
+    if tuple(_dev(out, "out", torch.bfloat16).shape) != (T, Hq, D):
+        raise ValueError(f"out must be {(T, Hq, D)}, got {tuple(out.shape)}")
+    rc = lib().fp8kv_prompt_attention(_ptr(q), strides[0], _ptr(k), strides[1], _ptr(v), strides[2],
+                                      _ptr(cu_seqlens), cu_seqlens.numel() - 1, T, int(max_seq_len), Hq, Hkv, D,
+                                      float(sm_scale), int(window_left), _ptr(out), _stream(stream))
+    _check("fp8kv_prompt_attention", rc)
+    return out
 
 
 def fp8kv_paged_attention_plan(B, M, Hq, Hkv, D, page_size, max_seq_len, window_left, split_tokens=0):
