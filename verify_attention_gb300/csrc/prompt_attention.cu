@@ -4,31 +4,38 @@
 // counterpart; the masks are those of fp8kv_paged_attention.)
 //
 // What bounds it: 4 * 128 operations for each visible (row, key) pair, on the
-// tensor cores; the K and V tiles come from L2.  One CTA computes two tiles of
-// 128 rows against the same K and V tiles: while the softmax of one tile runs,
-// the tensor cores work on the other.
+// tensor cores; the K and V tiles come from L2.  A work item is a pair of row
+// tiles of 128 rows against the same K and V tiles: while the softmax of one
+// tile runs, the tensor cores work on the other.
 //
 // Rows.  The G query heads of a KV head are packed: row r of a tile is position
 // r / G, head r % G, NP = 128 / G positions a tile (126 rows for G = 9).  The
 // rows of a tile then see nearly the same keys, so a diagonal or a window edge
 // costs little more than the keys it holds, and short prompts fill a tile.
 //
-// One CTA, 11 warps:
-//   warp 0     TMA: Q once, then K and V tiles of 128 keys through a ring of
-//              five 32 KiB slots; allocates and frees the tensor memory
-//   warp 1     issues the MMAs (one thread): per key tile P.V of the previous
-//              tile and Q.K^T of this one, for the first row tile, then for
-//              the second; S = Q.K^T from shared memory, O += P.V with P from
-//              tensor memory
-//   warps 2-5  softmax of the first row tile, one row per thread (warp w holds
-//   warps 6-9  ... of the second      TMEM lanes 32 (w % 4) ...)
-//   warp 10    zeroes the V rows of the first and last key tile that no row of
-//              the CTA sees (they may hold another sequence's values, or
-//              none): whatever is there, 0 * V reaches no output
-// Online softmax in the log2 domain; O is rescaled only when a row's maximum
-// grows by more than 2^8 (the weights stay below 2^8, sums are fp32).  P is
-// rounded to bf16, V's type, as the MMA needs both alike: 2^-9 of each weight,
-// the size of the output's own rounding.
+// Items.  The grid has one CTA per item; a resident CTA (one per SM) goes on
+// with the items of CTAs that have not started, which it cancels
+// (clusterlaunchcontrol), so that loads, set-up and output of one item overlap
+// the products of another, and the items are handed out longest first as SMs
+// come free, without a counter in memory.  Twelve warps:
+//   warp 0      loads by TMA: Q of each row tile once it is free, K and V tiles
+//               of 128 keys through a ring of five 32 KiB slots; allocates and
+//               frees the tensor memory
+//   warps 1, 2  issue the MMAs of the first and of the second row tile: per key
+//               tile Q.K^T, then P.V.  (One warp for both left the tensor cores
+//               idle 60% of the time: a wait or a commit takes it 40 to 100
+//               cycles, eight MMAs run 512.)
+//   warp 3      schedules: the next item, where its rows lie, into a queue; and
+//               zeroes the V rows of an item's first and last key tile that none
+//               of its rows sees (they may hold another sequence's values):
+//               whatever is there, 0 * V reaches no output
+//   warps 4-7   softmax and output of the first row tile, one row per thread
+//   warps 8-11  ... of the second         (warp w: TMEM lanes 32 (w % 4) ...)
+// Online softmax in the log2 domain over halves of a key tile, whose P.V starts
+// while the other half is exponentiated; O is rescaled only when a row's
+// maximum grows by more than 2^8 (the weights stay below 2^8, sums are fp32).
+// P is rounded to bf16, V's type, as the MMA needs both alike: 2^-9 of each
+// weight, the size of the output's own rounding.
 // TMEM columns: S/P of the two row tiles 0-127, 128-255 (P over the first half
 // of its S), O 256-383, 384-511.
 #include <stdio.h>
@@ -50,22 +57,29 @@ constexpr int NK = 128;                         // keys per tile
 constexpr int SLOT = NK * 256;                  // 32 KiB: two blocks of 128 rows x 64 dims (128-byte swizzled)
 constexpr int HALF = SLOT / 2;
 constexpr int SLOTS = 5;
-constexpr int WARPS = 11, THREADS = WARPS * 32;
+constexpr int WARPS = 12, THREADS = WARPS * 32;
+constexpr int QUEUE = 4;                        // items in the queue
 constexpr uint32_t TM_S = 0, TM_O = 256, TM_COLS = 512;
 constexpr int SMEM = 2 * SLOT + SLOTS * SLOT + 1024 + 512;
 
 enum {
-    B_Q = 0,
-    B_FULL = 1,
+    B_Q = 0,                                    // per row tile: Q loaded
+    B_QE = B_Q + 2,                             // ... read by its last Q.K^T
+    B_FULL = B_QE + 2,
     B_EMPTY = B_FULL + SLOTS,
     B_S = B_EMPTY + SLOTS,                      // per row tile: S ready
     B_P = B_S + 2,                              // per row tile and half: 64 columns of P ready
-    B_O = B_P + 4,                              // per row tile: O final
-    B_RAW = B_O + 2,                            // first / last V tile loaded, to be cleaned
-    B_STAGE = B_RAW + 2,                        // per row tile: output rows staged
-    B_IDLE = B_STAGE + 2,
-    B_COUNT
+    B_H = B_P + 4,                              // per row tile: P.V of the first half complete
+    B_O = B_H + 2,                              // per row tile: O final
+    B_OE = B_O + 2,                             // ... and read
+    B_RAW = B_OE + 2,                           // first / last V tile loaded, to be cleaned
+    B_ITEM = B_RAW + 2,                         // per queue entry: written
+    B_TAKEN = B_ITEM + QUEUE,                   // ... read by every role
+    B_NEXT = B_TAKEN + QUEUE,                   // answer of a cancel request
+    B_IDLE = B_NEXT + 1,                        // per MMA warp: nothing outstanding
+    B_COUNT = B_IDLE + 2
 };
+constexpr int ROLES = 1 + 2 + 8;                // readers of a queue entry: load, MMA, softmax warps
 
 struct Params {
     const int32_t* cu;          // [B + 1]
@@ -78,18 +92,33 @@ struct Params {
 constexpr uint32_t ID_QK = idesc(128, NK, false) | (1u << 7) | (1u << 10);
 constexpr uint32_t ID_PV = idesc(128, 128, true) | (1u << 7) | (1u << 10);
 
-__device__ __forceinline__ void mma_f16_ss(uint32_t d, uint64_t a, uint64_t b, uint32_t id, uint32_t acc) {
-    asm volatile(
-        "{ .reg .pred p; setp.ne.b32 p, %4, 0; "
-        "tcgen05.mma.cta_group::1.kind::f16 [%0], %1, %2, %3, p; }" ::"r"(d),
-        "l"(a), "l"(b), "r"(id), "r"(acc)
-        : "memory");
+// One thread of the (converged) warp, the same one every time.
+__device__ __forceinline__ bool elect_one() {
+    uint32_t r;
+    asm volatile("{ .reg .pred p; elect.sync _|p, 0xffffffff; selp.u32 %0, 1, 0, p; }" : "=r"(r));
+    return r != 0;
 }
 
-__device__ __forceinline__ void tma_store_3d(const CUtensorMap* tm, uint32_t src, int x, int y, int z) {
-    asm volatile("cp.async.bulk.tensor.3d.global.shared::cta.tile.bulk_group [%0, {%2, %3, %4}], [%1];" ::"l"(tm),
-                 "r"(src), "r"(x), "r"(y), "r"(z)
-                 : "memory");
+// Shared-memory matrix descriptor from its low word (see sdesc: address and
+// leading offset) with a stride of 1024 bytes and the 128-byte swizzle.
+__device__ __forceinline__ uint32_t desc_lo(uint32_t saddr, uint32_t lbo) {
+    return ((saddr >> 4) & 0x3FFFu) | ((lbo >> 4) << 16);
+}
+constexpr uint32_t DESC_HI = (1024u >> 4) | (1u << 14) | (2u << 29);
+
+__device__ __forceinline__ void mma_ss(uint32_t d, uint32_t a, uint32_t b, uint32_t id, uint32_t acc) {
+    asm volatile(
+        "{ .reg .pred p; .reg .b64 x, y; setp.ne.b32 p, %4, 0; mov.b64 x, {%1, %5}; mov.b64 y, {%2, %5}; "
+        "tcgen05.mma.cta_group::1.kind::f16 [%0], x, y, %3, p; }" ::"r"(d),
+        "r"(a), "r"(b), "r"(id), "r"(acc), "n"(DESC_HI)
+        : "memory");
+}
+__device__ __forceinline__ void mma_ts(uint32_t d, uint32_t a, uint32_t b, uint32_t id, uint32_t acc) {
+    asm volatile(
+        "{ .reg .pred p; .reg .b64 y; setp.ne.b32 p, %4, 0; mov.b64 y, {%2, %5}; "
+        "tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], y, %3, p; }" ::"r"(d),
+        "r"(a), "r"(b), "r"(id), "r"(acc), "n"(DESC_HI)
+        : "memory");
 }
 
 __device__ __forceinline__ uint64_t pack2(float lo, float hi) {
@@ -111,42 +140,87 @@ __device__ __forceinline__ uint64_t add2(uint64_t a, uint64_t b) {
     return r;
 }
 
-// Position of K and V tiles in the ring, in the order of their use:
-// K0 K1 V0 K2 V1 ... K(n-1) V(n-2) V(n-1).
-__device__ __forceinline__ int k_item(int j) { return j == 0 ? 0 : 2 * j - 1; }
-__device__ __forceinline__ int v_item(int j, int n) { return j == n - 1 ? 2 * n - 1 : 2 * j + 2; }
+__device__ __forceinline__ float max3(float a, float b, float c) {
+    float r;
+    asm("max.f32 %0, %1, %2, %3;" : "=f"(r) : "f"(a), "f"(b), "f"(c));
+    return r;
+}
+
+// Ask for a CTA of this grid that has not started to be cancelled; the answer
+// (16 bytes) arrives at `resp` and on `mbar`.
+__device__ __forceinline__ void cancel_request(uint32_t resp, uint32_t mbar) {
+    asm volatile("clusterlaunchcontrol.try_cancel.async.shared::cta.mbarrier::complete_tx::bytes.b128 [%0], [%1];" ::"r"(resp),
+                 "r"(mbar)
+                 : "memory");
+}
+// The cancelled CTA's index, or false when there was none left.
+__device__ __forceinline__ bool cancel_answer(uint32_t resp, int& x, int& y) {
+    uint32_t ok, a = 0, b = 0;
+    asm volatile(
+        "{ .reg .b128 h; .reg .pred p; .reg .b32 z, u; ld.shared.b128 h, [%3]; "
+        "clusterlaunchcontrol.query_cancel.is_canceled.pred.b128 p, h; selp.u32 %0, 1, 0, p; "
+        "@p clusterlaunchcontrol.query_cancel.get_first_ctaid.v4.b32.b128 {%1, %2, z, u}, h; }"
+        : "=r"(ok), "+r"(a), "+r"(b)
+        : "r"(resp)
+        : "memory");
+    x = (int)a;
+    y = (int)b;
+    return ok != 0;
+}
+
+// An item: rows p0 .. of the sequence of `len` tokens from token t0 on, KV head
+// hk; len = 0 ends the queue.
+struct Item {
+    int t0, len, p0, hk;
+    int tiles, j0, n;           // row tiles (1 or 2), first key tile, key tiles
+    int lo1, hi0;               // key tiles [0, hi0) of row tile 0, [lo1, n) of row tile 1
+    int see_lo, see_hi;         // keys that any row sees
+    __device__ __forceinline__ Item(int4 e, const Params& P) : t0(e.x), len(e.y), p0(e.z), hk(e.w) {
+        const int wl = P.window_left, last = len - 1;
+        tiles = p0 + P.NP < len ? 2 : 1;
+        see_lo = wl >= 0 ? max(0, p0 - wl) : 0;
+        see_hi = min(last, p0 + tiles * P.NP - 1);
+        j0 = see_lo / NK;
+        n = see_hi / NK + 1 - j0;
+        hi0 = min(last, p0 + P.NP - 1) / NK + 1 - j0;
+        lo1 = wl >= 0 ? max(0, p0 + P.NP - wl) / NK - j0 : 0;
+    }
+    __device__ __forceinline__ bool has(int i, int j) const { return i ? tiles == 2 && j >= lo1 : j < hi0; }
+    __device__ __forceinline__ int first(int i) const { return i ? lo1 : 0; }
+    __device__ __forceinline__ int last(int i) const { return (i ? n : hi0) - 1; }
+    // V tiles with rows that none of the item's rows sees: such a tile lands on
+    // a barrier of its own, for warp 3, which clears those rows and then
+    // arrives on the slot's barrier
+    __device__ __forceinline__ bool cleaned(int j) const {
+        return (j == n - 1 && (j0 + n) * NK - 1 > see_hi) || (j == 0 && j0 * NK < see_lo);
+    }
+};
 
 __global__ void __launch_bounds__(THREADS, 1)
     prompt_attention_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__ CUtensorMap tm_k,
-                            const __grid_constant__ CUtensorMap tm_v, const __grid_constant__ CUtensorMap tm_o,
-                            Params P) {
+                            const __grid_constant__ CUtensorMap tm_v, const Params P) {
     extern __shared__ uint8_t smem_raw[];
     uint8_t* smem = (uint8_t*)(((uintptr_t)smem_raw + 1023) & ~(uintptr_t)1023);
     uint8_t* qs = smem;                                     // two row tiles of 32 KiB
     uint8_t* ring = smem + 2 * SLOT;
-    uint64_t* bars = (uint64_t*)(ring + SLOTS * SLOT);
+    int4* queue = (int4*)(ring + SLOTS * SLOT);
+    int4* answer = queue + QUEUE;
+    uint64_t* bars = (uint64_t*)(answer + 1);
     uint32_t* tmem_slot = (uint32_t*)(bars + B_COUNT);
-    int* where = (int*)(tmem_slot + 1);                     // sequence start, length, first position
+    static_assert((QUEUE + 1) * 16 + B_COUNT * 8 + 4 <= 512, "shared memory behind the ring");
     auto bar = [&](int i) { return smem_u32(&bars[i]); };
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-    const int hk = blockIdx.x;
     const int rows = P.G * P.NP;                            // used rows of a tile
     pdl_launch_dependents();
 
     if (threadIdx.x == 0) {
-        mbar_init(bar(B_Q), 1);
-        for (int i = 0; i < SLOTS; ++i) {
-            mbar_init(bar(B_FULL + i), 1);
-            mbar_init(bar(B_EMPTY + i), 1);
+        for (int i = 0; i < B_COUNT; ++i) {
+            int count = 1;
+            if ((i >= B_P && i < B_P + 4) || (i >= B_OE && i < B_OE + 2)) count = 4;    // softmax warps
+            if (i >= B_EMPTY && i < B_EMPTY + SLOTS) count = 2;                         // MMA warps
+            if (i >= B_TAKEN && i < B_TAKEN + QUEUE) count = ROLES;
+            mbar_init(bar(i), count);
         }
-        for (int i = 0; i < 2; ++i) {
-            mbar_init(bar(B_S + i), 1);
-            mbar_init(bar(B_O + i), 1);
-            mbar_init(bar(B_RAW + i), 1);
-        }
-        for (int i = 0; i < 4; ++i) mbar_init(bar(B_P + i), 4);
-        for (int i = 0; i < 2; ++i) mbar_init(bar(B_STAGE + i), 4);
-        mbar_init(bar(B_IDLE), 1);
         fence_barrier_init();
     }
     if (warp == 0) {
@@ -158,7 +232,6 @@ __global__ void __launch_bounds__(THREADS, 1)
             prefetch_tensormap(&tm_q);
             prefetch_tensormap(&tm_k);
             prefetch_tensormap(&tm_v);
-            prefetch_tensormap(&tm_o);
         }
     }
     // rows behind G * NP take part in the MMAs: zeros there keep them finite
@@ -167,289 +240,386 @@ __global__ void __launch_bounds__(THREADS, 1)
         *(uint4*)(qs + blk * HALF + r * 128 + c * 16) = make_uint4(0, 0, 0, 0);
     }
     fence_proxy_async();
-    pdl_wait();
-    if (warp == 10) {
-        // Pair x (two row tiles, 2 NP positions) of the whole launch, the last
-        // ones first: sequence b owns the indices from cu[b] / (2 NP) + b on,
-        // at least as many as it has pairs, so the largest b whose first index
-        // is at most x is found by a 32-way search, without a scan.
-        const int PP = 2 * P.NP, x = (int)(gridDim.y - 1 - blockIdx.y);
-        int lo = 0, hi = P.B;
-        while (hi - lo > 1) {
-            const int step = (hi - lo + 31) / 32, at = lo + lane * step;
-            const uint32_t m = __ballot_sync(0xffffffffu, at < hi && P.cu[min(at, P.B)] / PP + at <= x);
-            lo += m ? (31 - __clz(m)) * step : 0;
-            hi = min(hi, lo + step);
-        }
-        const int s0 = P.cu[lo], s1 = P.cu[lo + 1];
-        const bool good = s0 >= 0 && s1 >= s0 && s1 <= P.T && s1 - s0 <= P.max_seq_len;
-        const int p0 = (x - (s0 / PP + lo)) * PP;
-        if (lane == 0) {
-            where[0] = s0;
-            where[1] = good && p0 >= 0 && p0 < s1 - s0 ? s1 - s0 : 0;   // 0: nothing to do
-            where[2] = p0;
-            if (hk == 0 && x < P.B) {                       // every sequence's bounds are looked at once
-                const int c0 = P.cu[x], c1 = P.cu[x + 1];
-                if (c0 < 0 || c1 < c0 || c1 > P.T || c1 - c0 > P.max_seq_len) flag(FP8KV_DEV_BAD_SEQ_LEN);
-            }
-        }
-    }
     fence_before();
     __syncthreads();
     fence_after();
     const uint32_t tmem = *tmem_slot;
-    const int t0 = where[0], len = where[1], p0 = where[2];
-    // per row tile i: positions p0 + i NP ..., keys [klo, khi] that its rows
-    // see, key tiles [jlo, jhi)
-    const int n_tiles_rows = len == 0 ? 0 : (p0 + P.NP < len ? 2 : 1);
-    auto key_lo = [&](int i) { return P.window_left >= 0 ? max(0, p0 + i * P.NP - P.window_left) : 0; };
-    auto key_hi = [&](int i) { return min(len - 1, p0 + (i + 1) * P.NP - 1); };
-    const int j0 = key_lo(0) / NK, j1 = len ? key_hi(max(n_tiles_rows - 1, 0)) / NK + 1 : 0;
-    const int n = j1 - j0;                                  // key tiles of the CTA
-    const int jlo1 = key_lo(1) / NK, jhi0 = len ? key_hi(0) / NK + 1 : 0;
-    // key tiles of row tile i, counted from j0: [lo_of(i), hi_of(i))
-    auto lo_of = [&](int i) { return i ? jlo1 - j0 : 0; };
-    auto hi_of = [&](int i) { return i ? (n_tiles_rows == 2 ? n : lo_of(1)) : jhi0 - j0; };
-    // V rows that no row of the CTA sees, in the first and the last key tile:
-    // such a V tile lands on a barrier of its own, for warp 10, which clears
-    // those rows and then arrives on the slot's barrier
-    const int see_lo = key_lo(0), see_hi = len ? key_hi(n_tiles_rows - 1) : 0;
-    const bool clean_first = j0 * NK < see_lo, clean_last = j1 * NK - 1 > see_hi;
-    auto cleaned = [&](int j) { return (j == n - 1 && clean_last) || (j == 0 && clean_first); };
+    pdl_wait();
     bool ok = true;
+    // the queue's next entry (every role reads every entry, in order); false
+    // after the last one
+    int taken = 0;
+    auto next_item = [&](int4& e) -> bool {
+        const int s = taken % QUEUE;
+        ok = __all_sync(0xffffffffu, mbar_wait(bar(B_ITEM + s), (taken / QUEUE) & 1));
+        if (!ok) return false;
+        e = queue[s];
+        ++taken;
+        __syncwarp();
+        if (lane == 0) mbar_arrive(bar(B_TAKEN + s));
+        return e.y != 0;
+    };
 
-    if (n_tiles_rows == 0) {
-        // no rows here
-    } else if (warp == 0) {
+    if (warp == 0) {
         // ------------------------------------------------------------ loads
-        if (lane == 0) {
-            uint64_t keep;                                  // K and V are read by many CTAs, Q by one
-            asm volatile("createpolicy.fractional.L2::evict_normal.b64 %0, 1.0;" : "=l"(keep));
-            mbar_expect_tx(bar(B_Q), n_tiles_rows * 2 * rows * 128);
-            for (int i = 0; i < n_tiles_rows; ++i)
-                for (int h = 0; h < 2; ++h)
-                    tma_load_3d(smem_u32(qs + i * SLOT + h * HALF), &tm_q, 64 * h, hk * P.G, t0 + p0 + i * P.NP,
-                                bar(B_Q), policy_evict_first());
-            int done = 0, raw = 0;
-            for (int it = 0; it < 2 * n && ok; ++it) {
-                // item -> tile: K0, then K(j), V(j - 1) in turn, V(n - 1) last
-                const bool is_k = it == 0 || ((it & 1) && it != 2 * n - 1);
-                const int j = it == 0 ? 0 : (it == 2 * n - 1 ? n - 1 : ((it & 1) ? (it + 1) / 2 : it / 2 - 1));
-                const int s = it % SLOTS, use = it / SLOTS;
-                if (use > 0) ok = mbar_wait(bar(B_EMPTY + s), (use - 1) & 1);
-                if (!ok) break;
-                const uint32_t full = !is_k && cleaned(j) ? bar(B_RAW + (j == n - 1)) : bar(B_FULL + s);
-                mbar_expect_tx(full, SLOT);
-                for (int h = 0; h < 2; ++h)
-                    tma_load_3d(smem_u32(ring + s * SLOT + h * HALF), is_k ? &tm_k : &tm_v, 64 * h, hk,
-                                t0 + (j0 + j) * NK, full, keep);
-                done = it + 1;
-                if (full != bar(B_FULL + s)) raw |= 1 << (j == n - 1);
+        uint64_t keep;                                      // K and V are read by many CTAs, Q by one
+        asm volatile("createpolicy.fractional.L2::evict_normal.b64 %0, 1.0;" : "=l"(keep));
+        const uint64_t once = policy_evict_first();
+        int4 e;
+        int done = 0, q_use[2] = {0, 0}, raw_use[2] = {0, 0};
+        while (next_item(e)) {
+            const Item it(e, P);
+            if (lane == 0) {
+                auto load_q = [&](int i) {
+                    if (q_use[i] > 0) ok = mbar_wait(bar(B_QE + i), (q_use[i] - 1) & 1);
+                    if (!ok) return;
+                    mbar_expect_tx(bar(B_Q + i), 2 * rows * 128);
+                    for (int h = 0; h < 2; ++h)
+                        tma_load_3d(smem_u32(qs + i * SLOT + h * HALF), &tm_q, 64 * h, it.hk * P.G,
+                                    it.t0 + it.p0 + i * P.NP, bar(B_Q + i), once);
+                    ++q_use[i];
+                };
+                load_q(0);
+                for (int u = 0; u < 2 * it.n && ok; ++u) {  // K(0) V(0) K(1) V(1) ...
+                    const int j = u >> 1, s = done % SLOTS, use = done / SLOTS;
+                    if (use > 0) ok = mbar_wait(bar(B_EMPTY + s), (use - 1) & 1);
+                    if (!ok) break;
+                    uint32_t full = bar(B_FULL + s);
+                    if ((u & 1) && it.cleaned(j)) {
+                        full = bar(B_RAW + (j == it.n - 1));
+                        if (j == it.n - 1) ++raw_use[1];
+                        else ++raw_use[0];
+                    }
+                    mbar_expect_tx(full, SLOT);
+                    for (int h = 0; h < 2; ++h)
+                        tma_load_3d(smem_u32(ring + s * SLOT + h * HALF), u & 1 ? &tm_v : &tm_k, 64 * h, it.hk,
+                                    it.t0 + (it.j0 + j) * NK, full, keep);
+                    ++done;
+                    if (u == 0 && it.tiles == 2) load_q(1);
+                }
             }
+            ok = __shfl_sync(0xffffffffu, ok, 0);
+            if (!ok) break;
+        }
+        if (lane == 0) {
             // never leave with copies into this CTA's shared memory in flight
-            mbar_wait(bar(B_Q), 0);
-            for (int e = 0; e < 2; ++e)
-                if (raw >> e & 1) mbar_wait(bar(B_RAW + e), 0);
-            for (int it = max(0, done - SLOTS); it < done; ++it) mbar_wait(bar(B_FULL + it % SLOTS), (it / SLOTS) & 1);
+#pragma unroll
+            for (int i = 0; i < 2; ++i) {
+                if (q_use[i]) mbar_wait(bar(B_Q + i), (q_use[i] - 1) & 1);
+                if (raw_use[i]) mbar_wait(bar(B_RAW + i), (raw_use[i] - 1) & 1);
+            }
+            for (int u = max(0, done - SLOTS); u < done; ++u) mbar_wait(bar(B_FULL + u % SLOTS), (u / SLOTS) & 1);
         }
         __syncwarp();
-    } else if (warp == 1) {
-        // --------------------------------------------------------- MMA issue
-        if (lane == 0) {
-            ok = mbar_wait(bar(B_Q), 0);
-            for (int j = 0; j <= n && ok; ++j) {
-                for (int i = 0; i < n_tiles_rows && ok; ++i) {
-                    if (j >= 1 && j - 1 >= lo_of(i) && j - 1 < hi_of(i)) {
-                        // O_i += P_i(j - 1) V(j - 1)
-                        const int vi = v_item(j - 1, n), c = j - 1 - lo_of(i);
-                        ok = mbar_wait(bar(B_FULL + vi % SLOTS), (vi / SLOTS) & 1);
-                        const uint32_t vt = smem_u32(ring + (vi % SLOTS) * SLOT);
-                        for (int h = 0; h < 2 && ok; ++h) {
-                            ok = mbar_wait(bar(B_P + 2 * i + h), c & 1);
+    } else if (warp < 3) {
+        // ------------------------------------- MMA issue of row tile i = warp - 1
+        const int i = warp - 1;
+        const bool leader = elect_one();
+        const uint32_t s_col = tmem + TM_S + 128 * i, o_col = tmem + TM_O + 128 * i;
+        const uint32_t q_lo = desc_lo(smem_u32(qs + i * SLOT), 16);
+        const uint32_t k_lo0 = desc_lo(smem_u32(ring), 16), v_lo0 = desc_lo(smem_u32(ring), HALF);
+        int slot = 0, phase = 0;                            // the ring's next item
+        auto advance = [&]() {
+            if (++slot == SLOTS) {
+                slot = 0;
+                phase ^= 1;
+            }
+        };
+        int tile = 0, items = 0;                            // key tiles and items of this row tile so far
+        int4 e;
+        while (next_item(e)) {
+            const Item it(e, P);
+            const bool mine = i < it.tiles;
+            const int jf = mine ? it.first(i) : 0, jl = mine ? it.last(i) : -1;
+            if (mine) {
+                ok = mbar_wait(bar(B_Q + i), items & 1);
+                ++items;
+            }
+            int v_slot = 0, v_phase = 0;
+            for (int j = 0; j <= it.n && ok; ++j) {
+                if (j > 0) {
+                    // O += P(j - 1) V(j - 1)
+                    const bool on = j - 1 >= jf && j - 1 <= jl;
+                    ok = mbar_wait(bar(B_FULL + v_slot), v_phase);
+                    if (!ok) break;
+                    if (on) {
+                        // O of the previous item has been read
+                        if (j - 1 == jf && items > 1) ok = mbar_wait(bar(B_OE + i), items & 1);
+                        const uint32_t v_lo = v_lo0 + v_slot * (SLOT >> 4);
+#pragma unroll
+                        for (int h = 0; h < 2; ++h) {
+                            if (ok) ok = mbar_wait(bar(B_P + 2 * i + h), tile & 1);
                             if (!ok) break;
                             fence_after();
+                            if (leader) {
 #pragma unroll
-                            for (int kk = 4 * h; kk < 4 * h + 4; ++kk)
-                                mma_f16_ts(tmem + TM_O + 128 * i, tmem + TM_S + 128 * i + 8 * kk,
-                                           sdesc(vt + kk * 2048, HALF, 1024), ID_PV, (c > 0 || kk > 0));
+                                for (int kk = 4 * h; kk < 4 * h + 4; ++kk)
+                                    mma_ts(o_col, s_col + 8 * kk, v_lo + kk * (2048 >> 4), ID_PV, j - 1 > jf || kk > 0);
+                                if (h == 0) mma_commit(bar(B_H + i));
+                            }
+                            __syncwarp();
                         }
-                        if (ok && j - 1 == hi_of(i) - 1) mma_commit(bar(B_O + i));
-                    }
-                    if (ok && j < n && j >= lo_of(i) && j < hi_of(i)) {
-                        // S_i = Q_i K(j)^T (over P_i(j - 1), which the MMAs above have read)
-                        const int ki = k_item(j);
-                        ok = mbar_wait(bar(B_FULL + ki % SLOTS), (ki / SLOTS) & 1);
                         if (!ok) break;
-                        fence_after();
-                        const uint32_t kt = smem_u32(ring + (ki % SLOTS) * SLOT), qt = smem_u32(qs + i * SLOT);
-#pragma unroll
-                        for (int ks = 0; ks < 8; ++ks) {
-                            const uint32_t off = (ks >> 2) * HALF + (ks & 3) * 32;
-                            mma_f16_ss(tmem + TM_S + 128 * i, sdesc(qt + off, 16, 1024), sdesc(kt + off, 16, 1024),
-                                       ID_QK, ks > 0);
-                        }
-                        mma_commit(bar(B_S + i));
+                        ++tile;
                     }
+                    if (leader) {
+                        if (on) mma_commit(bar(B_EMPTY + v_slot));
+                        else mbar_arrive(bar(B_EMPTY + v_slot));
+                        if (j - 1 == jl) mma_commit(bar(B_O + i));
+                    }
+                    __syncwarp();
                 }
-                // the slots this step has read, once its MMAs are complete
-                if (ok && j < n) mma_commit(bar(B_EMPTY + k_item(j) % SLOTS));
-                if (ok && j >= 1) mma_commit(bar(B_EMPTY + v_item(j - 1, n) % SLOTS));
+                if (j < it.n) {
+                    // S = Q K(j)^T, over P(j - 1), which the MMAs above have read
+                    const bool on = j >= jf && j <= jl;
+                    ok = mbar_wait(bar(B_FULL + slot), phase);
+                    if (!ok) break;
+                    fence_after();
+                    if (leader) {
+                        if (on) {
+                            const uint32_t k_lo = k_lo0 + slot * (SLOT >> 4);
+#pragma unroll
+                            for (int kk = 0; kk < 8; ++kk) {
+                                const uint32_t off = ((kk >> 2) * HALF + (kk & 3) * 32) >> 4;
+                                mma_ss(s_col, q_lo + off, k_lo + off, ID_QK, kk > 0);
+                            }
+                            mma_commit(bar(B_S + i));
+                            mma_commit(bar(B_EMPTY + slot));
+                            if (j == jl) mma_commit(bar(B_QE + i));
+                        } else {
+                            mbar_arrive(bar(B_EMPTY + slot));
+                        }
+                    }
+                    __syncwarp();
+                    advance();
+                    v_slot = slot;
+                    v_phase = phase;
+                    advance();
+                }
             }
-            // nothing the tensor cores still run may outlive the TMEM allocation
-            mma_commit(bar(B_IDLE));
-            mbar_wait(bar(B_IDLE), 0);
+            ok = __all_sync(0xffffffffu, ok);
+            if (!ok) break;
         }
+        // nothing the tensor cores still run may outlive the TMEM allocation
+        if (leader) mma_commit(bar(B_IDLE + i));
         __syncwarp();
-    } else if (warp == 10) {
-        // ----------------------------------------------- V rows nobody sees
-        for (int e = 0; e < 2; ++e) {
-            const int j = e ? n - 1 : 0;
-            if (!cleaned(j) || (e == 0 && j == n - 1)) continue;
-            const int vi = v_item(j, n), k0 = (j0 + j) * NK;
-            ok = mbar_wait(bar(B_RAW + e), 0);
-            if (!__all_sync(0xffffffffu, ok)) break;
-            uint8_t* vt = ring + (vi % SLOTS) * SLOT;
-            const int a = max(0, min(NK, see_lo - k0)), z = max(0, min(NK, see_hi + 1 - k0));
-            for (int i = lane; i < NK * 8; i += 32) {       // rows [0, a) and [z, 128)
-                const int r = i >> 3;
-                if (r >= a && r < z) continue;
-                *(uint4*)(vt + i * 16) = make_uint4(0, 0, 0, 0);
-                *(uint4*)(vt + HALF + i * 16) = make_uint4(0, 0, 0, 0);
+        mbar_wait(bar(B_IDLE + i), 0);
+        __syncwarp();
+    } else if (warp == 3) {
+        // ------------------------------------------------- schedule and clean
+        // Pair x (2 NP positions) of the launch, the last ones first: sequence
+        // b owns the indices from cu[b] / (2 NP) + b on, at least as many as it
+        // has pairs, so the largest b whose first index is at most x is found
+        // by a 32-way search, without a scan.
+        const int PP = 2 * P.NP;
+        int put = 0, bx = blockIdx.x, by = blockIdx.y;
+        auto put_item = [&](int4 e) {
+            const int s = put % QUEUE;
+            if (put >= QUEUE) ok = ok && __all_sync(0xffffffffu, mbar_wait(bar(B_TAKEN + s), (put / QUEUE - 1) & 1));
+            if (lane == 0 && ok) {
+                queue[s] = e;
+                mbar_arrive(bar(B_ITEM + s));
             }
-            fence_proxy_async();
             __syncwarp();
-            if (lane == 0) mbar_arrive(bar(B_FULL + vi % SLOTS));
+            ++put;
+        };
+        int base = 0, raw_use[2] = {0, 0};
+        auto clean = [&](int4 e) {
+            const Item it(e, P);
+#pragma unroll
+            for (int f = 0; f < 2; ++f) {
+                const int j = f ? it.n - 1 : 0;
+                if (!ok || !it.cleaned(j) || (f == 0 && j == it.n - 1)) continue;
+                ok = __all_sync(0xffffffffu, mbar_wait(bar(B_RAW + f), raw_use[f] & 1));
+                if (!ok) continue;
+                ++raw_use[f];
+                const int s = (base + 2 * j + 1) % SLOTS, k0 = (it.j0 + j) * NK;
+                uint8_t* vt = ring + s * SLOT;
+                const int a = max(0, min(NK, it.see_lo - k0)), z = max(0, min(NK, it.see_hi + 1 - k0));
+                for (int i = lane; i < NK * 8; i += 32) {   // rows [0, a) and [z, 128)
+                    const int r = i >> 3;
+                    if (r >= a && r < z) continue;
+                    *(uint4*)(vt + i * 16) = make_uint4(0, 0, 0, 0);
+                    *(uint4*)(vt + HALF + i * 16) = make_uint4(0, 0, 0, 0);
+                }
+                fence_proxy_async();
+                __syncwarp();
+                if (lane == 0) mbar_arrive(bar(B_FULL + s));
+            }
+            base += 2 * it.n;
+        };
+        // every item is put into the queue before the V tiles of the one
+        // before it are cleaned: the loads run ahead
+        int4 before = make_int4(0, 0, 0, 0);
+        bool more = true;
+        for (int k = 0; more && ok; ++k) {
+            const int x = (int)(gridDim.y - 1) - by, hk = bx;
+            // the request for the item after this one is under way meanwhile
+            if (lane == 0) {
+                fence_proxy_async();                        // the last answer was read before this one is written
+                mbar_expect_tx(bar(B_NEXT), 16);
+                cancel_request(smem_u32(answer), bar(B_NEXT));
+            }
+            int lo = 0, hi = P.B;
+            while (hi - lo > 1) {
+                const int step = (hi - lo + 31) / 32, at = lo + lane * step;
+                const uint32_t m = __ballot_sync(0xffffffffu, at < hi && P.cu[min(at, P.B)] / PP + at <= x);
+                lo += m ? (31 - __clz(m)) * step : 0;
+                hi = min(hi, lo + step);
+            }
+            const int s0 = P.cu[lo], s1 = P.cu[lo + 1];
+            const bool good = s0 >= 0 && s1 >= s0 && s1 <= P.T && s1 - s0 <= P.max_seq_len;
+            const int p0 = (x - (s0 / PP + lo)) * PP;
+            if (lane == 0 && hk == 0 && x < P.B) {          // every sequence's bounds are looked at once
+                const int c0 = P.cu[x], c1 = P.cu[x + 1];
+                if (c0 < 0 || c1 < c0 || c1 > P.T || c1 - c0 > P.max_seq_len) flag(FP8KV_DEV_BAD_SEQ_LEN);
+            }
+            if (good && p0 >= 0 && p0 < s1 - s0) {
+                const int4 e = make_int4(s0, s1 - s0, p0, hk);
+                put_item(e);
+                if (ok && before.y) clean(before);
+                before = e;
+            }
+            const bool got = mbar_wait(bar(B_NEXT), k & 1);
+            more = __all_sync(0xffffffffu, got && cancel_answer(smem_u32(answer), bx, by));
+            __syncwarp();
         }
-    } else if ((warp - 2) >> 2 < n_tiles_rows) {
-        // ----------------------------------------------------------- softmax
-        const int i = (warp - 2) >> 2, wq = warp & 3;
+        if (ok) put_item(make_int4(0, 0, 0, 0));
+        if (ok && before.y) clean(before);
+    } else {
+        // ----------------------------------------------- softmax and output
+        const int i = (warp - 4) >> 2, wq = warp & 3;
         const int r = wq * 32 + lane;
-        const int base = p0 + i * P.NP;                     // first position of the row tile
-        const int pos = base + min(r, rows - 1) / P.G;
-        const int lo_r = P.window_left >= 0 ? max(0, pos - P.window_left) : 0;
-        // the warp's bounds: key tiles inside them need no mask
-        const int pmin = base + min(wq * 32, rows - 1) / P.G;
-        const int plast = base + min(wq * 32 + 31, rows - 1) / P.G;
-        const int lomax = P.window_left >= 0 ? max(0, plast - P.window_left) : 0;
         const uint32_t lanes = tmem + ((uint32_t)(wq * 32) << 16);
         const uint32_t s_col = lanes + TM_S + 128 * i, o_col = lanes + TM_O + 128 * i;
         const float mult = P.scale_log2;
-        const int a = lo_of(i), z = hi_of(i);
-        float m_run = -INFINITY, l_run = 0.f;
+        // position of this row and of the warp's first and last within a tile
+        const int dpos = min(r, rows - 1) / P.G, head = min(r, rows - 1) % P.G;
+        const int dfirst = min(wq * 32, rows - 1) / P.G, dlast = min(wq * 32 + 31, rows - 1) / P.G;
+        int s_use = 0, o_use = 0;
+        int4 e;
+        while (next_item(e)) {
+            const Item it(e, P);
+            if (i >= it.tiles) continue;
+            const int tile0 = it.p0 + i * P.NP, pos = tile0 + dpos;
+            const int lo_r = P.window_left >= 0 ? max(0, pos - P.window_left) : 0;
+            // key tiles inside these bounds need no mask
+            const int pmin = tile0 + dfirst;
+            const int lomax = P.window_left >= 0 ? max(0, tile0 + dlast - P.window_left) : 0;
+            float m_run = -INFINITY, l_run = 0.f;
+            const int j_end = it.last(i);
 #pragma unroll 1
-        for (int j = a; j < z; ++j) {
-            const int k0 = (j0 + j) * NK;
-            ok = mbar_wait(bar(B_S + i), (j - a) & 1);
-            if (!__all_sync(0xffffffffu, ok)) { ok = false; break; }
-            fence_after();
-            uint32_t sv[4][32];
+            for (int j = it.first(i); j <= j_end; ++j) {
+                const int k0 = (it.j0 + j) * NK;
+                ok = mbar_wait(bar(B_S + i), s_use & 1);
+                // (the first half's product of the tile before: complete long
+                // since; waited for so that no phase of the barrier is missed)
+                if (ok && s_use > 0) ok = mbar_wait(bar(B_H + i), (s_use - 1) & 1);
+                if (!__all_sync(0xffffffffu, ok)) { ok = false; break; }
+                fence_after();
+                const bool need_mask = k0 + NK - 1 > pmin || k0 < lomax;
+                const uint64_t mult2 = pack2(mult, mult);
 #pragma unroll
-            for (int c = 0; c < 4; ++c) tmem_ld_x32(s_col + 32 * c, sv[c]);
-            tmem_wait_ld();
-            if (k0 + NK - 1 > pmin || k0 < lomax) {
-                // visible columns [c0, c1) of this row
-                const int c0 = lo_r - k0, c1 = pos - k0 + 1;
-#pragma unroll
-                for (int c = 0; c < 4; ++c)
-#pragma unroll
-                    for (int u = 0; u < 32; ++u)
-                        if (32 * c + u < c0 || 32 * c + u >= c1) sv[c][u] = 0xff800000u;   // -inf
-            }
-            float m4[4];
-#pragma unroll
-            for (int c = 0; c < 4; ++c) {
-                m4[c] = __uint_as_float(sv[c][0]);
-#pragma unroll
-                for (int u = 1; u < 32; ++u) m4[c] = fmaxf(m4[c], __uint_as_float(sv[c][u]));
-            }
-            const float tmax = fmaxf(fmaxf(m4[0], m4[1]), fmaxf(m4[2], m4[3])) * mult;
-            const bool grow = m_run != -INFINITY && tmax > m_run + 8.0f;
-            if (__any_sync(0xffffffffu, grow)) {
-                // S(j) ready means that P.V of the tiles before is complete
-                const float alpha = grow ? ex2(m_run - tmax) : 1.0f;
-#pragma unroll 1
-                for (int c = 0; c < 128; c += 32) {
-                    uint32_t ov[32];
-                    tmem_ld_x32(o_col + c, ov);
+                for (int h = 0; h < 2; ++h) {
+                    uint32_t sv[64];
+                    tmem_ld_x64(s_col + 64 * h, sv);
                     tmem_wait_ld();
+                    if (need_mask) {
+                        // this row's visible columns of the half as bits
+                        const int c0 = max(0, lo_r - k0 - 64 * h), c1 = min(64, pos - k0 - 64 * h + 1);
+                        const uint64_t below1 = c1 <= 0 ? 0ull : (c1 >= 64 ? ~0ull : (1ull << c1) - 1);
+                        const uint64_t below0 = c0 >= 64 ? ~0ull : (1ull << c0) - 1;
+                        const uint64_t see = below1 & ~below0;
+                        const uint32_t see0 = (uint32_t)see, see1 = (uint32_t)(see >> 32);
 #pragma unroll
-                    for (int u = 0; u < 32; ++u) ov[u] = __float_as_uint(__uint_as_float(ov[u]) * alpha);
-                    tmem_st_x32(o_col + c, ov);
-                }
-                tmem_wait_st();
-                if (grow) {
-                    l_run *= alpha;
-                    m_run = tmax;
-                }
-            }
-            if (m_run == -INFINITY) m_run = tmax;
-            const float neg = m_run == -INFINITY ? 0.f : -m_run;
-            const uint64_t mult2 = pack2(mult, mult), neg2 = pack2(neg, neg);
-            uint64_t sum2 = 0;
+                        for (int u = 0; u < 64; ++u)
+                            sv[u] = ((u < 32 ? see0 : see1) >> (u & 31)) & 1u ? sv[u] : 0xff800000u;   // -inf
+                    }
+                    float m2[2] = {__uint_as_float(sv[0]), __uint_as_float(sv[1])};
 #pragma unroll
-            for (int c = 0; c < 4; ++c) {
-                uint32_t pw[16];
+                    for (int u = 2; u < 62; u += 4) {
+                        m2[0] = max3(m2[0], __uint_as_float(sv[u]), __uint_as_float(sv[u + 1]));
+                        m2[1] = max3(m2[1], __uint_as_float(sv[u + 2]), __uint_as_float(sv[u + 3]));
+                    }
+                    const float tmax = max3(m2[0], m2[1], fmaxf(__uint_as_float(sv[62]), __uint_as_float(sv[63]))) * mult;
+                    const bool grow = m_run != -INFINITY && tmax > m_run + 8.0f;
+                    if (__any_sync(0xffffffffu, grow)) {
+                        // S(j) ready means that P.V of the tiles before is
+                        // complete; the first half's of this one is waited for
+                        if (h == 1) {
+                            ok = mbar_wait(bar(B_H + i), s_use & 1);
+                            if (!__all_sync(0xffffffffu, ok)) { ok = false; break; }
+                            fence_after();
+                        }
+                        const float alpha = grow ? ex2(m_run - tmax) : 1.0f;
+#pragma unroll 1
+                        for (int c = 0; c < 128; c += 32) {
+                            uint32_t ov[32];
+                            tmem_ld_x32(o_col + c, ov);
+                            tmem_wait_ld();
 #pragma unroll
-                for (int u = 0; u < 16; ++u) {
-                    float x0, x1;
-                    unpack2(fma2(pack2(__uint_as_float(sv[c][2 * u]), __uint_as_float(sv[c][2 * u + 1])), mult2, neg2),
-                            x0, x1);
-                    x0 = ex2(x0);
-                    x1 = ex2(x1);
-                    sum2 = add2(sum2, pack2(x0, x1));
-                    pw[u] = pack_bf16x2(x0, x1);
-                }
-                tmem_st_x16(s_col + 16 * c, pw);
-                if (c & 1) {                                // 64 columns of P: their MMAs may start
+                            for (int u = 0; u < 32; ++u) ov[u] = __float_as_uint(__uint_as_float(ov[u]) * alpha);
+                            tmem_st_x32(o_col + c, ov);
+                        }
+                        tmem_wait_st();
+                        if (grow) {
+                            l_run *= alpha;
+                            m_run = tmax;
+                        }
+                    }
+                    if (m_run == -INFINITY) m_run = tmax;
+                    const float neg = m_run == -INFINITY ? 0.f : -m_run;
+                    const uint64_t neg2 = pack2(neg, neg);
+                    uint64_t sum2[2] = {0, 0};
+                    uint32_t pw[32];
+#pragma unroll
+                    for (int u = 0; u < 32; ++u) {
+                        float x0, x1;
+                        unpack2(fma2(pack2(__uint_as_float(sv[2 * u]), __uint_as_float(sv[2 * u + 1])), mult2, neg2),
+                                x0, x1);
+                        x0 = ex2(x0);
+                        x1 = ex2(x1);
+                        sum2[u & 1] = add2(sum2[u & 1], pack2(x0, x1));
+                        pw[u] = pack_bf16x2(x0, x1);
+                    }
+                    tmem_st_x32(s_col + 32 * h, pw);
+                    float s0, s1;
+                    unpack2(add2(sum2[0], sum2[1]), s0, s1);
+                    l_run += s0 + s1;
                     tmem_wait_st();
                     fence_before();
                     __syncwarp();
-                    if (lane == 0) mbar_arrive(bar(B_P + 2 * i + (c >> 1)));
+                    if (lane == 0) mbar_arrive(bar(B_P + 2 * i + h));
                 }
+                if (!ok) break;
+                ++s_use;
             }
-            float s0, s1;
-            unpack2(sum2, s0, s1);
-            l_run += s0 + s1;
-        }
-        // ---------------------------------------------------------- epilogue
-        if (ok) ok = mbar_wait(bar(B_O + i), 0);
-        ok = __all_sync(0xffffffffu, ok);
-        if (ok) {
+            // ------------------------------------------------------ output
+            if (ok) ok = mbar_wait(bar(B_O + i), o_use & 1);
+            ok = __all_sync(0xffffffffu, ok);
+            if (!ok) break;
+            ++o_use;
             fence_after();
             const float inv = 1.0f / l_run;
-            const bool whole = base + P.NP <= len;          // every used row is one of the sequence
-            uint8_t* stage = qs + i * SLOT;                 // Q of this tile is consumed
-            const bool live = r < rows && base + r / P.G < len;
-            uint16_t* dst = P.out + ((int64_t)(t0 + pos) * P.Hq + hk * P.G + min(r, rows - 1) % P.G) * 128;
-#pragma unroll 1
-            for (int c = 0; c < 128; c += 32) {
+            uint32_t w[64];
+#pragma unroll
+            for (int c = 0; c < 4; ++c) {
                 uint32_t ov[32];
-                tmem_ld_x32(o_col + c, ov);
+                tmem_ld_x32(o_col + 32 * c, ov);
                 tmem_wait_ld();
 #pragma unroll
-                for (int v4 = 0; v4 < 4; ++v4) {
-                    uint32_t w[4];
-#pragma unroll
-                    for (int e = 0; e < 4; ++e)
-                        w[e] = pack_bf16x2(__uint_as_float(ov[8 * v4 + 2 * e]) * inv,
-                                           __uint_as_float(ov[8 * v4 + 2 * e + 1]) * inv);
-                    const uint4 q4 = make_uint4(w[0], w[1], w[2], w[3]);
-                    if (whole)
-                        *(uint4*)(stage + (c >> 6) * HALF + r * 128 + (((((c & 63) >> 3) + v4) ^ (r & 7)) << 4)) = q4;
-                    else if (live)
-                        *(uint4*)(dst + c + 8 * v4) = q4;
-                }
+                for (int u = 0; u < 16; ++u)
+                    w[16 * c + u] =
+                        pack_bf16x2(__uint_as_float(ov[2 * u]) * inv, __uint_as_float(ov[2 * u + 1]) * inv);
             }
-            if (whole) {
-                fence_proxy_async();
-                __syncwarp();
-                if (lane == 0) mbar_arrive(bar(B_STAGE + i));
-                if (warp == 2 + 4 * i && lane == 0 && mbar_wait(bar(B_STAGE + i), 0)) {
-                    for (int h = 0; h < 2; ++h)
-                        tma_store_3d(&tm_o, smem_u32(stage + h * HALF), 64 * h, hk * P.G, t0 + base);
-                    bulk_commit();
-                    bulk_wait_read();
-                }
+            // O is in registers: the next item's first P.V may overwrite it
+            fence_before();
+            __syncwarp();
+            if (lane == 0) mbar_arrive(bar(B_OE + i));
+            if (r < rows && pos < it.len) {
+                uint4* dst = (uint4*)(P.out + ((int64_t)(it.t0 + pos) * P.Hq + it.hk * P.G + head) * 128);
+#pragma unroll
+                for (int c = 0; c < 16; ++c) dst[c] = make_uint4(w[4 * c], w[4 * c + 1], w[4 * c + 2], w[4 * c + 3]);
             }
         }
     }
@@ -486,9 +656,9 @@ extern "C" int fp8kv_prompt_attention(const void* q, int64_t q_stride, const voi
     if (B == 0 || T == 0) return FP8KV_OK;                      // nothing to do; no pointer is read
     if (!q || !k || !v || !cu_seqlens || !out) return FP8KV_ERR_INVALID_ARG;
     if (!al16(q) || !al16(k) || !al16(v) || !al16(out)) return FP8KV_ERR_INVALID_ARG;
-    CUtensorMap tq, tk, tv, to;
+    CUtensorMap tq, tk, tv;
     if (!rows_map(&tq, q, Hq, q_stride, T, G, NP) || !rows_map(&tk, k, Hkv, k_stride, T, 1, prompt::NK) ||
-        !rows_map(&tv, v, Hkv, v_stride, T, 1, prompt::NK) || !rows_map(&to, out, Hq, (int64_t)Hq * 128, T, G, NP))
+        !rows_map(&tv, v, Hkv, v_stride, T, 1, prompt::NK))
         return FP8KV_ERR_CUDA;
     {
         static std::mutex mu;
@@ -517,7 +687,7 @@ extern "C" int fp8kv_prompt_attention(const void* q, int64_t q_stride, const voi
     P.scale_log2 = sm_scale * 1.4426950408889634f;
     const dim3 grid((unsigned)Hkv, (unsigned)pairs);
     const cudaError_t e = launch_pdl(prompt::prompt_attention_kernel, grid, dim3(prompt::THREADS), prompt::SMEM,
-                                     (cudaStream_t)stream, tq, tk, tv, to, P);
+                                     (cudaStream_t)stream, tq, tk, tv, P);
     if (e != cudaSuccess) {
         cudaGetLastError();
         return FP8KV_ERR_CUDA;
