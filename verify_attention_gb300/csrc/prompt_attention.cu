@@ -19,16 +19,16 @@
 // the products of another, and the items are handed out longest first as SMs
 // come free, without a counter in memory.  Twelve warps:
 //   warp 0      loads by TMA: Q of each row tile once it is free, K and V tiles
-//               of 128 keys through a ring of five 32 KiB slots; allocates and
+//               of 128 keys through a ring of four 32 KiB slots; allocates and
 //               frees the tensor memory
 //   warps 1, 2  issue the MMAs of the first and of the second row tile: per key
 //               tile Q.K^T, then P.V.  (One warp for both left the tensor cores
 //               idle 60% of the time: a wait or a commit takes it 40 to 100
 //               cycles, eight MMAs run 512.)
 //   warp 3      schedules: the next item, where its rows lie, into a queue; and
-//               zeroes the V rows of an item's first and last key tile that none
-//               of its rows sees (they may hold another sequence's values):
-//               whatever is there, 0 * V reaches no output
+//               zeroes the V rows of an item's last key tile that none of its
+//               rows sees (they may hold another sequence's values): whatever
+//               is there, 0 * V reaches no output
 //   warps 4-7   softmax and output of the first row tile, one row per thread
 //   warps 8-11  ... of the second         (warp w: TMEM lanes 32 (w % 4) ...)
 // Online softmax in the log2 domain over halves of a key tile, whose P.V starts
@@ -56,11 +56,11 @@ namespace prompt {
 constexpr int NK = 128;                         // keys per tile
 constexpr int SLOT = NK * 256;                  // 32 KiB: two blocks of 128 rows x 64 dims (128-byte swizzled)
 constexpr int HALF = SLOT / 2;
-constexpr int SLOTS = 5;
+constexpr int SLOTS = 4;
 constexpr int WARPS = 12, THREADS = WARPS * 32;
 constexpr int QUEUE = 4;                        // items in the queue
 constexpr uint32_t TM_S = 0, TM_O = 256, TM_COLS = 512;
-constexpr int SMEM = 2 * SLOT + SLOTS * SLOT + 1024 + 512;
+constexpr int SMEM = 2 * SLOT + SLOTS * SLOT + SLOT + 1024 + 512;    // Q, ring, output tile
 
 enum {
     B_Q = 0,                                    // per row tile: Q loaded
@@ -72,8 +72,11 @@ enum {
     B_H = B_P + 4,                              // per row tile: P.V of the first half complete
     B_O = B_H + 2,                              // per row tile: O final
     B_OE = B_O + 2,                             // ... and read
-    B_RAW = B_OE + 2,                           // first / last V tile loaded, to be cleaned
-    B_ITEM = B_RAW + 2,                         // per queue entry: written
+    B_STAGED = B_OE + 2,                        // per row tile: output tile written
+    B_SENT = B_STAGED + 2,                      // ... and read by its store
+    B_TURN = B_SENT + 2,                        // per row tile: its MMA warp's turn
+    B_RAW = B_TURN + 2,                         // last V tile loaded, to be cleaned
+    B_ITEM = B_RAW + 1,                         // per queue entry: written
     B_TAKEN = B_ITEM + QUEUE,                   // ... read by every role
     B_NEXT = B_TAKEN + QUEUE,                   // answer of a cancel request
     B_IDLE = B_NEXT + 1,                        // per MMA warp: nothing outstanding
@@ -90,6 +93,7 @@ struct Params {
 
 // bf16 operands: format code 1 for A and B.
 constexpr uint32_t ID_QK = idesc(128, NK, false) | (1u << 7) | (1u << 10);
+constexpr uint32_t ID_QK_HALF = idesc(128, NK / 2, false) | (1u << 7) | (1u << 10);
 constexpr uint32_t ID_PV = idesc(128, 128, true) | (1u << 7) | (1u << 10);
 
 // One thread of the (converged) warp, the same one every time.
@@ -119,6 +123,12 @@ __device__ __forceinline__ void mma_ts(uint32_t d, uint32_t a, uint32_t b, uint3
         "tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], y, %3, p; }" ::"r"(d),
         "r"(a), "r"(b), "r"(id), "r"(acc), "n"(DESC_HI)
         : "memory");
+}
+
+__device__ __forceinline__ void tma_store_3d(const CUtensorMap* tm, uint32_t src, int x, int y, int z) {
+    asm volatile("cp.async.bulk.tensor.3d.global.shared::cta.tile.bulk_group [%0, {%2, %3, %4}], [%1];" ::"l"(tm),
+                 "r"(src), "r"(x), "r"(y), "r"(z)
+                 : "memory");
 }
 
 __device__ __forceinline__ uint64_t pack2(float lo, float hi) {
@@ -169,41 +179,46 @@ __device__ __forceinline__ bool cancel_answer(uint32_t resp, int& x, int& y) {
 }
 
 // An item: rows p0 .. of the sequence of `len` tokens from token t0 on, KV head
-// hk; len = 0 ends the queue.
+// hk; len = 0 ends the queue.  Key tiles are counted from the first key that
+// any of its rows sees (see_lo).
 struct Item {
     int t0, len, p0, hk;
-    int tiles, j0, n;           // row tiles (1 or 2), first key tile, key tiles
-    int lo1, hi0;               // key tiles [0, hi0) of row tile 0, [lo1, n) of row tile 1
+    int tiles, n;               // row tiles (1 or 2), key tiles
     int see_lo, see_hi;         // keys that any row sees
+    int lo1, hi0;               // first key of row tile 1, last key of row tile 0
     __device__ __forceinline__ Item(int4 e, const Params& P) : t0(e.x), len(e.y), p0(e.z), hk(e.w) {
         const int wl = P.window_left, last = len - 1;
         tiles = p0 + P.NP < len ? 2 : 1;
         see_lo = wl >= 0 ? max(0, p0 - wl) : 0;
         see_hi = min(last, p0 + tiles * P.NP - 1);
-        j0 = see_lo / NK;
-        n = see_hi / NK + 1 - j0;
-        hi0 = min(last, p0 + P.NP - 1) / NK + 1 - j0;
-        lo1 = wl >= 0 ? max(0, p0 + P.NP - wl) / NK - j0 : 0;
+        n = (see_hi - see_lo) / NK + 1;
+        hi0 = min(last, p0 + P.NP - 1);
+        lo1 = wl >= 0 ? max(0, p0 + P.NP - wl) : 0;
     }
-    __device__ __forceinline__ bool has(int i, int j) const { return i ? tiles == 2 && j >= lo1 : j < hi0; }
-    __device__ __forceinline__ int first(int i) const { return i ? lo1 : 0; }
-    __device__ __forceinline__ int last(int i) const { return (i ? n : hi0) - 1; }
-    // V tiles with rows that none of the item's rows sees: such a tile lands on
+    __device__ __forceinline__ int key_lo(int i) const { return i ? lo1 : see_lo; }
+    __device__ __forceinline__ int key_hi(int i) const { return i ? see_hi : hi0; }
+    __device__ __forceinline__ int first(int i) const { return (key_lo(i) - see_lo) / NK; }
+    __device__ __forceinline__ int last(int i) const { return (key_hi(i) - see_lo) / NK; }
+    // every used row of row tile i is one of the sequence
+    __device__ __forceinline__ bool whole(int i, int NP) const { return p0 + (i + 1) * NP <= len; }
+    // keys k .. k + 63: does any row of row tile i see one of them?
+    __device__ __forceinline__ bool live(int i, int k) const { return k <= key_hi(i) && k + NK / 2 > key_lo(i); }
+    // the last V tile has rows that none of the item's rows sees: it lands on
     // a barrier of its own, for warp 3, which clears those rows and then
     // arrives on the slot's barrier
-    __device__ __forceinline__ bool cleaned(int j) const {
-        return (j == n - 1 && (j0 + n) * NK - 1 > see_hi) || (j == 0 && j0 * NK < see_lo);
-    }
+    __device__ __forceinline__ bool cleaned() const { return n * NK > see_hi - see_lo + 1; }
 };
 
 __global__ void __launch_bounds__(THREADS, 1)
     prompt_attention_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__ CUtensorMap tm_k,
-                            const __grid_constant__ CUtensorMap tm_v, const Params P) {
+                            const __grid_constant__ CUtensorMap tm_v, const __grid_constant__ CUtensorMap tm_o,
+                            const Params P) {
     extern __shared__ uint8_t smem_raw[];
     uint8_t* smem = (uint8_t*)(((uintptr_t)smem_raw + 1023) & ~(uintptr_t)1023);
     uint8_t* qs = smem;                                     // two row tiles of 32 KiB
     uint8_t* ring = smem + 2 * SLOT;
-    int4* queue = (int4*)(ring + SLOTS * SLOT);
+    uint8_t* stage = ring + SLOTS * SLOT;                   // an output tile of 32 KiB
+    int4* queue = (int4*)(stage + SLOT);
     int4* answer = queue + QUEUE;
     uint64_t* bars = (uint64_t*)(answer + 1);
     uint32_t* tmem_slot = (uint32_t*)(bars + B_COUNT);
@@ -216,7 +231,7 @@ __global__ void __launch_bounds__(THREADS, 1)
     if (threadIdx.x == 0) {
         for (int i = 0; i < B_COUNT; ++i) {
             int count = 1;
-            if ((i >= B_P && i < B_P + 4) || (i >= B_OE && i < B_OE + 2)) count = 4;    // softmax warps
+            if ((i >= B_P && i < B_P + 4) || (i >= B_OE && i < B_STAGED + 2)) count = 4;    // softmax warps
             if (i >= B_EMPTY && i < B_EMPTY + SLOTS) count = 2;                         // MMA warps
             if (i >= B_TAKEN && i < B_TAKEN + QUEUE) count = ROLES;
             mbar_init(bar(i), count);
@@ -232,6 +247,7 @@ __global__ void __launch_bounds__(THREADS, 1)
             prefetch_tensormap(&tm_q);
             prefetch_tensormap(&tm_k);
             prefetch_tensormap(&tm_v);
+            prefetch_tensormap(&tm_o);
         }
     }
     // rows behind G * NP take part in the MMAs: zeros there keep them finite
@@ -266,7 +282,7 @@ __global__ void __launch_bounds__(THREADS, 1)
         asm volatile("createpolicy.fractional.L2::evict_normal.b64 %0, 1.0;" : "=l"(keep));
         const uint64_t once = policy_evict_first();
         int4 e;
-        int done = 0, q_use[2] = {0, 0}, raw_use[2] = {0, 0};
+        int done = 0, q_use[2] = {0, 0}, raw_use = 0;
         while (next_item(e)) {
             const Item it(e, P);
             if (lane == 0) {
@@ -285,15 +301,14 @@ __global__ void __launch_bounds__(THREADS, 1)
                     if (use > 0) ok = mbar_wait(bar(B_EMPTY + s), (use - 1) & 1);
                     if (!ok) break;
                     uint32_t full = bar(B_FULL + s);
-                    if ((u & 1) && it.cleaned(j)) {
-                        full = bar(B_RAW + (j == it.n - 1));
-                        if (j == it.n - 1) ++raw_use[1];
-                        else ++raw_use[0];
+                    if (u == 2 * it.n - 1 && it.cleaned()) {
+                        full = bar(B_RAW);
+                        ++raw_use;
                     }
                     mbar_expect_tx(full, SLOT);
                     for (int h = 0; h < 2; ++h)
                         tma_load_3d(smem_u32(ring + s * SLOT + h * HALF), u & 1 ? &tm_v : &tm_k, 64 * h, it.hk,
-                                    it.t0 + (it.j0 + j) * NK, full, keep);
+                                    it.t0 + it.see_lo + j * NK, full, keep);
                     ++done;
                     if (u == 0 && it.tiles == 2) load_q(1);
                 }
@@ -306,8 +321,8 @@ __global__ void __launch_bounds__(THREADS, 1)
 #pragma unroll
             for (int i = 0; i < 2; ++i) {
                 if (q_use[i]) mbar_wait(bar(B_Q + i), (q_use[i] - 1) & 1);
-                if (raw_use[i]) mbar_wait(bar(B_RAW + i), (raw_use[i] - 1) & 1);
             }
+            if (raw_use) mbar_wait(bar(B_RAW), (raw_use - 1) & 1);
             for (int u = max(0, done - SLOTS); u < done; ++u) mbar_wait(bar(B_FULL + u % SLOTS), (u / SLOTS) & 1);
         }
         __syncwarp();
@@ -325,79 +340,100 @@ __global__ void __launch_bounds__(THREADS, 1)
                 phase ^= 1;
             }
         };
-        int tile = 0, items = 0;                            // key tiles and items of this row tile so far
+        int tile = 0, items = 0, turns = 0;                            // key tiles and items of this row tile so far
         int4 e;
         while (next_item(e)) {
             const Item it(e, P);
             const bool mine = i < it.tiles;
             const int jf = mine ? it.first(i) : 0, jl = mine ? it.last(i) : -1;
             if (mine) {
-                ok = mbar_wait(bar(B_Q + i), items & 1);
+                ok = __all_sync(0xffffffffu, mbar_wait(bar(B_Q + i), items & 1));
                 ++items;
             }
             int v_slot = 0, v_phase = 0;
+            bool v_live[2] = {false, false};                // halves of the key tile before that some row sees
             for (int j = 0; j <= it.n && ok; ++j) {
-                if (j > 0) {
+                const bool pv = j - 1 >= jf && j - 1 <= jl, qk = j >= jf && j <= jl && j < it.n;
+                // The two warps issue in turn, P.V and Q.K^T of one row tile
+                // behind those of the other: left alone they fall into step,
+                // both tiles' softmax at once and the tensor cores idle
+                // meanwhile (8192 tokens: 905 us).  What a step needs is waited
+                // for before its turn (881 us where it was not).
+                if (j > 0) ok = mbar_wait(bar(B_FULL + v_slot), v_phase);
+                if (ok && j < it.n) ok = mbar_wait(bar(B_FULL + slot), phase);
+                // O of the previous item has been read
+                if (ok && pv && j - 1 == jf && items > 1) ok = mbar_wait(bar(B_OE + i), items & 1);
+                if (ok && pv) ok = mbar_wait(bar(B_P + 2 * i), tile & 1);
+                ok = __all_sync(0xffffffffu, ok);
+                if (!ok) break;
+                if (i == 1 || turns > 0) ok = __all_sync(0xffffffffu, mbar_wait(bar(B_TURN + i), (i == 1 ? turns : turns - 1) & 1));
+                if (!ok) break;
+                ++turns;
+                fence_after();
+                if (pv) {
                     // O += P(j - 1) V(j - 1)
-                    const bool on = j - 1 >= jf && j - 1 <= jl;
-                    ok = mbar_wait(bar(B_FULL + v_slot), v_phase);
-                    if (!ok) break;
-                    if (on) {
-                        // O of the previous item has been read
-                        if (j - 1 == jf && items > 1) ok = mbar_wait(bar(B_OE + i), items & 1);
-                        const uint32_t v_lo = v_lo0 + v_slot * (SLOT >> 4);
-#pragma unroll
-                        for (int h = 0; h < 2; ++h) {
-                            if (ok) ok = mbar_wait(bar(B_P + 2 * i + h), tile & 1);
-                            if (!ok) break;
-                            fence_after();
-                            if (leader) {
-#pragma unroll
-                                for (int kk = 4 * h; kk < 4 * h + 4; ++kk)
-                                    mma_ts(o_col, s_col + 8 * kk, v_lo + kk * (2048 >> 4), ID_PV, j - 1 > jf || kk > 0);
-                                if (h == 0) mma_commit(bar(B_H + i));
-                            }
-                            __syncwarp();
-                        }
-                        if (!ok) break;
-                        ++tile;
-                    }
+                    const uint32_t v_lo = v_lo0 + v_slot * (SLOT >> 4);
                     if (leader) {
-                        if (on) mma_commit(bar(B_EMPTY + v_slot));
-                        else mbar_arrive(bar(B_EMPTY + v_slot));
+                        if (v_live[0]) {
+#pragma unroll
+                            for (int kk = 0; kk < 4; ++kk)
+                                mma_ts(o_col, s_col + 8 * kk, v_lo + kk * (2048 >> 4), ID_PV, j - 1 > jf || kk > 0);
+                        }
+                        mma_commit(bar(B_H + i));
+                    }
+                    __syncwarp();
+                    ok = __all_sync(0xffffffffu, mbar_wait(bar(B_P + 2 * i + 1), tile & 1));
+                    fence_after();
+                    if (leader && ok) {
+                        if (v_live[1]) {
+#pragma unroll
+                            for (int kk = 4; kk < 8; ++kk)
+                                mma_ts(o_col, s_col + 8 * kk, v_lo + kk * (2048 >> 4), ID_PV,
+                                       j - 1 > jf || kk > 4 || v_live[0]);
+                        }
+                        mma_commit(bar(B_EMPTY + v_slot));
                         if (j - 1 == jl) mma_commit(bar(B_O + i));
                     }
                     __syncwarp();
+                    ++tile;
+                } else if (j > 0 && leader) {
+                    mbar_arrive(bar(B_EMPTY + v_slot));
                 }
-                if (j < it.n) {
+                if (qk) {
                     // S = Q K(j)^T, over P(j - 1), which the MMAs above have read
-                    const bool on = j >= jf && j <= jl;
-                    ok = mbar_wait(bar(B_FULL + slot), phase);
-                    if (!ok) break;
-                    fence_after();
-                    if (leader) {
-                        if (on) {
-                            const uint32_t k_lo = k_lo0 + slot * (SLOT >> 4);
+                    const int k0 = it.see_lo + j * NK;
+                    v_live[0] = it.live(i, k0);
+                    v_live[1] = it.live(i, k0 + NK / 2);
+                    if (leader && ok) {
+                        // both halves, or the one that some row sees
+                        const bool both = v_live[0] && v_live[1];
+                        const int h = v_live[0] ? 0 : 1;
+                        const uint32_t k_lo = k_lo0 + slot * (SLOT >> 4) + h * (64 * 128 >> 4);
 #pragma unroll
-                            for (int kk = 0; kk < 8; ++kk) {
-                                const uint32_t off = ((kk >> 2) * HALF + (kk & 3) * 32) >> 4;
-                                mma_ss(s_col, q_lo + off, k_lo + off, ID_QK, kk > 0);
-                            }
-                            mma_commit(bar(B_S + i));
-                            mma_commit(bar(B_EMPTY + slot));
-                            if (j == jl) mma_commit(bar(B_QE + i));
-                        } else {
-                            mbar_arrive(bar(B_EMPTY + slot));
+                        for (int kk = 0; kk < 8; ++kk) {
+                            const uint32_t off = ((kk >> 2) * HALF + (kk & 3) * 32) >> 4;
+                            mma_ss(s_col + 64 * h, q_lo + off, k_lo + off, both ? ID_QK : ID_QK_HALF, kk > 0);
                         }
+                        mma_commit(bar(B_S + i));
                     }
-                    __syncwarp();
+                }
+                if (leader) {
+                    mbar_arrive(bar(B_TURN + 1 - i));
+                    if (qk) {
+                        mma_commit(bar(B_EMPTY + slot));
+                        if (j == jl) mma_commit(bar(B_QE + i));
+                    } else if (j < it.n) {
+                        mbar_arrive(bar(B_EMPTY + slot));
+                    }
+                }
+                __syncwarp();
+                if (j < it.n) {
                     advance();
                     v_slot = slot;
                     v_phase = phase;
                     advance();
                 }
             }
-            ok = __all_sync(0xffffffffu, ok);
             if (!ok) break;
         }
         // nothing the tensor cores still run may outlive the TMEM allocation
@@ -423,33 +459,46 @@ __global__ void __launch_bounds__(THREADS, 1)
             __syncwarp();
             ++put;
         };
-        int base = 0, raw_use[2] = {0, 0};
+        int base = 0, raw_use = 0;
         auto clean = [&](int4 e) {
             const Item it(e, P);
-#pragma unroll
-            for (int f = 0; f < 2; ++f) {
-                const int j = f ? it.n - 1 : 0;
-                if (!ok || !it.cleaned(j) || (f == 0 && j == it.n - 1)) continue;
-                ok = __all_sync(0xffffffffu, mbar_wait(bar(B_RAW + f), raw_use[f] & 1));
-                if (!ok) continue;
-                ++raw_use[f];
-                const int s = (base + 2 * j + 1) % SLOTS, k0 = (it.j0 + j) * NK;
-                uint8_t* vt = ring + s * SLOT;
-                const int a = max(0, min(NK, it.see_lo - k0)), z = max(0, min(NK, it.see_hi + 1 - k0));
-                for (int i = lane; i < NK * 8; i += 32) {   // rows [0, a) and [z, 128)
-                    const int r = i >> 3;
-                    if (r >= a && r < z) continue;
-                    *(uint4*)(vt + i * 16) = make_uint4(0, 0, 0, 0);
-                    *(uint4*)(vt + HALF + i * 16) = make_uint4(0, 0, 0, 0);
-                }
-                fence_proxy_async();
-                __syncwarp();
-                if (lane == 0) mbar_arrive(bar(B_FULL + s));
-            }
             base += 2 * it.n;
+            if (!it.cleaned()) return;
+            ok = __all_sync(0xffffffffu, mbar_wait(bar(B_RAW), raw_use & 1));
+            if (!ok) return;
+            ++raw_use;
+            const int s = (base - 1) % SLOTS, z = it.see_hi - it.see_lo - (it.n - 1) * NK + 1;
+            uint8_t* vt = ring + s * SLOT;
+            for (int i = z * 8 + lane; i < NK * 8; i += 32) {   // rows [z, 128)
+                *(uint4*)(vt + i * 16) = make_uint4(0, 0, 0, 0);
+                *(uint4*)(vt + HALF + i * 16) = make_uint4(0, 0, 0, 0);
+            }
+            fence_proxy_async();
+            __syncwarp();
+            if (lane == 0) mbar_arrive(bar(B_FULL + s));
         };
-        // every item is put into the queue before the V tiles of the one
-        // before it are cleaned: the loads run ahead
+        // the output tiles of an item, in the order in which they are staged
+        int sends[2] = {0, 0};
+        auto send = [&](int4 e) {
+            const Item it(e, P);
+#pragma unroll
+            for (int i = 0; i < 2; ++i) {
+                if (!ok || !it.whole(i, P.NP)) continue;
+                ok = __all_sync(0xffffffffu, mbar_wait(bar(B_STAGED + i), sends[i] & 1));
+                ++sends[i];
+                if (lane == 0 && ok) {
+                    for (int h = 0; h < 2; ++h)
+                        tma_store_3d(&tm_o, smem_u32(stage + h * HALF), 64 * h, it.hk * P.G,
+                                     it.t0 + it.p0 + i * P.NP);
+                    bulk_commit();
+                    bulk_wait_read();
+                    mbar_arrive(bar(B_SENT + i));
+                }
+                __syncwarp();
+            }
+        };
+        // every item is put into the queue before the one before it is cleaned
+        // and sent: the loads run ahead
         int4 before = make_int4(0, 0, 0, 0);
         bool more = true;
         for (int k = 0; more && ok; ++k) {
@@ -478,6 +527,7 @@ __global__ void __launch_bounds__(THREADS, 1)
                 const int4 e = make_int4(s0, s1 - s0, p0, hk);
                 put_item(e);
                 if (ok && before.y) clean(before);
+                if (ok && before.y) send(before);
                 before = e;
             }
             const bool got = mbar_wait(bar(B_NEXT), k & 1);
@@ -486,6 +536,7 @@ __global__ void __launch_bounds__(THREADS, 1)
         }
         if (ok) put_item(make_int4(0, 0, 0, 0));
         if (ok && before.y) clean(before);
+        if (ok && before.y) send(before);
     } else {
         // ----------------------------------------------- softmax and output
         const int i = (warp - 4) >> 2, wq = warp & 3;
@@ -497,36 +548,59 @@ __global__ void __launch_bounds__(THREADS, 1)
         const int dpos = min(r, rows - 1) / P.G, head = min(r, rows - 1) % P.G;
         const int dfirst = min(wq * 32, rows - 1) / P.G, dlast = min(wq * 32 + 31, rows - 1) / P.G;
         int s_use = 0, o_use = 0;
+        int sends[2] = {0, 0};                              // staged tiles so far, this item's among them
+        bool last_was_1 = false, before_was_1;              // the last one (before this item) was of row tile 1
         int4 e;
         while (next_item(e)) {
             const Item it(e, P);
+            before_was_1 = last_was_1;
+            if (it.whole(0, P.NP)) {
+                ++sends[0];
+                last_was_1 = it.whole(1, P.NP);
+                if (last_was_1) ++sends[1];
+            }
             if (i >= it.tiles) continue;
             const int tile0 = it.p0 + i * P.NP, pos = tile0 + dpos;
             const int lo_r = P.window_left >= 0 ? max(0, pos - P.window_left) : 0;
-            // key tiles inside these bounds need no mask
-            const int pmin = tile0 + dfirst;
+            // halves of key tiles inside these bounds need no mask
+            const int pmin = tile0 + dfirst, pmax = min(tile0 + dlast, it.key_hi(i));
+            const int lomin = P.window_left >= 0 ? max(0, tile0 + dfirst - P.window_left) : 0;
             const int lomax = P.window_left >= 0 ? max(0, tile0 + dlast - P.window_left) : 0;
             float m_run = -INFINITY, l_run = 0.f;
             const int j_end = it.last(i);
 #pragma unroll 1
             for (int j = it.first(i); j <= j_end; ++j) {
-                const int k0 = (it.j0 + j) * NK;
                 ok = mbar_wait(bar(B_S + i), s_use & 1);
                 // (the first half's product of the tile before: complete long
                 // since; waited for so that no phase of the barrier is missed)
                 if (ok && s_use > 0) ok = mbar_wait(bar(B_H + i), (s_use - 1) & 1);
                 if (!__all_sync(0xffffffffu, ok)) { ok = false; break; }
                 fence_after();
-                const bool need_mask = k0 + NK - 1 > pmin || k0 < lomax;
                 const uint64_t mult2 = pack2(mult, mult);
 #pragma unroll
                 for (int h = 0; h < 2; ++h) {
+                    const int k0 = it.see_lo + j * NK + 64 * h;
+                    if (k0 > pmax || k0 + 63 < lomin) {
+                        // no row of the warp sees a key of this half: P = 0
+                        // (and no MMA reads it when no row of the tile does)
+                        if (it.live(i, k0)) {
+                            uint32_t zero[32];
+#pragma unroll
+                            for (int u = 0; u < 32; ++u) zero[u] = 0;
+                            tmem_st_x32(s_col + 32 * h, zero);
+                            tmem_wait_st();
+                            fence_before();
+                        }
+                        __syncwarp();
+                        if (lane == 0) mbar_arrive(bar(B_P + 2 * i + h));
+                        continue;
+                    }
                     uint32_t sv[64];
                     tmem_ld_x64(s_col + 64 * h, sv);
                     tmem_wait_ld();
-                    if (need_mask) {
+                    if (k0 + 63 > pmin || k0 < lomax) {
                         // this row's visible columns of the half as bits
-                        const int c0 = max(0, lo_r - k0 - 64 * h), c1 = min(64, pos - k0 - 64 * h + 1);
+                        const int c0 = max(0, lo_r - k0), c1 = min(64, pos - k0 + 1);
                         const uint64_t below1 = c1 <= 0 ? 0ull : (c1 >= 64 ? ~0ull : (1ull << c1) - 1);
                         const uint64_t below0 = c0 >= 64 ? ~0ull : (1ull << c0) - 1;
                         const uint64_t see = below1 & ~below0;
@@ -535,13 +609,16 @@ __global__ void __launch_bounds__(THREADS, 1)
                         for (int u = 0; u < 64; ++u)
                             sv[u] = ((u < 32 ? see0 : see1) >> (u & 31)) & 1u ? sv[u] : 0xff800000u;   // -inf
                     }
-                    float m2[2] = {__uint_as_float(sv[0]), __uint_as_float(sv[1])};
+                    float m4[4];
 #pragma unroll
-                    for (int u = 2; u < 62; u += 4) {
-                        m2[0] = max3(m2[0], __uint_as_float(sv[u]), __uint_as_float(sv[u + 1]));
-                        m2[1] = max3(m2[1], __uint_as_float(sv[u + 2]), __uint_as_float(sv[u + 3]));
+                    for (int c = 0; c < 4; ++c) {
+                        m4[c] = max3(__uint_as_float(sv[c]), __uint_as_float(sv[c + 4]), __uint_as_float(sv[c + 8]));
+#pragma unroll
+                        for (int u = c + 12; u < 60; u += 8)
+                            m4[c] = max3(m4[c], __uint_as_float(sv[u]), __uint_as_float(sv[u + 4]));
+                        m4[c] = fmaxf(m4[c], __uint_as_float(sv[60 + c]));
                     }
-                    const float tmax = max3(m2[0], m2[1], fmaxf(__uint_as_float(sv[62]), __uint_as_float(sv[63]))) * mult;
+                    const float tmax = max3(m4[0], m4[1], fmaxf(m4[2], m4[3])) * mult;
                     const bool grow = m_run != -INFINITY && tmax > m_run + 8.0f;
                     if (__any_sync(0xffffffffu, grow)) {
                         // S(j) ready means that P.V of the tiles before is
@@ -603,24 +680,47 @@ __global__ void __launch_bounds__(THREADS, 1)
             const float inv = 1.0f / l_run;
             uint32_t w[64];
 #pragma unroll
-            for (int c = 0; c < 4; ++c) {
-                uint32_t ov[32];
-                tmem_ld_x32(o_col + 32 * c, ov);
+            for (int c = 0; c < 2; ++c) {
+                uint32_t ov[64];
+                tmem_ld_x64(o_col + 64 * c, ov);
                 tmem_wait_ld();
 #pragma unroll
-                for (int u = 0; u < 16; ++u)
-                    w[16 * c + u] =
+                for (int u = 0; u < 32; ++u)
+                    w[32 * c + u] =
                         pack_bf16x2(__uint_as_float(ov[2 * u]) * inv, __uint_as_float(ov[2 * u + 1]) * inv);
             }
             // O is in registers: the next item's first P.V may overwrite it
             fence_before();
             __syncwarp();
             if (lane == 0) mbar_arrive(bar(B_OE + i));
-            if (r < rows && pos < it.len) {
+            // A whole tile goes out as one tensor copy from shared memory (warp
+            // 3), so that the next item's first key tiles do not wait behind
+            // stores (3100 of an item's 17000 cycles, 16384 tokens, 512-key
+            // window).  The two row tiles share the staging tile, in order:
+            // each waits until the copy before its own has read it.  A
+            // sequence's last tile, with rows behind its end, is stored row by
+            // row.
+            if (it.whole(i, P.NP)) {
+                if (i == 1)
+                    ok = mbar_wait(bar(B_SENT), (sends[0] - 1) & 1);
+                else if (sends[0] > 1)
+                    ok = before_was_1 ? mbar_wait(bar(B_SENT + 1), (sends[1] - (it.whole(1, P.NP) ? 2 : 1)) & 1)
+                                      : mbar_wait(bar(B_SENT), sends[0] & 1);
+                ok = __all_sync(0xffffffffu, ok);
+                if (!ok) break;
+#pragma unroll
+                for (int c = 0; c < 16; ++c)
+                    *(uint4*)(stage + (c >> 3) * HALF + r * 128 + (((c ^ r) & 7) << 4)) =
+                        make_uint4(w[4 * c], w[4 * c + 1], w[4 * c + 2], w[4 * c + 3]);
+                fence_proxy_async();
+                __syncwarp();
+                if (lane == 0) mbar_arrive(bar(B_STAGED + i));
+            } else if (r < rows && pos < it.len) {
                 uint4* dst = (uint4*)(P.out + ((int64_t)(it.t0 + pos) * P.Hq + it.hk * P.G + head) * 128);
 #pragma unroll
                 for (int c = 0; c < 16; ++c) dst[c] = make_uint4(w[4 * c], w[4 * c + 1], w[4 * c + 2], w[4 * c + 3]);
             }
+            __syncwarp();
         }
     }
 
@@ -656,9 +756,9 @@ extern "C" int fp8kv_prompt_attention(const void* q, int64_t q_stride, const voi
     if (B == 0 || T == 0) return FP8KV_OK;                      // nothing to do; no pointer is read
     if (!q || !k || !v || !cu_seqlens || !out) return FP8KV_ERR_INVALID_ARG;
     if (!al16(q) || !al16(k) || !al16(v) || !al16(out)) return FP8KV_ERR_INVALID_ARG;
-    CUtensorMap tq, tk, tv;
+    CUtensorMap tq, tk, tv, to;
     if (!rows_map(&tq, q, Hq, q_stride, T, G, NP) || !rows_map(&tk, k, Hkv, k_stride, T, 1, prompt::NK) ||
-        !rows_map(&tv, v, Hkv, v_stride, T, 1, prompt::NK))
+        !rows_map(&tv, v, Hkv, v_stride, T, 1, prompt::NK) || !rows_map(&to, out, Hq, (int64_t)Hq * 128, T, G, NP))
         return FP8KV_ERR_CUDA;
     {
         static std::mutex mu;
@@ -687,7 +787,7 @@ extern "C" int fp8kv_prompt_attention(const void* q, int64_t q_stride, const voi
     P.scale_log2 = sm_scale * 1.4426950408889634f;
     const dim3 grid((unsigned)Hkv, (unsigned)pairs);
     const cudaError_t e = launch_pdl(prompt::prompt_attention_kernel, grid, dim3(prompt::THREADS), prompt::SMEM,
-                                     (cudaStream_t)stream, tq, tk, tv, P);
+                                     (cudaStream_t)stream, tq, tk, tv, to, P);
     if (e != cudaSuccess) {
         cudaGetLastError();
         return FP8KV_ERR_CUDA;
