@@ -223,16 +223,20 @@ def _check(out, lay, q, kc, vc, ks, vs, ps, window=-1, rows=None):
                                                    lay.block_table.numpy(), lay.seq_lens.numpy(), ks.item(), vs.item(),
                                                    SM, window)
     # bf16 output: half a step, 2^-8 of the value.  Softmax weights: f16 of 2^15
-    # times the weight against the running maximum, off by 2^-11 of itself (with
-    # exponentials, sums and the f32 product with the scale below 2^-14 more:
-    # under 2^-10 of mag) or, below f16's normal range, by 2^-25, that is 2^-40
-    # of the row's sum (at least 2^15): 2^-40 vsum.  Logits: a sum of 128
-    # products is eight accumulating steps of 16, each off by at most an ulp
-    # (2^-23) of the partial sum, whose size is at most a: 8 * 2^-23 a, which
-    # moves the output by at most 2^-20 lmag.  (That term matters only where
-    # |q| |k| is in the hundreds: with a = 560, 2 * 560 * 2^-20 is already 2^-10.)
+    # times the weight against the running maximum (more than 16 rows: 2^11
+    # times), off by 2^-11 of itself (with exponentials, sums and the f32 product
+    # with the scale below 2^-14 more: under 2^-10 of mag) or, below f16's normal
+    # range, by 2^-25, that is 2^-40 (2^-36) of the row's sum, which is at least
+    # 2^15 (2^11): times vsum.  Logits: a sum of 128 products is eight
+    # accumulating steps of 16, each off by at most an ulp (2^-23) of the partial
+    # sum, whose size is at most a: 8 * 2^-23 a, which moves the output by at
+    # most 2^-20 lmag.  (That term matters only where |q| |k| is in the hundreds:
+    # with a = 560, 2 * 560 * 2^-20 is already 2^-10.)  Partials of more than 16
+    # rows: f16, 2^-11 of each, so at most 2^-11 of mag.
     err = np.abs(out.double().cpu().numpy() - ref)
-    tol = 2.0 ** -8 * np.abs(ref) + 2.0 ** -10 * mag + 2.0 ** -20 * lmag + 2.0 ** -40 * vsum
+    many = q.shape[1] * q.shape[2] // kc.shape[1] > 16
+    tol = (2.0 ** -8 * np.abs(ref) + (2.0 ** -10 + many * 2.0 ** -11) * mag + 2.0 ** -20 * lmag +
+           2.0 ** (-36 if many else -40) * vsum)
     assert np.all(err <= tol), (float((err / tol).max()), float(err.max()))
 
 

@@ -66,7 +66,8 @@ extern "C" int fp8kv_device_status(unsigned int* status, int clear) {
     unsigned int s = 0;
     if (fp8kv::status_insert(&s, clear) || fp8kv::status_attention(&s, clear) ||
         fp8kv::status_attention_tc(&s, clear) || fp8kv::status_attention_layers(&s, clear) ||
-        fp8kv::status_attention_int4(&s, clear) || fp8kv::status_prompt(&s, clear))
+        fp8kv::status_attention_int4(&s, clear) || fp8kv::status_attention_int4_tc(&s, clear) ||
+        fp8kv::status_prompt(&s, clear))
         return FP8KV_ERR_CUDA;
     *status = s;
     return FP8KV_OK;

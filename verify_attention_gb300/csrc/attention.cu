@@ -1148,13 +1148,32 @@ static int attention_call(const void* k_new, const void* v_new, const void* q, c
                                     v_scale, (void*)k_cache, (void*)v_cache, num_pages, page_size, max_seq_len, s);
             if (rc) return rc;
         }
+        // more than 16 rows per KV head and partitions of whole 128-key tiles:
+        // the tcgen05 kernel, whose cost does not depend on the rows up to 128
+        // (64 sequences, 108 rows: INT4_TC_US us; the mma.sync kernel, which
+        // widens every key again for each 16 rows, 3097 us; one tile of 16
+        // rows: ROWS16)
+        const bool tc = tc_rows(M, Hq, Hkv) && plan.split_tokens % tc_tile_tokens() == 0;
+        const bool lpt = tc && B > 1 && row_tiles(M, Hq, Hkv) == 1 && plan.num_splits > 1;
+        if (lpt) {
+            // in the second half of the partials' area, which f16 leaves free
+            P.lpt_order = (const int32_t*)((const uint8_t*)workspace + rows * plan.num_splits * 128 * sizeof(uint16_t));
+            const cudaError_t e = launch_pdl(lpt_order_kernel, dim3(1), dim3(512), 0, s, seq_lens, B, M, P.R, P.G,
+                                             max_pages_per_seq, page_size, window_left, plan.split_pages,
+                                             plan.num_splits, max_seq_len, (int32_t*)P.lpt_order);
+            if (e != cudaSuccess) {
+                cudaGetLastError();
+                return FP8KV_ERR_CUDA;
+            }
+        }
         char text[256];
-        rc = launch_attention_int4(P, s, text, sizeof text);
+        rc = tc ? launch_attention_int4_tc(P, s, text, sizeof text) : launch_attention_int4(P, s, text, sizeof text);
         if (rc) return rc;
         if (plan.num_splits > 1) {
             const int64_t warps = (int64_t)B * M * Hq;
-            cudaError_t e = launch_pdl(attn_reduce_kernel<false>, dim3((unsigned)((warps + 7) / 8)), dim3(256), 0, s,
-                                       (const float*)P.ws_o, (const float*)P.ws_ml, seq_lens, B, M, Hq, P.G, P.R,
+            cudaError_t e = launch_pdl(tc ? attn_reduce_kernel<true> : attn_reduce_kernel<false>,
+                                       dim3((unsigned)((warps + 7) / 8)), dim3(256), 0, s, (const float*)P.ws_o,
+                                       (const float*)P.ws_ml, seq_lens, B, M, Hq, P.G, tc ? 128 : P.R,
                                        max_pages_per_seq, page_size, window_left, plan.split_pages, plan.num_splits,
                                        max_seq_len, v_scale, scale_stride, (uint16_t*)out);
             if (e != cudaSuccess) {

@@ -92,10 +92,14 @@ int launch_append_int4(const void* k, const void* v, const int32_t* seq_lens, co
                        int B, int M, int Hkv, const float* k_scale, const float* v_scale, void* k_cache,
                        void* v_cache, int num_pages, int page_size, int max_seq_len, cudaStream_t s);
 
-// Host launcher of the INT4 cache kernel (attention_int4.cu): partials as the
-// mma.sync kernels write them (fp32 O * v_scale, (max, sum)), partitions cut
-// from the key range of all R rows.  `text` describes the launch.
+// Host launchers of the INT4 cache kernels; `text` describes the launch.
+// attention_int4.cu (tiles of 16 rows): partials as the mma.sync kernels write
+// them (fp32 O * v_scale, (max, sum)), partitions cut from the key range of
+// all R rows.  attention_int4_tc.cu (tiles of 128 rows): partials as the
+// tcgen05 kernel writes them (f16 O / l without v_scale, (max, sum)); whole
+// 128-key partitions.
 int launch_attention_int4(const AttnParams& P, cudaStream_t s, char* text, size_t text_bytes);
+int launch_attention_int4_tc(const AttnParams& P, cudaStream_t s, char* text, size_t text_bytes);
 
 // Host launcher of the tcgen05 kernel (attention_tc.cu).  Returns
 // FP8KV_ERR_UNSUPPORTED when the shape is not one it implements.

@@ -30,6 +30,7 @@
 
 #include "attention.cuh"
 #include "common.cuh"
+#include "int4.cuh"
 
 namespace fp8kv {
 
@@ -54,33 +55,6 @@ __device__ __forceinline__ void cp16(uint32_t dst, const void* src, bool valid) 
 __device__ __forceinline__ void cp_commit() { asm volatile("cp.async.commit_group;" ::: "memory"); }
 template <int N>
 __device__ __forceinline__ void cp_wait() { asm volatile("cp.async.wait_group %0;" ::"n"(N) : "memory"); }
-
-__device__ __forceinline__ uint32_t hfma2(uint32_t a, uint32_t b, uint32_t c) {
-    uint32_t r;
-    asm("fma.rn.f16x2 %0, %1, %2, %3;" : "=r"(r) : "r"(a), "r"(b), "r"(c));
-    return r;
-}
-__device__ __forceinline__ uint32_t hmul2(uint32_t a, uint32_t b) {
-    uint32_t r;
-    asm("mul.rn.f16x2 %0, %1, %2;" : "=r"(r) : "r"(a), "r"(b));
-    return r;
-}
-
-// The four codes of each half word of z times the scales of s (f16x2, one per
-// half word) over 4: v[i] = the i-th codes' values n s / 4.
-struct Scale2 {
-    uint32_t s, c256, c16;      // s / 4, -264 s / 4, -24 s / 4
-};
-__device__ __forceinline__ Scale2 scale2(uint32_t s) {
-    return {hmul2(s, 0x34003400u), hmul2(s, 0xd420d420u), hmul2(s, 0xc600c600u)};
-}
-__device__ __forceinline__ void widen4(uint32_t z, const Scale2& k, uint32_t (&v)[4]) {
-    const uint32_t x = z << 2, y = z >> 6;
-    v[0] = hfma2((x & 0x003c003cu) | 0x5c005c00u, k.s, k.c256);
-    v[1] = hfma2((x & 0x03c003c0u) | 0x4c004c00u, k.s, k.c16);
-    v[2] = hfma2((y & 0x003c003cu) | 0x5c005c00u, k.s, k.c256);
-    v[3] = hfma2((y & 0x03c003c0u) | 0x4c004c00u, k.s, k.c16);
-}
 
 // Issue the copies of chunk `key0 / 32` of page `page` into a stage: K rows at
 // their column position (see the key order above), V rows with the 16-byte

@@ -1,0 +1,574 @@
+// attention_int4_tc.cu -- verifier rows (more than 16 per KV head) over the INT4
+// cache on the 5th-generation tensor cores.
+//
+// What bounds it: a tile of 128 keys is 18 KiB of pages, 800 cycles of one SM's
+// share of the HBM rate; its two products with 128 rows are 1024 cycles of the
+// tensor cores; and widened to f16 its K and V are written to shared memory
+// once and read once by the tensor cores (with Q in tensor memory), which with
+// the pages themselves is 164 KiB, 1300 cycles of shared-memory bandwidth.
+// That last figure is the bound.
+//
+// The values n s / 4 are exact in f16 (attention_int4.cu); within groups of
+// eight dimensions they are stored in the order 0 4 1 5 2 6 3 7 in which the
+// codes of a word widen, Q likewise, and the output is put back in order when
+// it is written.  Q rows are scaled by a power of two into f16's range.
+//
+// One CTA per (partition, row tile x KV head, sequence), 16 warps:
+//   warp 0           loads pages (bulk copies of the codes and of the scales of
+//                    a (page, head)) into a ring of 128-key stages
+//   warp 1           issues Q.K^T (one thread), S double-buffered
+//   warp 2           issues P.V
+//   warps 3, 12-15   widen K and V into swizzled f16 tiles
+//   warps 4-11       softmax: warps 4+q and 8+q share TMEM lane quarter q (32
+//                    rows, one per thread) and split the 128 columns in halves;
+//                    a tile's row maximum is exchanged through shared memory.
+//                    O is rescaled when a row's maximum grows by more than 2^4;
+//                    the weights are held as 2^11 times 2^(x - m), at most 2^15,
+//                    so that f16 keeps 11 bits of every weight down to 2^-25 of
+//                    the largest.
+// TMEM columns: Q 0-63, S/P 2 x 128 (64-319), O 320-447.
+#include <stdio.h>
+
+#include <mutex>
+#include <set>
+#include <utility>
+
+#include "attention.cuh"
+#include "common.cuh"
+#include "int4.cuh"
+#include "tcgen05.cuh"
+
+namespace fp8kv {
+
+int status_attention_int4_tc(unsigned int* s, int clear) { return read_status(s, clear); }
+
+namespace i4tc {
+
+constexpr int NK = 128;                                 // keys per tile
+constexpr int STAGES = 4;
+constexpr int OFF_V = NK * kInt4CodeBytes;              // of a stage: K codes, V codes, K scales, V scales
+constexpr int OFF_KS = 2 * NK * kInt4CodeBytes;
+constexpr int OFF_VS = OFF_KS + NK * kInt4ScaleBytes;
+constexpr int STAGE_BYTES = OFF_VS + NK * kInt4ScaleBytes;
+constexpr int BUFS = 2;                                 // widened K tiles, and V tiles
+constexpr int BUF = NK * 256, HALF = BUF / 2;           // two blocks of 128 keys x 64 dims (128-byte swizzled)
+constexpr int XCH_BYTES = 3 * 2 * 128 * 4;              // [tile parity 0, 1, row sums][half][row]
+constexpr int SMEM = 2 * BUFS * BUF + STAGES * STAGE_BYTES + XCH_BYTES + 1024 + 512;
+constexpr int EPI_STRIDE = 144;                         // staged half row (128 bytes), padded against bank conflicts
+static_assert(2 * 128 * EPI_STRIDE <= 2 * BUFS * BUF, "epilogue staging exceeds the widened tiles");
+constexpr uint32_t TM_Q = 0, TM_S = 64, TM_O = 320, TM_COLS = 512;
+constexpr int WARPS = 16, THREADS = WARPS * 32, CONV_WARPS = 5;
+constexpr float GROW = 4.0f, BIAS = 11.0f;              // see the head of the file
+
+enum {
+    B_STG_FULL = 0,
+    B_STG_EMPTY = B_STG_FULL + STAGES,
+    B_K_FULL = B_STG_EMPTY + STAGES,
+    B_K_EMPTY = B_K_FULL + BUFS,
+    B_V_FULL = B_K_EMPTY + BUFS,
+    B_V_EMPTY = B_V_FULL + BUFS,
+    B_S_FULL = B_V_EMPTY + BUFS,
+    B_S_EMPTY = B_S_FULL + 2,                           // P.V over this S buffer's P complete
+    B_P_FULL = B_S_EMPTY + 2,
+    B_O_DONE = B_P_FULL + 2,
+    B_O_FINAL = B_O_DONE + 1,
+    B_Q_READY = B_O_FINAL + 1,
+    B_IDLE = B_Q_READY + 1,
+    B_PAIR = B_IDLE + 1,                                // per TMEM lane quarter: its two softmax warps
+    B_COUNT = B_PAIR + 4
+};
+static_assert(B_COUNT * 8 + 16 <= 512, "barrier area");
+
+__device__ __forceinline__ void bulk_load(uint32_t dst, const void* src, uint32_t bytes, uint32_t bar) {
+    asm volatile("cp.async.bulk.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1], %2, [%3];" ::"r"(dst),
+                 "l"(src), "r"(bytes), "r"(bar)
+                 : "memory");
+}
+
+__device__ __forceinline__ bool elect_one() {
+    uint32_t r;
+    asm volatile("{ .reg .pred p; elect.sync _|p, 0xffffffff; selp.u32 %0, 1, 0, p; }" : "=r"(r));
+    return r != 0;
+}
+
+__device__ __forceinline__ float max3(float a, float b, float c) {
+    float r;
+    asm("max.f32 %0, %1, %2, %3;" : "=f"(r) : "f"(a), "f"(b), "f"(c));
+    return r;
+}
+
+// 32 codes (16 bytes, two blocks) of row r, widened into a tile: dims 32 c ...
+// of the row, 16-byte units of its two 128-byte rows swizzled by the row.
+__device__ __forceinline__ void widen_chunk(uint8_t* tile, int r, int c, uint4 codes, uint32_t scales) {
+    const uint32_t s2 = e4m3x2_to_f16x2(scales);
+    const Scale2 sa = scale2(prmt(s2, s2, 0x1010)), sb = scale2(prmt(s2, s2, 0x3232));
+    const uint32_t w[4] = {codes.x, codes.y, codes.z, codes.w};
+    uint8_t* row = tile + (c >> 1) * HALF + r * 128;
+#pragma unroll
+    for (int u = 0; u < 4; ++u) {
+        uint32_t v[4];
+        widen4(w[u], u < 2 ? sa : sb, v);
+        *(uint4*)(row + (((4 * (c & 1) + u) ^ (r & 7)) << 4)) = make_uint4(v[0], v[1], v[2], v[3]);
+    }
+}
+
+template <int PS>
+__global__ void __launch_bounds__(THREADS, 1) attention_int4_tc_kernel(AttnParams P) {
+    extern __shared__ uint8_t smem_raw[];
+    uint8_t* smem = (uint8_t*)(((uintptr_t)smem_raw + 1023) & ~(uintptr_t)1023);
+    uint8_t* kbuf = smem;                                   // BUFS x 32 KiB
+    uint8_t* vbuf = kbuf + BUFS * BUF;                      // BUFS x 32 KiB
+    uint8_t* stg = vbuf + BUFS * BUF;                       // STAGES x 18 KiB
+    float* xch = (float*)(stg + STAGES * STAGE_BYTES);
+    uint64_t* bars = (uint64_t*)((uint8_t*)xch + XCH_BYTES);
+    uint32_t* tmem_slot = (uint32_t*)(bars + B_COUNT);
+    auto bar = [&](int i) { return smem_u32(&bars[i]); };
+    const int RT = (P.R + 127) >> 7;
+    const int rt = blockIdx.y % RT;
+    int split = blockIdx.x, hk = blockIdx.y / RT, b = blockIdx.z;
+    const int R0 = rt * 128, RL = min(128, P.R - R0);
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    pdl_launch_dependents();
+    if (threadIdx.x == 0) {
+        for (int i = 0; i < B_COUNT; ++i) {
+            int count = 1;
+            if ((i >= B_STG_EMPTY && i < B_K_EMPTY) || (i >= B_V_FULL && i < B_V_EMPTY)) count = CONV_WARPS;
+            if ((i >= B_P_FULL && i < B_O_DONE) || i == B_Q_READY) count = 8;
+            if (i == B_IDLE || i >= B_PAIR) count = 2;
+            mbar_init(bar(i), count);
+        }
+        fence_barrier_init();
+    }
+    if (warp == 0) {
+        asm volatile("tcgen05.alloc.cta_group::1.sync.aligned.shared::cta.b32 [%0], %1;" ::"r"(smem_u32(tmem_slot)),
+                     "r"(TM_COLS)
+                     : "memory");
+        asm volatile("tcgen05.relinquish_alloc_permit.cta_group::1.sync.aligned;" ::: "memory");
+    }
+    fence_before();
+    __syncthreads();
+    fence_after();
+    const uint32_t tmem = *tmem_slot;
+    pdl_wait();
+    bool have_work = true;
+    if (P.lpt_order) {
+        // CTA i: KV head i mod Hkv of the slot of rank i / Hkv, longest first
+        const int lin = blockIdx.x + gridDim.x * (blockIdx.y + gridDim.y * blockIdx.z);
+        const int q = P.lpt_order[lin / P.Hkv];
+        hk = lin % P.Hkv;
+        if (q < 0) {
+            have_work = false;
+        } else {
+            b = q / P.num_splits;
+            split = q % P.num_splits;
+        }
+    }
+    const int L = P.seq_lens[b];
+    const bool seq_ok = !(L < P.M || L > P.max_seq_len || (L + PS - 1) / PS > P.mpps);
+    bool run = seq_ok && have_work;                         // uniform over the CTA
+    if (!seq_ok && !P.lpt_order && threadIdx.x == 0 && split == 0 && blockIdx.y == 0) flag(FP8KV_DEV_BAD_SEQ_LEN);
+    // keys visible to any row of the tile: from the first row's window start
+    // to the last row's position (row r is query m = r / G at L - M + m)
+    const int hi0 = L - P.M + (R0 + RL - 1) / P.G;
+    const int lo0 = (P.window_left >= 0) ? max(0, L - P.M + R0 / P.G - P.window_left) : 0;
+    const int first_page = lo0 / PS, last_page = hi0 / PS;
+    const int nsplit_b = (last_page - first_page + P.split_pages) / P.split_pages;
+    if (run && nsplit_b > P.num_splits) {
+        if (threadIdx.x == 0 && split == 0) flag(FP8KV_DEV_BAD_SEQ_LEN);
+        run = false;
+    }
+    if (split >= nsplit_b) run = false;
+    const int page_begin = first_page + split * P.split_pages;
+    const int n_pages = min(P.split_pages, last_page + 1 - page_begin);
+    constexpr int PPT = NK / PS;                            // pages per tile
+    const int n_tiles = (n_pages + PPT - 1) / PPT;
+    const int k_begin = page_begin * PS;
+    bool ok = true;
+
+    if (!run) {
+        // no keys of this sequence fall in this partition (or bad input)
+    } else if (warp == 0) {
+        // ---------------------------------------------------------- producer
+        // lane 4 p + k: copy k (K codes, V codes, K scales, V scales) of page p
+        // of the tile; a page id outside the pool reads as zeros
+        const int32_t* bt = P.block_table + (int64_t)b * P.mpps + page_begin;
+        const int p = lane >> 2, kind = lane & 3;
+        const uint8_t* cache = kind & 1 ? P.v_cache : P.k_cache;
+        const uint32_t bytes = kind < 2 ? PS * kInt4CodeBytes : PS * kInt4ScaleBytes;
+        const uint32_t off = (kind == 0 ? 0 : kind == 1 ? OFF_V : kind == 2 ? OFF_KS : OFF_VS) + p * bytes;
+        int issued = 0;
+        int next = p < PPT && p < n_pages ? bt[p] : -1;
+        for (int t = 0; t < n_tiles; ++t) {
+            const int s = t % STAGES, use = t / STAGES, page = next, at = t * PPT + p;
+            const bool mine = p < PPT && at < n_pages;
+            next = p < PPT && at + PPT < n_pages ? bt[at + PPT] : -1;
+            if (use > 0) ok = mbar_wait(bar(B_STG_EMPTY + s), (use - 1) & 1);
+            if (!__all_sync(0xffffffffu, ok)) break;
+            uint8_t* dst = stg + s * STAGE_BYTES + off;
+            const bool valid = mine && page >= 0 && page < P.num_pages;
+            if (mine && !valid)
+                for (uint32_t i = 0; i < bytes; i += 16) *(uint4*)(dst + i) = make_uint4(0, 0, 0, 0);
+            uint32_t total = valid ? bytes : 0;
+#pragma unroll
+            for (int o = 16; o >= 1; o >>= 1) total += __shfl_xor_sync(0xffffffffu, total, o);
+            if (lane == 0) mbar_expect_tx(bar(B_STG_FULL + s), total);
+            __syncwarp();
+            if (valid)
+                bulk_load(smem_u32(dst),
+                          cache + ((int64_t)page * P.Hkv + hk) * (PS * kInt4RowBytes) +
+                              (kind < 2 ? 0 : PS * kInt4CodeBytes),
+                          bytes, bar(B_STG_FULL + s));
+            issued = t + 1;
+        }
+        // never leave with copies into this CTA's shared memory in flight
+        for (int t = max(0, issued - STAGES); t < issued; ++t) mbar_wait(bar(B_STG_FULL + t % STAGES), (t / STAGES) & 1);
+        __syncwarp();
+    } else if (warp < 3) {
+        // ------------------------------------------------------ MMA issue
+        constexpr uint32_t ID_QK = idesc(128, NK, false), ID_PV = idesc(128, 128, true);
+        const bool leader = elect_one();
+        if (warp == 1) {
+            ok = mbar_wait(bar(B_Q_READY), 0);
+            for (int t = 0; t < n_tiles; ++t) {
+                const int sb = t & 1;
+                if (ok) ok = mbar_wait(bar(B_K_FULL + sb), (t >> 1) & 1);
+                // the buffer holds P(t - 2) until its P.V has read it
+                if (ok && t >= 2) ok = mbar_wait(bar(B_S_EMPTY + sb), ((t >> 1) - 1) & 1);
+                ok = __all_sync(0xffffffffu, ok);
+                if (!ok) break;
+                fence_after();
+                if (leader) {
+                    const uint32_t kt = smem_u32(kbuf + sb * BUF);
+#pragma unroll
+                    for (int ks = 0; ks < 8; ++ks)
+                        mma_f16_ts(tmem + TM_S + sb * 128, tmem + TM_Q + 8 * ks,
+                                   sdesc(kt + (ks >> 2) * HALF + (ks & 3) * 32, 16, 1024), ID_QK, ks > 0);
+                    mma_commit(bar(B_S_FULL + sb));
+                    mma_commit(bar(B_K_EMPTY + sb));
+                }
+                __syncwarp();
+            }
+        } else {
+            for (int u = 0; u < n_tiles; ++u) {
+                const int ub = u & 1;
+                ok = mbar_wait(bar(B_V_FULL + ub), (u >> 1) & 1);
+                if (ok) ok = mbar_wait(bar(B_P_FULL + ub), (u >> 1) & 1);
+                ok = __all_sync(0xffffffffu, ok);
+                if (!ok) break;
+                fence_after();
+                if (leader) {
+                    const uint32_t vf = smem_u32(vbuf + ub * BUF);
+#pragma unroll
+                    for (int kk = 0; kk < NK / 16; ++kk)
+                        mma_f16_ts(tmem + TM_O, tmem + TM_S + ub * 128 + 8 * kk, sdesc(vf + kk * 2048, HALF, 1024), ID_PV,
+                                   u > 0 || kk > 0);
+                    mma_commit(bar(B_O_DONE));
+                    mma_commit(bar(B_S_EMPTY + ub));
+                    mma_commit(bar(B_V_EMPTY + ub));
+                    if (u == n_tiles - 1) mma_commit(bar(B_O_FINAL));
+                }
+                __syncwarp();
+            }
+        }
+        // nothing the tensor cores still run may outlive the TMEM allocation
+        if (leader) mma_commit(bar(B_IDLE));
+        __syncwarp();
+        mbar_wait(bar(B_IDLE), 0);
+        __syncwarp();
+    } else if (warp == 3 || warp >= 12) {
+        // ---------------------------------------------------------- widening
+        // items of (key, 32 dims); eight lanes cover four keys x two chunks,
+        // which keeps the 16-byte stores free of bank conflicts
+        const int cw = warp == 3 ? 0 : warp - 11;
+        for (int t = 0; t < n_tiles; ++t) {
+            const int s = t % STAGES, tb = t & 1;
+            ok = mbar_wait(bar(B_STG_FULL + s), (t / STAGES) & 1);
+            if (ok && t >= BUFS) ok = mbar_wait(bar(B_K_EMPTY + tb), ((t >> 1) - 1) & 1);
+            if (!__all_sync(0xffffffffu, ok)) { ok = false; break; }
+            const uint8_t* src = stg + s * STAGE_BYTES;
+            const int rr = ((lane >> 1) & 3) + 4 * (lane >> 4), cc = (lane & 1) + 2 * ((lane >> 3) & 1);
+#pragma unroll 2
+            for (int g = cw; g < NK / 8; g += CONV_WARPS) {
+                const int r = 8 * g + rr;
+                widen_chunk(kbuf + tb * BUF, r, cc, *(const uint4*)(src + r * 64 + cc * 16),
+                            *(const uint16_t*)(src + OFF_KS + r * 8 + 2 * cc));
+            }
+            fence_proxy_async();
+            __syncwarp();
+            if (lane == 0) mbar_arrive(bar(B_K_FULL + tb));
+            if (t >= BUFS) ok = mbar_wait(bar(B_V_EMPTY + tb), ((t >> 1) - 1) & 1);
+            if (!__all_sync(0xffffffffu, ok)) { ok = false; break; }
+            // keys outside every row's range get scale 0: whatever their bytes
+            // are, zeros reach the output
+            const int k0 = k_begin + t * NK;
+            const int zlo = lo0 - k0, zhi = min(min(NK, (n_pages - t * PPT) * PS), hi0 + 1 - k0);
+#pragma unroll 2
+            for (int g = cw; g < NK / 8; g += CONV_WARPS) {
+                const int r = 8 * g + rr;
+                uint32_t sc = *(const uint16_t*)(src + OFF_VS + r * 8 + 2 * cc);
+                if (r < zlo || r >= zhi) sc = 0;
+                widen_chunk(vbuf + tb * BUF, r, cc, *(const uint4*)(src + OFF_V + r * 64 + cc * 16), sc);
+            }
+            fence_proxy_async();
+            __syncwarp();
+            if (lane == 0) {
+                mbar_arrive(bar(B_V_FULL + tb));
+                mbar_arrive(bar(B_STG_EMPTY + s));
+            }
+        }
+    } else {
+        // ------------------------------------------------------------ softmax
+        const int wq = warp & 3, half = (warp - 4) >> 2;
+        const int r = wq * 32 + lane;
+        const bool active = wq * 32 < RL;                   // the quarter holds at least one real row
+        const uint32_t lane_base = tmem + ((uint32_t)(wq * 32) << 16);
+        const int rr = R0 + min(r, RL - 1);                 // the row of the (b, hk) block
+        const int m = rr / P.G;
+        const int p_r = L - P.M + m;
+        const int lo_r = (P.window_left >= 0) ? max(0, p_r - P.window_left) : 0;
+        const int64_t row_idx = ((int64_t)b * P.M + m) * P.Hq + hk * P.G + rr % P.G;
+        const float vs = 4.0f * *P.v_scale;
+        const bool pad = r >= RL;                           // rows past M x G: Q = 0
+        float mult;
+        {
+            // this half's 64 dims of the row, times a power of two that puts
+            // the row maximum (of all 128) in [2^4, 2^5), as f16 into TMEM
+            const uint4* src = (const uint4*)(P.q + row_idx * 128) + 8 * half;
+            uint32_t qh[32];
+#pragma unroll
+            for (int u = 0; u < 8; ++u) {
+                const uint4 w = pad ? make_uint4(0, 0, 0, 0) : src[u];
+                qh[4 * u] = w.x;
+                qh[4 * u + 1] = w.y;
+                qh[4 * u + 2] = w.z;
+                qh[4 * u + 3] = w.w;
+            }
+            uint32_t am = 0;
+#pragma unroll
+            for (int u = 0; u < 32; ++u) am = max_bf16x2(am, qh[u] & 0x7fff7fffu);
+            xch[half * 128 + r] = fmaxf(bf16_lo(am), bf16_hi(am));
+            __syncwarp();
+            if (lane == 0) mbar_arrive(bar(B_PAIR + wq));
+            ok = __all_sync(0xffffffffu, mbar_wait(bar(B_PAIR + wq), 0));
+            const float amax = fmaxf(xch[r], xch[128 + r]);
+            int e = 4;
+            const uint32_t ab = __float_as_uint(amax);
+            if (amax > 0.f && ((ab >> 23) & 0xff) != 0xff) {
+                const int be = (int)((ab >> 23) & 0xff);
+                e = be ? be - 127 : -127;
+            }
+            const int sh = max(-120, min(120, 4 - e));
+            const float scale = ldexpf(1.0f, sh);
+            mult = 4.0f * *P.k_scale * P.sm_scale * 1.4426950408889634f * ldexpf(1.0f, -sh);
+            uint32_t qf[32];
+#pragma unroll
+            for (int u = 0; u < 8; ++u) {                   // dims 8u .. + 7 in the order 0 4 1 5 2 6 3 7
+                const uint32_t* x = qh + 4 * u;
+                qf[4 * u] = pack_f16x2(bf16_lo(x[0]) * scale, bf16_lo(x[2]) * scale);
+                qf[4 * u + 1] = pack_f16x2(bf16_hi(x[0]) * scale, bf16_hi(x[2]) * scale);
+                qf[4 * u + 2] = pack_f16x2(bf16_lo(x[1]) * scale, bf16_lo(x[3]) * scale);
+                qf[4 * u + 3] = pack_f16x2(bf16_hi(x[1]) * scale, bf16_hi(x[3]) * scale);
+            }
+            tmem_st_x32(lane_base + TM_Q + 32 * half, qf);
+            tmem_wait_st();
+        }
+        fence_before();
+        __syncwarp();
+        if (lane == 0) mbar_arrive(bar(B_Q_READY));
+
+        int pmin = p_r, lomax = lo_r, pmax = p_r, lomin = lo_r;
+#pragma unroll
+        for (int off = 1; off < 32; off <<= 1) {
+            pmin = min(pmin, __shfl_xor_sync(0xffffffffu, pmin, off));
+            lomax = max(lomax, __shfl_xor_sync(0xffffffffu, lomax, off));
+            pmax = max(pmax, __shfl_xor_sync(0xffffffffu, pmax, off));
+            lomin = min(lomin, __shfl_xor_sync(0xffffffffu, lomin, off));
+        }
+        float m_run = -INFINITY, l_run = 0.f;               // l_run: this half's columns only
+        for (int t = 0; t < n_tiles && ok; ++t) {
+            const int sb = t & 1;
+            ok = __all_sync(0xffffffffu, mbar_wait(bar(B_S_FULL + sb), (t >> 1) & 1));
+            if (!ok) break;
+            fence_after();
+            if (active) {
+                const int k0 = k_begin + t * NK + 64 * half;   // first key of this half
+                const bool dead = k0 > pmax || k0 + 63 < lomin;   // no row of this warp sees any: P = 0
+                uint32_t sv[64];
+                float hmax = -INFINITY;
+                if (!dead) {
+                    tmem_ld_x64(lane_base + TM_S + sb * 128 + 64 * half, sv);
+                    tmem_wait_ld();
+                    if (k0 + 63 > pmin || k0 < lomax) {
+                        // this row's visible columns of the half as bits
+                        const int jlo = max(0, lo_r - k0), jhi = min(64, p_r - k0 + 1);
+                        const uint64_t below_hi = jhi <= 0 ? 0ull : (jhi >= 64 ? ~0ull : (1ull << jhi) - 1);
+                        const uint64_t below_lo = jlo >= 64 ? ~0ull : (1ull << jlo) - 1;
+                        const uint64_t vis = below_hi & ~below_lo;
+                        const uint32_t vis_lo = (uint32_t)vis, vis_hi = (uint32_t)(vis >> 32);
+#pragma unroll
+                        for (int j = 0; j < 64; ++j)
+                            sv[j] = (((j < 32 ? vis_lo : vis_hi) >> (j & 31)) & 1u) ? sv[j] : 0xff800000u;   // -inf
+                    }
+                    float m4[4];
+#pragma unroll
+                    for (int c = 0; c < 4; ++c) {
+                        m4[c] = max3(__uint_as_float(sv[c]), __uint_as_float(sv[c + 4]), __uint_as_float(sv[c + 8]));
+#pragma unroll
+                        for (int u = c + 12; u < 60; u += 8)
+                            m4[c] = max3(m4[c], __uint_as_float(sv[u]), __uint_as_float(sv[u + 4]));
+                        m4[c] = fmaxf(m4[c], __uint_as_float(sv[60 + c]));
+                    }
+                    hmax = max3(m4[0], m4[1], fmaxf(m4[2], m4[3]));
+                }
+                // exchange with the partner warp (phase t + 1 of the pair barrier)
+                xch[(sb * 2 + half) * 128 + r] = hmax;
+                __syncwarp();
+                if (lane == 0) mbar_arrive(bar(B_PAIR + wq));
+                ok = __all_sync(0xffffffffu, mbar_wait(bar(B_PAIR + wq), (t + 1) & 1));
+                if (!ok) break;
+                const float tmax = fmaxf(xch[sb * 256 + r], xch[sb * 256 + 128 + r]) * mult;
+                const bool rescale = (m_run != -INFINITY) && (tmax > m_run + GROW);
+                if (__any_sync(0xffffffffu, rescale)) {
+                    // O holds P.V up to tile t - 1: wait for it, then rescale this half
+                    ok = __all_sync(0xffffffffu, mbar_wait(bar(B_O_DONE), (t - 1) & 1));
+                    if (!ok) break;
+                    fence_after();
+                    const float alpha = rescale ? ex2(m_run - tmax) : 1.0f;
+#pragma unroll 1
+                    for (int c = 0; c < 64; c += 32) {
+                        uint32_t ov[32];
+                        tmem_ld_x32(lane_base + TM_O + 64 * half + c, ov);
+                        tmem_wait_ld();
+#pragma unroll
+                        for (int j = 0; j < 32; ++j) ov[j] = __float_as_uint(__uint_as_float(ov[j]) * alpha);
+                        tmem_st_x32(lane_base + TM_O + 64 * half + c, ov);
+                    }
+                    tmem_wait_st();
+                    if (rescale) {
+                        l_run *= alpha;
+                        m_run = tmax;
+                    }
+                }
+                if (m_run == -INFINITY) m_run = tmax;
+                const float neg = (m_run == -INFINITY) ? 0.f : BIAS - m_run;
+                // P = 2^(s mult - m + 11) as f16 (masked keys are -inf and give
+                // 0); both halves' S reads are complete (pair barrier above)
+                float sum0 = 0.f, sum1 = 0.f;
+                uint32_t pw[32];
+                if (!dead) {
+#pragma unroll
+                    for (int j = 0; j < 32; ++j) {
+                        const float p0 = ex2(fmaf(__uint_as_float(sv[2 * j]), mult, neg));
+                        const float p1 = ex2(fmaf(__uint_as_float(sv[2 * j + 1]), mult, neg));
+                        sum0 += p0;
+                        sum1 += p1;
+                        pw[j] = pack_f16x2(p0, p1);
+                    }
+                } else {
+#pragma unroll
+                    for (int j = 0; j < 32; ++j) pw[j] = 0u;
+                }
+                tmem_st_x32(lane_base + TM_S + sb * 128 + 32 * half, pw);
+                l_run += sum0 + sum1;
+                tmem_wait_st();
+            }
+            fence_before();
+            __syncwarp();
+            if (lane == 0) mbar_arrive(bar(B_P_FULL + sb));
+        }
+        // ------------------------------------------------------------ epilogue
+        if (ok) ok = mbar_wait(bar(B_O_FINAL), 0);
+        ok = __all_sync(0xffffffffu, ok);
+        if (ok && active) {
+            fence_after();
+            // row sums of both halves: the next phase of the pair barrier
+            xch[(4 + half) * 128 + r] = l_run;
+            __syncwarp();
+            if (lane == 0) mbar_arrive(bar(B_PAIR + wq));
+            ok = __all_sync(0xffffffffu, mbar_wait(bar(B_PAIR + wq), (n_tiles + 1) & 1));
+        }
+        if (ok && active) {
+            const float l_tot = xch[4 * 128 + r] + xch[5 * 128 + r];
+            const bool direct = nsplit_b == 1;
+            // direct: bf16 of 4 v_scale O / l; partial: f16 of 4 O / l (|x| <=
+            // 7 * 448) beside its (max, sum); a row with no visible key here
+            // has l = 0: weight 0, values 0
+            const float f = direct ? vs / l_tot : (l_tot > 0.f ? 4.0f / l_tot : 0.f);
+            // the half row goes through shared memory (the widened tiles are
+            // free) to one bulk copy
+            uint8_t* row_stage = kbuf + (half * 128 + r) * EPI_STRIDE;
+#pragma unroll 1
+            for (int c = 0; c < 64; c += 32) {
+                uint32_t ov[32];
+                tmem_ld_x32(lane_base + TM_O + 64 * half + c, ov);
+                tmem_wait_ld();
+                uint4* dst = (uint4*)(row_stage + c * 2);
+#pragma unroll
+                for (int v4 = 0; v4 < 4; ++v4) {
+                    float x[8];
+#pragma unroll
+                    for (int i = 0; i < 8; ++i) x[i] = __uint_as_float(ov[8 * v4 + i]) * f;
+                    // columns 0 4 1 5 2 6 3 7 back in order
+                    dst[v4] = direct ? make_uint4(pack_bf16x2(x[0], x[2]), pack_bf16x2(x[4], x[6]),
+                                                  pack_bf16x2(x[1], x[3]), pack_bf16x2(x[5], x[7]))
+                                     : make_uint4(pack_f16x2(x[0], x[2]), pack_f16x2(x[4], x[6]),
+                                                  pack_f16x2(x[1], x[3]), pack_f16x2(x[5], x[7]));
+                }
+            }
+            if (r < RL) {
+                fence_proxy_async();        // the staged row, written by this thread, to the bulk copy
+                if (direct)
+                    bulk_store(P.out + row_idx * 128 + 64 * half, smem_u32(row_stage), 128);
+                else
+                    bulk_store((uint16_t*)P.ws_o + (row_idx * P.num_splits + split) * 128 + 64 * half,
+                               smem_u32(row_stage), 128);
+                bulk_commit();
+                bulk_wait_read();
+                if (!direct && half == 0)
+                    *(float2*)(P.ws_ml + (row_idx * P.num_splits + split) * 2) = make_float2(m_run, l_tot);
+            }
+        }
+    }
+
+    // ---------------------------------------------------------------- teardown
+    fence_before();
+    __syncthreads();
+    if (warp == 0) {
+        fence_after();
+        asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, %1;" ::"r"(tmem), "r"(TM_COLS) : "memory");
+    }
+}
+
+}  // namespace i4tc
+
+int launch_attention_int4_tc(const AttnParams& P, cudaStream_t s, char* text, size_t text_bytes) {
+    const int RT = (P.R + 127) / 128;
+    if ((P.split_pages * P.page_size) % i4tc::NK || (int64_t)RT * P.Hkv > 65535) return FP8KV_ERR_UNSUPPORTED;
+    static std::mutex mu;
+    static std::set<std::pair<int, const void*>> done;
+    auto kern = P.page_size == 32 ? i4tc::attention_int4_tc_kernel<32> : i4tc::attention_int4_tc_kernel<64>;
+    {
+        int dev = 0;
+        if (cudaGetDevice(&dev) != cudaSuccess) return FP8KV_ERR_CUDA;
+        std::lock_guard<std::mutex> lock(mu);
+        if (!done.count({dev, (const void*)kern})) {
+            if (cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, i4tc::SMEM) != cudaSuccess)
+                return FP8KV_ERR_CUDA;
+            done.insert({dev, (const void*)kern});
+        }
+    }
+    const dim3 grid(P.num_splits, P.Hkv * RT, P.B);
+    const cudaError_t e = launch_pdl(kern, grid, dim3(i4tc::THREADS), i4tc::SMEM, s, P);
+    if (e != cudaSuccess) {
+        cudaGetLastError();
+        return FP8KV_ERR_CUDA;
+    }
+    snprintf(text, text_bytes,
+             "attention_int4_tc<ps=%d> rows=%d row_tiles=%d splits=%d split_tokens=%d grid=%dx%dx%d threads=%d reduce=%d "
+             "order=%s",
+             P.page_size, P.R, RT, P.num_splits, P.split_pages * P.page_size, P.num_splits, P.Hkv * RT, P.B,
+             i4tc::THREADS, P.num_splits > 1 ? 1 : 0, P.lpt_order ? "longest_first" : "grid");
+    return FP8KV_OK;
+}
+
+}  // namespace fp8kv

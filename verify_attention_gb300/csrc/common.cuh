@@ -361,6 +361,7 @@ void set_dispatch(const char* text);    // per-thread record of the last dispatc
 int status_insert(unsigned int* s, int clear);     // insert.cu
 int status_attention(unsigned int* s, int clear);  // attention.cu
 int status_attention_int4(unsigned int* s, int clear);  // attention_int4.cu
+int status_attention_int4_tc(unsigned int* s, int clear);  // attention_int4_tc.cu
 int status_prompt(unsigned int* s, int clear);     // prompt_attention.cu
 
 // OR this translation unit's status word into *s, optionally clearing it.

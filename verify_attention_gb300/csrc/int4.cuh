@@ -1,0 +1,35 @@
+// int4.cuh -- widening of the INT4 cache's codes, shared by its kernels (the
+// arithmetic is explained at the head of attention_int4.cu).
+#pragma once
+#include <stdint.h>
+
+namespace fp8kv {
+
+__device__ __forceinline__ uint32_t hfma2(uint32_t a, uint32_t b, uint32_t c) {
+    uint32_t r;
+    asm("fma.rn.f16x2 %0, %1, %2, %3;" : "=r"(r) : "r"(a), "r"(b), "r"(c));
+    return r;
+}
+__device__ __forceinline__ uint32_t hmul2(uint32_t a, uint32_t b) {
+    uint32_t r;
+    asm("mul.rn.f16x2 %0, %1, %2;" : "=r"(r) : "r"(a), "r"(b));
+    return r;
+}
+
+// The four codes of each half word of z times the scales of s (f16x2, one per
+// half word) over 4: v[i] = the i-th codes' values n s / 4.
+struct Scale2 {
+    uint32_t s, c256, c16;      // s / 4, -264 s / 4, -24 s / 4
+};
+__device__ __forceinline__ Scale2 scale2(uint32_t s) {
+    return {hmul2(s, 0x34003400u), hmul2(s, 0xd420d420u), hmul2(s, 0xc600c600u)};
+}
+__device__ __forceinline__ void widen4(uint32_t z, const Scale2& k, uint32_t (&v)[4]) {
+    const uint32_t x = z << 2, y = z >> 6;
+    v[0] = hfma2((x & 0x003c003cu) | 0x5c005c00u, k.s, k.c256);
+    v[1] = hfma2((x & 0x03c003c0u) | 0x4c004c00u, k.s, k.c16);
+    v[2] = hfma2((y & 0x003c003cu) | 0x5c005c00u, k.s, k.c256);
+    v[3] = hfma2((y & 0x03c003c0u) | 0x4c004c00u, k.s, k.c16);
+}
+
+}  // namespace fp8kv
