@@ -13,12 +13,13 @@
 // codes of a word widen, Q likewise, and the output is put back in order when
 // it is written.  Q rows are scaled by a power of two into f16's range.
 //
-// One CTA per (partition, row tile x KV head, sequence), 16 warps:
+// One CTA per (partition, row tile x KV head, sequence), 20 warps:
 //   warp 0           loads pages (bulk copies of the codes and of the scales of
 //                    a (page, head)) into a ring of 128-key stages
 //   warp 1           issues Q.K^T (one thread), S double-buffered
 //   warp 2           issues P.V
-//   warps 3, 12-15   widen K and V into swizzled f16 tiles
+//   warps 12-19      widen K and V into swizzled f16 tiles (five warps took 3700
+//                    cycles a tile)
 //   warps 4-11       softmax: warps 4+q and 8+q share TMEM lane quarter q (32
 //                    rows, one per thread) and split the 128 columns in halves;
 //                    a tile's row maximum is exchanged through shared memory.
@@ -57,7 +58,10 @@ constexpr int SMEM = 2 * BUFS * BUF + STAGES * STAGE_BYTES + XCH_BYTES + 1024 + 
 constexpr int EPI_STRIDE = 144;                         // staged half row (128 bytes), padded against bank conflicts
 static_assert(2 * 128 * EPI_STRIDE <= 2 * BUFS * BUF, "epilogue staging exceeds the widened tiles");
 constexpr uint32_t TM_Q = 0, TM_S = 64, TM_O = 320, TM_COLS = 512;
-constexpr int WARPS = 16, THREADS = WARPS * 32, CONV_WARPS = 5;
+constexpr int WARPS = 20, THREADS = WARPS * 32, CONV_WARPS = 8;
+// registers: 640 x 96 at launch = 128 x (3 x 80 + 2 x 120) after the split
+constexpr int REGS_SERVICE = 80, REGS_SOFTMAX = 120;
+static_assert(128 * (3 * REGS_SERVICE + 2 * REGS_SOFTMAX) <= THREADS * 96, "register split above the launch's share");
 constexpr float GROW = 4.0f, BIAS = 11.0f;              // see the head of the file
 
 enum {
@@ -83,18 +87,6 @@ __device__ __forceinline__ void bulk_load(uint32_t dst, const void* src, uint32_
     asm volatile("cp.async.bulk.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1], %2, [%3];" ::"r"(dst),
                  "l"(src), "r"(bytes), "r"(bar)
                  : "memory");
-}
-
-__device__ __forceinline__ bool elect_one() {
-    uint32_t r;
-    asm volatile("{ .reg .pred p; elect.sync _|p, 0xffffffff; selp.u32 %0, 1, 0, p; }" : "=r"(r));
-    return r != 0;
-}
-
-__device__ __forceinline__ float max3(float a, float b, float c) {
-    float r;
-    asm("max.f32 %0, %1, %2, %3;" : "=f"(r) : "f"(a), "f"(b), "f"(c));
-    return r;
 }
 
 // 32 codes (16 bytes, two blocks) of row r, widened into a tile: dims 32 c ...
@@ -187,136 +179,8 @@ __global__ void __launch_bounds__(THREADS, 1) attention_int4_tc_kernel(AttnParam
 
     if (!run) {
         // no keys of this sequence fall in this partition (or bad input)
-    } else if (warp == 0) {
-        // ---------------------------------------------------------- producer
-        // lane 4 p + k: copy k (K codes, V codes, K scales, V scales) of page p
-        // of the tile; a page id outside the pool reads as zeros
-        const int32_t* bt = P.block_table + (int64_t)b * P.mpps + page_begin;
-        const int p = lane >> 2, kind = lane & 3;
-        const uint8_t* cache = kind & 1 ? P.v_cache : P.k_cache;
-        const uint32_t bytes = kind < 2 ? PS * kInt4CodeBytes : PS * kInt4ScaleBytes;
-        const uint32_t off = (kind == 0 ? 0 : kind == 1 ? OFF_V : kind == 2 ? OFF_KS : OFF_VS) + p * bytes;
-        int issued = 0;
-        int next = p < PPT && p < n_pages ? bt[p] : -1;
-        for (int t = 0; t < n_tiles; ++t) {
-            const int s = t % STAGES, use = t / STAGES, page = next, at = t * PPT + p;
-            const bool mine = p < PPT && at < n_pages;
-            next = p < PPT && at + PPT < n_pages ? bt[at + PPT] : -1;
-            if (use > 0) ok = mbar_wait(bar(B_STG_EMPTY + s), (use - 1) & 1);
-            if (!__all_sync(0xffffffffu, ok)) break;
-            uint8_t* dst = stg + s * STAGE_BYTES + off;
-            const bool valid = mine && page >= 0 && page < P.num_pages;
-            if (mine && !valid)
-                for (uint32_t i = 0; i < bytes; i += 16) *(uint4*)(dst + i) = make_uint4(0, 0, 0, 0);
-            uint32_t total = valid ? bytes : 0;
-#pragma unroll
-            for (int o = 16; o >= 1; o >>= 1) total += __shfl_xor_sync(0xffffffffu, total, o);
-            if (lane == 0) mbar_expect_tx(bar(B_STG_FULL + s), total);
-            __syncwarp();
-            if (valid)
-                bulk_load(smem_u32(dst),
-                          cache + ((int64_t)page * P.Hkv + hk) * (PS * kInt4RowBytes) +
-                              (kind < 2 ? 0 : PS * kInt4CodeBytes),
-                          bytes, bar(B_STG_FULL + s));
-            issued = t + 1;
-        }
-        // never leave with copies into this CTA's shared memory in flight
-        for (int t = max(0, issued - STAGES); t < issued; ++t) mbar_wait(bar(B_STG_FULL + t % STAGES), (t / STAGES) & 1);
-        __syncwarp();
-    } else if (warp < 3) {
-        // ------------------------------------------------------ MMA issue
-        constexpr uint32_t ID_QK = idesc(128, NK, false), ID_PV = idesc(128, 128, true);
-        const bool leader = elect_one();
-        if (warp == 1) {
-            ok = mbar_wait(bar(B_Q_READY), 0);
-            for (int t = 0; t < n_tiles; ++t) {
-                const int sb = t & 1;
-                if (ok) ok = mbar_wait(bar(B_K_FULL + sb), (t >> 1) & 1);
-                // the buffer holds P(t - 2) until its P.V has read it
-                if (ok && t >= 2) ok = mbar_wait(bar(B_S_EMPTY + sb), ((t >> 1) - 1) & 1);
-                ok = __all_sync(0xffffffffu, ok);
-                if (!ok) break;
-                fence_after();
-                if (leader) {
-                    const uint32_t kt = smem_u32(kbuf + sb * BUF);
-#pragma unroll
-                    for (int ks = 0; ks < 8; ++ks)
-                        mma_f16_ts(tmem + TM_S + sb * 128, tmem + TM_Q + 8 * ks,
-                                   sdesc(kt + (ks >> 2) * HALF + (ks & 3) * 32, 16, 1024), ID_QK, ks > 0);
-                    mma_commit(bar(B_S_FULL + sb));
-                    mma_commit(bar(B_K_EMPTY + sb));
-                }
-                __syncwarp();
-            }
-        } else {
-            for (int u = 0; u < n_tiles; ++u) {
-                const int ub = u & 1;
-                ok = mbar_wait(bar(B_V_FULL + ub), (u >> 1) & 1);
-                if (ok) ok = mbar_wait(bar(B_P_FULL + ub), (u >> 1) & 1);
-                ok = __all_sync(0xffffffffu, ok);
-                if (!ok) break;
-                fence_after();
-                if (leader) {
-                    const uint32_t vf = smem_u32(vbuf + ub * BUF);
-#pragma unroll
-                    for (int kk = 0; kk < NK / 16; ++kk)
-                        mma_f16_ts(tmem + TM_O, tmem + TM_S + ub * 128 + 8 * kk, sdesc(vf + kk * 2048, HALF, 1024), ID_PV,
-                                   u > 0 || kk > 0);
-                    mma_commit(bar(B_O_DONE));
-                    mma_commit(bar(B_S_EMPTY + ub));
-                    mma_commit(bar(B_V_EMPTY + ub));
-                    if (u == n_tiles - 1) mma_commit(bar(B_O_FINAL));
-                }
-                __syncwarp();
-            }
-        }
-        // nothing the tensor cores still run may outlive the TMEM allocation
-        if (leader) mma_commit(bar(B_IDLE));
-        __syncwarp();
-        mbar_wait(bar(B_IDLE), 0);
-        __syncwarp();
-    } else if (warp == 3 || warp >= 12) {
-        // ---------------------------------------------------------- widening
-        // items of (key, 32 dims); eight lanes cover four keys x two chunks,
-        // which keeps the 16-byte stores free of bank conflicts
-        const int cw = warp == 3 ? 0 : warp - 11;
-        for (int t = 0; t < n_tiles; ++t) {
-            const int s = t % STAGES, tb = t & 1;
-            ok = mbar_wait(bar(B_STG_FULL + s), (t / STAGES) & 1);
-            if (ok && t >= BUFS) ok = mbar_wait(bar(B_K_EMPTY + tb), ((t >> 1) - 1) & 1);
-            if (!__all_sync(0xffffffffu, ok)) { ok = false; break; }
-            const uint8_t* src = stg + s * STAGE_BYTES;
-            const int rr = ((lane >> 1) & 3) + 4 * (lane >> 4), cc = (lane & 1) + 2 * ((lane >> 3) & 1);
-#pragma unroll 2
-            for (int g = cw; g < NK / 8; g += CONV_WARPS) {
-                const int r = 8 * g + rr;
-                widen_chunk(kbuf + tb * BUF, r, cc, *(const uint4*)(src + r * 64 + cc * 16),
-                            *(const uint16_t*)(src + OFF_KS + r * 8 + 2 * cc));
-            }
-            fence_proxy_async();
-            __syncwarp();
-            if (lane == 0) mbar_arrive(bar(B_K_FULL + tb));
-            if (t >= BUFS) ok = mbar_wait(bar(B_V_EMPTY + tb), ((t >> 1) - 1) & 1);
-            if (!__all_sync(0xffffffffu, ok)) { ok = false; break; }
-            // keys outside every row's range get scale 0: whatever their bytes
-            // are, zeros reach the output
-            const int k0 = k_begin + t * NK;
-            const int zlo = lo0 - k0, zhi = min(min(NK, (n_pages - t * PPT) * PS), hi0 + 1 - k0);
-#pragma unroll 2
-            for (int g = cw; g < NK / 8; g += CONV_WARPS) {
-                const int r = 8 * g + rr;
-                uint32_t sc = *(const uint16_t*)(src + OFF_VS + r * 8 + 2 * cc);
-                if (r < zlo || r >= zhi) sc = 0;
-                widen_chunk(vbuf + tb * BUF, r, cc, *(const uint4*)(src + OFF_V + r * 64 + cc * 16), sc);
-            }
-            fence_proxy_async();
-            __syncwarp();
-            if (lane == 0) {
-                mbar_arrive(bar(B_V_FULL + tb));
-                mbar_arrive(bar(B_STG_EMPTY + s));
-            }
-        }
-    } else {
+    } else if (warp >= 4 && warp < 12) {
+        asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(REGS_SOFTMAX));
         // ------------------------------------------------------------ softmax
         const int wq = warp & 3, half = (warp - 4) >> 2;
         const int r = wq * 32 + lane;
@@ -453,22 +317,34 @@ __global__ void __launch_bounds__(THREADS, 1) attention_int4_tc_kernel(AttnParam
                 const float neg = (m_run == -INFINITY) ? 0.f : BIAS - m_run;
                 // P = 2^(s mult - m + 11) as f16 (masked keys are -inf and give
                 // 0); both halves' S reads are complete (pair barrier above)
-                float sum0 = 0.f, sum1 = 0.f;
-                uint32_t pw[32];
+                const uint32_t p_col = lane_base + TM_S + sb * 128 + 32 * half;
+                uint64_t sum2 = 0;
                 if (!dead) {
+                    const uint64_t mult2 = pack2(mult, mult), neg2 = pack2(neg, neg);
 #pragma unroll
-                    for (int j = 0; j < 32; ++j) {
-                        const float p0 = ex2(fmaf(__uint_as_float(sv[2 * j]), mult, neg));
-                        const float p1 = ex2(fmaf(__uint_as_float(sv[2 * j + 1]), mult, neg));
-                        sum0 += p0;
-                        sum1 += p1;
-                        pw[j] = pack_f16x2(p0, p1);
+                    for (int c = 0; c < 2; ++c) {
+                        uint32_t pw[16];
+#pragma unroll
+                        for (int j = 0; j < 16; ++j) {
+                            float p0, p1;
+                            unpack2(fma2(pack2(__uint_as_float(sv[32 * c + 2 * j]), __uint_as_float(sv[32 * c + 2 * j + 1])),
+                                         mult2, neg2),
+                                    p0, p1);
+                            p0 = ex2(p0);
+                            p1 = ex2(p1);
+                            sum2 = add2(sum2, pack2(p0, p1));
+                            pw[j] = pack_f16x2(p0, p1);
+                        }
+                        tmem_st_x16(p_col + 16 * c, pw);
                     }
                 } else {
+                    uint32_t zero[32];
 #pragma unroll
-                    for (int j = 0; j < 32; ++j) pw[j] = 0u;
+                    for (int j = 0; j < 32; ++j) zero[j] = 0u;
+                    tmem_st_x32(p_col, zero);
                 }
-                tmem_st_x32(lane_base + TM_S + sb * 128 + 32 * half, pw);
+                float sum0, sum1;
+                unpack2(sum2, sum0, sum1);
                 l_run += sum0 + sum1;
                 tmem_wait_st();
             }
@@ -526,6 +402,140 @@ __global__ void __launch_bounds__(THREADS, 1) attention_int4_tc_kernel(AttnParam
                 bulk_wait_read();
                 if (!direct && half == 0)
                     *(float2*)(P.ws_ml + (row_idx * P.num_splits + split) * 2) = make_float2(m_run, l_tot);
+            }
+        }
+    } else {
+        asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(REGS_SERVICE));
+        if (warp == 0) {
+            // ---------------------------------------------------------- producer
+            // lane 4 p + k: copy k (K codes, V codes, K scales, V scales) of page p
+            // of the tile; a page id outside the pool reads as zeros
+            const int32_t* bt = P.block_table + (int64_t)b * P.mpps + page_begin;
+            const int p = lane >> 2, kind = lane & 3;
+            const uint8_t* cache = kind & 1 ? P.v_cache : P.k_cache;
+            const uint32_t bytes = kind < 2 ? PS * kInt4CodeBytes : PS * kInt4ScaleBytes;
+            const uint32_t off = (kind == 0 ? 0 : kind == 1 ? OFF_V : kind == 2 ? OFF_KS : OFF_VS) + p * bytes;
+            int issued = 0;
+            int next = p < PPT && p < n_pages ? bt[p] : -1;
+            for (int t = 0; t < n_tiles; ++t) {
+                const int s = t % STAGES, use = t / STAGES, page = next, at = t * PPT + p;
+                const bool mine = p < PPT && at < n_pages;
+                next = p < PPT && at + PPT < n_pages ? bt[at + PPT] : -1;
+                if (use > 0) ok = mbar_wait(bar(B_STG_EMPTY + s), (use - 1) & 1);
+                if (!__all_sync(0xffffffffu, ok)) break;
+                uint8_t* dst = stg + s * STAGE_BYTES + off;
+                const bool valid = mine && page >= 0 && page < P.num_pages;
+                if (mine && !valid)
+                    for (uint32_t i = 0; i < bytes; i += 16) *(uint4*)(dst + i) = make_uint4(0, 0, 0, 0);
+                uint32_t total = valid ? bytes : 0;
+#pragma unroll
+                for (int o = 16; o >= 1; o >>= 1) total += __shfl_xor_sync(0xffffffffu, total, o);
+                if (lane == 0) mbar_expect_tx(bar(B_STG_FULL + s), total);
+                __syncwarp();
+                if (valid)
+                    bulk_load(smem_u32(dst),
+                              cache + ((int64_t)page * P.Hkv + hk) * (PS * kInt4RowBytes) +
+                                  (kind < 2 ? 0 : PS * kInt4CodeBytes),
+                              bytes, bar(B_STG_FULL + s));
+                issued = t + 1;
+            }
+            // never leave with copies into this CTA's shared memory in flight
+            for (int t = max(0, issued - STAGES); t < issued; ++t) mbar_wait(bar(B_STG_FULL + t % STAGES), (t / STAGES) & 1);
+            __syncwarp();
+        } else if (warp < 3) {
+            // ------------------------------------------------------ MMA issue
+            constexpr uint32_t ID_QK = idesc(128, NK, false), ID_PV = idesc(128, 128, true);
+            const bool leader = elect_one();
+            if (warp == 1) {
+                ok = mbar_wait(bar(B_Q_READY), 0);
+                for (int t = 0; t < n_tiles; ++t) {
+                    const int sb = t & 1;
+                    if (ok) ok = mbar_wait(bar(B_K_FULL + sb), (t >> 1) & 1);
+                    // the buffer holds P(t - 2) until its P.V has read it
+                    if (ok && t >= 2) ok = mbar_wait(bar(B_S_EMPTY + sb), ((t >> 1) - 1) & 1);
+                    ok = __all_sync(0xffffffffu, ok);
+                    if (!ok) break;
+                    fence_after();
+                    if (leader) {
+                        const uint32_t kt = smem_u32(kbuf + sb * BUF);
+#pragma unroll
+                        for (int ks = 0; ks < 8; ++ks)
+                            mma_f16_ts(tmem + TM_S + sb * 128, tmem + TM_Q + 8 * ks,
+                                       sdesc(kt + (ks >> 2) * HALF + (ks & 3) * 32, 16, 1024), ID_QK, ks > 0);
+                        mma_commit(bar(B_S_FULL + sb));
+                        mma_commit(bar(B_K_EMPTY + sb));
+                    }
+                    __syncwarp();
+                }
+            } else {
+                for (int u = 0; u < n_tiles; ++u) {
+                    const int ub = u & 1;
+                    ok = mbar_wait(bar(B_V_FULL + ub), (u >> 1) & 1);
+                    if (ok) ok = mbar_wait(bar(B_P_FULL + ub), (u >> 1) & 1);
+                    ok = __all_sync(0xffffffffu, ok);
+                    if (!ok) break;
+                    fence_after();
+                    if (leader) {
+                        const uint32_t vf = smem_u32(vbuf + ub * BUF);
+#pragma unroll
+                        for (int kk = 0; kk < NK / 16; ++kk)
+                            mma_f16_ts(tmem + TM_O, tmem + TM_S + ub * 128 + 8 * kk, sdesc(vf + kk * 2048, HALF, 1024), ID_PV,
+                                       u > 0 || kk > 0);
+                        mma_commit(bar(B_O_DONE));
+                        mma_commit(bar(B_S_EMPTY + ub));
+                        mma_commit(bar(B_V_EMPTY + ub));
+                        if (u == n_tiles - 1) mma_commit(bar(B_O_FINAL));
+                    }
+                    __syncwarp();
+                }
+            }
+            // nothing the tensor cores still run may outlive the TMEM allocation
+            if (leader) mma_commit(bar(B_IDLE));
+            __syncwarp();
+            mbar_wait(bar(B_IDLE), 0);
+            __syncwarp();
+        } else if (warp >= 12) {
+            // ---------------------------------------------------------- widening
+            // items of (key, 32 dims); eight lanes cover four keys x two chunks,
+            // which keeps the 16-byte stores free of bank conflicts.  A warp has
+            // 16 keys: 8 (cw + 8 u) + ..., u = 0, 1
+            const int cw = warp - 12;
+            const int r0 = 8 * cw + ((lane >> 1) & 3) + 4 * (lane >> 4), cc = (lane & 1) + 2 * ((lane >> 3) & 1);
+            for (int t = 0; t < n_tiles; ++t) {
+                const int s = t % STAGES, tb = t & 1;
+                ok = mbar_wait(bar(B_STG_FULL + s), (t / STAGES) & 1);
+                if (!__all_sync(0xffffffffu, ok)) { ok = false; break; }
+                const uint8_t* src = stg + s * STAGE_BYTES;
+                // keys outside every row's range get V scale 0: whatever their
+                // bytes are, zeros reach the output
+                const int k0 = k_begin + t * NK;
+                const int zlo = lo0 - k0, zhi = min(min(NK, (n_pages - t * PPT) * PS), hi0 + 1 - k0);
+                uint4 kc[2], vc[2];
+                uint32_t ksc[2], vsc[2];
+#pragma unroll
+                for (int u = 0; u < 2; ++u) {
+                    const int r = r0 + 64 * u;
+                    kc[u] = *(const uint4*)(src + r * 64 + cc * 16);
+                    ksc[u] = *(const uint16_t*)(src + OFF_KS + r * 8 + 2 * cc);
+                    vc[u] = *(const uint4*)(src + OFF_V + r * 64 + cc * 16);
+                    vsc[u] = *(const uint16_t*)(src + OFF_VS + r * 8 + 2 * cc);
+                    if (r < zlo || r >= zhi) vsc[u] = 0;
+                }
+                if (t >= BUFS) ok = mbar_wait(bar(B_K_EMPTY + tb), ((t >> 1) - 1) & 1);
+                if (!__all_sync(0xffffffffu, ok)) { ok = false; break; }
+                if (lane == 0) mbar_arrive(bar(B_STG_EMPTY + s));       // the stage is in registers
+#pragma unroll
+                for (int u = 0; u < 2; ++u) widen_chunk(kbuf + tb * BUF, r0 + 64 * u, cc, kc[u], ksc[u]);
+                fence_proxy_async();
+                __syncwarp();
+                if (lane == 0) mbar_arrive(bar(B_K_FULL + tb));
+                if (t >= BUFS) ok = mbar_wait(bar(B_V_EMPTY + tb), ((t >> 1) - 1) & 1);
+                if (!__all_sync(0xffffffffu, ok)) { ok = false; break; }
+#pragma unroll
+                for (int u = 0; u < 2; ++u) widen_chunk(vbuf + tb * BUF, r0 + 64 * u, cc, vc[u], vsc[u]);
+                fence_proxy_async();
+                __syncwarp();
+                if (lane == 0) mbar_arrive(bar(B_V_FULL + tb));
             }
         }
     }

@@ -24,12 +24,19 @@ struct Scale2 {
 __device__ __forceinline__ Scale2 scale2(uint32_t s) {
     return {hmul2(s, 0x34003400u), hmul2(s, 0xd420d420u), hmul2(s, 0xc600c600u)};
 }
+// (z & mask) | base as one instruction: written with the operators it becomes
+// two, 39 arithmetic-logic operations for 32 codes instead of 24.
+__device__ __forceinline__ uint32_t and_or(uint32_t z, uint32_t mask, uint32_t base) {
+    uint32_t r;
+    asm("lop3.b32 %0, %1, %2, %3, 0xea;" : "=r"(r) : "r"(z), "r"(mask), "r"(base));
+    return r;
+}
 __device__ __forceinline__ void widen4(uint32_t z, const Scale2& k, uint32_t (&v)[4]) {
     const uint32_t x = z << 2, y = z >> 6;
-    v[0] = hfma2((x & 0x003c003cu) | 0x5c005c00u, k.s, k.c256);
-    v[1] = hfma2((x & 0x03c003c0u) | 0x4c004c00u, k.s, k.c16);
-    v[2] = hfma2((y & 0x003c003cu) | 0x5c005c00u, k.s, k.c256);
-    v[3] = hfma2((y & 0x03c003c0u) | 0x4c004c00u, k.s, k.c16);
+    v[0] = hfma2(and_or(x, 0x003c003cu, 0x5c005c00u), k.s, k.c256);
+    v[1] = hfma2(and_or(x, 0x03c003c0u, 0x4c004c00u), k.s, k.c16);
+    v[2] = hfma2(and_or(y, 0x003c003cu, 0x5c005c00u), k.s, k.c256);
+    v[3] = hfma2(and_or(y, 0x03c003c0u, 0x4c004c00u), k.s, k.c16);
 }
 
 }  // namespace fp8kv

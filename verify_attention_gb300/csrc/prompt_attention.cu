@@ -96,13 +96,6 @@ constexpr uint32_t ID_QK = idesc(128, NK, false) | (1u << 7) | (1u << 10);
 constexpr uint32_t ID_QK_HALF = idesc(128, NK / 2, false) | (1u << 7) | (1u << 10);
 constexpr uint32_t ID_PV = idesc(128, 128, true) | (1u << 7) | (1u << 10);
 
-// One thread of the (converged) warp, the same one every time.
-__device__ __forceinline__ bool elect_one() {
-    uint32_t r;
-    asm volatile("{ .reg .pred p; elect.sync _|p, 0xffffffff; selp.u32 %0, 1, 0, p; }" : "=r"(r));
-    return r != 0;
-}
-
 // Shared-memory matrix descriptor from its low word (see sdesc: address and
 // leading offset) with a stride of 1024 bytes and the 128-byte swizzle.
 __device__ __forceinline__ uint32_t desc_lo(uint32_t saddr, uint32_t lbo) {
@@ -129,31 +122,6 @@ __device__ __forceinline__ void tma_store_3d(const CUtensorMap* tm, uint32_t src
     asm volatile("cp.async.bulk.tensor.3d.global.shared::cta.tile.bulk_group [%0, {%2, %3, %4}], [%1];" ::"l"(tm),
                  "r"(src), "r"(x), "r"(y), "r"(z)
                  : "memory");
-}
-
-__device__ __forceinline__ uint64_t pack2(float lo, float hi) {
-    uint64_t r;
-    asm("mov.b64 %0, {%1, %2};" : "=l"(r) : "f"(lo), "f"(hi));
-    return r;
-}
-__device__ __forceinline__ void unpack2(uint64_t v, float& lo, float& hi) {
-    asm("mov.b64 {%0, %1}, %2;" : "=f"(lo), "=f"(hi) : "l"(v));
-}
-__device__ __forceinline__ uint64_t fma2(uint64_t a, uint64_t b, uint64_t c) {
-    uint64_t r;
-    asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(r) : "l"(a), "l"(b), "l"(c));
-    return r;
-}
-__device__ __forceinline__ uint64_t add2(uint64_t a, uint64_t b) {
-    uint64_t r;
-    asm("add.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
-    return r;
-}
-
-__device__ __forceinline__ float max3(float a, float b, float c) {
-    float r;
-    asm("max.f32 %0, %1, %2, %3;" : "=f"(r) : "f"(a), "f"(b), "f"(c));
-    return r;
 }
 
 // Ask for a CTA of this grid that has not started to be cancelled; the answer
