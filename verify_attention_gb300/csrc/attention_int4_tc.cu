@@ -16,18 +16,21 @@
 // One CTA per (partition, row tile x KV head, sequence), 20 warps:
 //   warp 0           loads pages (bulk copies of the codes and of the scales of
 //                    a (page, head)) into a ring of 128-key stages
-//   warp 1           issues Q.K^T (one thread), S double-buffered
-//   warp 2           issues P.V
+//   warps 1, 2       issue the MMAs of the first and of the second half (64 keys)
+//                    of every tile: S = Q.K^T, then O += P.V
+//   warps 4-7, 8-11  softmax of the first and of the second half, a row per
+//                    thread (warps 4+q and 8+q: TMEM lane quarter q).  Each half
+//                    keeps its own maximum, sum and O, merged at the end, so the
+//                    two never wait for each other and one half's products run
+//                    during the other's softmax.  (One softmax over both, its
+//                    maximum exchanged through shared memory for every tile,
+//                    took 2800 cycles a tile.)  O is rescaled when a row's
+//                    maximum grows by more than 2^4; the weights are held as
+//                    2^11 times 2^(x - m), at most 2^15, so that f16 keeps 11
+//                    bits of every weight down to 2^-25 of the largest.
 //   warps 12-19      widen K and V into swizzled f16 tiles (five warps took 3700
 //                    cycles a tile)
-//   warps 4-11       softmax: warps 4+q and 8+q share TMEM lane quarter q (32
-//                    rows, one per thread) and split the 128 columns in halves;
-//                    a tile's row maximum is exchanged through shared memory.
-//                    O is rescaled when a row's maximum grows by more than 2^4;
-//                    the weights are held as 2^11 times 2^(x - m), at most 2^15,
-//                    so that f16 keeps 11 bits of every weight down to 2^-25 of
-//                    the largest.
-// TMEM columns: Q 0-63, S/P 2 x 128 (64-319), O 320-447.
+// TMEM columns: Q 0-63, S/P of the halves 64-127, 128-191, O 192-319, 320-447.
 #include <stdio.h>
 
 #include <mutex>
@@ -46,21 +49,21 @@ int status_attention_int4_tc(unsigned int* s, int clear) { return read_status(s,
 namespace i4tc {
 
 constexpr int NK = 128;                                 // keys per tile
-constexpr int STAGES = 4;
+constexpr int STAGES = 3;
 constexpr int OFF_V = NK * kInt4CodeBytes;              // of a stage: K codes, V codes, K scales, V scales
 constexpr int OFF_KS = 2 * NK * kInt4CodeBytes;
 constexpr int OFF_VS = OFF_KS + NK * kInt4ScaleBytes;
 constexpr int STAGE_BYTES = OFF_VS + NK * kInt4ScaleBytes;
-constexpr int BUFS = 2;                                 // widened K tiles, and V tiles
+constexpr int KBUFS = 2, VBUFS = 3;                     // widened tiles
 constexpr int BUF = NK * 256, HALF = BUF / 2;           // two blocks of 128 keys x 64 dims (128-byte swizzled)
-constexpr int XCH_BYTES = 3 * 2 * 128 * 4;              // [tile parity 0, 1, row sums][half][row]
-constexpr int SMEM = 2 * BUFS * BUF + STAGES * STAGE_BYTES + XCH_BYTES + 1024 + 512;
+constexpr int XCH_BYTES = 2 * 128 * 8;                  // (max, sum) of [half][row]
+constexpr int SMEM = (KBUFS + VBUFS) * BUF + STAGES * STAGE_BYTES + XCH_BYTES + 1024 + 512;
 constexpr int EPI_STRIDE = 144;                         // staged half row (128 bytes), padded against bank conflicts
-static_assert(2 * 128 * EPI_STRIDE <= 2 * BUFS * BUF, "epilogue staging exceeds the widened tiles");
-constexpr uint32_t TM_Q = 0, TM_S = 64, TM_O = 320, TM_COLS = 512;
+static_assert(2 * 128 * EPI_STRIDE <= (KBUFS + VBUFS) * BUF, "epilogue staging exceeds the widened tiles");
+constexpr uint32_t TM_Q = 0, TM_S = 64, TM_O = 192, TM_COLS = 512;
 constexpr int WARPS = 20, THREADS = WARPS * 32, CONV_WARPS = 8;
-// registers: 640 x 96 at launch = 128 x (3 x 80 + 2 x 120) after the split
-constexpr int REGS_SERVICE = 80, REGS_SOFTMAX = 120;
+// registers: 640 x 96 at launch = 128 x (3 x 72 + 2 x 128) after the split
+constexpr int REGS_SERVICE = 72, REGS_SOFTMAX = 128;
 static_assert(128 * (3 * REGS_SERVICE + 2 * REGS_SOFTMAX) <= THREADS * 96, "register split above the launch's share");
 constexpr float GROW = 4.0f, BIAS = 11.0f;              // see the head of the file
 
@@ -68,15 +71,14 @@ enum {
     B_STG_FULL = 0,
     B_STG_EMPTY = B_STG_FULL + STAGES,
     B_K_FULL = B_STG_EMPTY + STAGES,
-    B_K_EMPTY = B_K_FULL + BUFS,
-    B_V_FULL = B_K_EMPTY + BUFS,
-    B_V_EMPTY = B_V_FULL + BUFS,
-    B_S_FULL = B_V_EMPTY + BUFS,
-    B_S_EMPTY = B_S_FULL + 2,                           // P.V over this S buffer's P complete
-    B_P_FULL = B_S_EMPTY + 2,
-    B_O_DONE = B_P_FULL + 2,
-    B_O_FINAL = B_O_DONE + 1,
-    B_Q_READY = B_O_FINAL + 1,
+    B_K_EMPTY = B_K_FULL + KBUFS,
+    B_V_FULL = B_K_EMPTY + KBUFS,
+    B_V_EMPTY = B_V_FULL + VBUFS,
+    B_S = B_V_EMPTY + VBUFS,                             // per half: S ready
+    B_P = B_S + 2,                                      // per half: P written
+    B_O = B_P + 2,                                      // per half: O final
+    B_TURN = B_O + 2,                                   // per half: its MMA warp's turn
+    B_Q_READY = B_TURN + 2,
     B_IDLE = B_Q_READY + 1,
     B_PAIR = B_IDLE + 1,                                // per TMEM lane quarter: its two softmax warps
     B_COUNT = B_PAIR + 4
@@ -89,18 +91,20 @@ __device__ __forceinline__ void bulk_load(uint32_t dst, const void* src, uint32_
                  : "memory");
 }
 
-// 32 codes (16 bytes, two blocks) of row r, widened into a tile: dims 32 c ...
-// of the row, 16-byte units of its two 128-byte rows swizzled by the row.
-__device__ __forceinline__ void widen_chunk(uint8_t* tile, int r, int c, uint4 codes, uint32_t scales) {
+// 32 codes (16 bytes, two blocks), widened into four 16-byte units of shared
+// memory at `at[u]` + off.
+template <int OFF>
+__device__ __forceinline__ void widen_chunk(const uint32_t (&at)[4], uint4 codes, uint32_t scales) {
     const uint32_t s2 = e4m3x2_to_f16x2(scales);
     const Scale2 sa = scale2(prmt(s2, s2, 0x1010)), sb = scale2(prmt(s2, s2, 0x3232));
     const uint32_t w[4] = {codes.x, codes.y, codes.z, codes.w};
-    uint8_t* row = tile + (c >> 1) * HALF + r * 128;
 #pragma unroll
     for (int u = 0; u < 4; ++u) {
         uint32_t v[4];
         widen4(w[u], u < 2 ? sa : sb, v);
-        *(uint4*)(row + (((4 * (c & 1) + u) ^ (r & 7)) << 4)) = make_uint4(v[0], v[1], v[2], v[3]);
+        asm volatile("st.shared.v4.b32 [%0 + %5], {%1, %2, %3, %4};" ::"r"(at[u]), "r"(v[0]), "r"(v[1]), "r"(v[2]),
+                     "r"(v[3]), "n"(OFF)
+                     : "memory");
     }
 }
 
@@ -108,9 +112,9 @@ template <int PS>
 __global__ void __launch_bounds__(THREADS, 1) attention_int4_tc_kernel(AttnParams P) {
     extern __shared__ uint8_t smem_raw[];
     uint8_t* smem = (uint8_t*)(((uintptr_t)smem_raw + 1023) & ~(uintptr_t)1023);
-    uint8_t* kbuf = smem;                                   // BUFS x 32 KiB
-    uint8_t* vbuf = kbuf + BUFS * BUF;                      // BUFS x 32 KiB
-    uint8_t* stg = vbuf + BUFS * BUF;                       // STAGES x 18 KiB
+    uint8_t* kbuf = smem;                                   // KBUFS x 32 KiB
+    uint8_t* vbuf = kbuf + KBUFS * BUF;                     // VBUFS x 32 KiB
+    uint8_t* stg = vbuf + VBUFS * BUF;                      // STAGES x 18 KiB
     float* xch = (float*)(stg + STAGES * STAGE_BYTES);
     uint64_t* bars = (uint64_t*)((uint8_t*)xch + XCH_BYTES);
     uint32_t* tmem_slot = (uint32_t*)(bars + B_COUNT);
@@ -125,7 +129,9 @@ __global__ void __launch_bounds__(THREADS, 1) attention_int4_tc_kernel(AttnParam
         for (int i = 0; i < B_COUNT; ++i) {
             int count = 1;
             if ((i >= B_STG_EMPTY && i < B_K_EMPTY) || (i >= B_V_FULL && i < B_V_EMPTY)) count = CONV_WARPS;
-            if ((i >= B_P_FULL && i < B_O_DONE) || i == B_Q_READY) count = 8;
+            if ((i >= B_K_EMPTY && i < B_V_FULL) || (i >= B_V_EMPTY && i < B_S)) count = 2;    // MMA warps
+            if (i >= B_P && i < B_O) count = 4;
+            if (i == B_Q_READY) count = 8;
             if (i == B_IDLE || i >= B_PAIR) count = 2;
             mbar_init(bar(i), count);
         }
@@ -248,64 +254,57 @@ __global__ void __launch_bounds__(THREADS, 1) attention_int4_tc_kernel(AttnParam
             pmax = max(pmax, __shfl_xor_sync(0xffffffffu, pmax, off));
             lomin = min(lomin, __shfl_xor_sync(0xffffffffu, lomin, off));
         }
-        float m_run = -INFINITY, l_run = 0.f;               // l_run: this half's columns only
+        // this half's maximum and sum
+        float m_run = -INFINITY, l_run = 0.f;
+        const uint32_t s_col = lane_base + TM_S + 64 * half, o_col = lane_base + TM_O + 128 * half;
         for (int t = 0; t < n_tiles && ok; ++t) {
-            const int sb = t & 1;
-            ok = __all_sync(0xffffffffu, mbar_wait(bar(B_S_FULL + sb), (t >> 1) & 1));
+            ok = __all_sync(0xffffffffu, mbar_wait(bar(B_S + half), t & 1));
             if (!ok) break;
             fence_after();
-            if (active) {
-                const int k0 = k_begin + t * NK + 64 * half;   // first key of this half
-                const bool dead = k0 > pmax || k0 + 63 < lomin;   // no row of this warp sees any: P = 0
+            const int k0 = k_begin + t * NK + 64 * half;    // first key of this half
+            if (!active || k0 > pmax || k0 + 63 < lomin) {
+                // no row of this warp sees any key of it: P = 0
+                uint32_t zero[32];
+#pragma unroll
+                for (int j = 0; j < 32; ++j) zero[j] = 0u;
+                tmem_st_x32(s_col, zero);
+            } else {
                 uint32_t sv[64];
-                float hmax = -INFINITY;
-                if (!dead) {
-                    tmem_ld_x64(lane_base + TM_S + sb * 128 + 64 * half, sv);
-                    tmem_wait_ld();
-                    if (k0 + 63 > pmin || k0 < lomax) {
-                        // this row's visible columns of the half as bits
-                        const int jlo = max(0, lo_r - k0), jhi = min(64, p_r - k0 + 1);
-                        const uint64_t below_hi = jhi <= 0 ? 0ull : (jhi >= 64 ? ~0ull : (1ull << jhi) - 1);
-                        const uint64_t below_lo = jlo >= 64 ? ~0ull : (1ull << jlo) - 1;
-                        const uint64_t vis = below_hi & ~below_lo;
-                        const uint32_t vis_lo = (uint32_t)vis, vis_hi = (uint32_t)(vis >> 32);
+                tmem_ld_x64(s_col, sv);
+                tmem_wait_ld();
+                if (k0 + 63 > pmin || k0 < lomax) {
+                    // this row's visible columns of the half as bits
+                    const int jlo = max(0, lo_r - k0), jhi = min(64, p_r - k0 + 1);
+                    const uint64_t below_hi = jhi <= 0 ? 0ull : (jhi >= 64 ? ~0ull : (1ull << jhi) - 1);
+                    const uint64_t below_lo = jlo >= 64 ? ~0ull : (1ull << jlo) - 1;
+                    const uint64_t vis = below_hi & ~below_lo;
+                    const uint32_t vis_lo = (uint32_t)vis, vis_hi = (uint32_t)(vis >> 32);
 #pragma unroll
-                        for (int j = 0; j < 64; ++j)
-                            sv[j] = (((j < 32 ? vis_lo : vis_hi) >> (j & 31)) & 1u) ? sv[j] : 0xff800000u;   // -inf
-                    }
-                    float m4[4];
-#pragma unroll
-                    for (int c = 0; c < 4; ++c) {
-                        m4[c] = max3(__uint_as_float(sv[c]), __uint_as_float(sv[c + 4]), __uint_as_float(sv[c + 8]));
-#pragma unroll
-                        for (int u = c + 12; u < 60; u += 8)
-                            m4[c] = max3(m4[c], __uint_as_float(sv[u]), __uint_as_float(sv[u + 4]));
-                        m4[c] = fmaxf(m4[c], __uint_as_float(sv[60 + c]));
-                    }
-                    hmax = max3(m4[0], m4[1], fmaxf(m4[2], m4[3]));
+                    for (int j = 0; j < 64; ++j)
+                        sv[j] = (((j < 32 ? vis_lo : vis_hi) >> (j & 31)) & 1u) ? sv[j] : 0xff800000u;   // -inf
                 }
-                // exchange with the partner warp (phase t + 1 of the pair barrier)
-                xch[(sb * 2 + half) * 128 + r] = hmax;
-                __syncwarp();
-                if (lane == 0) mbar_arrive(bar(B_PAIR + wq));
-                ok = __all_sync(0xffffffffu, mbar_wait(bar(B_PAIR + wq), (t + 1) & 1));
-                if (!ok) break;
-                const float tmax = fmaxf(xch[sb * 256 + r], xch[sb * 256 + 128 + r]) * mult;
+                float m4[4];
+#pragma unroll
+                for (int c = 0; c < 4; ++c) {
+                    m4[c] = max3(__uint_as_float(sv[c]), __uint_as_float(sv[c + 4]), __uint_as_float(sv[c + 8]));
+#pragma unroll
+                    for (int u = c + 12; u < 60; u += 8)
+                        m4[c] = max3(m4[c], __uint_as_float(sv[u]), __uint_as_float(sv[u + 4]));
+                    m4[c] = fmaxf(m4[c], __uint_as_float(sv[60 + c]));
+                }
+                const float tmax = max3(m4[0], m4[1], fmaxf(m4[2], m4[3])) * mult;
                 const bool rescale = (m_run != -INFINITY) && (tmax > m_run + GROW);
                 if (__any_sync(0xffffffffu, rescale)) {
-                    // O holds P.V up to tile t - 1: wait for it, then rescale this half
-                    ok = __all_sync(0xffffffffu, mbar_wait(bar(B_O_DONE), (t - 1) & 1));
-                    if (!ok) break;
-                    fence_after();
+                    // S(t) ready means that this half's P.V up to t - 1 is complete
                     const float alpha = rescale ? ex2(m_run - tmax) : 1.0f;
 #pragma unroll 1
-                    for (int c = 0; c < 64; c += 32) {
+                    for (int c = 0; c < 128; c += 32) {
                         uint32_t ov[32];
-                        tmem_ld_x32(lane_base + TM_O + 64 * half + c, ov);
+                        tmem_ld_x32(o_col + c, ov);
                         tmem_wait_ld();
 #pragma unroll
                         for (int j = 0; j < 32; ++j) ov[j] = __float_as_uint(__uint_as_float(ov[j]) * alpha);
-                        tmem_st_x32(lane_base + TM_O + 64 * half + c, ov);
+                        tmem_st_x32(o_col + c, ov);
                     }
                     tmem_wait_st();
                     if (rescale) {
@@ -314,76 +313,73 @@ __global__ void __launch_bounds__(THREADS, 1) attention_int4_tc_kernel(AttnParam
                     }
                 }
                 if (m_run == -INFINITY) m_run = tmax;
+                // P = 2^(s mult - m + 11) as f16 (masked keys are -inf and give 0)
                 const float neg = (m_run == -INFINITY) ? 0.f : BIAS - m_run;
-                // P = 2^(s mult - m + 11) as f16 (masked keys are -inf and give
-                // 0); both halves' S reads are complete (pair barrier above)
-                const uint32_t p_col = lane_base + TM_S + sb * 128 + 32 * half;
+                const uint64_t mult2 = pack2(mult, mult), neg2 = pack2(neg, neg);
                 uint64_t sum2 = 0;
-                if (!dead) {
-                    const uint64_t mult2 = pack2(mult, mult), neg2 = pack2(neg, neg);
 #pragma unroll
-                    for (int c = 0; c < 2; ++c) {
-                        uint32_t pw[16];
+                for (int c = 0; c < 2; ++c) {
+                    uint32_t pw[16];
 #pragma unroll
-                        for (int j = 0; j < 16; ++j) {
-                            float p0, p1;
-                            unpack2(fma2(pack2(__uint_as_float(sv[32 * c + 2 * j]), __uint_as_float(sv[32 * c + 2 * j + 1])),
-                                         mult2, neg2),
-                                    p0, p1);
-                            p0 = ex2(p0);
-                            p1 = ex2(p1);
-                            sum2 = add2(sum2, pack2(p0, p1));
-                            pw[j] = pack_f16x2(p0, p1);
-                        }
-                        tmem_st_x16(p_col + 16 * c, pw);
+                    for (int j = 0; j < 16; ++j) {
+                        float p0, p1;
+                        unpack2(fma2(pack2(__uint_as_float(sv[32 * c + 2 * j]), __uint_as_float(sv[32 * c + 2 * j + 1])),
+                                     mult2, neg2),
+                                p0, p1);
+                        p0 = ex2(p0);
+                        p1 = ex2(p1);
+                        sum2 = add2(sum2, pack2(p0, p1));
+                        pw[j] = pack_f16x2(p0, p1);
                     }
-                } else {
-                    uint32_t zero[32];
-#pragma unroll
-                    for (int j = 0; j < 32; ++j) zero[j] = 0u;
-                    tmem_st_x32(p_col, zero);
+                    tmem_st_x16(s_col + 16 * c, pw);
                 }
                 float sum0, sum1;
                 unpack2(sum2, sum0, sum1);
                 l_run += sum0 + sum1;
-                tmem_wait_st();
             }
+            tmem_wait_st();
             fence_before();
             __syncwarp();
-            if (lane == 0) mbar_arrive(bar(B_P_FULL + sb));
+            if (lane == 0) mbar_arrive(bar(B_P + half));
         }
         // ------------------------------------------------------------ epilogue
-        if (ok) ok = mbar_wait(bar(B_O_FINAL), 0);
+        // both halves' O and (max, sum); this thread merges 64 dims of its row
+        for (int h = 0; h < 2; ++h)
+            if (ok) ok = mbar_wait(bar(B_O + h), 0);
+        float2* ml = (float2*)xch;
+        ml[half * 128 + r] = make_float2(m_run, l_run);
+        __syncwarp();
+        if (lane == 0) mbar_arrive(bar(B_PAIR + wq));
+        if (ok) ok = mbar_wait(bar(B_PAIR + wq), 1);
         ok = __all_sync(0xffffffffu, ok);
         if (ok && active) {
             fence_after();
-            // row sums of both halves: the next phase of the pair barrier
-            xch[(4 + half) * 128 + r] = l_run;
-            __syncwarp();
-            if (lane == 0) mbar_arrive(bar(B_PAIR + wq));
-            ok = __all_sync(0xffffffffu, mbar_wait(bar(B_PAIR + wq), (n_tiles + 1) & 1));
-        }
-        if (ok && active) {
-            const float l_tot = xch[4 * 128 + r] + xch[5 * 128 + r];
+            const float2 a = ml[r], z = ml[128 + r];
+            const float m_tot = fmaxf(a.x, z.x);
+            const float wa = a.x == -INFINITY ? 0.f : ex2(a.x - m_tot), wz = z.x == -INFINITY ? 0.f : ex2(z.x - m_tot);
+            const float l_tot = a.y * wa + z.y * wz;
             const bool direct = nsplit_b == 1;
             // direct: bf16 of 4 v_scale O / l; partial: f16 of 4 O / l (|x| <=
             // 7 * 448) beside its (max, sum); a row with no visible key here
             // has l = 0: weight 0, values 0
             const float f = direct ? vs / l_tot : (l_tot > 0.f ? 4.0f / l_tot : 0.f);
+            const float fa = wa * f, fz = wz * f;
             // the half row goes through shared memory (the widened tiles are
             // free) to one bulk copy
             uint8_t* row_stage = kbuf + (half * 128 + r) * EPI_STRIDE;
 #pragma unroll 1
             for (int c = 0; c < 64; c += 32) {
-                uint32_t ov[32];
-                tmem_ld_x32(lane_base + TM_O + 64 * half + c, ov);
+                uint32_t oa[32], oz[32];
+                tmem_ld_x32(lane_base + TM_O + 64 * half + c, oa);
+                tmem_ld_x32(lane_base + TM_O + 128 + 64 * half + c, oz);
                 tmem_wait_ld();
                 uint4* dst = (uint4*)(row_stage + c * 2);
 #pragma unroll
                 for (int v4 = 0; v4 < 4; ++v4) {
                     float x[8];
 #pragma unroll
-                    for (int i = 0; i < 8; ++i) x[i] = __uint_as_float(ov[8 * v4 + i]) * f;
+                    for (int i = 0; i < 8; ++i)
+                        x[i] = __uint_as_float(oa[8 * v4 + i]) * fa + __uint_as_float(oz[8 * v4 + i]) * fz;
                     // columns 0 4 1 5 2 6 3 7 back in order
                     dst[v4] = direct ? make_uint4(pack_bf16x2(x[0], x[2]), pack_bf16x2(x[4], x[6]),
                                                   pack_bf16x2(x[1], x[3]), pack_bf16x2(x[5], x[7]))
@@ -401,7 +397,7 @@ __global__ void __launch_bounds__(THREADS, 1) attention_int4_tc_kernel(AttnParam
                 bulk_commit();
                 bulk_wait_read();
                 if (!direct && half == 0)
-                    *(float2*)(P.ws_ml + (row_idx * P.num_splits + split) * 2) = make_float2(m_run, l_tot);
+                    *(float2*)(P.ws_ml + (row_idx * P.num_splits + split) * 2) = make_float2(m_tot, l_tot);
             }
         }
     } else {
@@ -444,50 +440,43 @@ __global__ void __launch_bounds__(THREADS, 1) attention_int4_tc_kernel(AttnParam
             __syncwarp();
         } else if (warp < 3) {
             // ------------------------------------------------------ MMA issue
-            constexpr uint32_t ID_QK = idesc(128, NK, false), ID_PV = idesc(128, 128, true);
+            constexpr uint32_t ID_QK = idesc(128, NK / 2, false), ID_PV = idesc(128, 128, true);
             const bool leader = elect_one();
-            if (warp == 1) {
-                ok = mbar_wait(bar(B_Q_READY), 0);
-                for (int t = 0; t < n_tiles; ++t) {
-                    const int sb = t & 1;
-                    if (ok) ok = mbar_wait(bar(B_K_FULL + sb), (t >> 1) & 1);
-                    // the buffer holds P(t - 2) until its P.V has read it
-                    if (ok && t >= 2) ok = mbar_wait(bar(B_S_EMPTY + sb), ((t >> 1) - 1) & 1);
-                    ok = __all_sync(0xffffffffu, ok);
-                    if (!ok) break;
-                    fence_after();
-                    if (leader) {
-                        const uint32_t kt = smem_u32(kbuf + sb * BUF);
+            const int half = warp - 1;
+            const uint32_t s_col = tmem + TM_S + 64 * half, o_col = tmem + TM_O + 128 * half;
+            const uint32_t k_lo = desc_lo(smem_u32(kbuf) + half * (64 * 128), 16);
+            const uint32_t v_lo = desc_lo(smem_u32(vbuf) + half * (64 * 128), HALF);
+            ok = mbar_wait(bar(B_Q_READY), 0);
+            for (int t = 0; t <= n_tiles; ++t) {
+                const int tb = t & 1, ub = (t + VBUFS - 1) % VBUFS;     // K buffer of this tile, V of the one before
+                if (ok && t < n_tiles) ok = mbar_wait(bar(B_K_FULL + tb), (t >> 1) & 1);
+                if (ok && t > 0) ok = mbar_wait(bar(B_V_FULL + ub), ((t - 1) / VBUFS) & 1);
+                if (ok && t > 0) ok = mbar_wait(bar(B_P + half), (t - 1) & 1);
+                if (ok && (half == 1 || t > 0)) ok = mbar_wait(bar(B_TURN + half), (half == 1 ? t : t - 1) & 1);
+                ok = __all_sync(0xffffffffu, ok);
+                if (!ok) break;
+                fence_after();
+                if (leader) {
+                    if (t > 0) {
+                        // O += P(t - 1) V(t - 1), 64 keys
+#pragma unroll
+                        for (int kk = 0; kk < 4; ++kk)
+                            mma_ts(o_col, s_col + 8 * kk, v_lo + ((ub * BUF + kk * 2048) >> 4), ID_PV, t > 1 || kk > 0);
+                    }
+                    if (t < n_tiles) {
+                        // S = Q K(t)^T over P(t - 1), which the MMAs above have read
 #pragma unroll
                         for (int ks = 0; ks < 8; ++ks)
-                            mma_f16_ts(tmem + TM_S + sb * 128, tmem + TM_Q + 8 * ks,
-                                       sdesc(kt + (ks >> 2) * HALF + (ks & 3) * 32, 16, 1024), ID_QK, ks > 0);
-                        mma_commit(bar(B_S_FULL + sb));
-                        mma_commit(bar(B_K_EMPTY + sb));
+                            mma_ts(s_col, tmem + TM_Q + 8 * ks,
+                                   k_lo + ((tb * BUF + (ks >> 2) * HALF + (ks & 3) * 32) >> 4), ID_QK, ks > 0);
+                        mma_commit(bar(B_S + half));
                     }
-                    __syncwarp();
+                    mbar_arrive(bar(B_TURN + 1 - half));
+                    if (t < n_tiles) mma_commit(bar(B_K_EMPTY + tb));
+                    if (t > 0) mma_commit(bar(B_V_EMPTY + ub));
+                    if (t == n_tiles) mma_commit(bar(B_O + half));
                 }
-            } else {
-                for (int u = 0; u < n_tiles; ++u) {
-                    const int ub = u & 1;
-                    ok = mbar_wait(bar(B_V_FULL + ub), (u >> 1) & 1);
-                    if (ok) ok = mbar_wait(bar(B_P_FULL + ub), (u >> 1) & 1);
-                    ok = __all_sync(0xffffffffu, ok);
-                    if (!ok) break;
-                    fence_after();
-                    if (leader) {
-                        const uint32_t vf = smem_u32(vbuf + ub * BUF);
-#pragma unroll
-                        for (int kk = 0; kk < NK / 16; ++kk)
-                            mma_f16_ts(tmem + TM_O, tmem + TM_S + ub * 128 + 8 * kk, sdesc(vf + kk * 2048, HALF, 1024), ID_PV,
-                                       u > 0 || kk > 0);
-                        mma_commit(bar(B_O_DONE));
-                        mma_commit(bar(B_S_EMPTY + ub));
-                        mma_commit(bar(B_V_EMPTY + ub));
-                        if (u == n_tiles - 1) mma_commit(bar(B_O_FINAL));
-                    }
-                    __syncwarp();
-                }
+                __syncwarp();
             }
             // nothing the tensor cores still run may outlive the TMEM allocation
             if (leader) mma_commit(bar(B_IDLE));
@@ -501,8 +490,14 @@ __global__ void __launch_bounds__(THREADS, 1) attention_int4_tc_kernel(AttnParam
             // 16 keys: 8 (cw + 8 u) + ..., u = 0, 1
             const int cw = warp - 12;
             const int r0 = 8 * cw + ((lane >> 1) & 3) + 4 * (lane >> 4), cc = (lane & 1) + 2 * ((lane >> 3) & 1);
+            // where the four 16-byte units of row r0's chunk go in a tile
+            // (swizzled by the row; row r0 + 64 is 8 KiB further)
+            uint32_t at[4];
+#pragma unroll
+            for (int u = 0; u < 4; ++u)
+                at[u] = smem_u32(kbuf) + (cc >> 1) * HALF + r0 * 128 + (((4 * (cc & 1) + u) ^ (r0 & 7)) << 4);
             for (int t = 0; t < n_tiles; ++t) {
-                const int s = t % STAGES, tb = t & 1;
+                const int s = t % STAGES, tb = t % KBUFS, vb = t % VBUFS;
                 ok = mbar_wait(bar(B_STG_FULL + s), (t / STAGES) & 1);
                 if (!__all_sync(0xffffffffu, ok)) { ok = false; break; }
                 const uint8_t* src = stg + s * STAGE_BYTES;
@@ -521,21 +516,26 @@ __global__ void __launch_bounds__(THREADS, 1) attention_int4_tc_kernel(AttnParam
                     vsc[u] = *(const uint16_t*)(src + OFF_VS + r * 8 + 2 * cc);
                     if (r < zlo || r >= zhi) vsc[u] = 0;
                 }
-                if (t >= BUFS) ok = mbar_wait(bar(B_K_EMPTY + tb), ((t >> 1) - 1) & 1);
+                if (t >= KBUFS) ok = mbar_wait(bar(B_K_EMPTY + tb), (t / KBUFS - 1) & 1);
                 if (!__all_sync(0xffffffffu, ok)) { ok = false; break; }
                 if (lane == 0) mbar_arrive(bar(B_STG_EMPTY + s));       // the stage is in registers
+                uint32_t to[4];
 #pragma unroll
-                for (int u = 0; u < 2; ++u) widen_chunk(kbuf + tb * BUF, r0 + 64 * u, cc, kc[u], ksc[u]);
+                for (int u = 0; u < 4; ++u) to[u] = at[u] + tb * BUF;
+                widen_chunk<0>(to, kc[0], ksc[0]);
+                widen_chunk<64 * 128>(to, kc[1], ksc[1]);
                 fence_proxy_async();
                 __syncwarp();
                 if (lane == 0) mbar_arrive(bar(B_K_FULL + tb));
-                if (t >= BUFS) ok = mbar_wait(bar(B_V_EMPTY + tb), ((t >> 1) - 1) & 1);
+                if (t >= VBUFS) ok = mbar_wait(bar(B_V_EMPTY + vb), (t / VBUFS - 1) & 1);
                 if (!__all_sync(0xffffffffu, ok)) { ok = false; break; }
 #pragma unroll
-                for (int u = 0; u < 2; ++u) widen_chunk(vbuf + tb * BUF, r0 + 64 * u, cc, vc[u], vsc[u]);
+                for (int u = 0; u < 4; ++u) to[u] = at[u] + (KBUFS + vb) * BUF;
+                widen_chunk<0>(to, vc[0], vsc[0]);
+                widen_chunk<64 * 128>(to, vc[1], vsc[1]);
                 fence_proxy_async();
                 __syncwarp();
-                if (lane == 0) mbar_arrive(bar(B_V_FULL + tb));
+                if (lane == 0) mbar_arrive(bar(B_V_FULL + vb));
             }
         }
     }

@@ -96,28 +96,6 @@ constexpr uint32_t ID_QK = idesc(128, NK, false) | (1u << 7) | (1u << 10);
 constexpr uint32_t ID_QK_HALF = idesc(128, NK / 2, false) | (1u << 7) | (1u << 10);
 constexpr uint32_t ID_PV = idesc(128, 128, true) | (1u << 7) | (1u << 10);
 
-// Shared-memory matrix descriptor from its low word (see sdesc: address and
-// leading offset) with a stride of 1024 bytes and the 128-byte swizzle.
-__device__ __forceinline__ uint32_t desc_lo(uint32_t saddr, uint32_t lbo) {
-    return ((saddr >> 4) & 0x3FFFu) | ((lbo >> 4) << 16);
-}
-constexpr uint32_t DESC_HI = (1024u >> 4) | (1u << 14) | (2u << 29);
-
-__device__ __forceinline__ void mma_ss(uint32_t d, uint32_t a, uint32_t b, uint32_t id, uint32_t acc) {
-    asm volatile(
-        "{ .reg .pred p; .reg .b64 x, y; setp.ne.b32 p, %4, 0; mov.b64 x, {%1, %5}; mov.b64 y, {%2, %5}; "
-        "tcgen05.mma.cta_group::1.kind::f16 [%0], x, y, %3, p; }" ::"r"(d),
-        "r"(a), "r"(b), "r"(id), "r"(acc), "n"(DESC_HI)
-        : "memory");
-}
-__device__ __forceinline__ void mma_ts(uint32_t d, uint32_t a, uint32_t b, uint32_t id, uint32_t acc) {
-    asm volatile(
-        "{ .reg .pred p; .reg .b64 y; setp.ne.b32 p, %4, 0; mov.b64 y, {%2, %5}; "
-        "tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], y, %3, p; }" ::"r"(d),
-        "r"(a), "r"(b), "r"(id), "r"(acc), "n"(DESC_HI)
-        : "memory");
-}
-
 __device__ __forceinline__ void tma_store_3d(const CUtensorMap* tm, uint32_t src, int x, int y, int z) {
     asm volatile("cp.async.bulk.tensor.3d.global.shared::cta.tile.bulk_group [%0, {%2, %3, %4}], [%1];" ::"l"(tm),
                  "r"(src), "r"(x), "r"(y), "r"(z)
