@@ -222,21 +222,20 @@ def _check(out, lay, q, kc, vc, ks, vs, ps, window=-1, rows=None):
     ref, mag, lmag, vsum = int4_np.paged_attention(q.double().cpu().numpy(), kc.cpu().numpy(), vc.cpu().numpy(), ps,
                                                    lay.block_table.numpy(), lay.seq_lens.numpy(), ks.item(), vs.item(),
                                                    SM, window)
-    # bf16 output: half a step, 2^-8 of the value.  Softmax weights: f16 of 2^15
-    # times the weight against the running maximum (more than 16 rows: 2^11
-    # times), off by 2^-11 of itself (with exponentials, sums and the f32 product
-    # with the scale below 2^-14 more: under 2^-10 of mag) or, below f16's normal
-    # range, by 2^-25, that is 2^-40 (2^-36) of the row's sum, which is at least
-    # 2^15 (2^11): times vsum.  Logits: a sum of 128 products is eight
-    # accumulating steps of 16, each off by at most an ulp (2^-23) of the partial
-    # sum, whose size is at most a: 8 * 2^-23 a, which moves the output by at
-    # most 2^-20 lmag.  (That term matters only where |q| |k| is in the hundreds:
-    # with a = 560, 2 * 560 * 2^-20 is already 2^-10.)  Partials of more than 16
-    # rows: f16, 2^-11 of each, so at most 2^-11 of mag.
+    # bf16 output: half a step, 2^-8 of the value.  Softmax weights: f16 of 2^11
+    # times the weight against a maximum that lags at most 2^4 behind, off by
+    # 2^-11 of itself (with exponentials, sums and the f32 product with the scale
+    # below 2^-14 more: under 2^-10 of mag) or, below f16's normal range, by
+    # 2^-25, that is 2^-36 of the row's sum, which is at least 2^11: times vsum.
+    # Logits: a sum of 128 products is eight accumulating steps of 16, each off by
+    # at most an ulp (2^-23) of the partial sum, whose size is at most a:
+    # 8 * 2^-23 a, which moves the output by at most 2^-20 lmag.  (That term
+    # matters only where |q| |k| is in the hundreds: with a = 560, 2 * 560 * 2^-20
+    # is already 2^-10.)  Partials of more than 16 rows: f16, 2^-11 of each, so at
+    # most 2^-11 of mag.
     err = np.abs(out.double().cpu().numpy() - ref)
     many = q.shape[1] * q.shape[2] // kc.shape[1] > 16
-    tol = (2.0 ** -8 * np.abs(ref) + (2.0 ** -10 + many * 2.0 ** -11) * mag + 2.0 ** -20 * lmag +
-           2.0 ** (-36 if many else -40) * vsum)
+    tol = (2.0 ** -8 * np.abs(ref) + (2.0 ** -10 + many * 2.0 ** -11) * mag + 2.0 ** -20 * lmag + 2.0 ** -36 * vsum)
     assert np.all(err <= tol), (float((err / tol).max()), float(err.max()))
 
 
@@ -312,6 +311,18 @@ def test_extreme_scales_logits_and_values(M):
     assert int(kc[:, :, 32 * 64:].max()) >= 0x70
     out = _attend(lay, q, kc, vc, ks, vs)
     _check(out, lay, q, kc, vc, ks, vs, 32)
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("M", [1, 12])
+@pytest.mark.parametrize("sm", [-0.3, 0.0])
+def test_negative_and_zero_softmax_scale(M, sm):
+    lay, q, kc, vc, ks, vs, k, v, slots = _case(43, [400, 20], M, 9, 2, 32)
+    fp8kv.fp8kv_cache_insert(k, v, slots, ks, vs, kc, vc)
+    bt, sl = lay.block_table.cuda(), lay.seq_lens.cuda()
+    out = fp8kv.fp8kv_paged_attention(q, kc, vc, bt, sl, 400, ks, vs, sm)
+    neg = fp8kv.fp8kv_paged_attention(-q if sm else torch.zeros_like(q), kc, vc, bt, sl, 400, ks, vs, abs(sm) or 1.0)
+    assert torch.equal(out, neg) if sm else bool((out.float() - neg.float()).abs().max() < 2.0 ** -8)
 
 
 @pytest.mark.gpu

@@ -45,6 +45,7 @@ constexpr int OFF_V = CK * kInt4CodeBytes;              // K codes, V codes, K s
 constexpr int OFF_KS = 2 * CK * kInt4CodeBytes;
 constexpr int OFF_VS = OFF_KS + CK * kInt4ScaleBytes;
 constexpr int STAGE_BYTES = OFF_VS + CK * kInt4ScaleBytes;   // 4608
+constexpr float GROW = 4.0f, BIAS = 11.0f;              // see the softmax
 constexpr int MERGE_STRIDE = 132;                       // floats per merged row: 128 of O, max, sum
 constexpr int SMEM = WARPS * STAGES * STAGE_BYTES;
 static_assert(WARPS * 16 * MERGE_STRIDE * 4 <= SMEM, "merge area exceeds the rings");
@@ -169,10 +170,12 @@ __global__ void __launch_bounds__(THREADS, 1) paged_attention_int4_kernel(AttnPa
                 e = be ? be - 127 : -127;
             }
             const int sh = max(-120, min(120, 4 - e));
-            const float scale = ldexpf(1.0f, sh);
+            // (the sign of sm_scale goes into q: the row maximum is taken before
+            // the multiplication below)
+            const float scale = copysignf(ldexpf(1.0f, sh), P.sm_scale);
 #pragma unroll
             for (int j = 0; j < 32; ++j) qf[hr][j] *= scale;
-            mult[hr] = 4.0f * ks * P.sm_scale * 1.4426950408889634f * ldexpf(1.0f, -sh);
+            mult[hr] = fmaxf(4.0f * ks * fabsf(P.sm_scale) * 1.4426950408889634f * ldexpf(1.0f, -sh), 1e-37f);
         }
         // word w of a key's 16 code bytes holds dims 8w .. 8w + 7 of the 32;
         // widen4 pairs dim f with f + 4, f = 0..3, and fills two k-steps
@@ -227,51 +230,57 @@ __global__ void __launch_bounds__(THREADS, 1) paged_attention_int4_kernel(AttnPa
                 mma_f16(sacc[j], qa[2 * w + 1], v[2], v[3]);
             }
         }
-        // ---- log2 units, masks, online softmax
-        const bool need_mask = (k0 + CK - 1 > pmin) || (k0 < lomax);
+        // ---- masks, online softmax in log2 units (s mult)
+        if ((k0 + CK - 1 > pmin) || (k0 < lomax)) {
 #pragma unroll
-        for (int j = 0; j < 4; ++j) {
+            for (int j = 0; j < 4; ++j)
 #pragma unroll
-            for (int e = 0; e < 4; ++e) {
-                float x = sacc[j][e] * mult[e >> 1];
-                if (need_mask) {
+                for (int e = 0; e < 4; ++e) {
                     const int key = k0 + 8 * j + 4 * (e & 1) + t;
-                    if (key > pr[e >> 1] || key < lor[e >> 1]) x = -INFINITY;
+                    if (key > pr[e >> 1] || key < lor[e >> 1]) sacc[j][e] = -INFINITY;
                 }
-                sacc[j][e] = x;
-            }
         }
-        float alpha[2];
+        // O is rescaled only when a row's maximum grows by more than 2^GROW
+        float tmax[2];
+        bool grow = false;
 #pragma unroll
         for (int hr = 0; hr < 2; ++hr) {
-            float tmax = -INFINITY;
+            float x = max3(sacc[0][2 * hr], sacc[0][2 * hr + 1], sacc[1][2 * hr]);
+            x = max3(x, sacc[1][2 * hr + 1], sacc[2][2 * hr]);
+            x = max3(x, sacc[2][2 * hr + 1], sacc[3][2 * hr]);
+            x = fmaxf(x, sacc[3][2 * hr + 1]);
+            x = fmaxf(x, __shfl_xor_sync(0xffffffffu, x, 1));
+            x = fmaxf(x, __shfl_xor_sync(0xffffffffu, x, 2));
+            tmax[hr] = x * mult[hr];
+            grow |= tmax[hr] > mrow[hr] + GROW;             // (the first visible keys too: mrow = -inf)
+        }
+        if (__any_sync(0xffffffffu, grow)) {
 #pragma unroll
-            for (int j = 0; j < 4; ++j) tmax = fmaxf(tmax, fmaxf(sacc[j][2 * hr], sacc[j][2 * hr + 1]));
-            tmax = fmaxf(tmax, __shfl_xor_sync(0xffffffffu, tmax, 1));
-            tmax = fmaxf(tmax, __shfl_xor_sync(0xffffffffu, tmax, 2));
-            const float mnew = fmaxf(mrow[hr], tmax);
-            alpha[hr] = (mnew == -INFINITY) ? 1.f : ex2(mrow[hr] - mnew);
-            // weights as 2^15 times 2^(x - max): f16 then keeps 11 bits of
-            // every weight down to 2^-29 of the largest
-            const float mref = (mnew == -INFINITY) ? 0.f : mnew - 15.0f;
-            mrow[hr] = mnew;
+            for (int hr = 0; hr < 2; ++hr) {
+                const float mnew = fmaxf(mrow[hr], tmax[hr]);
+                const float alpha = mrow[hr] == -INFINITY ? 1.f : ex2(mrow[hr] - mnew);
+                mrow[hr] = mnew;
+                lrow[hr] *= alpha;
+#pragma unroll
+                for (int i = 0; i < 16; ++i) {
+                    o[i][2 * hr] *= alpha;
+                    o[i][2 * hr + 1] *= alpha;
+                }
+            }
+        }
+#pragma unroll
+        for (int hr = 0; hr < 2; ++hr) {
+            // weights as 2^11 times 2^(x - m), at most 2^15: f16 then keeps 11
+            // bits of every weight down to 2^-25 of the largest
+            const float neg = (mrow[hr] == -INFINITY) ? 0.f : BIAS - mrow[hr];
             float sum = 0.f;
 #pragma unroll
             for (int j = 0; j < 4; ++j) {
-                sacc[j][2 * hr] = ex2(sacc[j][2 * hr] - mref);
-                sacc[j][2 * hr + 1] = ex2(sacc[j][2 * hr + 1] - mref);
+                sacc[j][2 * hr] = ex2(fmaf(sacc[j][2 * hr], mult[hr], neg));
+                sacc[j][2 * hr + 1] = ex2(fmaf(sacc[j][2 * hr + 1], mult[hr], neg));
                 sum += sacc[j][2 * hr] + sacc[j][2 * hr + 1];
             }
-            lrow[hr] = lrow[hr] * alpha[hr] + sum;
-        }
-        if (__any_sync(0xffffffffu, alpha[0] != 1.f || alpha[1] != 1.f)) {
-#pragma unroll
-            for (int i = 0; i < 16; ++i) {
-                o[i][0] *= alpha[0];
-                o[i][1] *= alpha[0];
-                o[i][2] *= alpha[1];
-                o[i][3] *= alpha[1];
-            }
+            lrow[hr] += sum;
         }
         // ---- O += P V.  Keys that no row sees (behind the end, before the
         // first window) get scale 0: whatever their bytes are, 0 reaches O

@@ -228,8 +228,10 @@ __global__ void __launch_bounds__(THREADS, 1) attention_int4_tc_kernel(AttnParam
                 e = be ? be - 127 : -127;
             }
             const int sh = max(-120, min(120, 4 - e));
-            const float scale = ldexpf(1.0f, sh);
-            mult = 4.0f * *P.k_scale * P.sm_scale * 1.4426950408889634f * ldexpf(1.0f, -sh);
+            // (the sign of sm_scale goes into q: the row maximum is taken before
+            // the multiplication)
+            const float scale = copysignf(ldexpf(1.0f, sh), P.sm_scale);
+            mult = fmaxf(4.0f * *P.k_scale * fabsf(P.sm_scale) * 1.4426950408889634f * ldexpf(1.0f, -sh), 1e-37f);
             uint32_t qf[32];
 #pragma unroll
             for (int u = 0; u < 8; ++u) {                   // dims 8u .. + 7 in the order 0 4 1 5 2 6 3 7
