@@ -1154,7 +1154,9 @@ static int attention_call(const void* k_new, const void* v_new, const void* q, c
         // widens every key again for each 16 rows, 3097 us; one tile of 16
         // rows: ROWS16)
         const bool tc = tc_rows(M, Hq, Hkv) && plan.split_tokens % tc_tile_tokens() == 0;
-        const bool lpt = tc && B > 1 && row_tiles(M, Hq, Hkv) == 1 && plan.num_splits > 1;
+        const bool lpt = B > 1 && (tc ? row_tiles(M, Hq, Hkv) : P.NT) == 1 && plan.num_splits > 1 &&
+                         plan.split_tokens % tc_tile_tokens() == 0 &&
+                         (int64_t)B * plan.num_splits * Hkv <= INT32_MAX;
         if (lpt) {
             // in the second half of the partials' area, which f16 leaves free
             P.lpt_order = (const int32_t*)((const uint8_t*)workspace + rows * plan.num_splits * 128 * sizeof(uint16_t));
@@ -1171,8 +1173,8 @@ static int attention_call(const void* k_new, const void* v_new, const void* q, c
         if (rc) return rc;
         if (plan.num_splits > 1) {
             const int64_t warps = (int64_t)B * M * Hq;
-            cudaError_t e = launch_pdl(tc ? attn_reduce_kernel<true> : attn_reduce_kernel<false>,
-                                       dim3((unsigned)((warps + 7) / 8)), dim3(256), 0, s, (const float*)P.ws_o,
+            cudaError_t e = launch_pdl(attn_reduce_kernel<true>, dim3((unsigned)((warps + 7) / 8)), dim3(256), 0, s,
+                                       (const float*)P.ws_o,
                                        (const float*)P.ws_ml, seq_lens, B, M, Hq, P.G, tc ? 128 : P.R,
                                        max_pages_per_seq, page_size, window_left, plan.split_pages, plan.num_splits,
                                        max_seq_len, v_scale, scale_stride, (uint16_t*)out);

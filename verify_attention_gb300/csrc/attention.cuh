@@ -93,11 +93,10 @@ int launch_append_int4(const void* k, const void* v, const int32_t* seq_lens, co
                        void* v_cache, int num_pages, int page_size, int max_seq_len, cudaStream_t s);
 
 // Host launchers of the INT4 cache kernels; `text` describes the launch.
-// attention_int4.cu (tiles of 16 rows): partials as the mma.sync kernels write
-// them (fp32 O * v_scale, (max, sum)), partitions cut from the key range of
-// all R rows.  attention_int4_tc.cu (tiles of 128 rows): partials as the
-// tcgen05 kernel writes them (f16 O / l without v_scale, (max, sum)); whole
-// 128-key partitions.
+// Partials as the tcgen05 kernel writes them (f16 O / l without v_scale, (max,
+// sum)).  attention_int4.cu: tiles of 16 rows, partitions cut from the key
+// range of all R rows.  attention_int4_tc.cu: tiles of 128 rows, whole 128-key
+// partitions, cut from the key range of the tile.
 int launch_attention_int4(const AttnParams& P, cudaStream_t s, char* text, size_t text_bytes);
 int launch_attention_int4_tc(const AttnParams& P, cudaStream_t s, char* text, size_t text_bytes);
 

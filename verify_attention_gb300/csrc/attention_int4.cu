@@ -26,7 +26,6 @@
 
 #include <mutex>
 #include <set>
-#include <utility>
 
 #include "attention.cuh"
 #include "common.cuh"
@@ -38,7 +37,6 @@ int status_attention_int4(unsigned int* s, int clear) { return read_status(s, cl
 
 namespace i4 {
 
-constexpr int WARPS = 12, THREADS = WARPS * 32;         // 168 registers a thread at one CTA per SM
 constexpr int STAGES = 4;                               // chunks of a warp's ring
 constexpr int CK = 32;                                  // keys per chunk
 constexpr int OFF_V = CK * kInt4CodeBytes;              // K codes, V codes, K scales, V scales
@@ -47,46 +45,73 @@ constexpr int OFF_VS = OFF_KS + CK * kInt4ScaleBytes;
 constexpr int STAGE_BYTES = OFF_VS + CK * kInt4ScaleBytes;   // 4608
 constexpr float GROW = 4.0f, BIAS = 11.0f;              // see the softmax
 constexpr int MERGE_STRIDE = 132;                       // floats per merged row: 128 of O, max, sum
-constexpr int SMEM = WARPS * STAGES * STAGE_BYTES;
-static_assert(WARPS * 16 * MERGE_STRIDE * 4 <= SMEM, "merge area exceeds the rings");
+static_assert(16 * MERGE_STRIDE * 4 <= STAGES * STAGE_BYTES, "merge area exceeds the rings");
 
-__device__ __forceinline__ void cp16(uint32_t dst, const void* src, bool valid) {
-    asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst), "l"(src), "r"(valid ? 16 : 0) : "memory");
+// 16 bytes from src + SRC to shared memory at dst + DST (zeros when bytes = 0)
+template <int DST, int SRC>
+__device__ __forceinline__ void cp16(uint32_t dst, const uint8_t* src, int bytes) {
+    asm volatile("cp.async.cg.shared.global [%0 + %3], [%1 + %4], 16, %2;" ::"r"(dst), "l"(src), "r"(bytes), "n"(DST), "n"(SRC)
+                 : "memory");
 }
 __device__ __forceinline__ void cp_commit() { asm volatile("cp.async.commit_group;" ::: "memory"); }
 template <int N>
 __device__ __forceinline__ void cp_wait() { asm volatile("cp.async.wait_group %0;" ::"n"(N) : "memory"); }
 
-// Issue the copies of chunk `key0 / 32` of page `page` into a stage: K rows at
-// their column position (see the key order above), V rows with the 16-byte
-// units exchanged on keys 2 and 3 of 4.  Pages outside the pool read as zeros.
-template <int PS>
-__device__ __forceinline__ void issue_chunk(uint32_t stage, const AttnParams& P, int page, int hk, int key_in_page,
-                                            int lane) {
-    const bool valid = page >= 0 && page < P.num_pages;
-    const int64_t base = valid ? ((int64_t)page * P.Hkv + hk) * (PS * kInt4RowBytes) : 0;
-    const uint8_t* kp = P.k_cache + base;
-    const uint8_t* vp = P.v_cache + base;
-    const int code0 = key_in_page * kInt4CodeBytes, scale0 = PS * kInt4CodeBytes + key_in_page * kInt4ScaleBytes;
-#pragma unroll
-    for (int u = 0; u < 4; ++u) {
-        const int i = lane + 32 * u, row = i >> 2, ch = i & 3;
-        const int kpos = (row & ~7) | ((row & 3) << 1) | ((row >> 2) & 1);
-        cp16(stage + kpos * 64 + ch * 16, kp + code0 + i * 16, valid);
-        cp16(stage + OFF_V + row * 64 + ((ch ^ (row & 2)) << 4), vp + code0 + i * 16, valid);
-    }
-    const uint8_t* sp = lane < 16 ? kp : vp;
-    cp16(stage + OFF_KS + lane * 16, sp + scale0 + (lane & 15) * 16, valid);
+// Where this lane's 16-byte pieces of a chunk go in a stage: K rows at their
+// column position (see the key order above), V rows with the 16-byte units
+// exchanged on keys 2 and 3 of 4.  Piece u of lane l is row (l >> 2) + 8 u.
+struct Lanes {
+    uint32_t k, v, s;
+};
+__device__ __forceinline__ Lanes lane_places(int lane) {
+    const int row = lane >> 2, ch = lane & 3;
+    return {(uint32_t)((((row & 3) << 1) | (row >> 2)) * 64 + ch * 16),
+            (uint32_t)(OFF_V + row * 64 + ((ch ^ (row & 2)) << 4)), (uint32_t)(OFF_KS + lane * 16)};
 }
 
+// Issue the copies of the chunk at key_in_page of page `page` into a stage.
+// Pages outside the pool read as zeros.
 template <int PS>
-__global__ void __launch_bounds__(THREADS, 1) paged_attention_int4_kernel(AttnParams P) {
+__device__ __forceinline__ void issue_chunk(uint32_t stage, const Lanes& at, const AttnParams& P, int page, int hk,
+                                            int key_in_page, int lane) {
+    const bool valid = page >= 0 && page < P.num_pages;
+    const int bytes = valid ? 16 : 0;
+    const int64_t base = valid ? ((int64_t)page * P.Hkv + hk) * (PS * kInt4RowBytes) : 0;
+    const int64_t code = base + key_in_page * kInt4CodeBytes + lane * 16;
+    const uint8_t *kp = P.k_cache + code, *vp = P.v_cache + code;
+    const uint8_t* sp = (lane < 16 ? P.k_cache : P.v_cache) + base + PS * kInt4CodeBytes +
+                        key_in_page * kInt4ScaleBytes + (lane & 15) * 16;
+    cp16<0, 0>(stage + at.k, kp, bytes);
+    cp16<512, 512>(stage + at.k, kp, bytes);
+    cp16<1024, 1024>(stage + at.k, kp, bytes);
+    cp16<1536, 1536>(stage + at.k, kp, bytes);
+    cp16<0, 0>(stage + at.v, vp, bytes);
+    cp16<512, 512>(stage + at.v, vp, bytes);
+    cp16<1024, 1024>(stage + at.v, vp, bytes);
+    cp16<1536, 1536>(stage + at.v, vp, bytes);
+    cp16<0, 0>(stage + at.s, sp, bytes);
+}
+
+// WARPS = 12, one CTA per SM, or 4, three CTAs per SM (168 registers a thread).
+template <int PS, int WARPS>
+__global__ void __launch_bounds__(WARPS * 32, 12 / WARPS) paged_attention_int4_kernel(AttnParams P) {
     extern __shared__ __align__(128) uint8_t smem[];
-    const int split = blockIdx.x, rt = blockIdx.y % P.NT, hk = blockIdx.y / P.NT, b = blockIdx.z;
+    constexpr int THREADS = WARPS * 32;
+    const int rt = blockIdx.y % P.NT;
+    int split = blockIdx.x, hk = blockIdx.y / P.NT, b = blockIdx.z;
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     const int g = lane >> 2, t = lane & 3;
     pdl_launch_dependents();
     pdl_wait();
+    if (P.lpt_order) {
+        // CTA i: KV head i mod Hkv of the slot of rank i / Hkv, longest first
+        const int lin = blockIdx.x + gridDim.x * (blockIdx.y + gridDim.y * blockIdx.z);
+        const int q = P.lpt_order[lin / P.Hkv];
+        if (q < 0) return;
+        hk = lin % P.Hkv;
+        b = q / P.num_splits;
+        split = q % P.num_splits;
+    }
     const int L = P.seq_lens[b];
     if (L < P.M || L > P.max_seq_len || (L + PS - 1) / PS > P.mpps) {
         if (threadIdx.x == 0 && split == 0 && blockIdx.y == 0) flag(FP8KV_DEV_BAD_SEQ_LEN);
@@ -111,6 +136,7 @@ __global__ void __launch_bounds__(THREADS, 1) paged_attention_int4_kernel(AttnPa
 
     // this warp's chunks: warp, warp + WARPS, ...; their page ids are read one
     // round ahead of the copies
+    const Lanes places = lane_places(lane);
     int next = warp;
     int page = next < n_chunks ? bt[next / CPP] : -1;
     auto issue = [&](int slot) {
@@ -118,7 +144,7 @@ __global__ void __launch_bounds__(THREADS, 1) paged_attention_int4_kernel(AttnPa
             const int cur = page, at = next;
             next += WARPS;
             page = next < n_chunks ? bt[next / CPP] : -1;
-            issue_chunk<PS>(ring + slot * STAGE_BYTES, P, cur, hk, (at % CPP) * CK, lane);
+            issue_chunk<PS>(ring + slot * STAGE_BYTES, places, P, cur, hk, (at % CPP) * CK, lane);
         }
         cp_commit();
     };
@@ -208,6 +234,7 @@ __global__ void __launch_bounds__(THREADS, 1) paged_attention_int4_kernel(AttnPa
         __syncwarp();                                   // every lane's copies of this chunk; reads of the last one done
         issue(fill);
         fill = fill + 1 == STAGES ? 0 : fill + 1;
+        const int cur_slot = slot;
         const uint8_t* st = smem + (warp * STAGES + slot) * STAGE_BYTES;
         slot = slot + 1 == STAGES ? 0 : slot + 1;
         const int k0 = key_begin + c * CK;
@@ -215,19 +242,33 @@ __global__ void __launch_bounds__(THREADS, 1) paged_attention_int4_kernel(AttnPa
         // ---- S = Q K^T
         float sacc[4][4];
 #pragma unroll
-        for (int j = 0; j < 4; ++j) {
-            sacc[j][0] = sacc[j][1] = sacc[j][2] = sacc[j][3] = 0.f;
-            const uint4 kw4 = *(const uint4*)(st + (8 * j + g) * 64 + 16 * t);
-            const int key = 8 * j + 4 * (g & 1) + (g >> 1);
-            const uint32_t s2 = e4m3x2_to_f16x2(*(const uint16_t*)(st + OFF_KS + key * 8 + 2 * t));
-            const Scale2 sa = scale2(prmt(s2, s2, 0x1010)), sb = scale2(prmt(s2, s2, 0x3232));
-            const uint32_t kw[4] = {kw4.x, kw4.y, kw4.z, kw4.w};
+        for (int jj = 0; jj < 4; jj += 4) {
+            uint32_t kw[4][4];
+            Scale2 sc[4][2];
+#pragma unroll
+            for (int j = 0; j < 4; ++j) {
+                const uint4 x = *(const uint4*)(st + (8 * (jj + j) + g) * 64 + 16 * t);
+                kw[j][0] = x.x;
+                kw[j][1] = x.y;
+                kw[j][2] = x.z;
+                kw[j][3] = x.w;
+                const int key = 8 * (jj + j) + 4 * (g & 1) + (g >> 1);
+                const uint32_t s2 = e4m3x2_to_f16x2(*(const uint16_t*)(st + OFF_KS + key * 8 + 2 * t));
+                sc[j][0] = scale2(prmt(s2, s2, 0x1010));
+                sc[j][1] = scale2(prmt(s2, s2, 0x3232));
+            }
 #pragma unroll
             for (int w = 0; w < 4; ++w) {
-                uint32_t v[4];
-                widen4(kw[w], w < 2 ? sa : sb, v);
-                mma_f16(sacc[j], qa[2 * w], v[0], v[1]);
-                mma_f16(sacc[j], qa[2 * w + 1], v[2], v[3]);
+                uint32_t v[4][4];
+#pragma unroll
+                for (int j = 0; j < 4; ++j) widen4(kw[j][w], sc[j][w >> 1], v[j]);
+#pragma unroll
+                for (int j = 0; j < 4; ++j) {
+                    if (w == 0) mma_f16_zero(sacc[jj + j], qa[0], v[j][0], v[j][1]);
+                    else mma_f16(sacc[jj + j], qa[2 * w], v[j][0], v[j][1]);
+                }
+#pragma unroll
+                for (int j = 0; j < 4; ++j) mma_f16(sacc[jj + j], qa[2 * w + 1], v[j][2], v[j][3]);
             }
         }
         // ---- masks, online softmax in log2 units (s mult)
@@ -284,7 +325,12 @@ __global__ void __launch_bounds__(THREADS, 1) paged_attention_int4_kernel(AttnPa
         }
         // ---- O += P V.  Keys that no row sees (behind the end, before the
         // first window) get scale 0: whatever their bytes are, 0 reaches O
-        const bool zero_v = (k0 + CK > L) || (k0 < lo0);
+        if (k0 + CK > L || k0 < lo0) {
+            __syncwarp();
+            if (k0 + lane >= L || k0 + lane < lo0)
+                *(uint2*)(smem + (warp * STAGES + cur_slot) * STAGE_BYTES + OFF_VS + lane * 8) = make_uint2(0u, 0u);
+            __syncwarp();
+        }
 #pragma unroll
         for (int kk = 0; kk < 2; ++kk) {
             uint32_t pa[4];
@@ -304,7 +350,6 @@ __global__ void __launch_bounds__(THREADS, 1) paged_attention_int4_kernel(AttnPa
                     w[2 * pr2 + e][0] = x.x;
                     w[2 * pr2 + e][1] = x.y;
                     by[e] = st[OFF_VS + key * 8 + g];
-                    if (zero_v && (k0 + key >= L || k0 + key < lo0)) by[e] = 0;
                 }
                 sc[pr2] = scale2(e4m3x2_to_f16x2(by[0] | (by[1] << 8)));
             }
@@ -374,42 +419,53 @@ __global__ void __launch_bounds__(THREADS, 1) paged_attention_int4_kernel(AttnPa
             *(uint2*)(P.out + row_idx * 128 + d4) =
                 make_uint2(pack_bf16x2(acc.x * f, acc.y * f), pack_bf16x2(acc.z * f, acc.w * f));
         } else {
-            *(float4*)(P.ws_o + (row_idx * P.num_splits + split) * 128 + d4) =
-                make_float4(acc.x * vs, acc.y * vs, acc.z * vs, acc.w * vs);
-            if (d4 == 0) {
-                P.ws_ml[(row_idx * P.num_splits + split) * 2] = mstar;
-                P.ws_ml[(row_idx * P.num_splits + split) * 2 + 1] = l;
-            }
+            // partial: f16 of 4 O / l (|x| <= 7 * 448) beside its (max, sum); a
+            // row with no visible key here has l = 0: weight 0, values 0
+            const float f = l > 0.f ? 4.0f / l : 0.f;
+            *(uint2*)((uint16_t*)P.ws_o + (row_idx * P.num_splits + split) * 128 + d4) =
+                make_uint2(pack_f16x2(acc.x * f, acc.y * f), pack_f16x2(acc.z * f, acc.w * f));
+            if (d4 == 0) *(float2*)(P.ws_ml + (row_idx * P.num_splits + split) * 2) = make_float2(mstar, l);
         }
     }
+}
+
+template <int PS, int WARPS>
+static int launch(const AttnParams& P, cudaStream_t s) {
+    static std::mutex mu;
+    static std::set<int> done;
+    auto kern = paged_attention_int4_kernel<PS, WARPS>;
+    constexpr int smem = WARPS * STAGES * STAGE_BYTES;
+    {
+        int dev = 0;
+        if (cudaGetDevice(&dev) != cudaSuccess) return FP8KV_ERR_CUDA;
+        std::lock_guard<std::mutex> lock(mu);
+        if (!done.count(dev)) {
+            if (cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, smem) != cudaSuccess)
+                return FP8KV_ERR_CUDA;
+            done.insert(dev);
+        }
+    }
+    const dim3 grid(P.num_splits, P.Hkv * P.NT, P.B);
+    const cudaError_t e = launch_pdl(kern, grid, dim3(WARPS * 32), smem, s, P);
+    return e == cudaSuccess ? FP8KV_OK : (cudaGetLastError(), FP8KV_ERR_CUDA);
 }
 
 }  // namespace i4
 
 int launch_attention_int4(const AttnParams& P, cudaStream_t s, char* text, size_t text_bytes) {
     if ((int64_t)P.Hkv * P.NT > 65535) return FP8KV_ERR_UNSUPPORTED;
-    static std::mutex mu;
-    static std::set<std::pair<int, const void*>> done;
-    auto kern = P.page_size == 32 ? i4::paged_attention_int4_kernel<32> : i4::paged_attention_int4_kernel<64>;
-    {
-        int dev = 0;
-        if (cudaGetDevice(&dev) != cudaSuccess) return FP8KV_ERR_CUDA;
-        std::lock_guard<std::mutex> lock(mu);
-        if (!done.count({dev, (const void*)kern})) {
-            if (cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, i4::SMEM) != cudaSuccess)
-                return FP8KV_ERR_CUDA;
-            done.insert({dev, (const void*)kern});
-        }
-    }
-    const dim3 grid(P.num_splits, P.Hkv * P.NT, P.B);
-    const cudaError_t e = launch_pdl(kern, grid, dim3(i4::THREADS), i4::SMEM, s, P);
-    if (e != cudaSuccess) {
-        cudaGetLastError();
-        return FP8KV_ERR_CUDA;
-    }
-    snprintf(text, text_bytes, "paged_attention_int4_mma<ps=%d> rows=%d row_tiles=%d splits=%d grid=%dx%dx%d threads=%d reduce=%d",
-             P.page_size, P.R, P.NT, P.num_splits, P.num_splits, P.Hkv * P.NT, P.B, i4::THREADS,
-             P.num_splits > 1 ? 1 : 0);
+    // Small CTAs, three to an SM, when there are enough of them: one's set-up
+    // and merge run beside the others' keys (64 sequences, 2048 CTAs: 384 us
+    // against 405); with fewer CTAs than that their warps would leave the SMs
+    // part empty (one sequence of 131072 keys, 152 CTAs: 106 us against 49).
+    const bool small = (int64_t)P.B * P.Hkv * P.NT * P.num_splits >= 3ll * num_sms();
+    const int rc = P.page_size == 32 ? (small ? i4::launch<32, 4>(P, s) : i4::launch<32, 12>(P, s))
+                                     : (small ? i4::launch<64, 4>(P, s) : i4::launch<64, 12>(P, s));
+    if (rc) return rc;
+    snprintf(text, text_bytes,
+             "paged_attention_int4_mma<ps=%d> rows=%d row_tiles=%d splits=%d grid=%dx%dx%d threads=%d reduce=%d order=%s",
+             P.page_size, P.R, P.NT, P.num_splits, P.num_splits, P.Hkv * P.NT, P.B, small ? 128 : 384,
+             P.num_splits > 1 ? 1 : 0, P.lpt_order ? "longest_first" : "grid");
     return FP8KV_OK;
 }
 
