@@ -97,7 +97,8 @@ def _ptr(t: Optional[torch.Tensor]) -> int:
 
 def _stream(stream) -> int:
     if stream is None:
-        stream = torch.cuda.current_stream()
+        # the handle of the current stream without a Stream object (0.3 us instead of 3)
+        return torch._C._cuda_getCurrentRawStream(torch.cuda.current_device())
     return stream.cuda_stream if hasattr(stream, "cuda_stream") else int(stream)
 
 
