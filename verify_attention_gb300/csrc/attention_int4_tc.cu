@@ -16,21 +16,23 @@
 // One CTA per (partition, row tile x KV head, sequence), 20 warps:
 //   warp 0           loads pages (bulk copies of the codes and of the scales of
 //                    a (page, head)) into a ring of 128-key stages
-//   warps 1, 2       issue the MMAs of the first and of the second half (64 keys)
-//                    of every tile: S = Q.K^T, then O += P.V
-//   warps 4-7, 8-11  softmax of the first and of the second half, a row per
-//                    thread (warps 4+q and 8+q: TMEM lane quarter q).  Each half
-//                    keeps its own maximum, sum and O, merged at the end, so the
-//                    two never wait for each other and one half's products run
-//                    during the other's softmax.  (One softmax over both, its
-//                    maximum exchanged through shared memory for every tile,
-//                    took 2800 cycles a tile.)  O is rescaled when a row's
-//                    maximum grows by more than 2^4; the weights are held as
-//                    2^11 times 2^(x - m), at most 2^15, so that f16 keeps 11
-//                    bits of every weight down to 2^-25 of the largest.
+//   warp 1           issues S = Q.K^T of the half tiles (64 keys) u = 0, 1, ...,
+//                    into three S buffers in turn
+//   warp 2           issues O += P(u).V
+//   warps 4-7, 8-11  softmax of the even and of the odd half tiles, a row per
+//                    thread (warps 4+q and 8+q: TMEM lane quarter q).  Each of
+//                    the two keeps its own maximum, sum and O, merged at the
+//                    end, so that they never wait for each other.  (One softmax
+//                    over whole tiles, the maximum exchanged through shared
+//                    memory, took 2800 cycles a tile; two with one S buffer
+//                    each, which idle while their next product runs, 2600.)  O
+//                    is rescaled when a row's maximum grows by more than 2^4;
+//                    the weights are held as 2^11 times 2^(x - m), at most
+//                    2^15, so that f16 keeps 11 bits of every weight down to
+//                    2^-25 of the largest.
 //   warps 12-19      widen K and V into swizzled f16 tiles (five warps took 3700
 //                    cycles a tile)
-// TMEM columns: Q 0-63, S/P of the halves 64-127, 128-191, O 192-319, 320-447.
+// TMEM columns: Q 0-63, S/P 3 x 64 (64-255), O 256-383, 384-511.
 #include <stdio.h>
 
 #include <mutex>
@@ -60,7 +62,7 @@ constexpr int XCH_BYTES = 2 * 128 * 8;                  // (max, sum) of [half][
 constexpr int SMEM = (KBUFS + VBUFS) * BUF + STAGES * STAGE_BYTES + XCH_BYTES + 1024 + 512;
 constexpr int EPI_STRIDE = 144;                         // staged half row (128 bytes), padded against bank conflicts
 static_assert(2 * 128 * EPI_STRIDE <= (KBUFS + VBUFS) * BUF, "epilogue staging exceeds the widened tiles");
-constexpr uint32_t TM_Q = 0, TM_S = 64, TM_O = 192, TM_COLS = 512;
+constexpr uint32_t TM_Q = 0, TM_S = 64, TM_O = 256, TM_COLS = 512;
 constexpr int WARPS = 20, THREADS = WARPS * 32, CONV_WARPS = 8;
 // registers: 640 x 96 at launch = 128 x (3 x 72 + 2 x 128) after the split
 constexpr int REGS_SERVICE = 72, REGS_SOFTMAX = 128;
@@ -74,11 +76,12 @@ enum {
     B_K_EMPTY = B_K_FULL + KBUFS,
     B_V_FULL = B_K_EMPTY + KBUFS,
     B_V_EMPTY = B_V_FULL + VBUFS,
-    B_S = B_V_EMPTY + VBUFS,                             // per half: S ready
-    B_P = B_S + 2,                                      // per half: P written
-    B_O = B_P + 2,                                      // per half: O final
-    B_TURN = B_O + 2,                                   // per half: its MMA warp's turn
-    B_Q_READY = B_TURN + 2,
+    B_S = B_V_EMPTY + VBUFS,                            // per softmax half and its tile mod 3: S ready
+    B_P = B_S + 6,                                      // ... P written
+    B_S_EMPTY = B_P + 6,                                // per S buffer: P.V of the P over it complete
+    B_PV = B_S_EMPTY + 3,                               // per half: its last P.V complete
+    B_O = B_PV + 2,                                     // per half: O final
+    B_Q_READY = B_O + 2,
     B_IDLE = B_Q_READY + 1,
     B_PAIR = B_IDLE + 1,                                // per TMEM lane quarter: its two softmax warps
     B_COUNT = B_PAIR + 4
@@ -129,10 +132,9 @@ __global__ void __launch_bounds__(THREADS, 1) attention_int4_tc_kernel(AttnParam
         for (int i = 0; i < B_COUNT; ++i) {
             int count = 1;
             if ((i >= B_STG_EMPTY && i < B_K_EMPTY) || (i >= B_V_FULL && i < B_V_EMPTY)) count = CONV_WARPS;
-            if ((i >= B_K_EMPTY && i < B_V_FULL) || (i >= B_V_EMPTY && i < B_S)) count = 2;    // MMA warps
-            if (i >= B_P && i < B_O) count = 4;
+            if (i >= B_P && i < B_S_EMPTY) count = 4;
             if (i == B_Q_READY) count = 8;
-            if (i == B_IDLE || i >= B_PAIR) count = 2;
+            if (i >= B_IDLE) count = 2;
             mbar_init(bar(i), count);
         }
         fence_barrier_init();
@@ -258,9 +260,10 @@ __global__ void __launch_bounds__(THREADS, 1) attention_int4_tc_kernel(AttnParam
         }
         // this half's maximum and sum
         float m_run = -INFINITY, l_run = 0.f;
-        const uint32_t s_col = lane_base + TM_S + 64 * half, o_col = lane_base + TM_O + 128 * half;
+        const uint32_t o_col = lane_base + TM_O + 128 * half;
         for (int t = 0; t < n_tiles && ok; ++t) {
-            ok = __all_sync(0xffffffffu, mbar_wait(bar(B_S + half), t & 1));
+            const uint32_t s_col = lane_base + TM_S + 64 * ((2 * t + half) % 3);
+            ok = __all_sync(0xffffffffu, mbar_wait(bar(B_S + 3 * half + t % 3), (t / 3) & 1));
             if (!ok) break;
             fence_after();
             const int k0 = k_begin + t * NK + 64 * half;    // first key of this half
@@ -297,7 +300,10 @@ __global__ void __launch_bounds__(THREADS, 1) attention_int4_tc_kernel(AttnParam
                 const float tmax = max3(m4[0], m4[1], fmaxf(m4[2], m4[3])) * mult;
                 const bool rescale = (m_run != -INFINITY) && (tmax > m_run + GROW);
                 if (__any_sync(0xffffffffu, rescale)) {
-                    // S(t) ready means that this half's P.V up to t - 1 is complete
+                    // O holds P.V up to tile t - 1 (t > 0: m_run was set): wait for it
+                    ok = __all_sync(0xffffffffu, mbar_wait(bar(B_PV + half), (t - 1) & 1));
+                    if (!ok) break;
+                    fence_after();
                     const float alpha = rescale ? ex2(m_run - tmax) : 1.0f;
 #pragma unroll 1
                     for (int c = 0; c < 128; c += 32) {
@@ -342,7 +348,7 @@ __global__ void __launch_bounds__(THREADS, 1) attention_int4_tc_kernel(AttnParam
             tmem_wait_st();
             fence_before();
             __syncwarp();
-            if (lane == 0) mbar_arrive(bar(B_P + half));
+            if (lane == 0) mbar_arrive(bar(B_P + 3 * half + t % 3));
         }
         // ------------------------------------------------------------ epilogue
         // both halves' O and (max, sum); this thread merges 64 dims of its row
@@ -440,45 +446,55 @@ __global__ void __launch_bounds__(THREADS, 1) attention_int4_tc_kernel(AttnParam
             // never leave with copies into this CTA's shared memory in flight
             for (int t = max(0, issued - STAGES); t < issued; ++t) mbar_wait(bar(B_STG_FULL + t % STAGES), (t / STAGES) & 1);
             __syncwarp();
-        } else if (warp < 3) {
+        } else if (warp == 1 || warp == 2) {
             // ------------------------------------------------------ MMA issue
             constexpr uint32_t ID_QK = idesc(128, NK / 2, false), ID_PV = idesc(128, 128, true);
             const bool leader = elect_one();
-            const int half = warp - 1;
-            const uint32_t s_col = tmem + TM_S + 64 * half, o_col = tmem + TM_O + 128 * half;
-            const uint32_t k_lo = desc_lo(smem_u32(kbuf) + half * (64 * 128), 16);
-            const uint32_t v_lo = desc_lo(smem_u32(vbuf) + half * (64 * 128), HALF);
-            ok = mbar_wait(bar(B_Q_READY), 0);
-            for (int t = 0; t <= n_tiles; ++t) {
-                const int tb = t & 1, ub = (t + VBUFS - 1) % VBUFS;     // K buffer of this tile, V of the one before
-                if (ok && t < n_tiles) ok = mbar_wait(bar(B_K_FULL + tb), (t >> 1) & 1);
-                if (ok && t > 0) ok = mbar_wait(bar(B_V_FULL + ub), ((t - 1) / VBUFS) & 1);
-                if (ok && t > 0) ok = mbar_wait(bar(B_P + half), (t - 1) & 1);
-                if (ok && (half == 1 || t > 0)) ok = mbar_wait(bar(B_TURN + half), (half == 1 ? t : t - 1) & 1);
-                ok = __all_sync(0xffffffffu, ok);
-                if (!ok) break;
-                fence_after();
-                if (leader) {
-                    if (t > 0) {
-                        // O += P(t - 1) V(t - 1), 64 keys
-#pragma unroll
-                        for (int kk = 0; kk < 4; ++kk)
-                            mma_ts(o_col, s_col + 8 * kk, v_lo + ((ub * BUF + kk * 2048) >> 4), ID_PV, t > 1 || kk > 0);
-                    }
-                    if (t < n_tiles) {
-                        // S = Q K(t)^T over P(t - 1), which the MMAs above have read
+            const int n_half = 2 * n_tiles;
+            if (warp == 1) {
+                // S(u) = Q K^T; the K buffer is free once the second half has read it
+                const uint32_t k_lo = desc_lo(smem_u32(kbuf), 16);
+                ok = mbar_wait(bar(B_Q_READY), 0);
+                for (int u = 0; u < n_half; ++u) {
+                    const int t = u >> 1, h = u & 1, tb = t % KBUFS, sb = u % 3;
+                    if (ok && h == 0) ok = mbar_wait(bar(B_K_FULL + tb), (t / KBUFS) & 1);
+                    if (ok && u >= 3) ok = mbar_wait(bar(B_S_EMPTY + sb), (u / 3 - 1) & 1);
+                    ok = __all_sync(0xffffffffu, ok);
+                    if (!ok) break;
+                    fence_after();
+                    if (leader) {
 #pragma unroll
                         for (int ks = 0; ks < 8; ++ks)
-                            mma_ts(s_col, tmem + TM_Q + 8 * ks,
-                                   k_lo + ((tb * BUF + (ks >> 2) * HALF + (ks & 3) * 32) >> 4), ID_QK, ks > 0);
-                        mma_commit(bar(B_S + half));
+                            mma_ts(tmem + TM_S + 64 * sb, tmem + TM_Q + 8 * ks,
+                                   k_lo + ((tb * BUF + h * (64 * 128) + (ks >> 2) * HALF + (ks & 3) * 32) >> 4), ID_QK,
+                                   ks > 0);
+                        mma_commit(bar(B_S + 3 * h + t % 3));
+                        if (h == 1) mma_commit(bar(B_K_EMPTY + tb));
                     }
-                    mbar_arrive(bar(B_TURN + 1 - half));
-                    if (t < n_tiles) mma_commit(bar(B_K_EMPTY + tb));
-                    if (t > 0) mma_commit(bar(B_V_EMPTY + ub));
-                    if (t == n_tiles) mma_commit(bar(B_O + half));
+                    __syncwarp();
                 }
-                __syncwarp();
+            } else {
+                // O += P(u) V
+                const uint32_t v_lo = desc_lo(smem_u32(vbuf), HALF);
+                for (int u = 0; u < n_half; ++u) {
+                    const int t = u >> 1, h = u & 1, vb = t % VBUFS, sb = u % 3;
+                    if (h == 0) ok = mbar_wait(bar(B_V_FULL + vb), (t / VBUFS) & 1);
+                    if (ok) ok = mbar_wait(bar(B_P + 3 * h + t % 3), (t / 3) & 1);
+                    ok = __all_sync(0xffffffffu, ok);
+                    if (!ok) break;
+                    fence_after();
+                    if (leader) {
+#pragma unroll
+                        for (int kk = 0; kk < 4; ++kk)
+                            mma_ts(tmem + TM_O + 128 * h, tmem + TM_S + 64 * sb + 8 * kk,
+                                   v_lo + ((vb * BUF + h * (64 * 128) + kk * 2048) >> 4), ID_PV, t > 0 || kk > 0);
+                        mma_commit(bar(B_PV + h));
+                        mma_commit(bar(B_S_EMPTY + sb));
+                        if (h == 1) mma_commit(bar(B_V_EMPTY + vb));
+                        if (t == n_tiles - 1) mma_commit(bar(B_O + h));
+                    }
+                    __syncwarp();
+                }
             }
             // nothing the tensor cores still run may outlive the TMEM allocation
             if (leader) mma_commit(bar(B_IDLE));
