@@ -51,12 +51,12 @@ int status_attention_int4_tc(unsigned int* s, int clear) { return read_status(s,
 namespace i4tc {
 
 constexpr int NK = 128;                                 // keys per tile
-constexpr int STAGES = 3;
+constexpr int STAGES = 5;
 constexpr int OFF_V = NK * kInt4CodeBytes;              // of a stage: K codes, V codes, K scales, V scales
 constexpr int OFF_KS = 2 * NK * kInt4CodeBytes;
 constexpr int OFF_VS = OFF_KS + NK * kInt4ScaleBytes;
 constexpr int STAGE_BYTES = OFF_VS + NK * kInt4ScaleBytes;
-constexpr int KBUFS = 2, VBUFS = 3;                     // widened tiles
+constexpr int KBUFS = 2, VBUFS = 2;                     // widened tiles
 constexpr int BUF = NK * 256, HALF = BUF / 2;           // two blocks of 128 keys x 64 dims (128-byte swizzled)
 constexpr int XCH_BYTES = 2 * 128 * 8;                  // (max, sum) of [half][row]
 constexpr int SMEM = (KBUFS + VBUFS) * BUF + STAGES * STAGE_BYTES + XCH_BYTES + 1024 + 512;
@@ -514,29 +514,44 @@ __global__ void __launch_bounds__(THREADS, 1) attention_int4_tc_kernel(AttnParam
 #pragma unroll
             for (int u = 0; u < 4; ++u)
                 at[u] = smem_u32(kbuf) + (cc >> 1) * HALF + r0 * 128 + (((4 * (cc & 1) + u) ^ (r0 & 7)) << 4);
-            for (int t = 0; t < n_tiles; ++t) {
-                const int s = t % STAGES, tb = t % KBUFS, vb = t % VBUFS;
-                ok = mbar_wait(bar(B_STG_FULL + s), (t / STAGES) & 1);
-                if (!__all_sync(0xffffffffu, ok)) { ok = false; break; }
-                const uint8_t* src = stg + s * STAGE_BYTES;
-                // keys outside every row's range get V scale 0: whatever their
-                // bytes are, zeros reach the output
-                const int k0 = k_begin + t * NK;
-                const int zlo = lo0 - k0, zhi = min(min(NK, (n_pages - t * PPT) * PS), hi0 + 1 - k0);
-                uint4 kc[2], vc[2];
-                uint32_t ksc[2], vsc[2];
+            uint4 kc[2], vc[2];
+            uint32_t ksc[2], vsc[2];
+            auto load_k = [&](int t) {
+                const uint8_t* src = stg + (t % STAGES) * STAGE_BYTES;
 #pragma unroll
                 for (int u = 0; u < 2; ++u) {
                     const int r = r0 + 64 * u;
                     kc[u] = *(const uint4*)(src + r * 64 + cc * 16);
                     ksc[u] = *(const uint16_t*)(src + OFF_KS + r * 8 + 2 * cc);
+                }
+            };
+            auto load_v = [&](int t) {
+                const uint8_t* src = stg + (t % STAGES) * STAGE_BYTES;
+                // keys outside every row's range get V scale 0: whatever their
+                // bytes are, zeros reach the output
+                const int k0 = k_begin + t * NK;
+                const int zlo = lo0 - k0, zhi = min(min(NK, (n_pages - t * PPT) * PS), hi0 + 1 - k0);
+#pragma unroll
+                for (int u = 0; u < 2; ++u) {
+                    const int r = r0 + 64 * u;
                     vc[u] = *(const uint4*)(src + OFF_V + r * 64 + cc * 16);
                     vsc[u] = *(const uint16_t*)(src + OFF_VS + r * 8 + 2 * cc);
                     if (r < zlo || r >= zhi) vsc[u] = 0;
                 }
-                if (t >= KBUFS) ok = mbar_wait(bar(B_K_EMPTY + tb), (t / KBUFS - 1) & 1);
-                if (!__all_sync(0xffffffffu, ok)) { ok = false; break; }
-                if (lane == 0) mbar_arrive(bar(B_STG_EMPTY + s));       // the stage is in registers
+            };
+            ok = __all_sync(0xffffffffu, mbar_wait(bar(B_STG_FULL), 0));
+            if (ok) {
+                load_k(0);
+                load_v(0);
+                __syncwarp();
+                if (lane == 0) mbar_arrive(bar(B_STG_EMPTY));           // the stage is in registers
+            }
+            for (int t = 0; t < n_tiles && ok; ++t) {
+                // K of this tile, then the next stage's K on its way while V of
+                // this tile is widened
+                const int tb = t % KBUFS, vb = t % VBUFS, s1 = (t + 1) % STAGES;
+                if (t >= KBUFS) ok = __all_sync(0xffffffffu, mbar_wait(bar(B_K_EMPTY + tb), (t / KBUFS - 1) & 1));
+                if (!ok) break;
                 uint32_t to[4];
 #pragma unroll
                 for (int u = 0; u < 4; ++u) to[u] = at[u] + tb * BUF;
@@ -545,8 +560,13 @@ __global__ void __launch_bounds__(THREADS, 1) attention_int4_tc_kernel(AttnParam
                 fence_proxy_async();
                 __syncwarp();
                 if (lane == 0) mbar_arrive(bar(B_K_FULL + tb));
-                if (t >= VBUFS) ok = mbar_wait(bar(B_V_EMPTY + vb), (t / VBUFS - 1) & 1);
-                if (!__all_sync(0xffffffffu, ok)) { ok = false; break; }
+                if (t + 1 < n_tiles) {
+                    ok = __all_sync(0xffffffffu, mbar_wait(bar(B_STG_FULL + s1), ((t + 1) / STAGES) & 1));
+                    if (!ok) break;
+                    load_k(t + 1);
+                }
+                if (t >= VBUFS) ok = __all_sync(0xffffffffu, mbar_wait(bar(B_V_EMPTY + vb), (t / VBUFS - 1) & 1));
+                if (!ok) break;
 #pragma unroll
                 for (int u = 0; u < 4; ++u) to[u] = at[u] + (KBUFS + vb) * BUF;
                 widen_chunk<0>(to, vc[0], vsc[0]);
@@ -554,6 +574,11 @@ __global__ void __launch_bounds__(THREADS, 1) attention_int4_tc_kernel(AttnParam
                 fence_proxy_async();
                 __syncwarp();
                 if (lane == 0) mbar_arrive(bar(B_V_FULL + vb));
+                if (t + 1 < n_tiles) {
+                    load_v(t + 1);
+                    __syncwarp();
+                    if (lane == 0) mbar_arrive(bar(B_STG_EMPTY + s1));
+                }
             }
         }
     }
