@@ -130,6 +130,29 @@ def test_many_sequences():
 
 
 @pytest.mark.gpu
+def test_only_empty_sequences():
+    q, k, v, _ = _inputs(3, [5], 4, 1)
+    out = torch.full_like(q, 3.0)
+    cu = torch.tensor([2, 2, 2, 2], dtype=torch.int32, device="cuda")
+    fp8kv.fp8kv_prompt_attention(q, k, v, cu, 0, SM, out=out)
+    assert bool((out == 3.0).all())
+
+
+@pytest.mark.gpu
+def test_rows_beyond_four_gigabytes():
+    """2001 sequences of up to 130 tokens, 72 heads: q and out of more than 2^32
+    bytes; the first and the last sequences against the definition."""
+    rng = np.random.default_rng(2)
+    lens = [int(n) for n in rng.integers(120, 131, 2001)]
+    q, k, v, cu = _inputs(14, lens, 9, 8)
+    assert q.numel() * 2 > 2 ** 32
+    out = fp8kv.fp8kv_prompt_attention(q, k, v, cu, 130, SM)
+    _check(out, q, k, v, cu[:4], -1)
+    _check(out, q, k, v, cu[-4:], -1)
+    _check(out, q, k, v, cu[1850:1853], -1)
+
+
+@pytest.mark.gpu
 @pytest.mark.parametrize("window", [-1, 60])
 def test_rows_of_no_sequence_may_hold_anything(window):
     """NaN and infinities before the first sequence, behind the last one and in

@@ -75,8 +75,8 @@ enum {
     B_STAGED = B_OE + 2,                        // per row tile: output tile written
     B_SENT = B_STAGED + 2,                      // ... and read by its store
     B_TURN = B_SENT + 2,                        // per row tile: its MMA warp's turn
-    B_RAW = B_TURN + 2,                         // last V tile loaded, to be cleaned
-    B_ITEM = B_RAW + 1,                         // per queue entry: written
+    B_RAW = B_TURN + 2,                         // per slot: an item's last V tile loaded, to be cleaned
+    B_ITEM = B_RAW + SLOTS,                     // per queue entry: written
     B_TAKEN = B_ITEM + QUEUE,                   // ... read by every role
     B_NEXT = B_TAKEN + QUEUE,                   // answer of a cancel request
     B_IDLE = B_NEXT + 1,                        // per MMA warp: nothing outstanding
@@ -150,8 +150,9 @@ struct Item {
     // keys k .. k + 63: does any row of row tile i see one of them?
     __device__ __forceinline__ bool live(int i, int k) const { return k <= key_hi(i) && k + NK / 2 > key_lo(i); }
     // the last V tile has rows that none of the item's rows sees: it lands on
-    // a barrier of its own, for warp 3, which clears those rows and then
-    // arrives on the slot's barrier
+    // its slot's second barrier, for warp 3, which clears those rows and then
+    // arrives on the slot's first (one barrier for all slots would take the
+    // loads of two short items at once)
     __device__ __forceinline__ bool cleaned() const { return n * NK > see_hi - see_lo + 1; }
 };
 
@@ -228,7 +229,8 @@ __global__ void __launch_bounds__(THREADS, 1)
         asm volatile("createpolicy.fractional.L2::evict_normal.b64 %0, 1.0;" : "=l"(keep));
         const uint64_t once = policy_evict_first();
         int4 e;
-        int done = 0, q_use[2] = {0, 0}, raw_use = 0;
+        int done = 0, q_use[2] = {0, 0};
+        uint32_t raw_now = 0, raw_odd = 0;                  // slots that hold a tile to be cleaned; slots with an odd number of such
         while (next_item(e)) {
             const Item it(e, P);
             if (lane == 0) {
@@ -247,9 +249,11 @@ __global__ void __launch_bounds__(THREADS, 1)
                     if (use > 0) ok = mbar_wait(bar(B_EMPTY + s), (use - 1) & 1);
                     if (!ok) break;
                     uint32_t full = bar(B_FULL + s);
+                    raw_now &= ~(1u << s);
                     if (u == 2 * it.n - 1 && it.cleaned()) {
-                        full = bar(B_RAW);
-                        ++raw_use;
+                        full = bar(B_RAW + s);
+                        raw_now |= 1u << s;
+                        raw_odd ^= 1u << s;
                     }
                     mbar_expect_tx(full, SLOT);
                     for (int h = 0; h < 2; ++h)
@@ -268,8 +272,11 @@ __global__ void __launch_bounds__(THREADS, 1)
             for (int i = 0; i < 2; ++i) {
                 if (q_use[i]) mbar_wait(bar(B_Q + i), (q_use[i] - 1) & 1);
             }
-            if (raw_use) mbar_wait(bar(B_RAW), (raw_use - 1) & 1);
-            for (int u = max(0, done - SLOTS); u < done; ++u) mbar_wait(bar(B_FULL + u % SLOTS), (u / SLOTS) & 1);
+            for (int u = max(0, done - SLOTS); u < done; ++u) {
+                const int t = u % SLOTS;
+                if (raw_now >> t & 1) mbar_wait(bar(B_RAW + t), (raw_odd >> t & 1) ^ 1);
+                else mbar_wait(bar(B_FULL + t), (u / SLOTS) & 1);
+            }
         }
         __syncwarp();
     } else if (warp < 3) {
@@ -286,7 +293,7 @@ __global__ void __launch_bounds__(THREADS, 1)
                 phase ^= 1;
             }
         };
-        int tile = 0, items = 0, turns = 0;                            // key tiles and items of this row tile so far
+        int tile = 0, items = 0, turns = 0;                 // key tiles and items of this row tile, steps of both, so far
         int4 e;
         while (next_item(e)) {
             const Item it(e, P);
@@ -405,15 +412,17 @@ __global__ void __launch_bounds__(THREADS, 1)
             __syncwarp();
             ++put;
         };
-        int base = 0, raw_use = 0;
+        int base = 0;
+        uint32_t raw_odd = 0;                               // slots with an odd number of tiles cleaned
         auto clean = [&](int4 e) {
             const Item it(e, P);
             base += 2 * it.n;
             if (!it.cleaned()) return;
-            ok = __all_sync(0xffffffffu, mbar_wait(bar(B_RAW), raw_use & 1));
+            const int s = (base - 1) % SLOTS;
+            ok = __all_sync(0xffffffffu, mbar_wait(bar(B_RAW + s), raw_odd >> s & 1));
             if (!ok) return;
-            ++raw_use;
-            const int s = (base - 1) % SLOTS, z = it.see_hi - it.see_lo - (it.n - 1) * NK + 1;
+            raw_odd ^= 1u << s;
+            const int z = it.see_hi - it.see_lo - (it.n - 1) * NK + 1;
             uint8_t* vt = ring + s * SLOT;
             for (int i = z * 8 + lane; i < NK * 8; i += 32) {   // rows [z, 128)
                 *(uint4*)(vt + i * 16) = make_uint4(0, 0, 0, 0);
