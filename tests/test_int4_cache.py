@@ -377,6 +377,57 @@ def test_noalloc_prepared_and_captured_calls(M):
 
 
 @pytest.mark.gpu
+def test_binding_refuses_what_the_library_cannot_see():
+    lay, q, kc, vc, ks, vs, k, v, slots = _case(37, [100, 50], 1, 9, 2, 32)
+    bt, sl = lay.block_table.cuda(), lay.seq_lens.cuda()
+    good = dict(q=q, k_cache=kc, v_cache=vc, block_table=bt, seq_lens=sl, max_seq_len=100, k_scale=ks, v_scale=vs,
+                sm_scale=SM)
+    for over in ({"k_scale": ks.cpu()}, {"v_scale": vs.double()}, {"k_scale": ks.repeat(2)}, {"seq_lens": sl[:1]},
+                 {"block_table": bt[:1]}, {"out": torch.empty_like(q)[:1]}, {"out": torch.empty_like(q).float()},
+                 {"num_pages": kc.shape[0] + 1}, {"v_cache": vc[:1]}, {"q": q.float()}):
+        with pytest.raises(ValueError):
+            fp8kv.fp8kv_paged_attention(**{**good, **over})
+        with pytest.raises(ValueError):
+            fp8kv.PreparedAttention(**{**good, **over})
+    for bad in ((k[:, :1], v[:, :1], slots), (k, v[:5], slots), (k, v, slots[:5])):
+        with pytest.raises(ValueError):
+            fp8kv.fp8kv_cache_insert(bad[0].contiguous(), bad[1].contiguous(), bad[2], ks, vs, kc, vc)
+    with pytest.raises(ValueError):
+        fp8kv.fp8kv_cache_gather(slots, ks, vs, kc, vc, k_out=k[:3])
+    with pytest.raises(fp8kv.Fp8kvError):                       # 17 rows per sequence
+        fp8kv.fp8kv_paged_attention(**{**good, "q": q.repeat(1, 17, 1, 1)})
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("M", [1, 12])
+def test_pages_beyond_four_gigabytes(M):
+    """A pool of more than 2^32 bytes; the sequence's pages at both ends of it."""
+    ps, H, G = 64, 8, 9
+    pages = 2 ** 32 // (H * ps * 72) + 64
+    kc = torch.empty((pages, H, ps * 72), dtype=torch.uint8, device="cuda")
+    vc = torch.empty_like(kc)
+    ids = torch.tensor([[pages - 1, 0, pages - 3, 1]], dtype=torch.int32)
+    for i in ids[0].tolist():
+        kc[i], vc[i] = 0x7F, 0x7F
+    g = torch.Generator(device="cuda").manual_seed(M)
+    L = 250
+    k, v = (torch.randn((L, H, 128), generator=g, device="cuda").to(torch.bfloat16) for _ in range(2))
+    q = torch.randn((1, M, G * H, 128), generator=g, device="cuda").to(torch.bfloat16)
+    pos = torch.arange(L)
+    slots = (ids[0].long()[pos // ps] * ps + pos % ps).cuda()
+    ks, vs = _scale(6 / 448), _scale(5 / 448)
+    fp8kv.fp8kv_cache_insert(k, v, slots, ks, vs, kc, vc)
+    ko, vo = fp8kv.fp8kv_cache_gather(slots, ks, vs, kc, vc)
+    n, sc = int4_np.encode_rows(k.float().cpu().numpy(), ks.item())
+    want = torch.from_numpy(n * np.repeat(int4_np.e4m3_value(sc), 16, -1)).float() * ks.cpu()
+    assert torch.equal(ko.cpu(), want.to(torch.bfloat16))
+    sl = torch.tensor([L], dtype=torch.int32, device="cuda")
+    out = fp8kv.fp8kv_paged_attention(q, kc, vc, ids.cuda(), sl, L, ks, vs, SM)
+    small = gen.PagedLayout(ps, 4, torch.arange(4, dtype=torch.int32)[None], sl.cpu())
+    _check(out, small, q, kc[ids[0].long().cuda()], vc[ids[0].long().cuda()], ks, vs, ps)
+
+
+@pytest.mark.gpu
 def test_page_order_does_not_matter():
     lay, q, kc, vc, ks, vs, k, v, slots = _case(31, [900], 12, 9, 2, 32)
     fp8kv.fp8kv_cache_insert(k, v, slots, ks, vs, kc, vc)

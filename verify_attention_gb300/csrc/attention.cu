@@ -1075,6 +1075,7 @@ static int attention_call(const void* k_new, const void* v_new, const void* q, c
     // which serves at most 16 rows per sequence and 144 per KV head
     const bool use_tc = fp8 && tc_rows(M, Hq, Hkv) && (plan.split_tokens % tc_tile_tokens()) == 0;
     if (!use_tc && tc_only(M, Hq, Hkv)) return FP8KV_ERR_UNSUPPORTED;
+    if (int4 && (int64_t)Hkv * ceil_div((int64_t)M * (Hq / Hkv), 16) > 65535) return FP8KV_ERR_UNSUPPORTED;   // grid
     if (B == 0) return FP8KV_OK;                                // nothing to do; no pointer is read
     if (!q || !k_cache || !v_cache || !block_table || !seq_lens || !out) return FP8KV_ERR_INVALID_ARG;
     if ((k_new != nullptr) != (v_new != nullptr) || (k_new && (!al16(k_new) || !al16(v_new))))
@@ -1150,9 +1151,9 @@ static int attention_call(const void* k_new, const void* v_new, const void* q, c
         }
         // more than 16 rows per KV head and partitions of whole 128-key tiles:
         // the tcgen05 kernel, whose cost does not depend on the rows up to 128
-        // (64 sequences, 108 rows: INT4_TC_US us; the mma.sync kernel, which
-        // widens every key again for each 16 rows, 3097 us; one tile of 16
-        // rows: ROWS16)
+        // (64 sequences, 108 rows: 624 us; the mma.sync kernel, which widens
+        // every key again for each 16 rows, 3097 us, but 349 us for one tile
+        // of 9 rows)
         const bool tc = tc_rows(M, Hq, Hkv) && plan.split_tokens % tc_tile_tokens() == 0;
         const bool lpt = B > 1 && (tc ? row_tiles(M, Hq, Hkv) : P.NT) == 1 && plan.num_splits > 1 &&
                          plan.split_tokens % tc_tile_tokens() == 0 &&

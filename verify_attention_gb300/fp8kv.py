@@ -166,10 +166,27 @@ def fp8kv_cache_insert(k, v, slot_mapping, k_scale, v_scale, k_cache, v_cache, s
     _check("fp8kv_cache_insert", rc)
 
 
+def _int4_call(q, k_cache, block_table, seq_lens, k_scale, v_scale, out, num_pages):
+    """Checks of an attention call over an INT4 cache beyond the library's own:
+    what it cannot see from pointers."""
+    B = q.shape[0]
+    if block_table.dim() != 2 or block_table.shape[0] != B or seq_lens.numel() != B:
+        raise ValueError(f"block_table must be [{B}][pages] and seq_lens [{B}]")
+    for t, n in ((k_scale, "k_scale"), (v_scale, "v_scale")):
+        if _dev(t, n, torch.float32).numel() != 1:
+            raise ValueError(f"{n} must be one fp32")
+    if out is not None and _dev(out, "out", torch.bfloat16).shape != q.shape:
+        raise ValueError("out must have the shape of q")
+    if num_pages is not None and num_pages > k_cache.shape[0]:
+        raise ValueError(f"num_pages is {num_pages}, the cache has {k_cache.shape[0]}")
+
+
 def _int4_rows(k, v, slot_mapping, heads, k_scale, v_scale):
     if v.shape != k.shape or k.shape[1] != heads or slot_mapping.numel() != k.shape[0]:
         raise ValueError(f"k, v must be [T][{heads}][D] and slot_mapping [T]")
-    _dev(k_scale, "k_scale", torch.float32), _dev(v_scale, "v_scale", torch.float32)
+    for t, n in ((k_scale, "k_scale"), (v_scale, "v_scale")):
+        if _dev(t, n, torch.float32).numel() != 1:
+            raise ValueError(f"{n} must be one fp32")
 
 
 def fp8kv_cache_gather(slot_mapping, k_scale, v_scale, k_cache, v_cache, k_out=None, v_out=None, stream=None):
@@ -302,6 +319,8 @@ def fp8kv_paged_attention(q, k_cache, v_cache, block_table, seq_lens, max_seq_le
     _dev(block_table, "block_table", torch.int32), _dev(seq_lens, "seq_lens", torch.int32)
     B, M, Hq, D = q.shape
     P, Hkv, page_size = _cache_shape(k_cache, v_cache, dt)
+    if dt == FP8KV_CACHE_INT4:
+        _int4_call(q, k_cache, block_table, seq_lens, k_scale, v_scale, out, num_pages)
     if num_pages is None:
         num_pages = P
     need = fp8kv_paged_attention_workspace_size(B, M, Hq, Hkv, D, page_size, max_seq_len, window_left,
@@ -330,6 +349,8 @@ def fp8kv_append_paged_attention(k_new, v_new, q, k_cache, v_cache, block_table,
     _dev(block_table, "block_table", torch.int32), _dev(seq_lens, "seq_lens", torch.int32)
     B, M, Hq, D = q.shape
     P, Hkv, page_size = _cache_shape(k_cache, v_cache, dt)
+    if dt == FP8KV_CACHE_INT4:
+        _int4_call(q, k_cache, block_table, seq_lens, k_scale, v_scale, out, num_pages)
     if tuple(k_new.shape) != (B, M, Hkv, D) or tuple(v_new.shape) != (B, M, Hkv, D):
         raise ValueError("k_new, v_new must be [B][M][Hkv][D]")
     if num_pages is None:
@@ -411,6 +432,8 @@ class PreparedAttention:
         _dev(block_table, "block_table", torch.int32), _dev(seq_lens, "seq_lens", torch.int32)
         B, M, Hq, D = q.shape
         P, Hkv, page_size = _cache_shape(k_cache, v_cache, dt)
+        if dt == FP8KV_CACHE_INT4:
+            _int4_call(q, k_cache, block_table, seq_lens, k_scale, v_scale, out, num_pages)
         if (k_new is None) != (v_new is None):
             raise ValueError("k_new and v_new go together")
         if k_new is not None:
@@ -459,6 +482,8 @@ def fp8kv_paged_attention_noalloc(q, k_cache, v_cache, block_table, seq_lens, ma
         raise ValueError(f"out must have the shape and device of q {tuple(q.shape)}, got {tuple(out.shape)}")
     B, M, Hq, D = q.shape
     P, Hkv, page_size = _cache_shape(k_cache, v_cache, dt)
+    if dt == FP8KV_CACHE_INT4:
+        _int4_call(q, k_cache, block_table, seq_lens, k_scale, v_scale, out, num_pages)
     rc = lib().fp8kv_paged_attention_noalloc(
         _ptr(q), _ptr(k_cache), _ptr(v_cache), dt, _ptr(block_table), block_table.shape[1], _ptr(seq_lens),
         int(max_seq_len), B, M, Hq, Hkv, D, page_size, int(P if num_pages is None else num_pages),
