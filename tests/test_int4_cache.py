@@ -295,6 +295,57 @@ def test_append_equals_insert_then_attention(lens, M, G, H, ps, window):
 
 
 @pytest.mark.gpu
+@pytest.mark.parametrize("lens,M,G,H,ps,window,split", [
+    ([130, 257, 12, 640], 12, 9, 2, 32, -1, 128), ([130, 128, 1], 1, 9, 3, 32, -1, 128), ([518], 16, 1, 2, 64, -1, 128),
+    ([4100], 12, 9, 1, 64, -1, 1024), ([300, 261], 8, 16, 2, 64, 100, 128), ([1030], 16, 8, 2, 32, 40, 256),
+    ([513, 100], 16, 9, 2, 64, -1, 128), ([40, 700], 3, 9, 1, 32, -1, 0)])
+def test_appended_tokens_on_either_side_of_a_partition(lens, M, G, H, ps, window, split):
+    """New tokens that begin in one partition and end in the next, several times
+    over, with other bytes in their rows before each call."""
+    lay, q, kc, vc, ks, vs, k, v, slots = _case(11 * sum(lens), lens, M, G, H, ps)
+    fp8kv.fp8kv_cache_insert(k, v, slots, ks, vs, kc, vc)
+    want = _attend(lay, q, kc, vc, ks, vs, window, split_tokens=split)
+    _check(want, lay, q, kc, vc, ks, vs, ps, window)
+    new = torch.cat([torch.arange(sum(lens[:b + 1]) - M, sum(lens[:b + 1])) for b in range(len(lens))]).cuda()
+    old = torch.ones(len(slots), dtype=torch.bool, device="cuda")
+    old[new] = False
+    other = torch.full_like(k, float("nan"))
+    kc2, vc2 = kc.clone(), vc.clone()
+    shape = (len(lens), M, H, 128)
+    call = fp8kv.PreparedAttention(q, kc2, vc2, lay.block_table.cuda(), lay.seq_lens.cuda(), max(lens), ks, vs, SM,
+                                   window_left=window, split_tokens=split, k_new=k[new].view(shape).contiguous(),
+                                   v_new=v[new].view(shape).contiguous())
+    for _ in range(20):
+        fp8kv.fp8kv_cache_insert(other, other, torch.where(old, -1, slots), ks, vs, kc2, vc2)
+        out = call()
+        assert torch.equal(kc2, kc) and torch.equal(vc2, vc)
+        assert torch.equal(out, want)
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("M", [1, 12])
+def test_append_to_pages_outside_the_pool(M):
+    """Flagged; those tokens are written nowhere, and their keys read as zeros."""
+    lay, q, kc, vc, ks, vs, k, v, slots = _case(3 + M, [70, 40], M, 9, 2, 32, extra=2)
+    fp8kv.fp8kv_cache_insert(k, v, slots, ks, vs, kc, vc)
+    before = kc.clone(), vc.clone()
+    bt = lay.block_table.clone()
+    bt[0, 2], bt[1, 1] = lay.num_pages, -1
+    new = torch.full((2, M, 2, 128), 100.0, dtype=torch.bfloat16, device="cuda")
+    fp8kv.fp8kv_device_status(clear=True)
+    out = fp8kv.fp8kv_append_paged_attention(new, new, q, kc, vc, bt.cuda(), lay.seq_lens.cuda(), 70, ks, vs, SM)
+    assert fp8kv.fp8kv_device_status(clear=True) != 0
+    changed = [(a != b).any(-1).any(-1).nonzero()[:, 0].tolist() for a, b in zip((kc, vc), before)]
+    # M = 12: tokens 58 .. 63 and 28 .. 31 still lie in good pages
+    good = sorted(int(lay.block_table[b, p]) for b, p in ((0, 1), (1, 0))) if M == 12 else []
+    assert changed == [good, good]
+    zero = gen.PagedLayout(32, lay.num_pages + 1, torch.where((bt < 0) | (bt >= lay.num_pages), lay.num_pages, bt),
+                           lay.seq_lens)
+    pad = [torch.cat([c, torch.zeros_like(c[:1])]) for c in (kc, vc)]
+    _check(out, zero, q, pad[0], pad[1], ks, vs, 32)
+
+
+@pytest.mark.gpu
 @pytest.mark.parametrize("M", [1, 12])
 def test_extreme_scales_logits_and_values(M):
     """Block scales up to 448 (a tensor scale far below the calibrated one) and

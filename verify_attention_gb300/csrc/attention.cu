@@ -1144,18 +1144,22 @@ static int attention_call(const void* k_new, const void* v_new, const void* q, c
         P.k_cache = (uint8_t*)k_cache;
         P.v_cache = (uint8_t*)v_cache;
         P.num_pages = num_pages;
-        if (k_new) {
+        // more than 16 rows per KV head and partitions of whole 128-key tiles:
+        // the tcgen05 kernel, whose cost does not depend on the rows up to 128
+        // (64 sequences, 108 rows: 618 us; the mma.sync kernel, which widens
+        // every key again for each 16 rows, 3097 us, but 348 us for one tile
+        // of 9 rows)
+        const bool tc = tc_rows(M, Hq, Hkv) && plan.split_tokens % tc_tile_tokens() == 0;
+        const bool one_tile = (tc ? row_tiles(M, Hq, Hkv) : P.NT) == 1;
+        if (k_new && one_tile) {                                // appended in the kernel
+            P.k_new = (const uint16_t*)k_new;
+            P.v_new = (const uint16_t*)v_new;
+        } else if (k_new) {
             rc = launch_append_int4(k_new, v_new, seq_lens, block_table, max_pages_per_seq, B, M, Hkv, k_scale,
                                     v_scale, (void*)k_cache, (void*)v_cache, num_pages, page_size, max_seq_len, s);
             if (rc) return rc;
         }
-        // more than 16 rows per KV head and partitions of whole 128-key tiles:
-        // the tcgen05 kernel, whose cost does not depend on the rows up to 128
-        // (64 sequences, 108 rows: 624 us; the mma.sync kernel, which widens
-        // every key again for each 16 rows, 3097 us, but 349 us for one tile
-        // of 9 rows)
-        const bool tc = tc_rows(M, Hq, Hkv) && plan.split_tokens % tc_tile_tokens() == 0;
-        const bool lpt = B > 1 && (tc ? row_tiles(M, Hq, Hkv) : P.NT) == 1 && plan.num_splits > 1 &&
+        const bool lpt = B > 1 && one_tile && plan.num_splits > 1 &&
                          plan.split_tokens % tc_tile_tokens() == 0 &&
                          (int64_t)B * plan.num_splits * Hkv <= INT32_MAX;
         if (lpt) {

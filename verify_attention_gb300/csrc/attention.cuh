@@ -30,7 +30,7 @@ struct AttnParams {
     // launch order) takes slot lpt_order[i / Hkv] and KV head i % Hkv, so
     // that the last CTAs to start are the shortest.  Null: grid order.
     const int32_t* lpt_order;
-    // append (tcgen05 path): the M new tokens of each sequence, bf16
+    // append (tcgen05 path, INT4 paths): the M new tokens of each sequence, bf16
     // [B][M][Hkv][128], are encoded into the cache at positions L - M + m by
     // the CTA whose partition holds them before it loads those pages; null
     // for a plain call

@@ -92,6 +92,27 @@ __device__ __forceinline__ void issue_chunk(uint32_t stage, const Lanes& at, con
     cp16<0, 0>(stage + at.s, sp, bytes);
 }
 
+// Append: the new tokens of sequence b (length L) at positions lo .. hi - 1 of
+// [L - M, L), KV head hk.  Only the CTA that reads them writes them, so no other
+// has to be waited for (one sequence of 256 keys: 7.1 us; the append as a launch
+// of its own 8.7).
+template <int PS>
+__device__ __forceinline__ void append(const AttnParams& P, int b, int hk, int L, int lo, int hi, int thread,
+                                       int threads) {
+    for (int i = thread; i < (hi - lo) * 8; i += threads) {
+        const int pos = lo + (i >> 3), block = i & 7;
+        const int page = P.block_table[(int64_t)b * P.mpps + pos / PS];
+        if (page < 0 || page >= P.num_pages) {
+            if (block == 0) flag(FP8KV_DEV_BAD_SLOT);
+            continue;
+        }
+        const int64_t src = ((((int64_t)b * P.M + (pos - (L - P.M))) * P.Hkv + hk) * 8 + block) * 2;
+        const uint4 *k = (const uint4*)P.k_new + src, *v = (const uint4*)P.v_new + src;
+        Int4Block(k[0], k[1], v[0], v[1], *P.k_scale, *P.v_scale)
+            .store(P.k_cache, P.v_cache, page, pos % PS, hk, P.Hkv, PS, block);
+    }
+}
+
 // WARPS = 12, one CTA per SM, or 4, three CTAs per SM (168 registers a thread).
 template <int PS, int WARPS>
 __global__ void __launch_bounds__(WARPS * 32, 12 / WARPS) paged_attention_int4_kernel(AttnParams P) {
@@ -112,6 +133,22 @@ __global__ void __launch_bounds__(WARPS * 32, 12 / WARPS) paged_attention_int4_k
         b = q / P.num_splits;
         split = q % P.num_splits;
     }
+    // what does not depend on the length is read beside it: q, and the first
+    // page id, right unless a window moves the partition (256 keys: 6.5 us
+    // without, 6.4 with)
+    const int32_t* table = P.block_table + (int64_t)b * P.mpps;
+    constexpr int CPP = PS / CK;                        // chunks per page
+    const int guess_at = min(split * P.split_pages + warp / CPP, P.mpps - 1), guess = table[guess_at];
+    const int R0 = rt * 16;
+    uint4 qw[2][4];
+#pragma unroll
+    for (int hr = 0; hr < 2; ++hr) {
+        const int r = R0 + g + 8 * hr, m = min(r, P.R - 1) / P.G;
+        const uint4* src = (const uint4*)(P.q + (((int64_t)b * P.M + m) * P.Hq + hk * P.G + min(r, P.R - 1) % P.G) * 128) + 4 * t;
+#pragma unroll
+        for (int u = 0; u < 4; ++u) qw[hr][u] = r < P.R ? src[u] : make_uint4(0, 0, 0, 0);
+    }
+    const float ks = *P.k_scale;
     const int L = P.seq_lens[b];
     if (L < P.M || L > P.max_seq_len || (L + PS - 1) / PS > P.mpps) {
         if (threadIdx.x == 0 && split == 0 && blockIdx.y == 0) flag(FP8KV_DEV_BAD_SEQ_LEN);
@@ -130,15 +167,21 @@ __global__ void __launch_bounds__(WARPS * 32, 12 / WARPS) paged_attention_int4_k
     const int n_pages = min(P.split_pages, last_page + 1 - page_begin);
     const int key_begin = page_begin * PS;
     const int n_chunks = (min(n_pages * PS, L - key_begin) + CK - 1) / CK;
-    const int32_t* bt = P.block_table + (int64_t)b * P.mpps + page_begin;
+    const int32_t* bt = table + page_begin;
     const uint32_t ring = smem_u32(smem) + warp * STAGES * STAGE_BYTES;
-    constexpr int CPP = PS / CK;                        // chunks per page
+
+    // append: this partition's new tokens, before its copies read them
+    const int app_lo = max(L - P.M, key_begin), app_hi = min(L, key_begin + n_pages * PS);
+    if (P.k_new && app_lo < app_hi) {                   // uniform over the CTA
+        append<PS>(P, b, hk, L, app_lo, app_hi, threadIdx.x, THREADS);
+        __syncthreads();
+    }
 
     // this warp's chunks: warp, warp + WARPS, ...; their page ids are read one
     // round ahead of the copies
     const Lanes places = lane_places(lane);
     int next = warp;
-    int page = next < n_chunks ? bt[next / CPP] : -1;
+    int page = next < n_chunks ? (page_begin + next / CPP == guess_at ? guess : bt[next / CPP]) : -1;
     auto issue = [&](int slot) {
         if (next < n_chunks) {
             const int cur = page, at = next;
@@ -152,13 +195,11 @@ __global__ void __launch_bounds__(WARPS * 32, 12 / WARPS) paged_attention_int4_k
     for (int s = 0; s < STAGES - 1; ++s) issue(s);
 
     // ---- rows g and g + 8 of the tile: positions, Q fragments
-    const int R0 = rt * 16;
     int pr[2], lor[2];
     float mult[2];
     uint32_t qa[8][4];
     {
         float qf[2][32];
-        const float ks = *P.k_scale;
 #pragma unroll
         for (int hr = 0; hr < 2; ++hr) {
             const int r = R0 + g + 8 * hr;
@@ -166,19 +207,12 @@ __global__ void __launch_bounds__(WARPS * 32, 12 / WARPS) paged_attention_int4_k
             pr[hr] = L - P.M + m;
             lor[hr] = (P.window_left >= 0) ? max(0, pr[hr] - P.window_left) : 0;
 #pragma unroll
-            for (int j = 0; j < 32; ++j) qf[hr][j] = 0.f;
-            if (r < P.R) {
-                const uint4* src =
-                    (const uint4*)(P.q + (((int64_t)b * P.M + m) * P.Hq + hk * P.G + r % P.G) * 128) + 4 * t;
+            for (int u = 0; u < 4; ++u) {
+                const uint32_t ww[4] = {qw[hr][u].x, qw[hr][u].y, qw[hr][u].z, qw[hr][u].w};
 #pragma unroll
-                for (int u = 0; u < 4; ++u) {
-                    const uint4 w = src[u];
-                    const uint32_t ww[4] = {w.x, w.y, w.z, w.w};
-#pragma unroll
-                    for (int e = 0; e < 4; ++e) {
-                        qf[hr][8 * u + 2 * e] = bf16_lo(ww[e]);
-                        qf[hr][8 * u + 2 * e + 1] = bf16_hi(ww[e]);
-                    }
+                for (int e = 0; e < 4; ++e) {
+                    qf[hr][8 * u + 2 * e] = bf16_lo(ww[e]);
+                    qf[hr][8 * u + 2 * e + 1] = bf16_hi(ww[e]);
                 }
             }
             // a power of two that puts the row maximum in [2^4, 2^5): the f16

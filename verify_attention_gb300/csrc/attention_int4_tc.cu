@@ -31,7 +31,11 @@
 //                    2^15, so that f16 keeps 11 bits of every weight down to
 //                    2^-25 of the largest.
 //   warps 12-19      widen K and V into swizzled f16 tiles (five warps took 3700
-//                    cycles a tile)
+//                    cycles a tile).  New tokens (append) are encoded by these
+//                    warps, a block of 16 elements a thread, written to the cache
+//                    and, so that no load has to wait for that, over their rows
+//                    of the staged pages (512 keys: 10.3 us; loads that wait 13.4,
+//                    an append kernel before this one 12.7).
 // TMEM columns: Q 0-63, S/P 3 x 64 (64-255), O 256-383, 384-511.
 #include <stdio.h>
 
@@ -84,7 +88,8 @@ enum {
     B_Q_READY = B_O + 2,
     B_IDLE = B_Q_READY + 1,
     B_PAIR = B_IDLE + 1,                                // per TMEM lane quarter: its two softmax warps
-    B_COUNT = B_PAIR + 4
+    B_APP = B_PAIR + 4,                                 // new tokens written over a staged tile
+    B_COUNT = B_APP + 1
 };
 static_assert(B_COUNT * 8 + 16 <= 512, "barrier area");
 
@@ -134,7 +139,8 @@ __global__ void __launch_bounds__(THREADS, 1) attention_int4_tc_kernel(AttnParam
             if ((i >= B_STG_EMPTY && i < B_K_EMPTY) || (i >= B_V_FULL && i < B_V_EMPTY)) count = CONV_WARPS;
             if (i >= B_P && i < B_S_EMPTY) count = 4;
             if (i == B_Q_READY) count = 8;
-            if (i >= B_IDLE) count = 2;
+            if (i >= B_IDLE && i < B_APP) count = 2;
+            if (i == B_APP) count = CONV_WARPS;
             mbar_init(bar(i), count);
         }
         fence_barrier_init();
@@ -163,6 +169,26 @@ __global__ void __launch_bounds__(THREADS, 1) attention_int4_tc_kernel(AttnParam
             split = q % P.num_splits;
         }
     }
+    // the first page ids, right unless a window moves the partition, are read
+    // beside the length
+    constexpr int PPT = NK / PS;                            // pages per tile
+    int guess_at = -1, guess = -1;
+    if (warp == 0) {
+        guess_at = min(split * P.split_pages + ((lane >> 2) & (PPT - 1)), P.mpps - 1);
+        guess = P.block_table[(int64_t)b * P.mpps + guess_at];
+    }
+    // so are the new tokens: block ct % 8 of token ct / 8 (at most 16)
+    const int ct = threadIdx.x - 12 * 32;
+    const bool has_new = P.k_new && ct >= 0 && ct < P.M * 8;
+    uint4 nk[2] = {}, nv[2] = {};
+    if (has_new) {
+        const int64_t src = ((((int64_t)b * P.M + (ct >> 3)) * P.Hkv + hk) * 8 + (ct & 7)) * 2;
+#pragma unroll
+        for (int u = 0; u < 2; ++u) {
+            nk[u] = ((const uint4*)P.k_new)[src + u];
+            nv[u] = ((const uint4*)P.v_new)[src + u];
+        }
+    }
     const int L = P.seq_lens[b];
     const bool seq_ok = !(L < P.M || L > P.max_seq_len || (L + PS - 1) / PS > P.mpps);
     bool run = seq_ok && have_work;                         // uniform over the CTA
@@ -180,9 +206,12 @@ __global__ void __launch_bounds__(THREADS, 1) attention_int4_tc_kernel(AttnParam
     if (split >= nsplit_b) run = false;
     const int page_begin = first_page + split * P.split_pages;
     const int n_pages = min(P.split_pages, last_page + 1 - page_begin);
-    constexpr int PPT = NK / PS;                            // pages per tile
     const int n_tiles = (n_pages + PPT - 1) / PPT;
     const int k_begin = page_begin * PS;
+    // append: the tiles that hold new tokens ([L - M, L) within the partition)
+    const int app_lo = max(L - P.M, k_begin), app_hi = min(L, k_begin + n_pages * PS);
+    const bool appends = P.k_new && app_lo < app_hi;
+    const int app_t0 = appends ? (app_lo - k_begin) / NK : 1 << 30, app_t1 = appends ? (app_hi - 1 - k_begin) / NK : -1;
     bool ok = true;
 
     if (!run) {
@@ -420,7 +449,7 @@ __global__ void __launch_bounds__(THREADS, 1) attention_int4_tc_kernel(AttnParam
             const uint32_t bytes = kind < 2 ? PS * kInt4CodeBytes : PS * kInt4ScaleBytes;
             const uint32_t off = (kind == 0 ? 0 : kind == 1 ? OFF_V : kind == 2 ? OFF_KS : OFF_VS) + p * bytes;
             int issued = 0;
-            int next = p < PPT && p < n_pages ? bt[p] : -1;
+            int next = p < PPT && p < n_pages ? (page_begin + p == guess_at ? guess : bt[p]) : -1;
             for (int t = 0; t < n_tiles; ++t) {
                 const int s = t % STAGES, use = t / STAGES, page = next, at = t * PPT + p;
                 const bool mine = p < PPT && at < n_pages;
@@ -539,7 +568,36 @@ __global__ void __launch_bounds__(THREADS, 1) attention_int4_tc_kernel(AttnParam
                     if (r < zlo || r >= zhi) vsc[u] = 0;
                 }
             };
+            // this thread's new block: its row of the partition, or none
+            Int4Block fresh;
+            int fresh_row = -1;
+            if (appends && has_new && L - P.M + (ct >> 3) >= app_lo && L - P.M + (ct >> 3) < app_hi) {
+                const int pos = L - P.M + (ct >> 3), page = P.block_table[(int64_t)b * P.mpps + pos / PS];
+                fresh = Int4Block(nk[0], nk[1], nv[0], nv[1], *P.k_scale, *P.v_scale);
+                if (page >= 0 && page < P.num_pages) {
+                    fresh_row = pos - k_begin;
+                    fresh.store(P.k_cache, P.v_cache, page, pos % PS, hk, P.Hkv, PS, ct & 7);
+                } else if ((ct & 7) == 0) {
+                    flag(FP8KV_DEV_BAD_SLOT);
+                }
+            }
+            // the new rows of tile t over its stage
+            auto patch = [&](int t) {
+                uint8_t* dst = stg + (t % STAGES) * STAGE_BYTES;
+                const int r = fresh_row - t * NK;
+                if (fresh_row >= 0 && r >= 0 && r < NK) {
+                    *(uint2*)(dst + r * 64 + 8 * (ct & 7)) = fresh.k;
+                    *(uint2*)(dst + OFF_V + r * 64 + 8 * (ct & 7)) = fresh.v;
+                    dst[OFF_KS + r * 8 + (ct & 7)] = fresh.ks;
+                    dst[OFF_VS + r * 8 + (ct & 7)] = fresh.vs;
+                    fence_proxy_async();                        // before the stage's next load
+                }
+                __syncwarp();
+                if (lane == 0) mbar_arrive(bar(B_APP));
+                ok = __all_sync(0xffffffffu, mbar_wait(bar(B_APP), (t - app_t0) & 1));
+            };
             ok = __all_sync(0xffffffffu, mbar_wait(bar(B_STG_FULL), 0));
+            if (ok && app_t0 == 0) patch(0);
             if (ok) {
                 load_k(0);
                 load_v(0);
@@ -562,6 +620,7 @@ __global__ void __launch_bounds__(THREADS, 1) attention_int4_tc_kernel(AttnParam
                 if (lane == 0) mbar_arrive(bar(B_K_FULL + tb));
                 if (t + 1 < n_tiles) {
                     ok = __all_sync(0xffffffffu, mbar_wait(bar(B_STG_FULL + s1), ((t + 1) / STAGES) & 1));
+                    if (ok && t + 1 >= app_t0 && t + 1 <= app_t1) patch(t + 1);
                     if (!ok) break;
                     load_k(t + 1);
                 }

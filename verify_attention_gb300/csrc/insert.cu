@@ -12,6 +12,7 @@
 // bf16 in and 8 B of codes out with one vector load and one vector store.
 #include "attention.cuh"
 #include "common.cuh"
+#include "int4.cuh"
 
 namespace fp8kv {
 
@@ -113,23 +114,6 @@ int launch_append(const void* k, const void* v, const int32_t* seq_lens, const i
 
 // ------------------------------------------------------- 4-bit insert/append
 
-// One block of 16 elements of K and of V into an INT4 cache row (page, head,
-// offset): 8 code bytes and one scale byte each.
-__device__ __forceinline__ void int4_store(const uint4* __restrict__ k, const uint4* __restrict__ v, int64_t src,
-                                           float ks, float vs, uint8_t* __restrict__ k_cache,
-                                           uint8_t* __restrict__ v_cache, int64_t page, int off, int h, int Hkv,
-                                           int page_size, int block) {
-    const int64_t base = (page * Hkv + h) * page_size * kInt4RowBytes;
-    const int64_t code = base + off * kInt4CodeBytes + block * 8;
-    const int64_t scale = base + page_size * kInt4CodeBytes + off * kInt4ScaleBytes + block;
-    uint8_t sk, sv;
-    const uint2 ck = int4_encode16(k[src], k[src + 1], ks, sk), cv = int4_encode16(v[src], v[src + 1], vs, sv);
-    *reinterpret_cast<uint2*>(k_cache + code) = ck;
-    *reinterpret_cast<uint2*>(v_cache + code) = cv;
-    k_cache[scale] = sk;
-    v_cache[scale] = sv;
-}
-
 // One thread per (token, head, 16-element block) of K and V: 64 bytes in, 18
 // bytes out; the eight threads of a row write its 64 code bytes and its 8
 // scale bytes side by side.
@@ -151,8 +135,8 @@ __global__ void __launch_bounds__(256) insert_int4_kernel(
         return;
     }
     const int64_t page = slot / page_size;
-    int4_store(k, v, 2 * i, *k_scale, *v_scale, k_cache, v_cache, page, (int)(slot - page * page_size), h, Hkv,
-               page_size, block);
+    Int4Block(k[2 * i], k[2 * i + 1], v[2 * i], v[2 * i + 1], *k_scale, *v_scale)
+        .store(k_cache, v_cache, page, (int)(slot - page * page_size), h, Hkv, page_size, block);
 }
 
 // The M new tokens of every sequence to positions L_b - M + m.
@@ -179,7 +163,8 @@ __global__ void __launch_bounds__(256) append_int4_kernel(
         if (block == 0) flag(FP8KV_DEV_BAD_SLOT);
         return;
     }
-    int4_store(k, v, 2 * i, *k_scale, *v_scale, k_cache, v_cache, page, pos % page_size, h, Hkv, page_size, block);
+    Int4Block(k[2 * i], k[2 * i + 1], v[2 * i], v[2 * i + 1], *k_scale, *v_scale)
+        .store(k_cache, v_cache, page, pos % page_size, h, Hkv, page_size, block);
 }
 
 int launch_append_int4(const void* k, const void* v, const int32_t* seq_lens, const int32_t* block_table, int mpps,

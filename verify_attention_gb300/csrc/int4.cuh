@@ -1,7 +1,10 @@
-// int4.cuh -- widening of the INT4 cache's codes, shared by its kernels (the
-// arithmetic is explained at the head of attention_int4.cu).
+// int4.cuh -- writing the INT4 cache's rows, and widening its codes, shared by
+// its kernels (the arithmetic is explained at the head of attention_int4.cu).
 #pragma once
 #include <stdint.h>
+
+#include "attention.cuh"
+#include "common.cuh"
 
 namespace fp8kv {
 
@@ -38,5 +41,27 @@ __device__ __forceinline__ void widen4(uint32_t z, const Scale2& k, uint32_t (&v
     v[2] = hfma2(and_or(y, 0x003c003cu, 0x5c005c00u), k.s, k.c256);
     v[3] = hfma2(and_or(y, 0x03c003c0u, 0x4c004c00u), k.s, k.c16);
 }
+
+// One block of 16 elements of K and of V: 8 code bytes and one scale byte each.
+struct Int4Block {
+    uint2 k, v;
+    uint8_t ks, vs;
+    Int4Block() = default;
+    __device__ __forceinline__ Int4Block(uint4 k0, uint4 k1, uint4 v0, uint4 v1, float kc, float vc) {
+        k = int4_encode16(k0, k1, kc, ks);
+        v = int4_encode16(v0, v1, vc, vs);
+    }
+    // into row `off` of (page, head) of the caches
+    __device__ __forceinline__ void store(uint8_t* __restrict__ k_cache, uint8_t* __restrict__ v_cache, int64_t page,
+                                          int off, int h, int Hkv, int page_size, int block) const {
+        const int64_t base = (page * Hkv + h) * page_size * kInt4RowBytes;
+        const int64_t code = base + off * kInt4CodeBytes + block * 8;
+        const int64_t scale = base + page_size * kInt4CodeBytes + off * kInt4ScaleBytes + block;
+        *reinterpret_cast<uint2*>(k_cache + code) = k;
+        *reinterpret_cast<uint2*>(v_cache + code) = v;
+        k_cache[scale] = ks;
+        v_cache[scale] = vs;
+    }
+};
 
 }  // namespace fp8kv
