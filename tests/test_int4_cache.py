@@ -323,6 +323,29 @@ def test_appended_tokens_on_either_side_of_a_partition(lens, M, G, H, ps, window
 
 
 @pytest.mark.gpu
+@pytest.mark.parametrize("window", [-1, 200])
+@pytest.mark.parametrize("L", [12, 128, 129, 700, 1000, 1001, 5])
+def test_one_sequence_shorter_than_its_partitions(L, window):
+    """Eight partitions that combine in a cluster, of which the sequence fills
+    some; lengths that are refused leave the output as it was."""
+    lay, q, kc, vc, ks, vs, k, v, slots = _case(L, [1100], 12, 9, 2, 32)
+    fp8kv.fp8kv_cache_insert(k, v, slots, ks, vs, kc, vc)
+    lay = gen.PagedLayout(32, lay.num_pages, lay.block_table, torch.tensor([L], dtype=torch.int32))
+    out = torch.full_like(q, 3.0)
+    fp8kv.fp8kv_device_status(clear=True)
+    fp8kv.fp8kv_paged_attention(q, kc, vc, lay.block_table.cuda(), lay.seq_lens.cuda(), 1000, ks, vs, SM, out=out,
+                                window_left=window, split_tokens=128)
+    text = fp8kv.fp8kv_last_dispatch()
+    # the 212 keys that 12 rows see through the window touch at most ceil(212 / 32) + 1 = 8 pages, two partitions
+    assert ("cluster=8" if window < 0 else "cluster=2") in text and "reduce=0" in text
+    if 12 <= L <= 1000:
+        _check(out, lay, q, kc, vc, ks, vs, 32, window)
+        assert fp8kv.fp8kv_device_status(clear=True) == 0
+    else:
+        assert bool((out == 3.0).all()) and fp8kv.fp8kv_device_status(clear=True) != 0
+
+
+@pytest.mark.gpu
 @pytest.mark.parametrize("M", [1, 12])
 def test_append_to_pages_outside_the_pool(M):
     """Flagged; those tokens are written nowhere, and their keys read as zeros."""

@@ -1173,10 +1173,12 @@ static int attention_call(const void* k_new, const void* v_new, const void* q, c
                 return FP8KV_ERR_CUDA;
             }
         }
+        // one sequence in at most 8 partitions: they combine in a cluster
+        P.cluster = tc && one_tile && B == 1 && plan.num_splits > 1 && plan.num_splits <= 8 ? plan.num_splits : 0;
         char text[256];
         rc = tc ? launch_attention_int4_tc(P, s, text, sizeof text) : launch_attention_int4(P, s, text, sizeof text);
         if (rc) return rc;
-        if (plan.num_splits > 1) {
+        if (plan.num_splits > 1 && !P.cluster) {
             const int64_t warps = (int64_t)B * M * Hq;
             cudaError_t e = launch_pdl(attn_reduce_kernel<true>, dim3((unsigned)((warps + 7) / 8)), dim3(256), 0, s,
                                        (const float*)P.ws_o,

@@ -36,6 +36,10 @@
 //                    and, so that no load has to wait for that, over their rows
 //                    of the staged pages (512 keys: 10.3 us; loads that wait 13.4,
 //                    an append kernel before this one 12.7).
+// One sequence in at most 8 partitions: the partitions of a KV head are a
+// thread-block cluster, and each CTA merges its share of the rows from the
+// others' shared memory (12 rows x 9 heads, 512 keys: 8.9 us; partials through
+// memory and a reduce kernel 10.3).
 // TMEM columns: Q 0-63, S/P 3 x 64 (64-255), O 256-383, 384-511.
 #include <stdio.h>
 
@@ -65,7 +69,8 @@ constexpr int BUF = NK * 256, HALF = BUF / 2;           // two blocks of 128 key
 constexpr int XCH_BYTES = 2 * 128 * 8;                  // (max, sum) of [half][row]
 constexpr int SMEM = (KBUFS + VBUFS) * BUF + STAGES * STAGE_BYTES + XCH_BYTES + 1024 + 512;
 constexpr int EPI_STRIDE = 144;                         // staged half row (128 bytes), padded against bank conflicts
-static_assert(2 * 128 * EPI_STRIDE <= (KBUFS + VBUFS) * BUF, "epilogue staging exceeds the widened tiles");
+constexpr int kMaxCluster = 8;
+static_assert(2 * 128 * EPI_STRIDE + 128 * 8 <= (KBUFS + VBUFS) * BUF, "epilogue staging exceeds the widened tiles");
 constexpr uint32_t TM_Q = 0, TM_S = 64, TM_O = 256, TM_COLS = 512;
 constexpr int WARPS = 20, THREADS = WARPS * 32, CONV_WARPS = 8;
 // registers: 640 x 96 at launch = 128 x (3 x 72 + 2 x 128) after the split
@@ -116,7 +121,7 @@ __device__ __forceinline__ void widen_chunk(const uint32_t (&at)[4], uint4 codes
     }
 }
 
-template <int PS>
+template <int PS, bool CL>     // CL: the partitions are a cluster
 __global__ void __launch_bounds__(THREADS, 1) attention_int4_tc_kernel(AttnParams P) {
     extern __shared__ uint8_t smem_raw[];
     uint8_t* smem = (uint8_t*)(((uintptr_t)smem_raw + 1023) & ~(uintptr_t)1023);
@@ -383,7 +388,9 @@ __global__ void __launch_bounds__(THREADS, 1) attention_int4_tc_kernel(AttnParam
         // both halves' O and (max, sum); this thread merges 64 dims of its row
         for (int h = 0; h < 2; ++h)
             if (ok) ok = mbar_wait(bar(B_O + h), 0);
+        const bool combine = CL && nsplit_b > 1;
         float2* ml = (float2*)xch;
+        float2* ml_all = (float2*)(kbuf + 2 * 128 * EPI_STRIDE);    // (max, sum) of the staged rows
         ml[half * 128 + r] = make_float2(m_run, l_run);
         __syncwarp();
         if (lane == 0) mbar_arrive(bar(B_PAIR + wq));
@@ -424,7 +431,10 @@ __global__ void __launch_bounds__(THREADS, 1) attention_int4_tc_kernel(AttnParam
                                                   pack_f16x2(x[1], x[3]), pack_f16x2(x[5], x[7]));
                 }
             }
-            if (r < RL) {
+            if (combine) {
+                // stays here: the cluster's CTAs read it below
+                if (half == 0) ml_all[r] = make_float2(m_tot, l_tot);
+            } else if (r < RL) {
                 fence_proxy_async();        // the staged row, written by this thread, to the bulk copy
                 if (direct)
                     bulk_store(P.out + row_idx * 128 + 64 * half, smem_u32(row_stage), 128);
@@ -435,6 +445,45 @@ __global__ void __launch_bounds__(THREADS, 1) attention_int4_tc_kernel(AttnParam
                 bulk_wait_read();
                 if (!direct && half == 0)
                     *(float2*)(P.ws_ml + (row_idx * P.num_splits + split) * 2) = make_float2(m_tot, l_tot);
+            }
+        }
+        if (CL) {
+            __syncwarp();
+            cluster_arrive();
+            cluster_wait();
+        }
+        if (combine) {
+            // the partitions of this KV head are a cluster (rank = partition):
+            // each merges every nsplit_b-th row, 16 threads a row
+            const int c = threadIdx.x & 15;
+            for (int row = split + nsplit_b * ((threadIdx.x - 128) >> 4); row < RL; row += 16 * nsplit_b) {
+                const uint8_t* at = kbuf + ((c >> 3) * 128 + row) * EPI_STRIDE + (c & 7) * 16;
+                float2 a[kMaxCluster];
+                float top = -INFINITY, den = 0.f, acc[8] = {};
+#pragma unroll
+                for (int j = 0; j < kMaxCluster; ++j) {
+                    a[j] = j < nsplit_b ? dsmem_ld8(dsmem_addr(ml_all + row, j)) : make_float2(-INFINITY, 0.f);
+                    top = fmaxf(top, a[j].x);
+                }
+#pragma unroll
+                for (int j = 0; j < kMaxCluster; ++j) {
+                    if (j >= nsplit_b) break;
+                    const uint4 x = dsmem_ld16(dsmem_addr(at, j));
+                    const float w = a[j].x == -INFINITY ? 0.f : ex2(a[j].x - top) * a[j].y;
+                    const uint32_t xs[4] = {x.x, x.y, x.z, x.w};
+                    den += w;
+#pragma unroll
+                    for (int u = 0; u < 4; ++u) {
+                        const float2 f = f16x2_to_f32x2(xs[u]);
+                        acc[2 * u] += w * f.x;
+                        acc[2 * u + 1] += w * f.y;
+                    }
+                }
+                const float f = 0.25f * vs / den;
+                const int64_t idx = ((int64_t)b * P.M + row / P.G) * P.Hq + hk * P.G + row % P.G;
+                *(uint4*)(P.out + idx * 128 + 8 * c) =
+                    make_uint4(pack_bf16x2(acc[0] * f, acc[1] * f), pack_bf16x2(acc[2] * f, acc[3] * f),
+                               pack_bf16x2(acc[4] * f, acc[5] * f), pack_bf16x2(acc[6] * f, acc[7] * f));
             }
         }
     } else {
@@ -643,6 +692,17 @@ __global__ void __launch_bounds__(THREADS, 1) attention_int4_tc_kernel(AttnParam
     }
 
     // ---------------------------------------------------------------- teardown
+    if (CL) {
+        // every warp of the cluster takes part in both barriers: the one before
+        // the rows are merged, and this one, before any shared memory goes
+        __syncwarp();
+        if (!run || warp < 4 || warp >= 12) {
+            cluster_arrive();
+            cluster_wait();
+        }
+        cluster_arrive();
+        cluster_wait();
+    }
     fence_before();
     __syncthreads();
     if (warp == 0) {
@@ -655,10 +715,14 @@ __global__ void __launch_bounds__(THREADS, 1) attention_int4_tc_kernel(AttnParam
 
 int launch_attention_int4_tc(const AttnParams& P, cudaStream_t s, char* text, size_t text_bytes) {
     const int RT = (P.R + 127) / 128;
+    if (P.cluster > 1 && (P.cluster > i4tc::kMaxCluster || P.cluster != P.num_splits || RT > 1 || P.lpt_order))
+        return FP8KV_ERR_UNSUPPORTED;
     if ((P.split_pages * P.page_size) % i4tc::NK || (int64_t)RT * P.Hkv > 65535) return FP8KV_ERR_UNSUPPORTED;
     static std::mutex mu;
     static std::set<std::pair<int, const void*>> done;
-    auto kern = P.page_size == 32 ? i4tc::attention_int4_tc_kernel<32> : i4tc::attention_int4_tc_kernel<64>;
+    auto kern = P.page_size == 32
+                    ? (P.cluster > 1 ? i4tc::attention_int4_tc_kernel<32, true> : i4tc::attention_int4_tc_kernel<32, false>)
+                    : (P.cluster > 1 ? i4tc::attention_int4_tc_kernel<64, true> : i4tc::attention_int4_tc_kernel<64, false>);
     {
         int dev = 0;
         if (cudaGetDevice(&dev) != cudaSuccess) return FP8KV_ERR_CUDA;
@@ -670,16 +734,16 @@ int launch_attention_int4_tc(const AttnParams& P, cudaStream_t s, char* text, si
         }
     }
     const dim3 grid(P.num_splits, P.Hkv * RT, P.B);
-    const cudaError_t e = launch_pdl(kern, grid, dim3(i4tc::THREADS), i4tc::SMEM, s, P);
+    const cudaError_t e = launch_pdl_cluster(kern, grid, dim3(i4tc::THREADS), i4tc::SMEM, s, P.cluster, P);
     if (e != cudaSuccess) {
         cudaGetLastError();
         return FP8KV_ERR_CUDA;
     }
     snprintf(text, text_bytes,
-             "attention_int4_tc<ps=%d> rows=%d row_tiles=%d splits=%d split_tokens=%d grid=%dx%dx%d threads=%d reduce=%d "
-             "order=%s",
+             "attention_int4_tc<ps=%d> rows=%d row_tiles=%d splits=%d split_tokens=%d grid=%dx%dx%d threads=%d cluster=%d "
+             "reduce=%d order=%s",
              P.page_size, P.R, RT, P.num_splits, P.split_pages * P.page_size, P.num_splits, P.Hkv * RT, P.B,
-             i4tc::THREADS, P.num_splits > 1 ? 1 : 0, P.lpt_order ? "longest_first" : "grid");
+             i4tc::THREADS, P.cluster > 1 ? P.cluster : 1, P.num_splits > 1 && P.cluster <= 1 ? 1 : 0, P.lpt_order ? "longest_first" : "grid");
     return FP8KV_OK;
 }
 
