@@ -232,6 +232,8 @@ int fp8kv_prompt_attention(const void* q, int64_t q_stride, const void* k, int64
  *   split_tokens: 0 = choose automatically; otherwise a positive multiple of
  *   page_size.  Returns FP8KV_OK and writes *num_splits (>= 1, the largest
  *   number of partitions any sequence can have) and *split_tokens_out.
+ * Over an INT4 cache a call with split_tokens = 0 may use fewer partitions than
+ * these, or up to 8 that combine on chip; the workspace size below serves it.
  */
 int fp8kv_paged_attention_plan(int B, int M, int Hq, int Hkv, int D, int page_size,
                                int max_seq_len, int window_left, int split_tokens,

@@ -346,6 +346,32 @@ def test_one_sequence_shorter_than_its_partitions(L, window):
 
 
 @pytest.mark.gpu
+@pytest.mark.parametrize("lens,M,G,H,ps,window,want", [
+    ([2000, 30, 1, 900], 1, 9, 2, 32, -1, "cluster"), ([400, 700], 2, 8, 3, 64, -1, "cluster"),
+    ([3000, 12, 500], 12, 9, 2, 64, -1, "cluster"), ([3000, 2500], 1, 4, 4, 32, 1500, "cluster"),
+    ([5000], 1, 12, 1, 64, -1, "cluster"), ([2500, 12] + [300] * 18, 12, 9, 8, 32, -1, "longest_first"),
+    ([2000, 12] + [300] * 18, 12, 9, 8, 32, -1, "splits=1 "),
+    ([100] * 39 + [500], 1, 9, 8, 32, -1, "threads=128"), ([6000] + [40] * 31, 1, 5, 8, 64, -1, "longest_first")])
+def test_automatic_partitions(lens, M, G, H, ps, window, want):
+    """Calls that are cut in the different ways: clusters of partitions some of
+    which are empty, one partition longest first, small CTAs.  A sequence whose
+    length is refused keeps its output rows and leaves the others' alone."""
+    lay, q, kc, vc, ks, vs, k, v, slots = _case(sum(lens), lens, M, G, H, ps)
+    fp8kv.fp8kv_cache_insert(k, v, slots, ks, vs, kc, vc)
+    out = _attend(lay, q, kc, vc, ks, vs, window)
+    assert want in fp8kv.fp8kv_last_dispatch()
+    _check(out, lay, q, kc, vc, ks, vs, ps, window)
+    fp8kv.fp8kv_device_status(clear=True)
+    sl = lay.seq_lens.clone()
+    sl[-1] = M - 1
+    again = torch.full_like(q, 3.0)
+    fp8kv.fp8kv_paged_attention(q, kc, vc, lay.block_table.cuda(), sl.cuda(), max(lens), ks, vs, SM, out=again,
+                                window_left=window)
+    assert fp8kv.fp8kv_device_status(clear=True) != 0
+    assert torch.equal(again[:-1], out[:-1]) and bool((again[-1] == 3.0).all())
+
+
+@pytest.mark.gpu
 @pytest.mark.parametrize("M", [1, 12])
 def test_append_to_pages_outside_the_pool(M):
     """Flagged; those tokens are written nowhere, and their keys read as zeros."""

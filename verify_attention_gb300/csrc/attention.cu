@@ -910,6 +910,7 @@ bool cache_map(CUtensorMap* m, const void* base, bool fp8, int Hkv, int PS, int 
 
 struct Plan {
     int split_pages, num_splits, split_tokens;
+    int pages;                  // spanned by the visible keys of the longest sequence
 };
 
 static int ceil_div(int64_t a, int64_t b) { return (int)((a + b - 1) / b); }
@@ -988,10 +989,70 @@ static int make_plan(int B, int M, int Hq, int Hkv, int D, int PS, int max_seq_l
         const int tile_pages = tc_tile_tokens() / PS;
         sp = (sp + tile_pages - 1) / tile_pages * tile_pages;
     }
+    p->pages = pages;
     p->split_pages = sp;
     p->num_splits = ceil_div(pages, sp);
     p->split_tokens = sp * PS;
     return FP8KV_OK;
+}
+
+// How an INT4 call is cut: pages per partition, partitions, warps per CTA of the
+// decode kernel, and whether the partitions of a (sequence, KV head) run as one
+// cluster.  The plan's partitions are a limit (they size the workspace), except
+// in a cluster, which needs none.  Lengths are only known on the device, so each
+// choice is judged by the mean of its estimated times with all sequences as long
+// as the longest and with lengths spread evenly up to it; the estimate's terms
+// were measured (us; 12 or 1 rows x 9 heads, 8 KV heads):
+//   tcgen05 kernel, one CTA an SM:             7 + 1.1 per 128 keys
+//   decode, 12 warps, one CTA an SM:           5 + 2 per 384 keys
+//   decode, 4 warps, three CTAs an SM:         5 + 2 per 128 keys, or 5 + 1 where
+//                                              an SM holds one
+//   partials and reduce kernel 2.5, cluster 1.2 (tcgen05) or 0.7, longest-first
+//   order 2.3
+// Against the plan's own partitions, decode: 4 x 16000 keys 48 -> 28 us, 16 x 4000
+// 36 -> 27; verifier rows: 64 x 4000 212 -> 168, 16 x 2000 44 -> 25.
+struct Int4Cut {
+    int split_pages, num_splits, warps;
+    bool cluster, lpt;
+};
+static Int4Cut int4_cut(const Plan& plan, bool tc, bool one_tile, bool given, int B, int64_t units, int PS) {
+    const int sms = num_sms(), tile = tc_tile_tokens() / PS;
+    Int4Cut best = {plan.split_pages, plan.num_splits, 12, false, false};
+    float best_us = INFINITY;
+    auto look = [&](int64_t want, int warps, bool cluster) {
+        int ns = plan.num_splits, sp = plan.split_pages;
+        if (!given) {
+            sp = ceil_div(ceil_div(plan.pages, std::max<int64_t>(1, want)), tile) * tile;
+            ns = ceil_div(plan.pages, sp);
+        }
+        if (cluster ? ns < 2 || ns > 8 || units > int4_clusters(ns) : ns > plan.num_splits) return;
+        const float keys = (float)std::min(sp, plan.pages) * PS;
+        const float rounds = ceilf(keys / (tc ? 128 : 32 * warps));
+        const float one = tc ? 7.f + 1.1f * rounds : 5.f + 2.f * rounds, alone = warps == 4 ? 5.f + rounds : one;
+        const int64_t slots = warps == 4 ? 3 * sms : sms, n = units * ns, rest = n % slots;
+        const bool lpt = B > 1 && one_tile && plan.num_splits > 1 && n > slots && sp % tile == 0 && n <= INT32_MAX;
+        const float tail = rest == 0 ? 0.f : (rest <= sms / 2 ? alone : one);
+        // (three CTAs of an SM are not in step: no whole waves)
+        const float equal = warps == 4 && n > slots ? (float)n / slots * one : (float)(n / slots) * one + tail;
+        const float spread = B > 1 ? std::max(n > slots ? one : tail, 0.5f * n * one / slots + 0.5f * one) : equal;
+        const float us = 0.5f * (equal + spread) + (ns > 1 ? (!cluster ? 2.5f : tc ? 1.2f : 0.7f) : 0.f) + (lpt ? 2.3f : 0.f);
+        if (us < best_us) {
+            best_us = us;
+            best = {sp, ns, warps, cluster, lpt};
+        }
+    };
+    // nothing is gained between whole waves of CTAs
+    for (int warps : {12, 4}) {
+        if (tc && warps == 4) break;
+        const int64_t slots = warps == 4 ? 3 * sms : sms;
+        look(plan.num_splits, warps, false);
+        if (given) continue;
+        look(1, warps, false);
+        for (int wave = 1; wave <= 3; ++wave) look(std::min<int64_t>(plan.num_splits, wave * slots / units), warps, false);
+    }
+    if (one_tile)
+        for (int ns = 2; ns <= 8 && units * ns <= sms; ++ns) look(ns, 12, true);
+    return best;
 }
 
 // Workspace: [partial O][partial (m, l)] when a sequence spans several
@@ -1159,31 +1220,34 @@ static int attention_call(const void* k_new, const void* v_new, const void* q, c
                                     v_scale, (void*)k_cache, (void*)v_cache, num_pages, page_size, max_seq_len, s);
             if (rc) return rc;
         }
-        const bool lpt = B > 1 && one_tile && plan.num_splits > 1 &&
-                         plan.split_tokens % tc_tile_tokens() == 0 &&
-                         (int64_t)B * plan.num_splits * Hkv <= INT32_MAX;
-        if (lpt) {
+        const int64_t units = (int64_t)B * Hkv * (tc ? row_tiles(M, Hq, Hkv) : P.NT);
+        const Int4Cut cut = int4_cut(plan, tc, one_tile, split_tokens > 0, B, units, page_size);
+        P.split_pages = cut.split_pages;
+        P.num_splits = cut.num_splits;
+        P.KW = cut.warps;
+        P.cluster = cut.cluster ? cut.num_splits : 0;
+        P.ws_ml = (float*)workspace + rows * cut.num_splits * 128;
+        if (cut.lpt) {
             // in the second half of the partials' area, which f16 leaves free
-            P.lpt_order = (const int32_t*)((const uint8_t*)workspace + rows * plan.num_splits * 128 * sizeof(uint16_t));
+            P.lpt_order =
+                (const int32_t*)((const uint8_t*)workspace + rows * cut.num_splits * 128 * sizeof(uint16_t));
             const cudaError_t e = launch_pdl(lpt_order_kernel, dim3(1), dim3(512), 0, s, seq_lens, B, M, P.R, P.G,
-                                             max_pages_per_seq, page_size, window_left, plan.split_pages,
-                                             plan.num_splits, max_seq_len, (int32_t*)P.lpt_order);
+                                             max_pages_per_seq, page_size, window_left, cut.split_pages,
+                                             cut.num_splits, max_seq_len, (int32_t*)P.lpt_order);
             if (e != cudaSuccess) {
                 cudaGetLastError();
                 return FP8KV_ERR_CUDA;
             }
         }
-        // one sequence in at most 8 partitions: they combine in a cluster
-        P.cluster = tc && one_tile && B == 1 && plan.num_splits > 1 && plan.num_splits <= 8 ? plan.num_splits : 0;
         char text[256];
         rc = tc ? launch_attention_int4_tc(P, s, text, sizeof text) : launch_attention_int4(P, s, text, sizeof text);
         if (rc) return rc;
-        if (plan.num_splits > 1 && !P.cluster) {
+        if (cut.num_splits > 1 && !cut.cluster) {
             const int64_t warps = (int64_t)B * M * Hq;
             cudaError_t e = launch_pdl(attn_reduce_kernel<true>, dim3((unsigned)((warps + 7) / 8)), dim3(256), 0, s,
                                        (const float*)P.ws_o,
                                        (const float*)P.ws_ml, seq_lens, B, M, Hq, P.G, tc ? 128 : P.R,
-                                       max_pages_per_seq, page_size, window_left, plan.split_pages, plan.num_splits,
+                                       max_pages_per_seq, page_size, window_left, cut.split_pages, cut.num_splits,
                                        max_seq_len, v_scale, scale_stride, (uint16_t*)out);
             if (e != cudaSuccess) {
                 cudaGetLastError();

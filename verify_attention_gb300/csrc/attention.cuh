@@ -17,9 +17,9 @@ struct AttnParams {
     float* ws_ml;               // [B*M*Hq][num_splits][2]
     uint16_t* out;              // bf16 [B][M][Hq][128]
     float sm_scale;
-    int mpps, B, M, Hq, Hkv, G, R, NT, KW, SG;   // SG: stages per key group
+    int mpps, B, M, Hq, Hkv, G, R, NT, KW, SG;   // SG: stages per key group (INT4: KW warps per CTA)
     int window_left, split_pages, num_splits, page_size, max_seq_len;
-    // > 1 (tcgen05 path, one sequence): the num_splits partitions of a (KV
+    // > 1 (tcgen05 path, one sequence; INT4 paths): the num_splits partitions of a (KV
     // head, sequence) form one thread-block cluster and combine their
     // partial results through distributed shared memory, without workspace
     // partials or the reduce kernel
@@ -99,6 +99,7 @@ int launch_append_int4(const void* k, const void* v, const int32_t* seq_lens, co
 // partitions, cut from the key range of the tile.
 int launch_attention_int4(const AttnParams& P, cudaStream_t s, char* text, size_t text_bytes);
 int launch_attention_int4_tc(const AttnParams& P, cudaStream_t s, char* text, size_t text_bytes);
+int int4_clusters(int n);   // clusters of n CTAs, one CTA an SM, resident at once
 
 // Host launcher of the tcgen05 kernel (attention_tc.cu).  Returns
 // FP8KV_ERR_UNSUPPORTED when the shape is not one it implements.

@@ -24,8 +24,10 @@
 // free of bank conflicts.
 #include <stdio.h>
 
+#include <map>
 #include <mutex>
 #include <set>
+#include <utility>
 
 #include "attention.cuh"
 #include "common.cuh"
@@ -45,7 +47,12 @@ constexpr int OFF_VS = OFF_KS + CK * kInt4ScaleBytes;
 constexpr int STAGE_BYTES = OFF_VS + CK * kInt4ScaleBytes;   // 4608
 constexpr float GROW = 4.0f, BIAS = 11.0f;              // see the softmax
 constexpr int MERGE_STRIDE = 132;                       // floats per merged row: 128 of O, max, sum
-static_assert(16 * MERGE_STRIDE * 4 <= STAGES * STAGE_BYTES, "merge area exceeds the rings");
+// the rings; after them, in the same bytes, the warps' merged rows and (in a
+// cluster) the CTA's
+template <int WARPS>
+constexpr int SMEM = WARPS * STAGES * STAGE_BYTES;
+static_assert((12 + 1) * 16 * MERGE_STRIDE * 4 <= SMEM<12> && (4 + 1) * 16 * MERGE_STRIDE * 4 <= SMEM<4>,
+              "merge area exceeds the rings");
 
 // 16 bytes from src + SRC to shared memory at dst + DST (zeros when bytes = 0)
 template <int DST, int SRC>
@@ -114,7 +121,10 @@ __device__ __forceinline__ void append(const AttnParams& P, int b, int hk, int L
 }
 
 // WARPS = 12, one CTA per SM, or 4, three CTAs per SM (168 registers a thread).
-template <int PS, int WARPS>
+// CL: the partitions of a (sequence, KV head) are a thread-block cluster and
+// merge their rows from each other's shared memory (one sequence of 4000 keys:
+// 11.2 us; partials through memory and a reduce kernel 13.7).
+template <int PS, int WARPS, bool CL>
 __global__ void __launch_bounds__(WARPS * 32, 12 / WARPS) paged_attention_int4_kernel(AttnParams P) {
     extern __shared__ __align__(128) uint8_t smem[];
     constexpr int THREADS = WARPS * 32;
@@ -452,6 +462,10 @@ __global__ void __launch_bounds__(WARPS * 32, 12 / WARPS) paged_attention_int4_k
             const float f = vs / l;
             *(uint2*)(P.out + row_idx * 128 + d4) =
                 make_uint2(pack_bf16x2(acc.x * f, acc.y * f), pack_bf16x2(acc.z * f, acc.w * f));
+        } else if (CL) {
+            float* dst = merge + (WARPS * 16 + r) * MERGE_STRIDE;
+            *(float4*)(dst + d4) = acc;
+            if (d4 == 0) *(float2*)(dst + 128) = make_float2(mstar, l);
         } else {
             // partial: f16 of 4 O / l (|x| <= 7 * 448) beside its (max, sum); a
             // row with no visible key here has l = 0: weight 0, values 0
@@ -461,45 +475,116 @@ __global__ void __launch_bounds__(WARPS * 32, 12 / WARPS) paged_attention_int4_k
             if (d4 == 0) *(float2*)(P.ws_ml + (row_idx * P.num_splits + split) * 2) = make_float2(mstar, l);
         }
     }
+    if (CL && nsplit_b > 1) {
+        // (CTAs of the cluster without keys have returned: the barriers count
+        // those that have not)
+        __syncwarp();
+        cluster_arrive();
+        cluster_wait();
+        for (int item = split * THREADS + threadIdx.x; item < rows * 32; item += nsplit_b * THREADS) {
+            const int r = item >> 5, d4 = (item & 31) * 4;
+            const float* at = merge + (WARPS * 16 + r) * MERGE_STRIDE;
+            float2 a[8];
+            uint4 x[8];
+            float top = -INFINITY, l = 0.f;
+#pragma unroll
+            for (int j = 0; j < 8; ++j) {
+                if (j >= nsplit_b) break;
+                a[j] = dsmem_ld8(dsmem_addr(at + 128, j));
+                x[j] = dsmem_ld16(dsmem_addr(at + d4, j));
+                top = fmaxf(top, a[j].x);
+            }
+            float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll
+            for (int j = 0; j < 8; ++j) {
+                if (j >= nsplit_b) break;
+                const float w = a[j].x == -INFINITY ? 0.f : ex2(a[j].x - top);
+                l += w * a[j].y;
+                acc.x += w * __uint_as_float(x[j].x);
+                acc.y += w * __uint_as_float(x[j].y);
+                acc.z += w * __uint_as_float(x[j].z);
+                acc.w += w * __uint_as_float(x[j].w);
+            }
+            const int m = (R0 + r) / P.G, hq = hk * P.G + (R0 + r) % P.G;
+            const float f = vs / l;
+            *(uint2*)(P.out + (((int64_t)b * P.M + m) * P.Hq + hq) * 128 + d4) =
+                make_uint2(pack_bf16x2(acc.x * f, acc.y * f), pack_bf16x2(acc.z * f, acc.w * f));
+        }
+        __syncwarp();
+        cluster_arrive();                               // no shared memory goes before all have read
+        cluster_wait();
+    }
 }
 
-template <int PS, int WARPS>
+template <int PS, int WARPS, bool CL>
 static int launch(const AttnParams& P, cudaStream_t s) {
     static std::mutex mu;
     static std::set<int> done;
-    auto kern = paged_attention_int4_kernel<PS, WARPS>;
-    constexpr int smem = WARPS * STAGES * STAGE_BYTES;
+    auto kern = paged_attention_int4_kernel<PS, WARPS, CL>;
     {
         int dev = 0;
         if (cudaGetDevice(&dev) != cudaSuccess) return FP8KV_ERR_CUDA;
         std::lock_guard<std::mutex> lock(mu);
         if (!done.count(dev)) {
-            if (cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, smem) != cudaSuccess)
+            if (cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, SMEM<WARPS>) != cudaSuccess)
                 return FP8KV_ERR_CUDA;
             done.insert(dev);
         }
     }
     const dim3 grid(P.num_splits, P.Hkv * P.NT, P.B);
-    const cudaError_t e = launch_pdl(kern, grid, dim3(WARPS * 32), smem, s, P);
+    const cudaError_t e = launch_pdl_cluster(kern, grid, dim3(WARPS * 32), SMEM<WARPS>, s, P.cluster, P);
     return e == cudaSuccess ? FP8KV_OK : (cudaGetLastError(), FP8KV_ERR_CUDA);
 }
 
 }  // namespace i4
 
+int int4_clusters(int n) {
+    static std::mutex mu;
+    static std::map<std::pair<int, int>, int> known;
+    int dev = 0;
+    if (n < 2 || n > 8 || cudaGetDevice(&dev) != cudaSuccess) return 0;
+    std::lock_guard<std::mutex> lock(mu);
+    auto it = known.find({dev, n});
+    if (it != known.end()) return it->second;
+    auto kern = i4::paged_attention_int4_kernel<32, 12, true>;
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = dim3(n);
+    cfg.blockDim = dim3(12 * 32);
+    cfg.dynamicSmemBytes = i4::SMEM<12>;
+    cudaLaunchAttribute attr[1];
+    attr[0].id = cudaLaunchAttributeClusterDimension;
+    attr[0].val.clusterDim.x = n;
+    attr[0].val.clusterDim.y = attr[0].val.clusterDim.z = 1;
+    cfg.attrs = attr;
+    cfg.numAttrs = 1;
+    int count = 0;
+    if (cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, i4::SMEM<12>) != cudaSuccess ||
+        cudaOccupancyMaxActiveClusters(&count, kern, &cfg) != cudaSuccess) {
+        cudaGetLastError();
+        count = 0;
+    }
+    return known[{dev, n}] = count;
+}
+
 int launch_attention_int4(const AttnParams& P, cudaStream_t s, char* text, size_t text_bytes) {
     if ((int64_t)P.Hkv * P.NT > 65535) return FP8KV_ERR_UNSUPPORTED;
-    // Small CTAs, three to an SM, when there are enough of them: one's set-up
+    if (P.cluster > 1 && (P.cluster > 8 || P.cluster != P.num_splits || P.NT > 1 || P.lpt_order || P.KW != 12))
+        return FP8KV_ERR_UNSUPPORTED;
+    // Small CTAs, three to an SM, where there are enough of them: one's set-up
     // and merge run beside the others' keys (64 sequences, 2048 CTAs: 384 us
-    // against 405); with fewer CTAs than that their warps would leave the SMs
-    // part empty (one sequence of 131072 keys, 152 CTAs: 106 us against 49).
-    const bool small = (int64_t)P.B * P.Hkv * P.NT * P.num_splits >= 3ll * num_sms();
-    const int rc = P.page_size == 32 ? (small ? i4::launch<32, 4>(P, s) : i4::launch<32, 12>(P, s))
-                                     : (small ? i4::launch<64, 4>(P, s) : i4::launch<64, 12>(P, s));
+    // against 405); few of them would leave the SMs part empty (one sequence of
+    // 131072 keys, 152 CTAs: 106 us against 49).
+    const bool small = P.KW == 4, ps32 = P.page_size == 32;
+    const int rc = P.cluster > 1 ? (ps32 ? i4::launch<32, 12, true>(P, s) : i4::launch<64, 12, true>(P, s))
+                   : small       ? (ps32 ? i4::launch<32, 4, false>(P, s) : i4::launch<64, 4, false>(P, s))
+                                 : (ps32 ? i4::launch<32, 12, false>(P, s) : i4::launch<64, 12, false>(P, s));
     if (rc) return rc;
     snprintf(text, text_bytes,
-             "paged_attention_int4_mma<ps=%d> rows=%d row_tiles=%d splits=%d grid=%dx%dx%d threads=%d reduce=%d order=%s",
-             P.page_size, P.R, P.NT, P.num_splits, P.num_splits, P.Hkv * P.NT, P.B, small ? 128 : 384,
-             P.num_splits > 1 ? 1 : 0, P.lpt_order ? "longest_first" : "grid");
+             "paged_attention_int4_mma<ps=%d> rows=%d row_tiles=%d splits=%d split_tokens=%d grid=%dx%dx%d threads=%d "
+             "cluster=%d reduce=%d order=%s",
+             P.page_size, P.R, P.NT, P.num_splits, P.split_pages * P.page_size, P.num_splits, P.Hkv * P.NT, P.B,
+             small ? 128 : 384, P.cluster > 1 ? P.cluster : 1, P.num_splits > 1 && P.cluster <= 1 ? 1 : 0,
+             P.lpt_order ? "longest_first" : "grid");
     return FP8KV_OK;
 }
 

@@ -36,7 +36,7 @@
 //                    and, so that no load has to wait for that, over their rows
 //                    of the staged pages (512 keys: 10.3 us; loads that wait 13.4,
 //                    an append kernel before this one 12.7).
-// One sequence in at most 8 partitions: the partitions of a KV head are a
+// At most 8 partitions in one wave of CTAs: those of a (sequence, KV head) are a
 // thread-block cluster, and each CTA merges its share of the rows from the
 // others' shared memory (12 rows x 9 heads, 512 keys: 8.9 us; partials through
 // memory and a reduce kernel 10.3).
