@@ -123,18 +123,30 @@ __device__ __forceinline__ uint2 int4_encode16(uint4 a, uint4 b, float c, uint8_
     if (sc == 0x7fu) return make_uint2(0x88888888u, 0x88888888u);
     float s, unused;
     e4m3x2_to_f32x2(sc, s, unused);
-    const float inv = __fdiv_rn(1.0f, __fmul_rn(s, c));
-    uint32_t o[2] = {0u, 0u};
+    const float inv = __frcp_rn(__fmul_rn(s, c));
+    // n + 8 in the low mantissa bits of 2^23 + 8 + n (the addition rounds to
+    // the nearest integer, ties to even); the words' sum of 16^e times those
+    // bits is the codes' word plus 16^e times 2^23's bits, 0xfb000000 in all
+    uint32_t o[2];
+    auto codes = [&](bool clamp) {
 #pragma unroll
-    for (int i = 0; i < 8; ++i) {
-        // n + 8 in the low mantissa bits of 2^23 + 8 + n: the addition rounds
-        // to the nearest integer, ties to even
-        const float lo = fminf(fmaxf(__fmul_rn(bf16_lo(w[i]), inv), -7.0f), 7.0f);
-        const float hi = fminf(fmaxf(__fmul_rn(bf16_hi(w[i]), inv), -7.0f), 7.0f);
-        const uint32_t cl = __float_as_uint(__fadd_rn(lo, 8388616.0f)) & 15u;
-        const uint32_t ch = __float_as_uint(__fadd_rn(hi, 8388616.0f)) & 15u;
-        o[i >> 2] |= (cl | (ch << 4)) << (8 * (i & 3));
-    }
+        for (int u = 0; u < 2; ++u) {
+            uint32_t acc = 0;
+#pragma unroll
+            for (int e = 7; e >= 0; --e) {
+                const uint32_t x = w[4 * u + (e >> 1)];
+                float t = __fmul_rn(e & 1 ? bf16_hi(x) : bf16_lo(x), inv);
+                if (clamp) t = fminf(fmaxf(t, -7.0f), 7.0f);
+                acc = acc * 16u + __float_as_uint(__fadd_rn(t, 8388616.0f));
+            }
+            o[u] = acc - 0xfb000000u;
+        }
+    };
+    // A scale that was rounded to a normal E4M3 number, without saturating, is
+    // at least amax / (7 c) / (1 + 2^-4): |x inv| stays below 7.44, which rounds
+    // to 7, and the clamps (a third of the instructions) can go.
+    if (sc >= 8u && r <= 448.0f) codes(false);
+    else codes(true);
     return make_uint2(o[0], o[1]);
 }
 

@@ -114,6 +114,11 @@ int launch_append(const void* k, const void* v, const int32_t* seq_lens, const i
 
 // ------------------------------------------------------- 4-bit insert/append
 
+// row / Hkv; the 64-bit division is three times as long as the 32-bit one
+__device__ __forceinline__ int64_t token_of(int64_t row, int Hkv) {
+    return row >> 32 ? row / Hkv : (int64_t)((uint32_t)row / (uint32_t)Hkv);
+}
+
 // One thread per (token, head, 16-element block) of K and V: 64 bytes in, 18
 // bytes out; the eight threads of a row write its 64 code bytes and its 8
 // scale bytes side by side.
@@ -126,7 +131,7 @@ __global__ void __launch_bounds__(256) insert_int4_kernel(
     const int64_t i = (int64_t)blockIdx.x * blockDim.x + threadIdx.x;
     if (i >= (int64_t)T * Hkv * 8) return;
     const int block = (int)(i & 7);
-    const int64_t row = i >> 3, t = row / Hkv;
+    const int64_t row = i >> 3, t = token_of(row, Hkv);
     const int h = (int)(row - t * Hkv);
     const int64_t slot = slots[t];
     if (slot < 0) return;
@@ -134,9 +139,9 @@ __global__ void __launch_bounds__(256) insert_int4_kernel(
         if (block == 0) flag(FP8KV_DEV_BAD_SLOT);
         return;
     }
-    const int64_t page = slot / page_size;
+    const int64_t page = slot >> (page_size == 64 ? 6 : 5);
     Int4Block(k[2 * i], k[2 * i + 1], v[2 * i], v[2 * i + 1], *k_scale, *v_scale)
-        .store(k_cache, v_cache, page, (int)(slot - page * page_size), h, Hkv, page_size, block);
+        .store(k_cache, v_cache, page, (int)slot & (page_size - 1), h, Hkv, page_size, block);
 }
 
 // The M new tokens of every sequence to positions L_b - M + m.
@@ -211,16 +216,20 @@ __device__ __forceinline__ void gather16(const uint8_t* __restrict__ cache, floa
 #pragma unroll
         for (int j = 0; j < 8; ++j) {
             const uint32_t b = cw[j >> 2] >> (8 * (j & 3));
-            // n s is exact in fp32 (3 + 4 significant bits)
-            const float lo = (float)((int)(b & 15u) - 8) * s, hi = (float)((int)((b >> 4) & 15u) - 8) * s;
-            w[j] = pack_bf16x2(__fmul_rn(lo, c), __fmul_rn(hi, c));
+            // n from the low mantissa bits of 2^23 + 8 + n (conversions from
+            // integer would keep their 16-lane unit busy for half of the
+            // kernel); n s is exact in fp32 (3 + 4 significant bits)
+            const float lo = __uint_as_float((b & 15u) | 0x4b000000u) - 8388616.0f;
+            const float hi = __uint_as_float(((b >> 4) & 15u) | 0x4b000000u) - 8388616.0f;
+            w[j] = pack_bf16x2(__fmul_rn(lo * s, c), __fmul_rn(hi * s, c));
         }
     }
     out[0] = make_uint4(w[0], w[1], w[2], w[3]);
     out[1] = make_uint4(w[4], w[5], w[6], w[7]);
 }
 
-// One thread per (token, head, 16-element block) of K and V.
+// One thread per (token, head, 16-element block) of K and V (8 elements a thread,
+// whose stores would cover whole lines: 71 us for 65536 tokens against 61).
 template <int DT>
 __global__ void __launch_bounds__(256) gather_kernel(const int64_t* __restrict__ slots, int T, int Hkv,
                                                      const float* __restrict__ k_scale,
@@ -234,7 +243,7 @@ __global__ void __launch_bounds__(256) gather_kernel(const int64_t* __restrict__
     const int64_t i = (int64_t)blockIdx.x * blockDim.x + threadIdx.x;
     if (i >= (int64_t)T * Hkv * 8) return;
     const int block = (int)(i & 7);
-    const int64_t row = i >> 3, t = row / Hkv;
+    const int64_t row = i >> 3, t = token_of(row, Hkv);
     const int h = (int)(row - t * Hkv);
     const int64_t slot = slots[t];
     if (slot < 0) return;
@@ -243,8 +252,8 @@ __global__ void __launch_bounds__(256) gather_kernel(const int64_t* __restrict__
         return;
     }
     const float ks = DT == FP8KV_CACHE_BF16 ? 1.f : *k_scale, vs = DT == FP8KV_CACHE_BF16 ? 1.f : *v_scale;
-    const int64_t page = slot / page_size;
-    const int off = (int)(slot - page * page_size);
+    const int64_t page = slot >> (page_size == 64 ? 6 : 5);
+    const int off = (int)slot & (page_size - 1);
     gather16<DT>(k_cache, ks, page, off, h, Hkv, page_size, block, k_out + 2 * i);
     gather16<DT>(v_cache, vs, page, off, h, Hkv, page_size, block, v_out + 2 * i);
 }
