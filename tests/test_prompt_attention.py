@@ -280,3 +280,42 @@ def test_prompt_insert_and_decode_together(ps, window):
         # the tolerance of tests/test_int4_cache.py
         tol = 2.0 ** -8 * np.abs(ref) + 2.0 ** -10 * mag + 2.0 ** -20 * lmag + 2.0 ** -36 * vsum
         assert np.all(np.abs(o.double().cpu().numpy() - ref) <= tol)
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("handle", [False, True])
+def test_outputs_of_a_call_on_another_stream(handle):
+    """What the calls allocate is filled on their stream: here the current stream
+    is busy until they are done."""
+    lens = [200, 70]
+    q, k, v, cu = _inputs(15, lens, 9, 2)
+    want = fp8kv.fp8kv_prompt_attention(q, k, v, cu, 200, SM)
+    kc, vc = (fp8kv.fp8kv_int4_cache(9, 2, 32) for _ in range(2))
+    one = torch.tensor([0.01], device="cuda")
+    slots = torch.arange(270, device="cuda")
+    fp8kv.fp8kv_cache_insert(k, v, slots, one, one, kc, vc)
+    rows = fp8kv.fp8kv_cache_gather(slots, one, one, kc, vc)
+    side = torch.cuda.Stream()
+    torch.cuda.synchronize()
+    torch.cuda._sleep(200_000_000)                               # about 0.1 s
+    s = side.cuda_stream if handle else side
+    out = fp8kv.fp8kv_prompt_attention(q, k, v, cu, 200, SM, stream=s)
+    got = fp8kv.fp8kv_cache_gather(slots, one, one, kc, vc, stream=s)
+    torch.cuda.synchronize()
+    assert torch.equal(out, want) and torch.equal(got[0], rows[0]) and torch.equal(got[1], rows[1])
+
+
+@pytest.mark.gpu
+def test_tensors_of_another_device_are_refused(monkeypatch):
+    q, k, v, cu = _inputs(16, [40], 4, 1)
+    kc, vc = (fp8kv.fp8kv_int4_cache(2, 1, 32) for _ in range(2))
+    one = torch.tensor([0.01], device="cuda")
+    slots = torch.arange(40, device="cuda")
+    bt, sl = torch.tensor([[0, 1]], dtype=torch.int32, device="cuda"), torch.tensor([40], dtype=torch.int32, device="cuda")
+    call = fp8kv.PreparedAttention(q[None, -1:].contiguous(), kc, vc, bt, sl, 40, one, one, SM)
+    monkeypatch.setattr(torch.cuda, "current_device", lambda: 1)
+    for f in (lambda: fp8kv.fp8kv_prompt_attention(q, k, v, cu, 40, SM, out=torch.empty_like(q)), call,
+              lambda: fp8kv.fp8kv_cache_insert(k, v, slots, one, one, kc, vc),
+              lambda: fp8kv.fp8kv_cache_gather(slots, one, one, kc, vc, torch.empty_like(k), torch.empty_like(v))):
+        with pytest.raises(ValueError, match="current device"):
+            f()

@@ -8,6 +8,7 @@ first call raises.
 """
 from __future__ import annotations
 
+import contextlib
 import ctypes
 import os
 from typing import Optional
@@ -95,11 +96,37 @@ def _ptr(t: Optional[torch.Tensor]) -> int:
     return t.data_ptr() if t is not None else 0
 
 
-def _stream(stream) -> int:
+def _stream(stream, t=None) -> int:
+    """The stream's handle; `t`, one of the call's tensors, must be on the current device."""
     if stream is None:
         # the handle of the current stream without a Stream object (0.3 us instead of 3)
-        return torch._C._cuda_getCurrentRawStream(torch.cuda.current_device())
+        device = torch.cuda.current_device()
+        if t is not None and t.get_device() != device:
+            raise ValueError(f"tensors on cuda:{t.get_device()}, but the current device is cuda:{device}")
+        return torch._C._cuda_getCurrentRawStream(device)
     return stream.cuda_stream if hasattr(stream, "cuda_stream") else int(stream)
+
+
+def _at(stream):
+    """What is allocated or filled for a call on `stream` belongs there: filled on
+    the current stream it might be filled after the call, and a workspace of the
+    current stream's pool might be handed out again before the call ends."""
+    if stream is None:
+        return contextlib.nullcontext()
+    return torch.cuda.stream(stream if hasattr(stream, "cuda_stream") else torch.cuda.ExternalStream(int(stream)))
+
+
+def _zeros(shape, device, stream):
+    t = torch.empty(shape, dtype=torch.bfloat16, device=device)
+    with _at(stream):
+        return t.zero_()
+
+
+def _workspace(need, device, stream):
+    if not need:
+        return None
+    with _at(stream):
+        return torch.empty(need, dtype=torch.uint8, device=device)
 
 
 def _check(fn, rc):
@@ -162,7 +189,7 @@ def fp8kv_cache_insert(k, v, slot_mapping, k_scale, v_scale, k_cache, v_cache, s
         _int4_rows(k, v, slot_mapping, heads, k_scale, v_scale)
     rc = lib().fp8kv_cache_insert(_ptr(k), _ptr(v), _ptr(slot_mapping), T, Hkv, D, _ptr(k_scale),
                                   _ptr(v_scale), _ptr(k_cache), _ptr(v_cache), num_pages, page_size,
-                                  dt, _stream(stream))
+                                  dt, _stream(stream, k_cache))
     _check("fp8kv_cache_insert", rc)
 
 
@@ -204,13 +231,13 @@ def fp8kv_cache_gather(slot_mapping, k_scale, v_scale, k_cache, v_cache, k_out=N
     outs = []
     for t, n in ((k_out, "k_out"), (v_out, "v_out")):
         if t is None:
-            t = torch.zeros((T, Hkv, D), dtype=torch.bfloat16, device=k_cache.device)
+            t = _zeros((T, Hkv, D), k_cache.device, stream)
         if tuple(_dev(t, n, torch.bfloat16).shape) != (T, Hkv, D):
             raise ValueError(f"{n} must be {(T, Hkv, D)}, got {tuple(t.shape)}")
         outs.append(t)
     rc = lib().fp8kv_cache_gather(_ptr(slot_mapping), T, Hkv, D, _ptr(k_scale), _ptr(v_scale), _ptr(k_cache),
                                   _ptr(v_cache), num_pages, page_size, dt, _ptr(outs[0]), _ptr(outs[1]),
-                                  _stream(stream))
+                                  _stream(stream, k_cache))
     _check("fp8kv_cache_gather", rc)
     return tuple(outs)
 
@@ -280,12 +307,12 @@ def fp8kv_prompt_attention(q, k, v, cu_seqlens, max_seq_len, sm_scale, window_le
     strides = [_token_rows(t, n, T) for t, n in ((q, "q"), (k, "k"), (v, "v"))]
     _dev(cu_seqlens, "cu_seqlens", torch.int32)
     if out is None:
-        out = torch.zeros((T, Hq, D), dtype=torch.bfloat16, device=q.device)
+        out = _zeros((T, Hq, D), q.device, stream)
     if tuple(_dev(out, "out", torch.bfloat16).shape) != (T, Hq, D):
         raise ValueError(f"out must be {(T, Hq, D)}, got {tuple(out.shape)}")
     rc = lib().fp8kv_prompt_attention(_ptr(q), strides[0], _ptr(k), strides[1], _ptr(v), strides[2],
                                       _ptr(cu_seqlens), cu_seqlens.numel() - 1, T, int(max_seq_len), Hq, Hkv, D,
-                                      float(sm_scale), int(window_left), _ptr(out), _stream(stream))
+                                      float(sm_scale), int(window_left), _ptr(out), _stream(stream, q))
     _check("fp8kv_prompt_attention", rc)
     return out
 
@@ -325,15 +352,15 @@ def fp8kv_paged_attention(q, k_cache, v_cache, block_table, seq_lens, max_seq_le
         num_pages = P
     need = fp8kv_paged_attention_workspace_size(B, M, Hq, Hkv, D, page_size, max_seq_len, window_left,
                                                 split_tokens)
-    if workspace is None and need:
-        workspace = torch.empty(need, dtype=torch.uint8, device=q.device)
+    if workspace is None:
+        workspace = _workspace(need, q.device, stream)
     if out is None:
         out = torch.empty_like(q)
     rc = lib().fp8kv_paged_attention(
         _ptr(q), _ptr(k_cache), _ptr(v_cache), dt, _ptr(block_table), block_table.shape[1],
         _ptr(seq_lens), int(max_seq_len), B, M, Hq, Hkv, D, page_size, int(num_pages), _ptr(k_scale),
         _ptr(v_scale), float(sm_scale), int(window_left), int(split_tokens), _ptr(workspace),
-        workspace.numel() if workspace is not None else 0, _ptr(out), _stream(stream))
+        workspace.numel() if workspace is not None else 0, _ptr(out), _stream(stream, q))
     _check("fp8kv_paged_attention", rc)
     return out
 
@@ -357,15 +384,15 @@ def fp8kv_append_paged_attention(k_new, v_new, q, k_cache, v_cache, block_table,
         num_pages = P
     need = fp8kv_paged_attention_workspace_size(B, M, Hq, Hkv, D, page_size, max_seq_len, window_left,
                                                 split_tokens)
-    if workspace is None and need:
-        workspace = torch.empty(need, dtype=torch.uint8, device=q.device)
+    if workspace is None:
+        workspace = _workspace(need, q.device, stream)
     if out is None:
         out = torch.empty_like(q)
     rc = lib().fp8kv_append_paged_attention(
         _ptr(k_new), _ptr(v_new), _ptr(q), _ptr(k_cache), _ptr(v_cache), dt, _ptr(block_table),
         block_table.shape[1], _ptr(seq_lens), int(max_seq_len), B, M, Hq, Hkv, D, page_size, int(num_pages),
         _ptr(k_scale), _ptr(v_scale), float(sm_scale), int(window_left), int(split_tokens), _ptr(workspace),
-        workspace.numel() if workspace is not None else 0, _ptr(out), _stream(stream))
+        workspace.numel() if workspace is not None else 0, _ptr(out), _stream(stream, q))
     _check("fp8kv_append_paged_attention", rc)
     return out
 
@@ -391,8 +418,8 @@ def fp8kv_paged_attention_per_head(q, k_cache, v_cache, block_table, seq_lens, m
         num_pages = P
     need = fp8kv_paged_attention_workspace_size(B, M, Hq, Hkv, D, page_size, max_seq_len, window_left,
                                                 split_tokens)
-    if workspace is None and need:
-        workspace = torch.empty(need, dtype=torch.uint8, device=q.device)
+    if workspace is None:
+        workspace = _workspace(need, q.device, stream)
     if out is None:
         out = torch.empty_like(q)
     args = (_ptr(q), _ptr(k_cache), _ptr(v_cache), _ptr(block_table), block_table.shape[1], _ptr(seq_lens),
@@ -463,7 +490,7 @@ class PreparedAttention:
             self._args = args
 
     def __call__(self, stream=None):
-        rc = self._fn(*self._args, _stream(stream))
+        rc = self._fn(*self._args, _stream(stream, self.out))
         if rc:
             raise Fp8kvError(self._name, rc)
         return self.out
@@ -488,7 +515,7 @@ def fp8kv_paged_attention_noalloc(q, k_cache, v_cache, block_table, seq_lens, ma
         _ptr(q), _ptr(k_cache), _ptr(v_cache), dt, _ptr(block_table), block_table.shape[1], _ptr(seq_lens),
         int(max_seq_len), B, M, Hq, Hkv, D, page_size, int(P if num_pages is None else num_pages),
         _ptr(k_scale), _ptr(v_scale), float(sm_scale), int(window_left), int(split_tokens), _ptr(out),
-        _stream(stream))
+        _stream(stream, q))
     _check("fp8kv_paged_attention_noalloc", rc)
     return out
 
