@@ -1018,6 +1018,9 @@ struct Int4Cut {
 static Int4Cut int4_cut(const Plan& plan, bool tc, bool one_tile, bool given, int B, int64_t units, int PS) {
     const int sms = num_sms(), tile = tc_tile_tokens() / PS;
     Int4Cut best = {plan.split_pages, plan.num_splits, 12, false, false};
+    // a single round of keys: nothing to choose
+    if (plan.num_splits == 1 && units <= sms && plan.pages * PS <= (tc ? 128 : 384)) return best;
+    const int* clusters = one_tile ? int4_clusters() : nullptr;
     float best_us = INFINITY;
     auto look = [&](int64_t want, int warps, bool cluster) {
         int ns = plan.num_splits, sp = plan.split_pages;
@@ -1025,7 +1028,7 @@ static Int4Cut int4_cut(const Plan& plan, bool tc, bool one_tile, bool given, in
             sp = ceil_div(ceil_div(plan.pages, std::max<int64_t>(1, want)), tile) * tile;
             ns = ceil_div(plan.pages, sp);
         }
-        if (cluster ? ns < 2 || ns > 8 || units > int4_clusters(ns) : ns > plan.num_splits) return;
+        if (cluster ? ns < 2 || ns > 8 || units > clusters[ns] : ns > plan.num_splits) return;
         const float keys = (float)std::min(sp, plan.pages) * PS;
         const float rounds = ceilf(keys / (tc ? 128 : 32 * warps));
         const float one = tc ? 7.f + 1.1f * rounds : 5.f + 2.f * rounds, alone = warps == 4 ? 5.f + rounds : one;

@@ -24,6 +24,7 @@
 // free of bank conflicts.
 #include <stdio.h>
 
+#include <array>
 #include <map>
 #include <mutex>
 #include <set>
@@ -538,32 +539,36 @@ static int launch(const AttnParams& P, cudaStream_t s) {
 
 }  // namespace i4
 
-int int4_clusters(int n) {
+const int* int4_clusters() {
     static std::mutex mu;
-    static std::map<std::pair<int, int>, int> known;
+    static std::map<int, std::array<int, 9>> known;
+    static const std::array<int, 9> none = {};
     int dev = 0;
-    if (n < 2 || n > 8 || cudaGetDevice(&dev) != cudaSuccess) return 0;
+    if (cudaGetDevice(&dev) != cudaSuccess) return none.data();
     std::lock_guard<std::mutex> lock(mu);
-    auto it = known.find({dev, n});
-    if (it != known.end()) return it->second;
+    auto it = known.find(dev);
+    if (it != known.end()) return it->second.data();
     auto kern = i4::paged_attention_int4_kernel<32, 12, true>;
-    cudaLaunchConfig_t cfg = {};
-    cfg.gridDim = dim3(n);
-    cfg.blockDim = dim3(12 * 32);
-    cfg.dynamicSmemBytes = i4::SMEM<12>;
-    cudaLaunchAttribute attr[1];
-    attr[0].id = cudaLaunchAttributeClusterDimension;
-    attr[0].val.clusterDim.x = n;
-    attr[0].val.clusterDim.y = attr[0].val.clusterDim.z = 1;
-    cfg.attrs = attr;
-    cfg.numAttrs = 1;
-    int count = 0;
-    if (cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, i4::SMEM<12>) != cudaSuccess ||
-        cudaOccupancyMaxActiveClusters(&count, kern, &cfg) != cudaSuccess) {
-        cudaGetLastError();
-        count = 0;
+    std::array<int, 9> count = {};
+    bool ok = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, i4::SMEM<12>) == cudaSuccess;
+    for (int n = 2; n <= 8 && ok; ++n) {
+        cudaLaunchConfig_t cfg = {};
+        cfg.gridDim = dim3(n);
+        cfg.blockDim = dim3(12 * 32);
+        cfg.dynamicSmemBytes = i4::SMEM<12>;
+        cudaLaunchAttribute attr[1];
+        attr[0].id = cudaLaunchAttributeClusterDimension;
+        attr[0].val.clusterDim.x = n;
+        attr[0].val.clusterDim.y = attr[0].val.clusterDim.z = 1;
+        cfg.attrs = attr;
+        cfg.numAttrs = 1;
+        ok = cudaOccupancyMaxActiveClusters(&count[n], kern, &cfg) == cudaSuccess;
     }
-    return known[{dev, n}] = count;
+    if (!ok) {
+        cudaGetLastError();
+        count.fill(0);                                      // no clusters
+    }
+    return (known[dev] = count).data();
 }
 
 int launch_attention_int4(const AttnParams& P, cudaStream_t s, char* text, size_t text_bytes) {
