@@ -537,3 +537,36 @@ def test_page_order_does_not_matter():
     inv[perm] = torch.arange(lay.num_pages)
     lay.block_table = inv[lay.block_table.long()].to(torch.int32)
     assert torch.equal(_attend(lay, q, kc[perm.cuda()], vc[perm.cuda()], ks, vs), want)
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("dt", [fp8kv.FP8KV_CACHE_E4M3, fp8kv.FP8KV_CACHE_BF16, fp8kv.FP8KV_CACHE_INT4])
+@pytest.mark.parametrize("T,H", [(1200, 16), (4999, 5)])
+def test_gather_of_few_and_many_rows(dt, T, H):
+    """Either side of the number of rows above which a thread takes 16 elements:
+    the rows of a slot are the same wherever and however they are read."""
+    ps, ks, vs = 64, _scale(0.02), _scale(0.03)
+    pages = T // ps + 2
+    if dt == fp8kv.FP8KV_CACHE_INT4:
+        kc, vc = (fp8kv.fp8kv_int4_cache(pages, H, ps) for _ in range(2))
+    else:
+        kc, vc = (torch.zeros((pages, H, ps, 128), device="cuda",
+                              dtype=torch.uint8 if dt == fp8kv.FP8KV_CACHE_E4M3 else torch.bfloat16) for _ in range(2))
+    g = gen.generator(T)
+    k, v = (torch.randn((T, H, 128), generator=g).to(torch.bfloat16).cuda() for _ in range(2))
+    slots = torch.randperm(pages * ps, generator=g)[:T].cuda()
+    fp8kv.fp8kv_cache_insert(k, v, slots, ks, vs, kc, vc)
+    ko, vo = fp8kv.fp8kv_cache_gather(slots, ks, vs, kc, vc)
+    some = torch.randperm(T, generator=g)[:100].cuda()
+    k1, v1 = fp8kv.fp8kv_cache_gather(slots[some], ks, vs, kc, vc)
+    assert torch.equal(ko[some], k1) and torch.equal(vo[some], v1)
+    if dt == fp8kv.FP8KV_CACHE_BF16:
+        assert torch.equal(ko, k) and torch.equal(vo, v)
+    elif dt == fp8kv.FP8KV_CACHE_INT4:
+        n, sc = int4_np.encode_rows(v.float().cpu().numpy(), vs.item())
+        want = torch.from_numpy(n * np.repeat(int4_np.e4m3_value(sc), 16, -1)).float() * vs.cpu()
+        assert torch.equal(vo.cpu(), want.to(torch.bfloat16))
+    else:
+        # E4M3: half a step, 2^-4 of the value or 2^-10 scale units; then fp32 and bf16 roundings, under 2^-7 of it
+        err = (vo.float() - v.float()).abs()
+        assert bool((err <= v.float().abs() * (2.0 ** -4 + 2.0 ** -7) + 0.03 * 2.0 ** -10).all())

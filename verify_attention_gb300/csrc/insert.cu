@@ -185,36 +185,46 @@ int launch_append_int4(const void* k, const void* v, const int32_t* seq_lens, co
 
 // ------------------------------------------------------------------- gather
 
-// 16 stored values of one cache as bf16 (two 16-byte stores): the row's
-// elements 16 * block ... + 15 of (page, head, offset).
-template <int DT>
-__device__ __forceinline__ void gather16(const uint8_t* __restrict__ cache, float c, int64_t page, int off, int h,
-                                         int Hkv, int page_size, int block, uint4* __restrict__ out) {
+// N (8 or 16) stored values of one cache as bf16: the elements N * part ... of
+// (page, head, offset).
+template <int DT, int N>
+__device__ __forceinline__ void gather_part(const uint8_t* __restrict__ cache, float c, int64_t page, int off, int h,
+                                            int Hkv, int page_size, int part, uint4* __restrict__ out) {
     const int64_t ph = page * Hkv + h;
-    uint32_t w[8];
+    uint32_t w[N / 2];
     if (DT == FP8KV_CACHE_BF16) {
-        const uint4* src = reinterpret_cast<const uint4*>(cache) + ((ph * page_size + off) * 16 + 2 * block);
-        out[0] = src[0];
-        out[1] = src[1];
+        const uint4* src = reinterpret_cast<const uint4*>(cache) + ((ph * page_size + off) * 16 + N / 8 * part);
+#pragma unroll
+        for (int j = 0; j < N / 8; ++j) out[j] = src[j];
         return;
     }
     if (DT == FP8KV_CACHE_E4M3) {
-        const uint4 x = *reinterpret_cast<const uint4*>(cache + (ph * page_size + off) * 128 + 16 * block);
-        const uint32_t cw[4] = {x.x, x.y, x.z, x.w};
+        const uint2* src = reinterpret_cast<const uint2*>(cache + (ph * page_size + off) * 128 + N * part);
+        uint32_t cw[N / 4];
+        if (N == 16) {
+            *reinterpret_cast<uint4*>(cw) = *reinterpret_cast<const uint4*>(src);
+        } else {
+            *reinterpret_cast<uint2*>(cw) = *src;
+        }
 #pragma unroll
-        for (int j = 0; j < 8; ++j) {
+        for (int j = 0; j < N / 2; ++j) {
             float lo, hi;
             e4m3x2_to_f32x2(cw[j >> 1] >> (16 * (j & 1)), lo, hi);
             w[j] = pack_bf16x2(__fmul_rn(lo, c), __fmul_rn(hi, c));
         }
     } else {
         const int64_t base = ph * page_size * kInt4RowBytes;
-        const uint2 x = *reinterpret_cast<const uint2*>(cache + base + off * kInt4CodeBytes + block * 8);
-        const uint32_t cw[2] = {x.x, x.y};
+        const uint32_t* src = reinterpret_cast<const uint32_t*>(cache + base + off * kInt4CodeBytes + N / 2 * part);
+        uint32_t cw[N / 8];
+        if (N == 16) {
+            *reinterpret_cast<uint2*>(cw) = *reinterpret_cast<const uint2*>(src);
+        } else {
+            cw[0] = *src;
+        }
         float s, unused;
-        e4m3x2_to_f32x2(cache[base + page_size * kInt4CodeBytes + off * kInt4ScaleBytes + block], s, unused);
+        e4m3x2_to_f32x2(cache[base + page_size * kInt4CodeBytes + off * kInt4ScaleBytes + N * part / 16], s, unused);
 #pragma unroll
-        for (int j = 0; j < 8; ++j) {
+        for (int j = 0; j < N / 2; ++j) {
             const uint32_t b = cw[j >> 2] >> (8 * (j & 3));
             // n from the low mantissa bits of 2^23 + 8 + n (conversions from
             // integer would keep their 16-lane unit busy for half of the
@@ -224,13 +234,15 @@ __device__ __forceinline__ void gather16(const uint8_t* __restrict__ cache, floa
             w[j] = pack_bf16x2(__fmul_rn(lo * s, c), __fmul_rn(hi * s, c));
         }
     }
-    out[0] = make_uint4(w[0], w[1], w[2], w[3]);
-    out[1] = make_uint4(w[4], w[5], w[6], w[7]);
+#pragma unroll
+    for (int j = 0; j < N / 8; ++j) out[j] = make_uint4(w[4 * j], w[4 * j + 1], w[4 * j + 2], w[4 * j + 3]);
 }
 
-// One thread per (token, head, 16-element block) of K and V (8 elements a thread,
-// whose stores would cover whole lines: 71 us for 65536 tokens against 61).
-template <int DT>
+// One thread per (token, head, N elements) of K and V.  N = 8 while all threads
+// are resident at once, for its shorter way from the slot to the last store (768
+// tokens of 8 heads: 2.4 us, N = 16 3.2); N = 16 for more, half the load and
+// store instructions (65536 tokens: 61 us, N = 8 71).
+template <int DT, int N>
 __global__ void __launch_bounds__(256) gather_kernel(const int64_t* __restrict__ slots, int T, int Hkv,
                                                      const float* __restrict__ k_scale,
                                                      const float* __restrict__ v_scale,
@@ -240,22 +252,23 @@ __global__ void __launch_bounds__(256) gather_kernel(const int64_t* __restrict__
                                                      uint4* __restrict__ v_out) {
     pdl_launch_dependents();
     pdl_wait();
+    constexpr int PARTS = 128 / N;
     const int64_t i = (int64_t)blockIdx.x * blockDim.x + threadIdx.x;
-    if (i >= (int64_t)T * Hkv * 8) return;
-    const int block = (int)(i & 7);
-    const int64_t row = i >> 3, t = token_of(row, Hkv);
+    if (i >= (int64_t)T * Hkv * PARTS) return;
+    const int part = (int)(i % PARTS);
+    const int64_t row = i / PARTS, t = token_of(row, Hkv);
     const int h = (int)(row - t * Hkv);
     const int64_t slot = slots[t];
     if (slot < 0) return;
     if (slot >= num_slots) {
-        if (block == 0) flag(FP8KV_DEV_BAD_SLOT);
+        if (part == 0) flag(FP8KV_DEV_BAD_SLOT);
         return;
     }
     const float ks = DT == FP8KV_CACHE_BF16 ? 1.f : *k_scale, vs = DT == FP8KV_CACHE_BF16 ? 1.f : *v_scale;
     const int64_t page = slot >> (page_size == 64 ? 6 : 5);
     const int off = (int)slot & (page_size - 1);
-    gather16<DT>(k_cache, ks, page, off, h, Hkv, page_size, block, k_out + 2 * i);
-    gather16<DT>(v_cache, vs, page, off, h, Hkv, page_size, block, v_out + 2 * i);
+    gather_part<DT, N>(k_cache, ks, page, off, h, Hkv, page_size, part, k_out + N / 8 * i);
+    gather_part<DT, N>(v_cache, vs, page, off, h, Hkv, page_size, part, v_out + N / 8 * i);
 }
 
 // ------------------------------------------------ fused RMSNorm+RoPE+insert
@@ -462,11 +475,13 @@ extern "C" int fp8kv_cache_gather(const int64_t* slot_mapping, int T, int Hkv, i
     if (cache_dtype != FP8KV_CACHE_BF16 && (!k_scale || !v_scale)) return FP8KV_ERR_INVALID_ARG;
     if (!aligned16(k_cache) || !aligned16(v_cache) || !aligned16(k_out) || !aligned16(v_out))
         return FP8KV_ERR_INVALID_ARG;
-    const int64_t blocks = ((int64_t)T * Hkv * 8 + 255) / 256;
+    const bool few = (int64_t)T * Hkv * 16 <= 2048ll * num_sms();
+    const int64_t blocks = ((int64_t)T * Hkv * (few ? 16 : 8) + 255) / 256;
     if (blocks > 0x7fffffff) return FP8KV_ERR_UNSUPPORTED;
-    auto kern = cache_dtype == FP8KV_CACHE_INT4   ? gather_kernel<FP8KV_CACHE_INT4>
-                : cache_dtype == FP8KV_CACHE_E4M3 ? gather_kernel<FP8KV_CACHE_E4M3>
-                                                  : gather_kernel<FP8KV_CACHE_BF16>;
+    auto kern =
+        cache_dtype == FP8KV_CACHE_INT4   ? (few ? gather_kernel<FP8KV_CACHE_INT4, 8> : gather_kernel<FP8KV_CACHE_INT4, 16>)
+        : cache_dtype == FP8KV_CACHE_E4M3 ? (few ? gather_kernel<FP8KV_CACHE_E4M3, 8> : gather_kernel<FP8KV_CACHE_E4M3, 16>)
+                                          : (few ? gather_kernel<FP8KV_CACHE_BF16, 8> : gather_kernel<FP8KV_CACHE_BF16, 16>);
     cudaError_t e = launch_pdl(kern, dim3((unsigned)blocks), dim3(256), 0, (cudaStream_t)stream, slot_mapping, T, Hkv,
                                k_scale, v_scale, (const uint8_t*)k_cache, (const uint8_t*)v_cache,
                                (int64_t)num_pages * page_size, page_size, (uint4*)k_out, (uint4*)v_out);
