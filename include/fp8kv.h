@@ -268,12 +268,14 @@ size_t fp8kv_paged_attention_workspace_size(int B, int M, int Hq, int Hkv, int D
  * through their log-sum-exp: by a reduce kernel over workspace partials, or,
  * for one sequence (B = 1) of 17 to 128 rows per KV head (one row tile) on an
  * E4M3 cache in at most 8 partitions, on chip by the partitions of a KV head running as one
- * thread-block cluster (fp8kv_last_dispatch reports "cluster=N").
+ * thread-block cluster (fp8kv_last_dispatch reports "cluster=N").  Over an
+ * INT4 cache any call of one row tile (16 or 128 rows per KV head) in 2 to 8
+ * partitions is combined on chip where all its clusters run at once.
  *
  *   q            (device) bf16 [B][M][Hq][D]
  *   k_cache, v_cache (device) [num_pages][Hkv][page_size][D] (cache_dtype)
  *   block_table  (device) int32 [B][max_pages_per_seq]; entries of pages with
- *                no visible key are never read
+ *                no visible key are never read (INT4: never used)
  *   seq_lens     (device) int32 [B]; max_seq_len (host) >= every seq_lens[b]
  *   k_scale, v_scale (device) fp32 scalars (E4M3 and INT4 only)
  *   sm_scale     (host) fp32 logit multiplier, e.g. 1/sqrt(D)
@@ -317,8 +319,9 @@ int fp8kv_paged_attention(const void* q, const void* k_cache, const void* v_cach
  * with those slots followed by fp8kv_paged_attention.  On the tensor-memory
  * path with one 128-row tile per KV head the CTA whose partition holds a new
  * position writes it before loading that page (no separate insert launch);
- * otherwise (a prefill chunk in several row tiles, or the mma.sync kernels)
- * an append kernel runs first.  k_new and v_new must be 16-byte aligned; B = 0 is a no-op.
+ * over an INT4 cache this holds for the mma.sync kernel too (one tile of 16
+ * rows per KV head); otherwise (several row tiles, or the mma.sync kernels over
+ * the other caches) an append kernel runs first.  k_new and v_new must be 16-byte aligned; B = 0 is a no-op.
  * Device check: a block-table entry outside [0, num_pages) at a new
  * position -> that token is not written (FP8KV_DEV_BAD_SLOT).
  */

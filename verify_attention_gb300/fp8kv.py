@@ -186,9 +186,11 @@ def fp8kv_cache_insert(k, v, slot_mapping, k_scale, v_scale, k_cache, v_cache, s
     T, Hkv, D = k.shape
     num_pages, heads, page_size = _cache_shape(k_cache, v_cache, dt)
     if dt == FP8KV_CACHE_INT4:
-        _int4_rows(k, v, slot_mapping, heads, k_scale, v_scale)
-    rc = lib().fp8kv_cache_insert(_ptr(k), _ptr(v), _ptr(slot_mapping), T, Hkv, D, _ptr(k_scale),
-                                  _ptr(v_scale), _ptr(k_cache), _ptr(v_cache), num_pages, page_size,
+        if heads != Hkv or v.shape != (T, Hkv, D) or slot_mapping.numel() != T:
+            raise ValueError(f"k, v must be [T][{heads}][D] and slot_mapping [T]")
+        _one_scale(k_scale, v_scale)
+    rc = lib().fp8kv_cache_insert(k.data_ptr(), v.data_ptr(), slot_mapping.data_ptr(), T, Hkv, D, _ptr(k_scale),
+                                  _ptr(v_scale), k_cache.data_ptr(), v_cache.data_ptr(), num_pages, page_size,
                                   dt, _stream(stream, k_cache))
     _check("fp8kv_cache_insert", rc)
 
@@ -199,21 +201,17 @@ def _int4_call(q, k_cache, block_table, seq_lens, k_scale, v_scale, out, num_pag
     B = q.shape[0]
     if block_table.dim() != 2 or block_table.shape[0] != B or seq_lens.numel() != B:
         raise ValueError(f"block_table must be [{B}][pages] and seq_lens [{B}]")
-    for t, n in ((k_scale, "k_scale"), (v_scale, "v_scale")):
-        if _dev(t, n, torch.float32).numel() != 1:
-            raise ValueError(f"{n} must be one fp32")
+    _one_scale(k_scale, v_scale)
     if out is not None and _dev(out, "out", torch.bfloat16).shape != q.shape:
         raise ValueError("out must have the shape of q")
     if num_pages is not None and num_pages > k_cache.shape[0]:
         raise ValueError(f"num_pages is {num_pages}, the cache has {k_cache.shape[0]}")
 
 
-def _int4_rows(k, v, slot_mapping, heads, k_scale, v_scale):
-    if v.shape != k.shape or k.shape[1] != heads or slot_mapping.numel() != k.shape[0]:
-        raise ValueError(f"k, v must be [T][{heads}][D] and slot_mapping [T]")
-    for t, n in ((k_scale, "k_scale"), (v_scale, "v_scale")):
-        if _dev(t, n, torch.float32).numel() != 1:
-            raise ValueError(f"{n} must be one fp32")
+def _one_scale(k_scale, v_scale):
+    _dev(k_scale, "k_scale", torch.float32), _dev(v_scale, "v_scale", torch.float32)
+    if k_scale.numel() != 1 or v_scale.numel() != 1:
+        raise ValueError("k_scale and v_scale must be one fp32 each")
 
 
 def fp8kv_cache_gather(slot_mapping, k_scale, v_scale, k_cache, v_cache, k_out=None, v_out=None, stream=None):
@@ -222,24 +220,23 @@ def fp8kv_cache_gather(slot_mapping, k_scale, v_scale, k_cache, v_cache, k_out=N
     outputs are allocated here).  Any cache type, per-tensor scales."""
     dt = _cache_dtype(k_cache)
     _dev(slot_mapping, "slot_mapping", torch.int64), _dev(k_cache, "k_cache"), _dev(v_cache, "v_cache")
-    if v_cache.dtype != k_cache.dtype or v_cache.shape != k_cache.shape:
+    if dt != FP8KV_CACHE_INT4 and (v_cache.dtype != k_cache.dtype or v_cache.shape != k_cache.shape):
         raise ValueError("k_cache and v_cache must have the same type and shape")
     num_pages, Hkv, page_size = _cache_shape(k_cache, v_cache, dt)
     T, D = slot_mapping.numel(), 128 if dt == FP8KV_CACHE_INT4 else k_cache.shape[3]
     if dt != FP8KV_CACHE_BF16:
         _dev(k_scale, "k_scale", torch.float32), _dev(v_scale, "v_scale", torch.float32)
-    outs = []
-    for t, n in ((k_out, "k_out"), (v_out, "v_out")):
-        if t is None:
-            t = _zeros((T, Hkv, D), k_cache.device, stream)
-        if tuple(_dev(t, n, torch.bfloat16).shape) != (T, Hkv, D):
-            raise ValueError(f"{n} must be {(T, Hkv, D)}, got {tuple(t.shape)}")
-        outs.append(t)
-    rc = lib().fp8kv_cache_gather(_ptr(slot_mapping), T, Hkv, D, _ptr(k_scale), _ptr(v_scale), _ptr(k_cache),
-                                  _ptr(v_cache), num_pages, page_size, dt, _ptr(outs[0]), _ptr(outs[1]),
-                                  _stream(stream, k_cache))
+    if k_out is None and v_out is None:
+        k_out, v_out = _zeros((2, T, Hkv, D), k_cache.device, stream).unbind(0)     # one fill instead of two
+    k_out = _zeros((T, Hkv, D), k_cache.device, stream) if k_out is None else _dev(k_out, "k_out", torch.bfloat16)
+    v_out = _zeros((T, Hkv, D), k_cache.device, stream) if v_out is None else _dev(v_out, "v_out", torch.bfloat16)
+    if k_out.shape != (T, Hkv, D) or v_out.shape != (T, Hkv, D):
+        raise ValueError(f"k_out and v_out must be {(T, Hkv, D)}, got {tuple(k_out.shape)} and {tuple(v_out.shape)}")
+    rc = lib().fp8kv_cache_gather(slot_mapping.data_ptr(), T, Hkv, D, _ptr(k_scale), _ptr(v_scale),
+                                  k_cache.data_ptr(), v_cache.data_ptr(), num_pages, page_size, dt, k_out.data_ptr(),
+                                  v_out.data_ptr(), _stream(stream, k_cache))
     _check("fp8kv_cache_gather", rc)
-    return tuple(outs)
+    return k_out, v_out
 
 
 def _head_scales(k_scale, v_scale, Hkv):
@@ -282,17 +279,16 @@ def fp8kv_qk_norm_rope_insert(q, k, v, positions, q_norm_w, k_norm_w, eps, cos_s
     _check("fp8kv_qk_norm_rope_insert", rc)
 
 
-def _token_rows(t: torch.Tensor, name: str, T: int):
+def _token_rows(t: torch.Tensor, name: str, T: int, heads: int, D: int):
     """bf16 [T][heads][D] with dense tokens; returns the elements between tokens."""
     if not t.is_cuda:
         raise ValueError(f"{name} must be a CUDA tensor")
     if t.dtype != torch.bfloat16:
         raise ValueError(f"{name} must be {torch.bfloat16}, got {t.dtype}")
-    n, heads, D = t.shape
     st = t.stride()
-    if n != T or st[2] != 1 or (heads > 1 and st[1] != D):
-        raise ValueError(f"{name} must be [{T}][heads][D] with dense tokens")
-    return st[0] if n > 1 else heads * D
+    if t.shape != (T, heads, D) or st[2] != 1 or (heads > 1 and st[1] != D):
+        raise ValueError(f"{name} must be [{T}][{heads}][{D}] with dense tokens")
+    return st[0] if T > 1 else heads * D
 
 
 def fp8kv_prompt_attention(q, k, v, cu_seqlens, max_seq_len, sm_scale, window_left=-1, out=None, stream=None):
@@ -302,17 +298,15 @@ def fp8kv_prompt_attention(q, k, v, cu_seqlens, max_seq_len, sm_scale, window_le
     sequence are left as they are (zeros when allocated here)."""
     T, Hq, D = q.shape
     Hkv = k.shape[1]
-    if k.shape[2] != D or v.shape != k.shape:
-        raise ValueError("k and v must be [T][Hkv][D] with the D of q")
-    strides = [_token_rows(t, n, T) for t, n in ((q, "q"), (k, "k"), (v, "v"))]
+    q_stride = _token_rows(q, "q", T, Hq, D)
+    k_stride, v_stride = _token_rows(k, "k", T, Hkv, D), _token_rows(v, "v", T, Hkv, D)
     _dev(cu_seqlens, "cu_seqlens", torch.int32)
-    if out is None:
-        out = _zeros((T, Hq, D), q.device, stream)
-    if tuple(_dev(out, "out", torch.bfloat16).shape) != (T, Hq, D):
+    out = _zeros((T, Hq, D), q.device, stream) if out is None else _dev(out, "out", torch.bfloat16)
+    if out.shape != (T, Hq, D):
         raise ValueError(f"out must be {(T, Hq, D)}, got {tuple(out.shape)}")
-    rc = lib().fp8kv_prompt_attention(_ptr(q), strides[0], _ptr(k), strides[1], _ptr(v), strides[2],
-                                      _ptr(cu_seqlens), cu_seqlens.numel() - 1, T, int(max_seq_len), Hq, Hkv, D,
-                                      float(sm_scale), int(window_left), _ptr(out), _stream(stream, q))
+    rc = lib().fp8kv_prompt_attention(q.data_ptr(), q_stride, k.data_ptr(), k_stride, v.data_ptr(), v_stride,
+                                      cu_seqlens.data_ptr(), cu_seqlens.numel() - 1, T, int(max_seq_len), Hq, Hkv, D,
+                                      float(sm_scale), int(window_left), out.data_ptr(), _stream(stream, q))
     _check("fp8kv_prompt_attention", rc)
     return out
 
