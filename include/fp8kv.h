@@ -291,8 +291,8 @@ size_t fp8kv_paged_attention_workspace_size(int B, int M, int Hq, int Hkv, int D
  * whole 128-key tiles (split_tokens 0 or a multiple of 128): a prefill chunk
  * at the end of the context, causal within the chunk, on the tcgen05 kernel
  * in 128-row tiles (Hkv * ceil(M * Hq/Hkv / 128) <= 65535); other shapes
- * return FP8KV_ERR_UNSUPPORTED.  B = 0 launches nothing and returns FP8KV_OK
- * without reading any pointer.
+ * return FP8KV_ERR_UNSUPPORTED (over an INT4 cache B > 65535 too).  B = 0
+ * launches nothing and returns FP8KV_OK without reading any pointer.
  * Device checks: seq_len < M, seq_len > max_seq_len or more pages than
  * max_pages_per_seq -> that sequence's output is left untouched
  * (FP8KV_DEV_BAD_SEQ_LEN); page ids outside [0, num_pages) read zeros.

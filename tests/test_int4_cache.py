@@ -80,6 +80,13 @@ def test_int4_entry_points_check_their_arguments(L):
     assert L.fp8kv_paged_attention_layers(ctypes.byref(layers), 1, 1, 12, 72, 8, 128, 32, 2, P16, 1 << 30, NULL) in (1, 2)
 
 
+def test_int4_attention_refuses_grids_that_do_not_exist(L):
+    att = dict(q=P16, k=P16, v=P16, dt=2, bt=P16, mpps=4, sl=P16, maxL=100, B=1, M=1, Hq=72, Hkv=8, D=128, ps=32, P=16,
+               ks=P16, vs=P16, sm=0.088, wl=-1, split=0, ws=P16, wsb=1 << 62, out=P16, stream=NULL)
+    for over in ({"B": 65536}, {"Hq": 65536, "Hkv": 65536}, {"M": 16, "Hq": 2 * 33000, "Hkv": 33000}):
+        assert L.fp8kv_paged_attention(*{**att, **over}.values()) == 2, over
+
+
 def test_binding_refuses_other_shapes():
     assert fp8kv._cache_dtype(torch.zeros((2, 8, 32 * 72), dtype=torch.uint8)) == fp8kv.FP8KV_CACHE_INT4
     assert fp8kv._cache_dtype(torch.zeros((2, 8, 32, 128), dtype=torch.uint8)) == fp8kv.FP8KV_CACHE_E4M3

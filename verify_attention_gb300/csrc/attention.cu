@@ -1139,7 +1139,8 @@ static int attention_call(const void* k_new, const void* v_new, const void* q, c
     // which serves at most 16 rows per sequence and 144 per KV head
     const bool use_tc = fp8 && tc_rows(M, Hq, Hkv) && (plan.split_tokens % tc_tile_tokens()) == 0;
     if (!use_tc && tc_only(M, Hq, Hkv)) return FP8KV_ERR_UNSUPPORTED;
-    if (int4 && (int64_t)Hkv * ceil_div((int64_t)M * (Hq / Hkv), 16) > 65535) return FP8KV_ERR_UNSUPPORTED;   // grid
+    if (int4 && ((int64_t)Hkv * ceil_div((int64_t)M * (Hq / Hkv), 16) > 65535 || B > 65535))
+        return FP8KV_ERR_UNSUPPORTED;                           // grid
     if (B == 0) return FP8KV_OK;                                // nothing to do; no pointer is read
     if (!q || !k_cache || !v_cache || !block_table || !seq_lens || !out) return FP8KV_ERR_INVALID_ARG;
     if ((k_new != nullptr) != (v_new != nullptr) || (k_new && (!al16(k_new) || !al16(v_new))))
