@@ -1020,7 +1020,8 @@ static Int4Cut int4_cut(const Plan& plan, bool tc, bool one_tile, bool given, in
     Int4Cut best = {plan.split_pages, plan.num_splits, 12, false, false};
     // a single round of keys: nothing to choose
     if (plan.num_splits == 1 && units <= sms && plan.pages * PS <= (tc ? 128 : 384)) return best;
-    const int* clusters = one_tile ? int4_clusters() : nullptr;
+    int clusters[9];
+    if (one_tile) int4_clusters(clusters);
     float best_us = INFINITY;
     auto look = [&](int64_t want, int warps, bool cluster) {
         int ns = plan.num_splits, sp = plan.split_pages;

@@ -99,7 +99,7 @@ int launch_append_int4(const void* k, const void* v, const int32_t* seq_lens, co
 // partitions, cut from the key range of the tile.
 int launch_attention_int4(const AttnParams& P, cudaStream_t s, char* text, size_t text_bytes);
 int launch_attention_int4_tc(const AttnParams& P, cudaStream_t s, char* text, size_t text_bytes);
-const int* int4_clusters(); // [n], n = 2 .. 8: clusters of n CTAs, one CTA an SM, resident at once
+void int4_clusters(int (&count)[9]);    // [n], n = 2 .. 8: clusters of n CTAs, one CTA an SM, resident at once
 
 // Host launcher of the tcgen05 kernel (attention_tc.cu).  Returns
 // FP8KV_ERR_UNSUPPORTED when the shape is not one it implements.

@@ -24,12 +24,6 @@
 // free of bank conflicts.
 #include <stdio.h>
 
-#include <array>
-#include <map>
-#include <mutex>
-#include <set>
-#include <utility>
-
 #include "attention.cuh"
 #include "common.cuh"
 #include "int4.cuh"
@@ -519,19 +513,9 @@ __global__ void __launch_bounds__(WARPS * 32, 12 / WARPS) paged_attention_int4_k
 
 template <int PS, int WARPS, bool CL>
 static int launch(const AttnParams& P, cudaStream_t s) {
-    static std::mutex mu;
-    static std::set<int> done;
+    static std::atomic<uint64_t> done{0};
     auto kern = paged_attention_int4_kernel<PS, WARPS, CL>;
-    {
-        int dev = 0;
-        if (cudaGetDevice(&dev) != cudaSuccess) return FP8KV_ERR_CUDA;
-        std::lock_guard<std::mutex> lock(mu);
-        if (!done.count(dev)) {
-            if (cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, SMEM<WARPS>) != cudaSuccess)
-                return FP8KV_ERR_CUDA;
-            done.insert(dev);
-        }
-    }
+    if (opt_in_smem(done, (const void*)kern, SMEM<WARPS>) != cudaSuccess) return (cudaGetLastError(), FP8KV_ERR_CUDA);
     const dim3 grid(P.num_splits, P.Hkv * P.NT, P.B);
     const cudaError_t e = launch_pdl_cluster(kern, grid, dim3(WARPS * 32), SMEM<WARPS>, s, P.cluster, P);
     return e == cudaSuccess ? FP8KV_OK : (cudaGetLastError(), FP8KV_ERR_CUDA);
@@ -539,36 +523,36 @@ static int launch(const AttnParams& P, cudaStream_t s) {
 
 }  // namespace i4
 
-const int* int4_clusters() {
-    static std::mutex mu;
-    static std::map<int, std::array<int, 9>> known;
-    static const std::array<int, 9> none = {};
+void int4_clusters(int (&count)[9]) {
+    static std::atomic<int> known[64][9];                   // [device][n]: 1 + count
     int dev = 0;
-    if (cudaGetDevice(&dev) != cudaSuccess) return none.data();
-    std::lock_guard<std::mutex> lock(mu);
-    auto it = known.find(dev);
-    if (it != known.end()) return it->second.data();
-    auto kern = i4::paged_attention_int4_kernel<32, 12, true>;
-    std::array<int, 9> count = {};
-    bool ok = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, i4::SMEM<12>) == cudaSuccess;
-    for (int n = 2; n <= 8 && ok; ++n) {
-        cudaLaunchConfig_t cfg = {};
-        cfg.gridDim = dim3(n);
-        cfg.blockDim = dim3(12 * 32);
-        cfg.dynamicSmemBytes = i4::SMEM<12>;
-        cudaLaunchAttribute attr[1];
-        attr[0].id = cudaLaunchAttributeClusterDimension;
-        attr[0].val.clusterDim.x = n;
-        attr[0].val.clusterDim.y = attr[0].val.clusterDim.z = 1;
-        cfg.attrs = attr;
-        cfg.numAttrs = 1;
-        ok = cudaOccupancyMaxActiveClusters(&count[n], kern, &cfg) == cudaSuccess;
+    for (int n = 0; n < 9; ++n) count[n] = 0;
+    if (cudaGetDevice(&dev) != cudaSuccess || dev >= 64) return;
+    for (int n = 2; n < 9; ++n) {
+        int k = known[dev][n].load(std::memory_order_relaxed);
+        if (!k) {
+            auto kern = i4::paged_attention_int4_kernel<32, 12, true>;
+            cudaLaunchConfig_t cfg = {};
+            cfg.gridDim = dim3(n);
+            cfg.blockDim = dim3(12 * 32);
+            cfg.dynamicSmemBytes = i4::SMEM<12>;
+            cudaLaunchAttribute attr[1];
+            attr[0].id = cudaLaunchAttributeClusterDimension;
+            attr[0].val.clusterDim.x = n;
+            attr[0].val.clusterDim.y = attr[0].val.clusterDim.z = 1;
+            cfg.attrs = attr;
+            cfg.numAttrs = 1;
+            int most = 0;
+            if (cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, i4::SMEM<12>) != cudaSuccess ||
+                cudaOccupancyMaxActiveClusters(&most, kern, &cfg) != cudaSuccess) {
+                cudaGetLastError();
+                most = 0;                                   // no clusters
+            }
+            k = 1 + most;
+            known[dev][n].store(k, std::memory_order_relaxed);
+        }
+        count[n] = k - 1;
     }
-    if (!ok) {
-        cudaGetLastError();
-        count.fill(0);                                      // no clusters
-    }
-    return (known[dev] = count).data();
 }
 
 int launch_attention_int4(const AttnParams& P, cudaStream_t s, char* text, size_t text_bytes) {

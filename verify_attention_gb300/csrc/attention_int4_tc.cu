@@ -43,10 +43,6 @@
 // TMEM columns: Q 0-63, S/P 3 x 64 (64-255), O 256-383, 384-511.
 #include <stdio.h>
 
-#include <mutex>
-#include <set>
-#include <utility>
-
 #include "attention.cuh"
 #include "common.cuh"
 #include "int4.cuh"
@@ -718,21 +714,12 @@ int launch_attention_int4_tc(const AttnParams& P, cudaStream_t s, char* text, si
     if (P.cluster > 1 && (P.cluster > i4tc::kMaxCluster || P.cluster != P.num_splits || RT > 1 || P.lpt_order))
         return FP8KV_ERR_UNSUPPORTED;
     if ((P.split_pages * P.page_size) % i4tc::NK || (int64_t)RT * P.Hkv > 65535) return FP8KV_ERR_UNSUPPORTED;
-    static std::mutex mu;
-    static std::set<std::pair<int, const void*>> done;
+    static std::atomic<uint64_t> done[2][2];                // [page size][cluster]
     auto kern = P.page_size == 32
                     ? (P.cluster > 1 ? i4tc::attention_int4_tc_kernel<32, true> : i4tc::attention_int4_tc_kernel<32, false>)
                     : (P.cluster > 1 ? i4tc::attention_int4_tc_kernel<64, true> : i4tc::attention_int4_tc_kernel<64, false>);
-    {
-        int dev = 0;
-        if (cudaGetDevice(&dev) != cudaSuccess) return FP8KV_ERR_CUDA;
-        std::lock_guard<std::mutex> lock(mu);
-        if (!done.count({dev, (const void*)kern})) {
-            if (cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, i4tc::SMEM) != cudaSuccess)
-                return FP8KV_ERR_CUDA;
-            done.insert({dev, (const void*)kern});
-        }
-    }
+    if (opt_in_smem(done[P.page_size == 64][P.cluster > 1], (const void*)kern, i4tc::SMEM) != cudaSuccess)
+        return (cudaGetLastError(), FP8KV_ERR_CUDA);
     const dim3 grid(P.num_splits, P.Hkv * RT, P.B);
     const cudaError_t e = launch_pdl_cluster(kern, grid, dim3(i4tc::THREADS), i4tc::SMEM, s, P.cluster, P);
     if (e != cudaSuccess) {

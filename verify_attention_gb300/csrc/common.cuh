@@ -7,6 +7,7 @@
 #include <cuda_runtime.h>
 #include <stdint.h>
 
+#include <atomic>
 #include <utility>
 
 #include "../../include/fp8kv.h"
@@ -381,6 +382,20 @@ template <typename... KArgs, typename... Args>
 static inline cudaError_t launch_pdl(void (*kernel)(KArgs...), dim3 grid, dim3 block, size_t smem,
                                      cudaStream_t stream, Args&&... args) {
     return launch_pdl_cluster(kernel, grid, block, smem, stream, 1, std::forward<Args>(args)...);
+}
+
+// Opt in to a kernel's dynamic shared memory, once per device (`done`: a bit for
+// each of the first 64; without a lock, as repeating it does no harm), so that
+// calls under capture issue no attribute change.
+static inline cudaError_t opt_in_smem(std::atomic<uint64_t>& done, const void* kernel, int bytes) {
+    int dev = 0;
+    cudaError_t e = cudaGetDevice(&dev);
+    if (e != cudaSuccess) return e;
+    const uint64_t bit = dev < 64 ? 1ull << dev : 0;
+    if (done.load(std::memory_order_relaxed) & bit) return cudaSuccess;
+    e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, bytes);
+    if (e == cudaSuccess) done.fetch_or(bit, std::memory_order_relaxed);
+    return e;
 }
 
 // ------------------------------------------------ thread-block clusters

@@ -40,9 +40,6 @@
 // of its S), O 256-383, 384-511.
 #include <stdio.h>
 
-#include <mutex>
-#include <set>
-
 #include "attention.cuh"
 #include "common.cuh"
 #include "tcgen05.cuh"
@@ -717,19 +714,9 @@ extern "C" int fp8kv_prompt_attention(const void* q, int64_t q_stride, const voi
     if (!rows_map(&tq, q, Hq, q_stride, T, G, NP) || !rows_map(&tk, k, Hkv, k_stride, T, 1, prompt::NK) ||
         !rows_map(&tv, v, Hkv, v_stride, T, 1, prompt::NK) || !rows_map(&to, out, Hq, (int64_t)Hq * 128, T, G, NP))
         return FP8KV_ERR_CUDA;
-    {
-        static std::mutex mu;
-        static std::set<int> done;
-        int dev = 0;
-        if (cudaGetDevice(&dev) != cudaSuccess) return FP8KV_ERR_CUDA;
-        std::lock_guard<std::mutex> lock(mu);
-        if (!done.count(dev)) {
-            if (cudaFuncSetAttribute(prompt::prompt_attention_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                                     prompt::SMEM) != cudaSuccess)
-                return FP8KV_ERR_CUDA;
-            done.insert(dev);
-        }
-    }
+    static std::atomic<uint64_t> done{0};
+    if (opt_in_smem(done, (const void*)prompt::prompt_attention_kernel, prompt::SMEM) != cudaSuccess)
+        return (cudaGetLastError(), FP8KV_ERR_CUDA);
     prompt::Params P = {};
     P.cu = cu_seqlens;
     P.out = (uint16_t*)out;
