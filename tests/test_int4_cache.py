@@ -577,3 +577,30 @@ def test_gather_of_few_and_many_rows(dt, T, H):
         # E4M3: half a step, 2^-4 of the value or 2^-10 scale units; then fp32 and bf16 roundings, under 2^-7 of it
         err = (vo.float() - v.float()).abs()
         assert bool((err <= v.float().abs() * (2.0 ** -4 + 2.0 ** -7) + 0.03 * 2.0 ** -10).all())
+
+
+@pytest.mark.gpu
+def test_calls_on_several_streams_at_once():
+    """Decode, verifier rows in a cluster and through partials, insert and gather
+    on streams of their own, each over its own cache, repeated."""
+    work = []
+    for seed, lens, M, split in ((1, [2000, 300], 1, 0), (2, [900], 12, 0), (3, [3000, 40], 12, 256), (4, [5000], 1, 512)):
+        lay, q, kc, vc, ks, vs, k, v, slots = _case(seed, lens, M, 9, 4, 32)
+        fp8kv.fp8kv_cache_insert(k, v, slots, ks, vs, kc, vc)
+        call = fp8kv.PreparedAttention(q, kc, vc, lay.block_table.cuda(), lay.seq_lens.cuda(), max(lens), ks, vs, SM,
+                                       split_tokens=split)
+        rows = fp8kv.fp8kv_cache_gather(slots, ks, vs, kc, vc)
+        work.append((call, call().clone(), (slots, ks, vs, kc, vc), rows, (k, v, slots, ks, vs, kc, vc),
+                     [torch.empty_like(r) for r in rows], torch.cuda.Stream()))
+    torch.cuda.synchronize()
+    for _ in range(30):
+        for call, _, g, _, ins, got, stream in work:
+            with torch.cuda.stream(stream):
+                fp8kv.fp8kv_cache_insert(*ins)
+                call()
+                fp8kv.fp8kv_cache_gather(*g, *got)
+    torch.cuda.synchronize()
+    for call, want, _, rows, _, got, _ in work:
+        assert torch.equal(call.out, want)
+        assert torch.equal(got[0], rows[0]) and torch.equal(got[1], rows[1])
+    assert fp8kv.fp8kv_device_status(clear=True) == 0
