@@ -319,3 +319,46 @@ def test_tensors_of_another_device_are_refused(monkeypatch):
               lambda: fp8kv.fp8kv_cache_gather(slots, one, one, kc, vc, torch.empty_like(k), torch.empty_like(v))):
         with pytest.raises(ValueError, match="current device"):
             f()
+
+
+# Items one of whose two row tiles is whole, then items with both, on every CTA:
+# the two share the staging tile of the output.
+
+def _staged_items(seed, NP, sequences, longest):
+    """Lengths whose last item has a whole first row tile and a partial, a
+    one-row or no second one, between sequences of whole items."""
+    rng = np.random.default_rng(seed)
+    ends = [NP, NP + 1, 2 * NP - 1]
+    return [2 * NP * int(rng.integers(0 if e else 1, longest)) + e
+            for e in (int(rng.choice([0, 0, *ends])) for _ in range(sequences))]
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("G,H", [(2, 8), (1, 4), (4, 3)])
+def test_output_tiles_of_items_with_one_whole_row_tile_exactly(G, H):
+    """With a window of its own key alone a row's output is that key's value,
+    bit for bit: items of one uncleaned key tile, far more than SMs."""
+    lens = _staged_items(G, 128 // G, 300, 4)
+    q, k, v, cu = _inputs(G, lens, G, H)
+    want = v.repeat_interleave(G, 1)
+    out = torch.empty_like(want)
+    for _ in range(40):
+        out.fill_(3.0)
+        fp8kv.fp8kv_prompt_attention(q, k, v, cu, max(lens), SM, window_left=0, out=out)
+        assert torch.equal(out, want)
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("G,H,window", [(8, 4, -1), (2, 4, 63), (16, 2, -1)])
+def test_output_tiles_of_items_with_one_whole_row_tile(G, H, window):
+    fp8kv.fp8kv_device_status(clear=True)
+    lens = _staged_items(10 + G, 128 // G, 150, 12)
+    q, k, v, cu = _inputs(20 + G, lens, G, H)
+    want = fp8kv.fp8kv_prompt_attention(q, k, v, cu, max(lens), SM, window_left=window)
+    _check(want, q, k, v, cu, window)
+    out = torch.empty_like(want)
+    for _ in range(40):
+        out.fill_(3.0)
+        fp8kv.fp8kv_prompt_attention(q, k, v, cu, max(lens), SM, window_left=window, out=out)
+        assert torch.equal(out, want)
+    assert fp8kv.fp8kv_device_status(clear=True) == 0

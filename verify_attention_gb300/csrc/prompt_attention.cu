@@ -70,8 +70,8 @@ enum {
     B_O = B_H + 2,                              // per row tile: O final
     B_OE = B_O + 2,                             // ... and read
     B_STAGED = B_OE + 2,                        // per row tile: output tile written
-    B_SENT = B_STAGED + 2,                      // ... and read by its store
-    B_TURN = B_SENT + 2,                        // per row tile: its MMA warp's turn
+    B_STAGE = B_STAGED + 2,                     // ... the staging tile is this row tile's to write
+    B_TURN = B_STAGE + 2,                       // per row tile: its MMA warp's turn
     B_RAW = B_TURN + 2,                         // per slot: an item's last V tile loaded, to be cleaned
     B_ITEM = B_RAW + SLOTS,                     // per queue entry: written
     B_TAKEN = B_ITEM + QUEUE,                   // ... read by every role
@@ -430,13 +430,23 @@ __global__ void __launch_bounds__(THREADS, 1)
             __syncwarp();
             if (lane == 0) mbar_arrive(bar(B_FULL + s));
         };
-        // the output tiles of an item, in the order in which they are staged
+        // The output tiles of an item, in the order in which they are staged.
+        // Both row tiles write one staging tile; this warp gives it to them, a
+        // tile at a time, once the copy of the one before has read it.  A row
+        // tile's next grant comes behind its last one's tile, so it waits for
+        // every phase of its barrier in turn and can miss none.  (Waiting for
+        // the other's copies instead, of which it need not see every one, a row
+        // tile took an older phase for the one it meant.)
         int sends[2] = {0, 0};
+        auto grant = [&](int i) {
+            if (lane == 0) mbar_arrive(bar(B_STAGE + i));
+        };
         auto send = [&](int4 e) {
             const Item it(e, P);
 #pragma unroll
             for (int i = 0; i < 2; ++i) {
                 if (!ok || !it.whole(i, P.NP)) continue;
+                if (i == 1) grant(1);
                 ok = __all_sync(0xffffffffu, mbar_wait(bar(B_STAGED + i), sends[i] & 1));
                 ++sends[i];
                 if (lane == 0 && ok) {
@@ -445,7 +455,6 @@ __global__ void __launch_bounds__(THREADS, 1)
                                      it.t0 + it.p0 + i * P.NP);
                     bulk_commit();
                     bulk_wait_read();
-                    mbar_arrive(bar(B_SENT + i));
                 }
                 __syncwarp();
             }
@@ -481,6 +490,7 @@ __global__ void __launch_bounds__(THREADS, 1)
                 put_item(e);
                 if (ok && before.y) clean(before);
                 if (ok && before.y) send(before);
+                if (ok && Item(e, P).whole(0, P.NP)) grant(0);
                 before = e;
             }
             const bool got = mbar_wait(bar(B_NEXT), k & 1);
@@ -500,18 +510,10 @@ __global__ void __launch_bounds__(THREADS, 1)
         // position of this row and of the warp's first and last within a tile
         const int dpos = min(r, rows - 1) / P.G, head = min(r, rows - 1) % P.G;
         const int dfirst = min(wq * 32, rows - 1) / P.G, dlast = min(wq * 32 + 31, rows - 1) / P.G;
-        int s_use = 0, o_use = 0;
-        int sends[2] = {0, 0};                              // staged tiles so far, this item's among them
-        bool last_was_1 = false, before_was_1;              // the last one (before this item) was of row tile 1
+        int s_use = 0, o_use = 0, staged = 0;
         int4 e;
         while (next_item(e)) {
             const Item it(e, P);
-            before_was_1 = last_was_1;
-            if (it.whole(0, P.NP)) {
-                ++sends[0];
-                last_was_1 = it.whole(1, P.NP);
-                if (last_was_1) ++sends[1];
-            }
             if (i >= it.tiles) continue;
             const int tile0 = it.p0 + i * P.NP, pos = tile0 + dpos;
             const int lo_r = P.window_left >= 0 ? max(0, pos - P.window_left) : 0;
@@ -651,17 +653,13 @@ __global__ void __launch_bounds__(THREADS, 1)
             // 3), so that the next item's first key tiles do not wait behind
             // stores (3100 of an item's 17000 cycles, 16384 tokens, 512-key
             // window).  The two row tiles share the staging tile, in order:
-            // each waits until the copy before its own has read it.  A
-            // sequence's last tile, with rows behind its end, is stored row by
-            // row.
+            // warp 3 gives it to each once the copy before its own has read it.
+            // A sequence's last tile, with rows behind its end, is stored row
+            // by row.
             if (it.whole(i, P.NP)) {
-                if (i == 1)
-                    ok = mbar_wait(bar(B_SENT), (sends[0] - 1) & 1);
-                else if (sends[0] > 1)
-                    ok = before_was_1 ? mbar_wait(bar(B_SENT + 1), (sends[1] - (it.whole(1, P.NP) ? 2 : 1)) & 1)
-                                      : mbar_wait(bar(B_SENT), sends[0] & 1);
-                ok = __all_sync(0xffffffffu, ok);
+                ok = __all_sync(0xffffffffu, mbar_wait(bar(B_STAGE + i), staged & 1));
                 if (!ok) break;
+                ++staged;
 #pragma unroll
                 for (int c = 0; c < 16; ++c)
                     *(uint4*)(stage + (c >> 3) * HALF + r * 128 + (((c ^ r) & 7) << 4)) =
