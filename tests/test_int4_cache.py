@@ -604,3 +604,32 @@ def test_calls_on_several_streams_at_once():
         assert torch.equal(call.out, want)
         assert torch.equal(got[0], rows[0]) and torch.equal(got[1], rows[1])
     assert fp8kv.fp8kv_device_status(clear=True) == 0
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("ps", [32, 64])
+def test_tiles_of_bad_pages_between_good_ones(ps):
+    """Whole key tiles, single pages and runs of them outside the pool, each slot
+    of the staging ring used several times with either, called again and again:
+    zeros where a page is bad, over what the slot held before and before what it
+    holds next."""
+    L, M = 40 * 128, 12
+    lay, q, kc, vc, ks, vs, k, v, slots = _case(ps, [L], M, 9, 1, ps, extra=3)
+    fp8kv.fp8kv_cache_insert(k * 8, v * 8, slots, ks, vs, kc, vc)
+    per = 128 // ps
+    rng = np.random.default_rng(ps)
+    bad = np.repeat(rng.integers(0, 3, 40) == 0, per)           # a third of the tiles, whole
+    bad |= rng.integers(0, 8, 40 * per) == 0                    # and pages anywhere
+    bad[-per:] = False
+    outside = torch.from_numpy(np.where(rng.integers(0, 2, len(bad)), -1 - rng.integers(0, 9, len(bad)),
+                                        lay.num_pages + rng.integers(0, 9, len(bad))).astype(np.int32))
+    lay.block_table[0, :len(bad)] = torch.where(torch.from_numpy(bad), outside, lay.block_table[0, :len(bad)])
+    out = _attend(lay, q, kc, vc, ks, vs, split_tokens=L)
+    assert "attention_int4_tc" in fp8kv.fp8kv_last_dispatch() and "splits=1 " in fp8kv.fp8kv_last_dispatch()
+    bt = lay.block_table
+    zero = gen.PagedLayout(ps, lay.num_pages + 1, torch.where((bt < 0) | (bt >= lay.num_pages), lay.num_pages, bt),
+                           lay.seq_lens)
+    pad = [torch.cat([c, torch.zeros_like(c[:1])]) for c in (kc, vc)]
+    _check(out, zero, q, pad[0], pad[1], ks, vs, ps)
+    for _ in range(30):
+        assert torch.equal(_attend(lay, q, kc, vc, ks, vs, split_tokens=L), out)

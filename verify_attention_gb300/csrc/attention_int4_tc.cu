@@ -503,11 +503,15 @@ __global__ void __launch_bounds__(THREADS, 1) attention_int4_tc_kernel(AttnParam
                 if (!__all_sync(0xffffffffu, ok)) break;
                 uint8_t* dst = stg + s * STAGE_BYTES + off;
                 const bool valid = mine && page >= 0 && page < P.num_pages;
-                if (mine && !valid)
+                if (mine && !valid) {
                     for (uint32_t i = 0; i < bytes; i += 16) *(uint4*)(dst + i) = make_uint4(0, 0, 0, 0);
+                    fence_proxy_async();                        // before a later tile's copy over them
+                }
                 uint32_t total = valid ? bytes : 0;
 #pragma unroll
                 for (int o = 16; o >= 1; o >>= 1) total += __shfl_xor_sync(0xffffffffu, total, o);
+                __syncwarp();                                   // every lane's zeros, before the arrival (the shuffles
+                                                                // order no memory)
                 if (lane == 0) mbar_expect_tx(bar(B_STG_FULL + s), total);
                 __syncwarp();
                 if (valid)
