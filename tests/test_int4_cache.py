@@ -633,3 +633,69 @@ def test_tiles_of_bad_pages_between_good_ones(ps):
     _check(out, zero, q, pad[0], pad[1], ks, vs, ps)
     for _ in range(30):
         assert torch.equal(_attend(lay, q, kc, vc, ks, vs, split_tokens=L), out)
+
+
+# ---------------------------------- GPU: every way of combining partitions
+
+def _check_route(out, text, lay, q, kc, vc, ks, vs, ps, window=-1):
+    """_check with the rounding of the partitions' partial outputs taken from the
+    route that the call reports, in place of the row count; NaN where the
+    definition has it, and nowhere else."""
+    ref, mag, lmag, vsum = int4_np.paged_attention(q.double().cpu().numpy(), kc.cpu().numpy(), vc.cpu().numpy(), ps,
+                                                   lay.block_table.numpy(), lay.seq_lens.numpy(), ks.item(), vs.item(),
+                                                   SM, window)
+    got = out.double().cpu().numpy()
+    assert np.array_equal(np.isnan(got), np.isnan(ref))
+    # The terms of _check, and: partials through the reduce kernel, and those of
+    # the tcgen05 kernel's clusters, are f16 of the partition's mean of n s: off
+    # by 2^-11 of it, which the partitions' weights (their sum is 1) turn into
+    # 2^-11 of mag at most, or below f16's normal range by 2^-25, v_scale times
+    # that in the output.  Clusters of the decode kernel exchange fp32.
+    f16 = "reduce=1" in text or ("int4_tc" in text and "cluster=1 " not in text)
+    tol = (2.0 ** -8 * np.abs(ref) + (2.0 ** -10 + f16 * 2.0 ** -11) * mag + 2.0 ** -20 * lmag + 2.0 ** -36 * vsum
+           + f16 * 2.0 ** -25 * vs.item())
+    ok = np.isnan(ref) | (np.abs(got - ref) <= tol)
+    assert ok.all(), float(np.nanmax(np.abs(got - ref) / tol))
+
+
+ROUTES = [
+    # lens, M, split_tokens, what the call reports (G = 9, H = 2, pages of 32)
+    ([257], 1, 512, "splits=1 "), ([257], 12, 512, "splits=1 "),
+    ([257], 1, 128, "cluster=3 "), ([257], 12, 128, "cluster=3 "),
+    ([1025], 1, 128, "reduce=1"), ([1025], 12, 128, "reduce=1"),           # 9 partitions: the reduce kernel's short form
+    ([2561], 1, 128, "reduce=1"), ([2561], 12, 128, "reduce=1"),           # 21: its long one
+    ([2561, 130, 1665, 13], 2, 128, "reduce=1"), ([2561, 130, 1665, 13], 12, 128, "reduce=1"),
+]
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("lens,M,split,route", ROUTES)
+def test_every_route_against_the_definition(lens, M, split, route):
+    lay, q, kc, vc, ks, vs, k, v, slots = _case(5 * sum(lens) + M, lens, M, 9, 2, 32)
+    v[::3] *= 2.0 ** -12                                        # small values beside large ones
+    fp8kv.fp8kv_cache_insert(k, v, slots, ks, vs, kc, vc)
+    out = _attend(lay, q, kc, vc, ks, vs, split_tokens=split)
+    text = fp8kv.fp8kv_last_dispatch()
+    assert route in text and ("int4_tc" in text) == (M * 9 > 16)
+    _check_route(out, text, lay, q, kc, vc, ks, vs, 32)
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("where", ["last", "partition", "first"])
+@pytest.mark.parametrize("lens,M,split,route", ROUTES)
+def test_a_nan_key_is_seen_however_the_keys_are_cut(lens, M, split, route, where):
+    """The newest token alone in the last partition, a whole partition, or the
+    oldest token, with a NaN in K of head 0: the rows that see it are NaN, the
+    others (earlier rows, the other head) as they were."""
+    lay, q, kc, vc, ks, vs, k, v, slots = _case(9 * sum(lens) + M, lens, M, 9, 2, 32)
+    at = 0
+    for n in lens:
+        lo, hi = {"last": (n - 1, n), "partition": (128, min(256, n)), "first": (0, 1)}[where]
+        k[at + lo:at + hi, 0, 77] = float("nan")
+        at += n
+    fp8kv.fp8kv_cache_insert(k, v, slots, ks, vs, kc, vc)
+    out = _attend(lay, q, kc, vc, ks, vs, split_tokens=split)
+    text = fp8kv.fp8kv_last_dispatch()
+    assert route in text
+    assert bool(out[0, -1, 0].isnan().all()) and not bool(out[..., 9:, :].isnan().any())
+    _check_route(out, text, lay, q, kc, vc, ks, vs, 32)

@@ -450,6 +450,14 @@ __global__ void __launch_bounds__(WARPS * 32, 12 / WARPS) paged_attention_int4_k
                 acc.z += wt * v4.z;
                 acc.w += wt * v4.w;
             }
+        } else {
+            // no key with a number for a score: no visible key at all (l = 0), or
+            // NaN scores only, which the maximum passes over but the sum holds.
+            // Those must not look like no key where partitions are combined:
+            // they go on with the maximum 0 (a NaN key as the last partition's
+            // only one would otherwise leave a finite output)
+            for (int w = 0; w < nw; ++w) l += merge[(w * 16 + r) * MERGE_STRIDE + 129];
+            if (l != l) mstar = 0.f;
         }
         const int m = (R0 + r) / P.G, hq = hk * P.G + (R0 + r) % P.G;
         const int64_t row_idx = ((int64_t)b * P.M + m) * P.Hq + hq;
