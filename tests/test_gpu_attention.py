@@ -538,3 +538,28 @@ def test_cfg5_serving_mix_full_size(layer):
     for (b, hk), r in ref.items():
         assert_close(o[b, :, hk * 9:(hk + 1) * 9, :], r, f"layer {layer} sequence {b} (L={lens[b]}) KV head {hk}")
     assert len(ref) == 8 * 8 + 56
+
+
+@pytest.mark.parametrize("dt", ["e4m3", "bf16"])
+@pytest.mark.parametrize("M,L,split", [(1, 257, 512), (1, 257, 128), (1, 2561, 128), (12, 257, 128), (12, 2561, 128)])
+def test_a_nan_key_is_seen_however_the_keys_are_cut(dt, M, L, split):
+    """The newest token, alone in the last partition or not, with a NaN in K of
+    head 0: the row that sees it is NaN, and no other."""
+    f = fp8kv()
+    g = gen.generator(L + M)
+    lay = gen.paged_layout([L], 32, g)
+    q = torch.randn((1, M, 18, 128), generator=g).to(torch.bfloat16).cuda()
+    k, v = (torch.randn((L, 2, 128), generator=g).to(torch.bfloat16).cuda() for _ in range(2))
+    s = torch.tensor([0.01], device="cuda")
+    kc, vc = (torch.zeros((lay.num_pages, 2, 32, 128), device="cuda",
+                          dtype=torch.uint8 if dt == "e4m3" else torch.bfloat16) for _ in range(2))
+    slots = lay.slots(0, range(L)).cuda()
+    call = (q, kc, vc, lay.block_table.cuda(), lay.seq_lens.cuda(), L, s, s, 128 ** -0.5)
+    f.fp8kv_cache_insert(k, v, slots, s, s, kc, vc)
+    want = f.fp8kv_paged_attention(*call, split_tokens=split)
+    assert not bool(want.isnan().any())
+    k[-1, 0, 77] = float("nan")
+    f.fp8kv_cache_insert(k, v, slots, s, s, kc, vc)
+    out = f.fp8kv_paged_attention(*call, split_tokens=split)
+    assert bool(out[0, -1, :9].isnan().all())
+    assert torch.equal(out[0, -1, 9:], want[0, -1, 9:]) and torch.equal(out[0, :-1], want[0, :-1])

@@ -549,6 +549,12 @@ __device__ __forceinline__ void attention_body(const CUtensorMap& tm_k, const CU
                 acc.z += w * v4.z;
                 acc.w += w * v4.w;
             }
+        } else {
+            // no visible key (l = 0), or NaN scores only, which the maximum
+            // passes over: with the maximum 0 their NaN sum still counts where
+            // partitions are combined
+            for (int k2 = 0; k2 < P.KW; ++k2) l += mergef[((int64_t)k2 * rows_pad + r) * kRowStride + 129];
+            if (l != l) mstar = 0.f;
         }
         const int m = r / P.G, hq = hk * P.G + r % P.G;
         const int64_t row_idx = ((int64_t)b * P.M + m) * P.Hq + hq;
