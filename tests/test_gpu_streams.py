@@ -1,0 +1,104 @@
+"""What a call on another stream allocates for itself: the memory is that
+stream's, not work's still queued on the current one."""
+import pytest
+import torch
+
+from verify_attention_gb300 import build, fp8kv, inputs as gen
+
+pytestmark = pytest.mark.gpu
+SM = 128 ** -0.5
+BUSY = 200_000_000          # cycles, about 0.1 s: longer than the host needs for all that follows
+
+
+@pytest.fixture(scope="module", autouse=True)
+def _lib():
+    build.build()
+
+
+def _tensors(cache, M, lens=(1500, 700), H=4, G=9, ps=32):
+    g = gen.generator(sum(lens) + M)
+    lay = gen.paged_layout(list(lens), ps, g)
+    B = len(lens)
+    q = torch.randn((B, M, G * H, 128), generator=g).to(torch.bfloat16).cuda()
+    k, v = (torch.randn((sum(lens), H, 128), generator=g).to(torch.bfloat16).cuda() for _ in range(2))
+    slots = torch.cat([lay.slots(b, range(n)) for b, n in enumerate(lens)]).cuda()
+    s = torch.tensor([0.01], device="cuda")
+    if cache == "int4":
+        kc, vc = (fp8kv.fp8kv_int4_cache(lay.num_pages, H, ps) for _ in range(2))
+    else:
+        kc, vc = (torch.zeros((lay.num_pages, H, ps, 128), dtype=torch.uint8, device="cuda") for _ in range(2))
+    fp8kv.fp8kv_cache_insert(k, v, slots, s, s, kc, vc)
+    call = dict(q=q, k_cache=kc, v_cache=vc, block_table=lay.block_table.cuda(), seq_lens=lay.seq_lens.cuda(),
+                max_seq_len=max(lens), k_scale=s, v_scale=s, sm_scale=SM)
+    return call, (k, v, slots, s)
+
+
+def _calls():
+    """name -> (shape, bytes of one output, call(stream) -> outputs)"""
+    out = {}
+    for cache in ("int4", "e4m3"):
+        for M in (1, 12):
+            c, (k, v, slots, s) = _tensors(cache, M)
+            out[f"{cache} M={M}"] = lambda st, c=c: (fp8kv.fp8kv_paged_attention(**c, stream=st),)
+            new = [x[:2 * M].view(2, M, 4, 128).contiguous() for x in (k, v)]
+            d = {**c, "k_cache": c["k_cache"].clone(), "v_cache": c["v_cache"].clone()}
+            out[f"append {cache} M={M}"] = (
+                lambda st, d=d, new=new: (fp8kv.fp8kv_append_paged_attention(*new, **d, stream=st),))
+            if M == 1:
+                out[f"gather {cache}"] = lambda st, c=c, slots=slots, s=s: fp8kv.fp8kv_cache_gather(
+                    slots, s, s, c["k_cache"], c["v_cache"], stream=st)
+                keep = torch.empty_like(k)
+                out[f"gather {cache}, k_out given"] = lambda st, c=c, slots=slots, s=s, keep=keep: fp8kv.fp8kv_cache_gather(
+                    slots, s, s, c["k_cache"], c["v_cache"], k_out=keep, stream=st)[1:]
+            if cache == "e4m3":
+                e = {**c, "k_scale": s.repeat(4), "v_scale": s.repeat(4)}
+                out[f"per head M={M}"] = lambda st, e=e: (fp8kv.fp8kv_paged_attention_per_head(**e, stream=st),)
+    g = gen.generator(9)
+    q, k, v = (torch.randn((900, h, 128), generator=g).to(torch.bfloat16).cuda() for h in (18, 2, 2))
+    cu = torch.tensor([0, 500, 900], dtype=torch.int32, device="cuda")
+    out["prompt"] = lambda st: (fp8kv.fp8kv_prompt_attention(q, k, v, cu, 500, SM, stream=st),)
+    return out
+
+
+NAMES = [f"{a}{c} M={m}" for a in ("", "append ") for c in ("int4", "e4m3") for m in (1, 12)] + [
+    f"gather {c}{x}" for c in ("int4", "e4m3") for x in ("", ", k_out given")] + ["per head M=1", "per head M=12", "prompt"]
+
+
+@pytest.fixture(scope="module")
+def calls():
+    return _calls()
+
+
+@pytest.mark.parametrize("name", NAMES)
+def test_an_output_takes_no_memory_that_queued_work_still_writes(calls, name):
+    """Blocks of the output's size, written by work queued on the current stream
+    and dropped, while the call runs at once on a side stream."""
+    call = calls[name]
+    want = [o.clone() for o in call(None)]
+    sizes = [o.untyped_storage().nbytes() for o in call(None)]
+    side = torch.cuda.Stream()
+    torch.cuda.synchronize()
+    torch.cuda.empty_cache()
+    torch.cuda._sleep(BUSY)
+    for n in sizes:
+        torch.empty(n, dtype=torch.uint8, device="cuda").fill_(7)       # queued behind the sleep, then free again
+    got = call(side)
+    side.synchronize()
+    torch.cuda.synchronize()
+    for a, b in zip(want, got):
+        assert torch.equal(a, b)
+
+
+@pytest.mark.parametrize("name", NAMES)
+def test_a_dropped_output_is_not_handed_out_while_the_call_runs(calls, name):
+    call = calls[name]
+    sizes = [o.untyped_storage().nbytes() for o in call(None)]
+    side = torch.cuda.Stream()
+    torch.cuda.synchronize()
+    torch.cuda.empty_cache()
+    with torch.cuda.stream(side):
+        torch.cuda._sleep(BUSY)
+    call(side)                                                          # its outputs are dropped here
+    others = [torch.full((n,), 7, dtype=torch.uint8, device="cuda") for n in sizes]
+    torch.cuda.synchronize()
+    assert all(bool((o == 7).all()) for o in others)

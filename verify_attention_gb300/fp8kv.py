@@ -108,18 +108,27 @@ def _stream(stream, t=None) -> int:
 
 
 def _at(stream):
-    """What is allocated or filled for a call on `stream` belongs there: filled on
-    the current stream it might be filled after the call, and a workspace of the
-    current stream's pool might be handed out again before the call ends."""
+    """What is allocated and filled for a call on `stream` belongs there, as under
+    torch.cuda.stream(stream): filled on the current stream it might be filled
+    after the call; memory of the current stream's pool might still be in use by
+    work queued there, and might be handed out again before the call ends.  (An
+    output allocated here and used on another stream is the caller's to order
+    and to record_stream, as with any tensor of torch's.)"""
     if stream is None:
         return contextlib.nullcontext()
     return torch.cuda.stream(stream if hasattr(stream, "cuda_stream") else torch.cuda.ExternalStream(int(stream)))
 
 
 def _zeros(shape, device, stream):
-    t = torch.empty(shape, dtype=torch.bfloat16, device=device)
     with _at(stream):
-        return t.zero_()
+        return torch.empty(shape, dtype=torch.bfloat16, device=device).zero_()
+
+
+def _empty_like(t, stream):
+    if stream is None:
+        return torch.empty_like(t)
+    with _at(stream):
+        return torch.empty_like(t)
 
 
 def _workspace(need, device, stream):
@@ -349,7 +358,7 @@ def fp8kv_paged_attention(q, k_cache, v_cache, block_table, seq_lens, max_seq_le
     if workspace is None:
         workspace = _workspace(need, q.device, stream)
     if out is None:
-        out = torch.empty_like(q)
+        out = _empty_like(q, stream)
     rc = lib().fp8kv_paged_attention(
         _ptr(q), _ptr(k_cache), _ptr(v_cache), dt, _ptr(block_table), block_table.shape[1],
         _ptr(seq_lens), int(max_seq_len), B, M, Hq, Hkv, D, page_size, int(num_pages), _ptr(k_scale),
@@ -381,7 +390,7 @@ def fp8kv_append_paged_attention(k_new, v_new, q, k_cache, v_cache, block_table,
     if workspace is None:
         workspace = _workspace(need, q.device, stream)
     if out is None:
-        out = torch.empty_like(q)
+        out = _empty_like(q, stream)
     rc = lib().fp8kv_append_paged_attention(
         _ptr(k_new), _ptr(v_new), _ptr(q), _ptr(k_cache), _ptr(v_cache), dt, _ptr(block_table),
         block_table.shape[1], _ptr(seq_lens), int(max_seq_len), B, M, Hq, Hkv, D, page_size, int(num_pages),
@@ -415,7 +424,7 @@ def fp8kv_paged_attention_per_head(q, k_cache, v_cache, block_table, seq_lens, m
     if workspace is None:
         workspace = _workspace(need, q.device, stream)
     if out is None:
-        out = torch.empty_like(q)
+        out = _empty_like(q, stream)
     args = (_ptr(q), _ptr(k_cache), _ptr(v_cache), _ptr(block_table), block_table.shape[1], _ptr(seq_lens),
             int(max_seq_len), B, M, Hq, Hkv, D, page_size, int(num_pages), _ptr(k_scale), _ptr(v_scale),
             float(sm_scale), int(window_left), int(split_tokens), _ptr(workspace),
