@@ -102,3 +102,55 @@ def test_a_dropped_output_is_not_handed_out_while_the_call_runs(calls, name):
     others = [torch.full((n,), 7, dtype=torch.uint8, device="cuda") for n in sizes]
     torch.cuda.synchronize()
     assert all(bool((o == 7).all()) for o in others)
+
+
+@pytest.mark.parametrize("raw", [False, True])
+@pytest.mark.parametrize("cache,M", [("int4", 1), ("int4", 12), ("e4m3", 12)])
+def test_prepared_call_on_another_stream_than_it_was_made_on(cache, M, raw):
+    """Its own output and workspace were allocated from a block that work queued
+    before still writes."""
+    c, _ = _tensors(cache, M)
+    want = fp8kv.fp8kv_paged_attention(**c, split_tokens=256).clone()
+    n = want.untyped_storage().nbytes()
+    need = fp8kv.fp8kv_paged_attention_workspace_size(2, M, 36, 4, 128, 32, 1500, -1, 256)
+    assert need > 0
+    side = torch.cuda.Stream()
+    torch.cuda.synchronize()
+    torch.cuda.empty_cache()
+    torch.cuda._sleep(BUSY)
+    blocks = [torch.empty(b, dtype=torch.uint8, device="cuda").fill_(7) for b in (n, need)]
+    del blocks
+    call = fp8kv.PreparedAttention(**c, split_tokens=256)
+    got = call(side.cuda_stream if raw else side)
+    side.synchronize()
+    torch.cuda.synchronize()
+    assert torch.equal(got, want)
+
+
+def test_prepared_call_dropped_while_it_runs_on_another_stream():
+    c, _ = _tensors("int4", 12)
+    call = fp8kv.PreparedAttention(**c, split_tokens=256)
+    sizes = [call.out.untyped_storage().nbytes(), call._keep[7].numel()]
+    side = torch.cuda.Stream()
+    torch.cuda.synchronize()
+    with torch.cuda.stream(side):
+        torch.cuda._sleep(BUSY)
+        call()
+    del call
+    others = [torch.full((n,), 7, dtype=torch.uint8, device="cuda") for n in sizes]
+    torch.cuda.synchronize()
+    assert all(bool((o == 7).all()) for o in others)
+
+
+def test_prepared_call_captured_on_another_stream():
+    c, _ = _tensors("int4", 1)
+    want = fp8kv.fp8kv_paged_attention(**c).clone()
+    call = fp8kv.PreparedAttention(**c)
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph, stream=torch.cuda.Stream()):
+        call()
+    call.out.zero_()
+    graph.replay()
+    torch.cuda.synchronize()
+    assert torch.equal(call.out, want)
+    assert torch.equal(call(), want)

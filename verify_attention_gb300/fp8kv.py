@@ -448,12 +448,50 @@ def fp8kv_append_paged_attention_per_head(k_new, v_new, q, k_cache, v_cache, blo
                                           v_new, stream)
 
 
+class _Owned:
+    """The tensors that a prepared call allocated for itself, on the stream that
+    was current then.  Another stream is ordered behind that allocation before
+    the first call on it, and the tensors are recorded on it, so that dropping
+    them while it still runs does not hand their memory out."""
+
+    def __init__(self, tensors):
+        self.tensors = tensors
+        self.handles, self.ready = None, None
+        if self.tensors:
+            device = self.tensors[0].get_device()
+            self.handles = {torch._C._cuda_getCurrentRawStream(device)}
+            with torch.cuda.device(device):
+                if not torch.cuda.is_current_stream_capturing():
+                    self.ready = torch.cuda.Event()
+                    self.ready.record()
+
+    def before_call(self, stream, handle):
+        if self.handles is None or handle in self.handles:
+            return
+        raw = stream is not None and not hasattr(stream, "cuda_stream")
+        s = torch.cuda.ExternalStream(handle) if raw else torch.cuda.current_stream() if stream is None else stream
+        with torch.cuda.stream(s):
+            if torch.cuda.is_current_stream_capturing():
+                # (torch.cuda.graph waits for the device before it captures; an
+                # event of work outside cannot be waited for inside)
+                return
+        if self.ready is not None:
+            s.wait_event(self.ready)
+        if not raw:
+            # a raw handle's stream may be destroyed before the tensors are freed
+            for t in self.tensors:
+                t.record_stream(s)
+        self.handles.add(handle)
+
+
 class PreparedAttention:
     """fp8kv_append_paged_attention (k_new, v_new given) or
     fp8kv_paged_attention over fixed tensors, marshalled once: each call
     passes the prepared arguments and the stream, nothing else.  For serving
     loops whose caches, metadata and buffers stay at fixed addresses; the
-    tensors must outlive the object."""
+    tensors must outlive the object, and the object its calls on a raw stream
+    handle and the graphs that captured it.  Calls share the workspace and the
+    output: on several streams they need one object each."""
 
     def __init__(self, q, k_cache, v_cache, block_table, seq_lens, max_seq_len, k_scale, v_scale, sm_scale,
                  window_left=-1, split_tokens=0, workspace=None, out=None, k_new=None, v_new=None, num_pages=None):
@@ -473,12 +511,16 @@ class PreparedAttention:
                     raise ValueError(f"{n} must be [B][M][Hkv][D]")
         need = fp8kv_paged_attention_workspace_size(B, M, Hq, Hkv, D, page_size, max_seq_len, window_left,
                                                     split_tokens)
+        own = []
         if workspace is None and need:
             workspace = torch.empty(need, dtype=torch.uint8, device=q.device)
+            own.append(workspace)
         if out is None:
             out = torch.empty_like(q)
+            own.append(out)
         if out.shape != q.shape:
             raise ValueError("out must have the shape of q")
+        self._own = _Owned(own)
         self.out, self._keep = out, (q, k_cache, v_cache, block_table, seq_lens, k_scale, v_scale, workspace, k_new,
                                      v_new)
         args = (_ptr(q), _ptr(k_cache), _ptr(v_cache), dt, _ptr(block_table), block_table.shape[1], _ptr(seq_lens),
@@ -493,7 +535,9 @@ class PreparedAttention:
             self._args = args
 
     def __call__(self, stream=None):
-        rc = self._fn(*self._args, _stream(stream, self.out))
+        handle = _stream(stream, self.out)
+        self._own.before_call(stream, handle)
+        rc = self._fn(*self._args, handle)
         if rc:
             raise Fp8kvError(self._name, rc)
         return self.out
