@@ -154,3 +154,30 @@ def test_prepared_call_captured_on_another_stream():
     torch.cuda.synchronize()
     assert torch.equal(call.out, want)
     assert torch.equal(call(), want)
+
+
+@pytest.mark.parametrize("raw", [False, True])
+def test_layers_call_on_another_stream_than_it_was_made_on(raw):
+    """The counters of its workspace are zero before the call, whatever was in
+    the block and whatever the current stream still has to do."""
+    layers = []
+    for window in (-1, 511, -1):
+        c, (k, v, _, _) = _tensors("e4m3", 12)
+        new = [x[:24].view(2, 12, 4, 128).contiguous() for x in (k, v)]
+        layers.append({**c, "window_left": window, "k_new": new[0], "v_new": new[1], "out": torch.empty_like(c["q"])})
+    n = fp8kv.fp8kv_paged_attention_layers(layers).ws_bytes
+    torch.cuda.synchronize()
+    want = [d["out"].clone() for d in layers]
+    for d in layers:
+        d["out"].fill_(3.0)
+    fp8kv.fp8kv_device_status(clear=True)
+    side = torch.cuda.Stream()
+    torch.cuda.synchronize()
+    torch.cuda.empty_cache()
+    torch.cuda._sleep(BUSY)
+    torch.empty(n, dtype=torch.uint8, device="cuda").fill_(7)
+    fp8kv.fp8kv_paged_attention_layers(layers, stream=side.cuda_stream if raw else side)
+    side.synchronize()
+    torch.cuda.synchronize()
+    assert fp8kv.fp8kv_device_status(clear=True) == 0
+    assert all(torch.equal(d["out"], w) for d, w in zip(layers, want))

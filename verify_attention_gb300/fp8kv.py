@@ -627,16 +627,21 @@ class PagedAttentionLayers:
         self.layers = arr
         self.n = len(layers)
         self.ws_bytes = fp8kv_paged_attention_layers_workspace_size(self.n, B, M, Hq, Hkv)
+        own = []
         if workspace is None:
-            # the counters at its start must be zero before the first call
+            # the counters at its start must be zero before the first call, on
+            # whatever stream that is
             workspace = torch.zeros(self.ws_bytes, dtype=torch.uint8, device=q0.device)
+            own.append(workspace)
+        self._own = _Owned(own)
         self.workspace = workspace
 
     def __call__(self, stream=None):
         B, M, Hq, Hkv, D, page_size = self.shape
+        handle = _stream(stream)
+        self._own.before_call(stream, handle)
         rc = lib().fp8kv_paged_attention_layers(ctypes.byref(self.layers), self.n, B, M, Hq, Hkv, D, page_size,
-                                                FP8KV_CACHE_E4M3, _ptr(self.workspace), self.workspace.numel(),
-                                                _stream(stream))
+                                                FP8KV_CACHE_E4M3, _ptr(self.workspace), self.workspace.numel(), handle)
         _check("fp8kv_paged_attention_layers", rc)
 
 
