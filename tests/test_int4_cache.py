@@ -699,3 +699,18 @@ def test_a_nan_key_is_seen_however_the_keys_are_cut(lens, M, split, route, where
     assert route in text
     assert bool(out[0, -1, 0].isnan().all()) and not bool(out[..., 9:, :].isnan().any())
     _check_route(out, text, lay, q, kc, vc, ks, vs, 32)
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("cache", ["e4m3", "int4"])
+def test_gather_refuses_scales_per_head(cache):
+    """It reads caches with one scale per tensor: a scale for each head would be
+    read as its first head's."""
+    kc, vc = (fp8kv.fp8kv_int4_cache(2, 4, 32) if cache == "int4" else
+              torch.zeros((2, 4, 32, 128), dtype=torch.uint8, device="cuda") for _ in range(2))
+    slots = torch.arange(10, device="cuda")
+    one, heads = _scale(0.5), torch.full((4,), 0.5, device="cuda")
+    fp8kv.fp8kv_cache_gather(slots, one, one, kc, vc)
+    for ks, vs in ((heads, one), (one, heads), (heads, heads), (one, one[:0])):
+        with pytest.raises(ValueError):
+            fp8kv.fp8kv_cache_gather(slots, ks, vs, kc, vc)

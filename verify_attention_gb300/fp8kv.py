@@ -234,7 +234,7 @@ def fp8kv_cache_gather(slot_mapping, k_scale, v_scale, k_cache, v_cache, k_out=N
     num_pages, Hkv, page_size = _cache_shape(k_cache, v_cache, dt)
     T, D = slot_mapping.numel(), 128 if dt == FP8KV_CACHE_INT4 else k_cache.shape[3]
     if dt != FP8KV_CACHE_BF16:
-        _dev(k_scale, "k_scale", torch.float32), _dev(v_scale, "v_scale", torch.float32)
+        _one_scale(k_scale, v_scale)
     if k_out is None and v_out is None:
         k_out, v_out = _zeros((2, T, Hkv, D), k_cache.device, stream).unbind(0)     # one fill instead of two
     k_out = _zeros((T, Hkv, D), k_cache.device, stream) if k_out is None else _dev(k_out, "k_out", torch.bfloat16)
