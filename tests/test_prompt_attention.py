@@ -362,3 +362,21 @@ def test_output_tiles_of_items_with_one_whole_row_tile(G, H, window):
         fp8kv.fp8kv_prompt_attention(q, k, v, cu, max(lens), SM, window_left=window, out=out)
         assert torch.equal(out, want)
     assert fp8kv.fp8kv_device_status(clear=True) == 0
+
+
+class _On:
+    def __init__(self, device):
+        self.device = device
+
+    def get_device(self):
+        return self.device
+
+
+@pytest.mark.parametrize("stream", [0, 1 << 20, type("S", (), {"cuda_stream": 1 << 20})()])
+def test_a_given_stream_does_not_hide_another_device(monkeypatch, stream):
+    """The kernels run on the current device: tensors of another one are refused
+    whether the stream is given or not."""
+    monkeypatch.setattr(torch.cuda, "current_device", lambda: 0)
+    assert fp8kv._stream(stream, _On(0)) == getattr(stream, "cuda_stream", stream)
+    with pytest.raises(ValueError, match="current device"):
+        fp8kv._stream(stream, _On(1))

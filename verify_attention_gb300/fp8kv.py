@@ -98,12 +98,13 @@ def _ptr(t: Optional[torch.Tensor]) -> int:
 
 def _stream(stream, t=None) -> int:
     """The stream's handle; `t`, one of the call's tensors, must be on the current device."""
-    if stream is None:
-        # the handle of the current stream without a Stream object (0.3 us instead of 3)
+    if stream is None or t is not None:
         device = torch.cuda.current_device()
         if t is not None and t.get_device() != device:
             raise ValueError(f"tensors on cuda:{t.get_device()}, but the current device is cuda:{device}")
-        return torch._C._cuda_getCurrentRawStream(device)
+        if stream is None:
+            # the handle of the current stream without a Stream object (0.3 us instead of 3)
+            return torch._C._cuda_getCurrentRawStream(device)
     return stream.cuda_stream if hasattr(stream, "cuda_stream") else int(stream)
 
 
