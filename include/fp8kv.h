@@ -71,8 +71,11 @@ typedef enum {
  * 16 integers n, every step rounded to fp32:
  *     r = amax|x| / (7 c)         s = max(e4m3_rne_satfinite(r), 2^-9)
  *     inv = 1 / (s c)             n = clamp(rint(x inv), -7, 7)   (ties to even)
- * and stands for n s c: off by at most half a step s c / 2 (and 2^-20 of it),
- * unless it saturates at 7 * 448 c.  A NaN in the block makes s NaN (0x7F) and
+ * and stands for n s c: off by at most half a step s c / 2 where s >= 7 * 2^-9,
+ * unless it saturates at 7 * 448 c.  Smaller scales are subnormal, and rounding
+ * one down (by up to 2^-10) clamps the block's largest elements: they are off by
+ * up to 7 * 2^-10 c (3.5 steps at s = 2^-9).  (Both bounds and 2^-18 of a step,
+ * for the fp32 roundings.)  A NaN in the block makes s NaN (0x7F) and
  * n = 0: the whole block reads as NaN.  Infinities saturate.
  * k_cache, v_cache: [num_pages][Hkv][page_size * 72] bytes; the bytes of one
  * (page, head) are page_size rows of 64 code bytes (byte i: element 2i in the

@@ -714,3 +714,34 @@ def test_gather_refuses_scales_per_head(cache):
     for ks, vs in ((heads, one), (one, heads), (heads, heads), (one, one[:0])):
         with pytest.raises(ValueError):
             fp8kv.fp8kv_cache_gather(slots, ks, vs, kc, vc)
+
+
+@pytest.mark.parametrize("c", [1.0, 0.0123, 37.0, 2.0 ** -100, 2.0 ** 100])
+def test_error_of_a_stored_value_over_all_block_scales(c):
+    """Blocks whose largest element is anything from far below the smallest block
+    scale to the largest: constant ones just below every border between two
+    scales, where the rounding of s costs most, and random ones."""
+    c32 = float(np.float32(c))
+    s = int4_np.e4m3_value(np.arange(127))[1:]                  # 2^-9 .. 448
+    border = (s[:-1] + s[1:]) / 2
+    rng = np.random.default_rng(11)
+    amax = np.concatenate([7 * c32 * border * 0.999, 7 * c32 * border * 1.001, 7 * c32 * s,
+                           7 * c32 * 2.0 ** rng.uniform(-14, np.log2(448), 2000)])
+    x = amax[:, None] * np.where(np.arange(16) % 2, rng.uniform(-1, 1, (len(amax), 16)), 1.0)
+    # bf16 rounded towards zero: above 448 * 7 c the value would saturate
+    bits = np.asarray(x, np.float32).view(np.uint32) & np.uint32(0xffff0000)
+    x = bits.view(np.float32).reshape(-1, 1, 16).repeat(8, 1).reshape(-1, 1, 128)
+    n, sc = int4_np.encode_rows(x, c)
+    assert sc.min() == 1 and sc.max() == 0x7e
+    step = np.repeat(int4_np.e4m3_value(sc), 16, -1) * c32
+    err = np.abs(x.astype(np.float64) - n * step)
+    # r = amax / (7 c).  s rounded down: r - s <= 2^-10 where s is subnormal (and
+    # s >= 2^-9 > r - 2^-10 below), 2^-4 s where it is normal, so clamping at 7 s c
+    # costs at most 7 * 2^-10 c or 7/16 of a step; rounding n costs half a step.
+    # r, s c and the reciprocal are fp32, each off by at most 2^-23 of itself, and
+    # r is at most 1.5 s: 7 * 1.5 * 3 * 2^-23 < 2^-18 of a step.
+    bound = np.where(step >= 7 * 2.0 ** -9 * c32, step / 2, np.maximum(step / 2, 7 * 2.0 ** -10 * c32))
+    assert np.all(err <= bound + 2.0 ** -18 * step)
+    # the second bound is needed: at s = 2^-9 more than three steps are reached
+    low = np.repeat(sc, 16, -1) == 1
+    assert err[low].max() > 3.3 * 2.0 ** -9 * c32
