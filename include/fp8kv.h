@@ -103,7 +103,8 @@ typedef enum {
  * (infinities included), NaN -> 0x7F with the input's sign, -0 -> 0x80.
  *     INT4:  the row's codes and block scales as described above.
  * Slots < 0 are skipped; slots not named are left untouched.  Duplicate
- * non-negative slots race (unspecified which token wins).
+ * non-negative slots race: such a row may hold parts of each of its tokens, and
+ * over an INT4 cache the codes of one under a block scale of another.
  *
  *   k, v          (device) bf16 [T][Hkv][D]
  *   slot_mapping  (device) int64 [T]
@@ -296,6 +297,9 @@ size_t fp8kv_paged_attention_workspace_size(int B, int M, int Hq, int Hkv, int D
  * in 128-row tiles (Hkv * ceil(M * Hq/Hkv / 128) <= 65535); other shapes
  * return FP8KV_ERR_UNSUPPORTED (over an INT4 cache B > 65535 too).  B = 0
  * launches nothing and returns FP8KV_OK without reading any pointer.
+ * A NaN in a K row reaches the rows that see it.  A NaN (BF16 cache: or an
+ * infinity) in a V row may reach, beyond those, the other rows of its KV head and
+ * sequence (0 * NaN), and nothing else.
  * Device checks: seq_len < M, seq_len > max_seq_len or more pages than
  * max_pages_per_seq -> that sequence's output is left untouched
  * (FP8KV_DEV_BAD_SEQ_LEN); page ids outside [0, num_pages) read zeros.

@@ -745,3 +745,17 @@ def test_error_of_a_stored_value_over_all_block_scales(c):
     # the second bound is needed: at s = 2^-9 more than three steps are reached
     low = np.repeat(sc, 16, -1) == 1
     assert err[low].max() > 3.3 * 2.0 ** -9 * c32
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("M,split", [(1, 0), (1, 128), (12, 0), (12, 128)])
+def test_a_nan_value_stays_with_its_head_and_sequence(M, split):
+    lay, q, kc, vc, ks, vs, k, v, slots = _case(71, [300, 257], M, 9, 2, 32)
+    fp8kv.fp8kv_cache_insert(k, v, slots, ks, vs, kc, vc)
+    want = _attend(lay, q, kc, vc, ks, vs, split_tokens=split)
+    v[-1, 1, 5] = float("nan")                                  # the newest token of the second sequence
+    fp8kv.fp8kv_cache_insert(k, v, slots, ks, vs, kc, vc)
+    out = _attend(lay, q, kc, vc, ks, vs, split_tokens=split)
+    assert torch.equal(out[0], want[0]) and torch.equal(out[1, :, :9], want[1, :, :9])
+    # the whole block of 16 elements of the row that sees it
+    assert bool(out[1, -1, 9:, :16].isnan().all()) and not bool(out[1, :, 9:, 16:].isnan().any())
