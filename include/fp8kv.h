@@ -295,8 +295,8 @@ size_t fp8kv_paged_attention_workspace_size(int B, int M, int Hq, int Hkv, int D
  * whole 128-key tiles (split_tokens 0 or a multiple of 128): a prefill chunk
  * at the end of the context, causal within the chunk, on the tcgen05 kernel
  * in 128-row tiles (Hkv * ceil(M * Hq/Hkv / 128) <= 65535); other shapes
- * return FP8KV_ERR_UNSUPPORTED (over an INT4 cache B > 65535 too).  B = 0
- * launches nothing and returns FP8KV_OK without reading any pointer.
+ * return FP8KV_ERR_UNSUPPORTED, as do B > 65535 and Hkv > 65535.  B = 0 launches
+ * nothing and returns FP8KV_OK without reading any pointer.
  * A NaN in a K row reaches the rows that see it.  A NaN (BF16 cache: or an
  * infinity) in a V row may reach, beyond those, the other rows of its KV head and
  * sequence (0 * NaN), and nothing else.

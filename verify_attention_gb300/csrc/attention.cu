@@ -594,8 +594,9 @@ __global__ void __maxnreg__(kDecodeRegs) paged_decode_kernel(
 // log-sum-exp.  Partials of the mma.sync kernels (F16 = false) are fp32
 // unnormalised O_p * v_scale with (m_p, l_p):
 //     O = sum_p 2^(m_p - m*) O_p / sum_p 2^(m_p - m*) l_p;
-// those of the tensor-memory kernel (F16 = true) are f16 O_p / l_p in E4M3
-// code units: O = v_scale * sum_p w_p O_p / sum_p w_p, w_p = 2^(m_p - m*) l_p.
+// those of the tensor-memory kernels and of the INT4 decode kernel (F16 = true)
+// are f16 O_p / l_p without v_scale (E4M3 code units; n s over an INT4 cache):
+// O = v_scale * sum_p w_p O_p / sum_p w_p, w_p = 2^(m_p - m*) l_p.
 // Longest-first order of the (sequence, partition) slots of a tcgen05 call
 // with one row tile of R rows (q = b * num_splits + s): slots ranked by
 // their number of 128-key tiles (in 63 classes of tiles_per_split), longest
@@ -1146,8 +1147,7 @@ static int attention_call(const void* k_new, const void* v_new, const void* q, c
     // which serves at most 16 rows per sequence and 144 per KV head
     const bool use_tc = fp8 && tc_rows(M, Hq, Hkv) && (plan.split_tokens % tc_tile_tokens()) == 0;
     if (!use_tc && tc_only(M, Hq, Hkv)) return FP8KV_ERR_UNSUPPORTED;
-    if (int4 && ((int64_t)Hkv * ceil_div((int64_t)M * (Hq / Hkv), 16) > 65535 || B > 65535))
-        return FP8KV_ERR_UNSUPPORTED;                           // grid
+    if (int4 && (int64_t)Hkv * ceil_div((int64_t)M * (Hq / Hkv), 16) > 65535) return FP8KV_ERR_UNSUPPORTED;   // grid
     if (B == 0) return FP8KV_OK;                                // nothing to do; no pointer is read
     if (!q || !k_cache || !v_cache || !block_table || !seq_lens || !out) return FP8KV_ERR_INVALID_ARG;
     if ((k_new != nullptr) != (v_new != nullptr) || (k_new && (!al16(k_new) || !al16(v_new))))

@@ -280,35 +280,32 @@ __global__ void __launch_bounds__(WARPS * 32, 12 / WARPS) paged_attention_int4_k
 
         // ---- S = Q K^T
         float sacc[4][4];
+        uint32_t kw[4][4];
+        Scale2 sc[4][2];
 #pragma unroll
-        for (int jj = 0; jj < 4; jj += 4) {
-            uint32_t kw[4][4];
-            Scale2 sc[4][2];
+        for (int j = 0; j < 4; ++j) {
+            const uint4 x = *(const uint4*)(st + (8 * j + g) * 64 + 16 * t);
+            kw[j][0] = x.x;
+            kw[j][1] = x.y;
+            kw[j][2] = x.z;
+            kw[j][3] = x.w;
+            const int key = 8 * j + 4 * (g & 1) + (g >> 1);
+            const uint32_t s2 = e4m3x2_to_f16x2(*(const uint16_t*)(st + OFF_KS + key * 8 + 2 * t));
+            sc[j][0] = scale2(prmt(s2, s2, 0x1010));
+            sc[j][1] = scale2(prmt(s2, s2, 0x3232));
+        }
+#pragma unroll
+        for (int w = 0; w < 4; ++w) {
+            uint32_t v[4][4];
+#pragma unroll
+            for (int j = 0; j < 4; ++j) widen4(kw[j][w], sc[j][w >> 1], v[j]);
 #pragma unroll
             for (int j = 0; j < 4; ++j) {
-                const uint4 x = *(const uint4*)(st + (8 * (jj + j) + g) * 64 + 16 * t);
-                kw[j][0] = x.x;
-                kw[j][1] = x.y;
-                kw[j][2] = x.z;
-                kw[j][3] = x.w;
-                const int key = 8 * (jj + j) + 4 * (g & 1) + (g >> 1);
-                const uint32_t s2 = e4m3x2_to_f16x2(*(const uint16_t*)(st + OFF_KS + key * 8 + 2 * t));
-                sc[j][0] = scale2(prmt(s2, s2, 0x1010));
-                sc[j][1] = scale2(prmt(s2, s2, 0x3232));
+                if (w == 0) mma_f16_zero(sacc[j], qa[0], v[j][0], v[j][1]);
+                else mma_f16(sacc[j], qa[2 * w], v[j][0], v[j][1]);
             }
 #pragma unroll
-            for (int w = 0; w < 4; ++w) {
-                uint32_t v[4][4];
-#pragma unroll
-                for (int j = 0; j < 4; ++j) widen4(kw[j][w], sc[j][w >> 1], v[j]);
-#pragma unroll
-                for (int j = 0; j < 4; ++j) {
-                    if (w == 0) mma_f16_zero(sacc[jj + j], qa[0], v[j][0], v[j][1]);
-                    else mma_f16(sacc[jj + j], qa[2 * w], v[j][0], v[j][1]);
-                }
-#pragma unroll
-                for (int j = 0; j < 4; ++j) mma_f16(sacc[jj + j], qa[2 * w + 1], v[j][2], v[j][3]);
-            }
+            for (int j = 0; j < 4; ++j) mma_f16(sacc[j], qa[2 * w + 1], v[j][2], v[j][3]);
         }
         // ---- masks, online softmax in log2 units (s mult)
         if ((k0 + CK - 1 > pmin) || (k0 < lomax)) {

@@ -16,8 +16,9 @@
 // Items.  The grid has one CTA per item; a resident CTA (one per SM) goes on
 // with the items of CTAs that have not started, which it cancels
 // (clusterlaunchcontrol), so that loads, set-up and output of one item overlap
-// the products of another, and the items are handed out longest first as SMs
-// come free, without a counter in memory.  Twelve warps:
+// the products of another, without a counter in memory.  Items are handed out
+// as SMs come free, the last sequence first and within a sequence from its end,
+// where the rows see the most keys.  Twelve warps:
 //   warp 0      loads by TMA: Q of each row tile once it is free, K and V tiles
 //               of 128 keys through a ring of four 32 KiB slots; allocates and
 //               frees the tensor memory
@@ -34,8 +35,8 @@
 // Online softmax in the log2 domain over halves of a key tile, whose P.V starts
 // while the other half is exponentiated; O is rescaled only when a row's
 // maximum grows by more than 2^8 (the weights stay below 2^8, sums are fp32).
-// P is rounded to bf16, V's type, as the MMA needs both alike: 2^-9 of each
-// weight, the size of the output's own rounding.
+// P is rounded to bf16, V's type, as the MMA needs both alike: at most 2^-8 of
+// each weight, the size of the output's own rounding.
 // TMEM columns: S/P of the two row tiles 0-127, 128-255 (P over the first half
 // of its S), O 256-383, 384-511.
 #include <stdio.h>
@@ -394,7 +395,7 @@ __global__ void __launch_bounds__(THREADS, 1)
         __syncwarp();
     } else if (warp == 3) {
         // ------------------------------------------------- schedule and clean
-        // Pair x (2 NP positions) of the launch, the last ones first: sequence
+        // Pair x (2 NP positions) of the launch, the last one first: sequence
         // b owns the indices from cu[b] / (2 NP) + b on, at least as many as it
         // has pairs, so the largest b whose first index is at most x is found
         // by a 32-way search, without a scan.
