@@ -89,6 +89,17 @@ typedef enum {
 #define FP8KV_DEV_BAD_POSITION  0x2u  /* position outside [0, max_pos)              */
 #define FP8KV_DEV_BAD_SEQ_LEN   0x4u  /* seq_len < M or beyond the block-table row  */
 #define FP8KV_DEV_WAIT_TIMEOUT  0x8u  /* a bounded pipeline wait gave up            */
+#define FP8KV_DEV_BAD_TREE      0x10u /* a tree's parent, token or path out of order */
+#define FP8KV_DEV_BAD_PROBS     0x20u /* a row of probabilities without a finite sum */
+
+/* Nodes of a tree of drafted tokens, at most (the bits of one mask word). */
+#define FP8KV_TREE_MAX_NODES 64
+
+/* Types of probabilities (fp8kv_verify_tree). */
+typedef enum {
+    FP8KV_PROBS_FP32 = 0,
+    FP8KV_PROBS_BF16 = 1
+} fp8kv_probs_dtype;
 
 /*
  * fp8kv_cache_insert -- write T new tokens into the paged K and V caches.
@@ -433,6 +444,152 @@ size_t fp8kv_paged_attention_layers_workspace_size(int n_layers, int B, int M, i
 int fp8kv_paged_attention_layers(const fp8kv_layer* layers, int n_layers, int B, int M, int Hq, int Hkv,
                                  int D, int page_size, int cache_dtype, void* workspace,
                                  size_t workspace_bytes, void* stream);
+
+/*
+ * Trees of drafted tokens.  The next five entry points are one step of
+ * speculative decoding over a tree (the pages verify a chain of 12 rows and leave
+ * the draft and the acceptance to the serving engine; a chain is the tree whose
+ * node m hangs from m - 1).  A tree has M nodes (M <= 64), the same M for every
+ * sequence of a batch: node 0 is the last accepted token, node m > 0 a drafted one
+ * behind node parents[m] < m.  A node whose parent is -1, or is padding itself, is
+ * padding (a sequence with fewer nodes).  The nodes' K and V rows are the last M of
+ * the cache: node m at index L - M + m of a sequence of L = seq_lens[b], whatever
+ * its depth; its position (what rotates it, and what a window counts) is
+ * L - M + depth.
+ *
+ * fp8kv_tree_metadata -- what the other calls of the step need from the parents:
+ *     tree_mask[b][m]    = bits of m and its ancestors (0 for padding)
+ *     positions[b][m]    = L - M + depth of m          (padding: L - M)
+ *     slot_mapping[b][m] = the cache slot of index L - M + m (padding: -1)
+ *
+ *   parents       (device) int32 [B][M]; parents[b][0] is not used
+ *   seq_lens      (device) int32 [B], the nodes included
+ *   block_table   (device) int32 [B][max_pages_per_seq]
+ *   max_seq_len   (host) >= every length
+ *   tree_mask     (device) uint64 [B][M];  positions, slot_mapping (device) int64 [B][M]
+ * B = 0 launches nothing and reads no pointer.
+ * Device checks: a parent outside [-1, m) -> padding, FP8KV_DEV_BAD_TREE; a length
+ * < M, > max_seq_len or beyond the block-table row -> mask 0, position 0, slot -1
+ * for the whole sequence, FP8KV_DEV_BAD_SEQ_LEN; a page outside [0, num_pages) ->
+ * slot -1, FP8KV_DEV_BAD_SLOT.
+ */
+int fp8kv_tree_metadata(const int32_t* parents, const int32_t* seq_lens, const int32_t* block_table,
+                        int max_pages_per_seq, int max_seq_len, int B, int M, int num_pages, int page_size,
+                        uint64_t* tree_mask, int64_t* positions, int64_t* slot_mapping, void* stream);
+
+/*
+ * fp8kv_rope_insert -- rotary positions on Q and K, then K and V into the cache:
+ * fp8kv_qk_norm_rope_insert without the norms, for every cache type, both layouts
+ * of the pairs and heads that rotate in part.  With pos = positions[t],
+ * c_k = cos_sin[pos][k], s_k = cos_sin[pos][rot_dim / 2 + k], for each Q and K head
+ * row x and k < rot_dim / 2, (i, j) = (k, k + rot_dim / 2), or (2 k, 2 k + 1) when
+ * interleaved:
+ *     o_i = bf16( fma(x_i, c_k, -(x_j * s_k)) )     o_j = bf16( fma(x_j, c_k, x_i * s_k) )
+ * in fp32; o = x for the elements behind rot_dim.  Q rows go to q_out, the rotated
+ * K rows and the V rows into the cache as in fp8kv_cache_insert.  Angles scaled for
+ * long contexts, and a factor on cosines and sines, are the table's.
+ *
+ *   q (device) bf16 [T][Hq][D], tokens q_stride elements apart; k, v bf16
+ *     [T][Hkv][D], k_stride and v_stride apart (views of one projection's output are
+ *     fine); strides >= heads * D and multiples of 8
+ *   positions (device) int64 [T];  cos_sin (device) fp32 [max_pos][rot_dim]
+ *   rot_dim (host) a multiple of 8, 8 .. D;  interleaved (host) 0 or not
+ *   q_out (device) bf16 [T][Hq][D], dense; must not overlap q, k or v
+ *   other arguments as fp8kv_cache_insert.
+ * Device checks: position outside [0, max_pos) -> token skipped entirely
+ * (FP8KV_DEV_BAD_POSITION); slot >= num_pages*page_size -> K/V of that token skipped
+ * (FP8KV_DEV_BAD_SLOT).  A negative slot skips the token's K/V, not its Q.
+ * T = 0 launches nothing and returns FP8KV_OK without reading any pointer.
+ */
+int fp8kv_rope_insert(const void* q, int64_t q_stride, const void* k, int64_t k_stride, const void* v,
+                      int64_t v_stride, const int64_t* positions, const float* cos_sin, int max_pos, int rot_dim,
+                      int interleaved, void* q_out, const int64_t* slot_mapping, int T, int Hq, int Hkv, int D,
+                      const float* k_scale, const float* v_scale, void* k_cache, void* v_cache, int num_pages,
+                      int page_size, int cache_dtype, void* stream);
+
+/*
+ * fp8kv_tree_attention -- fp8kv_paged_attention (k_new = v_new = NULL) or
+ * fp8kv_append_paged_attention for the M nodes of a tree: row m sees the L - M
+ * cached keys before the nodes and the nodes i whose bit is set in
+ * tree_mask[b][m] (an ancestor set with m itself, as fp8kv_tree_metadata writes
+ * it; bits >= M are ignored).  With window_left >= 0 row m, at position
+ * p_m = L - M + (bits in tree_mask[b][m]) - 1 (mask 0: L - M), sees of those the
+ * keys at positions >= p_m - window_left, node i being at position p_i.  A row without visible keys,
+ * and a row whose mask is 0 (padding), is written as zeros.  The mask of a chain
+ * gives fp8kv_paged_attention's result.
+ *
+ *   tree_mask  (device) uint64 [B][M]
+ *   split_tokens (host) 0, or a multiple of page_size; of 128 for more than 16 rows
+ *              M * Hq/Hkv per KV head
+ *   every other argument, the workspace and the device checks: as
+ *   fp8kv_append_paged_attention (per-tensor scales).
+ * Supported: D = 128, page_size 32 or 64, Hq % Hkv == 0, 1 <= M <= 64, every cache
+ * type.  With k_new, the rows of padding nodes are written too.
+ */
+int fp8kv_tree_attention(const void* k_new, const void* v_new, const void* q, void* k_cache, void* v_cache,
+                         int cache_dtype, const int32_t* block_table, int max_pages_per_seq, const int32_t* seq_lens,
+                         int max_seq_len, const uint64_t* tree_mask, int B, int M, int Hq, int Hkv, int D,
+                         int page_size, int num_pages, const float* k_scale, const float* v_scale, float sm_scale,
+                         int window_left, int split_tokens, void* workspace, size_t workspace_bytes, void* out,
+                         void* stream);
+
+/*
+ * fp8kv_verify_tree -- which drafted tokens stand, and the token after them.
+ * Row n of target_probs is the target's distribution p_n of the token behind node n,
+ * row n of draft_probs the distribution q_n that n's children were drawn from,
+ * independently (draft_probs = NULL: they were chosen, q_n is 1 at a child's
+ * token).  From node n = 0, with w = p_n and S = 1, n's children are taken in the
+ * order of their index; child m with token x stands when
+ *     w(x) > 0  and  uniforms[m] * S * q_n(x) < w(x)
+ * and the walk goes on at n = m; otherwise
+ *     w <- max(w - S q_n, 0), S <- sum of w     (NULL: S <- S - w(x), w(x) <- 0).
+ * When no child is left, the next token is the first v whose running sum of w
+ * exceeds uniforms[0] times the sum of w (of p_n, should nothing be left of it).
+ * With uniforms drawn from [0, 1) the tokens are distributed as the target alone
+ * would draw them.  A greedy target is one with rows of one 1.
+ *
+ *   target_probs, draft_probs (device) fp32 or bf16 (prob_dtype) [B][M][V], the rows
+ *     of consecutive nodes target_stride and draft_stride elements apart (>= V);
+ *     entries that are negative or NaN count as 0.  Rows of leaves of draft_probs
+ *     are not read.
+ *   tokens, parents (device) int32 [B][M] (tokens[b][0], parents[b][0] not used)
+ *   uniforms   (device) fp32 [B][M] in [0, 1)
+ *   out_tokens (device) int32 [B][M]: the tokens that stand, the next one, then -1
+ *   num_tokens (device) int32 [B]: how many those are, 1 .. M
+ *   path       (device) int32 [B][M]: node 0 and the nodes that stand, then -1
+ * Sums are held to 2^-45 of the weight they add (pairs of fp32).  Any V below 2^30;
+ * no workspace.  B = 0 launches nothing and reads no pointer.
+ * Device checks: a parent outside [-1, m), or a node's token outside [0, V) -> that
+ * node is padding, FP8KV_DEV_BAD_TREE; a row p_n without a positive, finite sum
+ * where the next token is drawn -> no next token (-1, not counted),
+ * FP8KV_DEV_BAD_PROBS.
+ */
+int fp8kv_verify_tree(const void* target_probs, int64_t target_stride, const void* draft_probs, int64_t draft_stride,
+                      int prob_dtype, const int32_t* tokens, const int32_t* parents, const float* uniforms, int B,
+                      int M, int V, int32_t* out_tokens, int32_t* num_tokens, int32_t* path, void* stream);
+
+/*
+ * fp8kv_cache_keep_path -- after the verification: in the caches of n_layers layers
+ * (one launch) the K and V rows of the nodes path[b][0 .. n) (the leading entries
+ * >= 0) go to indices L - M .. L - M + n - 1, as if all were read before any is
+ * written, and new_seq_lens[b] = L - M + n.  What was behind them stays.  The next
+ * token is not in the cache: with the next tree it is node 0.
+ *
+ *   k_caches, v_caches (host) arrays of n_layers (1 .. 64) device pointers, each a
+ *     cache of its own, all of the same cache_dtype, num_pages and Hkv
+ *   block_table, seq_lens (device) as fp8kv_paged_attention, the same for all layers
+ *   path         (device) int32 [B][M], as fp8kv_verify_tree writes it
+ *   new_seq_lens (device) int32 [B]; must not overlap the other arguments
+ * B = 0 launches nothing and reads no pointer.
+ * Device checks: a path that does not begin with 0, ascend below M and end in -1s ->
+ * that sequence keeps its rows and its length, FP8KV_DEV_BAD_TREE; a bad length
+ * likewise, FP8KV_DEV_BAD_SEQ_LEN; a page outside [0, num_pages) -> the rows from
+ * and to it are not moved, FP8KV_DEV_BAD_SLOT.
+ */
+int fp8kv_cache_keep_path(void* const* k_caches, void* const* v_caches, int n_layers, int cache_dtype,
+                          const int32_t* block_table, int max_pages_per_seq, const int32_t* seq_lens, int max_seq_len,
+                          const int32_t* path, int B, int M, int Hkv, int D, int num_pages, int page_size,
+                          int32_t* new_seq_lens, void* stream);
 
 /*
  * fp8kv_paged_attention_noalloc -- fp8kv_paged_attention without a

@@ -77,7 +77,8 @@ __device__ __forceinline__ RowPos row_pos(int r, int R, int G, int L, int M, int
 // Smem byte offset of 16-byte chunk `ch` of row `row` in a 128-byte-swizzled tile.
 __device__ __forceinline__ uint32_t swz(int row, int ch) { return row * 128 + (((ch ^ row) & 7) << 4); }
 
-template <int PS, bool FP8>
+// TREE: what a row sees among the last M keys is given by its mask word.
+template <int PS, bool FP8, bool TREE>
 __device__ __forceinline__ void attention_body(const CUtensorMap& tm_k, const CUtensorMap& tm_v,
                                                const AttnParams& P) {
     using C = Cfg<PS, FP8>;
@@ -244,8 +245,18 @@ __device__ __forceinline__ void attention_body(const CUtensorMap& tm_k, const CU
     const int rt = warp % P.NT, kg = warp / P.NT;
     const int g = lane >> 2, c = lane & 3;
     const int r0 = rt * 16 + g, r1 = r0 + 8;
-    const RowPos rp0 = row_pos(r0, P.R, P.G, L, P.M, P.window_left);
-    const RowPos rp1 = row_pos(r1, P.R, P.G, L, P.M, P.window_left);
+    RowPos rp0 = row_pos(r0, P.R, P.G, L, P.M, P.window_left);
+    RowPos rp1 = row_pos(r1, P.R, P.G, L, P.M, P.window_left);
+    const int base = L - P.M;
+    TreeRow tr0, tr1;
+    if (TREE) {
+        const int m0 = min(r0, P.R - 1) / P.G, m1 = min(r1, P.R - 1) / P.G;
+        tr0 = tree_row(P, b, m0, tree_word(P, b, m0), base);
+        tr1 = tree_row(P, b, m1, tree_word(P, b, m1), base);
+        // (the bounds below: every key before the nodes needs no mask)
+        rp0 = {base - 1, tr0.lo};
+        rp1 = {base - 1, tr1.lo};
+    }
 
     // Q fragments (A operand, 8 k-steps).  k-slot -> head-dim mapping:
     //   FP8 : k-step ks of thread c covers dims 32c + 4ks + {0,1 | 2,3}
@@ -381,7 +392,8 @@ __device__ __forceinline__ void attention_body(const CUtensorMap& tm_k, const CU
                     if (need_mask) {
                         const int key = kfirst + 8 * nt + 2 * c + (e & 1);
                         const RowPos& rp = (e >> 1) ? rp1 : rp0;
-                        if (key > rp.p || key < rp.lo) t = -INFINITY;
+                        if (TREE ? !tree_sees((e >> 1) ? tr1 : tr0, key, base) : key > rp.p || key < rp.lo)
+                            t = -INFINITY;
                     }
                     sacc[nt][e] = t;
                 }
@@ -560,8 +572,9 @@ __device__ __forceinline__ void attention_body(const CUtensorMap& tm_k, const CU
         const int64_t row_idx = ((int64_t)b * P.M + m) * P.Hq + hq;
         if (nsplit_b == 1) {
             const float f = vs / l;
-            *(uint2*)(P.out + row_idx * 128 + d4) =
-                make_uint2(pack_bf16x2(acc.x * f, acc.y * f), pack_bf16x2(acc.z * f, acc.w * f));
+            uint2 o2 = make_uint2(pack_bf16x2(acc.x * f, acc.y * f), pack_bf16x2(acc.z * f, acc.w * f));
+            if (TREE && (l == 0.f || tree_word(P, b, m) == 0)) o2 = make_uint2(0u, 0u);
+            *(uint2*)(P.out + row_idx * 128 + d4) = o2;
         } else {
             float* wo = P.ws_o + (row_idx * P.num_splits + split) * 128 + d4;
             *(float4*)wo = make_float4(acc.x * vs, acc.y * vs, acc.z * vs, acc.w * vs);
@@ -578,16 +591,16 @@ __device__ __forceinline__ void attention_body(const CUtensorMap& tm_k, const CU
 template <int PS, bool FP8>
 __global__ void __launch_bounds__(32 * (kMaxRowTiles + 1), 1) paged_attention_kernel(
     const __grid_constant__ CUtensorMap tm_k, const __grid_constant__ CUtensorMap tm_v, AttnParams P) {
-    attention_body<PS, FP8>(tm_k, tm_v, P);
+    attention_body<PS, FP8, false>(tm_k, tm_v, P);
 }
 
 // One row tile (decode): a handful of key-group warps, each with two or more
 // stages in flight, one CTA per SM; at most two warps per SM sub-partition,
 // so the register cap can be high enough to keep every fragment resident.
-template <int PS, bool FP8>
+template <int PS, bool FP8, bool TREE>
 __global__ void __maxnreg__(kDecodeRegs) paged_decode_kernel(
     const __grid_constant__ CUtensorMap tm_k, const __grid_constant__ CUtensorMap tm_v, AttnParams P) {
-    attention_body<PS, FP8>(tm_k, tm_v, P);
+    attention_body<PS, FP8, TREE>(tm_k, tm_v, P);
 }
 
 // One warp per output row (b, m, h): combine the partitions through their
@@ -661,14 +674,17 @@ __global__ void __launch_bounds__(512) lpt_order_kernel(const int32_t* __restric
     }
 }
 
-template <bool F16>
+// TREE: every row tile spans the keys from the window of the first node to the
+// end; a row that saw nothing, and a padding row, becomes zeros.
+template <bool F16, bool TREE>
 __global__ void __launch_bounds__(256) attn_reduce_kernel(const float* __restrict__ ws_o,
                                                           const float* __restrict__ ws_ml,
                                                           const int32_t* __restrict__ seq_lens, int B, int M,
                                                           int Hq, int G, int tile_rows, int mpps,
                                                           int page_size, int window_left, int split_pages,
                                                           int num_splits, int max_seq_len, const float* v_scale,
-                                                          int scale_stride, uint16_t* out) {
+                                                          int scale_stride, uint16_t* out,
+                                                          const uint64_t* __restrict__ tree) {
     pdl_launch_dependents();
     pdl_wait();
     const int64_t row = ((int64_t)blockIdx.x * blockDim.x + threadIdx.x) >> 5;
@@ -681,8 +697,9 @@ __global__ void __launch_bounds__(256) attn_reduce_kernel(const float* __restric
     // KV head), split into partitions exactly as the attention kernel did
     const int m = (int)(row / Hq % M), rk = m * G + (int)(row % Hq) % G;
     const int R0 = rk / tile_rows * tile_rows, RL = min(tile_rows, M * G - R0);
-    const int lo0 = (window_left >= 0) ? max(0, L - M + R0 / G - window_left) : 0;
-    const int first_page = lo0 / page_size, last_page = (L - M + (R0 + RL - 1) / G) / page_size;
+    const int lo0 = (window_left >= 0) ? max(0, L - M + (TREE ? 0 : R0 / G) - window_left) : 0;
+    const int first_page = lo0 / page_size, last_page = (TREE ? L - 1 : L - M + (R0 + RL - 1) / G) / page_size;
+    const bool padding = TREE && (tree[(int64_t)b * M + m] & (~0ull >> (64 - M))) == 0;
     const int ns = (last_page - first_page + split_pages) / split_pages;
     if (ns <= 1 || ns > num_splits) return;
     const float* ml = ws_ml + row * num_splits * 2;
@@ -744,8 +761,9 @@ __global__ void __launch_bounds__(256) attn_reduce_kernel(const float* __restric
 #pragma unroll
         for (int off = 16; off >= 1; off >>= 1) den += __shfl_xor_sync(0xffffffffu, den, off);
         const float f = vs / den;
-        *(uint2*)(out + row * 128 + lane * 4) =
-            make_uint2(pack_bf16x2(acc.x * f, acc.y * f), pack_bf16x2(acc.z * f, acc.w * f));
+        uint2 o2 = make_uint2(pack_bf16x2(acc.x * f, acc.y * f), pack_bf16x2(acc.z * f, acc.w * f));
+        if (TREE && (padding || den == 0.f)) o2 = make_uint2(0u, 0u);
+        *(uint2*)(out + row * 128 + lane * 4) = o2;
         return;
     }
     if (ns <= 16) {
@@ -810,8 +828,9 @@ __global__ void __launch_bounds__(256) attn_reduce_kernel(const float* __restric
 #pragma unroll
     for (int off = 16; off >= 1; off >>= 1) den += __shfl_xor_sync(0xffffffffu, den, off);
     const float f = 1.0f / den;
-    *(uint2*)(out + row * 128 + lane * 4) =
-        make_uint2(pack_bf16x2(acc.x * f, acc.y * f), pack_bf16x2(acc.z * f, acc.w * f));
+    uint2 o2 = make_uint2(pack_bf16x2(acc.x * f, acc.y * f), pack_bf16x2(acc.z * f, acc.w * f));
+    if (TREE && (padding || den == 0.f)) o2 = make_uint2(0u, 0u);
+    *(uint2*)(out + row * 128 + lane * 4) = o2;
 }
 
 }  // namespace fp8kv
@@ -1096,7 +1115,9 @@ template <int PS, bool FP8>
 static int launch(const CUtensorMap& tk, const CUtensorMap& tv, const AttnParams& P, cudaStream_t s) {
     using C = Cfg<PS, FP8>;
     const bool decode = P.NT == 1;
-    auto kern = decode ? paged_decode_kernel<PS, FP8> : paged_attention_kernel<PS, FP8>;
+    auto kern = !decode   ? paged_attention_kernel<PS, FP8>
+                : P.tree ? paged_decode_kernel<PS, FP8, true>
+                         : paged_decode_kernel<PS, FP8, false>;
     const int max_stages = decode ? kDecodeStageBudget / C::kStageBytes : C::kStages;
     if (ensure_smem((const void*)kern, C::smem_bytes(std::max(max_stages, P.KW * P.SG)))) return FP8KV_ERR_CUDA;
     dim3 grid(P.num_splits, P.Hkv, P.B);
@@ -1135,7 +1156,7 @@ static int attention_call(const void* k_new, const void* v_new, const void* q, c
                           const int32_t* seq_lens, int max_seq_len, int B, int M, int Hq, int Hkv, int D,
                           int page_size, int num_pages, const float* k_scale, const float* v_scale, int scale_stride,
                           float sm_scale, int window_left, int split_tokens, void* workspace, size_t workspace_bytes,
-                          void* out, void* stream) {
+                          void* out, void* stream, bool tree = false, const uint64_t* tree_mask = nullptr) {
     if (cache_dtype != FP8KV_CACHE_E4M3 && cache_dtype != FP8KV_CACHE_BF16 && cache_dtype != FP8KV_CACHE_INT4)
         return FP8KV_ERR_INVALID_ARG;
     const bool fp8 = cache_dtype == FP8KV_CACHE_E4M3, int4 = cache_dtype == FP8KV_CACHE_INT4;
@@ -1146,10 +1167,17 @@ static int attention_call(const void* k_new, const void* v_new, const void* q, c
     // 128-key tiles: tcgen05 kernel (128-row MMA tiles); otherwise mma.sync,
     // which serves at most 16 rows per sequence and 144 per KV head
     const bool use_tc = fp8 && tc_rows(M, Hq, Hkv) && (plan.split_tokens % tc_tile_tokens()) == 0;
-    if (!use_tc && tc_only(M, Hq, Hkv)) return FP8KV_ERR_UNSUPPORTED;
+    if (tree) {
+        // more than 16 rows per KV head: a tcgen05 kernel for every cache type
+        if (M > FP8KV_TREE_MAX_NODES || (tc_rows(M, Hq, Hkv) && plan.split_tokens % tc_tile_tokens()))
+            return FP8KV_ERR_UNSUPPORTED;
+    } else if (!use_tc && tc_only(M, Hq, Hkv)) {
+        return FP8KV_ERR_UNSUPPORTED;
+    }
     if (int4 && (int64_t)Hkv * ceil_div((int64_t)M * (Hq / Hkv), 16) > 65535) return FP8KV_ERR_UNSUPPORTED;   // grid
     if (B == 0) return FP8KV_OK;                                // nothing to do; no pointer is read
-    if (!q || !k_cache || !v_cache || !block_table || !seq_lens || !out) return FP8KV_ERR_INVALID_ARG;
+    if (!q || !k_cache || !v_cache || !block_table || !seq_lens || !out || (tree && !tree_mask))
+        return FP8KV_ERR_INVALID_ARG;
     if ((k_new != nullptr) != (v_new != nullptr) || (k_new && (!al16(k_new) || !al16(v_new))))
         return FP8KV_ERR_INVALID_ARG;
     if ((fp8 || int4) && (!k_scale || !v_scale)) return FP8KV_ERR_INVALID_ARG;
@@ -1210,6 +1238,7 @@ static int attention_call(const void* k_new, const void* v_new, const void* q, c
     P.num_splits = plan.num_splits;
     P.page_size = page_size;
     P.max_seq_len = max_seq_len;
+    P.tree = tree_mask;
 
     cudaStream_t s = (cudaStream_t)stream;
     if (int4) {
@@ -1223,7 +1252,9 @@ static int attention_call(const void* k_new, const void* v_new, const void* q, c
         // of 9 rows)
         const bool tc = tc_rows(M, Hq, Hkv) && plan.split_tokens % tc_tile_tokens() == 0;
         const bool one_tile = (tc ? row_tiles(M, Hq, Hkv) : P.NT) == 1;
-        if (k_new && one_tile) {                                // appended in the kernel
+        // appended in the kernel (the tcgen05 kernel's 256 widening threads take a
+        // block of 16 elements each)
+        if (k_new && one_tile && (!tc || M <= 32)) {
             P.k_new = (const uint16_t*)k_new;
             P.v_new = (const uint16_t*)v_new;
         } else if (k_new) {
@@ -1255,11 +1286,11 @@ static int attention_call(const void* k_new, const void* v_new, const void* q, c
         if (rc) return rc;
         if (cut.num_splits > 1 && !cut.cluster) {
             const int64_t warps = (int64_t)B * M * Hq;
-            cudaError_t e = launch_pdl(attn_reduce_kernel<true>, dim3((unsigned)((warps + 7) / 8)), dim3(256), 0, s,
-                                       (const float*)P.ws_o,
+            cudaError_t e = launch_pdl(tree ? attn_reduce_kernel<true, true> : attn_reduce_kernel<true, false>,
+                                       dim3((unsigned)((warps + 7) / 8)), dim3(256), 0, s, (const float*)P.ws_o,
                                        (const float*)P.ws_ml, seq_lens, B, M, Hq, P.G, tc ? 128 : P.R,
                                        max_pages_per_seq, page_size, window_left, cut.split_pages, cut.num_splits,
-                                       max_seq_len, v_scale, scale_stride, (uint16_t*)out);
+                                       max_seq_len, v_scale, scale_stride, (uint16_t*)out, tree_mask);
             if (e != cudaSuccess) {
                 cudaGetLastError();
                 return FP8KV_ERR_CUDA;
@@ -1268,11 +1299,12 @@ static int attention_call(const void* k_new, const void* v_new, const void* q, c
         set_dispatch(text);
         return FP8KV_OK;
     }
-    const int RT = use_tc ? row_tiles(M, Hq, Hkv) : 1;
+    const bool bf16_tc = tree && !fp8 && tc_rows(M, Hq, Hkv);
+    const int RT = use_tc || bf16_tc ? row_tiles(M, Hq, Hkv) : 1;
     // one sequence in at most 8 partitions and one row tile: the partitions
     // of a KV head run as one thread-block cluster and combine in distributed
     // shared memory
-    P.cluster = (use_tc && B == 1 && RT == 1 && plan.num_splits > 1 && plan.num_splits <= 8) ? plan.num_splits : 0;
+    P.cluster = ((use_tc || bf16_tc) && B == 1 && RT == 1 && plan.num_splits > 1 && plan.num_splits <= 8) ? plan.num_splits : 0;
     // several sequences split into partitions of unequal length: longest first
     const bool lpt = use_tc && B > 1 && RT == 1 && plan.num_splits > 1;
     if (lpt)
@@ -1298,8 +1330,11 @@ static int attention_call(const void* k_new, const void* v_new, const void* q, c
             return FP8KV_ERR_CUDA;
         }
     }
+    char buf[256];
     if (use_tc)
         rc = launch_attention_tc(tk, tv, P, s);
+    else if (bf16_tc)
+        rc = launch_attention_bf16_tc(tk, tv, P, s, buf, sizeof buf);
     else if (page_size == 32)
         rc = fp8 ? launch<32, true>(tk, tv, P, s) : launch<32, false>(tk, tv, P, s);
     else
@@ -1307,17 +1342,18 @@ static int attention_call(const void* k_new, const void* v_new, const void* q, c
     if (rc) return rc;
     if (plan.num_splits > 1 && P.cluster <= 1) {
         const int64_t warps = (int64_t)B * M * Hq;
-        cudaError_t e = launch_pdl(use_tc ? attn_reduce_kernel<true> : attn_reduce_kernel<false>,
-                                   dim3((unsigned)((warps + 7) / 8)), dim3(256), 0, s, (const float*)P.ws_o,
-                                   (const float*)P.ws_ml, seq_lens, B, M, Hq, P.G, use_tc ? 128 : P.R,
-                                   max_pages_per_seq, page_size, window_left, plan.split_pages, plan.num_splits,
-                                   max_seq_len, k_scale ? v_scale : nullptr, scale_stride, (uint16_t*)out);
+        cudaError_t e =
+            launch_pdl(use_tc ? (tree ? attn_reduce_kernel<true, true> : attn_reduce_kernel<true, false>)
+                              : (tree ? attn_reduce_kernel<false, true> : attn_reduce_kernel<false, false>),
+                       dim3((unsigned)((warps + 7) / 8)), dim3(256), 0, s, (const float*)P.ws_o,
+                       (const float*)P.ws_ml, seq_lens, B, M, Hq, P.G, use_tc || bf16_tc ? 128 : P.R,
+                       max_pages_per_seq, page_size, window_left, plan.split_pages, plan.num_splits, max_seq_len,
+                       k_scale ? v_scale : nullptr, scale_stride, (uint16_t*)out, tree_mask);
         if (e != cudaSuccess) {
             cudaGetLastError();
             return FP8KV_ERR_CUDA;
         }
     }
-    char buf[256];
     if (use_tc)
         snprintf(buf, sizeof buf,
                  "attention_tc<ps=%d,e4m3> rows=%d row_tiles=%d tile=128x128 splits=%d split_tokens=%d "
@@ -1325,7 +1361,7 @@ static int attention_call(const void* k_new, const void* v_new, const void* q, c
                  page_size, P.R, RT, plan.num_splits, plan.split_tokens, plan.num_splits, Hkv * RT, B, tc_threads(),
                  P.cluster > 1 ? P.cluster : 1, (plan.num_splits > 1 && P.cluster <= 1) ? 1 : 0,
                  lpt ? "longest_first" : "grid");
-    else
+    else if (!bf16_tc)
         snprintf(buf, sizeof buf,
                  "%s<ps=%d,%s> rows=%d row_tiles=%d key_groups=%d stages_per_group=%d splits=%d "
                  "split_tokens=%d grid=%dx%dx%d threads=%d reduce=%d",
@@ -1384,6 +1420,17 @@ extern "C" int fp8kv_append_paged_attention_per_head(const void* k_new, const vo
     return attention_call(k_new, v_new, q, k_cache, v_cache, FP8KV_CACHE_E4M3, block_table, max_pages_per_seq,
                           seq_lens, max_seq_len, B, M, Hq, Hkv, D, page_size, num_pages, k_scale, v_scale, 1,
                           sm_scale, window_left, split_tokens, workspace, workspace_bytes, out, stream);
+}
+
+extern "C" int fp8kv_tree_attention(const void* k_new, const void* v_new, const void* q, void* k_cache, void* v_cache,
+                                    int cache_dtype, const int32_t* block_table, int max_pages_per_seq,
+                                    const int32_t* seq_lens, int max_seq_len, const uint64_t* tree_mask, int B, int M,
+                                    int Hq, int Hkv, int D, int page_size, int num_pages, const float* k_scale,
+                                    const float* v_scale, float sm_scale, int window_left, int split_tokens,
+                                    void* workspace, size_t workspace_bytes, void* out, void* stream) {
+    return attention_call(k_new, v_new, q, k_cache, v_cache, cache_dtype, block_table, max_pages_per_seq, seq_lens,
+                          max_seq_len, B, M, Hq, Hkv, D, page_size, num_pages, k_scale, v_scale, 0, sm_scale,
+                          window_left, split_tokens, workspace, workspace_bytes, out, stream, true, tree_mask);
 }
 
 // ================================================ allocation-free variant

@@ -39,7 +39,48 @@ struct AttnParams {
     uint8_t* k_cache;
     uint8_t* v_cache;
     int num_pages;
+    // tree calls (kernels with TREE): the nodes that each row sees, [B][M] words
+    const uint64_t* tree;
 };
+
+// What row m of sequence b of a tree call sees: node i where bit i is set, and
+// the keys lo .. L - M - 1 before the nodes.  A node's position is L - M + its
+// depth, the number of its ancestors, and a window counts positions.  `base` is L - M.
+struct TreeRow {
+    uint64_t nodes;
+    int lo;
+    bool padding;               // mask 0: the row's output is zeros
+};
+__device__ __forceinline__ uint64_t tree_word(const AttnParams& P, int b, int m) {
+    return P.tree[(int64_t)b * P.M + m] & (~0ull >> (64 - P.M));
+}
+__device__ __forceinline__ TreeRow tree_row(const AttnParams& P, int b, int m, uint64_t word, int base) {
+    TreeRow t = {word, 0, word == 0};
+    if (P.window_left >= 0) {
+        const int depth = max(__popcll(word) - 1, 0);
+        t.lo = max(0, base + depth - P.window_left);
+        // (nodes are less than 64 positions apart)
+        if (P.window_left < depth)
+            for (uint64_t w = word; w; w &= w - 1) {
+                const int i = __ffsll(w) - 1;
+                if (max(__popcll(tree_word(P, b, i)) - 1, 0) < depth - P.window_left) t.nodes &= ~(1ull << i);
+            }
+    }
+    return t;
+}
+// The visible ones of the 64 keys from k0 on, as bits.
+__device__ __forceinline__ uint64_t tree_sees64(const TreeRow& t, int k0, int base) {
+    const int jlo = max(0, t.lo - k0), jhi = min(64, base - k0);
+    const uint64_t below_hi = jhi <= 0 ? 0ull : (jhi >= 64 ? ~0ull : (1ull << jhi) - 1);
+    const uint64_t below_lo = jlo >= 64 ? ~0ull : (1ull << jlo) - 1;
+    const int shift = base - k0;                // node i is key base + i
+    const uint64_t nodes = shift >= 64 || shift <= -64 ? 0ull : shift >= 0 ? t.nodes << shift : t.nodes >> -shift;
+    return (below_hi & ~below_lo) | nodes;
+}
+__device__ __forceinline__ bool tree_sees(const TreeRow& t, int key, int base) {
+    const unsigned i = (unsigned)(key - base);
+    return key < base ? key >= t.lo : i < 64u && ((t.nodes >> i) & 1ull);
+}
 
 // ------------------------------------------------ persistent multi-layer step
 // (attention_layers.cu): one launch runs the append + attention of several
@@ -105,6 +146,11 @@ void int4_clusters(int (&count)[9]);    // [n], n = 2 .. 8: clusters of n CTAs, 
 // FP8KV_ERR_UNSUPPORTED when the shape is not one it implements.
 int launch_attention_tc(const CUtensorMap& tk, const CUtensorMap& tv, const AttnParams& P, cudaStream_t s);
 int status_attention_tc(unsigned int* s, int clear);
+// Host launcher of the tcgen05 kernel over a BF16 cache (attention_bf16_tc.cu),
+// tree calls of more than 16 rows per KV head; partials as the mma.sync kernels
+// write them.  `text` describes the launch.
+int launch_attention_bf16_tc(const CUtensorMap& tk, const CUtensorMap& tv, const AttnParams& P, cudaStream_t s,
+                             char* text, size_t text_bytes);
 int tc_tile_tokens();   // keys per tile of the tcgen05 kernel
 int tc_threads();       // threads per CTA of the tcgen05 kernel
 

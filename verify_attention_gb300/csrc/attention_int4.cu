@@ -119,7 +119,8 @@ __device__ __forceinline__ void append(const AttnParams& P, int b, int hk, int L
 // CL: the partitions of a (sequence, KV head) are a thread-block cluster and
 // merge their rows from each other's shared memory (one sequence of 4000 keys:
 // 11.2 us; partials through memory and a reduce kernel 13.7).
-template <int PS, int WARPS, bool CL>
+// TREE: what a row sees among the last M keys is given by its mask word.
+template <int PS, int WARPS, bool CL, bool TREE>
 __global__ void __launch_bounds__(WARPS * 32, 12 / WARPS) paged_attention_int4_kernel(AttnParams P) {
     extern __shared__ __align__(128) uint8_t smem[];
     constexpr int THREADS = WARPS * 32;
@@ -201,6 +202,8 @@ __global__ void __launch_bounds__(WARPS * 32, 12 / WARPS) paged_attention_int4_k
 
     // ---- rows g and g + 8 of the tile: positions, Q fragments
     int pr[2], lor[2];
+    TreeRow tr[2];
+    const int base = L - P.M;
     float mult[2];
     uint32_t qa[8][4];
     {
@@ -211,6 +214,11 @@ __global__ void __launch_bounds__(WARPS * 32, 12 / WARPS) paged_attention_int4_k
             const int m = min(r, P.R - 1) / P.G;
             pr[hr] = L - P.M + m;
             lor[hr] = (P.window_left >= 0) ? max(0, pr[hr] - P.window_left) : 0;
+            if (TREE) {
+                tr[hr] = tree_row(P, b, m, tree_word(P, b, m), base);
+                pr[hr] = base - 1;                          // the last key that needs no mask
+                lor[hr] = tr[hr].lo;
+            }
 #pragma unroll
             for (int u = 0; u < 4; ++u) {
                 const uint32_t ww[4] = {qw[hr][u].x, qw[hr][u].y, qw[hr][u].z, qw[hr][u].w};
@@ -314,7 +322,8 @@ __global__ void __launch_bounds__(WARPS * 32, 12 / WARPS) paged_attention_int4_k
 #pragma unroll
                 for (int e = 0; e < 4; ++e) {
                     const int key = k0 + 8 * j + 4 * (e & 1) + t;
-                    if (key > pr[e >> 1] || key < lor[e >> 1]) sacc[j][e] = -INFINITY;
+                    if (TREE ? !tree_sees(tr[e >> 1], key, base) : key > pr[e >> 1] || key < lor[e >> 1])
+                        sacc[j][e] = -INFINITY;
                 }
         }
         // O is rescaled only when a row's maximum grows by more than 2^GROW
@@ -460,8 +469,9 @@ __global__ void __launch_bounds__(WARPS * 32, 12 / WARPS) paged_attention_int4_k
         const int64_t row_idx = ((int64_t)b * P.M + m) * P.Hq + hq;
         if (nsplit_b == 1) {
             const float f = vs / l;
-            *(uint2*)(P.out + row_idx * 128 + d4) =
-                make_uint2(pack_bf16x2(acc.x * f, acc.y * f), pack_bf16x2(acc.z * f, acc.w * f));
+            uint2 o2 = make_uint2(pack_bf16x2(acc.x * f, acc.y * f), pack_bf16x2(acc.z * f, acc.w * f));
+            if (TREE && (l == 0.f || tree_word(P, b, m) == 0)) o2 = make_uint2(0u, 0u);
+            *(uint2*)(P.out + row_idx * 128 + d4) = o2;
         } else if (CL) {
             float* dst = merge + (WARPS * 16 + r) * MERGE_STRIDE;
             *(float4*)(dst + d4) = acc;
@@ -507,8 +517,9 @@ __global__ void __launch_bounds__(WARPS * 32, 12 / WARPS) paged_attention_int4_k
             }
             const int m = (R0 + r) / P.G, hq = hk * P.G + (R0 + r) % P.G;
             const float f = vs / l;
-            *(uint2*)(P.out + (((int64_t)b * P.M + m) * P.Hq + hq) * 128 + d4) =
-                make_uint2(pack_bf16x2(acc.x * f, acc.y * f), pack_bf16x2(acc.z * f, acc.w * f));
+            uint2 o2 = make_uint2(pack_bf16x2(acc.x * f, acc.y * f), pack_bf16x2(acc.z * f, acc.w * f));
+            if (TREE && (l == 0.f || tree_word(P, b, m) == 0)) o2 = make_uint2(0u, 0u);
+            *(uint2*)(P.out + (((int64_t)b * P.M + m) * P.Hq + hq) * 128 + d4) = o2;
         }
         __syncwarp();
         cluster_arrive();                               // no shared memory goes before all have read
@@ -516,14 +527,19 @@ __global__ void __launch_bounds__(WARPS * 32, 12 / WARPS) paged_attention_int4_k
     }
 }
 
-template <int PS, int WARPS, bool CL>
-static int launch(const AttnParams& P, cudaStream_t s) {
+template <int PS, int WARPS, bool CL, bool TREE>
+static int launch_one(const AttnParams& P, cudaStream_t s) {
     static std::atomic<uint64_t> done{0};
-    auto kern = paged_attention_int4_kernel<PS, WARPS, CL>;
+    auto kern = paged_attention_int4_kernel<PS, WARPS, CL, TREE>;
     if (opt_in_smem(done, (const void*)kern, SMEM<WARPS>) != cudaSuccess) return (cudaGetLastError(), FP8KV_ERR_CUDA);
     const dim3 grid(P.num_splits, P.Hkv * P.NT, P.B);
     const cudaError_t e = launch_pdl_cluster(kern, grid, dim3(WARPS * 32), SMEM<WARPS>, s, P.cluster, P);
     return e == cudaSuccess ? FP8KV_OK : (cudaGetLastError(), FP8KV_ERR_CUDA);
+}
+
+template <int PS, int WARPS, bool CL>
+static int launch(const AttnParams& P, cudaStream_t s) {
+    return P.tree ? launch_one<PS, WARPS, CL, true>(P, s) : launch_one<PS, WARPS, CL, false>(P, s);
 }
 
 }  // namespace i4
@@ -536,7 +552,7 @@ void int4_clusters(int (&count)[9]) {
     for (int n = 2; n < 9; ++n) {
         int k = known[dev][n].load(std::memory_order_relaxed);
         if (!k) {
-            auto kern = i4::paged_attention_int4_kernel<32, 12, true>;
+            auto kern = i4::paged_attention_int4_kernel<32, 12, true, false>;
             cudaLaunchConfig_t cfg = {};
             cfg.gridDim = dim3(n);
             cfg.blockDim = dim3(12 * 32);

@@ -117,7 +117,9 @@ __device__ __forceinline__ void widen_chunk(const uint32_t (&at)[4], uint4 codes
     }
 }
 
-template <int PS, bool CL>     // CL: the partitions are a cluster
+// CL: the partitions are a cluster.  TREE: what a row sees among the last M keys is
+// given by its mask word, so every row tile spans the keys to the end.
+template <int PS, bool CL, bool TREE>
 __global__ void __launch_bounds__(THREADS, 1) attention_int4_tc_kernel(AttnParams P) {
     extern __shared__ uint8_t smem_raw[];
     uint8_t* smem = (uint8_t*)(((uintptr_t)smem_raw + 1023) & ~(uintptr_t)1023);
@@ -196,8 +198,8 @@ __global__ void __launch_bounds__(THREADS, 1) attention_int4_tc_kernel(AttnParam
     if (!seq_ok && !P.lpt_order && threadIdx.x == 0 && split == 0 && blockIdx.y == 0) flag(FP8KV_DEV_BAD_SEQ_LEN);
     // keys visible to any row of the tile: from the first row's window start
     // to the last row's position (row r is query m = r / G at L - M + m)
-    const int hi0 = L - P.M + (R0 + RL - 1) / P.G;
-    const int lo0 = (P.window_left >= 0) ? max(0, L - P.M + R0 / P.G - P.window_left) : 0;
+    const int hi0 = TREE ? L - 1 : L - P.M + (R0 + RL - 1) / P.G;
+    const int lo0 = (P.window_left >= 0) ? max(0, L - P.M + (TREE ? 0 : R0 / P.G) - P.window_left) : 0;
     const int first_page = lo0 / PS, last_page = hi0 / PS;
     const int nsplit_b = (last_page - first_page + P.split_pages) / P.split_pages;
     if (run && nsplit_b > P.num_splits) {
@@ -226,8 +228,11 @@ __global__ void __launch_bounds__(THREADS, 1) attention_int4_tc_kernel(AttnParam
         const uint32_t lane_base = tmem + ((uint32_t)(wq * 32) << 16);
         const int rr = R0 + min(r, RL - 1);                 // the row of the (b, hk) block
         const int m = rr / P.G;
-        const int p_r = L - P.M + m;
-        const int lo_r = (P.window_left >= 0) ? max(0, p_r - P.window_left) : 0;
+        const int base = L - P.M;
+        const uint64_t word = TREE ? tree_word(P, b, m) : 0;
+        const TreeRow tr = TREE ? tree_row(P, b, m, word, base) : TreeRow{};
+        const int p_r = TREE ? base - 1 : L - P.M + m;      // (a tree's rows: the last key that needs no mask)
+        const int lo_r = TREE ? tr.lo : (P.window_left >= 0) ? max(0, p_r - P.window_left) : 0;
         const int64_t row_idx = ((int64_t)b * P.M + m) * P.Hq + hk * P.G + rr % P.G;
         const float vs = 4.0f * *P.v_scale;
         const bool pad = r >= RL;                           // rows past M x G: Q = 0
@@ -288,6 +293,7 @@ __global__ void __launch_bounds__(THREADS, 1) attention_int4_tc_kernel(AttnParam
             pmax = max(pmax, __shfl_xor_sync(0xffffffffu, pmax, off));
             lomin = min(lomin, __shfl_xor_sync(0xffffffffu, lomin, off));
         }
+        if (TREE) pmax = L - 1;
         // this half's maximum and sum
         float m_run = -INFINITY, l_run = 0.f;
         const uint32_t o_col = lane_base + TM_O + 128 * half;
@@ -312,7 +318,7 @@ __global__ void __launch_bounds__(THREADS, 1) attention_int4_tc_kernel(AttnParam
                     const int jlo = max(0, lo_r - k0), jhi = min(64, p_r - k0 + 1);
                     const uint64_t below_hi = jhi <= 0 ? 0ull : (jhi >= 64 ? ~0ull : (1ull << jhi) - 1);
                     const uint64_t below_lo = jlo >= 64 ? ~0ull : (1ull << jlo) - 1;
-                    const uint64_t vis = below_hi & ~below_lo;
+                    const uint64_t vis = TREE ? tree_sees64(tr, k0, base) : below_hi & ~below_lo;
                     const uint32_t vis_lo = (uint32_t)vis, vis_hi = (uint32_t)(vis >> 32);
 #pragma unroll
                     for (int j = 0; j < 64; ++j)
@@ -404,6 +410,7 @@ __global__ void __launch_bounds__(THREADS, 1) attention_int4_tc_kernel(AttnParam
             // has l = 0: weight 0, values 0
             const float f = direct ? vs / l_tot : (l_tot > 0.f ? 4.0f / l_tot : 0.f);
             const float fa = wa * f, fz = wz * f;
+            const bool zero = TREE && direct && (word == 0 || l_tot == 0.f);
             // the half row goes through shared memory (the widened tiles are
             // free) to one bulk copy
             uint8_t* row_stage = kbuf + (half * 128 + r) * EPI_STRIDE;
@@ -419,7 +426,7 @@ __global__ void __launch_bounds__(THREADS, 1) attention_int4_tc_kernel(AttnParam
                     float x[8];
 #pragma unroll
                     for (int i = 0; i < 8; ++i)
-                        x[i] = __uint_as_float(oa[8 * v4 + i]) * fa + __uint_as_float(oz[8 * v4 + i]) * fz;
+                        x[i] = zero ? 0.f : __uint_as_float(oa[8 * v4 + i]) * fa + __uint_as_float(oz[8 * v4 + i]) * fz;
                     // columns 0 4 1 5 2 6 3 7 back in order
                     dst[v4] = direct ? make_uint4(pack_bf16x2(x[0], x[2]), pack_bf16x2(x[4], x[6]),
                                                   pack_bf16x2(x[1], x[3]), pack_bf16x2(x[5], x[7]))
@@ -477,9 +484,10 @@ __global__ void __launch_bounds__(THREADS, 1) attention_int4_tc_kernel(AttnParam
                 }
                 const float f = 0.25f * vs / den;
                 const int64_t idx = ((int64_t)b * P.M + row / P.G) * P.Hq + hk * P.G + row % P.G;
-                *(uint4*)(P.out + idx * 128 + 8 * c) =
-                    make_uint4(pack_bf16x2(acc[0] * f, acc[1] * f), pack_bf16x2(acc[2] * f, acc[3] * f),
-                               pack_bf16x2(acc[4] * f, acc[5] * f), pack_bf16x2(acc[6] * f, acc[7] * f));
+                uint4 o4 = make_uint4(pack_bf16x2(acc[0] * f, acc[1] * f), pack_bf16x2(acc[2] * f, acc[3] * f),
+                                      pack_bf16x2(acc[4] * f, acc[5] * f), pack_bf16x2(acc[6] * f, acc[7] * f));
+                if (TREE && (den == 0.f || tree_word(P, b, row / P.G) == 0)) o4 = make_uint4(0, 0, 0, 0);
+                *(uint4*)(P.out + idx * 128 + 8 * c) = o4;
             }
         }
     } else {
@@ -718,11 +726,15 @@ int launch_attention_int4_tc(const AttnParams& P, cudaStream_t s, char* text, si
     if (P.cluster > 1 && (P.cluster > i4tc::kMaxCluster || P.cluster != P.num_splits || RT > 1 || P.lpt_order))
         return FP8KV_ERR_UNSUPPORTED;
     if ((P.split_pages * P.page_size) % i4tc::NK || (int64_t)RT * P.Hkv > 65535) return FP8KV_ERR_UNSUPPORTED;
-    static std::atomic<uint64_t> done[2][2];                // [page size][cluster]
+    static std::atomic<uint64_t> done[2][2][2];             // [page size][cluster][tree]
+    const bool cl = P.cluster > 1, tree = P.tree != nullptr;
+    auto pick = [&](auto plain, auto trees) { return tree ? trees : plain; };
     auto kern = P.page_size == 32
-                    ? (P.cluster > 1 ? i4tc::attention_int4_tc_kernel<32, true> : i4tc::attention_int4_tc_kernel<32, false>)
-                    : (P.cluster > 1 ? i4tc::attention_int4_tc_kernel<64, true> : i4tc::attention_int4_tc_kernel<64, false>);
-    if (opt_in_smem(done[P.page_size == 64][P.cluster > 1], (const void*)kern, i4tc::SMEM) != cudaSuccess)
+                    ? (cl ? pick(i4tc::attention_int4_tc_kernel<32, true, false>, i4tc::attention_int4_tc_kernel<32, true, true>)
+                          : pick(i4tc::attention_int4_tc_kernel<32, false, false>, i4tc::attention_int4_tc_kernel<32, false, true>))
+                    : (cl ? pick(i4tc::attention_int4_tc_kernel<64, true, false>, i4tc::attention_int4_tc_kernel<64, true, true>)
+                          : pick(i4tc::attention_int4_tc_kernel<64, false, false>, i4tc::attention_int4_tc_kernel<64, false, true>));
+    if (opt_in_smem(done[P.page_size == 64][cl][tree], (const void*)kern, i4tc::SMEM) != cudaSuccess)
         return (cudaGetLastError(), FP8KV_ERR_CUDA);
     const dim3 grid(P.num_splits, P.Hkv * RT, P.B);
     const cudaError_t e = launch_pdl_cluster(kern, grid, dim3(i4tc::THREADS), i4tc::SMEM, s, P.cluster, P);

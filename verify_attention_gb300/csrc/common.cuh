@@ -445,6 +445,10 @@ int status_attention(unsigned int* s, int clear);  // attention.cu
 int status_attention_int4(unsigned int* s, int clear);  // attention_int4.cu
 int status_attention_int4_tc(unsigned int* s, int clear);  // attention_int4_tc.cu
 int status_prompt(unsigned int* s, int clear);     // prompt_attention.cu
+int status_draft_tree(unsigned int* s, int clear);   // draft_tree.cu
+int status_rope_insert(unsigned int* s, int clear);  // rope_insert.cu
+int status_verify_tree(unsigned int* s, int clear);  // verify_tree.cu
+int status_attention_bf16_tc(unsigned int* s, int clear);  // attention_bf16_tc.cu
 
 // OR this translation unit's status word into *s, optionally clearing it.
 static inline int read_status(unsigned int* s, int clear) {

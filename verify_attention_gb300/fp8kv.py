@@ -23,6 +23,8 @@ FP8KV_CACHE_BF16 = 1
 FP8KV_CACHE_INT4 = 2
 INT4_ROW_BYTES = 72         # a row of an INT4 cache: 64 bytes of codes, 8 of block scales
 DEV_BAD_SLOT, DEV_BAD_POSITION, DEV_BAD_SEQ_LEN, DEV_WAIT_TIMEOUT = 0x1, 0x2, 0x4, 0x8
+DEV_BAD_TREE, DEV_BAD_PROBS = 0x10, 0x20
+TREE_MAX_NODES = 64
 
 _lib = None
 
@@ -75,6 +77,19 @@ def lib() -> ctypes.CDLL:
         L.fp8kv_paged_attention_layers_workspace_size.argtypes = [i32] * 5
         L.fp8kv_paged_attention_layers.restype = i32
         L.fp8kv_paged_attention_layers.argtypes = [vp, i32, i32, i32, i32, i32, i32, i32, i32, vp, sz, vp]
+        L.fp8kv_tree_metadata.restype = i32
+        L.fp8kv_tree_metadata.argtypes = [vp, vp, vp, i32, i32, i32, i32, i32, i32, vp, vp, vp, vp]
+        L.fp8kv_rope_insert.restype = i32
+        L.fp8kv_rope_insert.argtypes = [vp, i64, vp, i64, vp, i64, vp, vp, i32, i32, i32, vp, vp, i32, i32, i32, i32,
+                                        vp, vp, vp, vp, i32, i32, i32, vp]
+        L.fp8kv_tree_attention.restype = i32
+        L.fp8kv_tree_attention.argtypes = [vp, vp, vp, vp, vp, i32, vp, i32, vp, i32, vp, i32, i32, i32, i32, i32,
+                                           i32, i32, vp, vp, f32, i32, i32, vp, sz, vp, vp]
+        L.fp8kv_verify_tree.restype = i32
+        L.fp8kv_verify_tree.argtypes = [vp, i64, vp, i64, i32, vp, vp, vp, i32, i32, i32, vp, vp, vp, vp]
+        L.fp8kv_cache_keep_path.restype = i32
+        L.fp8kv_cache_keep_path.argtypes = [vp, vp, i32, i32, vp, i32, vp, i32, vp, i32, i32, i32, i32, i32, i32, vp,
+                                            vp]
         L.fp8kv_e4m3_encode_bits.restype = i32
         L.fp8kv_e4m3_encode_bits.argtypes = [u32, sz, vp, vp]
         L.fp8kv_selftest_bounded_wait.restype = i32
@@ -321,6 +336,41 @@ def fp8kv_prompt_attention(q, k, v, cu_seqlens, max_seq_len, sm_scale, window_le
     return out
 
 
+def fp8kv_rope_insert(q, k, v, positions, cos_sin, slot_mapping, k_scale, v_scale, k_cache, v_cache, interleaved=False,
+                      q_out=None, stream=None):
+    """Rotary positions on Q and K, then K and V into the cache: q bf16 [T][Hq][D],
+    k, v bf16 [T][Hkv][D] (tokens dense, any distance apart), positions and
+    slot_mapping int64 [T], cos_sin fp32 [max_pos][rot_dim] (the cosines of a
+    position's rot_dim / 2 angles, then the sines), any cache type.  Pairs are the
+    elements (k, k + rot_dim / 2), or neighbours with ``interleaved``; the rest of a
+    head stays.  Returns the rotated Q, bf16 [T][Hq][D]; rows of tokens with a bad
+    position are left as they are (zeros when allocated here)."""
+    dt = _cache_dtype(k_cache)
+    T, Hq, D = q.shape
+    Hkv = k.shape[1]
+    q_stride = _token_rows(q, "q", T, Hq, D)
+    k_stride, v_stride = _token_rows(k, "k", T, Hkv, D), _token_rows(v, "v", T, Hkv, D)
+    _dev(positions, "positions", torch.int64), _dev(slot_mapping, "slot_mapping", torch.int64)
+    _dev(cos_sin, "cos_sin", torch.float32), _dev(k_cache, "k_cache"), _dev(v_cache, "v_cache")
+    num_pages, heads, page_size = _cache_shape(k_cache, v_cache, dt)
+    if heads != Hkv or v_cache.dtype != k_cache.dtype or v_cache.shape != k_cache.shape:
+        raise ValueError(f"k_cache and v_cache must have the same type and shape, of {Hkv} heads")
+    if positions.numel() != T or slot_mapping.numel() != T or cos_sin.dim() != 2:
+        raise ValueError(f"positions and slot_mapping must be [{T}], cos_sin [max_pos][rot_dim]")
+    if dt != FP8KV_CACHE_BF16:
+        _one_scale(k_scale, v_scale)
+    q_out = _zeros((T, Hq, D), q.device, stream) if q_out is None else _dev(q_out, "q_out", torch.bfloat16)
+    if q_out.shape != (T, Hq, D):
+        raise ValueError(f"q_out must be {(T, Hq, D)}, got {tuple(q_out.shape)}")
+    rc = lib().fp8kv_rope_insert(q.data_ptr(), q_stride, k.data_ptr(), k_stride, v.data_ptr(), v_stride,
+                                 positions.data_ptr(), cos_sin.data_ptr(), cos_sin.shape[0], cos_sin.shape[1],
+                                 int(interleaved), q_out.data_ptr(), slot_mapping.data_ptr(), T, Hq, Hkv, D,
+                                 _ptr(k_scale), _ptr(v_scale), k_cache.data_ptr(), v_cache.data_ptr(), num_pages,
+                                 page_size, dt, _stream(stream, k_cache))
+    _check("fp8kv_rope_insert", rc)
+    return q_out
+
+
 def fp8kv_paged_attention_plan(B, M, Hq, Hkv, D, page_size, max_seq_len, window_left, split_tokens=0):
     ns, st = ctypes.c_int(0), ctypes.c_int(0)
     rc = lib().fp8kv_paged_attention_plan(B, M, Hq, Hkv, D, page_size, max_seq_len, window_left,
@@ -486,8 +536,9 @@ class _Owned:
 
 
 class PreparedAttention:
-    """fp8kv_append_paged_attention (k_new, v_new given) or
-    fp8kv_paged_attention over fixed tensors, marshalled once: each call
+    """fp8kv_append_paged_attention (k_new, v_new given),
+    fp8kv_paged_attention, or with tree_mask (int64 [B][M]) fp8kv_tree_attention
+    over fixed tensors, marshalled once: each call
     passes the prepared arguments and the stream, nothing else.  For serving
     loops whose caches, metadata and buffers stay at fixed addresses; the
     tensors must outlive the object, and the object its calls on a raw stream
@@ -495,7 +546,8 @@ class PreparedAttention:
     output: on several streams they need one object each."""
 
     def __init__(self, q, k_cache, v_cache, block_table, seq_lens, max_seq_len, k_scale, v_scale, sm_scale,
-                 window_left=-1, split_tokens=0, workspace=None, out=None, k_new=None, v_new=None, num_pages=None):
+                 window_left=-1, split_tokens=0, workspace=None, out=None, k_new=None, v_new=None, num_pages=None,
+                 tree_mask=None):
         dt = _cache_dtype(k_cache)
         _dev(q, "q", torch.bfloat16), _dev(k_cache, "k_cache"), _dev(v_cache, "v_cache")
         _dev(block_table, "block_table", torch.int32), _dev(seq_lens, "seq_lens", torch.int32)
@@ -503,6 +555,8 @@ class PreparedAttention:
         P, Hkv, page_size = _cache_shape(k_cache, v_cache, dt)
         if dt == FP8KV_CACHE_INT4:
             _int4_call(q, k_cache, block_table, seq_lens, k_scale, v_scale, out, num_pages)
+        if tree_mask is not None:
+            _tree_call(q, k_cache, v_cache, block_table, seq_lens, tree_mask, k_scale, v_scale, out, num_pages, dt)
         if (k_new is None) != (v_new is None):
             raise ValueError("k_new and v_new go together")
         if k_new is not None:
@@ -523,7 +577,13 @@ class PreparedAttention:
             raise ValueError("out must have the shape of q")
         self._own = _Owned(own)
         self.out, self._keep = out, (q, k_cache, v_cache, block_table, seq_lens, k_scale, v_scale, workspace, k_new,
-                                     v_new)
+                                     v_new, tree_mask)
+        if tree_mask is not None:
+            self._fn, self._name = lib().fp8kv_tree_attention, "fp8kv_tree_attention"
+            self._args = _tree_args(q, k_cache, v_cache, dt, block_table, seq_lens, max_seq_len, tree_mask, k_scale,
+                                    v_scale, sm_scale, window_left, split_tokens, workspace, out, k_new, v_new,
+                                    num_pages)
+            return
         args = (_ptr(q), _ptr(k_cache), _ptr(v_cache), dt, _ptr(block_table), block_table.shape[1], _ptr(seq_lens),
                 int(max_seq_len), B, M, Hq, Hkv, D, page_size, int(P if num_pages is None else num_pages),
                 _ptr(k_scale), _ptr(v_scale), float(sm_scale), int(window_left), int(split_tokens), _ptr(workspace),
@@ -566,6 +626,213 @@ def fp8kv_paged_attention_noalloc(q, k_cache, v_cache, block_table, seq_lens, ma
         _stream(stream, q))
     _check("fp8kv_paged_attention_noalloc", rc)
     return out
+
+
+def _tree_rows(t: torch.Tensor, name: str, dtype, B: int, M: int):
+    _dev(t, name)
+    if t.dtype != dtype and not (dtype == torch.int64 and name == "tree_mask" and t.dtype == torch.uint64):
+        raise ValueError(f"{name} must be {dtype}, got {t.dtype}")
+    if t.shape != (B, M):
+        raise ValueError(f"{name} must be {(B, M)}, got {tuple(t.shape)}")
+    return t
+
+
+def fp8kv_tree_metadata(parents, seq_lens, block_table, page_size, max_seq_len, num_pages, tree_mask=None,
+                        positions=None, slot_mapping=None, stream=None):
+    """What a step over trees of drafted tokens needs from parents (int32 [B][M],
+    -1: padding; node 0 is the root): returns tree_mask (the bits of a node and its
+    ancestors), positions and slot_mapping, int64 [B][M] each.  seq_lens int32 [B]
+    (the M nodes included), block_table int32 [B][max_pages_per_seq]."""
+    _dev(parents, "parents", torch.int32), _dev(seq_lens, "seq_lens", torch.int32)
+    _dev(block_table, "block_table", torch.int32)
+    if parents.dim() != 2:
+        raise ValueError("parents must be [B][M]")
+    B, M = parents.shape
+    if block_table.dim() != 2 or block_table.shape[0] != B or seq_lens.numel() != B:
+        raise ValueError(f"block_table must be [{B}][pages] and seq_lens [{B}]")
+    given = (tree_mask, positions, slot_mapping)
+    for t, n in zip(given, ("tree_mask", "positions", "slot_mapping")):
+        if t is not None:
+            _tree_rows(t, n, torch.int64, B, M)
+    if any(t is None for t in given):
+        with _at(stream):
+            made = torch.empty((3, B, M), dtype=torch.int64, device=parents.device).unbind(0)
+        tree_mask, positions, slot_mapping = (m if t is None else t for t, m in zip(given, made))
+    rc = lib().fp8kv_tree_metadata(parents.data_ptr(), seq_lens.data_ptr(), block_table.data_ptr(),
+                                   block_table.shape[1], int(max_seq_len), B, M, int(num_pages), int(page_size),
+                                   tree_mask.data_ptr(), positions.data_ptr(), slot_mapping.data_ptr(),
+                                   _stream(stream, parents))
+    _check("fp8kv_tree_metadata", rc)
+    return tree_mask, positions, slot_mapping
+
+
+def _tree_call(q, k_cache, v_cache, block_table, seq_lens, tree_mask, k_scale, v_scale, out, num_pages, dt):
+    """Checks of a tree call beyond the library's own: what it cannot see from pointers."""
+    B, M = q.shape[:2]
+    _tree_rows(tree_mask, "tree_mask", torch.int64, B, M)
+    if block_table.dim() != 2 or block_table.shape[0] != B or seq_lens.numel() != B:
+        raise ValueError(f"block_table must be [{B}][pages] and seq_lens [{B}]")
+    if v_cache.dtype != k_cache.dtype or v_cache.shape != k_cache.shape:
+        raise ValueError("k_cache and v_cache must have the same type and shape")
+    if dt != FP8KV_CACHE_BF16:
+        _one_scale(k_scale, v_scale)
+    if out is not None and _dev(out, "out", torch.bfloat16).shape != q.shape:
+        raise ValueError("out must have the shape of q")
+    if num_pages is not None and num_pages > k_cache.shape[0]:
+        raise ValueError(f"num_pages is {num_pages}, the cache has {k_cache.shape[0]}")
+
+
+def _tree_args(q, k_cache, v_cache, dt, block_table, seq_lens, max_seq_len, tree_mask, k_scale, v_scale, sm_scale,
+               window_left, split_tokens, workspace, out, k_new, v_new, num_pages):
+    B, M, Hq, D = q.shape
+    P, Hkv, page_size = _cache_shape(k_cache, v_cache, dt)
+    return (_ptr(k_new), _ptr(v_new), _ptr(q), _ptr(k_cache), _ptr(v_cache), dt, _ptr(block_table),
+            block_table.shape[1], _ptr(seq_lens), int(max_seq_len), _ptr(tree_mask), B, M, Hq, Hkv, D, page_size,
+            int(P if num_pages is None else num_pages), _ptr(k_scale), _ptr(v_scale), float(sm_scale),
+            int(window_left), int(split_tokens), _ptr(workspace), workspace.numel() if workspace is not None else 0,
+            _ptr(out))
+
+
+def fp8kv_tree_attention(q, k_cache, v_cache, block_table, seq_lens, tree_mask, max_seq_len, k_scale, v_scale, sm_scale,
+                         window_left=-1, split_tokens=0, workspace=None, out=None, num_pages=None, k_new=None,
+                         v_new=None, stream=None):
+    """fp8kv_paged_attention for the M nodes of a tree: row m sees the cached keys
+    before the nodes and the nodes in tree_mask (int64 [B][M], fp8kv_tree_metadata).
+    Padding rows (mask 0) become zeros.  With k_new, v_new (bf16 [B][M][Hkv][D]) the
+    nodes' rows are appended first.  Any cache type, M up to 64."""
+    dt = _cache_dtype(k_cache)
+    _dev(q, "q", torch.bfloat16), _dev(k_cache, "k_cache"), _dev(v_cache, "v_cache")
+    _dev(block_table, "block_table", torch.int32), _dev(seq_lens, "seq_lens", torch.int32)
+    B, M, Hq, D = q.shape
+    _, Hkv, page_size = _cache_shape(k_cache, v_cache, dt)
+    _tree_call(q, k_cache, v_cache, block_table, seq_lens, tree_mask, k_scale, v_scale, out, num_pages, dt)
+    if (k_new is None) != (v_new is None):
+        raise ValueError("k_new and v_new go together")
+    if k_new is not None:
+        for t, n in ((k_new, "k_new"), (v_new, "v_new")):
+            if _dev(t, n, torch.bfloat16).shape != (B, M, Hkv, D):
+                raise ValueError(f"{n} must be [B][M][Hkv][D]")
+    need = fp8kv_paged_attention_workspace_size(B, M, Hq, Hkv, D, page_size, max_seq_len, window_left, split_tokens)
+    if workspace is None:
+        workspace = _workspace(need, q.device, stream)
+    if out is None:
+        out = _empty_like(q, stream)
+    args = _tree_args(q, k_cache, v_cache, dt, block_table, seq_lens, max_seq_len, tree_mask, k_scale, v_scale,
+                      sm_scale, window_left, split_tokens, workspace, out, k_new, v_new, num_pages)
+    _check("fp8kv_tree_attention", lib().fp8kv_tree_attention(*args, _stream(stream, q)))
+    return out
+
+
+def _prob_rows(t: torch.Tensor, name: str, B: int, M: int, V: int) -> int:
+    """Probabilities [B][M][V] with dense rows; returns the elements between rows."""
+    if not t.is_cuda:
+        raise ValueError(f"{name} must be a CUDA tensor")
+    st = t.stride()
+    if t.shape != (B, M, V) or (V > 1 and st[2] != 1) or (B > 1 and M > 1 and st[0] != M * st[1]):
+        raise ValueError(f"{name} must be {(B, M, V)} with dense rows, all the same distance apart")
+    step = st[1] if M > 1 else st[0] if B > 1 else V
+    if step < V:
+        raise ValueError(f"{name} must have rows that do not overlap")
+    return step
+
+
+def fp8kv_verify_tree(target_probs, draft_probs, tokens, parents, uniforms, out_tokens=None, num_tokens=None, path=None,
+                      stream=None):
+    """Which drafted tokens of a tree stand, and the token after them: target_probs
+    fp32 or bf16 [B][M][V] (row n: the token behind node n), draft_probs the same or
+    None (what n's children were drawn from; None: they were chosen), tokens and
+    parents int32 [B][M], uniforms fp32 [B][M] in [0, 1).  Returns out_tokens int32
+    [B][M] (the tokens that stand, the next one, -1s), num_tokens int32 [B] (how many
+    those are) and path int32 [B][M] (node 0, the nodes that stand, -1s)."""
+    if target_probs.dim() != 3:
+        raise ValueError("target_probs must be [B][M][V]")
+    B, M, V = target_probs.shape
+    if target_probs.dtype not in (torch.float32, torch.bfloat16):
+        raise ValueError(f"target_probs must be {torch.float32} or {torch.bfloat16}, got {target_probs.dtype}")
+    p_stride, q_stride = _prob_rows(target_probs, "target_probs", B, M, V), 0
+    if draft_probs is not None:
+        if draft_probs.dtype != target_probs.dtype:
+            raise ValueError(f"draft_probs must be {target_probs.dtype}, got {draft_probs.dtype}")
+        q_stride = _prob_rows(draft_probs, "draft_probs", B, M, V)
+    _tree_rows(tokens, "tokens", torch.int32, B, M), _tree_rows(parents, "parents", torch.int32, B, M)
+    _tree_rows(uniforms, "uniforms", torch.float32, B, M)
+    if out_tokens is None or num_tokens is None or path is None:
+        with _at(stream):
+            made = torch.empty((2 * M + 1) * B, dtype=torch.int32, device=target_probs.device)
+        out_tokens = made[:B * M].view(B, M) if out_tokens is None else out_tokens
+        path = made[B * M:2 * B * M].view(B, M) if path is None else path
+        num_tokens = made[2 * B * M:] if num_tokens is None else num_tokens
+    _tree_rows(out_tokens, "out_tokens", torch.int32, B, M), _tree_rows(path, "path", torch.int32, B, M)
+    if _dev(num_tokens, "num_tokens", torch.int32).shape != (B,):
+        raise ValueError(f"num_tokens must be {(B,)}, got {tuple(num_tokens.shape)}")
+    rc = lib().fp8kv_verify_tree(target_probs.data_ptr(), p_stride, _ptr(draft_probs), q_stride,
+                                 0 if target_probs.dtype == torch.float32 else 1, tokens.data_ptr(), parents.data_ptr(),
+                                 uniforms.data_ptr(), B, M, V, out_tokens.data_ptr(), num_tokens.data_ptr(),
+                                 path.data_ptr(), _stream(stream, target_probs))
+    _check("fp8kv_verify_tree", rc)
+    return out_tokens, num_tokens, path
+
+
+class PreparedKeepPath:
+    """fp8kv_cache_keep_path over fixed tensors, marshalled once: in every layer's
+    caches (lists of tensors of one type and shape) the rows of the nodes in path
+    (int32 [B][M], fp8kv_verify_tree) go to the first of the tree's indices, and
+    new_seq_lens (int32 [B]) becomes the length up to them.  The tensors must outlive
+    the object, and the object its calls on a raw stream handle and the graphs that
+    captured it."""
+
+    def __init__(self, k_caches, v_caches, block_table, seq_lens, path, max_seq_len, new_seq_lens=None, num_pages=None):
+        n = len(k_caches)
+        if n == 0 or len(v_caches) != n:
+            raise ValueError("k_caches and v_caches must be lists of the same length, one entry a layer")
+        first = k_caches[0]
+        dt = _cache_dtype(first)
+        P, Hkv, page_size = _cache_shape(first, v_caches[0], dt)
+        for t in (*k_caches, *v_caches):
+            if _dev(t, "caches").dtype != first.dtype or t.shape != first.shape or t.device != first.device:
+                raise ValueError("all caches must have the same type, shape and device")
+        if len({t.data_ptr() for t in (*k_caches, *v_caches)}) != 2 * n:
+            raise ValueError("every layer must have a K and a V cache of its own")
+        _dev(block_table, "block_table", torch.int32), _dev(seq_lens, "seq_lens", torch.int32)
+        _dev(path, "path", torch.int32)
+        if path.dim() != 2:
+            raise ValueError("path must be [B][M]")
+        B, M = path.shape
+        if block_table.dim() != 2 or block_table.shape[0] != B or seq_lens.numel() != B:
+            raise ValueError(f"block_table must be [{B}][pages] and seq_lens [{B}]")
+        if num_pages is not None and num_pages > P:
+            raise ValueError(f"num_pages is {num_pages}, the caches have {P}")
+        own = []
+        if new_seq_lens is None:
+            new_seq_lens = torch.empty(B, dtype=torch.int32, device=path.device)
+            own.append(new_seq_lens)
+        if _dev(new_seq_lens, "new_seq_lens", torch.int32).numel() != B:
+            raise ValueError(f"new_seq_lens must be [{B}]")
+        self._own = _Owned(own)
+        self.new_seq_lens = new_seq_lens
+        self._keep = (list(k_caches), list(v_caches), block_table, seq_lens, path)
+        ptrs = ctypes.c_void_p * n
+        self._k, self._v = (ptrs(*(t.data_ptr() for t in c)) for c in (k_caches, v_caches))
+        self._args = (ctypes.addressof(self._k), ctypes.addressof(self._v), n, dt, block_table.data_ptr(),
+                      block_table.shape[1], seq_lens.data_ptr(), int(max_seq_len), path.data_ptr(), B, M, Hkv,
+                      128 if dt == FP8KV_CACHE_INT4 else first.shape[3], int(P if num_pages is None else num_pages),
+                      page_size, new_seq_lens.data_ptr())
+        self._fn = lib().fp8kv_cache_keep_path
+
+    def __call__(self, stream=None):
+        handle = _stream(stream, self.new_seq_lens)
+        self._own.before_call(stream, handle)
+        _check("fp8kv_cache_keep_path", self._fn(*self._args, handle))
+        return self.new_seq_lens
+
+
+def fp8kv_cache_keep_path(k_caches, v_caches, block_table, seq_lens, path, max_seq_len, new_seq_lens=None,
+                          num_pages=None, stream=None):
+    """Move the accepted path's rows together in every layer's caches (see
+    PreparedKeepPath); returns new_seq_lens."""
+    with _at(stream):
+        call = PreparedKeepPath(k_caches, v_caches, block_table, seq_lens, path, max_seq_len, new_seq_lens, num_pages)
+    return call(stream)
 
 
 class fp8kv_layer(ctypes.Structure):
