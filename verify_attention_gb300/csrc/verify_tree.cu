@@ -19,10 +19,11 @@
 //
 // Whole numbers come out, so sums have to be good to far less than the smallest
 // probability: a border that moves by e flips a draw with probability e times the
-// number of tokens.  The FP64 units would bound the pass (two additions a token
-// are five times the time of the HBM reads).  The weights and the sums are pairs
-// of fp32 instead, hi + lo with the rounding error of each step in lo (the
-// two-sum and two-product of Dekker and Knuth): 2^-46 of the weight a step.
+// number of tokens.  FP64 would bound the pass (2 additions a clock and SM: five
+// times the time of the HBM reads; a first form with it in the scans took 17.8 us
+// for one sequence of 131072 tokens).  The weights, the sums and the prefixes are
+// pairs of fp32 instead, hi + lo with the rounding error of each step in lo (the
+// two-sum and two-product of Dekker and Knuth): 2^-45 of the weight a step.
 #include "attention.cuh"
 #include "common.cuh"
 
@@ -30,7 +31,7 @@ namespace fp8kv {
 
 int status_verify_tree(unsigned int* s, int clear) { return read_status(s, clear); }
 
-constexpr int kVerifyThreads = 512, kVerifyWarps = kVerifyThreads / 32, kVerifyMaxCluster = 8;
+constexpr int kVerifyThreads = 512, kVerifyWarps = kVerifyThreads / 32, kVerifyMaxCluster = 16;
 
 struct VerifyParams {
     const void *p, *q;
@@ -51,6 +52,51 @@ __device__ __forceinline__ F2 two_sum(float a, float b) {
     const float s = __fadd_rn(a, b), x = __fsub_rn(s, a);
     return {s, __fadd_rn(__fsub_rn(a, __fsub_rn(s, x)), __fsub_rn(b, x))};
 }
+// the same for |a| >= |b|, or a = 0
+__device__ __forceinline__ F2 fast_two_sum(float a, float b) {
+    const float s = __fadd_rn(a, b);
+    return {s, __fsub_rn(b, __fsub_rn(s, a))};
+}
+__device__ __forceinline__ F2 two_prod(float a, float b) {
+    const float p = __fmul_rn(a, b);
+    return {p, __fmaf_rn(a, b, -p)};
+}
+__device__ __forceinline__ F2 operator+(F2 a, F2 b) {
+    const F2 s = two_sum(a.hi, b.hi);
+    return fast_two_sum(s.hi, __fadd_rn(s.lo, __fadd_rn(a.lo, b.lo)));
+}
+__device__ __forceinline__ F2 operator-(F2 a, F2 b) { return a + F2{-b.hi, -b.lo}; }
+__device__ __forceinline__ F2 operator*(F2 a, F2 b) {
+    const F2 p = two_prod(a.hi, b.hi);
+    return fast_two_sum(p.hi, __fadd_rn(p.lo, __fmaf_rn(a.hi, b.lo, __fmul_rn(a.lo, b.hi))));
+}
+__device__ __forceinline__ bool operator>(F2 a, F2 b) { return __fadd_rn(__fsub_rn(a.hi, b.hi), __fsub_rn(a.lo, b.lo)) > 0.f; }
+__device__ __forceinline__ F2 shfl(F2 a, int lane) {
+    return {__shfl_sync(0xffffffffu, a.hi, lane), __shfl_sync(0xffffffffu, a.lo, lane)};
+}
+// lane l: the sum of lanes 0 .. l (n of them, a power of two).  Not unrolled: the
+// kernel's instructions come from L2 for every CTA, and short code runs sooner than
+// fast code.
+__device__ __forceinline__ F2 warp_scan(F2 a, int lane, int n) {
+#pragma unroll 1
+    for (int o = 1; o < n; o <<= 1) {
+        const F2 b = {__shfl_up_sync(0xffffffffu, a.hi, o), __shfl_up_sync(0xffffffffu, a.lo, o)};
+        const F2 c = a + b;
+        if (lane >= o) a = c;
+    }
+    return a;
+}
+// Of runs with the sums `run` that end at `end`: the first whose end exceeds t
+// (should the roundings leave none: the last that holds anything; -1: none does).
+__device__ __forceinline__ int locate(F2 run, F2 end, F2 t) {
+    const unsigned some = __ballot_sync(0xffffffffu, run.hi > 0.f);
+    const unsigned over = __ballot_sync(0xffffffffu, run.hi > 0.f && end > t);
+    return over ? __ffs(over) - 1 : 31 - __clz(some);
+}
+__device__ __forceinline__ F2 before_lane(F2 scan, int at, F2 base) {
+    const F2 left = shfl(scan, max(at, 1) - 1);
+    return at > 0 ? base + left : base;
+}
 
 // The weights of a node's row after k children fell: step j takes w to (w a_j -
 // b_j q)+, a_j a power of two that keeps the weights near 1 and b_j = S a_j.
@@ -58,13 +104,18 @@ struct VerifyStep {
     float a, bh, bl;
 };
 
+// (negative, zero and NaN: nothing left)
 __device__ __forceinline__ F2 step_weight(F2 w, float q, VerifyStep s) {
     const float th = __fmul_rn(s.bh, q), tl = __fmaf_rn(s.bl, q, __fmaf_rn(s.bh, q, -th));
     const F2 d = two_sum(__fmul_rn(w.hi, s.a), -th);
-    const float lo = __fadd_rn(d.lo, __fsub_rn(__fmul_rn(w.lo, s.a), tl));
-    const float hi = __fadd_rn(d.hi, lo);
-    // (negative, zero and NaN: nothing left)
-    return hi > 0.f ? F2{hi, __fsub_rn(lo, __fsub_rn(hi, d.hi))} : F2{0.f, 0.f};
+    const float lo = __fadd_rn(d.lo, __fmaf_rn(w.lo, s.a, -tl));
+    const bool some = __fadd_rn(d.hi, lo) > 0.f;
+    return {some ? d.hi : 0.f, some ? lo : 0.f};
+}
+// a node's first step: S = 1, so w - q, exactly
+__device__ __forceinline__ F2 first_step(float p, float q) {
+    const F2 d = two_sum(p, -q);
+    return {d.hi > 0.f ? d.hi : 0.f, d.hi > 0.f ? d.lo : 0.f};
 }
 
 template <typename T>
@@ -102,119 +153,156 @@ struct Row {
     const T* at;                // element -skew, on a 16-byte boundary
     int skew, V;
     __device__ __forceinline__ Row(const T* row, int skew_, int V_) : at(row - skew_), skew(skew_), V(V_) {}
-    __device__ __forceinline__ void load(int g, bool aligned, float (&f)[N]) const {
+    // any group, an element at a time; -1: zeros
+    __device__ __forceinline__ void load(int g, float (&f)[N]) const {
         const int first = N * g - skew;
-        if (aligned && first >= 0 && first + N <= V) {
-            widen(__ldg(reinterpret_cast<const uint4*>(at + (int64_t)N * g)), f);
-        } else {
 #pragma unroll
-            for (int i = 0; i < N; ++i) f[i] = first + i >= 0 && first + i < V ? prob(at[(int64_t)N * g + i]) : 0.f;
-        }
+        for (int i = 0; i < N; ++i) f[i] = g >= 0 && first + i >= 0 && first + i < V ? prob(at[(int64_t)N * g + i]) : 0.f;
     }
 };
 
-__device__ __forceinline__ double dsmem_ld_f64(uint32_t a) {
-    double v;
-    asm volatile("ld.shared::cluster.f64 %0, [%1];" : "=d"(v) : "r"(a) : "memory");
-    return v;
+// What a CTA tells the others of a pass: its sum, and where its walk stands.  Every
+// CTA walks by itself and all read the same inputs; should those change during the
+// call the walks may part, and no CTA may then wait for one, or send to one, that has
+// gone.  All see the same words, so all stop at the same pass.
+struct __align__(16) VerifyPart {
+    F2 sum;
+    int walk, unused;
+};
+__device__ __forceinline__ void send_part(uint32_t to, uint32_t mbar, F2 v, int walk) {
+    asm volatile("st.async.shared::cluster.mbarrier::complete_tx::bytes.v4.b32 [%0], {%1, %2, %3, %4}, [%5];" ::"r"(to),
+                 "r"(__float_as_uint(v.hi)), "r"(__float_as_uint(v.lo)), "r"(walk), "r"(0), "r"(mbar)
+                 : "memory");
 }
 
+enum { PASS_SUM = 1, PASS_DRAW = 2, PASS_ROW = 3, PASS_STOP = 4 };
+
 template <typename T, bool DRAFT>
-__global__ void __launch_bounds__(kVerifyThreads) verify_tree_kernel(VerifyParams P) {
-    constexpr int N = Row<T>::N, UNROLL = 4;
-    __shared__ int par[64], tok[64], fallen[64], path[64];
-    __shared__ float up[64], pw[64], qw[64];
+__global__ void __launch_bounds__(kVerifyThreads, 2) verify_tree_kernel(VerifyParams P) {
+    constexpr int N = Row<T>::N, U = (DRAFT ? 8 : 16) / N;      // groups a lane has in flight
+    __shared__ int tok[64], fallen[64], path[64];
+    __shared__ float un[64], pw[64], qw[64];
+    __shared__ unsigned kids[64][2], stands[2];         // bits: a node's children; nodes that stand as first children
     __shared__ VerifyStep steps[64];
-    __shared__ double warp_sum[kVerifyWarps], cta_sum[2], sums[kVerifyMaxCluster];
-    __shared__ int s_cur, s_fallen, s_state, s_depth;
+    __shared__ F2 warp_sum[2][kVerifyWarps];            // of the warps' runs; of the parts of one of them
+    __shared__ VerifyPart parts[2][kVerifyMaxCluster];
+    __shared__ __align__(8) uint64_t bars[2];
+    __shared__ F2 s_t, s_base;
+    __shared__ int s_cur, s_fallen, s_state, s_depth, s_warp;
     pdl_launch_dependents();
     const int C = P.cluster, rank = blockIdx.x % C, b = blockIdx.x / C;
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31, M = P.M, V = P.V;
     const T* p_rows = (const T*)P.p + (int64_t)b * M * P.p_stride;
     const T* q_rows = (const T*)P.q + (int64_t)b * M * P.q_stride;
-    pdl_wait();
-    if (tid < M) {
-        // a node's token in its parent's rows: the walk below reads no memory
-        const int64_t i = (int64_t)b * M + tid;
-        int pa = tid ? P.parents[i] : -1;
-        const int x = P.tokens[i];
-        up[tid] = P.uniforms[i];
-        if (pa < -1 || pa >= tid || (pa >= 0 && (x < 0 || x >= V))) {
-            if (tid) {
-                if (rank == 0) flag(FP8KV_DEV_BAD_TREE);
-                pa = -1;
-            }
-        }
-        par[tid] = pa;
-        tok[tid] = x;
-        pw[tid] = pa >= 0 ? prob(p_rows[pa * P.p_stride + x]) : 0.f;
-        qw[tid] = DRAFT && pa >= 0 ? prob(q_rows[pa * P.q_stride + x]) : 1.f;
-    }
+    if (tid < 64) kids[tid][0] = kids[tid][1] = 0;
     if (tid == 0) {
-        s_cur = s_depth = s_fallen = 0;
-        path[0] = 0;
+        mbar_init(smem_u32(&bars[0]), 1);
+        mbar_init(smem_u32(&bars[1]), 1);
+        fence_barrier_init();
     }
     __syncthreads();
-
-    // the walk's state, thread 0's: the next node to look at, S, the weight's
-    // scale (a power of two)
-    int m = 1;
-    double S = 1.0;
-    int passes = 0;
-    // states: 1 a pass for S of the current node, 2 the last draw, 3 the last draw
-    // from the node's own row (nothing was left of it)
-    while (true) {
+    if (C > 1) cluster_arrive_relaxed();                    // waited for before anything is sent
+    pdl_wait();
+    if (tid < 64) {
+        // a node's token in its parent's rows: the walk below reads no memory
+        const int64_t i = (int64_t)b * M + tid;
+        int pa = -1, x = 0;
+        float u = 0.f, w = 0.f, q = 1.f;
+        if (tid < M) {
+            if (tid) pa = P.parents[i];
+            x = P.tokens[i];
+            u = P.uniforms[i];
+        }
+        if (pa < -1 || pa >= tid || (pa >= 0 && (x < 0 || x >= V))) {
+            if (tid && rank == 0) flag(FP8KV_DEV_BAD_TREE);
+            pa = -1;
+        }
+        if (pa >= 0) {
+            w = prob(p_rows[pa * P.p_stride + x]);
+            if (DRAFT) q = prob(q_rows[pa * P.q_stride + x]);
+            atomicOr(&kids[pa][tid >> 5], 1u << lane);
+        }
+        w = fmaxf(w, 0.f);                                  // (NaN: 0)
+        q = fmaxf(q, 0.f);
+        tok[tid] = x;
+        un[tid] = u;
+        pw[tid] = w;
+        qw[tid] = q;
+        // u q < w, exactly
+        const F2 uq = two_prod(u, q);
+        const unsigned yes = __ballot_sync(0xffffffffu, w > 0.f && (uq.hi < w || (uq.hi == w && uq.lo < 0.f)));
+        if (lane == 0) stands[warp] = yes;
         if (tid == 0) {
-            int cur = s_cur, k = s_fallen, depth = s_depth, state = 2;
-            for (; m < M; ++m) {
-                if (par[m] != cur) continue;
+            s_cur = s_depth = s_fallen = 0;
+            path[0] = 0;
+        }
+    }
+    if (C > 1) cluster_wait();
+    __syncthreads();
+
+    // warp 0's (every lane the same): the children not yet looked at, and S
+    uint64_t rest = (uint64_t)kids[0][1] << 32 | kids[0][0];
+    F2 S = {1.f, 0.f};
+    int passes = 0, state = 0;
+    bool valid = true;
+    while (true) {
+        if (warp == 0 && state != PASS_ROW) {
+            // ---- the walk, to the next pass: one for S of the current node, or the
+            // last draw (from the node's own row, should nothing be left of it)
+            int cur = s_cur, k = s_fallen, depth = s_depth;
+            state = PASS_DRAW;
+            const uint64_t first = (uint64_t)stands[1] << 32 | stands[0];
+            while (rest) {
+                const int m = __ffsll(rest) - 1;
+                rest &= rest - 1;
                 const int x = tok[m];
-                double w = fmax((double)pw[m], 0.0);
-                const double qx = fmax((double)qw[m], 0.0);
-                if (DRAFT) {
-                    for (int j = 0; j < k; ++j)
-                        w = fmax(w * steps[j].a - ((double)steps[j].bh + (double)steps[j].bl) * qx, 0.0);
-                } else {
-                    for (int j = 0; j < k; ++j)
-                        if (fallen[j] == x) w = 0.0;
+                F2 w = {pw[m], 0.f};
+                bool yes = (first >> m) & 1;
+                if (k > 0) {
+                    const float qx = qw[m];
+#pragma unroll 1
+                    for (int j = 0; j < k; ++j) {
+                        if (DRAFT) w = step_weight(w, qx, steps[j]);
+                        else if (fallen[j] == x) w = {0.f, 0.f};
+                    }
+                    yes = w.hi > 0.f && w > two_prod(un[m], qx) * S;
                 }
-                if (w > 0.0 && (double)up[m] * S * qx < w) {
+                if (yes) {
                     cur = m;
-                    path[++depth] = m;
+                    ++depth;
+                    if (lane == 0) path[depth] = m;
+                    rest = (uint64_t)kids[m][1] << 32 | kids[m][0];
                     k = 0;
-                    S = 1.0;
+                    S = {1.f, 0.f};
                     continue;
                 }
+                __syncwarp();
                 if (DRAFT) {
-                    // (a step's factor from S as it was for this child)
-                    int e = 0;
-                    if (S > 0.0) e = min(max(-ilogb(S), -120), 120);
-                    const double bs = ldexp(S, e);
-                    const float bh = (float)bs;
-                    steps[k] = {ldexpf(1.0f, e), bh, (float)(bs - (double)bh)};
+                    // S a power of two away from [1, 2)
+                    const int e = S.hi > 0.f ? min(max(127 - (int)(__float_as_uint(S.hi) >> 23), -120), 120) : 0;
+                    const float a = __uint_as_float((unsigned)(127 + e) << 23);
+                    if (lane == 0) steps[k] = {a, S.hi * a, S.lo * a};
                 } else {
-                    fallen[k] = x;
-                    S -= w;
+                    if (lane == 0) fallen[k] = x;
+                    S = S - w;
                 }
+                __syncwarp();
                 ++k;
-                if (DRAFT) {
-                    int sib = m + 1;
-                    while (sib < M && par[sib] != cur) ++sib;
-                    if (sib < M) {
-                        m = sib;
-                        state = 1;
-                        break;
-                    }
+                if (DRAFT && rest) {
+                    state = PASS_SUM;
+                    break;
                 }
             }
-            s_cur = cur;
-            s_fallen = k;
-            s_depth = depth;
-            s_state = state;
+            if (lane == 0) {
+                s_cur = cur;
+                s_fallen = k;
+                s_depth = depth;
+                s_state = state;
+            }
         }
         __syncthreads();
-        int state = s_state, k = s_fallen;
-        const int cur = s_cur;
+        state = s_state;
+        const int cur = s_cur, k = state == PASS_ROW ? 0 : s_fallen;
         const T* p_row = p_rows + (int64_t)cur * P.p_stride;
         const T* q_row = q_rows + (int64_t)cur * P.q_stride;
         // groups of 16 bytes, cut at the boundaries of p's row; q's only if they are its own too
@@ -222,195 +310,238 @@ __global__ void __launch_bounds__(kVerifyThreads) verify_tree_kernel(VerifyParam
         const bool q_aligned = DRAFT && (int)((reinterpret_cast<uintptr_t>(q_row) & 15) / sizeof(T)) == skew;
         const Row<T> pr(p_row, skew, V), qr(q_row, skew, V);
         const int groups = (V + skew + N - 1) / N;
+        // those that one load brings from each row, without a look at the row's ends
+        const int whole0 = skew ? 1 : 0, whole1 = DRAFT && !q_aligned ? 0 : (V + skew) / N;
         const int per_warp = ((groups + C * kVerifyWarps - 1) / (C * kVerifyWarps) + 31) & ~31;
-        double total = 0.0;
-        for (int attempt = 0;; ++attempt) {
-            if (state == 3) k = 0;
-            // what is left of group g
-            auto weights = [&](int g, const float (&pf)[N], const float (&qf)[N], F2 (&w)[N]) {
+        // ---- stage 0: every warp's run of the row.  Behind the last pass, the CTA
+        // that holds the token goes on to stage 1: the run that holds it, a part a
+        // warp, and the warp of that part to stage 2: the token
+        int begin = (rank * kVerifyWarps + warp) * per_warp, end = min(groups, begin + per_warp);
+        F2 t = {0.f, 0.f}, run = {0.f, 0.f};                // the draw; the sum of the tokens before `begin`
+        int token = -1;
+        bool done = false;
+        for (int stage = 0; stage < 3; ++stage) {
+            F2 acc = {0.f, 0.f}, odd = {0.f, 0.f};           // two, for their latency
+            bool found = false;
+#pragma unroll 1
+            for (int g = begin; g < end && !found; g += 32 * U) {
+                float hi[U][N], qf[U][N], lo[U][N];
+                // (the groups at the row's ends, and all where p and q lie differently,
+                // an element at a time)
+                if (g >= whole0 && min(g + 32 * U, end) <= whole1) {
 #pragma unroll
-                for (int i = 0; i < N; ++i) w[i] = {fmaxf(pf[i], 0.f), 0.f};
-                if (DRAFT) {
-                    for (int j = 0; j < k; ++j) {
-                        const VerifyStep s = steps[j];
-#pragma unroll
-                        for (int i = 0; i < N; ++i) w[i] = step_weight(w[i], fmaxf(qf[i], 0.f), s);
+                    for (int u = 0; u < U; ++u) {
+                        const int at = g + 32 * u + lane;
+                        uint4 x = {}, y = {};
+                        if (at < end) {
+                            x = __ldg(reinterpret_cast<const uint4*>(pr.at) + at);
+                            if (DRAFT && k > 0) y = __ldg(reinterpret_cast<const uint4*>(qr.at) + at);
+                        }
+                        widen(x, hi[u]);
+                        if (DRAFT) widen(y, qf[u]);
                     }
                 } else {
-                    const int first = N * g - skew;
-                    for (int j = 0; j < k; ++j) {
-                        const unsigned at = (unsigned)(fallen[j] - first);
-                        if (at < (unsigned)N) {
 #pragma unroll
-                            for (int i = 0; i < N; ++i)
-                                if (at == (unsigned)i) w[i] = {0.f, 0.f};
-                        }
+                    for (int u = 0; u < U; ++u) {
+                        const int at = g + 32 * u + lane;
+                        pr.load(at < end ? at : -1, hi[u]);
+                        if (DRAFT && k > 0) qr.load(at < end ? at : -1, qf[u]);
                     }
                 }
-            };
-            // the sum of a warp's run
-            auto run_begin = [&](int r, int w) { return (r * kVerifyWarps + w) * per_warp; };
-            const int g0 = run_begin(rank, warp), g1 = min(groups, g0 + per_warp);
-            F2 acc = {0.f, 0.f};
-            for (int g = g0; g < g1; g += 32 * UNROLL) {
-                float pf[UNROLL][N], qf[UNROLL][N];
+                // what is left of them
 #pragma unroll
-                for (int u = 0; u < UNROLL; ++u) {
-                    const int at = g + 32 * u + lane;
-#pragma unroll
-                    for (int i = 0; i < N; ++i) pf[u][i] = qf[u][i] = 0.f;
-                    if (at < g1) {
-                        pr.load(at, true, pf[u]);
-                        if (DRAFT && k > 0) qr.load(at, q_aligned, qf[u]);
-                    }
-                }
-#pragma unroll
-                for (int u = 0; u < UNROLL; ++u) {
-                    F2 w[N];
-                    weights(g + 32 * u + lane, pf[u], qf[u], w);
+                for (int u = 0; u < U; ++u)
 #pragma unroll
                     for (int i = 0; i < N; ++i) {
-                        const F2 s = two_sum(acc.hi, w[i].hi);
-                        acc.hi = s.hi;
-                        acc.lo = __fadd_rn(acc.lo, __fadd_rn(s.lo, w[i].lo));
+                        hi[u][i] = fmaxf(hi[u][i], 0.f);
+                        lo[u][i] = 0.f;
+                        if (DRAFT && k > 0) {
+                            qf[u][i] = fmaxf(qf[u][i], 0.f);
+                            const F2 w = first_step(hi[u][i], qf[u][i]);
+                            hi[u][i] = w.hi;
+                            lo[u][i] = w.lo;
+                        }
+                    }
+                if (DRAFT) {
+#pragma unroll 1
+                    for (int j = 1; j < k; ++j) {
+                        const VerifyStep s = steps[j];
+#pragma unroll
+                        for (int u = 0; u < U; ++u)
+#pragma unroll
+                            for (int i = 0; i < N; ++i) {
+                                const F2 w = step_weight({hi[u][i], lo[u][i]}, qf[u][i], s);
+                                hi[u][i] = w.hi;
+                                lo[u][i] = w.lo;
+                            }
+                    }
+                } else {
+#pragma unroll 1
+                    for (int j = 0; j < k; ++j) {
+                        // (the token's place among this lane's)
+                        const int at = fallen[j] - (N * (g + lane) - skew);
+#pragma unroll
+                        for (int u = 0; u < U; ++u)
+#pragma unroll
+                            for (int i = 0; i < N; ++i)
+                                if (at == 32 * N * u + i) hi[u][i] = 0.f;
+                    }
+                }
+                if (stage < 2) {
+#pragma unroll
+                    for (int u = 0; u < U; ++u)
+#pragma unroll
+                        for (int i = 0; i < N; ++i) {
+                            F2& to = i & 1 ? odd : acc;
+                            const F2 s = two_sum(to.hi, hi[u][i]);
+                            to = {s.hi, __fadd_rn(to.lo, DRAFT ? __fadd_rn(s.lo, lo[u][i]) : s.lo)};
+                        }
+                } else {
+                    // the token whose running sum exceeds t
+#pragma unroll
+                    for (int u = 0; u < U; ++u) {
+                        if (found) continue;
+                        F2 mine = {0.f, 0.f};
+#pragma unroll
+                        for (int i = 0; i < N; ++i) mine = mine + F2{hi[u][i], lo[u][i]};
+                        const F2 scan = warp_scan(mine, lane, 32);
+                        F2 upto = before_lane(scan, lane, run);
+                        int top = -1, pick = -1;
+#pragma unroll
+                        for (int i = 0; i < N; ++i) {
+                            upto = upto + F2{hi[u][i], lo[u][i]};
+                            if (hi[u][i] > 0.f) {
+                                top = N * (g + 32 * u + lane) - skew + i;
+                                if (pick < 0 && upto > t) pick = top;
+                            }
+                        }
+                        const unsigned over = __ballot_sync(0xffffffffu, pick >= 0);
+                        const unsigned some = __ballot_sync(0xffffffffu, top >= 0);
+                        // (none, by the roundings of the sums: the last that holds anything)
+                        if (over | some)
+                            token = __shfl_sync(0xffffffffu, over ? pick : top, over ? __ffs(over) - 1 : 31 - __clz(some));
+                        found = over != 0;
+                        run = run + shfl(scan, 31);
                     }
                 }
             }
-            double sum = (double)acc.hi + (double)acc.lo;
-#pragma unroll
-            for (int o = 16; o >= 1; o >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, o);
-            if (lane == 0) warp_sum[warp] = sum;
+            if (stage == 2) break;
+            // ---- the sums of the warps
+            acc = fast_two_sum(acc.hi, acc.lo) + fast_two_sum(odd.hi, odd.lo);
+#pragma unroll 1
+            for (int o = 16; o >= 1; o >>= 1)
+                acc = acc + F2{__shfl_xor_sync(0xffffffffu, acc.hi, o), __shfl_xor_sync(0xffffffffu, acc.lo, o)};
+            if (lane == 0) warp_sum[stage][warp] = acc;
             __syncthreads();
-            if (tid == 0) {
-                double s = 0.0;
-                for (int w = 0; w < kVerifyWarps; ++w) s += warp_sum[w];
-                cta_sum[passes & 1] = s;
+            if (stage == 1) {
+                const F2 part = lane < kVerifyWarps ? warp_sum[1][lane] : F2{0.f, 0.f};
+                const F2 scan = warp_scan(part, lane, kVerifyWarps);
+                const int at = locate(part, run + scan, t);
+                run = before_lane(scan, at, run);
+                if (warp != at) break;
+                continue;                                   // stage 2, of the same run
             }
-            // (two places in turn: a CTA that is a pass ahead does not overwrite
-            // a sum that another still reads)
-            if (C > 1) {
-                __syncthreads();
-                cluster_arrive();
-                cluster_wait();
-                if (tid < C) sums[tid] = dsmem_ld_f64(dsmem_addr(&cta_sum[passes & 1], tid));
-            } else if (tid == 0) {
-                sums[0] = cta_sum[passes & 1];
+            // ---- stage 0: the parts of the CTAs, every one to every one, in two
+            // places in turn (one that is a pass ahead does not overwrite what
+            // another still reads)
+            const int turn = passes & 1;
+            VerifyPart* got = parts[turn];
+            if (warp == 0) {
+                const F2 mine = lane < kVerifyWarps ? warp_sum[0][lane] : F2{0.f, 0.f};
+                const F2 upto = warp_scan(mine, lane, kVerifyWarps);
+                const F2 all = shfl(upto, kVerifyWarps - 1);
+                const int walk = cur | k << 8 | state << 16;
+                bool ok = true;
+                if (C == 1) {
+                    if (lane == 0) got[0] = {all, walk, 0};
+                    __syncwarp();
+                } else {
+                    if (lane == 0) mbar_expect_tx(smem_u32(&bars[turn]), C * (int)sizeof(VerifyPart));
+                    if (lane < C) send_part(dsmem_addr(&got[rank], lane), dsmem_addr(&bars[turn], lane), all, walk);
+                    ok = __all_sync(0xffffffffu, mbar_wait(smem_u32(&bars[turn]), (passes >> 1) & 1));
+                }
+                const F2 part = lane < C ? got[lane].sum : F2{0.f, 0.f};
+                ok &= !__any_sync(0xffffffffu, lane < C && got[lane].walk != walk);
+                const F2 scan = warp_scan(part, lane, kVerifyMaxCluster);
+                const F2 total = shfl(scan, kVerifyMaxCluster - 1);
+                S = total;
+                int next = state, in = -1;
+                if (!ok) {
+                    next = PASS_STOP;
+                } else if (state != PASS_SUM) {
+                    if (total.hi > 0.f && total.hi <= 3.4e38f) {
+                        // the draw: the CTA and the warp's run that hold the token
+                        // whose running sum exceeds t
+                        t = F2{un[0], 0.f} * total;
+                        const int owner = locate(part, scan, t);
+                        const F2 base = before_lane(scan, owner, {0.f, 0.f});
+                        in = locate(mine, base + upto, t);
+                        run = before_lane(upto, in, base);
+                        if (owner != rank) in = -1;
+                    } else if (state == PASS_DRAW && !(total.hi > 0.f)) {
+                        next = PASS_ROW;
+                    } else {
+                        next = PASS_ROW + PASS_STOP;        // no token to draw
+                    }
+                }
+                if (lane == 0) {
+                    s_t = t;
+                    s_base = run;
+                    s_warp = in;
+                    s_state = next;
+                }
             }
             ++passes;
             __syncthreads();
-            total = 0.0;
-            for (int r = 0; r < C; ++r) total += sums[r];
-            if (state == 2 && !(total > 0.0)) {
-                state = 3;
-                __syncthreads();                            // warp_sum and sums are written again
-                continue;
+            const int next = s_state;
+            if (next == PASS_STOP) {
+                if (rank == 0 && tid == 0) flag(FP8KV_DEV_BAD_TREE);
+                return;
             }
-            if (state == 1) break;
-            // ---- the draw: the CTA, the warp's run and the token whose running
-            // sum exceeds t
-            const double t = (double)up[0] * total;
-            const bool valid = total > 0.0 && total <= 1.7e308;
-            double before = 0.0;
-            int owner = 0;
-            for (int r = 0; r < C; ++r) {
-                if (sums[r] > 0.0) owner = r;
-                if (before + sums[r] > t) break;
-                if (r + 1 < C) before += sums[r];
-            }
+            valid = next != PASS_ROW + PASS_STOP;
+            done = !valid || (state != PASS_SUM && next == state);
+            state = next;
+            if (!done || s_warp < 0) break;
+            t = s_t;
+            run = s_base;
+            const int r0 = (rank * kVerifyWarps + s_warp) * per_warp, r1 = min(groups, r0 + per_warp);
+            const int share = ((r1 - r0 + kVerifyWarps - 1) / kVerifyWarps + 31) & ~31;
+            begin = min(r0 + warp * share, r1);
+            end = min(begin + share, r1);
+        }
+        if (done) {
             const int depth = s_depth;
-            if (rank == 0) {
-                for (int i = tid; i < M; i += kVerifyThreads) {
-                    P.path[(int64_t)b * M + i] = i <= depth ? path[i] : -1;
-                    if (i != depth || !valid)
-                        P.out_tokens[(int64_t)b * M + i] = i < depth ? tok[path[i + 1]] : -1;
-                }
+            if (token >= 0 && lane == 0) P.out_tokens[(int64_t)b * M + depth] = token;
+            if (rank == 0 && tid < M) {
+                const int64_t i = (int64_t)b * M + tid;
+                P.path[i] = tid <= depth ? path[tid] : -1;
+                if (tid != depth || !valid) P.out_tokens[i] = tid < depth ? tok[path[tid + 1]] : -1;
                 if (tid == 0) {
                     P.num_tokens[b] = valid ? depth + 1 : depth;
                     if (!valid) flag(FP8KV_DEV_BAD_PROBS);
                 }
             }
-            if (valid && rank == owner) {
-                double base = 0.0;
-                for (int r = 0; r < owner; ++r) base += sums[r];
-                int w_at = 0;
-                double w_base = base;
-                for (int w = 0; w < kVerifyWarps; ++w) {
-                    if (warp_sum[w] > 0.0) {
-                        w_at = w;
-                        w_base = base;
-                    }
-                    if (base + warp_sum[w] > t) break;
-                    base += warp_sum[w];
-                }
-                if (warp == w_at) {
-                    int last = -1, found = -1;                  // tokens
-                    double run = w_base;
-                    for (int g = g0; g < g1 && found < 0; g += 32) {
-                        float pf[N], qf[N];
-                        F2 w[N];
-#pragma unroll
-                        for (int i = 0; i < N; ++i) pf[i] = qf[i] = 0.f;
-                        if (g + lane < g1) {
-                            pr.load(g + lane, true, pf);
-                            if (DRAFT && k > 0) qr.load(g + lane, q_aligned, qf);
-                        }
-                        weights(g + lane, pf, qf, w);
-                        double mine = 0.0;
-                        int top = -1;
-#pragma unroll
-                        for (int i = 0; i < N; ++i) {
-                            mine += (double)w[i].hi + (double)w[i].lo;
-                            if (w[i].hi > 0.f) top = N * (g + lane) - skew + i;
-                        }
-                        double incl = mine;
-#pragma unroll
-                        for (int o = 1; o < 32; o <<= 1) {
-                            const double x = __shfl_up_sync(0xffffffffu, incl, o);
-                            if (lane >= o) incl += x;
-                        }
-                        const uint32_t has = __ballot_sync(0xffffffffu, top >= 0);
-                        const uint32_t over = __ballot_sync(0xffffffffu, top >= 0 && run + incl > t);
-                        if (over) {
-                            const int l = __ffs(over) - 1;
-                            int pick = top;
-                            double at = run + incl - mine;
-#pragma unroll
-                            for (int i = N - 1; i >= 0; --i) {
-                                // the first element past t: the last one that the loop, backwards, finds past it
-                                double upto = at;
-#pragma unroll
-                                for (int j = 0; j <= i; ++j) upto += (double)w[j].hi + (double)w[j].lo;
-                                if (w[i].hi > 0.f && upto > t) pick = N * (g + lane) - skew + i;
-                            }
-                            found = __shfl_sync(0xffffffffu, pick, l);
-                        } else if (has) {
-                            last = __shfl_sync(0xffffffffu, top, 31 - __clz(has));
-                        }
-                        run += __shfl_sync(0xffffffffu, incl, 31);
-                    }
-                    // (a running sum that its roundings leave below t at the end of
-                    // the run: its last token with a weight)
-                    if (lane == 0) P.out_tokens[(int64_t)b * M + depth] = found >= 0 ? found : last;
-                }
-            }
             break;
         }
-        if (state != 1) break;
-        if (tid == 0) S = total;
-        // thread 0 goes on with the walk; the sums are written again behind its barrier
-        __syncthreads();
-    }
-    if (C > 1) {
-        // no shared memory goes before every CTA has read the sums
-        __syncwarp();
-        cluster_arrive();
-        cluster_wait();
+        __syncthreads();                                    // before warp 0 writes the walk's state again
     }
 }
 
 }  // namespace fp8kv
 
 using namespace fp8kv;
+
+// Opt in to clusters of 16, once per device (as opt_in_smem).
+static cudaError_t allow_cluster16(std::atomic<uint64_t>& done, const void* kernel) {
+    int dev = 0;
+    cudaError_t e = cudaGetDevice(&dev);
+    if (e != cudaSuccess) return e;
+    const uint64_t bit = dev < 64 ? 1ull << dev : 0;
+    if (done.load(std::memory_order_relaxed) & bit) return cudaSuccess;
+    e = cudaFuncSetAttribute(kernel, cudaFuncAttributeNonPortableClusterSizeAllowed, 1);
+    if (e == cudaSuccess) done.fetch_or(bit, std::memory_order_relaxed);
+    return e;
+}
 
 extern "C" int fp8kv_verify_tree(const void* target_probs, int64_t target_stride, const void* draft_probs,
                                  int64_t draft_stride, int prob_dtype, const int32_t* tokens, const int32_t* parents,
@@ -441,13 +572,21 @@ extern "C" int fp8kv_verify_tree(const void* target_probs, int64_t target_stride
     P.B = B;
     P.M = M;
     P.V = V;
-    // CTAs a sequence: as many as keep the SMs busy, each with a few thousand tokens at least
+    // CTAs a sequence: clusters of 16 (not portable, but one fits every GPC) down to 1
+    // as the batch grows, with some 500 CTAs, or half of that without a drafter's
+    // rows, and a few thousand tokens each.  (131072 tokens, chosen drafts: 6.2 us in
+    // 16 CTAs, 7.2 in 8, 16.6 in one; 64 trees of 100003, drawn: 44 us in 8 CTAs each,
+    // 57 in 4, 50 in 16.)
+    const int most = draft_probs ? 512 : 256;
     int c = 1;
-    while (c < kVerifyMaxCluster && (int64_t)B * c * 2 <= 2 * num_sms() && V / (2 * c) >= 2048) c *= 2;
+    while (c < kVerifyMaxCluster && (int64_t)B * c * 2 <= most && V / (2 * c) >= 2048) c *= 2;
     if ((int64_t)B * c > 0x7fffffff) return FP8KV_ERR_UNSUPPORTED;
     P.cluster = c;
     auto kern = f32 ? (draft_probs ? verify_tree_kernel<float, true> : verify_tree_kernel<float, false>)
                     : (draft_probs ? verify_tree_kernel<uint16_t, true> : verify_tree_kernel<uint16_t, false>);
+    static std::atomic<uint64_t> done[2][2];
+    if (c > 8 && allow_cluster16(done[f32][draft_probs != nullptr], (const void*)kern) != cudaSuccess)
+        return (cudaGetLastError(), FP8KV_ERR_CUDA);
     const cudaError_t e =
         launch_pdl_cluster(kern, dim3((unsigned)(B * c)), dim3(kVerifyThreads), 0, (cudaStream_t)stream, c, P);
     return e == cudaSuccess ? FP8KV_OK : (cudaGetLastError(), FP8KV_ERR_CUDA);
