@@ -1040,15 +1040,21 @@ static int make_plan(int B, int M, int Hq, int Hkv, int D, int PS, int max_seq_l
 struct Int4Cut {
     int split_pages, num_splits, warps;
     bool cluster, lpt;
+    float us;                   // the estimate
 };
-static Int4Cut int4_cut(const Plan& plan, bool tc, bool one_tile, bool given, int B, int64_t units, int PS) {
+// A tree's call of several row tiles is cut by the same rule over the other caches
+// too, with its kernel's terms; `even`: a window leaves every sequence the same keys.
+static Int4Cut int4_cut(const Plan& plan, bool tc, bool one_tile, bool given, int B, int64_t units, int PS,
+                        float tc_cta = 7.f, float tc_tile = 1.1f, bool even = false) {
     const int sms = num_sms(), tile = tc_tile_tokens() / PS;
-    Int4Cut best = {plan.split_pages, plan.num_splits, 12, false, false};
+    Int4Cut best = {plan.split_pages, plan.num_splits, 12, false, false, INFINITY};
     // a single round of keys: nothing to choose
-    if (plan.num_splits == 1 && units <= sms && plan.pages * PS <= (tc ? 128 : 384)) return best;
+    if (plan.num_splits == 1 && units <= sms && plan.pages * PS <= (tc ? 128 : 384)) {
+        best.us = tc ? tc_cta + tc_tile : 7.f;
+        return best;
+    }
     int clusters[9];
     if (one_tile) int4_clusters(clusters);
-    float best_us = INFINITY;
     auto look = [&](int64_t want, int warps, bool cluster) {
         int ns = plan.num_splits, sp = plan.split_pages;
         if (!given) {
@@ -1058,18 +1064,15 @@ static Int4Cut int4_cut(const Plan& plan, bool tc, bool one_tile, bool given, in
         if (cluster ? ns < 2 || ns > 8 || units > clusters[ns] : ns > plan.num_splits) return;
         const float keys = (float)std::min(sp, plan.pages) * PS;
         const float rounds = ceilf(keys / (tc ? 128 : 32 * warps));
-        const float one = tc ? 7.f + 1.1f * rounds : 5.f + 2.f * rounds, alone = warps == 4 ? 5.f + rounds : one;
+        const float one = tc ? tc_cta + tc_tile * rounds : 5.f + 2.f * rounds, alone = warps == 4 ? 5.f + rounds : one;
         const int64_t slots = warps == 4 ? 3 * sms : sms, n = units * ns, rest = n % slots;
         const bool lpt = B > 1 && one_tile && plan.num_splits > 1 && n > slots && sp % tile == 0 && n <= INT32_MAX;
         const float tail = rest == 0 ? 0.f : (rest <= sms / 2 ? alone : one);
         // (three CTAs of an SM are not in step: no whole waves)
         const float equal = warps == 4 && n > slots ? (float)n / slots * one : (float)(n / slots) * one + tail;
-        const float spread = B > 1 ? std::max(n > slots ? one : tail, 0.5f * n * one / slots + 0.5f * one) : equal;
+        const float spread = B > 1 && !even ? std::max(n > slots ? one : tail, 0.5f * n * one / slots + 0.5f * one) : equal;
         const float us = 0.5f * (equal + spread) + (ns > 1 ? (!cluster ? 2.5f : tc ? 1.2f : 0.7f) : 0.f) + (lpt ? 2.3f : 0.f);
-        if (us < best_us) {
-            best_us = us;
-            best = {sp, ns, warps, cluster, lpt};
-        }
+        if (us < best.us) best = {sp, ns, warps, cluster, lpt, us};
     };
     // nothing is gained between whole waves of CTAs
     for (int warps : {12, 4}) {
@@ -1082,6 +1085,26 @@ static Int4Cut int4_cut(const Plan& plan, bool tc, bool one_tile, bool given, in
     }
     if (one_tile)
         for (int ns = 2; ns <= 8 && units * ns <= sms; ++ns) look(ns, 12, true);
+    return best;
+}
+
+// An INT4 tree's call of RT > 1 row tiles, `units` (sequence, KV head) pairs: also how
+// many row tiles a CTA takes one after another.  A further row tile costs 5 us beside
+// its keys (the way from its Q over its first products to its output), a further wave
+// of CTAs 7: 128 pairs, 543 keys: 2 row tiles 25 us against 29, 3 33 against 38.5, 5
+// 55 against 74.
+static Int4Cut tree_cut(const Plan& plan, bool given, int B, int64_t units, int RT, int PS, float cta, float tile,
+                        bool even, int* row_loop) {
+    Int4Cut best = {};
+    for (int n = 1; n <= RT; ++n) {
+        if (n > 1 && ceil_div(RT, n) == ceil_div(RT, n - 1)) continue;     // no fewer CTAs than with less each
+        const Int4Cut cut = int4_cut(plan, true, false, given, B, units * ceil_div(RT, n), PS,
+                                     cta + 5.f * (n - 1), tile * n, even);
+        if (n == 1 || cut.us < best.us) {
+            best = cut;
+            *row_loop = n;
+        }
+    }
     return best;
 }
 
@@ -1239,7 +1262,9 @@ static int attention_call(const void* k_new, const void* v_new, const void* q, c
     P.page_size = page_size;
     P.max_seq_len = max_seq_len;
     P.tree = tree_mask;
+    P.row_loop = 1;
 
+    const bool even = window_left >= 0 && plan.pages < ceil_div(max_seq_len, page_size);
     cudaStream_t s = (cudaStream_t)stream;
     if (int4) {
         P.k_cache = (uint8_t*)k_cache;
@@ -1263,7 +1288,10 @@ static int attention_call(const void* k_new, const void* v_new, const void* q, c
             if (rc) return rc;
         }
         const int64_t units = (int64_t)B * Hkv * (tc ? row_tiles(M, Hq, Hkv) : P.NT);
-        const Int4Cut cut = int4_cut(plan, tc, one_tile, split_tokens > 0, B, units, page_size);
+        const Int4Cut cut = tree && tc && !one_tile
+                                ? tree_cut(plan, split_tokens > 0, B, (int64_t)B * Hkv, row_tiles(M, Hq, Hkv),
+                                           page_size, 7.f, 1.1f, even, &P.row_loop)
+                                : int4_cut(plan, tc, one_tile, split_tokens > 0, B, units, page_size);
         P.split_pages = cut.split_pages;
         P.num_splits = cut.num_splits;
         P.KW = cut.warps;
@@ -1301,6 +1329,14 @@ static int attention_call(const void* k_new, const void* v_new, const void* q, c
     }
     const bool bf16_tc = tree && !fp8 && tc_rows(M, Hq, Hkv);
     const int RT = use_tc || bf16_tc ? row_tiles(M, Hq, Hkv) : 1;
+    if (tree && RT > 1) {
+        const Int4Cut cut = int4_cut(plan, true, false, split_tokens > 0, B, (int64_t)B * Hkv * RT, page_size,
+                                     fp8 ? 6.f : 5.f, fp8 ? 1.2f : 0.9f, even);
+        plan.split_pages = P.split_pages = cut.split_pages;
+        plan.num_splits = P.num_splits = cut.num_splits;
+        plan.split_tokens = cut.split_pages * page_size;
+        if (P.ws_o) P.ws_ml = P.ws_o + rows * plan.num_splits * 128;
+    }
     // one sequence in at most 8 partitions and one row tile: the partitions
     // of a KV head run as one thread-block cluster and combine in distributed
     // shared memory

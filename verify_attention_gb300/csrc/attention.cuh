@@ -39,8 +39,10 @@ struct AttnParams {
     uint8_t* k_cache;
     uint8_t* v_cache;
     int num_pages;
-    // tree calls (kernels with TREE): the nodes that each row sees, [B][M] words
+    // tree calls (kernels with TREE): the nodes that each row sees, [B][M] words, and
+    // the row tiles that a CTA of a tcgen05 kernel takes one after another
     const uint64_t* tree;
+    int row_loop;
 };
 
 // What row m of sequence b of a tree call sees: node i where bit i is set, and

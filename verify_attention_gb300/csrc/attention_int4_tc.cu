@@ -62,7 +62,7 @@ constexpr int OFF_VS = OFF_KS + NK * kInt4ScaleBytes;
 constexpr int STAGE_BYTES = OFF_VS + NK * kInt4ScaleBytes;
 constexpr int KBUFS = 2, VBUFS = 2;                     // widened tiles
 constexpr int BUF = NK * 256, HALF = BUF / 2;           // two blocks of 128 keys x 64 dims (128-byte swizzled)
-constexpr int XCH_BYTES = 2 * 128 * 8;                  // (max, sum) of [half][row]
+constexpr int XCH_BYTES = 2 * 128 * 8 + 2 * 128 * 4;    // (max, sum) of [half][row]; of q, its maximum
 constexpr int SMEM = (KBUFS + VBUFS) * BUF + STAGES * STAGE_BYTES + XCH_BYTES + 1024 + 512;
 constexpr int EPI_STRIDE = 144;                         // staged half row (128 bytes), padded against bank conflicts
 constexpr int kMaxCluster = 8;
@@ -90,7 +90,8 @@ enum {
     B_IDLE = B_Q_READY + 1,
     B_PAIR = B_IDLE + 1,                                // per TMEM lane quarter: its two softmax warps
     B_APP = B_PAIR + 4,                                 // new tokens written over a staged tile
-    B_COUNT = B_APP + 1
+    B_O_FREE = B_APP + 1,                               // O of a row tile read
+    B_COUNT = B_O_FREE + 1
 };
 static_assert(B_COUNT * 8 + 16 <= 512, "barrier area");
 
@@ -118,7 +119,10 @@ __device__ __forceinline__ void widen_chunk(const uint32_t (&at)[4], uint4 codes
 }
 
 // CL: the partitions are a cluster.  TREE: what a row sees among the last M keys is
-// given by its mask word, so every row tile spans the keys to the end.
+// given by its mask word, so every row tile spans the same keys, to the end; a CTA
+// takes P.row_loop row tiles one after another, its loads and products running on
+// from one to the next (16 sequences, 288 rows, 543 keys: 33.1 us, a CTA per row
+// tile 38.5).
 template <int PS, bool CL, bool TREE>
 __global__ void __launch_bounds__(THREADS, 1) attention_int4_tc_kernel(AttnParams P) {
     extern __shared__ uint8_t smem_raw[];
@@ -131,9 +135,11 @@ __global__ void __launch_bounds__(THREADS, 1) attention_int4_tc_kernel(AttnParam
     uint32_t* tmem_slot = (uint32_t*)(bars + B_COUNT);
     auto bar = [&](int i) { return smem_u32(&bars[i]); };
     const int RT = (P.R + 127) >> 7;
-    const int rt = blockIdx.y % RT;
-    int split = blockIdx.x, hk = blockIdx.y / RT, b = blockIdx.z;
-    const int R0 = rt * 128, RL = min(128, P.R - R0);
+    // this CTA's row tiles rt .. rt + n_rt - 1
+    const int RG = TREE ? (RT + P.row_loop - 1) / P.row_loop : RT;
+    const int rt = TREE ? blockIdx.y % RG * P.row_loop : blockIdx.y % RT, n_rt = TREE ? min(P.row_loop, RT - rt) : 1;
+    int split = blockIdx.x, hk = blockIdx.y / RG, b = blockIdx.z;
+    const int R0 = rt * 128, RL = min(128, P.R - R0);      // the first one's rows
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     pdl_launch_dependents();
     if (threadIdx.x == 0) {
@@ -144,6 +150,7 @@ __global__ void __launch_bounds__(THREADS, 1) attention_int4_tc_kernel(AttnParam
             if (i == B_Q_READY) count = 8;
             if (i >= B_IDLE && i < B_APP) count = 2;
             if (i == B_APP) count = CONV_WARPS;
+            if (i == B_O_FREE) count = 8;
             mbar_init(bar(i), count);
         }
         fence_barrier_init();
@@ -216,12 +223,17 @@ __global__ void __launch_bounds__(THREADS, 1) attention_int4_tc_kernel(AttnParam
     const bool appends = P.k_new && app_lo < app_hi;
     const int app_t0 = appends ? (app_lo - k_begin) / NK : 1 << 30, app_t1 = appends ? (app_hi - 1 - k_begin) / NK : -1;
     bool ok = true;
+    // the work: the key tiles of each row tile, item it = (row tile) n_tiles + (key
+    // tile); rings and barriers go by the item
+    const int n_items = n_rt * n_tiles;
 
     if (!run) {
         // no keys of this sequence fall in this partition (or bad input)
     } else if (warp >= 4 && warp < 12) {
         asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(REGS_SOFTMAX));
         // ------------------------------------------------------------ softmax
+        for (int ri = 0; ri < n_rt; ++ri) {
+        const int R0 = (rt + ri) * 128, RL = min(128, P.R - R0), it0 = ri * n_tiles;
         const int wq = warp & 3, half = (warp - 4) >> 2;
         const int r = wq * 32 + lane;
         const bool active = wq * 32 < RL;                   // the quarter holds at least one real row
@@ -253,11 +265,12 @@ __global__ void __launch_bounds__(THREADS, 1) attention_int4_tc_kernel(AttnParam
             uint32_t am = 0;
 #pragma unroll
             for (int u = 0; u < 32; ++u) am = max_bf16x2(am, qh[u] & 0x7fff7fffu);
-            xch[half * 128 + r] = fmaxf(bf16_lo(am), bf16_hi(am));
+            float* qmax = xch + 2 * 2 * 128;
+            qmax[half * 128 + r] = fmaxf(bf16_lo(am), bf16_hi(am));
             __syncwarp();
             if (lane == 0) mbar_arrive(bar(B_PAIR + wq));
-            ok = __all_sync(0xffffffffu, mbar_wait(bar(B_PAIR + wq), 0));
-            const float amax = fmaxf(xch[r], xch[128 + r]);
+            ok = __all_sync(0xffffffffu, ok && mbar_wait(bar(B_PAIR + wq), 0));
+            const float amax = fmaxf(qmax[r], qmax[128 + r]);
             int e = 4;
             const uint32_t ab = __float_as_uint(amax);
             if (amax > 0.f && ((ab >> 23) & 0xff) != 0xff) {
@@ -293,13 +306,23 @@ __global__ void __launch_bounds__(THREADS, 1) attention_int4_tc_kernel(AttnParam
             pmax = max(pmax, __shfl_xor_sync(0xffffffffu, pmax, off));
             lomin = min(lomin, __shfl_xor_sync(0xffffffffu, lomin, off));
         }
-        if (TREE) pmax = L - 1;
+        if (TREE) {
+            pmax = L - 1;
+            if (ri + 1 < n_rt && R0 + 128 + r < P.R) {
+                // the next row tile's q (and mask word) on their way
+                const int rn = R0 + 128 + r, mn = rn / P.G;
+                const uint16_t* at = P.q + (((int64_t)b * P.M + mn) * P.Hq + hk * P.G + rn % P.G) * 128 + 64 * half;
+                asm volatile("prefetch.global.L1 [%0];" ::"l"(at));
+                asm volatile("prefetch.global.L1 [%0];" ::"l"(P.tree + (int64_t)b * P.M + mn));
+            }
+        }
         // this half's maximum and sum
         float m_run = -INFINITY, l_run = 0.f;
         const uint32_t o_col = lane_base + TM_O + 128 * half;
         for (int t = 0; t < n_tiles && ok; ++t) {
-            const uint32_t s_col = lane_base + TM_S + 64 * ((2 * t + half) % 3);
-            ok = __all_sync(0xffffffffu, mbar_wait(bar(B_S + 3 * half + t % 3), (t / 3) & 1));
+            const int it = it0 + t;
+            const uint32_t s_col = lane_base + TM_S + 64 * ((2 * it + half) % 3);
+            ok = __all_sync(0xffffffffu, mbar_wait(bar(B_S + 3 * half + it % 3), (it / 3) & 1));
             if (!ok) break;
             fence_after();
             const int k0 = k_begin + t * NK + 64 * half;    // first key of this half
@@ -337,7 +360,7 @@ __global__ void __launch_bounds__(THREADS, 1) attention_int4_tc_kernel(AttnParam
                 const bool rescale = (m_run != -INFINITY) && (tmax > m_run + GROW);
                 if (__any_sync(0xffffffffu, rescale)) {
                     // O holds P.V up to tile t - 1 (t > 0: m_run was set): wait for it
-                    ok = __all_sync(0xffffffffu, mbar_wait(bar(B_PV + half), (t - 1) & 1));
+                    ok = __all_sync(0xffffffffu, mbar_wait(bar(B_PV + half), (it - 1) & 1));
                     if (!ok) break;
                     fence_after();
                     const float alpha = rescale ? ex2(m_run - tmax) : 1.0f;
@@ -384,12 +407,12 @@ __global__ void __launch_bounds__(THREADS, 1) attention_int4_tc_kernel(AttnParam
             tmem_wait_st();
             fence_before();
             __syncwarp();
-            if (lane == 0) mbar_arrive(bar(B_P + 3 * half + t % 3));
+            if (lane == 0) mbar_arrive(bar(B_P + 3 * half + it % 3));
         }
         // ------------------------------------------------------------ epilogue
         // both halves' O and (max, sum); this thread merges 64 dims of its row
         for (int h = 0; h < 2; ++h)
-            if (ok) ok = mbar_wait(bar(B_O + h), 0);
+            if (ok) ok = mbar_wait(bar(B_O + h), ri & 1);
         const bool combine = CL && nsplit_b > 1;
         float2* ml = (float2*)xch;
         float2* ml_all = (float2*)(kbuf + 2 * 128 * EPI_STRIDE);    // (max, sum) of the staged rows
@@ -412,15 +435,18 @@ __global__ void __launch_bounds__(THREADS, 1) attention_int4_tc_kernel(AttnParam
             const float fa = wa * f, fz = wz * f;
             const bool zero = TREE && direct && (word == 0 || l_tot == 0.f);
             // the half row goes through shared memory (the widened tiles are
-            // free) to one bulk copy
+            // free) to one bulk copy; straight from the registers where a CTA takes
+            // several row tiles, as the next one's keys are being widened
             uint8_t* row_stage = kbuf + (half * 128 + r) * EPI_STRIDE;
+            uint16_t* row_out = (direct ? P.out + row_idx * 128 : (uint16_t*)P.ws_o + (row_idx * P.num_splits + split) * 128) + 64 * half;
 #pragma unroll 1
             for (int c = 0; c < 64; c += 32) {
                 uint32_t oa[32], oz[32];
                 tmem_ld_x32(lane_base + TM_O + 64 * half + c, oa);
                 tmem_ld_x32(lane_base + TM_O + 128 + 64 * half + c, oz);
                 tmem_wait_ld();
-                uint4* dst = (uint4*)(row_stage + c * 2);
+                uint4* dst = (uint4*)(TREE && n_rt > 1 ? (uint8_t*)(row_out + c) : row_stage + c * 2);
+                if (TREE && n_rt > 1 && r >= RL) continue;
 #pragma unroll
                 for (int v4 = 0; v4 < 4; ++v4) {
                     float x[8];
@@ -438,18 +464,25 @@ __global__ void __launch_bounds__(THREADS, 1) attention_int4_tc_kernel(AttnParam
                 // stays here: the cluster's CTAs read it below
                 if (half == 0) ml_all[r] = make_float2(m_tot, l_tot);
             } else if (r < RL) {
-                fence_proxy_async();        // the staged row, written by this thread, to the bulk copy
-                if (direct)
-                    bulk_store(P.out + row_idx * 128 + 64 * half, smem_u32(row_stage), 128);
-                else
-                    bulk_store((uint16_t*)P.ws_o + (row_idx * P.num_splits + split) * 128 + 64 * half,
-                               smem_u32(row_stage), 128);
-                bulk_commit();
-                bulk_wait_read();
+                if (!TREE || n_rt == 1) {
+                    fence_proxy_async();    // the staged row, written by this thread, to the bulk copy
+                    bulk_store(row_out, smem_u32(row_stage), 128);
+                    bulk_commit();
+                    bulk_wait_read();
+                }
                 if (!direct && half == 0)
                     *(float2*)(P.ws_ml + (row_idx * P.num_splits + split) * 2) = make_float2(m_tot, l_tot);
             }
         }
+        if (TREE && ri + 1 < n_rt) {
+            // O and Q are free for the next row tile (the pair barrier above: both
+            // halves' last S, hence all of Q's readers, are done)
+            fence_before();
+            __syncwarp();
+            if (lane == 0) mbar_arrive(bar(B_O_FREE));
+            if (ok) continue;
+        }
+        // (behind the last row tile)
         if (CL) {
             __syncwarp();
             cluster_arrive();
@@ -490,6 +523,8 @@ __global__ void __launch_bounds__(THREADS, 1) attention_int4_tc_kernel(AttnParam
                 *(uint4*)(P.out + idx * 128 + 8 * c) = o4;
             }
         }
+        break;
+        }
     } else {
         asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(REGS_SERVICE));
         if (warp == 0) {
@@ -503,10 +538,11 @@ __global__ void __launch_bounds__(THREADS, 1) attention_int4_tc_kernel(AttnParam
             const uint32_t off = (kind == 0 ? 0 : kind == 1 ? OFF_V : kind == 2 ? OFF_KS : OFF_VS) + p * bytes;
             int issued = 0;
             int next = p < PPT && p < n_pages ? (page_begin + p == guess_at ? guess : bt[p]) : -1;
-            for (int t = 0; t < n_tiles; ++t) {
-                const int s = t % STAGES, use = t / STAGES, page = next, at = t * PPT + p;
+            for (int it = 0, t = 0; it < n_items; ++it, t = t + 1 == n_tiles ? 0 : t + 1) {
+                const int s = it % STAGES, use = it / STAGES, page = next, at = t * PPT + p;
                 const bool mine = p < PPT && at < n_pages;
-                next = p < PPT && at + PPT < n_pages ? bt[at + PPT] : -1;
+                const int at2 = t + 1 == n_tiles ? p : at + PPT;        // (the first tile again, for the next rows)
+                next = p < PPT && at2 < n_pages ? bt[at2] : -1;
                 if (use > 0) ok = mbar_wait(bar(B_STG_EMPTY + s), (use - 1) & 1);
                 if (!__all_sync(0xffffffffu, ok)) break;
                 uint8_t* dst = stg + s * STAGE_BYTES + off;
@@ -527,7 +563,7 @@ __global__ void __launch_bounds__(THREADS, 1) attention_int4_tc_kernel(AttnParam
                               cache + ((int64_t)page * P.Hkv + hk) * (PS * kInt4RowBytes) +
                                   (kind < 2 ? 0 : PS * kInt4CodeBytes),
                               bytes, bar(B_STG_FULL + s));
-                issued = t + 1;
+                issued = it + 1;
             }
             // never leave with copies into this CTA's shared memory in flight
             for (int t = max(0, issued - STAGES); t < issued; ++t) mbar_wait(bar(B_STG_FULL + t % STAGES), (t / STAGES) & 1);
@@ -536,13 +572,18 @@ __global__ void __launch_bounds__(THREADS, 1) attention_int4_tc_kernel(AttnParam
             // ------------------------------------------------------ MMA issue
             constexpr uint32_t ID_QK = idesc(128, NK / 2, false), ID_PV = idesc(128, 128, true);
             const bool leader = elect_one();
-            const int n_half = 2 * n_tiles;
+            const int n_half = 2 * n_items;
             if (warp == 1) {
                 // S(u) = Q K^T; the K buffer is free once the second half has read it
                 const uint32_t k_lo = desc_lo(smem_u32(kbuf), 16);
-                ok = mbar_wait(bar(B_Q_READY), 0);
-                for (int u = 0; u < n_half; ++u) {
-                    const int t = u >> 1, h = u & 1, tb = t % KBUFS, sb = u % 3;
+                ok = true;
+                for (int u = 0, q_at = 0, q_phase = 0; u < n_half; ++u) {
+                    const int t = u >> 1, h = u & 1, tb = t % KBUFS, sb = u % 3;    // (t: the item)
+                    if (u == q_at) {                        // a row tile's first half
+                        ok = mbar_wait(bar(B_Q_READY), q_phase);
+                        q_at += 2 * n_tiles;
+                        q_phase ^= 1;
+                    }
                     if (ok && h == 0) ok = mbar_wait(bar(B_K_FULL + tb), (t / KBUFS) & 1);
                     if (ok && u >= 3) ok = mbar_wait(bar(B_S_EMPTY + sb), (u / 3 - 1) & 1);
                     ok = __all_sync(0xffffffffu, ok);
@@ -562,9 +603,10 @@ __global__ void __launch_bounds__(THREADS, 1) attention_int4_tc_kernel(AttnParam
             } else {
                 // O += P(u) V
                 const uint32_t v_lo = desc_lo(smem_u32(vbuf), HALF);
-                for (int u = 0; u < n_half; ++u) {
-                    const int t = u >> 1, h = u & 1, vb = t % VBUFS, sb = u % 3;
-                    if (h == 0) ok = mbar_wait(bar(B_V_FULL + vb), (t / VBUFS) & 1);
+                for (int u = 0, tile = 0, ri = 0; u < n_half; ++u) {
+                    const int t = u >> 1, h = u & 1, vb = t % VBUFS, sb = u % 3;    // (t: the item, tile: its key tile)
+                    if (TREE && h == 0 && tile == 0 && ri > 0) ok = mbar_wait(bar(B_O_FREE), (ri - 1) & 1);
+                    if (h == 0) ok = ok && mbar_wait(bar(B_V_FULL + vb), (t / VBUFS) & 1);
                     if (ok) ok = mbar_wait(bar(B_P + 3 * h + t % 3), (t / 3) & 1);
                     ok = __all_sync(0xffffffffu, ok);
                     if (!ok) break;
@@ -573,13 +615,17 @@ __global__ void __launch_bounds__(THREADS, 1) attention_int4_tc_kernel(AttnParam
 #pragma unroll
                         for (int kk = 0; kk < 4; ++kk)
                             mma_ts(tmem + TM_O + 128 * h, tmem + TM_S + 64 * sb + 8 * kk,
-                                   v_lo + ((vb * BUF + h * (64 * 128) + kk * 2048) >> 4), ID_PV, t > 0 || kk > 0);
+                                   v_lo + ((vb * BUF + h * (64 * 128) + kk * 2048) >> 4), ID_PV, tile > 0 || kk > 0);
                         mma_commit(bar(B_PV + h));
                         mma_commit(bar(B_S_EMPTY + sb));
                         if (h == 1) mma_commit(bar(B_V_EMPTY + vb));
-                        if (t == n_tiles - 1) mma_commit(bar(B_O + h));
+                        if (tile == n_tiles - 1) mma_commit(bar(B_O + h));
                     }
                     __syncwarp();
+                    if (h == 1 && ++tile == n_tiles) {
+                        tile = 0;
+                        ++ri;
+                    }
                 }
             }
             // nothing the tensor cores still run may outlive the TMEM allocation
@@ -611,8 +657,9 @@ __global__ void __launch_bounds__(THREADS, 1) attention_int4_tc_kernel(AttnParam
                     ksc[u] = *(const uint16_t*)(src + OFF_KS + r * 8 + 2 * cc);
                 }
             };
-            auto load_v = [&](int t) {
-                const uint8_t* src = stg + (t % STAGES) * STAGE_BYTES;
+            // (of item it, key tile t)
+            auto load_v = [&](int it, int t) {
+                const uint8_t* src = stg + (it % STAGES) * STAGE_BYTES;
                 // keys outside every row's range get V scale 0: whatever their
                 // bytes are, zeros reach the output
                 const int k0 = k_begin + t * NK;
@@ -657,11 +704,11 @@ __global__ void __launch_bounds__(THREADS, 1) attention_int4_tc_kernel(AttnParam
             if (ok && app_t0 == 0) patch(0);
             if (ok) {
                 load_k(0);
-                load_v(0);
+                load_v(0, 0);
                 __syncwarp();
                 if (lane == 0) mbar_arrive(bar(B_STG_EMPTY));           // the stage is in registers
             }
-            for (int t = 0; t < n_tiles && ok; ++t) {
+            for (int t = 0, tile = 0; t < n_items && ok; ++t) {         // (t: the item, tile: its key tile)
                 // K of this tile, then the next stage's K on its way while V of
                 // this tile is widened
                 const int tb = t % KBUFS, vb = t % VBUFS, s1 = (t + 1) % STAGES;
@@ -675,7 +722,8 @@ __global__ void __launch_bounds__(THREADS, 1) attention_int4_tc_kernel(AttnParam
                 fence_proxy_async();
                 __syncwarp();
                 if (lane == 0) mbar_arrive(bar(B_K_FULL + tb));
-                if (t + 1 < n_tiles) {
+                tile = tile + 1 == n_tiles ? 0 : tile + 1;
+                if (t + 1 < n_items) {
                     ok = __all_sync(0xffffffffu, mbar_wait(bar(B_STG_FULL + s1), ((t + 1) / STAGES) & 1));
                     if (ok && t + 1 >= app_t0 && t + 1 <= app_t1) patch(t + 1);
                     if (!ok) break;
@@ -690,8 +738,8 @@ __global__ void __launch_bounds__(THREADS, 1) attention_int4_tc_kernel(AttnParam
                 fence_proxy_async();
                 __syncwarp();
                 if (lane == 0) mbar_arrive(bar(B_V_FULL + vb));
-                if (t + 1 < n_tiles) {
-                    load_v(t + 1);
+                if (t + 1 < n_items) {
+                    load_v(t + 1, tile);
                     __syncwarp();
                     if (lane == 0) mbar_arrive(bar(B_STG_EMPTY + s1));
                 }
@@ -736,7 +784,9 @@ int launch_attention_int4_tc(const AttnParams& P, cudaStream_t s, char* text, si
                           : pick(i4tc::attention_int4_tc_kernel<64, false, false>, i4tc::attention_int4_tc_kernel<64, false, true>));
     if (opt_in_smem(done[P.page_size == 64][cl][tree], (const void*)kern, i4tc::SMEM) != cudaSuccess)
         return (cudaGetLastError(), FP8KV_ERR_CUDA);
-    const dim3 grid(P.num_splits, P.Hkv * RT, P.B);
+    if (tree && (P.row_loop < 1 || (P.row_loop > 1 && (cl || P.k_new)))) return FP8KV_ERR_UNSUPPORTED;
+    const int RG = tree ? (RT + P.row_loop - 1) / P.row_loop : RT;
+    const dim3 grid(P.num_splits, P.Hkv * RG, P.B);
     const cudaError_t e = launch_pdl_cluster(kern, grid, dim3(i4tc::THREADS), i4tc::SMEM, s, P.cluster, P);
     if (e != cudaSuccess) {
         cudaGetLastError();
@@ -745,7 +795,7 @@ int launch_attention_int4_tc(const AttnParams& P, cudaStream_t s, char* text, si
     snprintf(text, text_bytes,
              "attention_int4_tc<ps=%d> rows=%d row_tiles=%d splits=%d split_tokens=%d grid=%dx%dx%d threads=%d cluster=%d "
              "reduce=%d order=%s",
-             P.page_size, P.R, RT, P.num_splits, P.split_pages * P.page_size, P.num_splits, P.Hkv * RT, P.B,
+             P.page_size, P.R, RT, P.num_splits, P.split_pages * P.page_size, P.num_splits, P.Hkv * RG, P.B,
              i4tc::THREADS, P.cluster > 1 ? P.cluster : 1, P.num_splits > 1 && P.cluster <= 1 ? 1 : 0, P.lpt_order ? "longest_first" : "grid");
     return FP8KV_OK;
 }
