@@ -9,11 +9,13 @@
 // factor on all of them, are in the table.
 //
 // HBM bounds it: a row of 256 bytes is read and written once, the table row of a
-// token is read once for its heads.  A half warp takes HEADS heads of one token,
-// a thread four pairs of each (or eight elements behind rot), so that the table,
-// the slot and the position are in registers for all of them and their loads
-// are in flight together.  K rows then pass through shared memory: a thread
-// encodes eight (INT4: sixteen) neighbouring elements, whatever the pairs were.
+// token is read once for its heads.  A half warp takes one K and V head of a token,
+// or QH heads of its Q, a thread four pairs of each (or eight elements behind rot),
+// so that position and table row are in registers for all of them and every row's
+// load is in flight before the first is needed.  The K blocks are spread over the
+// grid, their encoding beside the others' loads (16381 tokens, INT4: 105 us, all K
+// blocks first 113).  K rows pass through shared memory, as a thread encodes eight (INT4: sixteen)
+// neighbouring elements, whatever the pairs were.
 #include "attention.cuh"
 #include "common.cuh"
 #include "int4.cuh"
@@ -21,6 +23,10 @@
 namespace fp8kv {
 
 int status_rope_insert(unsigned int* s, int clear) { return read_status(s, clear); }
+
+// Heads of Q a half warp takes: 16381 tokens of 72 + 8 heads, INT4: 2 heads 119 us, 4
+// 105 (6.6 TB/s), 8 109.
+constexpr int kRopeHeads = 4;
 
 struct RopeParams {
     const uint16_t *q, *k, *v;
@@ -31,122 +37,149 @@ struct RopeParams {
     uint16_t* q_out;
     uint8_t *k_cache, *v_cache;
     int64_t num_slots;
-    int max_pos, rot, T, Hq, Hkv, page_size, groups;
+    int max_pos, rot, T, Hq, Hkv, page_size;
+    int groups;                 // of QH heads of Q, a token
+    unsigned k_blocks, k_every;
 };
 
-template <int DT, int HEADS, bool PAIRS>
+// A thread's eight elements of a row: runs of four at a and b, which turn as pairs
+// (or, PAIRS, hold them as neighbours), or stay.
+struct RopeLane {
+    int a, b;
+    bool turns;
+    float c[4], s[4];
+    template <bool PAIRS>
+    __device__ __forceinline__ static RopeLane at(int i, int rot) {
+        RopeLane l;
+        l.turns = 8 * i < rot;
+        l.a = PAIRS || !l.turns ? 8 * i : 4 * i;
+        l.b = PAIRS || !l.turns ? 8 * i + 4 : rot / 2 + 4 * i;
+        return l;
+    }
+    __device__ __forceinline__ void angles(const float* cos_sin, int64_t pos, int rot, int i) {
+        if (!turns) return;
+        const float* row = cos_sin + pos * rot + 4 * i;
+        *reinterpret_cast<float4*>(c) = __ldg(reinterpret_cast<const float4*>(row));
+        *reinterpret_cast<float4*>(s) = __ldg(reinterpret_cast<const float4*>(row + rot / 2));
+    }
+    template <bool PAIRS>
+    __device__ __forceinline__ void turn(uint2& xa, uint2& xb) const {
+        if (!turns) return;
+        const uint32_t w[4] = {xa.x, xa.y, xb.x, xb.y};
+        float r[8];
+#pragma unroll
+        for (int j = 0; j < 4; ++j) {
+            // pair j: (x, y)
+            const uint32_t wx = PAIRS ? w[j] : w[j >> 1], wy = PAIRS ? w[j] : w[2 + (j >> 1)];
+            const float x = !PAIRS && (j & 1) ? bf16_hi(wx) : bf16_lo(wx);
+            const float y = PAIRS || (j & 1) ? bf16_hi(wy) : bf16_lo(wy);
+            r[PAIRS ? 2 * j : j] = __fmaf_rn(x, c[j], -__fmul_rn(y, s[j]));
+            r[PAIRS ? 2 * j + 1 : 4 + j] = __fmaf_rn(y, c[j], __fmul_rn(x, s[j]));
+        }
+        xa = make_uint2(pack_bf16x2(r[0], r[1]), pack_bf16x2(r[2], r[3]));
+        xb = make_uint2(pack_bf16x2(r[4], r[5]), pack_bf16x2(r[6], r[7]));
+    }
+};
+
+template <int DT, bool PAIRS>
 __global__ void __launch_bounds__(256) rope_insert_kernel(RopeParams P) {
+    constexpr int QH = kRopeHeads;
     __shared__ __align__(16) uint16_t rows[16][128 + 8];
     pdl_launch_dependents();
     const int half = threadIdx.x >> 4, i = threadIdx.x & 15;
-    const int64_t unit = (int64_t)blockIdx.x * 16 + half;
-    const int64_t t64 = unit / P.groups;
-    const bool in = t64 < P.T;
-    const int64_t t = in ? t64 : 0;
-    const int h0 = (int)(unit - t64 * P.groups) * HEADS;
-    const bool turns = 8 * i < P.rot;
-    const int ea = !turns || PAIRS ? 8 * i : 4 * i, eb = !turns || PAIRS ? 8 * i + 4 : P.rot / 2 + 4 * i;
+    RopeLane lane = RopeLane::at<PAIRS>(i, P.rot);
     pdl_wait();
-    const int64_t pos = in ? P.positions[t] : 0, slot = in ? P.slots[t] : -1;
-    uint2 xa[HEADS], xb[HEADS];
+    // every P.k_every-th block is one of K and V, while there are any
+    const unsigned kb = blockIdx.x / P.k_every;
+    if (blockIdx.x != kb * P.k_every || kb >= P.k_blocks) {
+        // ------------------------------------------------------------------- Q
+        const int64_t unit = (int64_t)(blockIdx.x - min(P.k_blocks, kb + 1)) * 16 + half;
+        const int64_t t = unit / P.groups;
+        if (t >= P.T) return;
+        const int h0 = (int)(unit - t * P.groups) * QH;
+        const int64_t pos = P.positions[t];
+        const uint16_t* src = P.q + t * P.q_stride + h0 * 128;
+        uint2 xa[QH], xb[QH];
 #pragma unroll
-    for (int u = 0; u < HEADS; ++u) {
-        const int h = h0 + u;
-        if (!in || h >= P.Hq + P.Hkv) continue;
-        const uint16_t* src = h < P.Hq ? P.q + t * P.q_stride + h * 128 : P.k + t * P.k_stride + (h - P.Hq) * 128;
-        xa[u] = *reinterpret_cast<const uint2*>(src + ea);
-        xb[u] = *reinterpret_cast<const uint2*>(src + eb);
+        for (int u = 0; u < QH; ++u) {
+            if (h0 + u >= P.Hq) break;
+            xa[u] = __ldcs(reinterpret_cast<const uint2*>(src + u * 128 + lane.a));
+            xb[u] = __ldcs(reinterpret_cast<const uint2*>(src + u * 128 + lane.b));
+        }
+        if (pos < 0 || pos >= P.max_pos) return;            // (flagged by the K blocks)
+        lane.angles(P.cos_sin, pos, P.rot, i);
+        uint16_t* dst = P.q_out + (t * P.Hq + h0) * 128;
+#pragma unroll
+        for (int u = 0; u < QH; ++u) {
+            if (h0 + u >= P.Hq) break;
+            lane.turn<PAIRS>(xa[u], xb[u]);
+            *reinterpret_cast<uint2*>(dst + u * 128 + lane.a) = xa[u];
+            *reinterpret_cast<uint2*>(dst + u * 128 + lane.b) = xb[u];
+        }
+        return;
     }
+    // ------------------------------------------------------------------- K and V
+    const int64_t unit = (int64_t)kb * 16 + half;
+    const bool in = unit < (int64_t)P.T * P.Hkv;
+    const int64_t t = in ? unit / P.Hkv : 0;
+    const int h = in ? (int)(unit - t * P.Hkv) : 0;
+    // INT4: threads 0-7 take the blocks of K, 8-15 those of V
+    const bool v_too = DT != FP8KV_CACHE_INT4 || i >= 8;
+    const int64_t pos = P.positions[t], slot = P.slots[t];
+    const uint16_t* src = P.k + t * P.k_stride + h * 128;
+    uint2 xa = *reinterpret_cast<const uint2*>(src + lane.a), xb = *reinterpret_cast<const uint2*>(src + lane.b);
+    const uint4* vrow = reinterpret_cast<const uint4*>(P.v + t * P.v_stride + h * 128);
+    uint4 v[2] = {};
+    if (DT == FP8KV_CACHE_INT4) {
+        if (v_too) {
+            v[0] = vrow[2 * (i & 7)];
+            v[1] = vrow[2 * (i & 7) + 1];
+        }
+    } else {
+        v[0] = vrow[i];
+    }
+    const float ks = DT == FP8KV_CACHE_BF16 ? 1.f : *P.k_scale, vs = DT == FP8KV_CACHE_BF16 ? 1.f : *P.v_scale;
     const bool pos_ok = pos >= 0 && pos < P.max_pos;
-    if (!pos_ok && i == 0 && h0 == 0) flag(FP8KV_DEV_BAD_POSITION);
-    const bool slot_ok = slot >= 0 && slot < P.num_slots;
-    if (in && pos_ok && slot >= P.num_slots && i == 0 && h0 == 0) flag(FP8KV_DEV_BAD_SLOT);
-    const bool live = in && pos_ok;
-    float4 c = make_float4(1.f, 1.f, 1.f, 1.f), s = make_float4(0.f, 0.f, 0.f, 0.f);
-    if (live && turns) {
-        const float* row = P.cos_sin + pos * P.rot + 4 * i;
-        c = *reinterpret_cast<const float4*>(row);
-        s = *reinterpret_cast<const float4*>(row + P.rot / 2);
+    if (in && i == 0 && h == 0) {
+        if (!pos_ok) flag(FP8KV_DEV_BAD_POSITION);
+        else if (slot >= P.num_slots) flag(FP8KV_DEV_BAD_SLOT);
     }
-    const float cc[4] = {c.x, c.y, c.z, c.w}, ss[4] = {s.x, s.y, s.z, s.w};
-#pragma unroll
-    for (int u = 0; u < HEADS; ++u) {
-        const int h = h0 + u;
-        const bool mine = live && h < P.Hq + P.Hkv, is_q = h < P.Hq;
-        if (mine && turns) {
-            const uint32_t w[4] = {xa[u].x, xa[u].y, xb[u].x, xb[u].y};
-            uint32_t o[4];
-            if (PAIRS) {
-#pragma unroll
-                for (int j = 0; j < 4; ++j) {
-                    const float x = bf16_lo(w[j]), y = bf16_hi(w[j]);
-                    o[j] = pack_bf16x2(__fmaf_rn(x, cc[j], -__fmul_rn(y, ss[j])), __fmaf_rn(y, cc[j], __fmul_rn(x, ss[j])));
-                }
-            } else {
-                float r[8];
-#pragma unroll
-                for (int j = 0; j < 4; ++j) {
-                    const float x = j & 1 ? bf16_hi(w[j >> 1]) : bf16_lo(w[j >> 1]);
-                    const float y = j & 1 ? bf16_hi(w[2 + (j >> 1)]) : bf16_lo(w[2 + (j >> 1)]);
-                    r[j] = __fmaf_rn(x, cc[j], -__fmul_rn(y, ss[j]));
-                    r[4 + j] = __fmaf_rn(y, cc[j], __fmul_rn(x, ss[j]));
-                }
-#pragma unroll
-                for (int j = 0; j < 4; ++j) o[j] = pack_bf16x2(r[2 * j], r[2 * j + 1]);
-            }
-            xa[u] = make_uint2(o[0], o[1]);
-            xb[u] = make_uint2(o[2], o[3]);
+    const bool stores = in && pos_ok && slot >= 0 && slot < P.num_slots;
+    if (stores) {
+        lane.angles(P.cos_sin, pos, P.rot, i);
+        lane.turn<PAIRS>(xa, xb);
+        *reinterpret_cast<uint2*>(&rows[half][lane.a]) = xa;
+        *reinterpret_cast<uint2*>(&rows[half][lane.b]) = xb;
+    }
+    __syncwarp();
+    if (!stores) return;
+    const int64_t page = slot >> (P.page_size == 64 ? 6 : 5);
+    const int off = (int)slot & (P.page_size - 1);
+    const uint4* krow = reinterpret_cast<const uint4*>(rows[half]);
+    if (DT == FP8KV_CACHE_INT4) {
+        const int block = i & 7;
+        uint8_t sc;
+        const uint2 codes = int4_encode16(v_too ? v[0] : krow[2 * block], v_too ? v[1] : krow[2 * block + 1],
+                                          v_too ? vs : ks, sc);
+        uint8_t* cache = (v_too ? P.v_cache : P.k_cache) + (page * P.Hkv + h) * P.page_size * kInt4RowBytes;
+        *reinterpret_cast<uint2*>(cache + off * kInt4CodeBytes + block * 8) = codes;
+        cache[P.page_size * kInt4CodeBytes + off * kInt4ScaleBytes + block] = sc;
+    } else {
+        const int64_t at = ((page * P.Hkv + h) * P.page_size + off) * 128 + 8 * i;
+        if (DT == FP8KV_CACHE_E4M3) {
+            *reinterpret_cast<uint2*>(P.k_cache + at) = e4m3_encode8(krow[i], ks);
+            *reinterpret_cast<uint2*>(P.v_cache + at) = e4m3_encode8(v[0], vs);
+        } else {
+            *reinterpret_cast<uint4*>(P.k_cache + 2 * at) = krow[i];
+            *reinterpret_cast<uint4*>(P.v_cache + 2 * at) = v[0];
         }
-        if (mine && is_q) {
-            uint16_t* dst = P.q_out + (t * P.Hq + h) * 128;
-            *reinterpret_cast<uint2*>(dst + ea) = xa[u];
-            *reinterpret_cast<uint2*>(dst + eb) = xb[u];
-        }
-        // K: the row in order through shared memory (the loop is uniform over
-        // the half warp; its two halves may disagree, so the whole warp meets)
-        const bool stores = mine && !is_q && slot_ok;
-        if (!__any_sync(0xffffffffu, stores)) continue;
-        if (stores) {
-            *reinterpret_cast<uint2*>(&rows[half][ea]) = xa[u];
-            *reinterpret_cast<uint2*>(&rows[half][eb]) = xb[u];
-        }
-        __syncwarp();
-        if (stores) {
-            const int hk = h - P.Hq;
-            const int64_t page = slot / P.page_size;
-            const int off = (int)(slot - page * P.page_size);
-            const uint4* vrow = reinterpret_cast<const uint4*>(P.v + t * P.v_stride + hk * 128);
-            const uint4* krow = reinterpret_cast<const uint4*>(rows[half]);
-            if (DT == FP8KV_CACHE_INT4) {
-                // threads 0-7: the blocks of K, 8-15: those of V
-                const bool is_k = i < 8;
-                const int block = i & 7;
-                const uint4 x0 = is_k ? krow[2 * block] : vrow[2 * block], x1 = is_k ? krow[2 * block + 1] : vrow[2 * block + 1];
-                uint8_t sc;
-                const uint2 codes = int4_encode16(x0, x1, is_k ? *P.k_scale : *P.v_scale, sc);
-                uint8_t* cache = (is_k ? P.k_cache : P.v_cache) + (page * P.Hkv + hk) * P.page_size * kInt4RowBytes;
-                *reinterpret_cast<uint2*>(cache + off * kInt4CodeBytes + block * 8) = codes;
-                cache[P.page_size * kInt4CodeBytes + off * kInt4ScaleBytes + block] = sc;
-            } else {
-                const int64_t at = ((page * P.Hkv + hk) * P.page_size + off) * 128 + 8 * i;
-                if (DT == FP8KV_CACHE_E4M3) {
-                    *reinterpret_cast<uint2*>(P.k_cache + at) = e4m3_encode8(krow[i], *P.k_scale);
-                    *reinterpret_cast<uint2*>(P.v_cache + at) = e4m3_encode8(vrow[i], *P.v_scale);
-                } else {
-                    *reinterpret_cast<uint4*>(P.k_cache + 2 * at) = krow[i];
-                    *reinterpret_cast<uint4*>(P.v_cache + 2 * at) = vrow[i];
-                }
-            }
-        }
-        __syncwarp();
     }
 }
 
 template <int DT>
-static cudaError_t launch_rope(const RopeParams& P, bool pairs, int heads, int64_t blocks, cudaStream_t s) {
-    auto kern = pairs ? (heads == 4 ? rope_insert_kernel<DT, 4, true> : rope_insert_kernel<DT, 1, true>)
-                      : (heads == 4 ? rope_insert_kernel<DT, 4, false> : rope_insert_kernel<DT, 1, false>);
-    return launch_pdl(kern, dim3((unsigned)blocks), dim3(256), 0, s, P);
+static cudaError_t launch_rope(const RopeParams& P, bool pairs, unsigned blocks, cudaStream_t s) {
+    auto kern = pairs ? rope_insert_kernel<DT, true> : rope_insert_kernel<DT, false>;
+    return launch_pdl(kern, dim3(blocks), dim3(256), 0, s, P);
 }
 
 }  // namespace fp8kv
@@ -195,12 +228,13 @@ extern "C" int fp8kv_rope_insert(const void* q, int64_t q_stride, const void* k,
     P.Hq = Hq;
     P.Hkv = Hkv;
     P.page_size = page_size;
-    const int heads = (int64_t)T * (Hq + Hkv) > 16 * 8 * (int64_t)num_sms() ? 4 : 1;
-    P.groups = (Hq + Hkv + heads - 1) / heads;
-    const int64_t blocks = ((int64_t)T * P.groups + 15) / 16;
+    P.groups = (Hq + kRopeHeads - 1) / kRopeHeads;
+    const int64_t k_blocks = ((int64_t)T * Hkv + 15) / 16, blocks = k_blocks + ((int64_t)T * P.groups + 15) / 16;
     if (blocks > 0x7fffffff) return FP8KV_ERR_UNSUPPORTED;
-    const cudaError_t e = cache_dtype == FP8KV_CACHE_E4M3   ? launch_rope<FP8KV_CACHE_E4M3>(P, interleaved != 0, heads, blocks, (cudaStream_t)stream)
-                          : cache_dtype == FP8KV_CACHE_BF16 ? launch_rope<FP8KV_CACHE_BF16>(P, interleaved != 0, heads, blocks, (cudaStream_t)stream)
-                                                            : launch_rope<FP8KV_CACHE_INT4>(P, interleaved != 0, heads, blocks, (cudaStream_t)stream);
+    P.k_blocks = (unsigned)k_blocks;
+    P.k_every = (unsigned)(blocks / k_blocks);
+    const cudaError_t e = cache_dtype == FP8KV_CACHE_E4M3   ? launch_rope<FP8KV_CACHE_E4M3>(P, interleaved != 0, (unsigned)blocks, (cudaStream_t)stream)
+                          : cache_dtype == FP8KV_CACHE_BF16 ? launch_rope<FP8KV_CACHE_BF16>(P, interleaved != 0, (unsigned)blocks, (cudaStream_t)stream)
+                                                            : launch_rope<FP8KV_CACHE_INT4>(P, interleaved != 0, (unsigned)blocks, (cudaStream_t)stream);
     return e == cudaSuccess ? FP8KV_OK : (cudaGetLastError(), FP8KV_ERR_CUDA);
 }
