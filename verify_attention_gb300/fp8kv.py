@@ -650,14 +650,18 @@ def fp8kv_tree_metadata(parents, seq_lens, block_table, page_size, max_seq_len, 
     B, M = parents.shape
     if block_table.dim() != 2 or block_table.shape[0] != B or seq_lens.numel() != B:
         raise ValueError(f"block_table must be [{B}][pages] and seq_lens [{B}]")
-    given = (tree_mask, positions, slot_mapping)
-    for t, n in zip(given, ("tree_mask", "positions", "slot_mapping")):
+    outs = []
+    for t, n in ((tree_mask, "tree_mask"), (positions, "positions"), (slot_mapping, "slot_mapping")):
         if t is not None:
             _tree_rows(t, n, torch.int64, B, M)
-    if any(t is None for t in given):
-        with _at(stream):
-            made = torch.empty((3, B, M), dtype=torch.int64, device=parents.device).unbind(0)
-        tree_mask, positions, slot_mapping = (m if t is None else t for t, m in zip(given, made))
+        elif stream is None:
+            # (three allocations are faster than the views of one)
+            t = torch.empty((B, M), dtype=torch.int64, device=parents.device)
+        else:
+            with _at(stream):
+                t = torch.empty((B, M), dtype=torch.int64, device=parents.device)
+        outs.append(t)
+    tree_mask, positions, slot_mapping = outs
     rc = lib().fp8kv_tree_metadata(parents.data_ptr(), seq_lens.data_ptr(), block_table.data_ptr(),
                                    block_table.shape[1], int(max_seq_len), B, M, int(num_pages), int(page_size),
                                    tree_mask.data_ptr(), positions.data_ptr(), slot_mapping.data_ptr(),
