@@ -74,16 +74,23 @@ __device__ __forceinline__ bool operator>(F2 a, F2 b) { return __fadd_rn(__fsub_
 __device__ __forceinline__ F2 shfl(F2 a, int lane) {
     return {__shfl_sync(0xffffffffu, a.hi, lane), __shfl_sync(0xffffffffu, a.lo, lane)};
 }
-// lane l: the sum of lanes 0 .. l (n of them, a power of two).  Not unrolled: the
-// kernel's instructions come from L2 for every CTA, and short code runs sooner than
-// fast code.
-__device__ __forceinline__ F2 warp_scan(F2 a, int lane, int n) {
-#pragma unroll 1
-    for (int o = 1; o < n; o <<= 1) {
+// lane l < N: the sum of lanes 0 .. l
+template <int N>
+__device__ __forceinline__ F2 warp_scan(F2 a, int lane) {
+#pragma unroll
+    for (int o = 1; o < N; o <<= 1) {
         const F2 b = {__shfl_up_sync(0xffffffffu, a.hi, o), __shfl_up_sync(0xffffffffu, a.lo, o)};
         const F2 c = a + b;
         if (lane >= o) a = c;
     }
+    return a;
+}
+// every lane: the sum of its N, in the same order for all
+template <int N>
+__device__ __forceinline__ F2 warp_total(F2 a) {
+#pragma unroll
+    for (int o = N / 2; o >= 1; o >>= 1)
+        a = a + F2{__shfl_xor_sync(0xffffffffu, a.hi, o), __shfl_xor_sync(0xffffffffu, a.lo, o)};
     return a;
 }
 // Of runs with the sums `run` that end at `end`: the first whose end exceeds t
@@ -404,7 +411,7 @@ __global__ void __launch_bounds__(kVerifyThreads, 2) verify_tree_kernel(VerifyPa
                         F2 mine = {0.f, 0.f};
 #pragma unroll
                         for (int i = 0; i < N; ++i) mine = mine + F2{hi[u][i], lo[u][i]};
-                        const F2 scan = warp_scan(mine, lane, 32);
+                        const F2 scan = warp_scan<32>(mine, lane);
                         F2 upto = before_lane(scan, lane, run);
                         int top = -1, pick = -1;
 #pragma unroll
@@ -428,14 +435,12 @@ __global__ void __launch_bounds__(kVerifyThreads, 2) verify_tree_kernel(VerifyPa
             if (stage == 2) break;
             // ---- the sums of the warps
             acc = fast_two_sum(acc.hi, acc.lo) + fast_two_sum(odd.hi, odd.lo);
-#pragma unroll 1
-            for (int o = 16; o >= 1; o >>= 1)
-                acc = acc + F2{__shfl_xor_sync(0xffffffffu, acc.hi, o), __shfl_xor_sync(0xffffffffu, acc.lo, o)};
+            acc = warp_total<32>(acc);
             if (lane == 0) warp_sum[stage][warp] = acc;
             __syncthreads();
             if (stage == 1) {
                 const F2 part = lane < kVerifyWarps ? warp_sum[1][lane] : F2{0.f, 0.f};
-                const F2 scan = warp_scan(part, lane, kVerifyWarps);
+                const F2 scan = warp_scan<kVerifyWarps>(part, lane);
                 const int at = locate(part, run + scan, t);
                 run = before_lane(scan, at, run);
                 if (warp != at) break;
@@ -448,8 +453,7 @@ __global__ void __launch_bounds__(kVerifyThreads, 2) verify_tree_kernel(VerifyPa
             VerifyPart* got = parts[turn];
             if (warp == 0) {
                 const F2 mine = lane < kVerifyWarps ? warp_sum[0][lane] : F2{0.f, 0.f};
-                const F2 upto = warp_scan(mine, lane, kVerifyWarps);
-                const F2 all = shfl(upto, kVerifyWarps - 1);
+                const F2 all = shfl(warp_total<kVerifyWarps>(mine), 0);
                 const int walk = cur | k << 8 | state << 16;
                 bool ok = true;
                 if (C == 1) {
@@ -462,8 +466,7 @@ __global__ void __launch_bounds__(kVerifyThreads, 2) verify_tree_kernel(VerifyPa
                 }
                 const F2 part = lane < C ? got[lane].sum : F2{0.f, 0.f};
                 ok &= !__any_sync(0xffffffffu, lane < C && got[lane].walk != walk);
-                const F2 scan = warp_scan(part, lane, kVerifyMaxCluster);
-                const F2 total = shfl(scan, kVerifyMaxCluster - 1);
+                const F2 total = shfl(warp_total<kVerifyMaxCluster>(part), 0);
                 S = total;
                 int next = state, in = -1;
                 if (!ok) {
@@ -473,11 +476,14 @@ __global__ void __launch_bounds__(kVerifyThreads, 2) verify_tree_kernel(VerifyPa
                         // the draw: the CTA and the warp's run that hold the token
                         // whose running sum exceeds t
                         t = F2{un[0], 0.f} * total;
+                        const F2 scan = warp_scan<kVerifyMaxCluster>(part, lane);
                         const int owner = locate(part, scan, t);
-                        const F2 base = before_lane(scan, owner, {0.f, 0.f});
-                        in = locate(mine, base + upto, t);
-                        run = before_lane(upto, in, base);
-                        if (owner != rank) in = -1;
+                        if (owner == rank) {
+                            const F2 base = before_lane(scan, owner, {0.f, 0.f});
+                            const F2 upto = warp_scan<kVerifyWarps>(mine, lane);
+                            in = locate(mine, base + upto, t);
+                            run = before_lane(upto, in, base);
+                        }
                     } else if (state == PASS_DRAW && !(total.hi > 0.f)) {
                         next = PASS_ROW;
                     } else {
