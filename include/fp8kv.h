@@ -516,7 +516,7 @@ int fp8kv_rope_insert(const void* q, int64_t q_stride, const void* k, int64_t k_
  * p_m = L - M + (bits in tree_mask[b][m]) - 1 (mask 0: L - M), sees of those the
  * keys at positions >= p_m - window_left, node i being at position p_i.  A row without visible keys,
  * and a row whose mask is 0 (padding), is written as zeros.  The mask of a chain
- * gives fp8kv_paged_attention's result.
+ * gives fp8kv_paged_attention's result (up to roundings).
  *
  *   tree_mask  (device) uint64 [B][M]
  *   split_tokens (host) 0, or a multiple of page_size; of 128 for more than 16 rows

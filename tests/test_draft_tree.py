@@ -361,7 +361,7 @@ def test_a_chain_is_the_plain_call(kind, M, Hq):
     c.check(plain)                                      # the same values, hence tolerance, whatever the kernel
     got = c.run()
     c.check(got)
-    if kind != "bf16" or M * Hq // 2 <= 16:
+    if kind == "int4" or M * Hq // 2 <= 16:
         assert torch.equal(got, plain)                  # the same kernel, the same order of operations
 
 

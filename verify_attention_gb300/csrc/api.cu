@@ -69,7 +69,7 @@ extern "C" int fp8kv_device_status(unsigned int* status, int clear) {
         fp8kv::status_attention_int4(&s, clear) || fp8kv::status_attention_int4_tc(&s, clear) ||
         fp8kv::status_prompt(&s, clear) || fp8kv::status_draft_tree(&s, clear) ||
         fp8kv::status_rope_insert(&s, clear) || fp8kv::status_verify_tree(&s, clear) ||
-        fp8kv::status_attention_bf16_tc(&s, clear))
+        fp8kv::status_attention_tree_tc(&s, clear))
         return FP8KV_ERR_CUDA;
     *status = s;
     return FP8KV_OK;

@@ -1189,7 +1189,8 @@ static int attention_call(const void* k_new, const void* v_new, const void* q, c
     // more than 16 query rows per KV head on E4M3 pages, partitions of whole
     // 128-key tiles: tcgen05 kernel (128-row MMA tiles); otherwise mma.sync,
     // which serves at most 16 rows per sequence and 144 per KV head
-    const bool use_tc = fp8 && tc_rows(M, Hq, Hkv) && (plan.split_tokens % tc_tile_tokens()) == 0;
+    const bool tree_tc = tree && !int4 && tc_rows(M, Hq, Hkv);
+    const bool use_tc = !tree && fp8 && tc_rows(M, Hq, Hkv) && (plan.split_tokens % tc_tile_tokens()) == 0;
     if (tree) {
         // more than 16 rows per KV head: a tcgen05 kernel for every cache type
         if (M > FP8KV_TREE_MAX_NODES || (tc_rows(M, Hq, Hkv) && plan.split_tokens % tc_tile_tokens()))
@@ -1327,8 +1328,9 @@ static int attention_call(const void* k_new, const void* v_new, const void* q, c
         set_dispatch(text);
         return FP8KV_OK;
     }
-    const bool bf16_tc = tree && !fp8 && tc_rows(M, Hq, Hkv);
-    const int RT = use_tc || bf16_tc ? row_tiles(M, Hq, Hkv) : 1;
+    const int RT = use_tc || tree_tc ? row_tiles(M, Hq, Hkv) : 1;
+    // partials in f16 beside v_scale
+    const bool f16_parts = use_tc || (tree_tc && fp8);
     if (tree && RT > 1) {
         const Int4Cut cut = int4_cut(plan, true, false, split_tokens > 0, B, (int64_t)B * Hkv * RT, page_size,
                                      fp8 ? 6.f : 5.f, fp8 ? 1.2f : 0.9f, even);
@@ -1340,13 +1342,13 @@ static int attention_call(const void* k_new, const void* v_new, const void* q, c
     // one sequence in at most 8 partitions and one row tile: the partitions
     // of a KV head run as one thread-block cluster and combine in distributed
     // shared memory
-    P.cluster = ((use_tc || bf16_tc) && B == 1 && RT == 1 && plan.num_splits > 1 && plan.num_splits <= 8) ? plan.num_splits : 0;
+    P.cluster = ((use_tc || tree_tc) && B == 1 && RT == 1 && plan.num_splits > 1 && plan.num_splits <= 8) ? plan.num_splits : 0;
     // several sequences split into partitions of unequal length: longest first
-    const bool lpt = use_tc && B > 1 && RT == 1 && plan.num_splits > 1;
+    const bool lpt = f16_parts && B > 1 && RT == 1 && plan.num_splits > 1;
     if (lpt)
         P.lpt_order = (const int32_t*)((const uint8_t*)workspace +
                                        (size_t)B * M * Hq * plan.num_splits * 128 * sizeof(uint16_t));
-    if (k_new && use_tc && RT == 1) {                               // appended in the kernel
+    if (k_new && f16_parts && RT == 1) {                            // appended in the kernel
         P.k_new = (const uint16_t*)k_new;
         P.v_new = (const uint16_t*)v_new;
         P.k_cache = (uint8_t*)k_cache;
@@ -1369,8 +1371,8 @@ static int attention_call(const void* k_new, const void* v_new, const void* q, c
     char buf[256];
     if (use_tc)
         rc = launch_attention_tc(tk, tv, P, s);
-    else if (bf16_tc)
-        rc = launch_attention_bf16_tc(tk, tv, P, s, buf, sizeof buf);
+    else if (tree_tc)
+        rc = launch_attention_tree_tc(tk, tv, P, fp8, s, buf, sizeof buf);
     else if (page_size == 32)
         rc = fp8 ? launch<32, true>(tk, tv, P, s) : launch<32, false>(tk, tv, P, s);
     else
@@ -1379,10 +1381,10 @@ static int attention_call(const void* k_new, const void* v_new, const void* q, c
     if (plan.num_splits > 1 && P.cluster <= 1) {
         const int64_t warps = (int64_t)B * M * Hq;
         cudaError_t e =
-            launch_pdl(use_tc ? (tree ? attn_reduce_kernel<true, true> : attn_reduce_kernel<true, false>)
-                              : (tree ? attn_reduce_kernel<false, true> : attn_reduce_kernel<false, false>),
+            launch_pdl(f16_parts ? (tree ? attn_reduce_kernel<true, true> : attn_reduce_kernel<true, false>)
+                                 : (tree ? attn_reduce_kernel<false, true> : attn_reduce_kernel<false, false>),
                        dim3((unsigned)((warps + 7) / 8)), dim3(256), 0, s, (const float*)P.ws_o,
-                       (const float*)P.ws_ml, seq_lens, B, M, Hq, P.G, use_tc || bf16_tc ? 128 : P.R,
+                       (const float*)P.ws_ml, seq_lens, B, M, Hq, P.G, use_tc || tree_tc ? 128 : P.R,
                        max_pages_per_seq, page_size, window_left, plan.split_pages, plan.num_splits, max_seq_len,
                        k_scale ? v_scale : nullptr, scale_stride, (uint16_t*)out, tree_mask);
         if (e != cudaSuccess) {
@@ -1397,7 +1399,7 @@ static int attention_call(const void* k_new, const void* v_new, const void* q, c
                  page_size, P.R, RT, plan.num_splits, plan.split_tokens, plan.num_splits, Hkv * RT, B, tc_threads(),
                  P.cluster > 1 ? P.cluster : 1, (plan.num_splits > 1 && P.cluster <= 1) ? 1 : 0,
                  lpt ? "longest_first" : "grid");
-    else if (!bf16_tc)
+    else if (!tree_tc)
         snprintf(buf, sizeof buf,
                  "%s<ps=%d,%s> rows=%d row_tiles=%d key_groups=%d stages_per_group=%d splits=%d "
                  "split_tokens=%d grid=%dx%dx%d threads=%d reduce=%d",

@@ -148,11 +148,12 @@ void int4_clusters(int (&count)[9]);    // [n], n = 2 .. 8: clusters of n CTAs, 
 // FP8KV_ERR_UNSUPPORTED when the shape is not one it implements.
 int launch_attention_tc(const CUtensorMap& tk, const CUtensorMap& tv, const AttnParams& P, cudaStream_t s);
 int status_attention_tc(unsigned int* s, int clear);
-// Host launcher of the tcgen05 kernel over a BF16 cache (attention_bf16_tc.cu),
-// tree calls of more than 16 rows per KV head; partials as the mma.sync kernels
-// write them.  `text` describes the launch.
-int launch_attention_bf16_tc(const CUtensorMap& tk, const CUtensorMap& tv, const AttnParams& P, cudaStream_t s,
-                             char* text, size_t text_bytes);
+// Host launcher of the tcgen05 kernel of tree calls of more than 16 rows per KV head
+// over an E4M3 or a BF16 cache (attention_tree_tc.cu).  Partials over E4M3 as the
+// other tcgen05 kernels write them, over BF16 as the mma.sync kernels do.  `text`
+// describes the launch.
+int launch_attention_tree_tc(const CUtensorMap& tk, const CUtensorMap& tv, const AttnParams& P, bool fp8,
+                             cudaStream_t s, char* text, size_t text_bytes);
 int tc_tile_tokens();   // keys per tile of the tcgen05 kernel
 int tc_threads();       // threads per CTA of the tcgen05 kernel
 

@@ -115,9 +115,7 @@ __device__ __forceinline__ int converter_index(int warp) { return warp < 4 ? war
 // DUAL: Q.K^T (warp 1) and P.V (warp 15) are issued by two threads, each
 // waiting only for its own operands; otherwise one thread issues Q.K^T(t)
 // then P.V(t - 1).
-// TREE: what a row sees among the last M keys is given by its mask word, so every
-// row tile spans the keys to the end of the sequence.
-template <int PS, bool DUAL, bool TREE>
+template <int PS, bool DUAL>
 __global__ void __launch_bounds__(THREADS, 1) attention_tc_kernel(const __grid_constant__ CUtensorMap tm_k,
                                                                  const __grid_constant__ CUtensorMap tm_v,
                                                                  AttnParams P) {
@@ -194,8 +192,8 @@ __global__ void __launch_bounds__(THREADS, 1) attention_tc_kernel(const __grid_c
         // trip of the block table off the path to the first page copy
         const int Lg = *(volatile const int*)(P.seq_lens + b);
         if (Lg >= P.M && Lg <= P.max_seq_len) {
-            const int hi_g = TREE ? Lg - 1 : Lg - P.M + (R0 + RL - 1) / P.G;
-            const int lo_g = (P.window_left >= 0) ? max(0, Lg - P.M + (TREE ? 0 : R0 / P.G) - P.window_left) : 0;
+            const int hi_g = Lg - P.M + (R0 + RL - 1) / P.G;
+            const int lo_g = (P.window_left >= 0) ? max(0, Lg - P.M + R0 / P.G - P.window_left) : 0;
             const int pb = lo_g / PS + split * P.split_pages;
             const int pe = min(pb + P.split_pages, hi_g / PS + 1);
             const int32_t* row = P.block_table + (int64_t)b * P.mpps;
@@ -242,8 +240,8 @@ __global__ void __launch_bounds__(THREADS, 1) attention_tc_kernel(const __grid_c
     if (!seq_ok && !P.lpt_order && threadIdx.x == 0 && split == 0 && blockIdx.y == 0) flag(FP8KV_DEV_BAD_SEQ_LEN);
     // keys visible to any row of the tile: from the first row's window start
     // to the last row's position (row r is query m = r / G at L - M + m)
-    const int hi0 = TREE ? L - 1 : L - P.M + (R0 + RL - 1) / P.G;
-    const int lo0 = (P.window_left >= 0) ? max(0, L - P.M + (TREE ? 0 : R0 / P.G) - P.window_left) : 0;
+    const int hi0 = L - P.M + (R0 + RL - 1) / P.G;
+    const int lo0 = (P.window_left >= 0) ? max(0, L - P.M + R0 / P.G - P.window_left) : 0;
     const int first_page = lo0 / PS, last_page = hi0 / PS;
     const int nsplit_b = (last_page - first_page + P.split_pages) / P.split_pages;
     if (run && nsplit_b > P.num_splits) {
@@ -532,11 +530,8 @@ __global__ void __launch_bounds__(THREADS, 1) attention_tc_kernel(const __grid_c
         const uint32_t lane_base = tmem + ((uint32_t)(wq * 32) << 16);
         const int rr = R0 + min(r, RL - 1);                 // the row of the (b, hk) block
         const int m = rr / P.G;
-        const int base = L - P.M;
-        const uint64_t word = TREE ? tree_word(P, b, m) : 0;
-        const TreeRow tr = TREE ? tree_row(P, b, m, word, base) : TreeRow{};
-        const int p_r = TREE ? base - 1 : L - P.M + m;      // (a tree's rows: the last key that needs no mask)
-        const int lo_r = TREE ? tr.lo : (P.window_left >= 0) ? max(0, p_r - P.window_left) : 0;
+        const int p_r = L - P.M + m;
+        const int lo_r = (P.window_left >= 0) ? max(0, p_r - P.window_left) : 0;
         const int64_t row_idx = ((int64_t)b * P.M + m) * P.Hq + hk * P.G + rr % P.G;
         const float vs = P.v_scale[P.scale_stride * hk];
         // rows past M*G get Q = 0: their (unused) weights stay finite and their
@@ -608,7 +603,6 @@ __global__ void __launch_bounds__(THREADS, 1) attention_tc_kernel(const __grid_c
             pmax = max(pmax, __shfl_xor_sync(0xffffffffu, pmax, off));
             lomin = min(lomin, __shfl_xor_sync(0xffffffffu, lomin, off));
         }
-        if (TREE) pmax = L - 1;
         float m_run = -INFINITY, l_run = 0.f;               // l_run: this half's columns only
         for (int t = 0; t < n_tiles; ++t) {
             const int sb = t & 1;
@@ -626,13 +620,7 @@ __global__ void __launch_bounds__(THREADS, 1) attention_tc_kernel(const __grid_c
                 if (!dead) {
                     tmem_ld_x64(scol, sv);
                     tmem_wait_ld();
-                    if (TREE && ((k0 + 63 > pmin) || (k0 < lomax))) {
-                        const uint64_t vis = tree_sees64(tr, k0, base);
-                        const uint32_t vis_lo = (uint32_t)vis, vis_hi = (uint32_t)(vis >> 32);
-#pragma unroll
-                        for (int j = 0; j < 64; ++j)
-                            sv[j] = (((j < 32 ? vis_lo : vis_hi) >> (j & 31)) & 1u) ? sv[j] : 0xff800000u;   // -inf
-                    } else if (DUAL && ((k0 + 63 > pmin) || (k0 < lomax))) {
+                    if (DUAL && ((k0 + 63 > pmin) || (k0 < lomax))) {
 #pragma unroll
                         for (int j = 0; j < 64; ++j)
                             if (k0 + j > p_r || k0 + j < lo_r) sv[j] = 0xff800000u;   // -inf
@@ -742,7 +730,6 @@ __global__ void __launch_bounds__(THREADS, 1) attention_tc_kernel(const __grid_c
             // its (max, sum), half the bytes of an fp32 partial
             // (a row with no visible key in this partition has l = 0: weight 0, values 0)
             const float f = direct ? vs / l_tot : (l_tot > 0.f ? 1.0f / l_tot : 0.f);
-            const bool zero = TREE && direct && (word == 0 || l_tot == 0.f);
             // This thread's half row (64 dims: bf16 output or fp32 partial)
             // goes through the free staging buffers to one bulk copy: stores
             // straight from the row-per-thread TMEM layout would touch a
@@ -753,11 +740,7 @@ __global__ void __launch_bounds__(THREADS, 1) attention_tc_kernel(const __grid_c
                 uint32_t ov[32];
                 tmem_ld_x32(lane_base + TM_O + 64 * half + c, ov);
                 tmem_wait_ld();
-                if (zero) {
-                    uint4* dst = (uint4*)(row_stage + c * 2);
-#pragma unroll
-                    for (int v4 = 0; v4 < 4; ++v4) dst[v4] = make_uint4(0, 0, 0, 0);
-                } else if (direct) {
+                if (direct) {
                     uint4* dst = (uint4*)(row_stage + c * 2);
 #pragma unroll
                     for (int v4 = 0; v4 < 4; ++v4)
@@ -891,11 +874,9 @@ __global__ void __launch_bounds__(THREADS, 1) attention_tc_kernel(const __grid_c
                 const float inv = vsc / lsum;
                 const int m = (R0 + r) / P.G;
                 const int64_t orow = ((int64_t)b * P.M + m) * P.Hq + hk * P.G + (R0 + r) % P.G;
-                uint4 o4 =
+                *(uint4*)(P.out + orow * 128 + 8 * ch) =
                     make_uint4(pack_bf16x2(acc[0] * inv, acc[1] * inv), pack_bf16x2(acc[2] * inv, acc[3] * inv),
                                pack_bf16x2(acc[4] * inv, acc[5] * inv), pack_bf16x2(acc[6] * inv, acc[7] * inv));
-                if (TREE && (lsum == 0.f || tree_word(P, b, m) == 0)) o4 = make_uint4(0, 0, 0, 0);
-                *(uint4*)(P.out + orow * 128 + 8 * ch) = o4;
             }
         }
         __syncwarp();
@@ -926,13 +907,10 @@ int launch_attention_tc(const CUtensorMap& tk, const CUtensorMap& tv, const Attn
     // two issuing threads when no new tokens are appended in the kernel (the
     // append encodes them in the converter warps, which then need all six)
     const bool dual = P.k_new == nullptr;
-    auto pick = [&](auto plain, auto trees) { return P.tree ? trees : plain; };
-    auto k = P.page_size == 32
-                 ? (dual ? pick(tc::attention_tc_kernel<32, true, false>, tc::attention_tc_kernel<32, true, true>)
-                         : pick(tc::attention_tc_kernel<32, false, false>, tc::attention_tc_kernel<32, false, true>))
-                 : (dual ? pick(tc::attention_tc_kernel<64, true, false>, tc::attention_tc_kernel<64, true, true>)
-                         : pick(tc::attention_tc_kernel<64, false, false>, tc::attention_tc_kernel<64, false, true>));
-    const void* kern = (const void*)k;
+    const void* kern = P.page_size == 32 ? (dual ? (const void*)tc::attention_tc_kernel<32, true>
+                                                 : (const void*)tc::attention_tc_kernel<32, false>)
+                                         : (dual ? (const void*)tc::attention_tc_kernel<64, true>
+                                                 : (const void*)tc::attention_tc_kernel<64, false>);
     {
         int dev = 0;
         if (cudaGetDevice(&dev) != cudaSuccess) return FP8KV_ERR_CUDA;
@@ -948,6 +926,8 @@ int launch_attention_tc(const CUtensorMap& tk, const CUtensorMap& tv, const Attn
     if (P.cluster > 1 && (P.cluster > 8 || P.cluster != P.num_splits)) return FP8KV_ERR_UNSUPPORTED;
     if (P.lpt_order && (RT > 1 || P.cluster > 1 || (int64_t)P.B * P.num_splits * P.Hkv > INT32_MAX))
         return FP8KV_ERR_UNSUPPORTED;
+    auto k = P.page_size == 32 ? (dual ? tc::attention_tc_kernel<32, true> : tc::attention_tc_kernel<32, false>)
+                               : (dual ? tc::attention_tc_kernel<64, true> : tc::attention_tc_kernel<64, false>);
     e = launch_pdl_cluster(k, grid, dim3(tc::THREADS), tc::SMEM, s, P.cluster, tk, tv, P);
     return e == cudaSuccess ? FP8KV_OK : (cudaGetLastError(), FP8KV_ERR_CUDA);
 }

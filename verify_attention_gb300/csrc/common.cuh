@@ -448,7 +448,7 @@ int status_prompt(unsigned int* s, int clear);     // prompt_attention.cu
 int status_draft_tree(unsigned int* s, int clear);   // draft_tree.cu
 int status_rope_insert(unsigned int* s, int clear);  // rope_insert.cu
 int status_verify_tree(unsigned int* s, int clear);  // verify_tree.cu
-int status_attention_bf16_tc(unsigned int* s, int clear);  // attention_bf16_tc.cu
+int status_attention_tree_tc(unsigned int* s, int clear);  // attention_tree_tc.cu
 
 // OR this translation unit's status word into *s, optionally clearing it.
 static inline int read_status(unsigned int* s, int clear) {
