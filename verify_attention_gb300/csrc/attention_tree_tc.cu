@@ -10,31 +10,40 @@
 // most 2^15, which keeps 11 bits down to 2^-25 of the largest.  Accumulators are fp32.
 //
 // What bounds it: a tile of 128 keys is 32 or 64 KiB of pages, 1400 or 2900 cycles of
-// one SM's share of the HBM rate; its two products with 128 rows are 1024 cycles of
-// the tensor cores.  The chain of a tile, from its scores over the weights to its
-// second product, is longer than either, so what counts is how many are under way:
-// the two softmax groups take half tiles (64 keys) in turn, each with its own
-// maximum, sum and O, merged at the end, and never wait for each other; three S
-// buffers keep the products ahead of them.  (E4M3, both groups on one tile with its
-// maximum exchanged through shared memory: 1.24 us a tile; so: xx.)
+// one SM's share of the HBM rate (long BF16 batches: 64 trees of 12 nodes, up to 32768
+// keys, 772 us, 5.7 TB/s).  Its two products with 128 rows are 1032 cycles of the
+// tensor cores, the way of a tile from its scores over the weights to the end of its
+// second product some 2000, so what counts is how much of it runs side by side:
+//   - the two softmax groups take half tiles (64 keys), each with its own maximum,
+//     sum, O, S and P, merged at the end, and never wait for each other (E4M3, both on
+//     one tile, its maximum exchanged through shared memory: 1.24 us a tile);
+//   - S is read into registers at once, and the next one computed meanwhile;
+//   - three threads issue the products (BF16: 0.80 us a tile; both halves' P.V by one
+//     thread, which then is busy for 1300 cycles a tile, 0.86);
+//   - BF16 stages of K and of V come and go by themselves (before: 0.89).
+// E4M3 takes 1.07 us a tile, 0.94 of it without the widening of V, which shares the
+// shared memory's bandwidth with the products (eight widening warps instead of four:
+// 1.20).
 //
 // One CTA per (partition, row tile x KV head, sequence):
-//   warp 0       TMA producer (tiles of 128 keys into a ring of stages)
-//   warp 1       issues S = Q.K^T of the half tiles u = 0, 1, ... into three buffers
-//   warp 2       issues O += P(u).V
+//   warp 0       TMA producer (tiles of 128 keys into rings of K and V stages); BF16: of
+//                K, warp 12 of V
+//   warp 1       issues S = Q.K^T of both halves of a tile (a product of 128 x 64 x 16
+//                takes 55 cycles to issue, one of 128 x 128 x 16 64)
+//   warps 2, 3   issue O += P.V of the even and of the odd half tiles
 //   warps 4-7, 8-11  softmax of the even and of the odd half tiles, a row a thread
 //                (warps 4+q and 8+q: TMEM lane quarter q); O is rescaled when a row's
 //                maximum grows by more than 2^GROW
-//   warps 3, 12-15   E4M3: widen V; with tokens to append they encode those, one
-//                8-element chunk a thread, and write them over their rows of the
-//                staged tile and into the f16 tile, the cache afterwards.  BF16: warp 3
-//                zeroes V rows that no row of the tile sees (behind the sequence's end,
-//                before its first window): whatever is stored there, 0 times it must
+//   warps 12-15  E4M3: widen V; with tokens to append they encode those, one 8-element
+//                chunk a thread, and write them over their rows of the staged tile and
+//                into the f16 tile, the cache afterwards
+//   warp 13      BF16: zeroes V rows that no row of the tile sees (behind the sequence's
+//                end, before its first window): whatever is stored there, 0 times it must
 //                not reach the output (E4M3: they are widened as zeros)
 // One sequence in 2 to 8 partitions of one row tile: those of a KV head are a
 // thread-block cluster, and each CTA merges its share of the rows from the others'
 // shared memory.
-// TMEM columns: Q 0-63, S/P 3 x 64 (64-255), O 256-383, 384-511.
+// TMEM columns: Q 0-63, S 64-127, 128-191, P 192-223, 224-255, O 256-383, 384-511.
 #include <stdio.h>
 
 #include "attention.cuh"
@@ -54,10 +63,10 @@ constexpr int kMaxStages = 4;
 template <bool FP8>
 struct Cfg {
     static constexpr int STAGES = FP8 ? kMaxStages : 3;
-    static constexpr int STG = (FP8 ? 2 : 4) * HALF;    // K, then V
-    static constexpr int OFF_V = STG / 2;
-    static constexpr int WARPS = FP8 ? 16 : 12, THREADS = 32 * WARPS, CONV = FP8 ? 5 : 1;
-    static constexpr int RING = STAGES * STG;
+    static constexpr int STG = (FP8 ? 1 : 2) * HALF;    // of K, or of V
+    static constexpr int OFF_V = STAGES * STG;          // V stages behind K's
+    static constexpr int WARPS = FP8 ? 16 : 14, THREADS = 32 * WARPS, CONV = FP8 ? 4 : 1;
+    static constexpr int RING = 2 * STAGES * STG;
     static constexpr int SMEM = RING + (FP8 ? VBUFS * VBUF : 0) + 3 * 2 * 128 * 4 + 1024 + 512;
 };
 // epilogue, in the ring (free once the last tile is consumed): half rows, f16, bf16 or
@@ -65,18 +74,20 @@ struct Cfg {
 constexpr int EPI_STRIDE = 272;
 static_assert(2 * 128 * EPI_STRIDE + 128 * 8 <= Cfg<true>::RING && Cfg<true>::RING <= Cfg<false>::RING,
               "epilogue staging exceeds the stage ring");
-constexpr uint32_t TM_Q = 0, TM_S = 64, TM_O = 256, TM_COLS = 512;
+constexpr uint32_t TM_Q = 0, TM_S = 64, TM_P = 192, TM_O = 256, TM_COLS = 512;
 constexpr int kMaxCluster = 8;
 
 enum {
-    B_STG_FULL = 0,
-    B_STG_EMPTY = B_STG_FULL + kMaxStages,
-    B_V_FULL = B_STG_EMPTY + kMaxStages,
+    B_K_FULL = 0,                                       // stages of K and of V
+    B_K_EMPTY = B_K_FULL + kMaxStages,
+    B_W_FULL = B_K_EMPTY + kMaxStages,
+    B_W_EMPTY = B_W_FULL + kMaxStages,
+    B_V_FULL = B_W_EMPTY + kMaxStages,                  // E4M3: widened V
     B_V_EMPTY = B_V_FULL + VBUFS,
-    B_S = B_V_EMPTY + VBUFS,                            // per half and its tile mod 3: S ready
-    B_P = B_S + 6,                                      // ... P written
-    B_S_EMPTY = B_P + 6,                                // per S buffer: P.V of the P over it complete
-    B_PV = B_S_EMPTY + 3,                               // per half: its last P.V complete
+    B_S = B_V_EMPTY + VBUFS,                            // per half: S ready
+    B_S_READ = B_S + 2,                                 // ... S read
+    B_P = B_S_READ + 2,                                 // ... P written
+    B_PV = B_P + 2,                                     // ... its last P.V complete
     B_O = B_PV + 2,                                     // per half: O final
     B_Q_READY = B_O + 2,
     B_IDLE = B_Q_READY + 1,
@@ -111,13 +122,14 @@ __global__ void __launch_bounds__(Cfg<FP8>::THREADS, 1) attention_tree_tc_kernel
     if (threadIdx.x == 0) {
         for (int i = 0; i < B_COUNT; ++i) {
             int count = 1;
-            // a stage: Q.K^T of both halves (one commit) and its V's readers: the
-            // widening warps, or P.V and warp 3
-            if (i >= B_STG_EMPTY && i < B_V_FULL) count = FP8 ? 1 + C::CONV : 3;
+            // V's readers: the widening warps, or P.V of both halves and warp 13
+            if (i >= B_W_EMPTY && i < B_V_FULL) count = FP8 ? C::CONV : 3;
             if (i >= B_V_FULL && i < B_V_EMPTY) count = C::CONV;
-            if (i >= B_P && i < B_S_EMPTY) count = 4;
+            if (i >= B_V_EMPTY && i < B_S) count = 2;
+            if (i >= B_S_READ && i < B_PV) count = 4;
             if (i == B_Q_READY) count = 8;
-            if (i >= B_IDLE && i < B_CLEAN) count = 2;
+            if (i == B_IDLE) count = 3;
+            if (i >= B_PAIR && i < B_CLEAN) count = 2;
             if (i >= B_PATCH) count = C::CONV;
             mbar_init(bar(i), count);
         }
@@ -153,16 +165,17 @@ __global__ void __launch_bounds__(Cfg<FP8>::THREADS, 1) attention_tree_tc_kernel
     }
     // the first page ids, right unless a window moves the partition, are read
     // beside the length
-    constexpr int PPT = NK / PS, BOXES = FP8 ? 2 : 4;       // pages per tile, copies per page
+    constexpr int PPT = NK / PS;                            // pages per tile
+    const bool loads = warp == 0 || (!FP8 && warp == 12);
     int guess_at = -1, guess = 0;
-    if (warp == 0) {
-        guess_at = min(split * P.split_pages + (lane / BOXES & (PPT - 1)), P.mpps - 1);
+    if (loads) {
+        guess_at = min(split * P.split_pages + (lane / 2 & (PPT - 1)), P.mpps - 1);
         guess = P.block_table[(int64_t)b * P.mpps + guess_at];
     }
     // so are the new tokens: a widening thread's first item (chunk ct % 16 of token
     // ct / 16) when the partition starts at or before the first of them
-    const int conv = warp == 3 ? 0 : warp - 11, ct = conv * 32 + lane;
-    const bool converts = warp == 3 || warp >= 12;
+    const int ct = (warp - 12) * 32 + lane;
+    const bool converts = warp >= (FP8 ? 12 : 13);
     uint4 first_k = make_uint4(0, 0, 0, 0), first_v = first_k;
     if (FP8 && P.k_new && converts && ct < P.M * 16) {
         const int64_t src = (((int64_t)b * P.M + (ct >> 4)) * P.Hkv + hk) * 16 + (ct & 15);
@@ -198,89 +211,96 @@ __global__ void __launch_bounds__(Cfg<FP8>::THREADS, 1) attention_tree_tc_kernel
 
     if (!run) {
         // no keys of this sequence fall in this partition (or bad input)
-    } else if (warp == 0) {
+    } else if (loads) {
         // ---------------------------------------------------------- producer
-        // lane BOXES p + j: copy j (E4M3: K, V; BF16: K dims 0-63, 64-127, V likewise)
-        // of page p of the tile
+        // Lane 2 p + j: copy j of page p of the tile.  E4M3: K and V; BF16: dims 0-63
+        // and 64-127 of K (warp 0) or of V (warp 12): a stage of K is free long before
+        // the V of its tile, and the loads of one do not wait for the other's
         const uint64_t policy = policy_evict_first();
         const int32_t* bt = P.block_table + (int64_t)b * P.mpps + page_begin;
-        const int p = lane / BOXES, box = lane % BOXES;
-        const bool is_k = box < BOXES / 2;
+        const int p = lane / 2, j = lane & 1;
+        const bool is_k = FP8 ? j == 0 : warp == 0;
+        const int full = is_k ? B_K_FULL : B_W_FULL;
+        uint8_t* ring = stg + (is_k ? 0 : C::OFF_V) + (FP8 ? 0 : j * HALF) + p * PS * 128;
         int issued = 0;
         int next = p < PPT && p < n_pages ? (page_begin + p == guess_at ? guess : bt[p]) : 0;
         for (int t = 0; t < n_tiles; ++t) {
             const int s = t % STAGES, use = t / STAGES, phys = next, at = t * PPT + p;
             const bool mine = p < PPT && at < n_pages;
             next = p < PPT && at + PPT < n_pages ? bt[at + PPT] : 0;
-            if (use > 0) ok = mbar_wait(bar(B_STG_EMPTY + s), (use - 1) & 1);
+            if (use > 0) {
+                if (FP8 || warp == 0) ok = mbar_wait(bar(B_K_EMPTY + s), (use - 1) & 1);
+                if (ok && (FP8 || warp != 0)) ok = mbar_wait(bar(B_W_EMPTY + s), (use - 1) & 1);
+            }
             if (!__all_sync(0xffffffffu, ok)) break;
-            if (lane == 0) mbar_expect_tx(bar(B_STG_FULL + s), min(PPT, n_pages - t * PPT) * PS * (FP8 ? 256 : 512));
+            const uint32_t bytes = min(PPT, n_pages - t * PPT) * PS * (FP8 ? 128 : 256);
+            if (lane == 0 || (FP8 && lane == 1)) mbar_expect_tx(bar(full + s), bytes);
             __syncwarp();
             if (mine)
-                tma_load_3d(smem_u32(stg + s * C::STG + box * HALF + p * PS * 128), is_k ? &tm_k : &tm_v,
-                            FP8 ? 0 : 64 * (box & 1), hk * PS, phys, bar(B_STG_FULL + s), policy);
+                tma_load_3d(smem_u32(ring + s * C::STG), is_k ? &tm_k : &tm_v, FP8 ? 0 : 64 * j, hk * PS, phys,
+                            bar(full + s), policy);
             __syncwarp();
             issued = t + 1;
         }
         // never leave with copies into this CTA's shared memory in flight
-        for (int t = max(0, issued - STAGES); t < issued; ++t) mbar_wait(bar(B_STG_FULL + t % STAGES), (t / STAGES) & 1);
+        for (int t = max(0, issued - STAGES); t < issued; ++t) mbar_wait(bar(full + t % STAGES), (t / STAGES) & 1);
         __syncwarp();
-    } else if (warp == 1 || warp == 2) {
+    } else if (warp < 4) {
         // ------------------------------------------------------ MMA issue
         constexpr uint32_t BF16 = FP8 ? 0 : (1u << 7) | (1u << 10);      // A and B format of kind::f16
-        constexpr uint32_t ID_QK = idesc(128, NK / 2, false) | BF16, ID_PV = idesc(128, 128, true) | BF16;
+        constexpr uint32_t ID_QK = idesc(128, NK, false) | BF16, ID_PV = idesc(128, 128, true) | BF16;
         const bool leader = elect_one();
-        const int n_half = 2 * n_tiles;
         if (warp == 1) {
+            // both halves of a tile at once
             ok = mbar_wait(bar(B_Q_READY), 0);
-            for (int u = 0; u < n_half; ++u) {
-                const int t = u >> 1, h = u & 1, s = t % STAGES, sb = u % 3;
-                if (ok && h == 0) ok = mbar_wait(bar(B_STG_FULL + s), (t / STAGES) & 1);
-                if (ok && h == 0 && t >= app_t0 && t <= app_t1) ok = mbar_wait(bar(B_PATCH + (t - app_t0)), 0);
-                if (ok && u >= 3) ok = mbar_wait(bar(B_S_EMPTY + sb), (u / 3 - 1) & 1);
+            for (int t = 0; t < n_tiles; ++t) {
+                const int s = t % STAGES;
+                if (ok) ok = mbar_wait(bar(B_K_FULL + s), (t / STAGES) & 1);
+                if (ok && t >= app_t0 && t <= app_t1) ok = mbar_wait(bar(B_PATCH + (t - app_t0)), 0);
+                for (int h = 0; h < 2; ++h)
+                    if (ok && t > 0) ok = mbar_wait(bar(B_S_READ + h), (t - 1) & 1);
                 ok = __all_sync(0xffffffffu, ok);
                 if (!ok) break;
                 fence_after();
                 if (leader) {
-                    const uint32_t k = smem_u32(stg + s * C::STG) + h * (64 * 128);
+                    const uint32_t k = smem_u32(stg + s * C::STG);
                     if (FP8) {
 #pragma unroll
                         for (int ks = 0; ks < 4; ++ks) {
                             const uint64_t bd = sdesc(k + ks * 32, 16, 1024);
-                            mma_f8_ts(tmem + TM_S + 64 * sb, tmem + TM_Q + 8 * ks, bd, ID_QK, ks > 0);
-                            mma_f8_ts(tmem + TM_S + 64 * sb, tmem + TM_Q + 32 + 8 * ks, bd, ID_QK, 1);
+                            mma_f8_ts(tmem + TM_S, tmem + TM_Q + 8 * ks, bd, ID_QK, ks > 0);
+                            mma_f8_ts(tmem + TM_S, tmem + TM_Q + 32 + 8 * ks, bd, ID_QK, 1);
                         }
                     } else {
 #pragma unroll
                         for (int ks = 0; ks < 8; ++ks)
-                            mma_ts(tmem + TM_S + 64 * sb, tmem + TM_Q + 8 * ks,
-                                   desc_lo(k + (ks >> 2) * HALF + (ks & 3) * 32, 16), ID_QK, ks > 0);
+                            mma_ts(tmem + TM_S, tmem + TM_Q + 8 * ks, desc_lo(k + (ks >> 2) * HALF + (ks & 3) * 32, 16), ID_QK,
+                                   ks > 0);
                     }
-                    mma_commit(bar(B_S + 3 * h + t % 3));
-                    if (h == 1) mma_commit(bar(B_STG_EMPTY + s));
+                    mma_commit(bar(B_S));
+                    mma_commit(bar(B_S + 1));
+                    mma_commit(bar(B_K_EMPTY + s));
                 }
                 __syncwarp();
             }
         } else {
-            for (int u = 0; u < n_half; ++u) {
-                const int t = u >> 1, h = u & 1, s = t % STAGES, vb = t % VBUFS, sb = u % 3;
-                if (h == 0) {
-                    ok = FP8 ? mbar_wait(bar(B_V_FULL + vb), (t / VBUFS) & 1) : mbar_wait(bar(B_STG_FULL + s), (t / STAGES) & 1);
-                    if (ok && dirty(t)) ok = mbar_wait(bar(B_CLEAN + (t > 0)), 0);
-                }
-                if (ok) ok = mbar_wait(bar(B_P + 3 * h + t % 3), (t / 3) & 1);
+            const int h = warp - 2;
+            for (int t = 0; t < n_tiles; ++t) {
+                const int s = t % STAGES, vb = t % VBUFS;
+                ok = FP8 ? mbar_wait(bar(B_V_FULL + vb), (t / VBUFS) & 1) : mbar_wait(bar(B_W_FULL + s), (t / STAGES) & 1);
+                if (ok && dirty(t)) ok = mbar_wait(bar(B_CLEAN + (t > 0)), 0);
+                if (ok) ok = mbar_wait(bar(B_P + h), t & 1);
                 ok = __all_sync(0xffffffffu, ok);
                 if (!ok) break;
                 fence_after();
                 if (leader) {
-                    const uint32_t v = smem_u32(FP8 ? vbuf + vb * VBUF : stg + s * C::STG + C::OFF_V) + h * (64 * 128);
+                    const uint32_t v = smem_u32(FP8 ? vbuf + vb * VBUF : stg + C::OFF_V + s * C::STG) + h * (64 * 128);
 #pragma unroll
                     for (int kk = 0; kk < 4; ++kk)
-                        mma_ts(tmem + TM_O + 128 * h, tmem + TM_S + 64 * sb + 8 * kk, desc_lo(v + kk * 2048, HALF), ID_PV,
+                        mma_ts(tmem + TM_O + 128 * h, tmem + TM_P + 32 * h + 8 * kk, desc_lo(v + kk * 2048, HALF), ID_PV,
                                t > 0 || kk > 0);
                     mma_commit(bar(B_PV + h));
-                    mma_commit(bar(B_S_EMPTY + sb));
-                    if (h == 1) mma_commit(FP8 ? bar(B_V_EMPTY + vb) : bar(B_STG_EMPTY + s));
+                    mma_commit(FP8 ? bar(B_V_EMPTY + vb) : bar(B_W_EMPTY + s));
                     if (t == n_tiles - 1) mma_commit(bar(B_O + h));
                 }
                 __syncwarp();
@@ -295,11 +315,11 @@ __global__ void __launch_bounds__(Cfg<FP8>::THREADS, 1) attention_tree_tc_kernel
         // ------------------------------------------------- V rows without a reader
         for (int t = 0; t < n_tiles; ++t) {
             const int s = t % STAGES;
-            ok = __all_sync(0xffffffffu, mbar_wait(bar(B_STG_FULL + s), (t / STAGES) & 1));
+            ok = __all_sync(0xffffffffu, mbar_wait(bar(B_W_FULL + s), (t / STAGES) & 1));
             if (!ok) break;
             if (dirty(t)) {
                 const int zlo = zlo_of(t), zhi = zhi_of(t);
-                uint8_t* v = stg + s * C::STG + C::OFF_V;
+                uint8_t* v = stg + C::OFF_V + s * C::STG;
                 for (int i = lane; i < NK * 16; i += 32) {
                     const int r = i >> 4;
                     if (r < zlo || r >= zhi) *(uint4*)(v + ((i >> 3) & 1) * HALF + r * 128 + (i & 7) * 16) = make_uint4(0, 0, 0, 0);
@@ -309,7 +329,7 @@ __global__ void __launch_bounds__(Cfg<FP8>::THREADS, 1) attention_tree_tc_kernel
                 if (lane == 0) mbar_arrive(bar(B_CLEAN + (t > 0)));
             }
             __syncwarp();
-            if (lane == 0) mbar_arrive(bar(B_STG_EMPTY + s));
+            if (lane == 0) mbar_arrive(bar(B_W_EMPTY + s));
         }
     } else if (converts) {
         // ---------------------------------------------------------- V widening
@@ -337,9 +357,10 @@ __global__ void __launch_bounds__(Cfg<FP8>::THREADS, 1) attention_tree_tc_kernel
         }
         for (int t = 0; t < n_tiles; ++t) {
             const int s = t % STAGES, vb = t % VBUFS;
-            ok = mbar_wait(bar(B_STG_FULL + s), (t / STAGES) & 1);
+            ok = mbar_wait(bar(B_W_FULL + s), (t / STAGES) & 1);
             const int k0 = k_begin + t * NK;
             const bool patched = t >= app_t0 && t <= app_t1;
+            if (patched) ok = ok && mbar_wait(bar(B_K_FULL + s), (t / STAGES) & 1);
             if (patched && __all_sync(0xffffffffu, ok)) {
                 // the new rows of K over the staged tile, before its Q.K^T
                 uint8_t* kst = stg + s * C::STG;
@@ -359,7 +380,7 @@ __global__ void __launch_bounds__(Cfg<FP8>::THREADS, 1) attention_tree_tc_kernel
             // rows [nlo, nhi) hold new tokens: their staged V may be old
             const int nlo = patched ? max(0, app_lo - k0) : 0, nhi = patched ? min(NK, app_hi - k0) : 0;
             const int zlo = zlo_of(t), zhi = zhi_of(t);
-            const uint8_t* src = stg + s * C::STG + C::OFF_V;
+            const uint8_t* src = stg + C::OFF_V + s * C::STG;
             uint8_t* dst = vbuf + vb * VBUF;
             constexpr int PER = (NK * 8 + CONV_THREADS - 1) / CONV_THREADS;   // chunks a thread
             uint4 code[PER];
@@ -405,7 +426,7 @@ __global__ void __launch_bounds__(Cfg<FP8>::THREADS, 1) attention_tree_tc_kernel
             fence_proxy_async();
             __syncwarp();
             if (lane == 0) {
-                mbar_arrive(bar(B_STG_EMPTY + s));
+                mbar_arrive(bar(B_W_EMPTY + s));
                 mbar_arrive(bar(B_V_FULL + vb));
             }
         }
@@ -503,23 +524,31 @@ __global__ void __launch_bounds__(Cfg<FP8>::THREADS, 1) attention_tree_tc_kernel
         for (int off = 1; off < 32; off <<= 1) lomax = max(lomax, __shfl_xor_sync(0xffffffffu, lomax, off));
         // this half's maximum and sum
         float m_run = -INFINITY, l_run = 0.f;
-        const uint32_t o_col = lane_base + TM_O + 128 * half;
+        const uint32_t o_col = lane_base + TM_O + 128 * half, s_col = lane_base + TM_S + 64 * half;
+        const uint32_t p_col = lane_base + TM_P + 32 * half;
         for (int t = 0; t < n_tiles && ok; ++t) {
-            const uint32_t s_col = lane_base + TM_S + 64 * ((2 * t + half) % 3);
-            ok = __all_sync(0xffffffffu, mbar_wait(bar(B_S + 3 * half + t % 3), (t / 3) & 1));
+            ok = __all_sync(0xffffffffu, mbar_wait(bar(B_S + half), t & 1));
             if (!ok) break;
             fence_after();
             const int k0 = k_begin + t * NK + 64 * half;    // first key of this half
             if (!active || k0 >= L) {
                 // no row of this warp sees any key of it: P = 0
+                if (lane == 0) mbar_arrive(bar(B_S_READ + half));
+                if (t > 0) ok = __all_sync(0xffffffffu, mbar_wait(bar(B_PV + half), (t - 1) & 1));
+                if (!ok) break;
+                fence_after();
                 uint32_t zero[32];
 #pragma unroll
                 for (int j = 0; j < 32; ++j) zero[j] = 0u;
-                tmem_st_x32(s_col, zero);
+                tmem_st_x32(p_col, zero);
             } else {
                 uint32_t sv[64];
                 tmem_ld_x64(s_col, sv);
                 tmem_wait_ld();
+                // S is in registers: the next product may go over it
+                fence_before();
+                __syncwarp();
+                if (lane == 0) mbar_arrive(bar(B_S_READ + half));
                 if (k0 + 63 >= base || k0 < lomax) {
                     const uint64_t vis = tree_sees64(tr, k0, base);
                     const uint32_t vis_lo = (uint32_t)vis, vis_hi = (uint32_t)(vis >> 32);
@@ -564,22 +593,21 @@ __global__ void __launch_bounds__(Cfg<FP8>::THREADS, 1) attention_tree_tc_kernel
                 const float neg = (m_run == -INFINITY) ? 0.f : BIAS - m_run;
                 const uint64_t mult2 = pack2(mult, mult), neg2 = pack2(neg, neg);
                 uint64_t sum2 = 0;
+                uint32_t pw[32];
 #pragma unroll
-                for (int c = 0; c < 2; ++c) {
-                    uint32_t pw[16];
-#pragma unroll
-                    for (int j = 0; j < 16; ++j) {
-                        float p0, p1;
-                        unpack2(fma2(pack2(__uint_as_float(sv[32 * c + 2 * j]), __uint_as_float(sv[32 * c + 2 * j + 1])),
-                                     mult2, neg2),
-                                p0, p1);
-                        p0 = ex2(p0);
-                        p1 = ex2(p1);
-                        sum2 = add2(sum2, pack2(p0, p1));
-                        pw[j] = FP8 ? pack_f16x2(p0, p1) : pack_bf16x2(p0, p1);
-                    }
-                    tmem_st_x16(s_col + 16 * c, pw);
+                for (int j = 0; j < 32; ++j) {
+                    float p0, p1;
+                    unpack2(fma2(pack2(__uint_as_float(sv[2 * j]), __uint_as_float(sv[2 * j + 1])), mult2, neg2), p0, p1);
+                    p0 = ex2(p0);
+                    p1 = ex2(p1);
+                    sum2 = add2(sum2, pack2(p0, p1));
+                    pw[j] = FP8 ? pack_f16x2(p0, p1) : pack_bf16x2(p0, p1);
                 }
+                // P.V of tile t - 1 has read P
+                if (t > 0) ok = __all_sync(0xffffffffu, mbar_wait(bar(B_PV + half), (t - 1) & 1));
+                if (!ok) break;
+                fence_after();
+                tmem_st_x32(p_col, pw);
                 float sum0, sum1;
                 unpack2(sum2, sum0, sum1);
                 l_run += sum0 + sum1;
@@ -587,7 +615,7 @@ __global__ void __launch_bounds__(Cfg<FP8>::THREADS, 1) attention_tree_tc_kernel
             tmem_wait_st();
             fence_before();
             __syncwarp();
-            if (lane == 0) mbar_arrive(bar(B_P + 3 * half + t % 3));
+            if (lane == 0) mbar_arrive(bar(B_P + half));
         }
         // ------------------------------------------------------------ epilogue
         // both halves' O and (max, sum); this thread merges 64 dims of its row
