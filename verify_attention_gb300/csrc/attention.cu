@@ -1342,7 +1342,9 @@ static int attention_call(const void* k_new, const void* v_new, const void* q, c
     // one sequence in at most 8 partitions and one row tile: the partitions
     // of a KV head run as one thread-block cluster and combine in distributed
     // shared memory
-    P.cluster = ((use_tc || tree_tc) && B == 1 && RT == 1 && plan.num_splits > 1 && plan.num_splits <= 8) ? plan.num_splits : 0;
+    P.cluster = (((use_tc && RT == 1) || tree_tc) && B == 1 && plan.num_splits > 1 && plan.num_splits <= 8)
+                    ? plan.num_splits
+                    : 0;
     // several sequences split into partitions of unequal length: longest first
     const bool lpt = f16_parts && B > 1 && RT == 1 && plan.num_splits > 1;
     if (lpt)

@@ -40,7 +40,7 @@
 //   warp 13      BF16: zeroes V rows that no row of the tile sees (behind the sequence's
 //                end, before its first window): whatever is stored there, 0 times it must
 //                not reach the output (E4M3: they are widened as zeros)
-// One sequence in 2 to 8 partitions of one row tile: those of a KV head are a
+// One sequence in 2 to 8 partitions: those of a KV head and row tile are a
 // thread-block cluster, and each CTA merges its share of the rows from the others'
 // shared memory.
 // TMEM columns: Q 0-63, S 64-127, 128-191, P 192-223, 224-255, O 256-383, 384-511.
@@ -783,7 +783,7 @@ int launch_attention_tree_tc(const CUtensorMap& tk, const CUtensorMap& tv, const
     const int RT = (P.R + 127) / 128;
     if (!P.tree || P.R <= 16 || (int64_t)RT * P.Hkv > 65535 || (P.split_pages * P.page_size) % ttc::NK || P.scale_stride)
         return FP8KV_ERR_UNSUPPORTED;
-    if (P.cluster > 1 && (P.cluster > ttc::kMaxCluster || P.cluster != P.num_splits || RT > 1 || P.lpt_order))
+    if (P.cluster > 1 && (P.cluster > ttc::kMaxCluster || P.cluster != P.num_splits || P.lpt_order))
         return FP8KV_ERR_UNSUPPORTED;
     if ((P.k_new && (!fp8 || RT > 1)) || (P.lpt_order && RT > 1)) return FP8KV_ERR_UNSUPPORTED;
     const dim3 grid(P.num_splits, P.Hkv * RT, P.B);
