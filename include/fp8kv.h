@@ -522,7 +522,7 @@ int fp8kv_rope_insert(const void* q, int64_t q_stride, const void* k, int64_t k_
  *   split_tokens (host) 0, or a multiple of page_size; of 128 for more than 16 rows
  *              M * Hq/Hkv per KV head
  *   every other argument, the workspace and the device checks: as
- *   fp8kv_append_paged_attention (per-tensor scales).
+ *   fp8kv_append_paged_attention (per-tensor scales); out must not overlap q.
  * Supported: D = 128, page_size 32 or 64, Hq % Hkv == 0, 1 <= M <= 64, every cache
  * type.  With k_new, the rows of padding nodes are written too.
  */
@@ -576,7 +576,7 @@ int fp8kv_verify_tree(const void* target_probs, int64_t target_stride, const voi
  * token is not in the cache: with the next tree it is node 0.
  *
  *   k_caches, v_caches (host) arrays of n_layers (1 .. 64) device pointers, each a
- *     cache of its own, all of the same cache_dtype, num_pages and Hkv
+ *     cache of its own (none overlaps another), all of the same cache_dtype, num_pages and Hkv
  *   block_table, seq_lens (device) as fp8kv_paged_attention, the same for all layers
  *   path         (device) int32 [B][M], as fp8kv_verify_tree writes it
  *   new_seq_lens (device) int32 [B]; must not overlap the other arguments

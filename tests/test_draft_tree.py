@@ -47,7 +47,9 @@ def test_rope_insert_checks_its_arguments(L):
     _refusals(L.fp8kv_rope_insert, args, [
         ({"q": NULL}, 1), ({"k": NULL}, 1), ({"v": NULL}, 1), ({"pos": NULL}, 1), ({"cs": NULL}, 1), ({"qo": NULL}, 1),
         ({"slot": NULL}, 1), ({"kc": NULL}, 1), ({"vc": NULL}, 1), ({"ks": NULL}, 1), ({"vs": NULL, "dt": 2}, 1),
-        ({"qo": P16}, 1), ({"q": odd}, 1), ({"cs": odd}, 1), ({"kc": odd}, 1), ({"qs": 9208}, 1), ({"qs": 9220}, 1),
+        ({"qo": P16}, 1), ({"qo": ctypes.c_void_p((1 << 20) + 4 * 18432 - 16)}, 1),
+        ({"k": ctypes.c_void_p((1 << 24) + 4 * 18432 - 16)}, 1), ({"v": ctypes.c_void_p((1 << 24) - 4 * 2048 + 16)}, 1),
+        ({"q": odd}, 1), ({"cs": odd}, 1), ({"kc": odd}, 1), ({"qs": 9208}, 1), ({"qs": 9220}, 1),
         ({"ks_": 1016}, 1), ({"vs_": 1028}, 1), ({"rot": 0}, 1), ({"rot": 136}, 1), ({"rot": 63}, 1), ({"rot": 12}, 2),
         ({"D": 64, "rot": 64}, 2), ({"ps": 48}, 2), ({"dt": 3}, 1), ({"T": -1}, 1), ({"maxp": 0}, 1), ({"Hq": 0}, 1),
         ({"T": 0, "q": NULL}, 0)])
@@ -56,8 +58,9 @@ def test_rope_insert_checks_its_arguments(L):
 def test_tree_attention_checks_its_arguments(L):
     args = dict(kn=NULL, vn=NULL, q=P16, k=P16, v=P16, dt=0, bt=P16, mpps=4, sl=P16, maxL=100, mask=P16, B=1, M=12,
                 Hq=72, Hkv=8, D=128, ps=32, P=16, ks=P16, vs=P16, sm=0.088, wl=-1, split=0, ws=P16, wsb=1 << 30,
-                out=P16, s=NULL)
+                out=Q16, s=NULL)
     _refusals(L.fp8kv_tree_attention, args, [
+        ({"out": P16}, 1), ({"out": ctypes.c_void_p((1 << 20) + 12 * 18432 - 16)}, 1),
         ({"mask": NULL}, 1), ({"q": NULL}, 1), ({"out": NULL}, 1), ({"M": 65, "maxL": 128}, 2), ({"M": 0}, 1),
         ({"D": 64}, 2), ({"ps": 16}, 2), ({"wl": -2}, 1), ({"Hq": 70}, 1), ({"kn": P16}, 1), ({"ks": NULL}, 1),
         ({"split": 96}, 2), ({"split": 64, "dt": 1}, 2), ({"split": 32, "dt": 2}, 2), ({"dt": 5}, 1),
@@ -81,10 +84,12 @@ def test_keep_path_checks_its_arguments(L):
     two = (ctypes.c_void_p * 2)(1 << 20, 1 << 21)
     odd = (ctypes.c_void_p * 2)(1 << 20, (1 << 21) + 8)
     none = (ctypes.c_void_p * 2)(1 << 20, None)
-    args = dict(k=two, v=two, n=2, dt=0, bt=P16, mpps=4, sl=P16, maxL=100, path=P16, B=2, M=12, Hkv=8, D=128, P=16,
+    other = (ctypes.c_void_p * 2)(1 << 22, 1 << 23)
+    half = (ctypes.c_void_p * 2)(1 << 22, (1 << 22) + 16 * 8 * 32 * 128 - 16)
+    args = dict(k=two, v=other, n=2, dt=0, bt=P16, mpps=4, sl=P16, maxL=100, path=P16, B=2, M=12, Hkv=8, D=128, P=16,
                 ps=32, new=Q16, s=NULL)
     _refusals(L.fp8kv_cache_keep_path, args, [
-        ({"k": NULL}, 1), ({"v": none}, 1), ({"v": odd}, 1), ({"bt": NULL}, 1), ({"sl": NULL}, 1), ({"path": NULL}, 1),
+        ({"k": NULL}, 1), ({"v": none}, 1), ({"v": odd}, 1), ({"v": two}, 1), ({"v": half}, 1), ({"bt": NULL}, 1), ({"sl": NULL}, 1), ({"path": NULL}, 1),
         ({"new": NULL}, 1), ({"new": P16}, 1), ({"new": ctypes.c_void_p((1 << 20) + 4)}, 1), ({"n": 0}, 1),
         ({"n": 65}, 2), ({"M": 65, "maxL": 128}, 2), ({"dt": 9}, 1), ({"D": 64}, 2), ({"ps": 16}, 2), ({"maxL": 11}, 1),
         ({"Hkv": 0}, 1), ({"B": 0, "k": NULL}, 0)])
@@ -658,6 +663,9 @@ def test_keep_path(kind, layers, B, M, H, ps):
         assert np.array_equal(c.cpu().numpy() if kind != "bf16" else c.float().cpu().numpy(), w)
     assert new.tolist() == [n - M + int((path[b] >= 0).sum()) for b, n in enumerate(lens)]
     _status()
+    with pytest.raises(ValueError):
+        fp8kv.fp8kv_cache_keep_path(caches[:layers], caches[:layers], _cuda(bt), _cuda(np.array(lens, np.int32)),
+                                    _cuda(path), max(lens))
 
 
 @pytest.mark.gpu

@@ -1210,6 +1210,8 @@ static int attention_call(const void* k_new, const void* v_new, const void* q, c
     if (max_seq_len < M || (int64_t)max_seq_len > (int64_t)max_pages_per_seq * page_size)
         return FP8KV_ERR_INVALID_ARG;
     if (!(sm_scale == sm_scale)) return FP8KV_ERR_INVALID_ARG;
+    // (the CTAs of several partitions read the same Q rows)
+    if (tree && overlap(out, (size_t)B * M * Hq * D * 2, q, (size_t)B * M * Hq * D * 2)) return FP8KV_ERR_INVALID_ARG;
     const size_t need = ws_bytes(B, M, Hq, Hkv, plan);
     if (need && (!workspace || workspace_bytes < need || !al16(workspace))) return FP8KV_ERR_WORKSPACE;
 

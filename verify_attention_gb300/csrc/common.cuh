@@ -437,6 +437,12 @@ __device__ __forceinline__ float2 dsmem_ld8(uint32_t a) {
 }
 __device__ __forceinline__ void cluster_wait() { asm volatile("barrier.cluster.wait.acquire.aligned;" ::: "memory"); }
 
+// two ranges of bytes (host)
+inline bool overlap(const void* a, size_t na, const void* b, size_t nb) {
+    const uintptr_t x = reinterpret_cast<uintptr_t>(a), y = reinterpret_cast<uintptr_t>(b);
+    return x < y + nb && y < x + na;
+}
+
 int launch_status();                    // FP8KV_OK or FP8KV_ERR_CUDA after a launch
 int num_sms();                          // SM count of the current device
 void set_dispatch(const char* text);    // per-thread record of the last dispatch

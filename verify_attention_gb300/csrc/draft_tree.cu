@@ -1,6 +1,8 @@
 // draft_tree.cu -- what a step of speculative decoding over a tree of drafted
 // tokens needs beside its attention: the tree's ancestors, positions and cache
 // slots before it, and the accepted path's cache rows moved together after it.
+#include <algorithm>
+
 #include "attention.cuh"
 #include "common.cuh"
 
@@ -212,11 +214,6 @@ __global__ void __launch_bounds__(256) keep_path_kernel(const __grid_constant__ 
 
 using namespace fp8kv;
 
-static bool overlap(const void* a, size_t na, const void* b, size_t nb) {
-    const uintptr_t x = reinterpret_cast<uintptr_t>(a), y = reinterpret_cast<uintptr_t>(b);
-    return x < y + nb && y < x + na;
-}
-
 extern "C" int fp8kv_tree_metadata(const int32_t* parents, const int32_t* seq_lens, const int32_t* block_table,
                                    int max_pages_per_seq, int max_seq_len, int B, int M, int num_pages, int page_size,
                                    uint64_t* tree_mask, int64_t* positions, int64_t* slot_mapping, void* stream) {
@@ -255,12 +252,20 @@ extern "C" int fp8kv_cache_keep_path(void* const* k_caches, void* const* v_cache
         overlap(new_seq_lens, len_bytes, block_table, len_bytes * max_pages_per_seq))
         return FP8KV_ERR_INVALID_ARG;
     KeepParams P;
+    uintptr_t at[2 * kMaxLayers];
     for (int i = 0; i < n_layers; ++i) {
-        const uintptr_t k = reinterpret_cast<uintptr_t>(k_caches[i]), v = reinterpret_cast<uintptr_t>(v_caches[i]);
-        if (!k || !v || (k & 15) || (v & 15)) return FP8KV_ERR_INVALID_ARG;
         P.k[i] = (uint8_t*)k_caches[i];
         P.v[i] = (uint8_t*)v_caches[i];
+        at[2 * i] = reinterpret_cast<uintptr_t>(P.k[i]);
+        at[2 * i + 1] = reinterpret_cast<uintptr_t>(P.v[i]);
+        if (!P.k[i] || !P.v[i] || ((at[2 * i] | at[2 * i + 1]) & 15)) return FP8KV_ERR_INVALID_ARG;
     }
+    // rows of a cache that is there twice would move twice
+    const int row_bytes = cache_dtype == FP8KV_CACHE_BF16 ? 256 : cache_dtype == FP8KV_CACHE_E4M3 ? 128 : kInt4RowBytes;
+    const uintptr_t cache_bytes = (uintptr_t)num_pages * Hkv * page_size * row_bytes;
+    std::sort(at, at + 2 * n_layers);
+    for (int i = 1; i < 2 * n_layers; ++i)
+        if (at[i] - at[i - 1] < cache_bytes) return FP8KV_ERR_INVALID_ARG;
     P.block_table = block_table;
     P.seq_lens = seq_lens;
     P.path = path;

@@ -205,7 +205,12 @@ extern "C" int fp8kv_rope_insert(const void* q, int64_t q_stride, const void* k,
     if (cache_dtype != FP8KV_CACHE_BF16 && (!k_scale || !v_scale)) return FP8KV_ERR_INVALID_ARG;
     for (const void* p : {q, k, v, (const void*)cos_sin, (const void*)q_out, (const void*)k_cache, (const void*)v_cache})
         if (reinterpret_cast<uintptr_t>(p) & 15) return FP8KV_ERR_INVALID_ARG;
-    if (q == q_out) return FP8KV_ERR_INVALID_ARG;
+    // rows are read while others are written
+    const size_t out_bytes = (size_t)T * Hq * D * 2, k_row = (size_t)Hkv * D * 2;
+    if (overlap(q_out, out_bytes, q, (size_t)(T - 1) * q_stride * 2 + (size_t)Hq * D * 2) ||
+        overlap(q_out, out_bytes, k, (size_t)(T - 1) * k_stride * 2 + k_row) ||
+        overlap(q_out, out_bytes, v, (size_t)(T - 1) * v_stride * 2 + k_row))
+        return FP8KV_ERR_INVALID_ARG;
     RopeParams P;
     P.q = (const uint16_t*)q;
     P.k = (const uint16_t*)k;

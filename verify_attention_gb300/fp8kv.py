@@ -795,7 +795,8 @@ class PreparedKeepPath:
         for t in (*k_caches, *v_caches):
             if _dev(t, "caches").dtype != first.dtype or t.shape != first.shape or t.device != first.device:
                 raise ValueError("all caches must have the same type, shape and device")
-        if len({t.data_ptr() for t in (*k_caches, *v_caches)}) != 2 * n:
+        at, size = sorted(t.data_ptr() for t in (*k_caches, *v_caches)), first.numel() * first.element_size()
+        if any(b - a < size for a, b in zip(at, at[1:])):
             raise ValueError("every layer must have a K and a V cache of its own")
         _dev(block_table, "block_table", torch.int32), _dev(seq_lens, "seq_lens", torch.int32)
         _dev(path, "path", torch.int32)
