@@ -24,6 +24,7 @@
 // for one sequence of 131072 tokens).  The weights, the sums and the prefixes are
 // pairs of fp32 instead, hi + lo with the rounding error of each step in lo (the
 // two-sum and two-product of Dekker and Knuth): 2^-45 of the weight a step.
+#include <stdlib.h>
 #include "attention.cuh"
 #include "common.cuh"
 
@@ -31,7 +32,7 @@ namespace fp8kv {
 
 int status_verify_tree(unsigned int* s, int clear) { return read_status(s, clear); }
 
-constexpr int kVerifyThreads = 512, kVerifyWarps = kVerifyThreads / 32, kVerifyMaxCluster = 16;
+constexpr int kVerifyThreads = 256, kVerifyWarps = kVerifyThreads / 32, kVerifyMaxCluster = 16;
 
 struct VerifyParams {
     const void *p, *q;
@@ -107,22 +108,24 @@ __device__ __forceinline__ F2 before_lane(F2 scan, int at, F2 base) {
 
 // The weights of a node's row after k children fell: step j takes w to (w a_j -
 // b_j q)+, a_j a power of two that keeps the weights near 1 and b_j = S a_j.
-struct VerifyStep {
-    float a, bh, bl;
+struct __align__(16) VerifyStep {
+    float a, bh, bl, unused;
 };
 
-// (negative, zero and NaN: nothing left)
+// (Negative, zero and NaN: nothing left.  The differences are exact by the short sum:
+// where the first operand is the smaller one, either nothing is left, or they are
+// within a factor of two of each other and the difference itself is exact.)
 __device__ __forceinline__ F2 step_weight(F2 w, float q, VerifyStep s) {
     const float th = __fmul_rn(s.bh, q), tl = __fmaf_rn(s.bl, q, __fmaf_rn(s.bh, q, -th));
-    const F2 d = two_sum(__fmul_rn(w.hi, s.a), -th);
+    const F2 d = fast_two_sum(__fmul_rn(w.hi, s.a), -th);
     const float lo = __fadd_rn(d.lo, __fmaf_rn(w.lo, s.a, -tl));
     const bool some = __fadd_rn(d.hi, lo) > 0.f;
     return {some ? d.hi : 0.f, some ? lo : 0.f};
 }
 // a node's first step: S = 1, so w - q, exactly
 __device__ __forceinline__ F2 first_step(float p, float q) {
-    const F2 d = two_sum(p, -q);
-    return {d.hi > 0.f ? d.hi : 0.f, d.hi > 0.f ? d.lo : 0.f};
+    const F2 d = fast_two_sum(p, -q);
+    return {fmaxf(d.hi, 0.f), d.hi > 0.f ? d.lo : 0.f};
 }
 
 template <typename T>
@@ -152,19 +155,28 @@ __device__ __forceinline__ void widen(uint4 x, float (&f)[8]) {
     }
 }
 
-// One row as groups of N elements on 16-byte boundaries: group g holds elements
-// N g - skew .. + N - 1, those outside [0, V) as zeros.
+// One row as groups of 16 bytes: group g holds elements N g - skew .. + N - 1, those
+// outside [0, V) as zeros.
 template <typename T>
 struct Row {
     static constexpr int N = 16 / sizeof(T);
-    const T* at;                // element -skew, on a 16-byte boundary
+    const T* at;                // element -skew
     int skew, V;
-    __device__ __forceinline__ Row(const T* row, int skew_, int V_) : at(row - skew_), skew(skew_), V(V_) {}
-    // any group, an element at a time; -1: zeros
-    __device__ __forceinline__ void load(int g, float (&f)[N]) const {
+    bool aligned;               // on a 16-byte boundary
+    __device__ __forceinline__ Row(const T* row, int skew_, int V_)
+        : at(row - skew_), skew(skew_), V(V_), aligned((reinterpret_cast<uintptr_t>(row - skew_) & 15) == 0) {}
+    __device__ __forceinline__ uint4 load(int g) const {
         const int first = N * g - skew;
+        if (aligned && first >= 0 && first + N <= V) return __ldg(reinterpret_cast<const uint4*>(at) + g);
+        uint32_t w[4] = {};
 #pragma unroll
-        for (int i = 0; i < N; ++i) f[i] = g >= 0 && first + i >= 0 && first + i < V ? prob(at[(int64_t)N * g + i]) : 0.f;
+        for (int i = 0; i < N; ++i)
+            if (first + i >= 0 && first + i < V) {
+                const T x = at[(int64_t)N * g + i];
+                if constexpr (N == 4) w[i] = __float_as_uint(x);
+                else w[i >> 1] |= (uint32_t)x << (16 * (i & 1));
+            }
+        return {w[0], w[1], w[2], w[3]};
     }
 };
 
@@ -185,8 +197,8 @@ __device__ __forceinline__ void send_part(uint32_t to, uint32_t mbar, F2 v, int 
 enum { PASS_SUM = 1, PASS_DRAW = 2, PASS_ROW = 3, PASS_STOP = 4 };
 
 template <typename T, bool DRAFT>
-__global__ void __launch_bounds__(kVerifyThreads, 2) verify_tree_kernel(VerifyParams P) {
-    constexpr int N = Row<T>::N, U = (DRAFT ? 8 : 16) / N;      // groups a lane has in flight
+__global__ void __launch_bounds__(kVerifyThreads, DRAFT ? 3 : 4) verify_tree_kernel(VerifyParams P) {
+    constexpr int N = Row<T>::N, U = (DRAFT ? 8 : 16) / N;      // groups a lane has in flight of a row
     __shared__ int tok[64], fallen[64], path[64];
     __shared__ float un[64], pw[64], qw[64];
     __shared__ unsigned kids[64][2], stands[2];         // bits: a node's children; nodes that stand as first children
@@ -288,7 +300,7 @@ __global__ void __launch_bounds__(kVerifyThreads, 2) verify_tree_kernel(VerifyPa
                     // S a power of two away from [1, 2)
                     const int e = S.hi > 0.f ? min(max(127 - (int)(__float_as_uint(S.hi) >> 23), -120), 120) : 0;
                     const float a = __uint_as_float((unsigned)(127 + e) << 23);
-                    if (lane == 0) steps[k] = {a, S.hi * a, S.lo * a};
+                    if (lane == 0) steps[k] = {a, S.hi * a, S.lo * a, 0.f};
                 } else {
                     if (lane == 0) fallen[k] = x;
                     S = S - w;
@@ -312,14 +324,49 @@ __global__ void __launch_bounds__(kVerifyThreads, 2) verify_tree_kernel(VerifyPa
         const int cur = s_cur, k = state == PASS_ROW ? 0 : s_fallen;
         const T* p_row = p_rows + (int64_t)cur * P.p_stride;
         const T* q_row = q_rows + (int64_t)cur * P.q_stride;
-        // groups of 16 bytes, cut at the boundaries of p's row; q's only if they are its own too
+        // groups of 16 bytes, cut at the boundaries of p's row (q's may be others)
         const int skew = (int)((reinterpret_cast<uintptr_t>(p_row) & 15) / sizeof(T));
-        const bool q_aligned = DRAFT && (int)((reinterpret_cast<uintptr_t>(q_row) & 15) / sizeof(T)) == skew;
         const Row<T> pr(p_row, skew, V), qr(q_row, skew, V);
         const int groups = (V + skew + N - 1) / N;
-        // those that one load brings from each row, without a look at the row's ends
-        const int whole0 = skew ? 1 : 0, whole1 = DRAFT && !q_aligned ? 0 : (V + skew) / N;
         const int per_warp = ((groups + C * kVerifyWarps - 1) / (C * kVerifyWarps) + 31) & ~31;
+        // what is left of a group
+        auto weigh = [&](uint4 x, uint4 y, int g, float (&hi)[N], float (&lo)[N]) {
+            widen(x, hi);
+            if (DRAFT) {
+                float qf[N];
+                widen(y, qf);
+#pragma unroll
+                for (int i = 0; i < N; ++i) {
+                    qf[i] = fmaxf(qf[i], 0.f);
+                    const F2 w = first_step(hi[i], qf[i]);  // (k = 0: q is 0 here)
+                    hi[i] = w.hi;
+                    lo[i] = w.lo;
+                }
+#pragma unroll 1
+                for (int j = 1; j < k; ++j) {
+                    const VerifyStep s = steps[j];
+#pragma unroll
+                    for (int i = 0; i < N; ++i) {
+                        const F2 w = step_weight({hi[i], lo[i]}, qf[i], s);
+                        hi[i] = w.hi;
+                        lo[i] = w.lo;
+                    }
+                }
+            } else {
+#pragma unroll
+                for (int i = 0; i < N; ++i) {
+                    hi[i] = fmaxf(hi[i], 0.f);
+                    lo[i] = 0.f;
+                }
+#pragma unroll 1
+                for (int j = 0; j < k; ++j) {
+                    const int at = fallen[j] - (N * g - skew);
+#pragma unroll
+                    for (int i = 0; i < N; ++i)
+                        if (at == i) hi[i] = 0.f;
+                }
+            }
+        };
         // ---- stage 0: every warp's run of the row.  Behind the last pass, the CTA
         // that holds the token goes on to stage 1: the run that holds it, a part a
         // warp, and the warp of that part to stage 2: the token
@@ -328,111 +375,95 @@ __global__ void __launch_bounds__(kVerifyThreads, 2) verify_tree_kernel(VerifyPa
         int token = -1;
         bool done = false;
         for (int stage = 0; stage < 3; ++stage) {
-            F2 acc = {0.f, 0.f}, odd = {0.f, 0.f};           // two, for their latency
-            bool found = false;
-#pragma unroll 1
-            for (int g = begin; g < end && !found; g += 32 * U) {
-                float hi[U][N], qf[U][N], lo[U][N];
-                // (the groups at the row's ends, and all where p and q lie differently,
-                // an element at a time)
-                if (g >= whole0 && min(g + 32 * U, end) <= whole1) {
-#pragma unroll
-                    for (int u = 0; u < U; ++u) {
-                        const int at = g + 32 * u + lane;
-                        uint4 x = {}, y = {};
-                        if (at < end) {
-                            x = __ldg(reinterpret_cast<const uint4*>(pr.at) + at);
-                            if (DRAFT && k > 0) y = __ldg(reinterpret_cast<const uint4*>(qr.at) + at);
-                        }
-                        widen(x, hi[u]);
-                        if (DRAFT) widen(y, qf[u]);
-                    }
-                } else {
-#pragma unroll
-                    for (int u = 0; u < U; ++u) {
-                        const int at = g + 32 * u + lane;
-                        pr.load(at < end ? at : -1, hi[u]);
-                        if (DRAFT && k > 0) qr.load(at < end ? at : -1, qf[u]);
-                    }
+            auto fetch = [&](int g, uint4& x, uint4& y) {
+                x = y = {};
+                if (g < end) {
+                    x = pr.load(g);
+                    if (DRAFT && k > 0) y = qr.load(g);
                 }
-                // what is left of them
+            };
+            if (stage == 2) {
+                // the token whose running sum exceeds t
+                for (int g = begin; g < end; g += 32) {
+                    uint4 x, y;
+                    float hi[N], lo[N];
+                    fetch(g + lane, x, y);
+                    weigh(x, y, g + lane, hi, lo);
+                    F2 mine = {0.f, 0.f};
 #pragma unroll
-                for (int u = 0; u < U; ++u)
+                    for (int i = 0; i < N; ++i) mine = mine + F2{hi[i], lo[i]};
+                    const F2 scan = warp_scan<32>(mine, lane);
+                    F2 upto = before_lane(scan, lane, run);
+                    int top = -1, pick = -1;
 #pragma unroll
                     for (int i = 0; i < N; ++i) {
-                        hi[u][i] = fmaxf(hi[u][i], 0.f);
-                        lo[u][i] = 0.f;
-                        if (DRAFT && k > 0) {
-                            qf[u][i] = fmaxf(qf[u][i], 0.f);
-                            const F2 w = first_step(hi[u][i], qf[u][i]);
-                            hi[u][i] = w.hi;
-                            lo[u][i] = w.lo;
+                        upto = upto + F2{hi[i], lo[i]};
+                        if (hi[i] > 0.f) {
+                            top = N * (g + lane) - skew + i;
+                            if (pick < 0 && upto > t) pick = top;
                         }
                     }
-                if (DRAFT) {
-#pragma unroll 1
-                    for (int j = 1; j < k; ++j) {
-                        const VerifyStep s = steps[j];
-#pragma unroll
-                        for (int u = 0; u < U; ++u)
-#pragma unroll
-                            for (int i = 0; i < N; ++i) {
-                                const F2 w = step_weight({hi[u][i], lo[u][i]}, qf[u][i], s);
-                                hi[u][i] = w.hi;
-                                lo[u][i] = w.lo;
-                            }
-                    }
-                } else {
-#pragma unroll 1
-                    for (int j = 0; j < k; ++j) {
-                        // (the token's place among this lane's)
-                        const int at = fallen[j] - (N * (g + lane) - skew);
-#pragma unroll
-                        for (int u = 0; u < U; ++u)
-#pragma unroll
-                            for (int i = 0; i < N; ++i)
-                                if (at == 32 * N * u + i) hi[u][i] = 0.f;
-                    }
+                    const unsigned over = __ballot_sync(0xffffffffu, pick >= 0);
+                    const unsigned some = __ballot_sync(0xffffffffu, top >= 0);
+                    // (none, by the roundings of the sums: the last that holds anything)
+                    if (over | some)
+                        token = __shfl_sync(0xffffffffu, over ? pick : top, over ? __ffs(over) - 1 : 31 - __clz(some));
+                    if (over) break;
+                    run = run + shfl(scan, 31);
                 }
-                if (stage < 2) {
+                break;
+            }
+            F2 acc = {0.f, 0.f}, odd = {0.f, 0.f};           // two, for their latency
+            auto add = [&](uint4 x, uint4 y, int g) {
+                float hi[N], lo[N];
+                weigh(x, y, g, hi, lo);
 #pragma unroll
-                    for (int u = 0; u < U; ++u)
+                for (int i = 0; i < N; ++i) {
+                    F2& to = i & 1 ? odd : acc;
+                    const F2 s = two_sum(to.hi, hi[i]);
+                    to = {s.hi, __fadd_rn(to.lo, DRAFT ? __fadd_rn(s.lo, lo[i]) : s.lo)};
+                }
+            };
+            int g = begin;
+            const int whole = min(end, qr.aligned ? (V + skew) / N : 0) - 31;
+            if (g == 0 && skew && g < end) {
+                uint4 x, y;
+                fetch(lane, x, y);
+                add(x, y, lane);
+                g = 32;
+            }
+            if (g < whole) {
+                // U chunks in flight, through running pointers
+                const bool both = DRAFT && k > 0;
+                int left = (whole - g + 31) >> 5;
+                const uint4 *px = reinterpret_cast<const uint4*>(pr.at) + g + lane,
+                            *py = reinterpret_cast<const uint4*>(qr.at) + g + lane;
+                uint4 x[U], y[U];
 #pragma unroll
-                        for (int i = 0; i < N; ++i) {
-                            F2& to = i & 1 ? odd : acc;
-                            const F2 s = two_sum(to.hi, hi[u][i]);
-                            to = {s.hi, __fadd_rn(to.lo, DRAFT ? __fadd_rn(s.lo, lo[u][i]) : s.lo)};
-                        }
-                } else {
-                    // the token whose running sum exceeds t
+                for (int u = 0; u < U; ++u) {
+                    x[u] = y[u] = {};
+                    if (u < left) x[u] = __ldg(px + 32 * u);
+                    if (both && u < left) y[u] = __ldg(py + 32 * u);
+                }
+#pragma unroll 1
+                for (; left > 0; left -= U, px += 32 * U, py += 32 * U) {
 #pragma unroll
                     for (int u = 0; u < U; ++u) {
-                        if (found) continue;
-                        F2 mine = {0.f, 0.f};
-#pragma unroll
-                        for (int i = 0; i < N; ++i) mine = mine + F2{hi[u][i], lo[u][i]};
-                        const F2 scan = warp_scan<32>(mine, lane);
-                        F2 upto = before_lane(scan, lane, run);
-                        int top = -1, pick = -1;
-#pragma unroll
-                        for (int i = 0; i < N; ++i) {
-                            upto = upto + F2{hi[u][i], lo[u][i]};
-                            if (hi[u][i] > 0.f) {
-                                top = N * (g + 32 * u + lane) - skew + i;
-                                if (pick < 0 && upto > t) pick = top;
-                            }
-                        }
-                        const unsigned over = __ballot_sync(0xffffffffu, pick >= 0);
-                        const unsigned some = __ballot_sync(0xffffffffu, top >= 0);
-                        // (none, by the roundings of the sums: the last that holds anything)
-                        if (over | some)
-                            token = __shfl_sync(0xffffffffu, over ? pick : top, over ? __ffs(over) - 1 : 31 - __clz(some));
-                        found = over != 0;
-                        run = run + shfl(scan, 31);
+                        if (u >= left) break;
+                        const uint4 xu = x[u], yu = y[u];
+                        if (u + U < left) x[u] = __ldg(px + 32 * (u + U));
+                        if (both && u + U < left) y[u] = __ldg(py + 32 * (u + U));
+                        add(xu, yu, g + lane);
+                        g += 32;
                     }
                 }
             }
-            if (stage == 2) break;
+#pragma unroll 1
+            for (; g < end; g += 32) {
+                uint4 x, y;
+                fetch(g + lane, x, y);
+                add(x, y, g + lane);
+            }
             // ---- the sums of the warps
             acc = fast_two_sum(acc.hi, acc.lo) + fast_two_sum(odd.hi, odd.lo);
             acc = warp_total<32>(acc);
@@ -583,9 +614,10 @@ extern "C" int fp8kv_verify_tree(const void* target_probs, int64_t target_stride
     // rows, and a few thousand tokens each.  (131072 tokens, chosen drafts: 6.2 us in
     // 16 CTAs, 7.2 in 8, 16.6 in one; 64 trees of 100003, drawn: 44 us in 8 CTAs each,
     // 57 in 4, 50 in 16.)
-    const int most = draft_probs ? 512 : 256;
+    const int most = 512;
     int c = 1;
     while (c < kVerifyMaxCluster && (int64_t)B * c * 2 <= most && V / (2 * c) >= 2048) c *= 2;
+    if (getenv("VC") && atoi(getenv("VC"))) c = atoi(getenv("VC"));
     if ((int64_t)B * c > 0x7fffffff) return FP8KV_ERR_UNSUPPORTED;
     P.cluster = c;
     auto kern = f32 ? (draft_probs ? verify_tree_kernel<float, true> : verify_tree_kernel<float, false>)
