@@ -21,10 +21,9 @@
 // probability: a border that moves by e flips a draw with probability e times the
 // number of tokens.  FP64 would bound the pass (2 additions a clock and SM: five
 // times the time of the HBM reads; a first form with it in the scans took 17.8 us
-// for one sequence of 131072 tokens).  The weights, the sums and the prefixes are
+// for one sequence of 131072 tokens, this one 6).  The weights, the sums and the prefixes are
 // pairs of fp32 instead, hi + lo with the rounding error of each step in lo (the
 // two-sum and two-product of Dekker and Knuth): 2^-45 of the weight a step.
-#include <stdlib.h>
 #include "attention.cuh"
 #include "common.cuh"
 
@@ -32,6 +31,8 @@ namespace fp8kv {
 
 int status_verify_tree(unsigned int* s, int clear) { return read_status(s, clear); }
 
+// Small CTAs, three or four an SM: while one waits for its cluster others add (64 trees
+// of 100003 tokens, drawn: 38 us in CTAs of 512 threads, two an SM).
 constexpr int kVerifyThreads = 256, kVerifyWarps = kVerifyThreads / 32, kVerifyMaxCluster = 16;
 
 struct VerifyParams {
@@ -424,6 +425,9 @@ __global__ void __launch_bounds__(kVerifyThreads, DRAFT ? 3 : 4) verify_tree_ker
                     to = {s.hi, __fadd_rn(to.lo, DRAFT ? __fadd_rn(s.lo, lo[i]) : s.lo)};
                 }
             };
+            // whole chunks of 32 groups, the next U on their way (64 trees, drawn: 46 us with
+            // their loads behind branches that look at the row's ends); the others, and
+            // all where q lies differently from p, one by one
             int g = begin;
             const int whole = min(end, qr.aligned ? (V + skew) / N : 0) - 31;
             if (g == 0 && skew && g < end) {
@@ -433,7 +437,6 @@ __global__ void __launch_bounds__(kVerifyThreads, DRAFT ? 3 : 4) verify_tree_ker
                 g = 32;
             }
             if (g < whole) {
-                // U chunks in flight, through running pointers
                 const bool both = DRAFT && k > 0;
                 int left = (whole - g + 31) >> 5;
                 const uint4 *px = reinterpret_cast<const uint4*>(pr.at) + g + lane,
@@ -610,14 +613,13 @@ extern "C" int fp8kv_verify_tree(const void* target_probs, int64_t target_stride
     P.M = M;
     P.V = V;
     // CTAs a sequence: clusters of 16 (not portable, but one fits every GPC) down to 1
-    // as the batch grows, with some 500 CTAs, or half of that without a drafter's
-    // rows, and a few thousand tokens each.  (131072 tokens, chosen drafts: 6.2 us in
-    // 16 CTAs, 7.2 in 8, 16.6 in one; 64 trees of 100003, drawn: 44 us in 8 CTAs each,
-    // 57 in 4, 50 in 16.)
+    // as the batch grows, with some 500 CTAs, about what fits at once, and a few
+    // thousand tokens each.  (131072 tokens, chosen drafts: 6.2 us in 16 CTAs, 7.9 in
+    // 8, 31 in one; 64 trees of 100003, drawn: 30.7 us in 8 CTAs each, 43 in 4, 31.8 in
+    // 16, chosen 16.0, 20.5, 18.9; 8 such trees 13.6 in 16, 16.8 in 8.)
     const int most = 512;
     int c = 1;
     while (c < kVerifyMaxCluster && (int64_t)B * c * 2 <= most && V / (2 * c) >= 2048) c *= 2;
-    if (getenv("VC") && atoi(getenv("VC"))) c = atoi(getenv("VC"));
     if ((int64_t)B * c > 0x7fffffff) return FP8KV_ERR_UNSUPPORTED;
     P.cluster = c;
     auto kern = f32 ? (draft_probs ? verify_tree_kernel<float, true> : verify_tree_kernel<float, false>)
