@@ -629,7 +629,7 @@ def test_verify_when_nothing_is_left():
 @pytest.mark.gpu
 @pytest.mark.parametrize("kind", CACHES)
 @pytest.mark.parametrize("layers,B,M,H,ps", [(1, 1, 12, 8, 32), (3, 5, 64, 2, 64), (48, 2, 7, 1, 32), (2, 40, 1, 4, 32),
-                                             (2, 3, 33, 40, 32)])
+                                             (2, 3, 33, 40, 32), (64, 40, 5, 1, 32)])
 def test_keep_path(kind, layers, B, M, H, ps):
     rng = np.random.default_rng(M + layers)
     lens = [int(n) for n in rng.integers(M, M + 150, B)]
