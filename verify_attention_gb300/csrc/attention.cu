@@ -1335,7 +1335,7 @@ static int attention_call(const void* k_new, const void* v_new, const void* q, c
     const bool f16_parts = use_tc || (tree_tc && fp8);
     if (tree && RT > 1) {
         const Int4Cut cut = int4_cut(plan, true, false, split_tokens > 0, B, (int64_t)B * Hkv * RT, page_size,
-                                     fp8 ? 6.f : 5.f, fp8 ? 1.1f : 0.8f, even);
+                                     fp8 ? 6.f : 5.f, fp8 ? 0.95f : 0.8f, even);
         plan.split_pages = P.split_pages = cut.split_pages;
         plan.num_splits = P.num_splits = cut.num_splits;
         plan.split_tokens = cut.split_pages * page_size;

@@ -21,9 +21,11 @@
 //   - three threads issue the products (BF16: 0.80 us a tile; both halves' P.V by one
 //     thread, which then is busy for 1300 cycles a tile, 0.86);
 //   - BF16 stages of K and of V come and go by themselves (before: 0.89).
-// E4M3 takes 1.07 us a tile, 0.94 of it without the widening of V, which shares the
-// shared memory's bandwidth with the products (eight widening warps instead of four:
-// 1.20).
+// E4M3 takes 0.90 us a tile (64 trees of 12 nodes, up to 32768 keys: 487 us).  There a
+// softmax warp's 360 instructions a half tile, one after another, are what takes longest;
+// the widening of V has to stay below that (addresses computed for each chunk, and its
+// halves exchanged after they were widened: 1.07; eight warps for it instead of four, as
+// it was then: 1.20).
 //
 // One CTA per (partition, row tile x KV head, sequence):
 //   warp 0       TMA producer (tiles of 128 keys into rings of K and V stages); BF16: of
@@ -380,36 +382,45 @@ __global__ void __launch_bounds__(Cfg<FP8>::THREADS, 1) attention_tree_tc_kernel
             // rows [nlo, nhi) hold new tokens: their staged V may be old
             const int nlo = patched ? max(0, app_lo - k0) : 0, nhi = patched ? min(NK, app_hi - k0) : 0;
             const int zlo = zlo_of(t), zhi = zhi_of(t);
-            const uint8_t* src = stg + C::OFF_V + s * C::STG;
+            // chunk c of rows r0 + (CONV_THREADS / 8) u, in two halves
+            const int r0 = ct >> 3, c = ct & 7, c16 = 2 * (c & 3);
+            const bool low = c < 4;
+            const uint8_t* src = stg + C::OFF_V + s * C::STG + r0 * 128 + (((c ^ r0) & 7) << 4);
             uint8_t* dst = vbuf + vb * VBUF;
-            constexpr int PER = (NK * 8 + CONV_THREADS - 1) / CONV_THREADS;   // chunks a thread
-            uint4 code[PER];
+            constexpr int PER = NK * 8 / CONV_THREADS;      // chunks a thread
+            static_assert(!FP8 || CONV_THREADS % 64 == 0 && PER * CONV_THREADS == NK * 8, "a row's swizzle is that of row r0");
+            // the order of the two stores alternates so that each quarter warp covers all
+            // 32 banks
+            uint8_t* first = dst + (c >> 2) * HALF + r0 * 128 + (((c16 + !low) ^ r0) & 7) * 16;
+            uint8_t* second = dst + (c >> 2) * HALF + r0 * 128 + (((c16 + low) ^ r0) & 7) * 16;
+            uint2 cf[PER], cg[PER];
+            const uint8_t *sf = src + (low ? 0 : 8), *sg = src + (low ? 8 : 0);
+            const bool whole = zlo <= 0 && zhi >= NK && !patched;
+            if (whole) {
 #pragma unroll
-            for (int u = 0; u < PER; ++u) {
-                const int i = ct + CONV_THREADS * u, r = i >> 3, c = i & 7;
-                code[u] = i < NK * 8 && r >= zlo && r < zhi ? *(const uint4*)(src + r * 128 + (((c ^ r) & 7) << 4))
-                                                            : make_uint4(0, 0, 0, 0);
+                for (int u = 0; u < PER; ++u) {
+                    cf[u] = *(const uint2*)(sf + u * CONV_THREADS * 16);
+                    cg[u] = *(const uint2*)(sg + u * CONV_THREADS * 16);
+                }
+            } else {
+#pragma unroll
+                for (int u = 0; u < PER; ++u) {
+                    const int r = r0 + CONV_THREADS / 8 * u;
+                    const bool in = r >= zlo && r < zhi;
+                    cf[u] = in ? *(const uint2*)(sf + u * CONV_THREADS * 16) : make_uint2(0, 0);
+                    cg[u] = in ? *(const uint2*)(sg + u * CONV_THREADS * 16) : make_uint2(0, 0);
+                }
             }
 #pragma unroll
             for (int u = 0; u < PER; ++u) {
-                const int i = ct + CONV_THREADS * u, r = i >> 3, c = i & 7;
-                if (i >= NK * 8) break;
+                const int r = r0 + CONV_THREADS / 8 * u;
                 if (r >= nlo && r < nhi) continue;
-                uint4 lo, hi;
-                lo.x = e4m3x2_to_f16x2(code[u].x);
-                lo.y = e4m3x2_to_f16x2(code[u].x >> 16);
-                lo.z = e4m3x2_to_f16x2(code[u].y);
-                lo.w = e4m3x2_to_f16x2(code[u].y >> 16);
-                hi.x = e4m3x2_to_f16x2(code[u].z);
-                hi.y = e4m3x2_to_f16x2(code[u].z >> 16);
-                hi.z = e4m3x2_to_f16x2(code[u].w);
-                hi.w = e4m3x2_to_f16x2(code[u].w >> 16);
-                uint8_t* blk = dst + (c >> 2) * HALF + r * 128;
-                const int c16 = 2 * (c & 3);
-                // the order alternates so that each quarter warp covers all 32 banks
-                const int a0 = ((c16 ^ r) & 7) << 4, a1 = (((c16 + 1) ^ r) & 7) << 4;
-                *(uint4*)(blk + (c < 4 ? a0 : a1)) = c < 4 ? lo : hi;
-                *(uint4*)(blk + (c < 4 ? a1 : a0)) = c < 4 ? hi : lo;
+                *(uint4*)(first + u * CONV_THREADS * 16) =
+                    make_uint4(e4m3x2_to_f16x2(cf[u].x), e4m3x2_to_f16x2(cf[u].x >> 16), e4m3x2_to_f16x2(cf[u].y),
+                               e4m3x2_to_f16x2(cf[u].y >> 16));
+                *(uint4*)(second + u * CONV_THREADS * 16) =
+                    make_uint4(e4m3x2_to_f16x2(cg[u].x), e4m3x2_to_f16x2(cg[u].x >> 16), e4m3x2_to_f16x2(cg[u].y),
+                               e4m3x2_to_f16x2(cg[u].y >> 16));
             }
             if (patched) {
                 for (int it = ct; it < n_app * 16; it += CONV_THREADS) {
