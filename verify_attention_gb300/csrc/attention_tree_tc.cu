@@ -21,8 +21,9 @@
 //   - three threads issue the products (BF16: 0.80 us a tile; both halves' P.V by one
 //     thread, which then is busy for 1300 cycles a tile, 0.86);
 //   - BF16 stages of K and of V come and go by themselves (before: 0.89).
-// E4M3 takes 0.90 us a tile (64 trees of 12 nodes, up to 32768 keys: 487 us).  There a
-// softmax warp's 360 instructions a half tile, one after another, are what takes longest;
+// BF16 takes 0.78 us a tile, E4M3 0.89 (64 trees of 12 nodes, up to 32768 keys: 487
+// us): a softmax warp's way through a half tile (the wait for S 130 cycles, reading it
+// 140, the maximum 240, the exponentials 700, P 140) with the products' between them;
 // the widening of V has to stay below that (addresses computed for each chunk, and its
 // halves exchanged after they were widened: 1.07; eight warps for it instead of four, as
 // it was then: 1.20).
@@ -603,6 +604,10 @@ __global__ void __launch_bounds__(Cfg<FP8>::THREADS, 1) attention_tree_tc_kernel
                 // P = 2^(s mult - m + BIAS) (masked keys are -inf and give 0)
                 const float neg = (m_run == -INFINITY) ? 0.f : BIAS - m_run;
                 const uint64_t mult2 = pack2(mult, mult), neg2 = pack2(neg, neg);
+                // P.V of tile t - 1 has read P (the wait behind the exponentials: 3% slower over BF16)
+                if (t > 0) ok = __all_sync(0xffffffffu, mbar_wait(bar(B_PV + half), (t - 1) & 1));
+                if (!ok) break;
+                fence_after();
                 uint64_t sum2 = 0;
                 uint32_t pw[32];
 #pragma unroll
@@ -614,10 +619,6 @@ __global__ void __launch_bounds__(Cfg<FP8>::THREADS, 1) attention_tree_tc_kernel
                     sum2 = add2(sum2, pack2(p0, p1));
                     pw[j] = FP8 ? pack_f16x2(p0, p1) : pack_bf16x2(p0, p1);
                 }
-                // P.V of tile t - 1 has read P
-                if (t > 0) ok = __all_sync(0xffffffffu, mbar_wait(bar(B_PV + half), (t - 1) & 1));
-                if (!ok) break;
-                fence_after();
                 tmem_st_x32(p_col, pw);
                 float sum0, sum1;
                 unpack2(sum2, sum0, sum1);
