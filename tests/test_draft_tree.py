@@ -347,10 +347,24 @@ class Case:
     ([2100, 500], 64, 9, 1, 32, "ragged", 200, 0),
     ([900], 33, 12, 2, 32, "chain", 3, 0),              # a window shorter than the tree is deep
     ([777], 64, 2, 1, 64, "chain", 20, 128),            # 128 rows a head, nodes over two tiles
+    ([3000], 64, 18, 2, 64, "ragged", -1, 512),         # five row tiles of one sequence, six partitions each
+    ([5003], 40, 9, 1, 32, "tree", -1, 8192),           # one partition of forty key tiles
+    ([4100], 34, 4, 1, 32, "star", 4000, 0),            # a second row tile of eight rows
 ])
 def test_tree_attention(kind, lens, M, Hq, H, ps, shape, window, split):
     c = Case(M * 1000 + len(lens), kind, lens, M, Hq, H, ps, shape)
     c.check(c.run(window, split), window)
+    _status()
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("kind", ["e4m3", "bf16"])
+@pytest.mark.parametrize("ns", [2, 5, 8])
+def test_row_tiles_combine_in_clusters(kind, ns):
+    """Partitions of one sequence are a cluster for each KV head and row tile."""
+    c = Case(ns, kind, [128 * ns - 5], 50, 6, 2, 32, "tree")
+    c.check(c.run(split=128))
+    assert f"cluster={ns} reduce=0" in fp8kv.fp8kv_last_dispatch()
     _status()
 
 
@@ -540,6 +554,12 @@ def test_verify_truncated_rows_and_strided_views(draft):
     views = [w[..., 3 + i:3 + i + V] for i, w in enumerate(wide)]     # p and q on different boundaries
     views[0].copy_(torch.from_numpy(p))
     views[1].copy_(torch.from_numpy(q))
+    got = fp8kv.fp8kv_verify_tree(views[0], views[1] if draft else None, _cuda(tok), _cuda(par), _cuda(u))
+    _check_verify(p, q if draft else None, tok, par, u, got)
+    # the same in bf16, rows of both on odd boundaries of their own
+    halves = [v.to(torch.bfloat16) for v in wide]
+    views = [w[..., 3 + i:3 + i + V] for i, w in enumerate(halves)]
+    p, q = (v.float().cpu().numpy() for v in views)
     got = fp8kv.fp8kv_verify_tree(views[0], views[1] if draft else None, _cuda(tok), _cuda(par), _cuda(u))
     _check_verify(p, q if draft else None, tok, par, u, got)
     _status()
@@ -816,6 +836,38 @@ def test_a_step_in_a_graph_with_new_contents(kind):
         assert torch.equal(a, b)
     assert all(torch.equal(a, b) for a, b in zip(got[1:4], want[1:]))
     assert all(torch.equal(a, b) for a, b in zip(got[4], s.caches))
+    _status()
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("kind", CACHES)
+@pytest.mark.parametrize("M,Hq", [(4, 8), (12, 72)])
+def test_pages_beyond_four_gigabytes(kind, M, Hq):
+    """The last pages of caches of 5 GiB: the same bytes and outputs as those of small ones."""
+    H, ps, n = 8, 64, 200
+    page = H * ps * {"bf16": 256, "e4m3": 128, "int4": 72}[kind]
+    g = torch.Generator(device="cuda").manual_seed(M)
+    x = torch.randn((n, Hq + 2 * H, 128), generator=g, device="cuda").to(torch.bfloat16)
+    cs = torch.randn((256, 64), generator=g, device="cuda")
+    s, pos, sl = _scale(0.03), torch.arange(n, device="cuda"), torch.tensor([n], dtype=torch.int32, device="cuda")
+    par = _cuda(_tree(np.random.default_rng(M), 1, M, "tree"))
+    path = torch.tensor([[0] + list(range(2, M)) + [-1]], dtype=torch.int32, device="cuda")
+    got = []
+    for pages in (4, (5 << 30) // page):
+        kc, vc = (torch.empty_like(_empty(kind, 1, H, ps)).new_empty((pages, *_empty(kind, 1, H, ps).shape[1:]))
+                  for _ in range(2))
+        kc[-4:].zero_(), vc[-4:].zero_()
+        bt = torch.arange(pages - 1, pages - 5, -1, dtype=torch.int32, device="cuda")[None]
+        slots = bt[0, pos // ps].long() * ps + pos % ps
+        q = fp8kv.fp8kv_rope_insert(x[:, :Hq], x[:, Hq:Hq + H], x[:, Hq + H:], pos, cs, slots, s, s, kc, vc)
+        mask, _, node_slots = fp8kv.fp8kv_tree_metadata(par, sl, bt, ps, n, pages)
+        assert torch.equal(node_slots[0], slots[n - M:])
+        out = fp8kv.fp8kv_tree_attention(q[n - M:][None].contiguous(), kc, vc, bt, sl, mask, n, s, s, SM)
+        new = fp8kv.fp8kv_cache_keep_path([kc], [vc], bt, sl, path, n)
+        got.append((q, out, new, *fp8kv.fp8kv_cache_gather(slots, s, s, kc, vc), kc[-4:].clone(), vc[-4:].clone()))
+        del kc, vc
+    for a, b in zip(*got):
+        assert torch.equal(a, b)
     _status()
 
 
