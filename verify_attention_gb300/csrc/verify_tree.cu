@@ -32,7 +32,8 @@ namespace fp8kv {
 int status_verify_tree(unsigned int* s, int clear) { return read_status(s, clear); }
 
 // Small CTAs, three or four an SM: while one waits for its cluster others add (64 trees
-// of 100003 tokens, drawn: 38 us in CTAs of 512 threads, two an SM).
+// of 100003 tokens, drawn: 38 us in CTAs of 512 threads, two an SM).  Two an SM where a
+// chunk is 256 bf16 tokens of p and q, for their registers (30.4 us; three 32.7).
 constexpr int kVerifyThreads = 256, kVerifyWarps = kVerifyThreads / 32, kVerifyMaxCluster = 16;
 
 struct VerifyParams {
@@ -198,8 +199,8 @@ __device__ __forceinline__ void send_part(uint32_t to, uint32_t mbar, F2 v, int 
 enum { PASS_SUM = 1, PASS_DRAW = 2, PASS_ROW = 3, PASS_STOP = 4 };
 
 template <typename T, bool DRAFT>
-__global__ void __launch_bounds__(kVerifyThreads, DRAFT ? 3 : 4) verify_tree_kernel(VerifyParams P) {
-    constexpr int N = Row<T>::N, U = (DRAFT ? 8 : 16) / N;      // groups a lane has in flight of a row
+__global__ void __launch_bounds__(kVerifyThreads, !DRAFT ? 4 : sizeof(T) == 4 ? 3 : 2) verify_tree_kernel(VerifyParams P) {
+    constexpr int N = Row<T>::N, U = DRAFT && N == 4 ? 2 : 16 / N;      // groups a lane has in flight of a row
     __shared__ int tok[64], fallen[64], path[64];
     __shared__ float un[64], pw[64], qw[64];
     __shared__ unsigned kids[64][2], stands[2];         // bits: a node's children; nodes that stand as first children
