@@ -88,13 +88,17 @@ __device__ __forceinline__ F2 warp_scan(F2 a, int lane) {
     }
     return a;
 }
-// every lane: the sum of its N, in the same order for all
+// every lane: the sum of its N, the same for all (both sides of an exchange get the
+// same sum and error; hi goes on without waiting for lo, which is joined at the end)
 template <int N>
 __device__ __forceinline__ F2 warp_total(F2 a) {
 #pragma unroll
-    for (int o = N / 2; o >= 1; o >>= 1)
-        a = a + F2{__shfl_xor_sync(0xffffffffu, a.hi, o), __shfl_xor_sync(0xffffffffu, a.lo, o)};
-    return a;
+    for (int o = N / 2; o >= 1; o >>= 1) {
+        const F2 b = {__shfl_xor_sync(0xffffffffu, a.hi, o), __shfl_xor_sync(0xffffffffu, a.lo, o)};
+        const F2 s = two_sum(a.hi, b.hi);
+        a = {s.hi, __fadd_rn(s.lo, __fadd_rn(a.lo, b.lo))};
+    }
+    return fast_two_sum(a.hi, a.lo);
 }
 // Of runs with the sums `run` that end at `end`: the first whose end exceeds t
 // (should the roundings leave none: the last that holds anything; -1: none does).
