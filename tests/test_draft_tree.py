@@ -369,6 +369,22 @@ def test_row_tiles_combine_in_clusters(kind, ns):
 
 
 @pytest.mark.gpu
+@pytest.mark.parametrize("M,Hq,window,split", [(33, 10, -1, 0), (40, 18, -1, 0), (64, 6, 50, 0), (33, 10, -1, 256),
+                                                 (33, 10, 100, 0), (40, 18, 130, 0), (33, 10, 150, 128)])
+def test_several_row_tiles_a_cta_end_inside_a_warp(M, Hq, window, split):
+    """INT4 pages: the last row tile has 37, 104, 64 rows; with a window, which leaves
+    64 sequences of 2 KV heads the same keys, a CTA takes several row tiles."""
+    rng = np.random.default_rng(M)
+    c = Case(M + 1, "int4", [int(n) for n in rng.integers(M, 300, 63)] + [300], M, Hq, 2, 32, "ragged")
+    c.check(c.run(window, split), window)
+    tiles = (M * Hq // 2 + 127) // 128
+    dispatch = fp8kv.fp8kv_last_dispatch()
+    rows = int(dispatch.split("grid=")[1].split("x")[1])
+    assert f"row_tiles={tiles} " in dispatch and (window < 0 or rows < 2 * tiles), dispatch
+    _status()
+
+
+@pytest.mark.gpu
 @pytest.mark.parametrize("kind", CACHES)
 @pytest.mark.parametrize("M,Hq", [(2, 4), (12, 18), (16, 18)])
 def test_a_chain_is_the_plain_call(kind, M, Hq):

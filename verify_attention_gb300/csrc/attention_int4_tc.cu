@@ -446,7 +446,9 @@ __global__ void __launch_bounds__(THREADS, 1) attention_int4_tc_kernel(AttnParam
                 tmem_ld_x32(lane_base + TM_O + 128 + 64 * half + c, oz);
                 tmem_wait_ld();
                 uint4* dst = (uint4*)(TREE && n_rt > 1 ? (uint8_t*)(row_out + c) : row_stage + c * 2);
-                if (TREE && n_rt > 1 && r >= RL) continue;
+                // (the last row tile may end inside a warp, and the next read of O is one
+                // of the whole warp)
+                const bool stores = !TREE || n_rt == 1 || r < RL;
 #pragma unroll
                 for (int v4 = 0; v4 < 4; ++v4) {
                     float x[8];
@@ -454,11 +456,13 @@ __global__ void __launch_bounds__(THREADS, 1) attention_int4_tc_kernel(AttnParam
                     for (int i = 0; i < 8; ++i)
                         x[i] = zero ? 0.f : __uint_as_float(oa[8 * v4 + i]) * fa + __uint_as_float(oz[8 * v4 + i]) * fz;
                     // columns 0 4 1 5 2 6 3 7 back in order
-                    dst[v4] = direct ? make_uint4(pack_bf16x2(x[0], x[2]), pack_bf16x2(x[4], x[6]),
-                                                  pack_bf16x2(x[1], x[3]), pack_bf16x2(x[5], x[7]))
-                                     : make_uint4(pack_f16x2(x[0], x[2]), pack_f16x2(x[4], x[6]),
-                                                  pack_f16x2(x[1], x[3]), pack_f16x2(x[5], x[7]));
+                    const uint4 o4 = direct ? make_uint4(pack_bf16x2(x[0], x[2]), pack_bf16x2(x[4], x[6]),
+                                                         pack_bf16x2(x[1], x[3]), pack_bf16x2(x[5], x[7]))
+                                            : make_uint4(pack_f16x2(x[0], x[2]), pack_f16x2(x[4], x[6]),
+                                                         pack_f16x2(x[1], x[3]), pack_f16x2(x[5], x[7]));
+                    if (stores) dst[v4] = o4;
                 }
+                __syncwarp();
             }
             if (combine) {
                 // stays here: the cluster's CTAs read it below
