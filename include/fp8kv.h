@@ -516,7 +516,10 @@ int fp8kv_rope_insert(const void* q, int64_t q_stride, const void* k, int64_t k_
  * p_m = L - M + (bits in tree_mask[b][m]) - 1 (mask 0: L - M), sees of those the
  * keys at positions >= p_m - window_left, node i being at position p_i.  A row without visible keys,
  * and a row whose mask is 0 (padding), is written as zeros.  The mask of a chain
- * gives fp8kv_paged_attention's result (up to roundings).
+ * gives fp8kv_paged_attention's result (up to roundings).  The K and V rows of a node
+ * that is in no row's mask reach no output, whatever they hold (nobody writes those of
+ * padding, slot -1); of the others' V rows, as of the context's: a NaN or an infinity
+ * may reach rows that do not see it (fp8kv_paged_attention), a sibling's too.
  *
  *   tree_mask  (device) uint64 [B][M]
  *   split_tokens (host) 0, or a multiple of page_size; of 128 for more than 16 rows

@@ -488,6 +488,114 @@ def test_nan_stays_with_the_rows_that_see_it(kind):
     assert torch.isfinite(got[0, keep]).all()
 
 
+def _poison(cache, kind, page, off, ps):
+    """The row's bytes as those that Case finds in rows of no sequence: NaN."""
+    if kind == "int4":
+        cache[page, :, off * 64:off * 64 + 64] = 0x7f
+        cache[page, :, ps * 64 + off * 8:ps * 64 + off * 8 + 8] = 0x7f
+    else:
+        cache[page, :, off] = 0x7f if kind == "e4m3" else float("nan")
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("kind", CACHES)
+@pytest.mark.parametrize("lens,M,Hq,H,ps,window,split", [
+    ([300, 45, 8], 8, 4, 2, 32, -1, 0),                 # up to 16 rows a head
+    ([8, 100], 8, 4, 2, 64, -1, 0),                     # nodes from key 0 on
+    ([2500], 15, 2, 2, 64, 700, 0),                     # several partitions
+    ([260, 31, 90], 12, 18, 2, 32, -1, 0),              # one row tile; nodes over two key tiles
+    ([1000], 12, 18, 2, 64, -1, 128),                   # a cluster
+    ([1029, 517], 12, 18, 2, 32, -1, 128),              # nodes over two partitions, longest first
+    ([777], 12, 18, 2, 32, 5, 0),                       # a first tile with keys before the window, holes and an end
+    ([400, 130, 64], 64, 18, 2, 32, -1, 0),             # several row tiles; trees over two key tiles, from key 0 on
+    ([160], 60, 9, 1, 32, -1, 128),                     # nodes over two partitions
+    ([700] * 40, 33, 20, 4, 32, 300, 0),                # INT4: several row tiles a CTA
+    ([1301], 50, 18, 2, 64, -1, 256),
+])
+def test_stale_rows_of_padding_nodes_reach_no_output(kind, lens, M, Hq, H, ps, window, split):
+    """Nobody writes the rows of padding nodes (slot -1): whatever is there."""
+    c = Case(M * 100 + len(lens), kind, lens, M, Hq, H, ps, "ragged")
+    if not (c.mask == 0).any():
+        c.mask[:, M // 2] = 0
+    want, tol = c.want(window)
+    for b, m in zip(*np.nonzero(c.mask == 0)):
+        at = c.lens[b] - M + m
+        for cache in (c.kc, c.vc):
+            _poison(cache, kind, int(c.bt[b, at // ps]), int(at % ps), ps)
+    got = c.run(window, split).double().cpu().numpy()
+    assert np.isfinite(got).all()
+    assert np.all(np.abs(got - want) <= tol), np.abs(got - want).max()
+    assert np.all(got[c.mask == 0] == 0)
+    _status()
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("kind", CACHES)
+@pytest.mark.parametrize("lens,M,Hq,H", [([200, 40], 8, 4, 2), ([1500], 12, 18, 2), ([300, 2000], 24, 18, 2),
+                                         ([160, 90], 40, 6, 2), ([260], 30, 8, 2)])
+def test_appended_rows_of_padding_nodes_reach_no_output(kind, lens, M, Hq, H):
+    """With k_new the rows of padding nodes are written too, NaN here."""
+    c = Case(M, kind, lens, M, Hq, H, 32, "ragged")
+    c.mask[:, M // 2] = 0
+    pos = np.array([[n - M + m for m in range(M)] for n in c.lens])
+    slots = _cuda(np.take_along_axis(c.bt, pos // 32, 1).astype(np.int64) * 32 + pos % 32).reshape(-1)
+    g = torch.Generator().manual_seed(6)
+    kn, vn = (torch.randn((len(lens), M, H, 128), generator=g).to(torch.bfloat16).cuda() for _ in range(2))
+    fp8kv.fp8kv_cache_insert(kn.view(-1, H, 128), vn.view(-1, H, 128), slots, c.ks, c.vs, c.kc, c.vc)
+    want, tol = c.want()
+    pad = torch.from_numpy(c.mask == 0).cuda()
+    kn[pad] = float("nan")
+    vn[pad] = float("nan")
+    got = c.run(k_new=kn, v_new=vn).double().cpu().numpy()
+    assert np.isfinite(got).all()
+    assert np.all(np.abs(got - want) <= tol), np.abs(got - want).max()
+    _status()
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("kind", CACHES)
+@pytest.mark.parametrize("M,Hq", [(8, 4), (12, 18), (40, 18)])
+def test_ragged_trees_over_an_uninitialised_cache(kind, M, Hq):
+    """Metadata, rotary insert of the context and of the nodes, attention: rows that the
+    insert skips hold NaN."""
+    H, ps, lens = 2, 32, [70, 45, 200]
+    rng = np.random.default_rng(M)
+    bt_np, pages = _layout(rng, lens, ps)
+    par = _tree(rng, 3, M, "ragged")
+    par[0, 2] = par[1, M - 1] = -1
+    fill = float("nan") if kind == "bf16" else 0x7f
+    kc, vc = _empty(kind, pages, H, ps, fill), _empty(kind, pages, H, ps, fill)
+    x = torch.randn((sum(lens), Hq + 2 * H, 128), generator=torch.Generator().manual_seed(M)).to(torch.bfloat16).cuda()
+    ang = np.arange(256)[:, None] * 1e4 ** (-np.arange(64) / 64)
+    cs, s = _cuda(np.concatenate([np.cos(ang), np.sin(ang)], 1).astype(np.float32)), _scale(0.03)
+    bt, sl = _cuda(bt_np, np.array(lens, np.int32))
+    mask, pos, slot = fp8kv.fp8kv_tree_metadata(_cuda(par), sl, bt, ps, max(lens), pages)
+    q, first = [], 0
+    for b, n in enumerate(lens):
+        y = x[first:first + n]
+        first += n
+        p = torch.cat([torch.arange(n - M, device="cuda"), pos[b]])
+        at = torch.from_numpy(bt_np[b, np.arange(n - M) // ps].astype(np.int64) * ps + np.arange(n - M) % ps).cuda()
+        q.append(fp8kv.fp8kv_rope_insert(y[:, :Hq], y[:, Hq:Hq + H], y[:, Hq + H:], p, cs, torch.cat([at, slot[b]]), s,
+                                         s, kc, vc)[n - M:])
+    got = fp8kv.fp8kv_tree_attention(torch.stack(q), kc, vc, bt, sl, mask, max(lens), s, s, SM).double().cpu().numpy()
+    assert np.isfinite(got).all()
+    words = mask.cpu().numpy()
+    assert np.all(got[words == 0] == 0) and (words == 0).any()
+    kk, vv = _values(kc, kind, ps, s), _values(vc, kind, ps, s)
+    qmax = max(float(t.abs().max()) for t in q)
+    for b, n in enumerate(lens):
+        ids = bt_np[b, :(n + ps - 1) // ps]
+        k, v = (a[ids].transpose(1, 0, 2, 3).reshape(H, -1, 128)[:, :n] for a in (kk, vv))
+        want = tree_np.attention(q[b].double().cpu().numpy(), k, v, tree_np.sees(words[b], M, n, -1), SM)
+        # the bounds of Case.want, of the rows that are held
+        vmax, kmax = np.nanmax(np.abs(v)), np.nanmax(np.abs(k))
+        e = 0 if kind == "bf16" else 128 * 2.0 ** -17 * qmax * kmax * SM
+        tol = ((2.0 ** -8 if kind == "bf16" else 2.0 ** -10) + 2 * e + 2.0 ** -16) * vmax + 2.0 ** -8 * np.abs(want)
+        assert np.all(np.abs(got[b] - want) <= tol), (b, np.abs(got[b] - want).max())
+    _status()
+
+
 # -------------------------------------------------------------- verification
 
 def _probs(rng, B, M, V, sharp=2.0, zero=0.0):

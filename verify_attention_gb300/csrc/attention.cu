@@ -249,10 +249,13 @@ __device__ __forceinline__ void attention_body(const CUtensorMap& tm_k, const CU
     RowPos rp1 = row_pos(r1, P.R, P.G, L, P.M, P.window_left);
     const int base = L - P.M;
     TreeRow tr0, tr1;
+    uint32_t words = 0;         // of this thread's rows
     if (TREE) {
         const int m0 = min(r0, P.R - 1) / P.G, m1 = min(r1, P.R - 1) / P.G;
-        tr0 = tree_row(P, b, m0, tree_word(P, b, m0), base);
-        tr1 = tree_row(P, b, m1, tree_word(P, b, m1), base);
+        const uint64_t w0 = tree_word(P, b, m0), w1 = tree_word(P, b, m1);
+        words = (uint32_t)(w0 | w1);
+        tr0 = tree_row(P, b, m0, w0, base);
+        tr1 = tree_row(P, b, m1, w1, base);
         // (the bounds below: every key before the nodes needs no mask)
         rp0 = {base - 1, tr0.lo};
         rp1 = {base - 1, tr1.lo};
@@ -429,10 +432,13 @@ __device__ __forceinline__ void attention_body(const CUtensorMap& tm_k, const CU
                 }
             }
             // ---- O += P V  (2 k-steps of 16 keys)
-            // keys outside every row's range (past the sequence end, or before
-            // the first window) contribute exact zeros even if stale data there
-            // is not finite
-            const bool zero_v = (kfirst + 31 >= L) || (kfirst < lo0);
+            // keys outside every row's range (past the sequence end, before the
+            // first window, a tree's padding) contribute exact zeros even if stale
+            // data there is not finite
+            // (the warp's lanes have all rows of a tree call, at most 16)
+            uint32_t holes = 0;
+            if (TREE && kfirst + 31 >= base) holes = ~__reduce_or_sync(0xffffffffu, words) & ((1u << P.M) - 1);
+            const bool zero_v = (kfirst + 31 >= L) || (kfirst < lo0) || holes;
 #pragma unroll
             for (int kk = 0; kk < 2; ++kk) {
                 uint32_t pa[4];
@@ -455,6 +461,10 @@ __device__ __forceinline__ void attention_body(const CUtensorMap& tm_k, const CU
                     kz[1] = key + 1 >= L || key + 1 < lo0;
                     kz[2] = key + 8 >= L || key + 8 < lo0;
                     kz[3] = key + 9 >= L || key + 9 < lo0;
+                    if (TREE) {
+#pragma unroll
+                        for (int i = 0; i < 4; ++i) kz[i] |= tree_hole(holes, key + (i & 1) + 8 * (i >> 1), base);
+                    }
                 }
                 if (FP8) {
 #pragma unroll

@@ -84,6 +84,21 @@ __device__ __forceinline__ bool tree_sees(const TreeRow& t, int key, int base) {
     return key < base ? key >= t.lo : i < 64u && ((t.nodes >> i) & 1ull);
 }
 
+// The nodes of a sequence that no row's word has: padding, whose rows nobody writes.
+// Their weights are 0, and their V counts as zeros, like that of keys behind the end: 0
+// times a stale NaN must not reach the rows of others.  (A whole warp; lanes behind
+// the last word read it again.)
+__device__ __forceinline__ uint64_t tree_holes(const AttnParams& P, int b, int lane) {
+    const uint64_t* at = P.tree + (int64_t)b * P.M;
+    const uint64_t w = at[min(lane, P.M - 1)] | at[min(lane + 32, P.M - 1)];
+    const uint32_t lo = __reduce_or_sync(0xffffffffu, (uint32_t)w), hi = __reduce_or_sync(0xffffffffu, (uint32_t)(w >> 32));
+    return ~((uint64_t)hi << 32 | lo) & (~0ull >> (64 - P.M));
+}
+__device__ __forceinline__ bool tree_hole(uint64_t holes, int key, int base) {
+    const unsigned i = (unsigned)(key - base);
+    return i < 64u && ((holes >> i) & 1ull);
+}
+
 // ------------------------------------------------ persistent multi-layer step
 // (attention_layers.cu): one launch runs the append + attention of several
 // layers, layer after layer.

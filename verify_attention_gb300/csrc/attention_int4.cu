@@ -203,6 +203,7 @@ __global__ void __launch_bounds__(WARPS * 32, 12 / WARPS) paged_attention_int4_k
     // ---- rows g and g + 8 of the tile: positions, Q fragments
     int pr[2], lor[2];
     TreeRow tr[2];
+    uint32_t words = 0;
     const int base = L - P.M;
     float mult[2];
     uint32_t qa[8][4];
@@ -215,7 +216,9 @@ __global__ void __launch_bounds__(WARPS * 32, 12 / WARPS) paged_attention_int4_k
             pr[hr] = L - P.M + m;
             lor[hr] = (P.window_left >= 0) ? max(0, pr[hr] - P.window_left) : 0;
             if (TREE) {
-                tr[hr] = tree_row(P, b, m, tree_word(P, b, m), base);
+                const uint64_t w = tree_word(P, b, m);
+                words |= (uint32_t)w;
+                tr[hr] = tree_row(P, b, m, w, base);
                 pr[hr] = base - 1;                          // the last key that needs no mask
                 lor[hr] = tr[hr].lo;
             }
@@ -368,11 +371,14 @@ __global__ void __launch_bounds__(WARPS * 32, 12 / WARPS) paged_attention_int4_k
             }
             lrow[hr] += sum;
         }
-        // ---- O += P V.  Keys that no row sees (behind the end, before the
-        // first window) get scale 0: whatever their bytes are, 0 reaches O
-        if (k0 + CK > L || k0 < lo0) {
+        // ---- O += P V.  Keys that no row sees (behind the end, before the first
+        // window, a tree's padding) get scale 0: whatever their bytes are, 0 reaches O
+        // (the warp's lanes have all rows of a tree call, at most 16)
+        uint32_t holes = 0;
+        if (TREE && k0 + CK > base) holes = ~__reduce_or_sync(0xffffffffu, words) & ((1u << P.M) - 1);
+        if (k0 + CK > L || k0 < lo0 || holes) {
             __syncwarp();
-            if (k0 + lane >= L || k0 + lane < lo0)
+            if (k0 + lane >= L || k0 + lane < lo0 || (TREE && tree_hole(holes, k0 + lane, base)))
                 *(uint2*)(smem + (warp * STAGES + cur_slot) * STAGE_BYTES + OFF_VS + lane * 8) = make_uint2(0u, 0u);
             __syncwarp();
         }

@@ -118,6 +118,10 @@ __device__ __forceinline__ void widen_chunk(const uint32_t (&at)[4], uint4 codes
     }
 }
 
+__device__ __forceinline__ void st_zero16(uint32_t a) {
+    asm volatile("st.shared.v4.b32 [%0], {%1, %1, %1, %1};" ::"r"(a), "r"(0) : "memory");
+}
+
 // CL: the partitions are a cluster.  TREE: what a row sees among the last M keys is
 // given by its mask word, so every row tile spans the same keys, to the end; a CTA
 // takes P.row_loop row tiles one after another, its loads and products running on
@@ -650,6 +654,8 @@ __global__ void __launch_bounds__(THREADS, 1) attention_int4_tc_kernel(AttnParam
 #pragma unroll
             for (int u = 0; u < 4; ++u)
                 at[u] = smem_u32(kbuf) + (cc >> 1) * HALF + r0 * 128 + (((4 * (cc & 1) + u) ^ (r0 & 7)) << 4);
+            // this thread's rows of the last two tiles, which hold the nodes, that are padding
+            uint32_t drop = 0;
             uint4 kc[2], vc[2];
             uint32_t ksc[2], vsc[2];
             auto load_k = [&](int t) {
@@ -704,6 +710,12 @@ __global__ void __launch_bounds__(THREADS, 1) attention_int4_tc_kernel(AttnParam
                 if (lane == 0) mbar_arrive(bar(B_APP));
                 ok = __all_sync(0xffffffffu, mbar_wait(bar(B_APP), (t - app_t0) & 1));
             };
+            const uint64_t holes = TREE ? tree_holes(P, b, lane) : 0;
+            if (TREE && holes) {
+#pragma unroll
+                for (int i = 0; i < 4; ++i)
+                    if (tree_hole(holes, k_begin + (n_tiles - 1 - (i >> 1)) * NK + r0 + 64 * (i & 1), L - P.M)) drop |= 1u << i;
+            }
             ok = __all_sync(0xffffffffu, mbar_wait(bar(B_STG_FULL), 0));
             if (ok && app_t0 == 0) patch(0);
             if (ok) {
@@ -739,6 +751,14 @@ __global__ void __launch_bounds__(THREADS, 1) attention_int4_tc_kernel(AttnParam
                 for (int u = 0; u < 4; ++u) to[u] = at[u] + (KBUFS + vb) * BUF;
                 widen_chunk<0>(to, vc[0], vsc[0]);
                 widen_chunk<64 * 128>(to, vc[1], vsc[1]);
+                if (TREE && drop) {
+                    // a tree's padding: zeros over what was stored
+                    const int back = tile == 0 ? 0 : n_tiles - tile;        // tiles behind this one
+#pragma unroll 1
+                    for (int u = 0; u < 2 && back < 2; ++u)
+                        if ((drop >> (2 * back + u)) & 1)
+                            for (int w = 0; w < 4; ++w) st_zero16(to[w] + u * 64 * 128);
+                }
                 fence_proxy_async();
                 __syncwarp();
                 if (lane == 0) mbar_arrive(bar(B_V_FULL + vb));

@@ -41,8 +41,8 @@
 //                chunk a thread, and write them over their rows of the staged tile and
 //                into the f16 tile, the cache afterwards
 //   warp 13      BF16: zeroes V rows that no row of the tile sees (behind the sequence's
-//                end, before its first window): whatever is stored there, 0 times it must
-//                not reach the output (E4M3: they are widened as zeros)
+//                end, before its first window, padding nodes): whatever is stored there, 0
+//                times it must not reach the output (E4M3: they are widened as zeros)
 // One sequence in 2 to 8 partitions: those of a KV head and row tile are a
 // thread-block cluster, and each CTA merges its share of the rows from the others'
 // shared memory.
@@ -95,12 +95,12 @@ enum {
     B_Q_READY = B_O + 2,
     B_IDLE = B_Q_READY + 1,
     B_PAIR = B_IDLE + 1,                                // per TMEM lane quarter: its two softmax warps
-    B_CLEAN = B_PAIR + 4,                               // BF16: V rows of the first, the last tile zeroed
-    B_PATCH = B_CLEAN + 2,                              // appended K rows written over a staged tile, one barrier for
+    B_CLEAN = B_PAIR + 4,                               // BF16: V rows of the first, the last, the last but one tile zeroed
+    B_PATCH = B_CLEAN + 3,                              // appended K rows written over a staged tile, one barrier for
                                                         // each of the (at most two) tiles that hold any
     B_COUNT = B_PATCH + 2
 };
-static_assert(B_COUNT * 8 + 16 <= 512, "barrier area");
+static_assert(B_COUNT * 8 + 16 + Cfg<true>::CONV * 8 <= 512, "barrier area");
 
 template <int PS, bool FP8, bool CL>     // CL: the partitions are a cluster
 __global__ void __launch_bounds__(Cfg<FP8>::THREADS, 1) attention_tree_tc_kernel(
@@ -202,10 +202,19 @@ __global__ void __launch_bounds__(Cfg<FP8>::THREADS, 1) attention_tree_tc_kernel
     const int n_pages = min(P.split_pages, last_page + 1 - page_begin);
     const int n_tiles = (n_pages + PPT - 1) / PPT;
     const int k_begin = page_begin * PS;
-    // V rows of tile t without a reader: those outside [zlo, zhi)
+    // (E4M3: in shared memory, each widening warp its own; 64 trees of 12 nodes 2% slower
+    // with them in the widening loop's registers)
+    const uint64_t holes = !FP8 && (warp == 2 || warp == 3 || converts) ? tree_holes(P, b, lane) : 0;
+    uint64_t* warp_holes = bars + B_COUNT + 2 + (warp - 12);
+    // V rows of tile t without a reader: those outside [zlo, zhi), and padding nodes
+    // (the nodes are in the last two tiles of a partition, if it has any)
     auto zlo_of = [&](int t) { return max(0, lo0 - (k_begin + t * NK)); };
     auto zhi_of = [&](int t) { return min(NK, L - (k_begin + t * NK)); };
-    auto dirty = [&](int t) { return !FP8 && ((t == 0 && zlo_of(t) > 0) || (t == n_tiles - 1 && zhi_of(t) < NK)); };
+    auto holes_in = [&](int t) { return holes && k_begin + t * NK + NK > L - P.M; };
+    auto dirty = [&](int t) {
+        return !FP8 && ((t == 0 && zlo_of(t) > 0) || (t == n_tiles - 1 && zhi_of(t) < NK) || holes_in(t));
+    };
+    auto clean = [&](int t) { return B_CLEAN + (t == 0 ? 0 : t == n_tiles - 1 ? 1 : 2); };
     // append: the new tokens in this partition, and the tiles that hold them
     const int app_lo = max(L - P.M, k_begin), app_hi = min(L, k_begin + n_pages * PS);
     const bool appends = FP8 && P.k_new && run && app_lo < app_hi;
@@ -291,7 +300,7 @@ __global__ void __launch_bounds__(Cfg<FP8>::THREADS, 1) attention_tree_tc_kernel
             for (int t = 0; t < n_tiles; ++t) {
                 const int s = t % STAGES, vb = t % VBUFS;
                 ok = FP8 ? mbar_wait(bar(B_V_FULL + vb), (t / VBUFS) & 1) : mbar_wait(bar(B_W_FULL + s), (t / STAGES) & 1);
-                if (ok && dirty(t)) ok = mbar_wait(bar(B_CLEAN + (t > 0)), 0);
+                if (ok && dirty(t)) ok = mbar_wait(bar(clean(t)), 0);
                 if (ok) ok = mbar_wait(bar(B_P + h), t & 1);
                 ok = __all_sync(0xffffffffu, ok);
                 if (!ok) break;
@@ -321,15 +330,16 @@ __global__ void __launch_bounds__(Cfg<FP8>::THREADS, 1) attention_tree_tc_kernel
             ok = __all_sync(0xffffffffu, mbar_wait(bar(B_W_FULL + s), (t / STAGES) & 1));
             if (!ok) break;
             if (dirty(t)) {
-                const int zlo = zlo_of(t), zhi = zhi_of(t);
+                const int zlo = zlo_of(t), zhi = zhi_of(t), node0 = L - P.M - (k_begin + t * NK);
                 uint8_t* v = stg + C::OFF_V + s * C::STG;
                 for (int i = lane; i < NK * 16; i += 32) {
                     const int r = i >> 4;
-                    if (r < zlo || r >= zhi) *(uint4*)(v + ((i >> 3) & 1) * HALF + r * 128 + (i & 7) * 16) = make_uint4(0, 0, 0, 0);
+                    if (r < zlo || r >= zhi || tree_hole(holes, r, node0))
+                        *(uint4*)(v + ((i >> 3) & 1) * HALF + r * 128 + (i & 7) * 16) = make_uint4(0, 0, 0, 0);
                 }
                 fence_proxy_async();
                 __syncwarp();
-                if (lane == 0) mbar_arrive(bar(B_CLEAN + (t > 0)));
+                if (lane == 0) mbar_arrive(bar(clean(t)));
             }
             __syncwarp();
             if (lane == 0) mbar_arrive(bar(B_W_EMPTY + s));
@@ -358,6 +368,8 @@ __global__ void __launch_bounds__(Cfg<FP8>::THREADS, 1) attention_tree_tc_kernel
             app_item(ct, kc0, vc0, pos0, chunk0);
             page0 = P.block_table[(int64_t)b * P.mpps + pos0 / PS];
         }
+        if (const uint64_t w = tree_holes(P, b, lane); lane == 0) *warp_holes = w;
+        __syncwarp();
         for (int t = 0; t < n_tiles; ++t) {
             const int s = t % STAGES, vb = t % VBUFS;
             ok = mbar_wait(bar(B_W_FULL + s), (t / STAGES) & 1);
@@ -396,7 +408,7 @@ __global__ void __launch_bounds__(Cfg<FP8>::THREADS, 1) attention_tree_tc_kernel
             uint8_t* second = dst + (c >> 2) * HALF + r0 * 128 + (((c16 + low) ^ r0) & 7) * 16;
             uint2 cf[PER], cg[PER];
             const uint8_t *sf = src + (low ? 0 : 8), *sg = src + (low ? 8 : 0);
-            const bool whole = zlo <= 0 && zhi >= NK && !patched;
+            const bool whole = zlo <= 0 && k0 + NK <= L - P.M;     // (no nodes)
             if (whole) {
 #pragma unroll
                 for (int u = 0; u < PER; ++u) {
@@ -404,10 +416,11 @@ __global__ void __launch_bounds__(Cfg<FP8>::THREADS, 1) attention_tree_tc_kernel
                     cg[u] = *(const uint2*)(sg + u * CONV_THREADS * 16);
                 }
             } else {
+                const uint64_t holes = *warp_holes;
 #pragma unroll
                 for (int u = 0; u < PER; ++u) {
                     const int r = r0 + CONV_THREADS / 8 * u;
-                    const bool in = r >= zlo && r < zhi;
+                    const bool in = r >= zlo && r < zhi && !tree_hole(holes, k0 + r, L - P.M);
                     cf[u] = in ? *(const uint2*)(sf + u * CONV_THREADS * 16) : make_uint2(0, 0);
                     cg[u] = in ? *(const uint2*)(sg + u * CONV_THREADS * 16) : make_uint2(0, 0);
                 }
@@ -430,6 +443,7 @@ __global__ void __launch_bounds__(Cfg<FP8>::THREADS, 1) attention_tree_tc_kernel
                     if (it != ct) app_item(it, kc, vc, pos, chunk);
                     const int r = pos - k0, c = chunk >> 1;
                     if (r < 0 || r >= NK) continue;
+                    if (tree_hole(*warp_holes, pos, L - P.M)) vc = make_uint2(0, 0);
                     *(uint4*)(dst + (c >> 2) * HALF + r * 128 + ((((2 * (c & 3) + (chunk & 1)) ^ r) & 7) << 4)) =
                         make_uint4(e4m3x2_to_f16x2(vc.x), e4m3x2_to_f16x2(vc.x >> 16), e4m3x2_to_f16x2(vc.y),
                                    e4m3x2_to_f16x2(vc.y >> 16));
