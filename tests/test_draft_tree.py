@@ -107,6 +107,66 @@ def test_binding_refuses_what_the_library_cannot_see():
         fp8kv._tree_rows(t(2, 4), "path", torch.int32, 2, 4)
 
 
+class _Shapes:
+    """CUDA tensors without memory, their pointers null: what the binding lets through,
+    the library refuses (Fp8kvError) before anything could be launched."""
+
+    def __init__(self, kind, D=128, row=128, heads=2, v_heads=2, v_ps=32):
+        z = lambda *shape, t=torch.bfloat16: torch.empty(shape, dtype=t, device="cuda")  # noqa: E731
+        i32, i64, f32 = torch.int32, torch.int64, torch.float32
+        T, H, B, M = 6, 2, 2, 3
+        if kind == "int4":
+            self.kc, self.vc = z(8, heads, 32 * 72, t=torch.uint8), z(8, v_heads, v_ps * 72, t=torch.uint8)
+        else:
+            t = torch.uint8 if kind == "e4m3" else torch.bfloat16
+            self.kc, self.vc = z(8, heads, 32, row, t=t), z(8, v_heads, v_ps, row, t=t)
+        k, v, q, slots, pos, s = z(T, H, D), z(T, H, D), z(T, 4, D), z(T, t=i64), z(T, t=i64), z(1, t=f32)
+        cs, w, hs = z(64, D, t=f32), z(D), z(H, t=f32)
+        qb, bt, sl, mask, new = z(B, M, 4, D), z(B, 4, t=i32), z(B, t=i32), z(B, M, t=i64), z(B, M, H, D)
+        c, sm = (self.kc, self.vc), D ** -0.5
+        self.calls = {
+            "insert": lambda: fp8kv.fp8kv_cache_insert(k, v, slots, s, s, *c),
+            "rope": lambda: fp8kv.fp8kv_rope_insert(q, k, v, pos, cs, slots, s, s, *c, q_out=z(T, 4, D)),
+            "attention": lambda: fp8kv.fp8kv_paged_attention(qb, *c, bt, sl, 100, s, s, sm),
+            "append": lambda: fp8kv.fp8kv_append_paged_attention(new, new, qb, *c, bt, sl, 100, s, s, sm),
+            "noalloc": lambda: fp8kv.fp8kv_paged_attention_noalloc(qb, *c, bt, sl, 100, s, s, sm, out=z(B, M, 4, D)),
+            "tree": lambda: fp8kv.fp8kv_tree_attention(qb, *c, bt, sl, mask, 100, s, s, sm),
+            "prepared": lambda: fp8kv.PreparedAttention(qb, *c, bt, sl, 100, s, s, sm, tree_mask=mask)(),
+        }
+        if kind == "e4m3":
+            self.calls["head insert"] = lambda: fp8kv.fp8kv_cache_insert_per_head(k, v, slots, hs, hs, *c)
+            self.calls["head attention"] = lambda: fp8kv.fp8kv_paged_attention_per_head(qb, *c, bt, sl, 100, hs, hs, sm)
+            self.calls["norm"] = lambda: fp8kv.fp8kv_qk_norm_rope_insert(q, k, v, pos, w, w, 1e-6, cs, z(T, 4, D), slots, s,
+                                                                         s, *c)
+
+
+@pytest.mark.parametrize("kind", CACHES)
+def test_binding_compares_the_caches_with_the_call(L, kind, monkeypatch):
+    """Rows of another length, another number of heads, a V cache of another shape: the
+    kernels would write and read beyond the caches."""
+    from torch._subclasses import FakeTensorMode
+    monkeypatch.setattr(fp8kv, "_stream", lambda stream, t=None: 0)
+    monkeypatch.setattr(fp8kv._Owned, "__init__", lambda self, tensors: None)
+    monkeypatch.setattr(fp8kv._Owned, "before_call", lambda self, stream, handle: None)
+    with FakeTensorMode():
+        for name, call in _Shapes(kind).calls.items():
+            with pytest.raises(fp8kv.Fp8kvError):               # null pointers
+                call()
+        bad = [dict(v_heads=1), dict(v_ps=64)]
+        if kind != "int4":
+            bad += [dict(row=64), dict(row=256), dict(D=64, row=128)]
+        for over in bad:
+            for name, call in _Shapes(kind, **over).calls.items():
+                with pytest.raises(ValueError):
+                    call()
+                    raise AssertionError((name, over))
+        for name in ("insert", "rope", "head insert", "norm"):
+            call = _Shapes(kind, heads=1, v_heads=1).calls.get(name)
+            if call:
+                with pytest.raises(ValueError):
+                    call()
+
+
 # ----------------------------------------------------------------- inputs
 
 def _tree(rng, B, M, shape):

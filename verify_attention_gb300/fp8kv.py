@@ -177,10 +177,15 @@ def _cache_dtype(cache: torch.Tensor) -> int:
     raise ValueError("cache must be uint8 (E4M3 codes, or INT4 pages) or bfloat16")
 
 
-def _cache_shape(k_cache: torch.Tensor, v_cache: torch.Tensor, dt: int):
-    """(num_pages, Hkv, page_size) of a pair of caches."""
+def _cache_shape(k_cache: torch.Tensor, v_cache: torch.Tensor, dt: int, D: Optional[int] = None):
+    """(num_pages, Hkv, page_size) of a pair of caches.  The library takes the
+    bytes of a row from D, the call's (None: the caches' own is passed)."""
     if dt != FP8KV_CACHE_INT4:
-        num_pages, Hkv, page_size, _ = k_cache.shape
+        num_pages, Hkv, page_size, row = k_cache.shape
+        if D is not None and row != D:
+            raise ValueError(f"k_cache and v_cache have rows of {row} elements, the call has heads of {D}")
+        if v_cache.dtype != k_cache.dtype or v_cache.shape != k_cache.shape:
+            raise ValueError("k_cache and v_cache must have the same type and shape")
         return num_pages, Hkv, page_size
     num_pages, Hkv, nbytes = k_cache.shape
     if nbytes % INT4_ROW_BYTES:
@@ -209,10 +214,10 @@ def fp8kv_cache_insert(k, v, slot_mapping, k_scale, v_scale, k_cache, v_cache, s
     _dev(k, "k", torch.bfloat16), _dev(v, "v", torch.bfloat16)
     _dev(slot_mapping, "slot_mapping", torch.int64), _dev(k_cache, "k_cache"), _dev(v_cache, "v_cache")
     T, Hkv, D = k.shape
-    num_pages, heads, page_size = _cache_shape(k_cache, v_cache, dt)
+    num_pages, heads, page_size = _cache_shape(k_cache, v_cache, dt, D)
+    if heads != Hkv or v.shape != k.shape or slot_mapping.numel() != T:
+        raise ValueError(f"k, v must be [T][{heads}][D] and slot_mapping [T]")
     if dt == FP8KV_CACHE_INT4:
-        if heads != Hkv or v.shape != (T, Hkv, D) or slot_mapping.numel() != T:
-            raise ValueError(f"k, v must be [T][{heads}][D] and slot_mapping [T]")
         _one_scale(k_scale, v_scale)
     rc = lib().fp8kv_cache_insert(k.data_ptr(), v.data_ptr(), slot_mapping.data_ptr(), T, Hkv, D, _ptr(k_scale),
                                   _ptr(v_scale), k_cache.data_ptr(), v_cache.data_ptr(), num_pages, page_size,
@@ -245,8 +250,6 @@ def fp8kv_cache_gather(slot_mapping, k_scale, v_scale, k_cache, v_cache, k_out=N
     outputs are allocated here).  Any cache type, per-tensor scales."""
     dt = _cache_dtype(k_cache)
     _dev(slot_mapping, "slot_mapping", torch.int64), _dev(k_cache, "k_cache"), _dev(v_cache, "v_cache")
-    if dt != FP8KV_CACHE_INT4 and (v_cache.dtype != k_cache.dtype or v_cache.shape != k_cache.shape):
-        raise ValueError("k_cache and v_cache must have the same type and shape")
     num_pages, Hkv, page_size = _cache_shape(k_cache, v_cache, dt)
     T, D = slot_mapping.numel(), 128 if dt == FP8KV_CACHE_INT4 else k_cache.shape[3]
     if dt != FP8KV_CACHE_BF16:
@@ -278,7 +281,9 @@ def fp8kv_cache_insert_per_head(k, v, slot_mapping, k_scale, v_scale, k_cache, v
     _dev(k_cache, "k_cache", torch.uint8), _dev(v_cache, "v_cache", torch.uint8)
     T, Hkv, D = k.shape
     _head_scales(k_scale, v_scale, Hkv)
-    num_pages, _, page_size, _ = k_cache.shape
+    num_pages, heads, page_size = _cache_shape(k_cache, v_cache, FP8KV_CACHE_E4M3, D)
+    if heads != Hkv or v.shape != k.shape or slot_mapping.numel() != T:
+        raise ValueError(f"k, v must be [T][{heads}][D] and slot_mapping [T]")
     rc = lib().fp8kv_cache_insert_per_head(_ptr(k), _ptr(v), _ptr(slot_mapping), T, Hkv, D, _ptr(k_scale),
                                            _ptr(v_scale), _ptr(k_cache), _ptr(v_cache), num_pages, page_size,
                                            _stream(stream))
@@ -296,7 +301,11 @@ def fp8kv_qk_norm_rope_insert(q, k, v, positions, q_norm_w, k_norm_w, eps, cos_s
     _dev(v_cache, "v_cache", torch.uint8)
     T, Hq, D = q.shape
     Hkv = k.shape[1]
-    num_pages, _, page_size, _ = k_cache.shape
+    num_pages, heads, page_size = _cache_shape(k_cache, v_cache, FP8KV_CACHE_E4M3, D)
+    if k.shape != (T, heads, D) or v.shape != k.shape or q_out.shape != q.shape:
+        raise ValueError(f"k, v must be [{T}][{heads}][{D}] and q_out of the shape of q")
+    if positions.numel() != T or slot_mapping.numel() != T:
+        raise ValueError(f"positions and slot_mapping must be [{T}]")
     rc = lib().fp8kv_qk_norm_rope_insert(
         _ptr(q), _ptr(k), _ptr(v), _ptr(positions), _ptr(q_norm_w), _ptr(k_norm_w), float(eps),
         _ptr(cos_sin), cos_sin.shape[0], _ptr(q_out), _ptr(slot_mapping), T, Hq, Hkv, D, _ptr(k_scale),
@@ -352,9 +361,9 @@ def fp8kv_rope_insert(q, k, v, positions, cos_sin, slot_mapping, k_scale, v_scal
     k_stride, v_stride = _token_rows(k, "k", T, Hkv, D), _token_rows(v, "v", T, Hkv, D)
     _dev(positions, "positions", torch.int64), _dev(slot_mapping, "slot_mapping", torch.int64)
     _dev(cos_sin, "cos_sin", torch.float32), _dev(k_cache, "k_cache"), _dev(v_cache, "v_cache")
-    num_pages, heads, page_size = _cache_shape(k_cache, v_cache, dt)
-    if heads != Hkv or v_cache.dtype != k_cache.dtype or v_cache.shape != k_cache.shape:
-        raise ValueError(f"k_cache and v_cache must have the same type and shape, of {Hkv} heads")
+    num_pages, heads, page_size = _cache_shape(k_cache, v_cache, dt, D)
+    if heads != Hkv:
+        raise ValueError(f"k_cache and v_cache must be of {Hkv} heads")
     if positions.numel() != T or slot_mapping.numel() != T or cos_sin.dim() != 2:
         raise ValueError(f"positions and slot_mapping must be [{T}], cos_sin [max_pos][rot_dim]")
     if dt != FP8KV_CACHE_BF16:
@@ -399,7 +408,7 @@ def fp8kv_paged_attention(q, k_cache, v_cache, block_table, seq_lens, max_seq_le
     _dev(q, "q", torch.bfloat16), _dev(k_cache, "k_cache"), _dev(v_cache, "v_cache")
     _dev(block_table, "block_table", torch.int32), _dev(seq_lens, "seq_lens", torch.int32)
     B, M, Hq, D = q.shape
-    P, Hkv, page_size = _cache_shape(k_cache, v_cache, dt)
+    P, Hkv, page_size = _cache_shape(k_cache, v_cache, dt, D)
     if dt == FP8KV_CACHE_INT4:
         _int4_call(q, k_cache, block_table, seq_lens, k_scale, v_scale, out, num_pages)
     if num_pages is None:
@@ -429,7 +438,7 @@ def fp8kv_append_paged_attention(k_new, v_new, q, k_cache, v_cache, block_table,
     _dev(q, "q", torch.bfloat16), _dev(k_cache, "k_cache"), _dev(v_cache, "v_cache")
     _dev(block_table, "block_table", torch.int32), _dev(seq_lens, "seq_lens", torch.int32)
     B, M, Hq, D = q.shape
-    P, Hkv, page_size = _cache_shape(k_cache, v_cache, dt)
+    P, Hkv, page_size = _cache_shape(k_cache, v_cache, dt, D)
     if dt == FP8KV_CACHE_INT4:
         _int4_call(q, k_cache, block_table, seq_lens, k_scale, v_scale, out, num_pages)
     if tuple(k_new.shape) != (B, M, Hkv, D) or tuple(v_new.shape) != (B, M, Hkv, D):
@@ -460,7 +469,7 @@ def fp8kv_paged_attention_per_head(q, k_cache, v_cache, block_table, seq_lens, m
     _dev(q, "q", torch.bfloat16), _dev(k_cache, "k_cache", torch.uint8), _dev(v_cache, "v_cache", torch.uint8)
     _dev(block_table, "block_table", torch.int32), _dev(seq_lens, "seq_lens", torch.int32)
     B, M, Hq, D = q.shape
-    P, Hkv, page_size, _ = k_cache.shape
+    P, Hkv, page_size = _cache_shape(k_cache, v_cache, FP8KV_CACHE_E4M3, D)
     _head_scales(k_scale, v_scale, Hkv)
     if (k_new is None) != (v_new is None):
         raise ValueError("k_new and v_new go together")
@@ -552,7 +561,7 @@ class PreparedAttention:
         _dev(q, "q", torch.bfloat16), _dev(k_cache, "k_cache"), _dev(v_cache, "v_cache")
         _dev(block_table, "block_table", torch.int32), _dev(seq_lens, "seq_lens", torch.int32)
         B, M, Hq, D = q.shape
-        P, Hkv, page_size = _cache_shape(k_cache, v_cache, dt)
+        P, Hkv, page_size = _cache_shape(k_cache, v_cache, dt, D)
         if dt == FP8KV_CACHE_INT4:
             _int4_call(q, k_cache, block_table, seq_lens, k_scale, v_scale, out, num_pages)
         if tree_mask is not None:
@@ -616,7 +625,7 @@ def fp8kv_paged_attention_noalloc(q, k_cache, v_cache, block_table, seq_lens, ma
     if out.shape != q.shape or out.device != q.device:
         raise ValueError(f"out must have the shape and device of q {tuple(q.shape)}, got {tuple(out.shape)}")
     B, M, Hq, D = q.shape
-    P, Hkv, page_size = _cache_shape(k_cache, v_cache, dt)
+    P, Hkv, page_size = _cache_shape(k_cache, v_cache, dt, D)
     if dt == FP8KV_CACHE_INT4:
         _int4_call(q, k_cache, block_table, seq_lens, k_scale, v_scale, out, num_pages)
     rc = lib().fp8kv_paged_attention_noalloc(
@@ -676,8 +685,6 @@ def _tree_call(q, k_cache, v_cache, block_table, seq_lens, tree_mask, k_scale, v
     _tree_rows(tree_mask, "tree_mask", torch.int64, B, M)
     if block_table.dim() != 2 or block_table.shape[0] != B or seq_lens.numel() != B:
         raise ValueError(f"block_table must be [{B}][pages] and seq_lens [{B}]")
-    if v_cache.dtype != k_cache.dtype or v_cache.shape != k_cache.shape:
-        raise ValueError("k_cache and v_cache must have the same type and shape")
     if dt != FP8KV_CACHE_BF16:
         _one_scale(k_scale, v_scale)
     if out is not None and _dev(out, "out", torch.bfloat16).shape != q.shape:
@@ -689,7 +696,7 @@ def _tree_call(q, k_cache, v_cache, block_table, seq_lens, tree_mask, k_scale, v
 def _tree_args(q, k_cache, v_cache, dt, block_table, seq_lens, max_seq_len, tree_mask, k_scale, v_scale, sm_scale,
                window_left, split_tokens, workspace, out, k_new, v_new, num_pages):
     B, M, Hq, D = q.shape
-    P, Hkv, page_size = _cache_shape(k_cache, v_cache, dt)
+    P, Hkv, page_size = _cache_shape(k_cache, v_cache, dt, D)
     return (_ptr(k_new), _ptr(v_new), _ptr(q), _ptr(k_cache), _ptr(v_cache), dt, _ptr(block_table),
             block_table.shape[1], _ptr(seq_lens), int(max_seq_len), _ptr(tree_mask), B, M, Hq, Hkv, D, page_size,
             int(P if num_pages is None else num_pages), _ptr(k_scale), _ptr(v_scale), float(sm_scale),
@@ -708,7 +715,7 @@ def fp8kv_tree_attention(q, k_cache, v_cache, block_table, seq_lens, tree_mask, 
     _dev(q, "q", torch.bfloat16), _dev(k_cache, "k_cache"), _dev(v_cache, "v_cache")
     _dev(block_table, "block_table", torch.int32), _dev(seq_lens, "seq_lens", torch.int32)
     B, M, Hq, D = q.shape
-    _, Hkv, page_size = _cache_shape(k_cache, v_cache, dt)
+    _, Hkv, page_size = _cache_shape(k_cache, v_cache, dt, D)
     _tree_call(q, k_cache, v_cache, block_table, seq_lens, tree_mask, k_scale, v_scale, out, num_pages, dt)
     if (k_new is None) != (v_new is None):
         raise ValueError("k_new and v_new go together")
