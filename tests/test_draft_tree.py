@@ -750,6 +750,33 @@ def test_verify_truncated_rows_and_strided_views(draft):
 
 
 @pytest.mark.gpu
+@pytest.mark.parametrize("dtype", ["fp32", "bf16"])
+def test_chosen_drafts_at_every_boundary_of_a_row(dtype):
+    """Rows that start at each place of a 16-byte group, in CTAs of many whole chunks;
+    without draft_probs its stride means nothing."""
+    rng = np.random.default_rng(15)
+    B, M, V = 300, 3, 50001
+    p, _ = _probs(rng, 1, 2 * M, V)
+    pick = rng.integers(0, 2 * M, (B, M))
+    tp = torch.from_numpy(p[0]).to(torch.float32 if dtype == "fp32" else torch.bfloat16)
+    rows = tp.cuda()[_cuda(pick)]
+    p = tp.float().numpy()[pick]
+    par = _tree(rng, B, M, "tree")
+    tok = _draws(rng, p, par)
+    u = np.minimum(rng.random((B, M)).astype(np.float32), np.float32(1 - 2.0 ** -24))
+    dev = _cuda(tok, par, u)
+    got = fp8kv.fp8kv_verify_tree(rows, None, *dev)
+    _check_verify(p, None, tok, par, u, got)
+    for stride in (1, V + 2):
+        again = [torch.empty_like(t) for t in got]
+        rc = fp8kv.lib().fp8kv_verify_tree(rows.data_ptr(), V, 0, stride, 0 if dtype == "fp32" else 1,
+                                           *(t.data_ptr() for t in dev), B, M, V,
+                                           *(t.data_ptr() for t in again), torch.cuda.current_stream().cuda_stream)
+        assert rc == 0 and all(torch.equal(a, b) for a, b in zip(got, again))
+    _status()
+
+
+@pytest.mark.gpu
 def test_verify_a_greedy_target_and_certain_cases():
     """Rows of one 1: the path follows the target's tokens whatever the numbers."""
     rng = np.random.default_rng(6)
