@@ -1,6 +1,7 @@
 """A step over trees of drafted tokens: argument checks (CPU), and metadata, rotary
 insert, attention, verification and the kept path on the GPU against float64."""
 import ctypes
+from fractions import Fraction
 
 import numpy as np
 import pytest
@@ -773,6 +774,59 @@ def test_chosen_drafts_at_every_boundary_of_a_row(dtype):
                                            *(t.data_ptr() for t in dev), B, M, V,
                                            *(t.data_ptr() for t in again), torch.cuda.current_stream().cuda_stream)
         assert rc == 0 and all(torch.equal(a, b) for a, b in zip(got, again))
+    _status()
+
+
+def _after_falls(p, q, k):
+    """What k falls leave of p, exact up to a common factor."""
+    w = [max(a - b, 0) for a, b in zip(p, q)]
+    for _ in range(k - 1):
+        S = sum(w)
+        w = [max(a - S * b, 0) for a, b in zip(w, q)]
+        while 0 < sum(w) < 1:
+            w = [2 * a for a in w]
+    return w
+
+
+@pytest.mark.gpu
+def test_verify_draws_what_little_many_falls_leave():
+    """A drafter that is the target but for a little weight on a token which the target
+    does not have; every sibling drew that one and falls, each fall leaving that little
+    of the weights, so that what is left are differences of their last bits.  A weight
+    is off by 2^-45 of the one before the fall, and p and q differ by 2^-24 of
+    themselves where anything is left: 2^-21 in all, and the draws keep 2^-16 of the
+    sum from every border."""
+    drawn = 0
+    for seed in range(60):
+        rng = np.random.default_rng(seed)
+        A = int(rng.integers(4, 40))
+        share = rng.random(A) + 0.5
+        share /= share.sum()
+        extra = 2.0 ** -float(rng.integers(5, 10))
+        p = np.concatenate([share, [0]]).astype(np.float32)
+        q = np.concatenate([share * (1 - extra), [extra]]).astype(np.float32)
+        pf, qf = ([Fraction(float(x)) for x in r] for r in (p, q))
+        for k in range(2, 10):
+            w = _after_falls(pf, qf, k)
+            ends, total = np.cumsum(np.array(w, object)), sum(w)
+            if total == 0:
+                continue
+            u0, want = [], []
+            for i, x in enumerate(w):
+                u = np.float32(float((ends[i] - x / 2) / total))
+                t = Fraction(float(u)) * total
+                if min(t - ends[i] + x, ends[i] - t) > total / 2 ** 16:
+                    u0.append(u)
+                    want.append(i)
+            B, M = len(u0), k + 1
+            u = np.full((B, M), 0.5, np.float32)
+            u[:, 0] = u0
+            rows = [torch.from_numpy(r).cuda().expand(B, M, A + 1).contiguous() for r in (p, q)]
+            par, tok = np.zeros((B, M), np.int32), np.full((B, M), A, np.int32)
+            out, num, _ = fp8kv.fp8kv_verify_tree(*rows, *_cuda(tok, par, u))
+            assert num.tolist() == [1] * B and out[:, 0].tolist() == want, (seed, k)
+            drawn += B
+    assert drawn > 2000
     _status()
 
 

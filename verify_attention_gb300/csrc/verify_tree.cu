@@ -120,13 +120,16 @@ struct __align__(16) VerifyStep {
 
 // (Negative, zero and NaN: nothing left.  The differences are exact by the short sum:
 // where the first operand is the smaller one, either nothing is left, or they are
-// within a factor of two of each other and the difference itself is exact.)
+// within a factor of two of each other and the difference itself is exact.  Little may
+// be left of hi then, and lo be the larger one: the pair is put in order, as the next
+// step and whoever asks for hi > 0 expect it.  The short sum is exact there too: d.hi is
+// a multiple of the last places of both operands, lo at most a few of them, so d.hi is
+// one of lo's last place.)
 __device__ __forceinline__ F2 step_weight(F2 w, float q, VerifyStep s) {
     const float th = __fmul_rn(s.bh, q), tl = __fmaf_rn(s.bl, q, __fmaf_rn(s.bh, q, -th));
     const F2 d = fast_two_sum(__fmul_rn(w.hi, s.a), -th);
-    const float lo = __fadd_rn(d.lo, __fmaf_rn(w.lo, s.a, -tl));
-    const bool some = __fadd_rn(d.hi, lo) > 0.f;
-    return {some ? d.hi : 0.f, some ? lo : 0.f};
+    const F2 left = fast_two_sum(d.hi, __fadd_rn(d.lo, __fmaf_rn(w.lo, s.a, -tl)));
+    return {fmaxf(left.hi, 0.f), left.hi > 0.f ? left.lo : 0.f};
 }
 // a node's first step: S = 1, so w - q, exactly
 __device__ __forceinline__ F2 first_step(float p, float q) {
