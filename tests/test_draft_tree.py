@@ -831,6 +831,45 @@ def test_verify_draws_what_little_many_falls_leave():
 
 
 @pytest.mark.gpu
+@pytest.mark.parametrize("draft", [True, False])
+def test_verify_sums_of_many_small_weights(draft):
+    """Four million tokens a CTA, a few of weight 1 or some at the start of every warp's
+    run and then 2^-26 (1 + 2^-13) each: a thread's sum of those is multiples of 2^-39 beside its
+    1, so every sum is exact in a pair whose parts are in order (a low part that only
+    grows loses 2^-39 a token behind 2^-14: tens of tokens by the end of a run).  The
+    draw t is the product of u and the sum, off by 2^-47 of it: 2^-37, and a token's
+    width is 2^-26; draws nearer than 2^-30 to a border are left out."""
+    B, V, one = 257, 1 << 22, 1 << 39
+    w = np.full(V, (1 << 13) + 1, np.int64)             # units of 2^-39
+    run = V // 8
+    for i in range(8):
+        for lane in range(32):
+            w[i * run + 4 * lane:i * run + 4 * lane + 2] = one
+    rng = np.random.default_rng(2)
+    w[2:4096:4] = rng.integers(1 << 21, 1 << 22, 1024) << 16       # (so that draws fall anywhere in a token)
+    ends = np.cumsum(w)
+    total = int(ends[-1])
+    u, want = [], []
+    for _ in range(4 * B):
+        v = int(rng.integers(7)) * run + int(rng.integers(run // 2, run))
+        x = np.float32(int(ends[v]) / total)
+        t = Fraction(float(x)) * total
+        at = int(np.searchsorted(ends, int(t), side="right"))
+        if min(t - int(ends[at]) + int(w[at]), int(ends[at]) - t) > 512:
+            u.append([x])
+            want.append(at)
+    u, want = u[:B], want[:B]
+    assert len(u) == B
+    row = torch.from_numpy((w / one).astype(np.float32)).cuda()
+    assert np.array_equal(row.double().cpu().numpy() * one, w)
+    p = row.expand(B, 1, V).contiguous()
+    none = torch.zeros((B, 1), dtype=torch.int32, device="cuda")
+    out, num, _ = fp8kv.fp8kv_verify_tree(p, p if draft else None, none, none, _cuda(np.array(u, np.float32)))
+    assert num.tolist() == [1] * B and out[:, 0].tolist() == want
+    _status()
+
+
+@pytest.mark.gpu
 def test_verify_a_greedy_target_and_certain_cases():
     """Rows of one 1: the path follows the target's tokens whatever the numbers."""
     rng = np.random.default_rng(6)

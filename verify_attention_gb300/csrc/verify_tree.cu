@@ -23,7 +23,8 @@
 // times the time of the HBM reads; a first form with it in the scans took 17.8 us
 // for one sequence of 131072 tokens, this one 6).  The weights, the sums and the prefixes are
 // pairs of fp32 instead, hi + lo with the rounding error of each step in lo (the
-// two-sum and two-product of Dekker and Knuth): 2^-45 of the weight a step.
+// two-sum and two-product of Dekker and Knuth): at most 2^-45 of a weight a fall, 2^-44
+// of a sum a token that is added to it.
 #include "attention.cuh"
 #include "common.cuh"
 
@@ -433,6 +434,13 @@ __global__ void __launch_bounds__(kVerifyThreads, !DRAFT ? 4 : sizeof(T) == 4 ? 
                     to = {s.hi, __fadd_rn(to.lo, DRAFT ? __fadd_rn(s.lo, lo[i]) : s.lo)};
                 }
             };
+            // lo grows by up to 2^-24 of the sum a token: it is put back into place every four
+            // to eight tokens of a sum, so that a token's rounding of lo stays below 2^-44 of
+            // the sum (by the end only: 2^-24 of a lo that grows with the tokens)
+            auto in_order = [&] {
+                acc = fast_two_sum(acc.hi, acc.lo);
+                odd = fast_two_sum(odd.hi, odd.lo);
+            };
             // whole chunks of 32 groups, the next U on their way (64 trees, drawn: 46 us with
             // their loads behind branches that look at the row's ends); the others, and
             // all where q lies differently from p, one by one (`!both ||` beside qr.aligned would
@@ -444,6 +452,7 @@ __global__ void __launch_bounds__(kVerifyThreads, !DRAFT ? 4 : sizeof(T) == 4 ? 
                 fetch(lane, x, y);
                 add(x, y, lane);
                 g = 32;
+                in_order();
             }
             if (g < whole) {
                 const bool both = DRAFT && k > 0;
@@ -468,6 +477,7 @@ __global__ void __launch_bounds__(kVerifyThreads, !DRAFT ? 4 : sizeof(T) == 4 ? 
                         add(xu, yu, g + lane);
                         g += 32;
                     }
+                    in_order();
                 }
             }
 #pragma unroll 1
@@ -475,9 +485,10 @@ __global__ void __launch_bounds__(kVerifyThreads, !DRAFT ? 4 : sizeof(T) == 4 ? 
                 uint4 x, y;
                 fetch(g + lane, x, y);
                 add(x, y, g + lane);
+                in_order();
             }
             // ---- the sums of the warps
-            acc = fast_two_sum(acc.hi, acc.lo) + fast_two_sum(odd.hi, odd.lo);
+            acc = acc + odd;
             acc = warp_total<32>(acc);
             if (lane == 0) warp_sum[stage][warp] = acc;
             __syncthreads();
