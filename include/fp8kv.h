@@ -548,8 +548,10 @@ int fp8kv_tree_attention(const void* k_new, const void* v_new, const void* q, vo
  *     w <- max(w - S q_n, 0), S <- sum of w     (NULL: S <- S - w(x), w(x) <- 0).
  * When no child is left, the next token is the first v whose running sum of w
  * exceeds uniforms[0] times the sum of w (of p_n, should nothing be left of it).
- * With uniforms drawn from [0, 1) the tokens are distributed as the target alone
- * would draw them.  A greedy target is one with rows of one 1.
+ * With uniforms drawn from [0, 1) and rows that sum to 1 the tokens are distributed as
+ * the target alone would draw them (S begins at 1, not at a row's sum: what a row's sum
+ * lacks, some 2^-9 of a bf16 row, the distribution may be off by).  A greedy target is
+ * one with rows of one 1.
  *
  *   target_probs, draft_probs (device) fp32 or bf16 (prob_dtype) [B][M][V], the rows
  *     of consecutive nodes target_stride and draft_stride elements apart (>= V);
@@ -558,7 +560,8 @@ int fp8kv_tree_attention(const void* k_new, const void* v_new, const void* q, vo
  *   tokens, parents (device) int32 [B][M] (tokens[b][0], parents[b][0] not used)
  *   uniforms   (device) fp32 [B][M] in [0, 1)
  *   out_tokens (device) int32 [B][M]: the tokens that stand, the next one, then -1
- *   num_tokens (device) int32 [B]: how many those are, 1 .. M
+ *   num_tokens (device) int32 [B]: how many those are, 1 .. M; without a next token
+ *     (FP8KV_DEV_BAD_PROBS) one less, 0 .. M - 1
  *   path       (device) int32 [B][M]: node 0 and the nodes that stand, then -1
  * Pairs of fp32: a weight is off by at most 2^-45 of what it was before the fall, a
  * sum by (16 + V / (256 c)) 2^-44 of itself, c = 1 .. 16 CTAs a sequence (1 for more

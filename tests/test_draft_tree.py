@@ -913,6 +913,32 @@ def test_verify_distributes_tokens_as_the_target():
 
 
 @pytest.mark.gpu
+@pytest.mark.parametrize("draft", [True, False])
+def test_verify_distributes_the_second_token_too(draft):
+    """Behind each first token that stands, the counts of the second: binomial, 6 sigma
+    (chosen drafts: two tokens that the drafter likes best, at either node)."""
+    rng = np.random.default_rng(13)
+    B, V = 200000, 6
+    p, q = (np.repeat(x, B, 0) for x in _probs(rng, 1, 5, V, sharp=1.0))
+    par = np.tile(np.array([-1, 0, 0, 1, 1], np.int32), (B, 1))
+    tok = _draws(rng, q, par) if draft else np.tile(np.array([0, 2, 4, 1, 3], np.int32), (B, 1))
+    u = np.minimum(rng.random((B, 5)).astype(np.float32), np.float32(1 - 2.0 ** -24))
+    out, num, path = (t.cpu().numpy() for t in fp8kv.fp8kv_verify_tree(
+        _cuda(p), _cuda(q) if draft else None, _cuda(tok), _cuda(par), _cuda(u)))
+
+    def binomial(tokens, row):
+        e = row.astype(np.float64) * len(tokens)
+        assert np.all(np.abs(np.bincount(tokens, minlength=V) - e) <= 6 * np.sqrt(e * (1 - e / len(tokens))) + 1)
+
+    binomial(out[:, 0], p[0, 0])
+    behind = path[:, 1] == 1
+    assert behind.sum() > 5000
+    # (the tree's second token hangs on node 1: its row)
+    binomial(out[behind, 1], p[0, 1])
+    assert num.min() >= 1 and (num[behind] >= 2).all()
+
+
+@pytest.mark.gpu
 def test_verify_flags_bad_input():
     V, M = 40, 4
     p = torch.full((6, M, V), 1.0 / V, device="cuda")

@@ -754,7 +754,7 @@ def fp8kv_verify_tree(target_probs, draft_probs, tokens, parents, uniforms, out_
     None (what n's children were drawn from; None: they were chosen), tokens and
     parents int32 [B][M], uniforms fp32 [B][M] in [0, 1).  Returns out_tokens int32
     [B][M] (the tokens that stand, the next one, -1s), num_tokens int32 [B] (how many
-    those are) and path int32 [B][M] (node 0, the nodes that stand, -1s)."""
+    those are: 0 .. M, 0 where a root row without a sum has none to draw) and path int32 [B][M] (node 0, the nodes that stand, -1s)."""
     if target_probs.dim() != 3:
         raise ValueError("target_probs must be [B][M][V]")
     B, M, V = target_probs.shape
