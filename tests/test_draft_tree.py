@@ -534,6 +534,22 @@ def test_negative_scale_and_large_logits(kind, M, Hq):
 
 @pytest.mark.gpu
 @pytest.mark.parametrize("kind", CACHES)
+@pytest.mark.parametrize("lens,M,Hq,split", [([900], 4, 4, 0), ([900, 70], 12, 18, 0), ([500], 40, 18, 0),
+                                             ([900], 12, 18, 128)])
+def test_a_negative_scale_is_that_of_negated_queries(kind, lens, M, Hq, split):
+    """-sm_scale with -q: the same logits, hence the same bits in every kernel (negation
+    is exact in every type that holds q), and the values of the oracle."""
+    c = Case(18, kind, lens, M, Hq, 2, 32, "ragged")
+    got = c.run(split=split)
+    c.check(got)
+    neg = fp8kv.fp8kv_tree_attention(-c.q.cuda(), c.kc, c.vc, _cuda(c.bt), _cuda(np.array(c.lens, np.int32)),
+                                     _cuda(c.mask), max(c.lens), c.ks, c.vs, -SM, split_tokens=split)
+    assert torch.equal(neg, got)
+    _status()
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("kind", CACHES)
 def test_nan_stays_with_the_rows_that_see_it(kind):
     """A NaN key among the nodes reaches its descendants and no sibling's row."""
     c = Case(31, kind, [200], 12, 18, 2, 32, "star")
