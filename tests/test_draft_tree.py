@@ -488,6 +488,30 @@ def test_appended_nodes(kind, lens, M, Hq, H, window):
 
 @pytest.mark.gpu
 @pytest.mark.parametrize("kind", CACHES)
+@pytest.mark.parametrize("M,Hq,lens", [(4, 4, [200, 34]), (12, 18, [200, 100]), (40, 6, [150, 70]), (40, 18, [150, 70])])
+def test_appended_nodes_on_pages_outside_the_pool(kind, M, Hq, lens):
+    """They are not written, and read as zeros, as after an insert of the others."""
+    c = Case(M + 5, kind, lens, M, Hq, 2, 32, "tree")
+    for b, n in enumerate(c.lens):
+        c.bt[b, (n - 1) // 32] = (-1, c.pages)[b]       # the last page, on which nodes are
+    pos = np.array([[n - M + m for m in range(M)] for n in c.lens])
+    page = np.take_along_axis(c.bt, pos // 32, 1).astype(np.int64)
+    good = (page >= 0) & (page < c.pages)
+    slots = _cuda(np.where(good, page * 32 + pos % 32, -1)).reshape(-1)
+    g = torch.Generator().manual_seed(7)
+    kn, vn = (torch.randn((len(lens), M, 2, 128), generator=g).to(torch.bfloat16).cuda() for _ in range(2))
+    whole = c.kc.clone(), c.vc.clone()
+    fp8kv.fp8kv_cache_insert(kn.view(-1, 2, 128), vn.view(-1, 2, 128), slots, c.ks, c.vs, *whole)
+    got = c.run(k_new=kn, v_new=vn)
+    for a, w, s in ((c.kc, whole[0], c.ks), (c.vc, whole[1], c.vs)):
+        assert np.array_equal(_values(a, kind, 32, s), _values(w, kind, 32, s), equal_nan=True)
+    _status(fp8kv.DEV_BAD_SLOT)
+    assert torch.equal(got, c.run())
+    _status()
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("kind", CACHES)
 def test_masks_of_any_kind(kind):
     """Words that are no ancestor sets (a node that sees a later one, not itself),
     bits beyond M, and none."""

@@ -360,8 +360,13 @@ __global__ void __launch_bounds__(Cfg<FP8>::THREADS, 1) attention_tree_tc_kernel
             kc = e4m3_encode8(have ? first_k : ((const uint4*)P.k_new)[src], ksc);
             vc = e4m3_encode8(have ? first_v : ((const uint4*)P.v_new)[src], vsc);
         };
-        // this thread's first item is kept (its page id is read here and used behind
-        // the tiles, where the cache is written)
+        // (a token on a page outside the pool is not written: its row stays the zeros of
+        // the staged page)
+        auto held = [&](int it, int pos, int page) {
+            if (it != ct) page = P.block_table[(int64_t)b * P.mpps + pos / PS];
+            return page >= 0 && page < P.num_pages;
+        };
+        // this thread's first item is kept, and its page id
         uint2 kc0 = make_uint2(0, 0), vc0 = kc0;
         int pos0 = -1, chunk0 = 0, page0 = -1;
         if (ct < n_app * 16) {
@@ -384,7 +389,8 @@ __global__ void __launch_bounds__(Cfg<FP8>::THREADS, 1) attention_tree_tc_kernel
                     int pos = pos0, chunk = chunk0;
                     if (it != ct) app_item(it, kc, vc, pos, chunk);
                     const int r = pos - k0;
-                    if (r >= 0 && r < NK) *(uint2*)(kst + r * 128 + ((((chunk >> 1) ^ r) & 7) << 4) + (chunk & 1) * 8) = kc;
+                    if (r >= 0 && r < NK && held(it, pos, page0))
+                        *(uint2*)(kst + r * 128 + ((((chunk >> 1) ^ r) & 7) << 4) + (chunk & 1) * 8) = kc;
                 }
                 fence_proxy_async();                        // for the tensor cores' read of K
                 __syncwarp();
@@ -443,7 +449,7 @@ __global__ void __launch_bounds__(Cfg<FP8>::THREADS, 1) attention_tree_tc_kernel
                     if (it != ct) app_item(it, kc, vc, pos, chunk);
                     const int r = pos - k0, c = chunk >> 1;
                     if (r < 0 || r >= NK) continue;
-                    if (tree_hole(*warp_holes, pos, L - P.M)) vc = make_uint2(0, 0);
+                    if (tree_hole(*warp_holes, pos, L - P.M) || !held(it, pos, page0)) vc = make_uint2(0, 0);
                     *(uint4*)(dst + (c >> 2) * HALF + r * 128 + ((((2 * (c & 3) + (chunk & 1)) ^ r) & 7) << 4)) =
                         make_uint4(e4m3x2_to_f16x2(vc.x), e4m3x2_to_f16x2(vc.x >> 16), e4m3x2_to_f16x2(vc.y),
                                    e4m3x2_to_f16x2(vc.y >> 16));
