@@ -466,7 +466,8 @@ int fp8kv_paged_attention_layers(const fp8kv_layer* layers, int n_layers, int B,
  *   seq_lens      (device) int32 [B], the nodes included
  *   block_table   (device) int32 [B][max_pages_per_seq]
  *   max_seq_len   (host) >= every length
- *   tree_mask     (device) uint64 [B][M];  positions, slot_mapping (device) int64 [B][M]
+ *   tree_mask     (device) uint64 [B][M];  positions, slot_mapping (device) int64 [B][M];
+ *                 none overlaps another or an input
  * B = 0 launches nothing and reads no pointer.
  * Device checks: a parent outside [-1, m) -> padding, FP8KV_DEV_BAD_TREE; a length
  * < M, > max_seq_len or beyond the block-table row -> mask 0, position 0, slot -1
@@ -525,7 +526,8 @@ int fp8kv_rope_insert(const void* q, int64_t q_stride, const void* k, int64_t k_
  *   split_tokens (host) 0, or a multiple of page_size; of 128 for more than 16 rows
  *              M * Hq/Hkv per KV head
  *   every other argument, the workspace and the device checks: as
- *   fp8kv_append_paged_attention (per-tensor scales); out must not overlap q.
+ *   fp8kv_append_paged_attention (per-tensor scales); out must not overlap q, k_new,
+ *   v_new or tree_mask.
  * Supported: D = 128, page_size 32 or 64, Hq % Hkv == 0, 1 <= M <= 64, every cache
  * type.  With k_new, the rows of padding nodes are written too.
  */
@@ -563,6 +565,8 @@ int fp8kv_tree_attention(const void* k_new, const void* v_new, const void* q, vo
  *   num_tokens (device) int32 [B]: how many those are, 1 .. M; without a next token
  *     (FP8KV_DEV_BAD_PROBS) one less, 0 .. M - 1
  *   path       (device) int32 [B][M]: node 0 and the nodes that stand, then -1
+ *     The outputs overlap neither one another nor an input, but out_tokens and path
+ *     may each be one of the [B][M] inputs itself.
  * Pairs of fp32: a weight is off by at most 2^-45 of what it was before the fall, a
  * sum by (16 + V / (256 c)) 2^-44 of itself, c = 1 .. 16 CTAs a sequence (1 for more
  * than 256 sequences, 16 for up to 16 of 65536 tokens or more).  Any V up to 2^30; no

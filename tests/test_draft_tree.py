@@ -81,6 +81,31 @@ def test_verify_checks_its_arguments(L):
         ({"B": 0, "p": NULL}, 0)])
 
 
+def test_outputs_that_overlap_are_refused(L):
+    """Whole or by their last bytes; addresses a MiB apart otherwise."""
+    at = lambda i, back=0: ctypes.c_void_p((i << 20) - back)  # noqa: E731
+    B, M, V = 2, 12, 1000
+    meta = dict(par=at(1), sl=at(2), bt=at(3), mpps=4, maxL=100, B=B, M=M, P=16, ps=32, mask=at(4), pos=at(5),
+                slot=at(6), s=NULL)
+    over = [{n: at(i, d)} for n, own in (("mask", 4), ("pos", 5), ("slot", 6)) for i, size in
+            ((1, 96), (2, 8), (3, 32), (4, 192), (5, 192), (6, 192)) if i != own for d in (0, 184, 4 - size)]
+    _refusals(L.fp8kv_tree_metadata, meta, [(o, 1) for o in over])
+    ver = dict(p=at(1), ps=V, q=at(2), qs=V, dt=0, tok=at(3), par=at(4), u=at(5), B=B, M=M, V=V, out=at(6), num=at(7),
+               path=at(8), s=NULL)
+    rows, whole = 4 * B * M, 4 * B * M * V
+    _refusals(L.fp8kv_verify_tree, ver, [
+        *(({n: at(i, d)}, 1) for n in ("out", "path") for i in (1, 2) for d in (0, rows - 4, 4 - whole)),
+        *(({n: at(i, d)}, 1) for n in ("out", "path") for i in (3, 4, 5) for d in (rows - 4, 4, -4, 4 - rows)),
+        *(({"num": at(i, d)}, 1) for i in (1, 2, 3, 4, 5, 6, 8) for d in (0, 4, -4)),
+        ({"out": at(8)}, 1), ({"path": at(6, 4)}, 1), ({"path": at(7)}, 1), ({"out": at(7, rows - 4)}, 1),
+        ({"q": NULL, "out": at(1, 4)}, 1), ({"dt": 1, "out": at(1, 4 - whole // 2)}, 1)])
+    att = dict(kn=at(1), vn=at(2), q=at(3), k=at(16), v=at(17), dt=0, bt=at(18), mpps=4, sl=at(19), maxL=100, mask=at(20),
+               B=1, M=M, Hq=72, Hkv=8, D=128, ps=32, P=16, ks=at(21), vs=at(22), sm=0.088, wl=-1, split=0, ws=at(23),
+               wsb=1 << 30, out=at(30), s=NULL)
+    out = M * 72 * 256
+    _refusals(L.fp8kv_tree_attention, att, [({"out": at(i, d)}, 1) for i in (1, 2, 3, 20) for d in (0, out - 16, -16)])
+
+
 def test_keep_path_checks_its_arguments(L):
     two = (ctypes.c_void_p * 2)(1 << 20, 1 << 21)
     odd = (ctypes.c_void_p * 2)(1 << 20, (1 << 21) + 8)
@@ -906,6 +931,23 @@ def test_verify_sums_of_many_small_weights(draft):
     none = torch.zeros((B, 1), dtype=torch.int32, device="cuda")
     out, num, _ = fp8kv.fp8kv_verify_tree(p, p if draft else None, none, none, _cuda(np.array(u, np.float32)))
     assert num.tolist() == [1] * B and out[:, 0].tolist() == want
+    _status()
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("B,V", [(1, 70000), (40, 9000), (300, 500)])
+def test_verify_writes_over_the_rows_that_it_read(B, V):
+    """out_tokens and path may be [B][M] inputs: a sequence's CTAs have read their rows."""
+    rng = np.random.default_rng(B)
+    M = 7
+    p, q = _probs(rng, B, M, V)
+    par = _tree(rng, B, M, "tree")
+    tok = _draws(rng, q, par)
+    u = np.minimum(rng.random((B, M)).astype(np.float32), np.float32(1 - 2.0 ** -24))
+    args = _cuda(p, q, tok, par, u)
+    want = fp8kv.fp8kv_verify_tree(*args)
+    got = fp8kv.fp8kv_verify_tree(*args, out_tokens=args[2], path=args[3])
+    assert all(torch.equal(a, b) for a, b in zip(got, want))
     _status()
 
 

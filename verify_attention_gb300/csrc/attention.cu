@@ -1220,8 +1220,13 @@ static int attention_call(const void* k_new, const void* v_new, const void* q, c
     if (max_seq_len < M || (int64_t)max_seq_len > (int64_t)max_pages_per_seq * page_size)
         return FP8KV_ERR_INVALID_ARG;
     if (!(sm_scale == sm_scale)) return FP8KV_ERR_INVALID_ARG;
-    // (the CTAs of several partitions read the same Q rows)
-    if (tree && overlap(out, (size_t)B * M * Hq * D * 2, q, (size_t)B * M * Hq * D * 2)) return FP8KV_ERR_INVALID_ARG;
+    // (the CTAs of several partitions read the same Q rows and mask words)
+    if (tree) {
+        const size_t q_bytes = (size_t)B * M * Hq * D * 2, new_bytes = (size_t)B * M * Hkv * D * 2;
+        if (overlap(out, q_bytes, q, q_bytes) || overlap(out, q_bytes, tree_mask, (size_t)B * M * 8) ||
+            (k_new && (overlap(out, q_bytes, k_new, new_bytes) || overlap(out, q_bytes, v_new, new_bytes))))
+            return FP8KV_ERR_INVALID_ARG;
+    }
     const size_t need = ws_bytes(B, M, Hq, Hkv, plan);
     if (need && (!workspace || workspace_bytes < need || !al16(workspace))) return FP8KV_ERR_WORKSPACE;
 

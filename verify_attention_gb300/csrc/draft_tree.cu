@@ -224,6 +224,15 @@ extern "C" int fp8kv_tree_metadata(const int32_t* parents, const int32_t* seq_le
     if (max_seq_len < M || (int64_t)max_seq_len > (int64_t)max_pages_per_seq * page_size) return FP8KV_ERR_INVALID_ARG;
     if (B == 0) return FP8KV_OK;                                // nothing to do; no pointer is read
     if (!parents || !seq_lens || !block_table || !tree_mask || !positions || !slot_mapping) return FP8KV_ERR_INVALID_ARG;
+    // sequences write their outputs while others still read
+    const size_t nodes = (size_t)B * M, row_bytes = nodes * 8;
+    const void* outs[3] = {tree_mask, positions, slot_mapping};
+    for (int i = 0; i < 3; ++i) {
+        if (overlap(outs[i], row_bytes, parents, nodes * 4) || overlap(outs[i], row_bytes, seq_lens, (size_t)B * 4) ||
+            overlap(outs[i], row_bytes, block_table, (size_t)B * max_pages_per_seq * 4) ||
+            overlap(outs[i], row_bytes, outs[(i + 1) % 3], row_bytes))
+            return FP8KV_ERR_INVALID_ARG;
+    }
     // a small batch: one sequence an SM, so that no warp waits for another's loads
     const int warps = B <= num_sms() ? 1 : 4;
     const cudaError_t e =

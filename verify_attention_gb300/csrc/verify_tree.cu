@@ -618,6 +618,23 @@ extern "C" int fp8kv_verify_tree(const void* target_probs, int64_t target_stride
     const uintptr_t size = f32 ? 4 : 2;
     if (reinterpret_cast<uintptr_t>(target_probs) % size || reinterpret_cast<uintptr_t>(draft_probs) % size)
         return FP8KV_ERR_INVALID_ARG;
+    // sequences write their outputs while others still read
+    const size_t row_bytes = (size_t)B * M * 4, len_bytes = (size_t)B * 4;
+    const size_t p_bytes = ((size_t)((int64_t)B * M - 1) * target_stride + V) * size;
+    const size_t q_bytes = draft_probs ? ((size_t)((int64_t)B * M - 1) * draft_stride + V) * size : 0;
+    for (const void* in : {(const void*)tokens, (const void*)parents, (const void*)uniforms}) {
+        if (overlap(num_tokens, len_bytes, in, row_bytes)) return FP8KV_ERR_INVALID_ARG;
+        // (a sequence's own row is read before it is written)
+        for (const void* rows : {(const void*)out_tokens, (const void*)path})
+            if (rows != in && overlap(rows, row_bytes, in, row_bytes)) return FP8KV_ERR_INVALID_ARG;
+    }
+    for (const void* rows : {(const void*)out_tokens, (const void*)path})
+        if (overlap(rows, row_bytes, target_probs, p_bytes) || overlap(rows, row_bytes, draft_probs, q_bytes) ||
+            overlap(rows, row_bytes, num_tokens, len_bytes))
+            return FP8KV_ERR_INVALID_ARG;
+    if (overlap(out_tokens, row_bytes, path, row_bytes) || overlap(num_tokens, len_bytes, target_probs, p_bytes) ||
+        overlap(num_tokens, len_bytes, draft_probs, q_bytes))
+        return FP8KV_ERR_INVALID_ARG;
     VerifyParams P;
     P.p = target_probs;
     // (chosen drafts: p's own rows stand for q's, which nothing reads, so that they lie
