@@ -123,6 +123,8 @@ __global__ void __launch_bounds__(Cfg<FP8>::THREADS, 1) attention_tree_tc_kernel
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     pdl_launch_dependents();
     if (threadIdx.x == 0) {
+        // (as a loop: 64 trees of 12 nodes and 4096 keys, E4M3, 190 us instead of 184)
+#pragma unroll
         for (int i = 0; i < B_COUNT; ++i) {
             int count = 1;
             // V's readers: the widening warps, or P.V of both halves and warp 13
@@ -370,8 +372,8 @@ __global__ void __launch_bounds__(Cfg<FP8>::THREADS, 1) attention_tree_tc_kernel
         uint2 kc0 = make_uint2(0, 0), vc0 = kc0;
         int pos0 = -1, chunk0 = 0, page0 = -1;
         if (ct < n_app * 16) {
+            page0 = P.block_table[(int64_t)b * P.mpps + (app_lo + (ct >> 4)) / PS];
             app_item(ct, kc0, vc0, pos0, chunk0);
-            page0 = P.block_table[(int64_t)b * P.mpps + pos0 / PS];
         }
         if (const uint64_t w = tree_holes(P, b, lane); lane == 0) *warp_holes = w;
         __syncwarp();
