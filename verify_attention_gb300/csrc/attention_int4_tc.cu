@@ -191,7 +191,7 @@ __global__ void __launch_bounds__(THREADS, 1) attention_int4_tc_kernel(AttnParam
         guess_at = min(split * P.split_pages + ((lane >> 2) & (PPT - 1)), P.mpps - 1);
         guess = P.block_table[(int64_t)b * P.mpps + guess_at];
     }
-    // so are the new tokens: block ct % 8 of token ct / 8 (at most 16)
+    // so are the new tokens: block ct % 8 of token ct / 8 (at most 32)
     const int ct = threadIdx.x - 12 * 32;
     const bool has_new = P.k_new && ct >= 0 && ct < P.M * 8;
     uint4 nk[2] = {}, nv[2] = {};

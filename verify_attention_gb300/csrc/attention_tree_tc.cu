@@ -21,7 +21,7 @@
 //   - three threads issue the products (BF16: 0.80 us a tile; both halves' P.V by one
 //     thread, which then is busy for 1300 cycles a tile, 0.86);
 //   - BF16 stages of K and of V come and go by themselves (before: 0.89).
-// BF16 takes 0.78 us a tile, E4M3 0.89 (64 trees of 12 nodes, up to 32768 keys: 487
+// BF16 takes 0.78 us a tile, E4M3 0.89 (64 trees of 12 nodes, up to 32768 keys: 495
 // us): a softmax warp's way through a half tile (the wait for S 130 cycles, reading it
 // 140, the maximum 240, the exponentials 700, P 140) with the products' between them;
 // the widening of V has to stay below that (addresses computed for each chunk, and its
@@ -204,8 +204,8 @@ __global__ void __launch_bounds__(Cfg<FP8>::THREADS, 1) attention_tree_tc_kernel
     const int n_pages = min(P.split_pages, last_page + 1 - page_begin);
     const int n_tiles = (n_pages + PPT - 1) / PPT;
     const int k_begin = page_begin * PS;
-    // (E4M3: in shared memory, each widening warp its own; 64 trees of 12 nodes 2% slower
-    // with them in the widening loop's registers)
+    // (E4M3: in shared memory, each widening warp its own, none of the widening loop's
+    // registers)
     const uint64_t holes = !FP8 && (warp == 2 || warp == 3 || converts) ? tree_holes(P, b, lane) : 0;
     uint64_t* warp_holes = bars + B_COUNT + 2 + (warp - 12);
     // V rows of tile t without a reader: those outside [zlo, zhi), and padding nodes

@@ -34,7 +34,7 @@ int status_verify_tree(unsigned int* s, int clear) { return read_status(s, clear
 
 // Small CTAs, three or four an SM: while one waits for its cluster others add (64 trees
 // of 100003 tokens, drawn: 38 us in CTAs of 512 threads, two an SM).  Two an SM where a
-// chunk is 256 bf16 tokens of p and q, for their registers (30.4 us; three 32.7).
+// chunk is 256 bf16 tokens of p and q, for their registers (30.2 us; three 33.2).
 constexpr int kVerifyThreads = 256, kVerifyWarps = kVerifyThreads / 32, kVerifyMaxCluster = 16;
 
 struct VerifyParams {
@@ -653,9 +653,9 @@ extern "C" int fp8kv_verify_tree(const void* target_probs, int64_t target_stride
     P.V = V;
     // CTAs a sequence: clusters of 16 (not portable, but one fits every GPC) down to 1
     // as the batch grows, with some 500 CTAs, about what fits at once, and a few
-    // thousand tokens each.  (131072 tokens, chosen drafts: 6.2 us in 16 CTAs, 7.9 in
-    // 8, 31 in one; 64 trees of 100003, drawn: 30.7 us in 8 CTAs each, 43 in 4, 31.8 in
-    // 16, chosen 16.0, 20.5, 18.9; 8 such trees 13.6 in 16, 16.8 in 8.)
+    // thousand tokens each.  (131072 tokens, chosen drafts: 5.6 us in 16 CTAs, 7.6 in
+    // 8, 32 in one; 64 trees of 100003, drawn: 31.8 us in 8 CTAs each, 46.5 in 4, 32.8 in
+    // 16, chosen 15.5, 21.0, 18.4; 8 such trees 13.2 in 16, 16.8 in 8.)
     const int most = 512;
     int c = 1;
     while (c < kVerifyMaxCluster && (int64_t)B * c * 2 <= most && V / (2 * c) >= 2048) c *= 2;
