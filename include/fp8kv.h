@@ -569,7 +569,7 @@ int fp8kv_tree_attention(const void* k_new, const void* v_new, const void* q, vo
  *     may each be one of the [B][M] inputs itself.
  * Pairs of fp32: a weight is off by at most 2^-45 of what it was before the fall, a
  * sum by (16 + V / (256 c)) 2^-44 of itself, c = 1 .. 16 CTAs a sequence (1 for more
- * than 256 sequences, 16 for up to 16 of 65536 tokens or more).  Any V up to 2^30; no
+ * than 256 sequences, 16 for up to 32 of 32768 tokens or more).  Any V up to 2^30; no
  * workspace.  B = 0 launches nothing and reads no pointer.
  * Device checks: a parent outside [-1, m), or a node's token outside [0, V) -> that
  * node is padding, FP8KV_DEV_BAD_TREE; a row p_n without a positive, finite sum
