@@ -555,6 +555,21 @@ def test_masks_of_any_kind(kind):
 
 @pytest.mark.gpu
 @pytest.mark.parametrize("kind", CACHES)
+@pytest.mark.parametrize("M,Hq", [(8, 4), (16, 14), (31, 10)])
+@pytest.mark.parametrize("window", [0, 1, 3])
+def test_masks_of_any_kind_behind_a_short_window(kind, M, Hq, window):
+    """A node's position is its number of bits, not its index: nodes far below a row's
+    own position by their index are seen, in the half of a key tile before the others."""
+    rng = np.random.default_rng(M + window)
+    c = Case(M, kind, [int(x) for x in 64 * rng.integers(1, 9, 12) - rng.integers(1, M, 12) + M], M, Hq, 2, 64)
+    words = rng.integers(0, 1 << M, (12, M))
+    words[:, :M // 2] = (1 << M) - 1 - (rng.integers(0, 1 << M, (12, M // 2)) & rng.integers(0, 1 << M, (12, M // 2)))
+    c.check(c.run(window, tree_mask=_cuda(words)), window, mask=words)
+    _status()
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("kind", CACHES)
 @pytest.mark.parametrize("M,Hq", [(4, 4), (12, 18), (24, 18)])
 def test_bad_sequences_leave_their_rows(kind, M, Hq):
     c = Case(21, kind, [100, 60, 90], M, Hq, 2, 32)

@@ -302,7 +302,9 @@ __global__ void __launch_bounds__(THREADS, 1) attention_int4_tc_kernel(AttnParam
         __syncwarp();
         if (lane == 0) mbar_arrive(bar(B_Q_READY));
 
-        int pmin = p_r, lomax = lo_r, pmax = p_r, lomin = lo_r;
+        // (a tree's rows may see nodes at lower keys than where the context that they see
+        // would begin: a window counts a node's position, whatever its index)
+        int pmin = p_r, lomax = lo_r, pmax = p_r, lomin = TREE ? min(lo_r, base) : lo_r;
 #pragma unroll
         for (int off = 1; off < 32; off <<= 1) {
             pmin = min(pmin, __shfl_xor_sync(0xffffffffu, pmin, off));
